@@ -25,7 +25,8 @@ BUILD = os.path.join(PKG, "_build")
 SO = os.path.join(PKG, "libfa.so")
 TEST_SO = os.path.join(PKG, "libfa_waittest.so")
 SOURCES = ["fa_api.cu", "fa_fwd_sm103.cu", "fa_fwd_f32.cu", "fa_bwd_sm103.cu", "fa_bwd_noalloc.cu",
-           "fa_decode_sm103.cu", "fa_fp8_sm103.cu"]
+           "fa_decode_sm103.cu", "fa_fp8_sm103.cu", "fa_cache_api.cu", "fa_cache_sm103.cu",
+           "fa_paged_sm103.cu"]
 # the units that read FA_TEST_WITHHOLD; the test library takes the others from the product build
 TEST_SOURCES = ["fa_api.cu", "fa_fwd_sm103.cu", "fa_bwd_sm103.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -145,8 +145,6 @@ int fill_empty_launch(void *o, float *lse, size_t rows, int d, int elem_bytes, c
 }
 
 // ------------------------------------------------------------ validation
-namespace {
-
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // A buffer of n elements: non-null and 16-byte aligned, or anything when n == 0.
@@ -178,6 +176,8 @@ int check_device()
         cache[dev] = ok ? 1 : 2;
     return ok ? OK : ERR_UNSUPPORTED;
 }
+
+namespace {
 
 // Shapes, flags and scale shared by every entry point.
 int check_sizes(int B, int H, int Tq, int Tk, int d, int causal, float scale)
@@ -554,12 +554,15 @@ int fa_sync_status(fa_stream_t stream)
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (cudaStreamSynchronize(s) != cudaSuccess)
         return FA_ERR_CUDA;
-    int wf = 0, wb = 0, wd = 0;
-    if (fa::fwd_status_fetch_clear(s, &wf) != fa::OK || fa::bwd_status_fetch_clear(s, &wb) != fa::OK ||
-        fa::dec_status_fetch_clear(s, &wd) != fa::OK)
+    int w[5] = {0, 0, 0, 0, 0};
+    if (fa::fwd_status_fetch_clear(s, &w[0]) != fa::OK || fa::bwd_status_fetch_clear(s, &w[1]) != fa::OK ||
+        fa::dec_status_fetch_clear(s, &w[2]) != fa::OK || fa::paged_status_fetch_clear(s, &w[3]) != fa::OK ||
+        fa::cache_status_fetch_clear(s, &w[4]) != fa::OK)
         return FA_ERR_CUDA;
-    const int w = wf ? wf : (wb ? wb : wd);
-    return w ? (w & 0xFF) : FA_OK;
+    for (int i = 0; i < 5; ++i)
+        if (w[i])
+            return w[i] & 0xFF;
+    return FA_OK;
 }
 
 const char *fa_status_string(int status)
@@ -575,6 +578,8 @@ const char *fa_status_string(int status)
         return "CUDA runtime or driver error";
     case FA_ERR_TIMEOUT:
         return "a device-side bounded wait timed out; outputs of that call are invalid";
+    case FA_ERR_BAD_INDEX:
+        return "a length, count or page number in device memory is out of range; that sequence or page was left out";
     default:
         return "unknown status";
     }

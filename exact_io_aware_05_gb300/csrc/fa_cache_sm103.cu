@@ -1,0 +1,665 @@
+// fa_cache_sm103.cu -- rotary positions with several axes, the write of new tokens into the
+// paged key/value cache, and eviction from it by accumulated attention weight (sm_103a).
+//
+// Rotation.  Pair i of a row turns by theta = p f_i (p the token's position on the pair's
+// axis).  Only theta modulo one turn matters, so f_i / 2 pi is held as a 64-bit fraction of a
+// turn: p times it, in wrapping 64-bit integer arithmetic, is the angle modulo one turn with no
+// reduction at all and an error of p 2^-65 turns, at any position.  The two top bits (rounded)
+// are the quadrant, the rest an angle in [-pi/4, pi/4], where the Taylor series of sine and
+// cosine are below half an fp32 ulp after x^9 and x^10.
+//
+// What bounds these kernels is memory: a rotation reads and writes each element once.  A thread
+// owns 8 pairs of one token (two 16-byte loads in bf16), computes their sines and cosines once
+// and runs over the heads with them.
+#include <climits>
+
+#include "fa_common.cuh"
+#include "fa_internal.h"
+
+namespace fa {
+
+__device__ int g_cache_status;   // device status word of the kernels in this file
+
+namespace {
+
+constexpr int kStatusBadIndex = 5;
+
+// ------------------------------------------------------------------ rotation
+struct RopeTable {
+    unsigned long long turns[128];
+    unsigned char axis[128];
+};
+
+struct Row3 {   // one strided [B][H][T][d] tensor
+    void *p;
+    long long sb, sh, st;
+};
+
+__device__ __forceinline__ void phase_sincos(unsigned long long turns, int pos, float &sn, float &cs)
+{
+    const unsigned long long ph = turns * (unsigned long long)(long long)pos;
+    const unsigned long long up = ph + (1ull << 61);      // to the nearest quarter turn
+    const uint32_t quad = (uint32_t)(up >> 62);
+    const int rest = (int)((long long)(ph - ((up >> 62) << 62)) >> 30);   // units of 2^-34 turns
+    const float x = (float)rest * 3.6572952e-10f;         // 2 pi 2^-34: |x| <= pi / 4
+    const float z = x * x;
+    float s = fmaf(z, 2.7557319e-6f, -1.9841270e-4f);
+    s = fmaf(z, s, 8.3333333e-3f);
+    s = fmaf(z, s, -1.6666667e-1f);
+    s = fmaf(x * z, s, x);
+    float c = fmaf(z, -2.7557319e-7f, 2.4801587e-5f);
+    c = fmaf(z, c, -1.3888889e-3f);
+    c = fmaf(z, c, 4.1666667e-2f);
+    c = fmaf(z, c, -0.5f);
+    c = fmaf(z, c, 1.0f);
+    const float a = (quad & 1) ? c : s, b = (quad & 1) ? s : c;
+    sn = (quad & 2) ? -a : a;
+    cs = ((quad + 1) & 2) ? -b : b;
+}
+
+// 8 consecutive elements as fp32, from and to memory.
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&x)[8])
+{
+    const uint4 w = *reinterpret_cast<const uint4 *>(p);
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(u[i] << 16);
+        x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+    }
+}
+__device__ __forceinline__ void load8(const float *p, float (&x)[8])
+{
+    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&x)[8])
+{
+    *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                                               pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+}
+__device__ __forceinline__ void store8(float *p, const float (&x)[8])
+{
+    reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+
+// The 16 features of one thread: two runs of 8 at e0 and e1.  Thread v < rot / 16 has pairs
+// 8 v .. 8 v + 7; the others 16 features that pass through.
+struct Slice {
+    int e0, e1, pair;   // pair < 0: pass through
+};
+__device__ __forceinline__ Slice slice_of(int v, int rot, int interleaved)
+{
+    Slice s;
+    if (v < rot / 16) {
+        s.pair = 8 * v;
+        s.e0 = interleaved ? 16 * v : 8 * v;
+        s.e1 = interleaved ? 16 * v + 8 : rot / 2 + 8 * v;
+    } else {
+        s.pair = -1;
+        s.e0 = 16 * v;
+        s.e1 = 16 * v + 8;
+    }
+    return s;
+}
+
+// Turns the pairs held in (a, b): pair j is (a[j], b[j]), or, interleaved, two neighbours.
+template <bool INTER>
+__device__ __forceinline__ void turn(float (&a)[8], float (&b)[8], const float (&sn)[8], const float (&cs)[8])
+{
+    if constexpr (!INTER) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float x = a[j], y = b[j];
+            a[j] = fmaf(-y, sn[j], x * cs[j]);
+            b[j] = fmaf(x, sn[j], y * cs[j]);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float x = a[2 * j], y = a[2 * j + 1], u = b[2 * j], w = b[2 * j + 1];
+            a[2 * j] = fmaf(-y, sn[j], x * cs[j]);
+            a[2 * j + 1] = fmaf(x, sn[j], y * cs[j]);
+            b[2 * j] = fmaf(-w, sn[4 + j], u * cs[4 + j]);
+            b[2 * j + 1] = fmaf(u, sn[4 + j], w * cs[4 + j]);
+        }
+    }
+}
+
+struct RopeArgs {
+    Row3 x[2], y[2];
+    int H0, H;            // heads of the first tensor, of both
+    const int *pos;       // [axes][n]
+    long long n;          // B * T
+    int T, rot, heads_per_cta;
+    float sign;
+};
+
+constexpr int kRopeThreads = 256;
+
+template <typename E, int D, bool INTER>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeTable tab,
+                                                            const __grid_constant__ RopeArgs a)
+{
+    constexpr int TPR = D / 16;                          // threads a row
+    const int v = threadIdx.x % TPR;
+    const long long tok = (long long)blockIdx.x * (kRopeThreads / TPR) + threadIdx.x / TPR;
+    if (tok >= a.n)
+        return;
+    const long long b = tok / a.T, t = tok - b * a.T;
+    const Slice sl = slice_of(v, a.rot, INTER);
+    float sn[8], cs[8];
+    if (sl.pair >= 0) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int p = a.pos[(long long)tab.axis[sl.pair + j] * a.n + tok];
+            phase_sincos(tab.turns[sl.pair + j], p, sn[j], cs[j]);
+            sn[j] *= a.sign;
+        }
+    }
+    const int h0 = blockIdx.y * a.heads_per_cta, h1 = min(a.H, h0 + a.heads_per_cta);
+    for (int h = h0; h < h1; ++h) {
+        const int w = h >= a.H0;
+        const Row3 &xi = a.x[w], &yi = a.y[w];
+        const int hh = h - (w ? a.H0 : 0);
+        const E *x = static_cast<const E *>(xi.p) + b * xi.sb + hh * xi.sh + t * xi.st;
+        E *y = static_cast<E *>(yi.p) + b * yi.sb + hh * yi.sh + t * yi.st;
+        float p[8], q[8];
+        load8(x + sl.e0, p);
+        load8(x + sl.e1, q);
+        if (sl.pair >= 0)
+            turn<INTER>(p, q, sn, cs);
+        store8(y + sl.e0, p);
+        store8(y + sl.e1, q);
+    }
+}
+
+RopeTable table_of(const fa_rope_spec &s)
+{
+    RopeTable t;
+    for (int i = 0; i < 128; ++i) {
+        t.turns[i] = s.turns[i];
+        t.axis[i] = s.axis[i];
+    }
+    return t;
+}
+
+Row3 row3(const fa_heads &x) { return Row3{x.data, x.stride_b, x.stride_h, x.stride_t}; }
+
+// Heads one thread runs over: as many as leave enough threads to fill the device.
+int heads_per_cta(long long tokens, int H, int d)
+{
+    const long long want = (long long)device_sm_count() * 1024;
+    const long long all = tokens * H * (d / 16);
+    const long long n = all / want;
+    return (int)(n < 1 ? 1 : n > 8 ? 8 : n);
+}
+
+template <typename E, int D>
+int rope_run(const RopeTable &t, const RopeArgs &a, int interleaved, cudaStream_t s)
+{
+    constexpr int TOK = kRopeThreads / (D / 16);
+    const dim3 grid((unsigned)((a.n + TOK - 1) / TOK), (unsigned)((a.H + a.heads_per_cta - 1) / a.heads_per_cta));
+    if (interleaved)
+        rope_kernel<E, D, true><<<grid, kRopeThreads, 0, s>>>(t, a);
+    else
+        rope_kernel<E, D, false><<<grid, kRopeThreads, 0, s>>>(t, a);
+    return cudaGetLastError() == cudaSuccess ? OK : ERR_CUDA;
+}
+
+template <typename E>
+int rope_width(int d, const RopeTable &t, const RopeArgs &a, int interleaved, cudaStream_t s)
+{
+    return d == 64 ? rope_run<E, 64>(t, a, interleaved, s)
+                   : d == 128 ? rope_run<E, 128>(t, a, interleaved, s) : rope_run<E, 256>(t, a, interleaved, s);
+}
+
+// ------------------------------------------------------------------ append
+struct AppendArgs {
+    Row3 q, qo, k, v;
+    int Hq, Hkv, B, T, rot, rotate, heads_per_cta;
+    const int *pos;
+    const int *block_table, *lens, *seen, *new_lens;
+    void *kp, *vp;
+    const float *ks, *vs;
+    float *weight;
+    int *order;
+    int num_pages, max_pages, ps_shift;
+};
+
+// 8 values into the cache: bf16, or e4m3 codes of x / scale.
+template <bool FP8>
+__device__ __forceinline__ void put8(void *base, long long at, const float (&x)[8], float scale)
+{
+    if constexpr (FP8) {
+        uint2 w;
+        w.x = pack_e4m3x4(__fdiv_rn(x[0], scale), __fdiv_rn(x[1], scale), __fdiv_rn(x[2], scale), __fdiv_rn(x[3], scale));
+        w.y = pack_e4m3x4(__fdiv_rn(x[4], scale), __fdiv_rn(x[5], scale), __fdiv_rn(x[6], scale), __fdiv_rn(x[7], scale));
+        *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(base) + at) = w;
+    } else {
+        store8(static_cast<__nv_bfloat16 *>(base) + at, x);
+    }
+}
+
+// Heads run q, then k, then v; a token's slot and page are looked up once per thread.
+template <int D, bool INTER, bool FP8>
+__global__ void __launch_bounds__(kRopeThreads) append_kernel(const __grid_constant__ RopeTable tab,
+                                                              const __grid_constant__ AppendArgs a)
+{
+    constexpr int TPR = D / 16;
+    const int vec = threadIdx.x % TPR;
+    const long long n = (long long)a.B * a.T;
+    const long long tok = (long long)blockIdx.x * (kRopeThreads / TPR) + threadIdx.x / TPR;
+    if (tok >= n)
+        return;
+    const int b = (int)(tok / a.T), t = (int)(tok - (long long)b * a.T);
+    const int len = a.lens[b], cap = a.max_pages << a.ps_shift;
+    const int nb = a.new_lens ? a.new_lens[b] : a.T;
+    if (len < 0 || len > cap || nb < 0 || nb > a.T || nb > len) {
+        if (vec == 0 && t == 0 && blockIdx.y == 0)
+            atomicCAS(&g_cache_status, 0, kStatusBadIndex);
+        return;
+    }
+    if (t >= nb)
+        return;
+    const int slot = len - nb + t;
+    const Slice sl = slice_of(vec, a.rotate ? a.rot : 0, INTER);
+    const int h0 = blockIdx.y * a.heads_per_cta, h1 = min(a.Hq + 2 * a.Hkv, h0 + a.heads_per_cta);
+    float sn[8], cs[8];
+    if (sl.pair >= 0 && h0 < a.Hq + a.Hkv) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            phase_sincos(tab.turns[sl.pair + j], a.pos[(long long)tab.axis[sl.pair + j] * n + tok], sn[j], cs[j]);
+    }
+    int page = 0;
+    bool page_ok = true;
+    if (h1 > a.Hq) {
+        page = a.block_table[(long long)b * a.max_pages + (slot >> a.ps_shift)];
+        page_ok = page >= 0 && page < a.num_pages;
+        if (!page_ok && vec == 0)
+            atomicCAS(&g_cache_status, 0, kStatusBadIndex);
+    }
+    const int row = slot & ((1 << a.ps_shift) - 1);
+    for (int h = h0; h < h1; ++h) {
+        float x[8], y[8];
+        if (h < a.Hq) {
+            const __nv_bfloat16 *p = static_cast<const __nv_bfloat16 *>(a.q.p) + b * a.q.sb + h * a.q.sh + t * a.q.st;
+            __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.qo.p) + b * a.qo.sb + h * a.qo.sh + t * a.qo.st;
+            load8(p + sl.e0, x);
+            load8(p + sl.e1, y);
+            if (sl.pair >= 0)
+                turn<INTER>(x, y, sn, cs);
+            store8(o + sl.e0, x);
+            store8(o + sl.e1, y);
+        } else if (page_ok) {
+            const bool isv = h >= a.Hq + a.Hkv;
+            const int hk = h - a.Hq - (isv ? a.Hkv : 0);
+            const Row3 &r = isv ? a.v : a.k;
+            const __nv_bfloat16 *p = static_cast<const __nv_bfloat16 *>(r.p) + b * r.sb + hk * r.sh + t * r.st;
+            load8(p + sl.e0, x);
+            load8(p + sl.e1, y);
+            if (!isv && sl.pair >= 0)
+                turn<INTER>(x, y, sn, cs);
+            const long long at = ((((long long)page * a.Hkv + hk) << a.ps_shift) + row) * D;
+            const float scale = FP8 ? (isv ? a.vs : a.ks)[hk] : 1.f;
+            put8<FP8>(isv ? a.vp : a.kp, at + sl.e0, x, scale);
+            put8<FP8>(isv ? a.vp : a.kp, at + sl.e1, y, scale);
+            if (!isv && vec == 0) {
+                const long long w = ((long long)b * a.Hkv + hk) * cap + slot;
+                if (a.weight)
+                    a.weight[w] = 0.f;
+                if (a.order)
+                    a.order[w] = (a.seen ? a.seen[b] - nb : len - nb) + t;
+            }
+        }
+    }
+}
+
+template <int D, bool FP8>
+int append_run(const RopeTable &t, const AppendArgs &a, int interleaved, cudaStream_t s)
+{
+    constexpr int TOK = kRopeThreads / (D / 16);
+    const long long n = (long long)a.B * a.T;
+    const int H = a.Hq + 2 * a.Hkv;
+    const dim3 grid((unsigned)((n + TOK - 1) / TOK), (unsigned)((H + a.heads_per_cta - 1) / a.heads_per_cta));
+    if (interleaved)
+        append_kernel<D, true, FP8><<<grid, kRopeThreads, 0, s>>>(t, a);
+    else
+        append_kernel<D, false, FP8><<<grid, kRopeThreads, 0, s>>>(t, a);
+    return cudaGetLastError() == cudaSuccess ? OK : ERR_CUDA;
+}
+
+// ------------------------------------------------------------------ evict
+struct EvictArgs {
+    const float *weight;
+    const int *order, *lens, *seen, *block_table;
+    float *weight_out;
+    int *order_out, *lens_out, *kept;
+    uint8_t *k, *v;
+    int B, Hkv, budget, n_first, n_recent, cap, num_pages, max_pages, ps_shift, row_bytes;
+};
+
+constexpr int kSelThreads = 1024;
+
+// Rank of an entry: larger stays.  Floats in their order (-0 as 0, a NaN as the least); the
+// largest value is kept for protected entries.
+__device__ __forceinline__ uint32_t rank_key(float w, bool is_protected)
+{
+    if (is_protected)
+        return 0xFFFFFFFFu;
+    if (w != w)
+        return 0u;
+    const uint32_t u = __float_as_uint(w + 0.f);
+    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+// Sum of x over the block, in every thread.
+__device__ __forceinline__ int block_sum(int x, int *scratch)
+{
+    x = __reduce_add_sync(0xffffffffu, x);
+    __syncthreads();
+    if (lane_id() == 0)
+        scratch[warp_id()] = x;
+    __syncthreads();
+    return __reduce_add_sync(0xffffffffu, lane_id() < blockDim.x / 32 ? scratch[lane_id()] : 0);
+}
+
+// Number of true predicates in the lower threads of the block, and in all of it.
+__device__ __forceinline__ int block_rank(bool p, int &total, int *scratch)
+{
+    const uint32_t m = __ballot_sync(0xffffffffu, p);
+    __syncthreads();
+    if (lane_id() == 0)
+        scratch[warp_id()] = __popc(m);
+    __syncthreads();
+    const int c = lane_id() < blockDim.x / 32 ? scratch[lane_id()] : 0;
+    total = __reduce_add_sync(0xffffffffu, c);
+    const int before = __reduce_add_sync(0xffffffffu, lane_id() < warp_id() ? c : 0);
+    return before + __popc(m & ((1u << lane_id()) - 1u));
+}
+
+// One CTA per (sequence, KV head): finds the rank of the last entry that stays (radix select,
+// 8 bits a pass) and the slot up to which entries of that very rank stay, then pairs the kept
+// entries behind the new length with the holes in front of it.
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_constant__ EvictArgs a)
+{
+    __shared__ int hist[256], scratch[32], pick[2];
+    const int unit = blockIdx.x, b = unit / a.Hkv, tid = threadIdx.x;
+    const int len = a.lens[b];
+    int *kept = a.kept + (long long)unit * a.budget;
+    const long long base = (long long)unit * a.cap;
+    if (len < 0 || len > a.cap) {
+        if (tid == 0)
+            atomicCAS(&g_cache_status, 0, kStatusBadIndex);
+        for (int j = tid; j < a.budget; j += kSelThreads)
+            kept[j] = -1;
+        return;
+    }
+    const float *weight = a.weight + base;
+    const int *order = a.order ? a.order + base : nullptr;
+    const int end = min(len, a.budget);
+    const int recent = (a.seen ? a.seen[b] : len) - a.n_recent;
+    auto key = [&](int i) {
+        const bool prot = order && (order[i] < a.n_first || (a.n_recent > 0 && order[i] >= recent));
+        return rank_key(weight[i], prot);
+    };
+    if (len <= a.budget) {
+        for (int j = tid; j < a.budget; j += kSelThreads)
+            kept[j] = j < end ? j : -1;
+    } else {
+        uint32_t prefix = 0, mask = 0;
+        int need = end;   // entries still to be taken among those that match the prefix
+        for (int shift = 24; shift >= 0; shift -= 8) {
+            for (int i = tid; i < 256; i += kSelThreads)
+                hist[i] = 0;
+            __syncthreads();
+            for (int i = tid; i < len; i += kSelThreads) {
+                const uint32_t u = key(i);
+                if ((u & mask) == prefix)
+                    atomicAdd(&hist[(u >> shift) & 255], 1);
+            }
+            __syncthreads();
+            if (tid == 0) {
+                int left = need, d = 255;
+                while (d > 0 && hist[d] < left)
+                    left -= hist[d--];
+                pick[0] = d;
+                pick[1] = left;
+            }
+            __syncthreads();
+            prefix |= (uint32_t)pick[0] << shift;
+            mask |= 255u << shift;
+            need = pick[1];
+            __syncthreads();
+        }
+        // slots up to `edge` of the entries whose rank is `prefix` itself stay
+        int equal = 0;
+        for (int i = tid; i < len; i += kSelThreads)
+            equal += key(i) == prefix;
+        equal = block_sum(equal, scratch);
+        int edge = INT_MAX;
+        if (equal > need) {
+            int done = 0;
+            for (int i0 = 0; i0 < len && edge == INT_MAX; i0 += kSelThreads) {
+                const int i = i0 + tid;
+                const bool eq = i < len && key(i) == prefix;
+                int total;
+                const int r = done + block_rank(eq, total, scratch);
+                if (tid == 0)
+                    pick[0] = INT_MAX;
+                __syncthreads();
+                if (eq && r == need - 1)
+                    pick[0] = i;
+                __syncthreads();
+                edge = pick[0];
+                done += total;
+            }
+        }
+        auto stays = [&](int i) {
+            const uint32_t u = key(i);
+            return u > prefix || (u == prefix && i <= edge);
+        };
+        // kept entries behind the new length, in order, for the moment at the front of `kept`
+        int movers = 0;
+        for (int i0 = end; i0 < len; i0 += kSelThreads) {
+            const int i = i0 + tid;
+            const bool m = i < len && stays(i);
+            int total;
+            const int r = movers + block_rank(m, total, scratch);
+            if (m)
+                kept[r] = i;
+            movers += total;
+        }
+        __syncthreads();
+        // the holes take them, from the last tile to the first: a hole's rank is at most its
+        // slot, so a tile overwrites no entry that a lower tile still has to read
+        int left = movers;
+        for (int i0 = (end - 1) / kSelThreads * kSelThreads; i0 >= 0; i0 -= kSelThreads) {
+            const int i = i0 + tid;
+            const bool hole = i < end && !stays(i);
+            int total;
+            const int r = block_rank(hole, total, scratch);
+            left -= total;
+            const int from = hole ? kept[left + r] : i;
+            __syncthreads();
+            if (i < end)
+                kept[i] = from;
+        }
+    }
+    __syncthreads();
+    for (int j = tid; j < end; j += kSelThreads) {
+        const int i = kept[j];
+        a.weight_out[base + j] = weight[i];
+        if (order)
+            a.order_out[base + j] = order[i];
+    }
+}
+
+// Rows of the moved entries: each warp takes 32 entries of one (sequence, KV head) and copies
+// K and V of those that moved.  Sources lie behind the new length and targets in front of it.
+__global__ void __launch_bounds__(256) evict_move_kernel(const __grid_constant__ EvictArgs a)
+{
+    const int unit = blockIdx.x, b = unit / a.Hkv, h = unit - b * a.Hkv, lane = threadIdx.x & 31;
+    if (blockIdx.y == 0 && h == 0 && threadIdx.x == 0) {
+        const int len = a.lens[b];
+        a.lens_out[b] = min(len, a.budget);
+    }
+    const int *table = a.block_table + (long long)b * a.max_pages;
+    const int vecs = a.row_bytes / 16;
+    auto at = [&](int slot) -> long long {
+        const int page = table[slot >> a.ps_shift];
+        if (page < 0 || page >= a.num_pages)
+            return -1;
+        return ((((long long)page * a.Hkv + h) << a.ps_shift) + (slot & ((1 << a.ps_shift) - 1))) * a.row_bytes;
+    };
+    for (int j0 = (blockIdx.y * 8 + (threadIdx.x >> 5)) * 32; j0 < a.budget; j0 += gridDim.y * 256) {
+        const int j = j0 + lane;
+        const int i = j < a.budget ? a.kept[(long long)unit * a.budget + j] : -1;
+        long long from = -1, to = -1;
+        if (i >= 0 && i != j) {
+            from = at(i);
+            to = at(j);
+            if (from < 0 || to < 0) {
+                atomicCAS(&g_cache_status, 0, kStatusBadIndex);
+                from = -1;
+            }
+        }
+        uint32_t todo = __ballot_sync(0xffffffffu, from >= 0);
+        while (todo) {
+            const int l = __ffs(todo) - 1;
+            todo &= todo - 1;
+            const long long f = __shfl_sync(0xffffffffu, from, l), t = __shfl_sync(0xffffffffu, to, l);
+            for (int e = lane; e < 2 * vecs; e += 32) {
+                uint8_t *pool = e < vecs ? a.k : a.v;
+                const int o = (e < vecs ? e : e - vecs) * 16;
+                *reinterpret_cast<uint4 *>(pool + t + o) = *reinterpret_cast<const uint4 *>(pool + f + o);
+            }
+        }
+    }
+}
+
+int shift_of(int page_size)
+{
+    int s = 0;
+    while ((1 << s) < page_size)
+        ++s;
+    return s;
+}
+
+}  // namespace
+
+int rope_launch(const fa_heads *x, const fa_heads *y, int n, const int *positions, const fa_rope_spec &spec, int B,
+                int T, int dtype, int inverse, cudaStream_t s)
+{
+    RopeArgs a;
+    for (int i = 0; i < 2; ++i) {
+        a.x[i] = row3(x[i < n ? i : 0]);
+        a.y[i] = row3(y[i < n ? i : 0]);
+    }
+    a.H0 = x[0].H;
+    a.H = x[0].H + (n > 1 ? x[1].H : 0);
+    a.pos = positions;
+    a.n = (long long)B * T;
+    a.T = T;
+    a.rot = spec.rot;
+    a.heads_per_cta = heads_per_cta(a.n, a.H, spec.d);
+    if ((a.H + a.heads_per_cta - 1) / a.heads_per_cta > 65535)
+        a.heads_per_cta = (a.H + 65534) / 65535;
+    a.sign = inverse ? -1.f : 1.f;
+    const RopeTable t = table_of(spec);
+    return dtype == FA_F32 ? rope_width<float>(spec.d, t, a, spec.interleaved, s)
+                           : rope_width<__nv_bfloat16>(spec.d, t, a, spec.interleaved, s);
+}
+
+int append_launch(const fa_kv_cache &c, const fa_heads &k, const fa_heads &v, const fa_heads *q,
+                  const fa_heads *q_out, const int *positions, const fa_rope_spec *spec, const int *new_lens, int T,
+                  cudaStream_t s)
+{
+    AppendArgs a;
+    a.k = row3(k);
+    a.v = row3(v);
+    a.q = q ? row3(*q) : Row3{nullptr, 0, 0, 0};
+    a.qo = q ? row3(*q_out) : Row3{nullptr, 0, 0, 0};
+    a.Hq = q ? q->H : 0;
+    a.Hkv = c.Hkv;
+    a.B = c.B;
+    a.T = T;
+    a.rotate = spec != nullptr;
+    a.rot = spec ? spec->rot : 0;
+    a.pos = positions;
+    a.block_table = c.block_table;
+    a.lens = c.lens;
+    a.seen = c.seen;
+    a.new_lens = new_lens;
+    a.kp = c.k;
+    a.vp = c.v;
+    a.ks = c.k_scale;
+    a.vs = c.v_scale;
+    a.weight = c.weight;
+    a.order = c.order;
+    a.num_pages = c.num_pages;
+    a.max_pages = c.max_pages;
+    a.ps_shift = shift_of(c.page_size);
+    const int H = a.Hq + 2 * a.Hkv;
+    a.heads_per_cta = heads_per_cta((long long)c.B * T, H, c.d);
+    if ((H + a.heads_per_cta - 1) / a.heads_per_cta > 65535)
+        a.heads_per_cta = (H + 65534) / 65535;
+    RopeTable t{};
+    if (spec)
+        t = table_of(*spec);
+    const int inter = spec ? spec->interleaved : 0;
+    const bool f8 = c.dtype == FA_E4M3;
+    switch (c.d) {
+    case 64:
+        return f8 ? append_run<64, true>(t, a, inter, s) : append_run<64, false>(t, a, inter, s);
+    case 128:
+        return f8 ? append_run<128, true>(t, a, inter, s) : append_run<128, false>(t, a, inter, s);
+    default:
+        return f8 ? append_run<256, true>(t, a, inter, s) : append_run<256, false>(t, a, inter, s);
+    }
+}
+
+int evict_launch(const fa_kv_cache &c, int budget, int n_first, int n_recent, float *weight_out, int *order_out,
+                 int *lens_out, int *kept, cudaStream_t s)
+{
+    EvictArgs a;
+    a.weight = c.weight;
+    a.order = c.order;
+    a.lens = c.lens;
+    a.seen = c.seen;
+    a.block_table = c.block_table;
+    a.weight_out = weight_out;
+    a.order_out = order_out;
+    a.lens_out = lens_out;
+    a.kept = kept;
+    a.k = static_cast<uint8_t *>(c.k);
+    a.v = static_cast<uint8_t *>(c.v);
+    a.B = c.B;
+    a.Hkv = c.Hkv;
+    a.budget = budget;
+    a.n_first = n_first;
+    a.n_recent = n_recent;
+    a.cap = c.max_pages * c.page_size;
+    a.num_pages = c.num_pages;
+    a.max_pages = c.max_pages;
+    a.ps_shift = shift_of(c.page_size);
+    a.row_bytes = c.d * (c.dtype == FA_E4M3 ? 1 : 2);
+    const int units = c.B * c.Hkv;
+    evict_select_kernel<<<units, kSelThreads, 0, s>>>(a);
+    const int blocks = (budget + 255) / 256;
+    evict_move_kernel<<<dim3(units, blocks < 64 ? blocks : 64), 256, 0, s>>>(a);
+    return cudaGetLastError() == cudaSuccess ? OK : ERR_CUDA;
+}
+
+int cache_status_fetch_clear(cudaStream_t s, int *host_word)
+{
+    int zero = 0;
+    if (cudaMemcpyFromSymbolAsync(host_word, g_cache_status, sizeof(int), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+        cudaMemcpyToSymbolAsync(g_cache_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s) != cudaSuccess ||
+        cudaStreamSynchronize(s) != cudaSuccess)
+        return ERR_CUDA;
+    return OK;
+}
+
+}  // namespace fa

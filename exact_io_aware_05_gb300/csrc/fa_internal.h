@@ -7,10 +7,12 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "../../include/fa.h"
+
 namespace fa {
 
 // Status codes, identical to fa_status in include/fa.h.
-enum : int { OK = 0, ERR_INVALID_ARG = 1, ERR_UNSUPPORTED = 2, ERR_CUDA = 3, ERR_TIMEOUT = 4 };
+enum : int { OK = 0, ERR_INVALID_ARG = 1, ERR_UNSUPPORTED = 2, ERR_CUDA = 3, ERR_TIMEOUT = 4, ERR_BAD_INDEX = 5 };
 
 // Encodes a 3-D tiled TMA map over a contiguous [planes][rows][inner] tensor
 // with 128-byte swizzle; the box is [1][box_rows][box_inner].  Returns OK or
@@ -18,6 +20,14 @@ enum : int { OK = 0, ERR_INVALID_ARG = 1, ERR_UNSUPPORTED = 2, ERR_CUDA = 3, ERR
 int encode_tmap_3d(CUtensorMap *map, const void *base, CUtensorMapDataType dtype, int elem_bytes,
                    uint64_t inner, uint64_t rows, uint64_t planes, uint32_t box_inner,
                    uint32_t box_rows);
+
+// Argument checks shared by the entry points: 16-byte alignment, a buffer of n elements that
+// is non-null and aligned (or anything when n == 0), overlap of two byte ranges, and the
+// sm_103 check of the current device (cached).
+bool aligned16(const void *p);
+bool present16(const void *p, size_t n);
+bool overlaps(const void *a, size_t na, const void *b, size_t nb);
+int check_device();
 
 int device_sm_count();          // SMs of the current device (cached per device)
 uint64_t wait_timeout_ns();     // bounded-wait limit for device spin waits
@@ -129,5 +139,20 @@ int decode_launch(const void *q, const void *k, const void *v, void *o, float *l
 int fwd_status_fetch_clear(cudaStream_t s, int *host_word);
 int bwd_status_fetch_clear(cudaStream_t s, int *host_word);
 int dec_status_fetch_clear(cudaStream_t s, int *host_word);
+
+// Rotary positions and the paged cache (fa_cache_sm103.cu, fa_paged_sm103.cu); arguments
+// already validated by fa_cache_api.cu.  Structures as in include/fa.h.
+int rope_launch(const fa_heads *x, const fa_heads *y, int n, const int *positions, const fa_rope_spec &spec, int B,
+                int T, int dtype, int inverse, cudaStream_t s);
+int append_launch(const fa_kv_cache &c, const fa_heads &k, const fa_heads &v, const fa_heads *q,
+                  const fa_heads *q_out, const int *positions, const fa_rope_spec *spec, const int *new_lens, int T,
+                  cudaStream_t s);
+int evict_launch(const fa_kv_cache &c, int budget, int n_first, int n_recent, float *weight_out, int *order_out,
+                 int *lens_out, int *kept, cudaStream_t s);
+size_t paged_workspace_bytes(int B, int Hq, int Hkv, int Tq, int max_len, int d, int accumulate);
+int paged_launch(const fa_kv_cache &c, const void *q, void *o, float *lse, int Hq, int Tq, int causal, float scale,
+                 int accumulate, void *workspace, cudaStream_t s);
+int cache_status_fetch_clear(cudaStream_t s, int *host_word);
+int paged_status_fetch_clear(cudaStream_t s, int *host_word);
 
 }  // namespace fa

@@ -55,7 +55,37 @@ _lib.fa_sync_status.restype = _i
 _lib.fa_status_string.argtypes = [_i]
 _lib.fa_status_string.restype = ctypes.c_char_p
 
-FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_TIMEOUT = range(5)
+
+class _Heads(ctypes.Structure):
+    _fields_ = [("data", _vp), ("stride_b", ctypes.c_longlong), ("stride_h", ctypes.c_longlong),
+                ("stride_t", ctypes.c_longlong), ("H", _i)]
+
+
+class _RopeSpec(ctypes.Structure):
+    _fields_ = [("d", _i), ("rot", _i), ("n_axes", _i), ("interleaved", _i),
+                ("turns", ctypes.c_ulonglong * 128), ("axis", ctypes.c_ubyte * 128)]
+
+
+class _KVCache(ctypes.Structure):
+    _fields_ = [(n, _vp) for n in ("k", "v", "k_scale", "v_scale", "block_table", "lens", "seen", "weight", "order")] + \
+               [(n, _i) for n in ("B", "Hkv", "d", "page_size", "num_pages", "max_pages", "dtype")]
+
+
+_lib.fa_rope_spec_init.argtypes = [_vp, _i, _i, _i, _vp, _vp, _i]
+_lib.fa_rope_spec_init.restype = _i
+_lib.fa_rope.argtypes = [_vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _vp]
+_lib.fa_rope.restype = _i
+_lib.fa_cache_append.argtypes = [_vp] * 8 + [_i, _vp]
+_lib.fa_cache_append.restype = _i
+_lib.fa_decode_paged_workspace_bytes.argtypes = [_i] * 8
+_lib.fa_decode_paged_workspace_bytes.restype = _sz
+_lib.fa_decode_paged.argtypes = [_vp, _vp, _vp, _vp, _i, _i, _i, _f, _i, _vp, _sz, _vp]
+_lib.fa_decode_paged.restype = _i
+_lib.fa_cache_evict.argtypes = [_vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp]
+_lib.fa_cache_evict.restype = _i
+
+FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_TIMEOUT, FA_ERR_BAD_INDEX = range(6)
+FA_BF16, FA_F32, FA_E4M3 = range(3)
 
 
 class FAError(RuntimeError):
@@ -386,3 +416,302 @@ def attention_backward(q, k, v, o, lse, dO, causal: bool, scale: float, workspac
         (fa_bwd_deterministic if deterministic else fa_bwd)(q, k, v, o, lse, dO, dq, dk, dv, causal, scale, ws,
                                                             stream)
     return dq, dk, dv
+
+
+# ---------------------------------------------------------------- rotary positions
+class RopeSpec:
+    """Rotary positions of head width d: `freqs` gives the frequency of each of the rot / 2
+    pairs in radians per position, `axis` the axis of each pair (default: all on axis 0).
+    Pair i is features i and i + rot / 2, or, interleaved, 2i and 2i + 1; the d - rot features
+    behind the pairs pass through.  Host data only; keep it for all calls."""
+
+    def __init__(self, d: int, freqs, axis=None, interleaved: bool = False):
+        freqs = [float(f) for f in freqs]
+        axis = [0] * len(freqs) if axis is None else [int(a) for a in axis]
+        if len(axis) != len(freqs):
+            raise ValueError(f"axis: expected {len(freqs)} entries, got {len(axis)}")
+        if not freqs or len(freqs) > 128 or min(axis) < 0 or max(axis) > 255:
+            raise ValueError("freqs, axis: 8 to 128 pairs with axes from 0")
+        self.d, self.rot, self.n_axes, self.interleaved = int(d), 2 * len(freqs), max(axis) + 1, bool(interleaved)
+        self._c = _RopeSpec()
+        _check("fa_rope_spec_init", _lib.fa_rope_spec_init(
+            ctypes.byref(self._c), self.d, self.rot, self.n_axes, (ctypes.c_double * len(freqs))(*freqs),
+            (ctypes.c_ubyte * len(axis))(*axis), int(self.interleaved)))
+        self._ref = ctypes.addressof(self._c)
+
+
+def rope_spec(d: int, sections=None, base: float = 10000.0, rot: int | None = None,
+              interleaved: bool = False) -> RopeSpec:
+    """The usual frequencies base^(-2i / rot); `sections` splits the rot / 2 pairs into runs,
+    one per axis (for instance (16, 24, 24) for time, height and width at rot = 128)."""
+    rot = d if rot is None else rot
+    sections = (rot // 2,) if sections is None else tuple(sections)
+    if sum(sections) != rot // 2:
+        raise ValueError(f"sections: {sections} do not add up to {rot // 2} pairs")
+    axis = [a for a, n in enumerate(sections) for _ in range(n)]
+    return RopeSpec(d, [base ** (-2.0 * i / rot) for i in range(rot // 2)], axis, interleaved)
+
+
+def _on(device: torch.device, stream):
+    """The stream to launch on: the given one, else the current stream of the tensors' device."""
+    if stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return _stream(stream)
+
+
+class _device_of:
+    """Makes the tensors' device current for a call, if it is not."""
+
+    __slots__ = ("want", "had")
+
+    def __init__(self, device: torch.device):
+        if device.type != "cuda":
+            raise ValueError(f"expected CUDA tensors, got {device}")
+        self.want = device.index if device.index is not None else torch.cuda.current_device()
+
+    def __enter__(self):
+        self.had = torch.cuda.current_device()
+        if self.had != self.want:
+            torch.cuda.set_device(self.want)
+
+    def __exit__(self, *exc):
+        if self.had != self.want:
+            torch.cuda.set_device(self.had)
+
+
+def _record(stream, *tensors) -> None:
+    """Tells the allocator that tensors allocated here are used on `stream`."""
+    if stream is not None and hasattr(stream, "cuda_stream"):
+        for t in tensors:
+            t.record_stream(stream)
+
+
+def _heads(t: torch.Tensor, name: str, dtype, shape, device) -> _Heads:
+    """A [B, H, T, d] tensor by strides; only the last dimension has to be contiguous."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name}: expected device {device}, got {t.device}")
+    sb, sh, st, sd = t.stride()
+    if sd != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    # the stride of a dimension of one entry is never used: torch leaves any value there
+    B, H, T, _ = shape
+    return _Heads(t.data_ptr(), sb if B > 1 else 0, sh if H > 1 else 0, st if T > 1 else 0, H)
+
+
+def _rope(fn, q, q_out, positions, spec, k, k_out, inverse, stream):
+    if q.dim() != 4 or (k is None) != (k_out is None) or (k is not None and k.dim() != 4):
+        raise ValueError("q, k must be [B, H, T, d], with an output for each")
+    B, Hq, T, d = q.shape
+    dev = q.device
+    if d != spec.d:
+        raise ValueError(f"q: expected head width {spec.d}, got {d}")
+    _need(positions, "positions", torch.int32, (spec.n_axes, B, T), dev)
+    n = 1 if k is None else 2
+    x, y = (_Heads * 2)(), (_Heads * 2)()
+    x[0] = _heads(q, "q", q.dtype, q.shape, dev)
+    y[0] = _heads(q_out, "q_out", q.dtype, q.shape, dev)
+    if k is not None:
+        shape = torch.Size((B, k.shape[1], T, d))
+        x[1] = _heads(k, "k", q.dtype, shape, dev)
+        y[1] = _heads(k_out, "k_out", q.dtype, shape, dev)
+    if q.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"q: expected torch.bfloat16 or torch.float32, got {q.dtype}")
+    with _device_of(dev):
+        _check(fn, _lib.fa_rope(x, y, n, positions.data_ptr(), spec._ref, B, T,
+                                FA_F32 if q.dtype == torch.float32 else FA_BF16, inverse, _on(dev, stream)))
+
+
+def fa_rope(q, q_out, positions, spec: RopeSpec, k=None, k_out=None, stream=None) -> None:
+    """q_out = q [B, Hq, T, d] (and k_out = k [B, Hk, T, d]) with their pairs turned by the
+    positions, int32 [n_axes, B, T].  bf16 or float32; strided views with contiguous rows are
+    taken as they are; an output may be its input."""
+    _rope("fa_rope", q, q_out, positions, spec, k, k_out, 0, stream)
+
+
+def fa_rope_bwd(dq_out, dq, positions, spec: RopeSpec, k=None, k_out=None, stream=None) -> None:
+    """Backward of fa_rope: dq, the gradient of q, from dq_out, the gradient of q_out (and
+    k_out from k, the gradients of k and of the rotated k)."""
+    _rope("fa_rope_bwd", dq_out, dq, positions, spec, k, k_out, 1, stream)
+
+
+def rope_forward(q, k, positions, spec: RopeSpec, stream=None):
+    """Allocates contiguous outputs and runs fa_rope on q and k: what fa_fwd takes."""
+    q_out, k_out = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k))
+    fa_rope(q, q_out, positions, spec, k, k_out, stream)
+    _record(stream, q_out, k_out)
+    return q_out, k_out
+
+
+def rope_backward(dq_out, dk_out, positions, spec: RopeSpec, stream=None):
+    """Allocates and returns the gradients of q and k from those of rope_forward's outputs."""
+    dq, dk = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (dq_out, dk_out))
+    fa_rope_bwd(dq_out, dq, positions, spec, dk_out, dk, stream)
+    _record(stream, dq, dk)
+    return dq, dk
+
+
+# ---------------------------------------------------------------- paged key/value cache
+class KVCache:
+    """Handle of a paged cache (fa_kv_cache in include/fa.h): checks the tensors once and keeps
+    them.  k, v: [num_pages, Hkv, page_size, d] bf16, or uint8 e4m3 codes with k_scale and
+    v_scale [Hkv] float32; block_table [B, max_pages] int32; lens [B] int32 (entries of each
+    sequence, updated by the caller and by fa_cache_evict); seen [B] int32 (tokens ever
+    appended; default: lens); weight float32 and order int32 [B, Hkv, max_pages * page_size],
+    both optional.  The contents are read at each call, so tensors are changed in place."""
+
+    def __init__(self, k, v, block_table, lens, k_scale=None, v_scale=None, weight=None, order=None, seen=None):
+        if k.dim() != 4 or block_table.dim() != 2:
+            raise ValueError("k must be [num_pages, Hkv, page_size, d] and block_table [B, max_pages]")
+        dev = k.device
+        num_pages, Hkv, ps, d = k.shape
+        B, max_pages = block_table.shape
+        if k.dtype not in (torch.bfloat16, torch.uint8):
+            raise TypeError(f"k: expected torch.bfloat16 or torch.uint8 (e4m3 codes), got {k.dtype}")
+        _need(k, "k", k.dtype, (num_pages, Hkv, ps, d), dev)
+        _need(v, "v", k.dtype, (num_pages, Hkv, ps, d), dev)
+        _need(block_table, "block_table", torch.int32, (B, max_pages), dev)
+        _need(lens, "lens", torch.int32, (B,), dev)
+        codes = k.dtype == torch.uint8
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if (t is not None) != codes:
+                raise ValueError(f"{name}: needed with e4m3 codes and only with them")
+            if t is not None:
+                _need(t, name, torch.float32, (Hkv,), dev)
+        if seen is not None:
+            _need(seen, "seen", torch.int32, (B,), dev)
+        if weight is not None:
+            _need(weight, "weight", torch.float32, (B, Hkv, max_pages * ps), dev)
+        if order is not None:
+            _need(order, "order", torch.int32, (B, Hkv, max_pages * ps), dev)
+        self.k, self.v, self.block_table, self.lens = k, v, block_table, lens
+        self.k_scale, self.v_scale, self.weight, self.order, self.seen = k_scale, v_scale, weight, order, seen
+        self.B, self.Hkv, self.d, self.page_size, self.num_pages, self.max_pages = B, Hkv, d, ps, num_pages, max_pages
+        self.device = dev
+        self._c = _KVCache(*(_ptr(t) for t in (k, v, k_scale, v_scale, block_table, lens, seen, weight, order)),
+                           B, Hkv, d, ps, num_pages, max_pages, FA_E4M3 if codes else FA_BF16)
+        self._ref = ctypes.addressof(self._c)
+
+
+def alloc_kv_cache(B: int, Hkv: int, d: int, max_len: int, page_size: int = 16, k_scale=None, v_scale=None,
+                   weight: bool = False, device="cuda") -> KVCache:
+    """An empty cache with pages of its own for every sequence, up to max_len entries each: bf16,
+    or e4m3 when the scales are given; with `weight` the accumulated weights, arrival numbers
+    and token counts that eviction needs."""
+    pages = -(-max_len // page_size)
+    i32 = dict(dtype=torch.int32, device=device)
+    dt = torch.bfloat16 if k_scale is None else torch.uint8
+    k, v = (torch.zeros((B * pages, Hkv, page_size, d), dtype=dt, device=device) for _ in range(2))
+    table = torch.arange(B * pages, **i32).view(B, pages)
+    slots = (B, Hkv, pages * page_size)
+    return KVCache(k, v, table, torch.zeros(B, **i32), k_scale, v_scale,
+                   torch.zeros(slots, dtype=torch.float32, device=device) if weight else None,
+                   torch.zeros(slots, **i32) if weight else None, torch.zeros(B, **i32) if weight else None)
+
+
+def fa_cache_append(cache: KVCache, k, v, positions=None, spec: RopeSpec | None = None, q=None, q_out=None,
+                    new_lens=None, stream=None) -> None:
+    """Writes the first new_lens[b] (default: all) of the T rows of k and v [B, Hkv, T, d] as the
+    last entries of sequence b; cache.lens (and seen) count them already.  With a spec, k is
+    rotated by positions [n_axes, B, T] on the way, and q [B, Hq, T, d] into q_out."""
+    dev, B = cache.device, cache.B
+    if k.dim() != 4 or (q is not None and q.dim() != 4):
+        raise ValueError("k, v, q must be [B, H, T, d]")
+    T = k.shape[2]
+    shape = torch.Size((B, cache.Hkv, T, cache.d))
+    kh, vh = _heads(k, "k", torch.bfloat16, shape, dev), _heads(v, "v", torch.bfloat16, shape, dev)
+    if (positions is None) != (spec is None):
+        raise ValueError("positions and spec come together")
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out come together")
+    if q is not None and spec is None:
+        raise ValueError("q is rotated: it needs a spec and positions")
+    pos = qh = oh = new = None
+    if spec is not None:
+        _need(positions, "positions", torch.int32, (spec.n_axes, B, T), dev)
+        pos = positions.data_ptr()
+    if q is not None:
+        qshape = torch.Size((B, q.shape[1], T, cache.d))
+        qh = ctypes.byref(_heads(q, "q", torch.bfloat16, qshape, dev))
+        oh = ctypes.byref(_heads(q_out, "q_out", torch.bfloat16, qshape, dev))
+    if new_lens is not None:
+        _need(new_lens, "new_lens", torch.int32, (B,), dev)
+        new = new_lens.data_ptr()
+    with _device_of(dev):
+        _check("fa_cache_append", _lib.fa_cache_append(
+            cache._ref, ctypes.byref(kh), ctypes.byref(vh), qh, oh, pos, None if spec is None else spec._ref, new, T,
+            _on(dev, stream)))
+
+
+def fa_decode_paged_workspace_bytes(cache: KVCache, Hq: int, Tq: int = 1, accumulate: bool = False) -> int:
+    """Workspace of fa_decode_paged for these sizes, 0 for sizes that it refuses."""
+    return int(_lib.fa_decode_paged_workspace_bytes(cache.B, Hq, cache.Hkv, Tq, cache.max_pages, cache.page_size,
+                                                    cache.d, int(bool(accumulate))))
+
+
+def fa_decode_paged(cache: KVCache, q, o, lse, scale: float, workspace: torch.Tensor, causal: bool = True,
+                    accumulate: bool = False, stream=None) -> None:
+    """O and lse of q [B, Hq, Tq, d] (the last Tq tokens of every sequence) over the cache; with
+    `accumulate`, cache.weight grows by each entry's attention probabilities."""
+    dev = cache.device
+    if q.dim() != 4:
+        raise ValueError("q must be [B, Hq, Tq, d]")
+    B, Hq, Tq, d = q.shape
+    shape = (cache.B, Hq, Tq, cache.d)
+    _need(q, "q", torch.bfloat16, shape, dev)
+    _need(o, "o", torch.bfloat16, shape, dev)
+    _need(lse, "lse", torch.float32, shape[:3], dev)
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace: must be a contiguous tensor on the same device")
+    with _device_of(dev):
+        _check("fa_decode_paged", _lib.fa_decode_paged(
+            cache._ref, q.data_ptr(), o.data_ptr(), lse.data_ptr(), Hq, Tq, int(bool(causal)), float(scale),
+            int(bool(accumulate)), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+            _on(dev, stream)))
+
+
+def attention_decode_paged(cache: KVCache, q, scale: float, causal: bool = True, accumulate: bool = False,
+                           workspace=None, stream=None):
+    """Allocates O, lse (and the workspace if not given) and runs fa_decode_paged."""
+    if q.dim() != 4:
+        raise ValueError("q must be [B, Hq, Tq, d]")
+    o = torch.empty_like(q)
+    lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+    if workspace is None:
+        n = fa_decode_paged_workspace_bytes(cache, q.shape[1], q.shape[2], accumulate)
+        workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
+    fa_decode_paged(cache, q, o, lse, scale, workspace, causal, accumulate, stream)
+    _record(stream, o, lse, workspace)
+    return o, lse
+
+
+def fa_cache_evict(cache: KVCache, budget: int, weight_out=None, order_out=None, lens_out=None, kept=None,
+                   n_first: int = 0, n_recent: int = 0, stream=None) -> torch.Tensor:
+    """Keeps min(lens, budget) entries of each sequence and KV head: the first n_first and last
+    n_recent tokens, then those of the largest cache.weight.  K and V rows move in place; weight,
+    order and lens are updated in place unless outputs are given.  Returns kept, int32
+    [B, Hkv, budget]: the old slot of each entry, -1 behind the new length."""
+    dev = cache.device
+    if cache.weight is None:
+        raise ValueError("the cache has no weight")
+    weight_out = cache.weight if weight_out is None else weight_out
+    order_out = cache.order if order_out is None else order_out
+    lens_out = cache.lens if lens_out is None else lens_out
+    _need(weight_out, "weight_out", torch.float32, cache.weight.shape, dev)
+    if (order_out is None) != (cache.order is None):
+        raise ValueError("order_out: needed with a cache that has an order and only with it")
+    if order_out is not None:
+        _need(order_out, "order_out", torch.int32, cache.weight.shape, dev)
+    _need(lens_out, "lens_out", torch.int32, (cache.B,), dev)
+    if kept is None:
+        kept = torch.empty((cache.B, cache.Hkv, max(int(budget), 0)), dtype=torch.int32, device=dev)
+        _record(stream, kept)
+    _need(kept, "kept", torch.int32, (cache.B, cache.Hkv, budget), dev)
+    with _device_of(dev):
+        _check("fa_cache_evict", _lib.fa_cache_evict(
+            cache._ref, int(budget), int(n_first), int(n_recent), weight_out.data_ptr(), _ptr(order_out),
+            lens_out.data_ptr(), kept.data_ptr(), _on(dev, stream)))
+    return kept

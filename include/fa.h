@@ -32,7 +32,9 @@
  * Errors.  Calls are asynchronous on `stream` (a cudaStream_t; NULL is the
  * legacy default stream).  The return value reports argument validation and
  * launch errors only.  A device-side failure (a bounded wait that timed out)
- * is recorded in a per-device status word and returned by fa_sync_status().
+ * is recorded in a per-device status word and returned by fa_sync_status();
+ * so is a length, count or page number in device memory that is out of range
+ * (the cache calls below, which then leave that sequence or page alone).
  * On any nonzero return, no kernel was launched and outputs are untouched,
  * except FA_ERR_CUDA from a failed launch.
  */
@@ -50,7 +52,9 @@ typedef enum {
     FA_ERR_INVALID_ARG = 1,   /* null/misaligned pointer, bad size, aliasing outputs, bad scale */
     FA_ERR_UNSUPPORTED = 2,   /* head width not supported, or the device is not sm_103 */
     FA_ERR_CUDA = 3,          /* a CUDA runtime/driver call failed */
-    FA_ERR_TIMEOUT = 4        /* a device-side bounded wait ran out (from fa_sync_status) */
+    FA_ERR_TIMEOUT = 4,       /* a device-side bounded wait ran out (from fa_sync_status) */
+    FA_ERR_BAD_INDEX = 5      /* a length, count or page number on the device is out of range
+                                 (from fa_sync_status) */
 } fa_status;
 
 typedef struct CUstream_st *fa_stream_t;   /* identical to cudaStream_t */
@@ -156,6 +160,171 @@ size_t fa_decode_workspace_bytes(int B, int H, int Tq, int Tk, int d);   /* 0: i
 int fa_decode(const void *q, const void *k, const void *v, void *o, float *lse,
               int B, int H, int Tq, int Tk, int d, int causal, float scale,
               void *workspace, size_t workspace_bytes, fa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Rotary positions and the paged key/value cache.  One serving step is
+ *     fa_cache_append (rotate q and k, write k and v into the pages)
+ *     fa_decode_paged (attend over the pages, add up the attention weights)
+ *     fa_cache_evict  (now and then: give the least used entries back)
+ * and fa_rope is the rotation by itself, before fa_fwd and, transposed, after
+ * fa_bwd.
+ * ------------------------------------------------------------------------ */
+
+/* Element types of fa_rope and of a cache. */
+typedef enum {
+    FA_BF16 = 0,
+    FA_F32 = 1,
+    FA_E4M3 = 2
+} fa_dtype;
+
+/*
+ * A [B][H][T][d] tensor by strides, in elements; the d values of a row are
+ * contiguous.  Strides are nonnegative and, in bytes, multiples of 16 (a view
+ * of a packed [B][T][heads][d] projection is one).
+ */
+typedef struct {
+    void *data;
+    long long stride_b, stride_h, stride_t;
+    int H;
+} fa_heads;
+
+/*
+ * Rotary positions with up to FA_ROPE_MAX_AXES axes (time, height, width, ...).
+ * The first `rot` of the d features form rot / 2 pairs (x_i, y_i): features i
+ * and i + rot / 2, or, interleaved, 2i and 2i + 1.  Pair i turns by
+ * theta_i = p f_i with f_i its frequency (radians per position) and p the
+ * token's position on the pair's axis:
+ *     x_i' = x_i cos theta_i - y_i sin theta_i
+ *     y_i' = y_i cos theta_i + x_i sin theta_i
+ * Features from rot on pass through.  Angles are exact to 2^-32 turns plus the
+ * rounding of f_i to 2^-64 turns times the position, however far the position.
+ * Fill it with fa_rope_spec_init (host memory; nothing on the device).
+ */
+#define FA_ROPE_MAX_AXES 8
+typedef struct {
+    int d, rot, n_axes, interleaved;
+    unsigned long long turns[128];   /* f_i / 2 pi in units of 2^-64 turns */
+    unsigned char axis[128];
+} fa_rope_spec;
+
+/*
+ * d in {64, 128, 256}; rot a multiple of 16, 16 <= rot <= d; freqs: rot / 2
+ * finite values, |f| < 2^31; axis: rot / 2 values below n_axes (1 to
+ * FA_ROPE_MAX_AXES), or NULL for axis 0 throughout; interleaved 0 or 1.
+ */
+int fa_rope_spec_init(fa_rope_spec *spec, int d, int rot, int n_axes, const double *freqs,
+                      const unsigned char *axis, int interleaved);
+
+/*
+ * y = x rotated, for n (1 or 2, such as q and k) tensors that share B, T and
+ * the positions: x[i], y[i] with x[i].H == y[i].H.  inverse = 1 turns the other
+ * way, which is the rotation's transpose: applied to the gradient of y it gives
+ * the gradient of x.  positions: int32 [n_axes][B][T] in device memory, any
+ * value.  dtype FA_BF16 or FA_F32, for x and y alike; the arithmetic is fp32,
+ * rounded once.  y[i] may be x[i] itself (same data and strides); otherwise no
+ * element of y is shared with x, with the positions or within y (checked where
+ * the tensors are contiguous; strided views of one buffer are the caller's
+ * care).  B, T and H may be 0.
+ */
+int fa_rope(const fa_heads *x, const fa_heads *y, int n, const int *positions, const fa_rope_spec *spec,
+            int B, int T, int dtype, int inverse, fa_stream_t stream);
+
+/*
+ * A paged cache of B sequences, all pointers to device memory:
+ *   k, v         [num_pages][Hkv][page_size][d], bf16 (FA_BF16) or e4m3 codes
+ *                (FA_E4M3), 128-byte aligned
+ *   k_scale, v_scale  [Hkv] f32, FA_E4M3 only: a code c of head h stands for
+ *                c * scale[h] (positive, finite); NULL for FA_BF16
+ *   block_table  [B][max_pages] int32: entry i of sequence b (its slot i) is
+ *                row i % page_size of page block_table[b][i / page_size]
+ *   lens         [B] int32: entries of each sequence, 0 to max_pages * page_size
+ *   seen         [B] int32: tokens ever appended to each sequence; NULL: lens
+ *                (right until something is evicted)
+ *   weight       [B][Hkv][max_pages * page_size] f32: accumulated attention
+ *                weight of each entry, or NULL
+ *   order        [B][Hkv][max_pages * page_size] int32: arrival number of each
+ *                entry (the first token of a sequence has 0), or NULL
+ * page_size is 16, 32, 64, 128 or 256; d 64, 128 or 256.  Only the pages and
+ * rows in front of lens are read: what lies behind them may hold anything.
+ * Sequences may share pages that none of them writes to (fa_cache_append and
+ * fa_cache_evict write).  num_pages * Hkv and B * Hkv must fit in 31 bits, and
+ * max_pages * page_size too.  The struct is read during the call only; a page
+ * number outside 0 .. num_pages - 1 in front of lens, or a length outside its
+ * range, is FA_ERR_BAD_INDEX from fa_sync_status and is never dereferenced.
+ */
+typedef struct {
+    void *k, *v;
+    const float *k_scale, *v_scale;
+    const int *block_table;
+    const int *lens;
+    const int *seen;
+    float *weight;
+    int *order;
+    int B, Hkv, d, page_size, num_pages, max_pages;
+    int dtype;
+} fa_kv_cache;
+
+/*
+ * Writes new tokens into the cache.  k and v: bf16 [B][Hkv][T][d] by strides.
+ * Of sequence b the first new_lens[b] (NULL: T) of its T rows are new tokens;
+ * `lens` counts them already: they take slots lens[b] - new_lens[b] up to
+ * lens[b] - 1, in order, with weight 0 and arrival number seen[b] - new_lens[b]
+ * onwards.  Rows past new_lens[b] are not read, and nothing else is written.
+ * With a spec, k is rotated first (fp32, positions as in fa_rope: [n_axes][B][T]),
+ * and q, if given, is rotated into q_out (bf16 [B][Hq][T][d] by strides; q_out
+ * may be q; rows past new_lens[b] are left alone).  Without a spec, positions, q
+ * and q_out are NULL.  What is written is the fp32 value rounded once to bf16,
+ * or to e4m3 after division by the head's scale (to nearest even, saturating at
+ * +-448; NaN stays NaN).  The new rows of different sequences must fall on
+ * different pages.  A sequence with new_lens outside 0 .. min(T, lens) is left
+ * alone (FA_ERR_BAD_INDEX).
+ */
+int fa_cache_append(const fa_kv_cache *cache, const fa_heads *k, const fa_heads *v, const fa_heads *q,
+                    const fa_heads *q_out, const int *positions, const fa_rope_spec *spec,
+                    const int *new_lens, int T, fa_stream_t stream);
+
+/*
+ * Attention of the last Tq (1 to 16) tokens of every sequence over the cache:
+ * q, o bf16 [B][Hq][Tq][d], lse f32 [B][Hq][Tq], contiguous.  Hq is a multiple
+ * of Hkv; query head h reads KV head h / (Hq / Hkv).  With causal != 0 row t sees
+ * slots up to lens[b] - Tq + t (bottom-right, as fa_decode; the Tq rows' own
+ * tokens are the last entries), else every slot.  A row that sees nothing gets
+ * O = 0 and lse = -inf.  Scores, statistics and the row sums are fp32; the
+ * keys are split over the thread blocks in equal shares of the whole batch, and
+ * partial results are joined in a fixed order: the same call gives the same
+ * bits, but a sequence's last bits may depend on the other lengths.
+ * accumulate = 1 adds, for every entry, the sum of its probabilities over the
+ * head group's rows (Hq / Hkv heads x Tq) to cache->weight.
+ * workspace: fa_decode_paged_workspace_bytes bytes, 256-byte aligned, contents
+ * on entry ignored, not shared by calls that may overlap in time.  A sequence
+ * with a length out of range counts as empty, a page out of range as masked.
+ */
+size_t fa_decode_paged_workspace_bytes(int B, int Hq, int Hkv, int Tq, int max_pages, int page_size, int d,
+                                       int accumulate);   /* 0: invalid or unsupported sizes */
+int fa_decode_paged(const fa_kv_cache *cache, const void *q, void *o, float *lse, int Hq, int Tq, int causal,
+                    float scale, int accumulate, void *workspace, size_t workspace_bytes, fa_stream_t stream);
+
+/*
+ * Evicts, for every sequence and KV head on its own, down to `budget` (>= 1)
+ * entries.  Kept are the min(lens, budget) first ones in this order: protected
+ * entries (arrival number below n_first, or at least seen - n_recent), then by
+ * larger weight, a NaN counting as the least; of equals the lower slot.  The
+ * kept entries that lie behind the new length move, in order, into the slots of
+ * the evicted ones in front of it: nothing else moves, so the order of slots is
+ * not the order of arrival afterwards (`order` has that).  Written:
+ *   K and V rows of the moved entries, in place;
+ *   kept       [B][Hkv][budget] int32: the old slot of each entry, -1 behind the
+ *              new length;
+ *   weight_out, order_out  like cache->weight and cache->order (which they may
+ *              be), the entries in front of the new length only; order_out NULL
+ *              exactly when cache->order is;
+ *   lens_out   [B] int32 (may be cache->lens): min(lens, budget).
+ * n_first, n_recent >= 0 with n_first + n_recent <= budget; either one > 0 needs
+ * cache->order.  cache->weight is needed.  A sequence with a length out of range
+ * is left alone; so is a row whose page is out of range.
+ */
+int fa_cache_evict(const fa_kv_cache *cache, int budget, int n_first, int n_recent, float *weight_out,
+                   int *order_out, int *lens_out, int *kept, fa_stream_t stream);
 
 /*
  * Bytes of device workspace fa_bwd and fa_bwd_deterministic need for these
@@ -275,7 +444,8 @@ int fa_bwd_noalloc(const void *q, const void *k, const void *v, const void *o, c
 /*
  * Synchronises `stream`, then returns and clears the device status word of
  * the current device: FA_OK, FA_ERR_TIMEOUT (a kernel's bounded wait ran out;
- * its outputs are invalid) or FA_ERR_CUDA (the synchronise failed).
+ * its outputs are invalid), FA_ERR_BAD_INDEX (see fa_kv_cache) or FA_ERR_CUDA
+ * (the synchronise failed).
  */
 int fa_sync_status(fa_stream_t stream);
 
