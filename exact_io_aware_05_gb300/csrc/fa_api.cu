@@ -82,6 +82,27 @@ int encode_tmap_3d_strided(CUtensorMap *map, const void *base, CUtensorMapDataTy
 }
 
 
+int encode_tmap(CUtensorMap *map, const void *base, CUtensorMapDataType dtype, int rank, const uint64_t *dims,
+                const uint64_t *strides, const uint32_t *box, CUtensorMapSwizzle swizzle)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn || rank > 5)
+        return ERR_CUDA;
+    cuuint64_t gd[5], gs[5];
+    cuuint32_t bx[5], es[5];
+    for (int i = 0; i < rank; ++i) {
+        gd[i] = dims[i];
+        bx[i] = box[i];
+        es[i] = 1;
+        if (i + 1 < rank)
+            gs[i] = strides[i];
+    }
+    return fn(map, dtype, (cuuint32_t)rank, const_cast<void *>(base), gd, gs, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? OK
+               : ERR_CUDA;
+}
+
 int device_sm_count()
 {
     static int cache[kMaxDevices] = {0};

@@ -140,6 +140,11 @@ int fwd_status_fetch_clear(cudaStream_t s, int *host_word);
 int bwd_status_fetch_clear(cudaStream_t s, int *host_word);
 int dec_status_fetch_clear(cudaStream_t s, int *host_word);
 
+// Encodes a tiled TMA map of `rank` dimensions (innermost first; strides in bytes of all but the
+// innermost) with the given swizzle.  Returns OK or ERR_CUDA.
+int encode_tmap(CUtensorMap *map, const void *base, CUtensorMapDataType dtype, int rank, const uint64_t *dims,
+                const uint64_t *strides, const uint32_t *box, CUtensorMapSwizzle swizzle);
+
 // Rotary positions and the paged cache (fa_cache_sm103.cu, fa_paged_sm103.cu); arguments
 // already validated by fa_cache_api.cu.  Structures as in include/fa.h.
 int rope_launch(const fa_heads *x, const fa_heads *y, int n, const int *positions, const fa_rope_spec &spec, int B,

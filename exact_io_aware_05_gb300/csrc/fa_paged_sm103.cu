@@ -3,9 +3,30 @@
 //
 // Formulas, per sequence, KV head and query row r of its head group: s_j = c q_r . k_j over the
 // row's slots j, m = max s, p_j = e^{s_j - m} / l with l = sum e^{s_j - m}, o = sum p_j v_j,
-// lse = m + ln l; with accumulate, weight_j += sum_r p_j.  The slots are split into chunks, each
-// chunk leaves (m, l, sum e^{s - m} v) per row, and a second kernel joins them.
+// lse = m + ln l; with accumulate, weight_j += sum_r p_j.  Everything below is in log2 units.
+//
+// What bounds it: K and V are read once, 4 d bytes an entry in bf16, and M = Hq / Hkv * Tq rows use
+// them: 2 M / 2 flops a byte, far below the device's ratio for M up to 64.  So the design is
+// about keeping loads in flight and spreading them evenly:
+//   * The batch's tiles of 64 entries (all sequences and KV heads in a row) are cut into equal
+//     shares, one per CTA, whatever the lengths: a share begins and ends anywhere, so at most its
+//     first and last head are partial, and a partial state (m, l, sum e^{s - m} v) goes to one of
+//     the CTA's two workspace slots.  A second kernel, launched early and waiting for the first,
+//     joins the slots of each head in order (the same bits on every run).
+//   * One warp fills a ring of tiles by TMA, a box per page (all 128-byte column chunks of its
+//     rows at once, swizzled); page numbers are read one tile ahead.
+//   * Four warps compute with m16n8k16 products out of registers (ldmatrix): a warp owns 16 query
+//     rows and a quarter, half or all of a tile's entries (1, 2 or 4 row tiles).  The tensor cores
+//     of the fifth generation want 128 rows a product; with 1 to 64 rows they would run mostly
+//     empty, and their accumulators would have to come back for the softmax: the warp-level
+//     products leave S in the registers that P V takes.
+//   * P enters its product as two bf16 numbers (its leading 8 bits and the rest), so its error is
+//     2^-17 and not 2^-9, which would be as large as the output's own rounding.  e4m3 codes become
+//     f16 exactly; there q is scaled by a power of two per row and P by 2^15, which keeps
+//     probabilities down to 2^-29 in f16's normal range, with 11 bits.
 #include <climits>
+
+#include <cuda_fp16.h>
 
 #include "fa_common.cuh"
 #include "fa_internal.h"
@@ -17,30 +38,118 @@ __device__ int g_paged_status;   // device status word of the kernels in this fi
 namespace {
 
 constexpr int kStatusBadIndex = 5;
-constexpr int kChunk = 256;      // slots a CTA
+constexpr int KT = 64;           // entries a tile
+constexpr int kMathWarps = 4;
+constexpr int kThreads = 32 * (kMathWarps + 1);
+constexpr int kSMs = 152;        // the grid is made for the GB300's; results depend on it, not on the device
+constexpr int kMaxRows = 64;     // query rows of a head group that one CTA takes at a time
+constexpr float kPShift = 15.f;  // e4m3: probabilities are scaled by 2^15
+
+enum PagedSite : int { SITE_PAGED_FULL = 1, SITE_PAGED_EMPTY = 2 };
+
+template <int D, bool FP8, int RT>
+struct Cfg {
+    static constexpr int ELEM = FP8 ? 1 : 2;
+    static constexpr int ROWB = D * ELEM;                          // bytes of an entry's K or V row
+    static constexpr int CB = ROWB < 128 ? ROWB : 128;             // bytes of a column chunk
+    static constexpr int TILE = KT * ROWB;                         // K or V of a tile
+    static constexpr int STAGE = 2 * TILE;
+    static constexpr int QPITCH = D * 2 + 16;                      // bytes of a query row in shared memory
+    static constexpr int OC = 32;                                  // features merged at a time
+    static constexpr int OPITCH = OC + 4;                          // floats of a merge row
+    static constexpr int NQ = RT * 16 * QPITCH, NO = kMathWarps * 16 * OPITCH * 4, NML = kMathWarps * 16 * 8;
+    static constexpr int SMALL = 1024 + NQ + NO + NML + RT * 16 * 4 + 24 * 12 + 64;
+    // two CTAs an SM where the accumulators leave registers for it; the ring takes what is left
+    static constexpr int CTAS = D == 256 ? 1 : 2;
+    static constexpr int FIT = ((CTAS == 2 ? 113 : 227) * 1024 - SMALL) / STAGE;
+    static constexpr int NST = FIT < 12 ? FIT : 12;
+    static_assert(NST >= 2, "shared memory");
+    static constexpr int OFF_Q = NST * STAGE;
+    static constexpr int OFF_O = OFF_Q + NQ;
+    static constexpr int OFF_ML = OFF_O + NO;
+    static constexpr int OFF_RS = OFF_ML + NML;                    // scale of each row's scores
+    static constexpr int OFF_BAR = OFF_RS + RT * 16 * 4;           // full[NST], empty[NST]
+    static constexpr int OFF_OK = OFF_BAR + 16 * NST;              // per stage: which 16-entry groups are there
+    static constexpr int OFF_MISC = (OFF_OK + 4 * NST + 15) / 16 * 16;   // abort flag, reduction scratch
+    static constexpr int SMEM = OFF_MISC + 16 + 8 * (kMathWarps + 1) + 1024;
+    static_assert(SMEM <= 227 * 1024, "shared memory");
+};
 
 struct PagedArgs {
     const __nv_bfloat16 *q;
     __nv_bfloat16 *o;
     float *lse, *weight;
-    const void *k, *v;
     const float *ks, *vs;
     const int *block_table, *lens;
-    float *part;     // [unit][chunk][row][D + 2]
-    float *scores;   // [unit][row][cap], log2 units
-    int Hq, Hkv, G, Tq, causal, num_pages, max_pages, ps_shift, cap, chunks;
+    float *part;     // [2 grid][rows][D] then m, l [rows]
+    float *scores;   // [sequence][KV head][row][cap]
+    int B, Hq, Hkv, G, Tq, M, rows, RB, causal, num_pages, max_pages, ps_shift, cap, grid;
     float scale_log2;
+    uint64_t timeout_ns;
 };
 
-template <bool FP8>
-__device__ __forceinline__ float element(const void *p, long long i)
+// ------------------------------------------------------------------ instructions
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr)
 {
-    if constexpr (FP8)
-        return __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<const uint8_t *>(p)[i], __NV_E4M3)));
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+template <bool HALF>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    if constexpr (HALF)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                     "{%0, %1, %2, %3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
     else
-        return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                     "{%0, %1, %2, %3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Two e4m3 codes (in the low or high half of x) as two f16.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t x)
+{
+    uint32_t y;
+    asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
+{
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int y, int z, int w)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+        : "memory");
+}
+__device__ __forceinline__ void math_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kMathWarps) : "memory"); }
+__device__ __forceinline__ float quad_max(float x)
+{
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+    return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+}
+__device__ __forceinline__ float quad_sum(float x)
+{
+    x += __shfl_xor_sync(0xffffffffu, x, 1);
+    return x + __shfl_xor_sync(0xffffffffu, x, 2);
 }
 
+// ------------------------------------------------------------------ shares
 __device__ __forceinline__ int length_of(const PagedArgs &a, int b)
 {
     const int len = a.lens[b];
@@ -50,155 +159,713 @@ __device__ __forceinline__ int length_of(const PagedArgs &a, int b)
     }
     return len;
 }
+__device__ __forceinline__ int tiles_of(const PagedArgs &a, int b) { return (length_of(a, b) + KT - 1) / KT; }
 
-// Slots row r = g Tq + t of a head group sees.
-__device__ __forceinline__ int seen_by(const PagedArgs &a, int len, int r)
+// Tiles a CTA takes of the batch's `total`: equal shares, but at least 2, below which the
+// joining costs more than the tile.
+__device__ __forceinline__ long long share_of(const PagedArgs &a, long long total)
 {
-    return a.causal ? len - a.Tq + r % a.Tq + 1 : len;
+    const long long c = (total + a.grid - 1) / a.grid;
+    return c < 2 ? 2 : c;
 }
 
-// Block-wide maximum and sum over kChunk threads.
-template <bool MAX>
-__device__ __forceinline__ float block_reduce(float x, float *scratch)
+__device__ __forceinline__ long long warp_sum64(long long x)
 {
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        const float y = __shfl_xor_sync(0xffffffffu, x, off);
-        x = MAX ? fmaxf(x, y) : x + y;
-    }
-    __syncthreads();
-    if (lane_id() == 0)
-        scratch[warp_id()] = x;
-    __syncthreads();
-    x = scratch[0];
-    for (int i = 1; i < kChunk / 32; ++i)
-        x = MAX ? fmaxf(x, scratch[i]) : x + scratch[i];
+    for (int off = 16; off > 0; off >>= 1)
+        x += __shfl_xor_sync(0xffffffffu, x, off);
     return x;
 }
 
-template <int D, bool FP8>
-__global__ void __launch_bounds__(kChunk) paged_kernel(const __grid_constant__ PagedArgs a)
+// Tiles of sequences [0, n) per KV head and row block, over the whole block of threads.
+__device__ __forceinline__ long long block_tiles(const PagedArgs &a, int n, volatile long long *scratch)
 {
-    __shared__ float q[D], p[kChunk], scratch[8];
-    __shared__ long long rows[kChunk];
-    const long long unit = blockIdx.x / a.chunks;
-    const int chunk = (int)(blockIdx.x - unit * a.chunks), tid = threadIdx.x;
-    const int b = (int)(unit / a.Hkv), h = (int)(unit - (long long)b * a.Hkv), M = a.G * a.Tq;
-    const int len = length_of(a, b), slot = chunk * kChunk + tid;
-    if (chunk * kChunk >= len)
+    long long x = 0;
+    for (int b = threadIdx.x; b < n; b += blockDim.x)
+        x += tiles_of(a, b);
+    x = warp_sum64(x);
+    if (lane_id() == 0)
+        scratch[warp_id()] = x;
+    __syncthreads();
+    x = 0;
+    for (int w = 0; w < (int)blockDim.x / 32; ++w)
+        x += scratch[w];
+    __syncthreads();
+    return x;
+}
+
+// A CTA's place in the batch's tiles: sequence b, unit ul (row block, KV head) in it, tile.
+struct Place {
+    int b, ul, tile, nt;
+    long long left;   // tiles still to do
+};
+
+__device__ __forceinline__ Place place_of(const PagedArgs &a, long long t0, long long left)
+{
+    const int per = a.Hkv * a.RB, lane = (int)lane_id();
+    Place p{a.B, 0, 0, 0, left};
+    long long base = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+        const int b = b0 + lane;
+        const int nt = b < a.B ? tiles_of(a, b) : 0;
+        long long inc = (long long)nt * per;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, inc, off);
+            if (lane >= off)
+                inc += y;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, base + inc > t0);
+        if (past) {
+            const int src = __ffs(past) - 1;
+            const long long end = base + __shfl_sync(0xffffffffu, inc, src);
+            p.nt = __shfl_sync(0xffffffffu, nt, src);
+            p.b = b0 + src;
+            const long long in = t0 - (end - (long long)p.nt * per);
+            p.ul = (int)(in / p.nt);
+            p.tile = (int)(in - (long long)p.ul * p.nt);
+            return p;
+        }
+        base += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    return p;
+}
+
+// Tiles of the current unit that belong to this CTA; and on to the next unit.
+__device__ __forceinline__ int segment(const Place &p) { return (int)min((long long)(p.nt - p.tile), p.left); }
+__device__ __forceinline__ void next_unit(const PagedArgs &a, Place &p, int done)
+{
+    p.left -= done;
+    p.tile = 0;
+    if (p.left > 0 && ++p.ul == a.Hkv * a.RB) {
+        p.ul = 0;
+        do {
+            ++p.b;
+            p.nt = tiles_of(a, p.b);
+        } while (p.nt == 0);
+    }
+}
+
+// ------------------------------------------------------------------ attention
+template <int D, bool FP8, int RT>
+__global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
+    paged_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                 const __grid_constant__ PagedArgs a)
+{
+    using C = Cfg<D, FP8, RT>;
+    constexpr int KW = kMathWarps / RT;             // warps that share a row tile's entries
+    constexpr int KSTEPS = D / 16;                  // products along the head width, per 8 entries
+    constexpr bool QREG = D <= 64;                  // query fragments stay in registers
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t sbase = (raw + 1023u) & ~1023u;
+    uint8_t *smem = smem_raw + (sbase - raw);
+    const uint32_t bar0 = sbase + C::OFF_BAR;
+    volatile uint32_t *there = reinterpret_cast<volatile uint32_t *>(smem + C::OFF_OK);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_MISC);
+    const int lane = (int)lane_id(), warp = (int)warp_id();
+    const WaitCtx ctx{abort_flag, &g_paged_status, a.timeout_ns};
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::NST; ++s) {
+            mbar_init(bar0 + 8u * s, 1);
+            mbar_init(bar0 + 8u * (C::NST + s), kMathWarps);
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    const long long total = block_tiles(a, a.B, reinterpret_cast<volatile long long *>(smem + C::OFF_MISC + 16)) *
+                            a.Hkv * a.RB;
+    const long long share = share_of(a, total), t0 = share * blockIdx.x;
+    if (t0 >= total)
         return;
-    long long at = -1;
-    if (slot < len) {
-        const int page = a.block_table[(long long)b * a.max_pages + (slot >> a.ps_shift)];
-        if (page >= 0 && page < a.num_pages)
-            at = ((((long long)page * a.Hkv + h) << a.ps_shift) + (slot & ((1 << a.ps_shift) - 1))) * D;
-        else
-            atomicCAS(&g_paged_status, 0, kStatusBadIndex);
-    }
-    rows[tid] = at;
-    const float ks = FP8 ? a.ks[h] : 1.f, vs = FP8 ? a.vs[h] : 1.f;
-    for (int r = 0; r < M; ++r) {
-        const __nv_bfloat16 *qg = a.q + (((long long)b * a.Hq + h * a.G) * a.Tq + r) * D;
-        __syncthreads();
-        for (int e = tid; e < D; e += kChunk)
-            q[e] = __bfloat162float(qg[e]);
-        __syncthreads();
-        float s = -INFINITY;
-        if (at >= 0 && slot < seen_by(a, len, r)) {
-            float dot = 0.f;
-            for (int e = 0; e < D; ++e)
-                dot = fmaf(q[e], element<FP8>(a.k, at + e), dot);
-            s = dot * (ks * a.scale_log2);
+    Place p = place_of(a, t0, min(share, total - t0));
+    // rows of a page in one box, and boxes of a tile
+    const int bp_shift = a.ps_shift < 6 ? a.ps_shift : 6, boxes = KT >> bp_shift;
+
+    if (warp == kMathWarps) {
+        // ---------------------------------------------------------- loads: lane 2 i is K of box i, 2 i + 1 V
+        const bool mine = lane < 2 * boxes;
+        const CUtensorMap *map = (lane & 1) ? &tm_v : &tm_k;
+        const int box = lane >> 1;
+        const uint32_t dst = (uint32_t)((lane & 1) * C::TILE + (box << bp_shift) * C::ROWB);
+        const uint32_t box_bytes = (uint32_t)(C::ROWB << bp_shift);
+        if (lane < 2)
+            tma_prefetch_desc(map);
+        uint32_t n = 0;
+        bool ok = true;
+        while (ok && p.left > 0) {
+            const int len = length_of(a, p.b), h = p.ul % a.Hkv, cnt = segment(p);
+            const int *table = a.block_table + (long long)p.b * a.max_pages;
+            auto page_at = [&](int tile) {   // -1: nothing there
+                const int slot = tile * KT + (box << bp_shift);
+                return mine && slot < len ? table[slot >> a.ps_shift] : -1;
+            };
+            int page = page_at(p.tile);
+            for (int i = 0; i < cnt; ++i, ++n) {
+                const int tile = p.tile + i, slot = tile * KT + (box << bp_shift);
+                const int next = i + 1 < cnt ? page_at(tile + 1) : -1;
+                const uint32_t st = n % C::NST;
+                if (n >= C::NST && !mbar_wait_warp(bar0 + 8u * (C::NST + st), (n / C::NST - 1) & 1u, ctx, SITE_PAGED_EMPTY)) {
+                    ok = false;
+                    break;
+                }
+                const bool inside = mine && slot < len, good = inside && page >= 0 && page < a.num_pages;
+                if (inside && !good)
+                    atomicCAS(&g_paged_status, 0, kStatusBadIndex);
+                // groups of 16 entries whose page is there and that begin in front of the length
+                uint32_t groups = 0;
+                if (good && !(lane & 1))
+                    for (int g = 0; g < (1 << bp_shift) / 16; ++g)
+                        if (slot + 16 * g < len)
+                            groups |= 1u << ((box << bp_shift) / 16 + g);
+                groups = __reduce_or_sync(0xffffffffu, groups);
+                const uint32_t loads = __popc(__ballot_sync(0xffffffffu, good));
+                if (lane == 0) {
+                    there[st] = groups;
+                    mbar_arrive_expect_tx(bar0 + 8u * st, loads * box_bytes);
+                }
+                __syncwarp();
+                if (good)
+                    tma_load_4d(sbase + st * C::STAGE + dst, map, bar0 + 8u * st, 0, slot & ((1 << a.ps_shift) - 1), 0,
+                                page * a.Hkv + h);
+                page = next;
+            }
+            if (ok)
+                next_unit(a, p, cnt);
         }
-        if (a.scores && slot < len)
-            a.scores[((long long)unit * M + r) * a.cap + slot] = s;
-        const float m = block_reduce<true>(s, scratch);
-        const float w = s == -INFINITY ? 0.f : exp2f(s - m);
-        p[tid] = w;
-        const float l = block_reduce<false>(w, scratch);
-        float *dst = a.part + ((unit * a.chunks + chunk) * M + r) * (D + 2);
-        if (tid < D) {
-            float acc = 0.f;
-            for (int j = 0; j < kChunk; ++j)
-                if (rows[j] >= 0)
-                    acc = fmaf(p[j], element<FP8>(a.v, rows[j] + tid), acc);
-            dst[tid] = acc * vs;
-        }
-        if (tid == 0) {
-            dst[D] = m;
-            dst[D + 1] = l;
+        if (!ok)   // copies already issued land before the CTA exits
+            for (uint32_t s = n < C::NST ? 0 : n - C::NST; s < n; ++s)
+                mbar_wait_drain(bar0 + 8u * (s % C::NST), (s / C::NST) & 1u);
+    } else {
+        // ---------------------------------------------------------- math
+        const int rt = warp % RT, kw = warp / RT, c4 = lane & 3, r0 = lane >> 2;
+        const float *rs = reinterpret_cast<const float *>(smem + C::OFF_RS);
+        float2 *ml = reinterpret_cast<float2 *>(smem + C::OFF_ML);
+        float *ob = reinterpret_cast<float *>(smem + C::OFF_O);
+        const uint32_t q_lane = sbase + C::OFF_Q + (rt * 16 + (lane & 15)) * C::QPITCH + (lane >> 4) * 16;
+        uint32_t n = 0;
+        bool ok = true;
+        while (p.left > 0) {
+            const int len = length_of(a, p.b), h = p.ul % a.Hkv, rb = p.ul / a.Hkv, cnt = segment(p);
+            const int row0 = rb * a.rows, nrows = min(a.rows, a.M - row0);
+            // ---- the unit's query rows: bf16, or f16 over the row's power of two with features in
+            // the order in which the codes of four neighbours come out of a register
+            const long long grow = ((long long)p.b * a.Hq + h * a.G) * a.Tq + row0;   // first row of q and o
+            for (int r = warp; r < RT * 16; r += kMathWarps) {
+                uint32_t w[D / 64];
+                float big = 0.f;
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i) {
+                    w[i] = r < nrows ? reinterpret_cast<const uint32_t *>(a.q + (grow + r) * D)[i * 32 + lane] : 0u;
+                    big = fmaxf(big, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xFFFF0000u))));
+                }
+                uint8_t *qr = smem + C::OFF_Q + r * C::QPITCH;
+                float scale = a.scale_log2;
+                if constexpr (FP8) {
+#pragma unroll
+                    for (int off = 16; off > 0; off >>= 1)
+                        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
+                    // 2^-e brings the row's largest value into [1, 4); zeros and infinities stay
+                    const int x = (int)(__float_as_uint(big) >> 23);
+                    const int e = x == 255 || x == 0 ? 0 : min(x - 127, 126);
+                    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+                    scale *= a.ks[h] / down;
+#pragma unroll
+                    for (int i = 0; i < D / 64; ++i) {
+                        const int f = i * 64 + 2 * lane, c = (f & 15) >> 2;   // features f, f + 1
+                        const int at = (f & ~15) + 2 * c + ((f & 2) ? 8 : 0);
+                        reinterpret_cast<uint32_t *>(qr)[at / 2] =
+                            pack_f16x2(__uint_as_float(w[i] << 16) * down, __uint_as_float(w[i] & 0xFFFF0000u) * down);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < D / 64; ++i)
+                        reinterpret_cast<uint32_t *>(qr)[i * 32 + lane] = w[i];
+                }
+                if (lane == 0)
+                    reinterpret_cast<float *>(smem + C::OFF_RS)[r] = scale;
+            }
+            math_sync();
+            uint32_t qf[QREG ? KSTEPS : 1][4];
+            if constexpr (QREG) {
+#pragma unroll
+                for (int k = 0; k < KSTEPS; ++k)
+                    ldsm4(qf[k], q_lane + k * 32);
+            }
+            const float sc0 = rs[rt * 16 + r0], sc1 = rs[rt * 16 + r0 + 8];
+            // slots that the thread's two rows see; a row past the last sees what the others may
+            const int ra = row0 + rt * 16 + r0, rz = ra + 8;
+            const int all = a.causal ? len - a.Tq + 1 : len;   // slots that every row sees
+            const int lim0 = a.causal && ra < a.M ? len - a.Tq + ra % a.Tq + 1 : len;
+            const int lim1 = a.causal && rz < a.M ? len - a.Tq + rz % a.Tq + 1 : len;
+            const bool st0 = a.scores && rt * 16 + r0 < nrows, st1 = a.scores && rt * 16 + r0 + 8 < nrows;
+            float *sp = a.scores ? a.scores + (((long long)p.b * a.Hkv + h) * a.M + ra) * a.cap : nullptr;
+
+            float o[D / 8][4];
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+                o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+            float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+
+            for (int i = 0; i < cnt; ++i, ++n) {
+                const uint32_t st = n % C::NST;
+                if (!mbar_wait_warp(bar0 + 8u * st, (n / C::NST) & 1u, ctx, SITE_PAGED_FULL))
+                    ok = false;   // the CTA gives up: no more is computed or written, and its warps still meet
+                const uint32_t groups = ok ? there[st] : 0u;
+#pragma unroll 1
+                for (int j = 0; j < RT; ++j) {
+                    const int g = kw * RT + j, key0 = (p.tile + i) * KT + g * 16;
+                    if (!((groups >> g) & 1u)) {
+                        if (ok && key0 < len) {   // a page out of range: masked
+                            const float2 none = make_float2(-INFINITY, -INFINITY);
+#pragma unroll
+                            for (int t = 0; t < 2; ++t) {
+                                if (st0)
+                                    *reinterpret_cast<float2 *>(sp + key0 + 8 * t + 2 * c4) = none;
+                                if (st1)
+                                    *reinterpret_cast<float2 *>(sp + 8ll * a.cap + key0 + 8 * t + 2 * c4) = none;
+                            }
+                        }
+                        continue;
+                    }
+                    // the group's rows lie in one box: [chunk][row in box][CB bytes], swizzled
+                    const int gb = (g * 16) >> bp_shift, gr = (g * 16) & ((1 << bp_shift) - 1);
+                    const uint32_t base = sbase + st * C::STAGE + (uint32_t)((gb << bp_shift) * C::ROWB + gr * C::CB);
+                    const uint32_t chunk = (uint32_t)(C::CB << bp_shift);
+                    auto unit_at = [&](uint32_t from, int row, int unit) -> uint32_t {   // 16-byte unit of a row
+                        constexpr int UPC = C::CB / 16;
+                        const int sw = C::CB == 128 ? (row & 7) : ((row >> 1) & 3);
+                        return from + (unit / UPC) * chunk + row * C::CB + (((unit % UPC) ^ sw) << 4);
+                    };
+                    // ---- S = Q K^T: 16 rows x 16 entries, two accumulators for each 8 entries
+                    float s[2][4], s2[2][4];
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+                        s[t][0] = s[t][1] = s[t][2] = s[t][3] = s2[t][0] = s2[t][1] = s2[t][2] = s2[t][3] = 0.f;
+                    const int krow = (lane & 7) + ((lane >> 4) << 3), kunit = (lane >> 3) & 1;
+                    if constexpr (!FP8) {
+#pragma unroll
+                        for (int k = 0; k < KSTEPS; ++k) {
+                            uint32_t kf[4], qa[4];
+                            ldsm4(kf, unit_at(base, krow, 2 * k + kunit));
+                            if constexpr (QREG) {
+                                qa[0] = qf[k][0], qa[1] = qf[k][1], qa[2] = qf[k][2], qa[3] = qf[k][3];
+                            } else {
+                                ldsm4(qa, q_lane + k * 32);
+                            }
+                            mma16816<false>(k & 1 ? s2[0] : s[0], qa, kf[0], kf[1]);
+                            mma16816<false>(k & 1 ? s2[1] : s[1], qa, kf[2], kf[3]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < KSTEPS; k += 2) {   // a 16-byte unit is 16 features
+                            uint32_t kf[4], qa[4], qb[4];
+                            ldsm4(kf, unit_at(base, krow, k + kunit));
+                            if constexpr (QREG) {
+                                qa[0] = qf[k][0], qa[1] = qf[k][1], qa[2] = qf[k][2], qa[3] = qf[k][3];
+                                qb[0] = qf[k + 1][0], qb[1] = qf[k + 1][1], qb[2] = qf[k + 1][2], qb[3] = qf[k + 1][3];
+                            } else {
+                                ldsm4(qa, q_lane + k * 32);
+                                ldsm4(qb, q_lane + k * 32 + 32);
+                            }
+                            mma16816<true>(s[0], qa, e4m3x2_to_f16x2(kf[0]), e4m3x2_to_f16x2(kf[0] >> 16));
+                            mma16816<true>(s[1], qa, e4m3x2_to_f16x2(kf[2]), e4m3x2_to_f16x2(kf[2] >> 16));
+                            mma16816<true>(s2[0], qb, e4m3x2_to_f16x2(kf[1]), e4m3x2_to_f16x2(kf[1] >> 16));
+                            mma16816<true>(s2[1], qb, e4m3x2_to_f16x2(kf[3]), e4m3x2_to_f16x2(kf[3] >> 16));
+                        }
+                    }
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        s[t][0] = (s[t][0] + s2[t][0]) * sc0;
+                        s[t][1] = (s[t][1] + s2[t][1]) * sc0;
+                        s[t][2] = (s[t][2] + s2[t][2]) * sc1;
+                        s[t][3] = (s[t][3] + s2[t][3]) * sc1;
+                    }
+                    if (key0 + 16 > all) {
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            const int key = key0 + 8 * t + 2 * c4;
+                            s[t][0] = key < lim0 ? s[t][0] : -INFINITY;
+                            s[t][1] = key + 1 < lim0 ? s[t][1] : -INFINITY;
+                            s[t][2] = key < lim1 ? s[t][2] : -INFINITY;
+                            s[t][3] = key + 1 < lim1 ? s[t][3] : -INFINITY;
+                        }
+                    }
+                    if (a.scores) {
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            if (st0)
+                                *reinterpret_cast<float2 *>(sp + key0 + 8 * t + 2 * c4) = make_float2(s[t][0], s[t][1]);
+                            if (st1)
+                                *reinterpret_cast<float2 *>(sp + 8ll * a.cap + key0 + 8 * t + 2 * c4) =
+                                    make_float2(s[t][2], s[t][3]);
+                        }
+                    }
+                    // ---- online softmax
+                    constexpr float SH = FP8 ? kPShift : 0.f;
+                    const float n0 = fmaxf(m0, quad_max(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]))) - SH);
+                    const float n1 = fmaxf(m1, quad_max(fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]))) - SH);
+                    const float b0 = n0 == -INFINITY ? 0.f : n0, b1 = n1 == -INFINITY ? 0.f : n1;
+                    if (__any_sync(0xffffffffu, n0 > m0 || n1 > m1)) {
+                        const float f0 = ex2_approx(m0 - b0), f1 = ex2_approx(m1 - b1);
+                        l0 *= f0;
+                        l1 *= f1;
+#pragma unroll
+                        for (int d = 0; d < D / 8; ++d) {
+                            o[d][0] *= f0;
+                            o[d][1] *= f0;
+                            o[d][2] *= f1;
+                            o[d][3] *= f1;
+                        }
+                        m0 = n0;
+                        m1 = n1;
+                    }
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        s[t][0] = ex2_approx(s[t][0] - b0);
+                        s[t][1] = ex2_approx(s[t][1] - b0);
+                        s[t][2] = ex2_approx(s[t][2] - b1);
+                        s[t][3] = ex2_approx(s[t][3] - b1);
+                        l0 += s[t][0] + s[t][1];
+                        l1 += s[t][2] + s[t][3];
+                    }
+                    // ---- O += P V; entries behind the length hold anything: their V reads as 0
+                    uint32_t v0 = 0xFFFFFFFFu, v1 = 0xFFFFFFFFu;
+                    if (key0 + 16 > len) {
+                        const int e = len - key0 - 2 * c4;
+                        v0 = (e > 0 ? 0xFFFFu : 0u) | (e > 1 ? 0xFFFF0000u : 0u);
+                        v1 = (e > 8 ? 0xFFFFu : 0u) | (e > 9 ? 0xFFFF0000u : 0u);
+                    }
+                    const uint32_t vbase = base + C::TILE;
+                    const int vrow = (lane & 7) + (((lane >> 3) & 1) << 3), vunit = lane >> 4;
+                    if constexpr (!FP8) {
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const float pa = s[x >> 1][(x & 1) * 2], pb = s[x >> 1][(x & 1) * 2 + 1];
+                            hi[x] = pack_bf16x2(pa, pb);
+                            lo[x] = pack_bf16x2(pa - __uint_as_float(hi[x] << 16), pb - __uint_as_float(hi[x] & 0xFFFF0000u));
+                        }
+#pragma unroll
+                        for (int d = 0; d < D / 16; ++d) {
+                            uint32_t vf[4];
+                            ldsm4_t(vf, unit_at(vbase, vrow, 2 * d + vunit));
+                            vf[0] &= v0, vf[1] &= v1, vf[2] &= v0, vf[3] &= v1;
+                            mma16816<false>(o[2 * d], hi, vf[0], vf[1]);
+                            mma16816<false>(o[2 * d + 1], hi, vf[2], vf[3]);
+                            mma16816<false>(o[2 * d], lo, vf[0], vf[1]);
+                            mma16816<false>(o[2 * d + 1], lo, vf[2], vf[3]);
+                        }
+                    } else {
+                        uint32_t pf[4];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            pf[x] = pack_f16x2(s[x >> 1][(x & 1) * 2], s[x >> 1][(x & 1) * 2 + 1]);
+#pragma unroll
+                        for (int d = 0; d < D / 32; ++d) {   // two 16-byte units: 32 features
+                            uint32_t vf[4];
+                            ldsm4_t(vf, unit_at(vbase, vrow, 2 * d + vunit));
+                            vf[0] &= v0, vf[1] &= v1, vf[2] &= v0, vf[3] &= v1;
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) {
+                                // a register holds features (f, f + 1) of entries 2 c and 2 c + 1: pair the entries
+                                const uint32_t x = __byte_perm(vf[2 * u], 0, 0x3120), y = __byte_perm(vf[2 * u + 1], 0, 0x3120);
+                                mma16816<true>(o[4 * d + 2 * u], pf, e4m3x2_to_f16x2(x), e4m3x2_to_f16x2(y));
+                                mma16816<true>(o[4 * d + 2 * u + 1], pf, e4m3x2_to_f16x2(x >> 16), e4m3x2_to_f16x2(y >> 16));
+                            }
+                        }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(bar0 + 8u * (C::NST + st));
+            }
+
+            // ---- the warps' states of each row tile together, then out, 32 features at a time
+            l0 = quad_sum(l0);
+            l1 = quad_sum(l1);
+            if (c4 == 0) {
+                ml[warp * 16 + r0] = make_float2(m0, l0);
+                ml[warp * 16 + r0 + 8] = make_float2(m1, l1);
+            }
+            math_sync();
+            auto top = [&](int rt_, int r) {   // largest of a row's maxima
+                float x = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < KW; ++w)
+                    x = fmaxf(x, ml[(w * RT + rt_) * 16 + r].x);
+                return x;
+            };
+            auto weight = [](float m, float t) { return m == -INFINITY ? 0.f : ex2_approx(m - t); };
+            const float f0 = weight(m0, top(rt, r0)), f1 = weight(m1, top(rt, r0 + 8));
+            const bool whole = p.tile == 0 && cnt == p.nt;
+            const long long slot = 2ll * blockIdx.x + (t0 + (min(share, total - t0) - p.left) == t0 ? 0 : 1);
+            float *part = a.part + slot * a.rows * (D + 2);
+            const float vs = FP8 ? a.vs[h] : 1.f;
+#pragma unroll
+            for (int sl = 0; sl < D / C::OC; ++sl) {
+                float *mine = ob + (warp * 16 + r0) * C::OPITCH;
+#pragma unroll
+                for (int x = 0; x < 4; x += 2) {
+                    const float(&p0)[4] = o[sl * 4 + x], (&p1)[4] = o[sl * 4 + x + 1];
+                    if constexpr (!FP8) {
+                        *reinterpret_cast<float2 *>(mine + 8 * x + 2 * c4) = make_float2(p0[0] * f0, p0[1] * f0);
+                        *reinterpret_cast<float2 *>(mine + 8 * x + 8 + 2 * c4) = make_float2(p1[0] * f0, p1[1] * f0);
+                        *reinterpret_cast<float2 *>(mine + 8 * C::OPITCH + 8 * x + 2 * c4) = make_float2(p0[2] * f1, p0[3] * f1);
+                        *reinterpret_cast<float2 *>(mine + 8 * C::OPITCH + 8 * x + 8 + 2 * c4) = make_float2(p1[2] * f1, p1[3] * f1);
+                    } else {   // even and odd features of a 16-feature unit
+                        *reinterpret_cast<float4 *>(mine + 8 * x + 4 * c4) = make_float4(p0[0] * f0, p1[0] * f0, p0[1] * f0, p1[1] * f0);
+                        *reinterpret_cast<float4 *>(mine + 8 * C::OPITCH + 8 * x + 4 * c4) =
+                            make_float4(p0[2] * f1, p1[2] * f1, p0[3] * f1, p1[3] * f1);
+                    }
+                }
+                math_sync();
+#pragma unroll
+                for (int e = 0; e < RT; ++e) {
+                    const int at = e * 128 + (int)threadIdx.x, row = at >> 3, col = (at & 7) * 4;
+                    const int rt_ = row >> 4, r = row & 15;
+                    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int w = 0; w < KW; ++w) {
+                        const float4 y = *reinterpret_cast<const float4 *>(ob + ((w * RT + rt_) * 16 + r) * C::OPITCH + col);
+                        x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+                    }
+                    if (row >= nrows || !ok)
+                        continue;
+                    const float t = top(rt_, r);
+                    float l = 0.f;
+#pragma unroll
+                    for (int w = 0; w < KW; ++w) {
+                        const float2 y = ml[(w * RT + rt_) * 16 + r];
+                        l = fmaf(y.y, weight(y.x, t), l);
+                    }
+                    const float k = whole ? (l == 0.f ? 0.f : vs / l) : vs;
+                    if (whole) {
+                        uint2 y;
+                        y.x = pack_bf16x2(x.x * k, x.y * k);
+                        y.y = pack_bf16x2(x.z * k, x.w * k);
+                        *reinterpret_cast<uint2 *>(a.o + (grow + row) * D + sl * C::OC + col) = y;
+                        if (sl == 0 && col == 0)
+                            a.lse[grow + row] = l == 0.f ? -INFINITY : (t + log2f(l)) * 0.69314718055994530942f;
+                    } else {
+                        // 8-byte stores: a slot of `rows` (D + 2) floats is a multiple of 8 bytes
+                        float2 *dst = reinterpret_cast<float2 *>(part + (long long)row * D + sl * C::OC + col);
+                        dst[0] = make_float2(x.x * k, x.y * k);
+                        dst[1] = make_float2(x.z * k, x.w * k);
+                        if (sl == 0 && col == 0) {
+                            part[(long long)a.rows * D + row] = t;
+                            part[(long long)a.rows * (D + 1) + row] = l;
+                        }
+                    }
+                }
+                math_sync();
+            }
+            next_unit(a, p, cnt);
         }
     }
 }
 
-// One CTA per (unit, row): o and lse from the chunks' states.
+// ------------------------------------------------------------------ join
+// Where a unit's states are: CTAs c0 .. c1, the first one's in slot s0, the others' in their
+// first slots.  c0 == c1: the whole unit was one CTA's and its o and lse are written.
+struct Parts {
+    int c0, c1;
+    long long s0;
+    bool none;   // no entry at all
+};
+
+__device__ __forceinline__ Parts parts_of(const PagedArgs &a, int b, int ul, volatile long long *scratch)
+{
+    const int per = a.Hkv * a.RB, nt = tiles_of(a, b);
+    const long long before = block_tiles(a, b, scratch) * per, total = block_tiles(a, a.B, scratch) * per;
+    const long long share = share_of(a, total), t = before + (long long)ul * nt;
+    Parts p;
+    p.none = nt == 0;
+    p.c0 = (int)(t / share);
+    p.c1 = (int)((t + nt - 1) / share);
+    p.s0 = 2ll * p.c0 + (t == p.c0 * share ? 0 : 1);
+    return p;
+}
+
+// Blocks [0, units * rows): o and lse of one row of a unit whose entries were split (or of a
+// sequence without any).  Blocks from there: 256 entries' weights of one (sequence, KV head).
 template <int D>
-__global__ void __launch_bounds__(D) paged_join_kernel(const __grid_constant__ PagedArgs a)
+__global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ PagedArgs a, int wchunks)
 {
-    const int M = a.G * a.Tq;
-    const long long unit = blockIdx.x / M;
-    const int r = (int)(blockIdx.x - unit * M), b = (int)(unit / a.Hkv), h = (int)(unit - (long long)b * a.Hkv);
-    const int n = (length_of(a, b) + kChunk - 1) / kChunk;
-    const float *src = a.part + (unit * a.chunks * M + r) * (D + 2);
-    const long long stride = (long long)M * (D + 2);
-    float m = -INFINITY, l = 0.f, acc = 0.f;
-    for (int i = 0; i < n; ++i)
-        m = fmaxf(m, src[i * stride + D]);
-    if (m != -INFINITY)
-        for (int i = 0; i < n; ++i) {
-            const float mi = src[i * stride + D];
-            const float w = mi == -INFINITY ? 0.f : exp2f(mi - m);
-            l = fmaf(w, src[i * stride + D + 1], l);
-            acc = fmaf(w, src[i * stride + threadIdx.x], acc);
+    __shared__ long long scratch[4];
+    __shared__ float row_lse[kMaxRows];
+    const int tid = threadIdx.x, per = a.Hkv * a.RB;
+    const long long rows_total = (long long)a.B * per * a.rows, blk = blockIdx.x;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (blk < rows_total) {
+        const int row = (int)(blk % a.rows);
+        const long long unit = blk / a.rows;
+        const int b = (int)(unit / per), ul = (int)(unit - (long long)b * per), h = ul % a.Hkv, rb = ul / a.Hkv;
+        if (rb * a.rows + row >= a.M)
+            return;
+        const Parts p = parts_of(a, b, ul, scratch);
+        if (!p.none && p.c0 == p.c1)
+            return;
+        const long long grow = ((long long)b * a.Hq + h * a.G) * a.Tq + rb * a.rows + row;
+        const long long stride = (long long)a.rows * (D + 2);
+        float m = -INFINITY, l = 0.f, x[D / 64] = {};
+        if (!p.none) {
+            auto slot = [&](int c) { return a.part + (c == p.c0 ? p.s0 : 2ll * c) * stride; };
+            for (int c = p.c0; c <= p.c1; ++c)
+                m = fmaxf(m, slot(c)[(long long)a.rows * D + row]);
+            if (m != -INFINITY)
+#pragma unroll 4
+                for (int c = p.c0; c <= p.c1; ++c) {
+                    const float *s = slot(c);
+                    const float mc = s[(long long)a.rows * D + row], w = mc == -INFINITY ? 0.f : ex2_approx(mc - m);
+                    l = fmaf(w, s[(long long)a.rows * (D + 1) + row], l);
+                    if (tid < 64)
+#pragma unroll
+                        for (int i = 0; i < D / 64; ++i)
+                            x[i] = fmaf(w, s[(long long)row * D + i * 64 + tid], x[i]);
+                }
         }
-    const long long row = ((long long)b * a.Hq + h * a.G) * a.Tq + r;
-    a.o[row * D + threadIdx.x] = __float2bfloat16(l == 0.f ? 0.f : acc / l);
-    if (threadIdx.x == 0)
-        a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
-}
-
-// weight_j += sum over the head group's rows of p_j, from the stored scores and lse.
-__global__ void __launch_bounds__(256) paged_weight_kernel(const __grid_constant__ PagedArgs a)
-{
-    const int M = a.G * a.Tq;
-    const long long unit = blockIdx.x;
-    const int b = (int)(unit / a.Hkv), h = (int)(unit - (long long)b * a.Hkv), len = length_of(a, b);
-    for (int j = blockIdx.y * 256 + threadIdx.x; j < len; j += gridDim.y * 256) {
-        float sum = 0.f;
-        for (int r = 0; r < M; ++r) {
-            const float lse = a.lse[((long long)b * a.Hq + h * a.G) * a.Tq + r];
-            const float s = a.scores[(unit * M + r) * a.cap + j];
-            if (s != -INFINITY)
-                sum += exp2f(s - lse * 1.4426950408889634f);
+        if (tid < 64) {
+            const float k = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i)
+                a.o[grow * D + i * 64 + tid] = __float2bfloat16(x[i] * k);
+            if (tid == 0)
+                a.lse[grow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
         }
-        a.weight[unit * a.cap + j] += sum;
+        return;
+    }
+    // ---- weight_j += sum over the rows of p_j = 2^{s_j - lse}
+    const long long wb = blk - rows_total, uh = wb / wchunks;
+    const int b = (int)(uh / a.Hkv), h = (int)(uh - (long long)b * a.Hkv), len = length_of(a, b);
+    const int first = (int)(wb - uh * wchunks) * 256;
+    if (first >= len)
+        return;
+    float sum[2] = {0.f, 0.f};
+    for (int rb = 0; rb < a.RB; ++rb) {
+        const Parts p = parts_of(a, b, rb * a.Hkv + h, scratch);
+        const int row0 = rb * a.rows, nrows = min(a.rows, a.M - row0);
+        const long long stride = (long long)a.rows * (D + 2);
+        for (int r = tid; r < nrows; r += 128) {
+            float y;
+            if (p.c0 == p.c1) {
+                y = a.lse[((long long)b * a.Hq + h * a.G) * a.Tq + row0 + r] * 1.4426950408889634f;
+            } else {
+                float m = -INFINITY, l = 0.f;
+                auto slot = [&](int c) { return a.part + (c == p.c0 ? p.s0 : 2ll * c) * stride + (long long)a.rows * D + r; };
+                for (int c = p.c0; c <= p.c1; ++c)
+                    m = fmaxf(m, *slot(c));
+                if (m != -INFINITY)
+                    for (int c = p.c0; c <= p.c1; ++c) {
+                        const float *s = slot(c);
+                        l = fmaf(s[a.rows], s[0] == -INFINITY ? 0.f : ex2_approx(s[0] - m), l);
+                    }
+                y = l == 0.f ? -INFINITY : m + log2f(l);
+            }
+            // a row that saw nothing has no finite score either: 2^{-inf - 0}
+            row_lse[r] = y == -INFINITY ? 0.f : y;
+        }
+        __syncthreads();
+        const float *sp = a.scores + (uh * a.M + row0) * a.cap;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int j = first + i * 128 + tid;
+            if (j < len)
+#pragma unroll 4
+                for (int r = 0; r < nrows; ++r)
+                    sum[i] += ex2_approx(sp[(long long)r * a.cap + j] - row_lse[r]);
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int j = first + i * 128 + tid;
+        if (j < len)
+            a.weight[uh * a.cap + j] += sum[i];
     }
 }
 
-template <int D, bool FP8>
-int paged_run(const PagedArgs &a, int units, cudaStream_t s)
+// ------------------------------------------------------------------ host
+size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+int rows_of(int M) { return M < kMaxRows ? M : kMaxRows; }
+int row_tiles(int M) { return M <= 16 ? 1 : M <= 32 ? 2 : 4; }
+int grid_of(int d) { return kSMs * (d == 256 ? 1 : 2); }
+
+size_t part_bytes(int M, int d) { return round256((size_t)2 * grid_of(d) * rows_of(M) * (d + 2) * sizeof(float)); }
+
+// K or V pool as [page, KV head][column chunk][row][CB bytes]; a box is all chunks of a page's
+// rows (64 at most).
+int encode_pool(CUtensorMap *map, const void *base, const fa_kv_cache &c, int box_rows)
 {
-    if (a.chunks > 0)
-        paged_kernel<D, FP8><<<(unsigned)((long long)units * a.chunks), kChunk, 0, s>>>(a);
-    paged_join_kernel<D><<<units * a.G * a.Tq, D, 0, s>>>(a);
-    if (a.scores && a.chunks > 0)
-        paged_weight_kernel<<<dim3(units, a.chunks < 64 ? a.chunks : 64), 256, 0, s>>>(a);
+    const bool f8 = c.dtype == FA_E4M3;
+    const int elem = f8 ? 1 : 2, rowb = c.d * elem, cb = rowb < 128 ? rowb : 128;
+    const uint64_t dims[4] = {(uint64_t)(cb / elem), (uint64_t)c.page_size, (uint64_t)(rowb / cb),
+                              (uint64_t)c.num_pages * c.Hkv};
+    const uint64_t strides[3] = {(uint64_t)rowb, (uint64_t)cb, (uint64_t)c.page_size * rowb};
+    const uint32_t box[4] = {(uint32_t)(cb / elem), (uint32_t)box_rows, (uint32_t)(rowb / cb), 1};
+    return encode_tmap(map, base, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, dims, strides,
+                       box, cb == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
+template <int D, bool FP8, int RT>
+int launch_main(const CUtensorMap &tk, const CUtensorMap &tv, const PagedArgs &a, int grid, cudaStream_t s)
+{
+    using C = Cfg<D, FP8, RT>;
+    if (cudaFuncSetAttribute(paged_kernel<D, FP8, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
+        return ERR_CUDA;
+    paged_kernel<D, FP8, RT><<<grid, kThreads, C::SMEM, s>>>(tk, tv, a);
     return cudaGetLastError() == cudaSuccess ? OK : ERR_CUDA;
 }
 
-size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
-
-size_t part_bytes(int B, int Hq, int Tq, int max_len, int d)
+template <int D>
+int paged_run(const fa_kv_cache &c, PagedArgs &a, cudaStream_t s)
 {
-    return round256((size_t)B * Hq * Tq * ((max_len + kChunk - 1) / kChunk) * (d + 2) * sizeof(float));
+    const bool f8 = c.dtype == FA_E4M3;
+    const int rt = row_tiles(a.M);
+    const long long most = (long long)a.B * a.Hkv * a.RB * ((a.cap + KT - 1) / KT);   // tiles, at most
+    int st = OK;
+    if (most > 0) {
+        CUtensorMap tk, tv;
+        const int box = c.page_size < KT ? c.page_size : KT;
+        if ((st = encode_pool(&tk, c.k, c, box)) != OK || (st = encode_pool(&tv, c.v, c, box)) != OK)
+            return st;
+        const int grid = (int)(most < a.grid ? most : a.grid);
+        if (f8)
+            st = rt == 1   ? launch_main<D, true, 1>(tk, tv, a, grid, s)
+                 : rt == 2 ? launch_main<D, true, 2>(tk, tv, a, grid, s)
+                           : launch_main<D, true, 4>(tk, tv, a, grid, s);
+        else
+            st = rt == 1   ? launch_main<D, false, 1>(tk, tv, a, grid, s)
+                 : rt == 2 ? launch_main<D, false, 2>(tk, tv, a, grid, s)
+                           : launch_main<D, false, 4>(tk, tv, a, grid, s);
+        if (st != OK)
+            return st;
+    }
+    const int wchunks = a.scores ? (a.cap + 255) / 256 : 0;
+    const long long blocks = (long long)a.B * a.Hkv * a.RB * a.rows + (long long)a.B * a.Hkv * wchunks;
+    if (blocks > INT_MAX)
+        return ERR_UNSUPPORTED;
+    // launched while the first kernel runs, waits for it inside
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(128);
+    cfg.stream = s;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, paged_join_kernel<D>, a, wchunks) == cudaSuccess ? OK : ERR_CUDA;
 }
 
 }  // namespace
 
 size_t paged_workspace_bytes(int B, int Hq, int Hkv, int Tq, int max_len, int d, int accumulate)
 {
-    (void)Hkv;
-    return part_bytes(B, Hq, Tq, max_len, d) + (accumulate ? round256((size_t)B * Hq * Tq * max_len * sizeof(float)) : 0);
+    return part_bytes(Hq / Hkv * Tq, d) + (accumulate ? round256((size_t)B * Hq * Tq * max_len * sizeof(float)) : 0);
 }
 
 int paged_launch(const fa_kv_cache &c, const void *q, void *o, float *lse, int Hq, int Tq, int causal, float scale,
@@ -209,41 +876,31 @@ int paged_launch(const fa_kv_cache &c, const void *q, void *o, float *lse, int H
     a.o = static_cast<__nv_bfloat16 *>(o);
     a.lse = lse;
     a.weight = c.weight;
-    a.k = c.k;
-    a.v = c.v;
     a.ks = c.k_scale;
     a.vs = c.v_scale;
     a.block_table = c.block_table;
     a.lens = c.lens;
+    a.B = c.B;
     a.Hq = Hq;
     a.Hkv = c.Hkv;
     a.G = Hq / c.Hkv;
     a.Tq = Tq;
+    a.M = a.G * Tq;
+    a.rows = rows_of(a.M);
+    a.RB = (a.M + a.rows - 1) / a.rows;
     a.causal = causal;
     a.num_pages = c.num_pages;
     a.max_pages = c.max_pages;
     a.ps_shift = 0;
     while ((1 << a.ps_shift) < c.page_size)
         ++a.ps_shift;
-    a.cap = c.max_pages * c.page_size;
-    a.chunks = (a.cap + kChunk - 1) / kChunk;
+    a.cap = c.num_pages > 0 ? c.max_pages * c.page_size : 0;   // no pages: every length above 0 is out of range
+    a.grid = grid_of(c.d);
     a.part = static_cast<float *>(workspace);
-    a.scores = accumulate ? reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) +
-                                                      part_bytes(c.B, Hq, Tq, a.cap, c.d))
-                          : nullptr;
+    a.scores = accumulate ? reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + part_bytes(a.M, c.d)) : nullptr;
     a.scale_log2 = scale * 1.4426950408889634f;
-    const int units = c.B * c.Hkv;
-    if ((long long)units * (a.chunks > 0 ? a.chunks : 1) > INT_MAX)
-        return ERR_UNSUPPORTED;
-    const bool f8 = c.dtype == FA_E4M3;
-    switch (c.d) {
-    case 64:
-        return f8 ? paged_run<64, true>(a, units, s) : paged_run<64, false>(a, units, s);
-    case 128:
-        return f8 ? paged_run<128, true>(a, units, s) : paged_run<128, false>(a, units, s);
-    default:
-        return f8 ? paged_run<256, true>(a, units, s) : paged_run<256, false>(a, units, s);
-    }
+    a.timeout_ns = wait_timeout_ns();
+    return c.d == 64 ? paged_run<64>(c, a, s) : c.d == 128 ? paged_run<128>(c, a, s) : paged_run<256>(c, a, s);
 }
 
 int paged_status_fetch_clear(cudaStream_t s, int *host_word)
