@@ -379,10 +379,194 @@ __device__ __forceinline__ int block_rank(bool p, int &total, int *scratch)
     return before + __popc(m & ((1u << lane_id()) - 1u));
 }
 
-// One CTA per (sequence, KV head): finds the rank of the last entry that stays (radix select,
-// 8 bits a pass) and the slot up to which entries of that very rank stay, then pairs the kept
+// ---- selection by a cluster per (sequence, KV head)
+// The entries' ranks are read once and stay in shared memory, a contiguous run of slots per CTA.
+// Three passes of a radix select (11, 11 and 10 bits; counts of the whole cluster read over
+// distributed shared memory, every CTA finds the digit for itself) give the rank of the last
+// entry that stays; then one scan per question over runs of consecutive slots per thread: which
+// of several equals stay, and the numbers of the holes in front of the new length and of the kept
+// entries behind it.  The kept ones wait at the front of `kept` until every hole has read its own.
+constexpr int kSelBits = 11, kSelBins = 1 << kSelBits;
+constexpr int kSelItems = 49;                                // entries a thread, at most (odd: see run)
+constexpr int kSelFixed = 3 * kSelBins * 4 + 2 * 32 * 4 + 32;   // shared memory besides the ranks
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ int cluster_load(const int *p, int rank)   // the same word of another CTA
+{
+    uint32_t addr;
+    int x;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(x) : "r"(addr) : "memory");
+    return x;
+}
+
+// Sum of x over the lower threads of the block, and over all of it.
+__device__ __forceinline__ int block_scan(int x, int &total, int *scratch)
+{
+    int inc = x;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, off);
+        if ((int)lane_id() >= off)
+            inc += y;
+    }
+    __syncthreads();
+    if (lane_id() == 31)
+        scratch[warp_id()] = inc;
+    __syncthreads();
+    const int c = scratch[lane_id()];
+    total = __reduce_add_sync(0xffffffffu, c);
+    return __reduce_add_sync(0xffffffffu, lane_id() < warp_id() ? c : 0) + inc - x;
+}
+
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_constant__ EvictArgs a, int cs)
+{
+    extern __shared__ int sel_smem[];
+    int *hist = sel_smem, *scratch = hist + 3 * kSelBins, *share = scratch + 32, *pick = share + 32;
+    uint32_t *keys = reinterpret_cast<uint32_t *>(pick + 8);
+    const int rank = (int)blockIdx.x % cs, unit = (int)blockIdx.x / cs, b = unit / a.Hkv, tid = threadIdx.x;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int len = a.lens[b];
+    int *kept = a.kept + (long long)unit * a.budget;
+    const long long base = (long long)unit * a.cap;
+    const bool bad = len < 0 || len > a.cap;
+    const int end = bad ? 0 : min(len, a.budget);
+    if (bad && tid == 0)
+        atomicCAS(&g_cache_status, 0, kStatusBadIndex);
+    for (int j = end + rank * kSelThreads + tid; j < a.budget; j += cs * kSelThreads)
+        kept[j] = -1;
+    if (bad)
+        return;   // the whole cluster
+    const float *weight = a.weight + base;
+    const int *order = a.order ? a.order + base : nullptr;
+    if (len <= a.budget) {
+        for (int j = rank * kSelThreads + tid; j < end; j += cs * kSelThreads) {
+            kept[j] = j;
+            a.weight_out[base + j] = weight[j];
+            if (order)
+                a.order_out[base + j] = order[j];
+        }
+        return;
+    }
+    for (int i = tid; i < 3 * kSelBins; i += kSelThreads)
+        hist[i] = 0;
+    const int per = (len + cs - 1) / cs, lo = min(len, rank * per), n = min(len, lo + per) - lo;
+    const int recent = (a.seen ? a.seen[b] : len) - a.n_recent;
+    const bool ages = order && (a.n_first > 0 || a.n_recent > 0);
+    __syncthreads();
+    for (int i = tid; i < n; i += kSelThreads) {
+        bool prot = false;
+        if (ages) {
+            const int at = order[lo + i];
+            prot = at < a.n_first || (a.n_recent > 0 && at >= recent);
+        }
+        const uint32_t u = rank_key(weight[lo + i], prot);
+        keys[i] = u;
+        atomicAdd(&hist[u >> 21], 1);
+    }
+    uint32_t prefix = 0;
+    int need = end, equal = 0;   // still to be taken among those that match the prefix; how many do
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+        int *hp = hist + pass * kSelBins;
+        if (pass > 0) {
+            const uint32_t mask = pass == 1 ? 0xFFE00000u : 0xFFFFFC00u;
+            for (int i = tid; i < n; i += kSelThreads) {
+                const uint32_t u = keys[i];
+                if ((u & mask) == prefix)
+                    atomicAdd(&hp[pass == 1 ? (u >> 10) & 2047 : u & 1023], 1);
+            }
+        }
+        cluster_sync();
+        // bins from the top, two a thread
+        const int d0 = kSelBins - 1 - 2 * tid, d1 = d0 - 1;
+        int c0 = 0, c1 = 0;
+        for (int r = 0; r < cs; ++r) {
+            c0 += cluster_load(hp + d0, r);
+            c1 += cluster_load(hp + d1, r);
+        }
+        int total;
+        const int before = block_scan(c0 + c1, total, scratch);
+        if (before < need && need <= before + c0 + c1) {
+            const bool first = need <= before + c0;
+            pick[0] = first ? d0 : d1;
+            pick[1] = need - before - (first ? 0 : c0);
+            pick[2] = first ? c0 : c1;
+        }
+        __syncthreads();
+        prefix |= (uint32_t)pick[0] << shift;
+        need = pick[1];
+        equal = pick[2];
+    }
+    // an odd run of consecutive slots per thread: the runs of a warp lie in different banks
+    const int q = ((n + kSelThreads - 1) / kSelThreads) | 1, i0 = min(n, tid * q), i1 = min(n, i0 + q);
+    int edge = INT_MAX;   // slots below it stay among the entries whose rank is `prefix` itself
+    if (equal > need) {
+        int mine = 0, total;
+        for (int i = i0; i < i1; ++i)
+            mine += keys[i] == prefix;
+        int r = block_scan(mine, total, scratch);
+        if (tid == 0) {
+            share[0] = total;
+            pick[3] = INT_MAX;
+        }
+        cluster_sync();
+        for (int c = 0; c < rank; ++c)
+            r += cluster_load(share, c);
+        for (int i = i0; i < i1; ++i)
+            if (keys[i] == prefix && r++ == need - 1)
+                pick[3] = i + 1;
+        __syncthreads();
+        // this CTA's entries behind the last one to stay, wherever that is
+        int before = 0;
+        for (int c = 0; c < rank; ++c)
+            before += cluster_load(share, c);
+        edge = before >= need ? 0 : pick[3];
+    }
+    auto stays = [&](int i) {
+        const uint32_t u = keys[i];
+        return u > prefix || (u == prefix && i < edge);
+    };
+    // holes in front of the new length in the low half, kept entries behind it in the high half
+    int mine = 0, total;
+    for (int i = i0; i < i1; ++i)
+        mine += lo + i < end ? (stays(i) ? 0 : 1) : (stays(i) ? 1 << 16 : 0);
+    const int before = block_scan(mine, total, scratch);
+    if (tid == 0) {
+        share[1] = total & 0xFFFF;
+        share[2] = total >> 16;
+    }
+    cluster_sync();
+    int hole = before & 0xFFFF, mover = before >> 16;
+    for (int c = 0; c < rank; ++c) {
+        hole += cluster_load(share + 1, c);
+        mover += cluster_load(share + 2, c);
+    }
+    for (int i = i0, m = mover; i < i1; ++i)
+        if (lo + i >= end && stays(i))
+            kept[m++] = lo + i;
+    cluster_sync();
+    for (int i = i0; i < i1 && lo + i < end; ++i)
+        keys[i] = stays(i) ? lo + i : kept[hole++];
+    cluster_sync();
+    for (int i = tid; i < n && lo + i < end; i += kSelThreads) {
+        const int from = (int)keys[i], j = lo + i;
+        kept[j] = from;
+        a.weight_out[base + j] = weight[from];
+        if (order)
+            a.order_out[base + j] = order[from];
+    }
+}
+
+// The same for lengths whose ranks do not fit the shared memory of a cluster: one CTA per
+// (sequence, KV head) reads them at every pass.  Finds the rank of the last entry that stays
+// (radix select, 8 bits a pass) and the slot up to which entries of that very rank stay, then pairs the kept
 // entries behind the new length with the holes in front of it.
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_constant__ EvictArgs a)
+__global__ void __launch_bounds__(kSelThreads) evict_select_long_kernel(const __grid_constant__ EvictArgs a)
 {
     __shared__ int hist[256], scratch[32], pick[2];
     const int unit = blockIdx.x, b = unit / a.Hkv, tid = threadIdx.x;
@@ -496,17 +680,21 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
     }
 }
 
-// Rows of the moved entries: each warp takes 32 entries of one (sequence, KV head) and copies
-// K and V of those that moved.  Sources lie behind the new length and targets in front of it.
+// Rows of the moved entries: each warp takes 32 entries of one (sequence, KV head), lists those
+// that moved and copies their K and V rows, eight 16-byte loads in flight a lane.  Sources lie
+// behind the new length and targets in front of it.
 __global__ void __launch_bounds__(256) evict_move_kernel(const __grid_constant__ EvictArgs a)
 {
+    __shared__ long long list[8][32][2];
     const int unit = blockIdx.x, b = unit / a.Hkv, h = unit - b * a.Hkv, lane = threadIdx.x & 31;
+    long long(*moves)[2] = list[threadIdx.x >> 5];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (blockIdx.y == 0 && h == 0 && threadIdx.x == 0) {
         const int len = a.lens[b];
         a.lens_out[b] = min(len, a.budget);
     }
     const int *table = a.block_table + (long long)b * a.max_pages;
-    const int vecs = a.row_bytes / 16;
+    const int vshift = 31 - __clz(a.row_bytes / 16), vecs = 1 << vshift;   // 16-byte vectors of a row
     auto at = [&](int slot) -> long long {
         const int page = table[slot >> a.ps_shift];
         if (page < 0 || page >= a.num_pages)
@@ -525,17 +713,34 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const __grid_constant__
                 from = -1;
             }
         }
-        uint32_t todo = __ballot_sync(0xffffffffu, from >= 0);
-        while (todo) {
-            const int l = __ffs(todo) - 1;
-            todo &= todo - 1;
-            const long long f = __shfl_sync(0xffffffffu, from, l), t = __shfl_sync(0xffffffffu, to, l);
-            for (int e = lane; e < 2 * vecs; e += 32) {
-                uint8_t *pool = e < vecs ? a.k : a.v;
-                const int o = (e < vecs ? e : e - vecs) * 16;
-                *reinterpret_cast<uint4 *>(pool + t + o) = *reinterpret_cast<const uint4 *>(pool + f + o);
+        const uint32_t todo = __ballot_sync(0xffffffffu, from >= 0);
+        if (from >= 0) {
+            const int r = __popc(todo & ((1u << lane) - 1u));
+            moves[r][0] = from;
+            moves[r][1] = to;
+        }
+        __syncwarp();
+        const int count = __popc(todo) << (vshift + 1);   // vectors of K and V
+        for (int e0 = lane; e0 < count; e0 += 32 * 8) {
+            uint4 x[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int e = e0 + 32 * u;
+                if (e < count) {
+                    const int m = e >> (vshift + 1), o = e & (vecs - 1);
+                    x[u] = *reinterpret_cast<const uint4 *>((e & vecs ? a.v : a.k) + moves[m][0] + o * 16);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int e = e0 + 32 * u;
+                if (e < count) {
+                    const int m = e >> (vshift + 1), o = e & (vecs - 1);
+                    *reinterpret_cast<uint4 *>((e & vecs ? a.v : a.k) + moves[m][1] + o * 16) = x[u];
+                }
             }
         }
+        __syncwarp();
     }
 }
 
@@ -646,10 +851,44 @@ int evict_launch(const fa_kv_cache &c, int budget, int n_first, int n_recent, fl
     a.ps_shift = shift_of(c.page_size);
     a.row_bytes = c.d * (c.dtype == FA_E4M3 ? 1 : 2);
     const int units = c.B * c.Hkv;
-    evict_select_kernel<<<units, kSelThreads, 0, s>>>(a);
+    // CTAs per (sequence, KV head): 1024 entries or more each, as long as all are resident
+    int cs = 1;
+    while (cs < 8 && a.cap / (2 * cs) >= kSelThreads && (long long)units * 2 * cs <= 2ll * device_sm_count())
+        cs *= 2;
+    while (cs < 8 && (a.cap + cs - 1) / cs > kSelItems * kSelThreads)
+        cs *= 2;
+    const int per = (a.cap + cs - 1) / cs;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at;
+    cfg.stream = s;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    if (per <= kSelItems * kSelThreads && (long long)units * cs <= INT_MAX) {
+        const int smem = kSelFixed + per * 4;
+        if (cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kSelFixed + kSelItems * kSelThreads * 4) != cudaSuccess)
+            return ERR_CUDA;
+        cfg.gridDim = dim3((unsigned)(units * cs));
+        cfg.blockDim = dim3(kSelThreads);
+        cfg.dynamicSmemBytes = smem;
+        at.id = cudaLaunchAttributeClusterDimension;
+        at.val.clusterDim.x = cs;
+        at.val.clusterDim.y = at.val.clusterDim.z = 1;
+        if (cudaLaunchKernelEx(&cfg, evict_select_kernel, a, cs) != cudaSuccess)
+            return ERR_CUDA;
+    } else {
+        evict_select_long_kernel<<<units, kSelThreads, 0, s>>>(a);
+        if (cudaGetLastError() != cudaSuccess)
+            return ERR_CUDA;
+    }
+    // launched while the selection runs, waits for it inside
     const int blocks = (budget + 255) / 256;
-    evict_move_kernel<<<dim3(units, blocks < 64 ? blocks : 64), 256, 0, s>>>(a);
-    return cudaGetLastError() == cudaSuccess ? OK : ERR_CUDA;
+    cfg.gridDim = dim3(units, blocks < 64 ? blocks : 64);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    return cudaLaunchKernelEx(&cfg, evict_move_kernel, a) == cudaSuccess ? OK : ERR_CUDA;
 }
 
 int cache_status_fetch_clear(cudaStream_t s, int *host_word)

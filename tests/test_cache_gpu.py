@@ -532,7 +532,9 @@ EVICT = [
     ([1], 1, 0, 0, 1, 64, 16, False, "random"),
     ([2, 1, 0, 5], 1, 0, 1, 2, 64, 16, False, "random"),
     ([100, 33, 17, 64], 33, 4, 8, 2, 128, 16, False, "random"),
-    ([1100, 1024, 2049, 3000], 1024, 0, 0, 1, 64, 64, False, "equal"),
+    ([1100, 1024, 2049, 2900], 1024, 0, 0, 1, 64, 64, False, "equal"),
+    ([9000, 8193, 4097], 5000, 3, 40, 1, 64, 16, False, "equal"),
+    ([17000, 9], 8190, 3, 40, 2, 64, 128, True, "few"),
     ([3000, 1500], 1025, 2, 100, 2, 64, 32, True, "few"),
     ([500, 4100], 300, 10, 290, 1, 256, 16, False, "random"),
     ([5000], 4999, 0, 0, 3, 128, 256, False, "special"),
@@ -603,6 +605,22 @@ def test_evict(fa, case, in_place):
                 ev[table[j // ps], h, j % ps] = v0[table[src_t // ps], h, src_t % ps]
     assert torch.equal(cache.k.view(torch.uint8), ek.view(torch.uint8))
     assert torch.equal(cache.v.view(torch.uint8), ev.view(torch.uint8))
+
+
+def test_evict_longest(fa):
+    """More entries than fit a cluster's shared memory."""
+    n, budget = 402000, 100001
+    cache = make_cache(fa, 54, [n], 1, 64, 256, weight=True)
+    cache.weight.copy_(weights_of("few", gen(55), tuple(cache.weight.shape)) + (cache.weight < 0.5))
+    w0, k0 = cache.weight.clone(), cache.k.clone()
+    kept = fa.fa_cache_evict(cache, budget, n_first=4, n_recent=1000)
+    assert fa.fa_sync_status() == fa.FA_OK and int(cache.lens[0]) == budget
+    order = np.arange(n)
+    src = R.evict(w0[0, 0].cpu().numpy(), order, n, n, budget, 4, 1000)
+    assert kept[0, 0].tolist() == src
+    src_t, j, table = torch.tensor(src, device=DEV), torch.arange(budget, device=DEV), cache.block_table[0].long()
+    assert torch.equal(cache.weight[0, 0, :budget], w0[0, 0][src_t])
+    assert torch.equal(cache.k[table[j // 256], 0, j % 256], k0[table[src_t // 256], 0, src_t % 256])
 
 
 def test_evict_without_order(fa):
