@@ -97,10 +97,9 @@ int cache_check(const fa_kv_cache *c)
     if ((reinterpret_cast<uintptr_t>(c->k) & 127u) || (reinterpret_cast<uintptr_t>(c->v) & 127u))
         return FA_ERR_INVALID_ARG;
     const uintptr_t words = reinterpret_cast<uintptr_t>(c->lens) | reinterpret_cast<uintptr_t>(c->block_table) |
-                            reinterpret_cast<uintptr_t>(c->seen) | reinterpret_cast<uintptr_t>(c->weight) |
-                            reinterpret_cast<uintptr_t>(c->order) | reinterpret_cast<uintptr_t>(c->k_scale) |
+                            reinterpret_cast<uintptr_t>(c->seen) | reinterpret_cast<uintptr_t>(c->k_scale) |
                             reinterpret_cast<uintptr_t>(c->v_scale);
-    if (words & 3u)
+    if ((words & 3u) || !fa::aligned16(c->weight) || !fa::aligned16(c->order))
         return FA_ERR_INVALID_ARG;
     if ((c->dtype == FA_E4M3) != (c->k_scale != nullptr) || (c->dtype == FA_E4M3) != (c->v_scale != nullptr))
         return FA_ERR_INVALID_ARG;
@@ -363,8 +362,8 @@ int fa_cache_evict(const fa_kv_cache *cache, int budget, int n_first, int n_rece
         return FA_ERR_INVALID_ARG;
     if (!weight_out || !lens_out || !kept)
         return FA_ERR_INVALID_ARG;
-    if ((reinterpret_cast<uintptr_t>(weight_out) | reinterpret_cast<uintptr_t>(order_out) |
-         reinterpret_cast<uintptr_t>(lens_out) | reinterpret_cast<uintptr_t>(kept)) & 3u)
+    if (!fa::aligned16(weight_out) || !fa::aligned16(order_out) || !fa::aligned16(kept) ||
+        (reinterpret_cast<uintptr_t>(lens_out) & 3u))
         return FA_ERR_INVALID_ARG;
     if (!cache_disjoint(cache))
         return FA_ERR_INVALID_ARG;

@@ -381,14 +381,17 @@ __device__ __forceinline__ int block_rank(bool p, int &total, int *scratch)
 
 // ---- selection by a cluster per (sequence, KV head)
 // The entries' ranks are read once and stay in shared memory, a contiguous run of slots per CTA.
-// Three passes of a radix select (11, 11 and 10 bits; counts of the whole cluster read over
-// distributed shared memory, every CTA finds the digit for itself) give the rank of the last
-// entry that stays; then one scan per question over runs of consecutive slots per thread: which
+// Four passes of a radix select of 8 bits (counts of the whole cluster read over distributed
+// shared memory, every CTA finds the digit for itself; fewer when all that match a prefix stay)
+// give the rank of the last entry that stays.  Digits of 11 bits save a pass but read 8 times the
+// counts from every CTA: 53 us for 32 units of up to 32768 entries, where this takes 19.  Then one
+// scan per question over runs of consecutive slots per thread: which
 // of several equals stay, and the numbers of the holes in front of the new length and of the kept
 // entries behind it.  The kept ones wait at the front of `kept` until every hole has read its own.
-constexpr int kSelBits = 11, kSelBins = 1 << kSelBits;
+constexpr int kSelBins = 256, kSelPasses = 4;
 constexpr int kSelItems = 49;                                // entries a thread, at most (odd: see run)
-constexpr int kSelFixed = 3 * kSelBins * 4 + 2 * 32 * 4 + 32;   // shared memory besides the ranks
+constexpr int kSelCopies = 8;                                // of the first pass's counts: most ranks share a few digits
+constexpr int kSelFixed = (kSelPasses + kSelCopies) * kSelBins * 4 + 2 * 32 * 4 + 32;   // shared memory besides the ranks
 
 __device__ __forceinline__ void cluster_sync()
 {
@@ -424,8 +427,8 @@ __device__ __forceinline__ int block_scan(int x, int &total, int *scratch)
 
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_constant__ EvictArgs a, int cs)
 {
-    extern __shared__ int sel_smem[];
-    int *hist = sel_smem, *scratch = hist + 3 * kSelBins, *share = scratch + 32, *pick = share + 32;
+    extern __shared__ __align__(16) int sel_smem[];
+    int *copies = sel_smem, *hist = copies + kSelCopies * kSelBins, *scratch = hist + kSelPasses * kSelBins, *share = scratch + 32, *pick = share + 32;
     uint32_t *keys = reinterpret_cast<uint32_t *>(pick + 8);
     const int rank = (int)blockIdx.x % cs, unit = (int)blockIdx.x / cs, b = unit / a.Hkv, tid = threadIdx.x;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -451,56 +454,71 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
         }
         return;
     }
-    for (int i = tid; i < 3 * kSelBins; i += kSelThreads)
-        hist[i] = 0;
+    for (int i = tid; i < (kSelCopies + kSelPasses) * kSelBins; i += kSelThreads)
+        copies[i] = 0;
     const int per = (len + cs - 1) / cs, lo = min(len, rank * per), n = min(len, lo + per) - lo;
     const int recent = (a.seen ? a.seen[b] : len) - a.n_recent;
     const bool ages = order && (a.n_first > 0 || a.n_recent > 0);
     __syncthreads();
-    for (int i = tid; i < n; i += kSelThreads) {
-        bool prot = false;
-        if (ages) {
-            const int at = order[lo + i];
-            prot = at < a.n_first || (a.n_recent > 0 && at >= recent);
+    for (int i0 = tid; i0 < n; i0 += 4 * kSelThreads) {   // four loads in flight
+        float w[4];
+        int at[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int i = i0 + u * kSelThreads;
+            w[u] = i < n ? weight[lo + i] : 0.f;
+            at[u] = ages && i < n ? order[lo + i] : 0;
         }
-        const uint32_t u = rank_key(weight[lo + i], prot);
-        keys[i] = u;
-        atomicAdd(&hist[u >> 21], 1);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int i = i0 + u * kSelThreads;
+            if (i < n) {
+                const uint32_t k = rank_key(w[u], ages && (at[u] < a.n_first || (a.n_recent > 0 && at[u] >= recent)));
+                keys[i] = k;
+                atomicAdd(&copies[(k >> 24) * kSelCopies + (tid & (kSelCopies - 1))], 1);
+            }
+        }
     }
     uint32_t prefix = 0;
     int need = end, equal = 0;   // still to be taken among those that match the prefix; how many do
 #pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
-        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    for (int pass = 0; pass < kSelPasses; ++pass) {
+        const int shift = 24 - 8 * pass;
         int *hp = hist + pass * kSelBins;
         if (pass > 0) {
-            const uint32_t mask = pass == 1 ? 0xFFE00000u : 0xFFFFFC00u;
             for (int i = tid; i < n; i += kSelThreads) {
                 const uint32_t u = keys[i];
-                if ((u & mask) == prefix)
-                    atomicAdd(&hp[pass == 1 ? (u >> 10) & 2047 : u & 1023], 1);
+                if ((u ^ prefix) >> (shift + 8) == 0)
+                    atomicAdd(&hp[(u >> shift) & 255], 1);
+            }
+        } else {
+            __syncthreads();
+            if (tid < kSelBins) {
+                const int4 x = reinterpret_cast<const int4 *>(copies)[2 * tid], y = reinterpret_cast<const int4 *>(copies)[2 * tid + 1];
+                hp[tid] = x.x + x.y + x.z + x.w + y.x + y.y + y.z + y.w;
             }
         }
         cluster_sync();
-        // bins from the top, two a thread
-        const int d0 = kSelBins - 1 - 2 * tid, d1 = d0 - 1;
-        int c0 = 0, c1 = 0;
-        for (int r = 0; r < cs; ++r) {
-            c0 += cluster_load(hp + d0, r);
-            c1 += cluster_load(hp + d1, r);
-        }
+        // four threads a bin, bins from the top
+        const int d = kSelBins - 1 - (tid >> 2);
+        int c = 0;
+        for (int r = tid & 3; r < cs; r += 4)
+            c += cluster_load(hp + d, r);
+        c += __shfl_xor_sync(0xffffffffu, c, 1);
+        c += __shfl_xor_sync(0xffffffffu, c, 2);
         int total;
-        const int before = block_scan(c0 + c1, total, scratch);
-        if (before < need && need <= before + c0 + c1) {
-            const bool first = need <= before + c0;
-            pick[0] = first ? d0 : d1;
-            pick[1] = need - before - (first ? 0 : c0);
-            pick[2] = first ? c0 : c1;
+        const int before = block_scan((tid & 3) ? 0 : c, total, scratch);
+        if ((tid & 3) == 0 && before < need && need <= before + c) {
+            pick[0] = d;
+            pick[1] = need - before;
+            pick[2] = c;
         }
         __syncthreads();
         prefix |= (uint32_t)pick[0] << shift;
         need = pick[1];
         equal = pick[2];
+        if (equal == need)   // all that match stay: the lower digits do not matter
+            break;
     }
     // an odd run of consecutive slots per thread: the runs of a warp lie in different banks
     const int q = ((n + kSelThreads - 1) / kSelThreads) | 1, i0 = min(n, tid * q), i1 = min(n, i0 + q);
@@ -553,12 +571,27 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
     for (int i = i0; i < i1 && lo + i < end; ++i)
         keys[i] = stays(i) ? lo + i : kept[hole++];
     cluster_sync();
-    for (int i = tid; i < n && lo + i < end; i += kSelThreads) {
-        const int from = (int)keys[i], j = lo + i;
-        kept[j] = from;
-        a.weight_out[base + j] = weight[from];
-        if (order)
-            a.order_out[base + j] = order[from];
+    const int front = min(n, end - lo);
+    for (int i0 = tid; i0 < front; i0 += 4 * kSelThreads) {
+        float w[4];
+        int at[4], from[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int i = i0 + u * kSelThreads;
+            from[u] = i < front ? (int)keys[i] : 0;
+            w[u] = weight[from[u]];
+            at[u] = order ? order[from[u]] : 0;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int i = i0 + u * kSelThreads, j = lo + i;
+            if (i < front) {
+                kept[j] = from[u];
+                a.weight_out[base + j] = w[u];
+                if (order)
+                    a.order_out[base + j] = at[u];
+            }
+        }
     }
 }
 
@@ -851,9 +884,10 @@ int evict_launch(const fa_kv_cache &c, int budget, int n_first, int n_recent, fl
     a.ps_shift = shift_of(c.page_size);
     a.row_bytes = c.d * (c.dtype == FA_E4M3 ? 1 : 2);
     const int units = c.B * c.Hkv;
-    // CTAs per (sequence, KV head): 1024 entries or more each, as long as all are resident
+    // CTAs per (sequence, KV head): 1024 entries or more each, at most one CTA an SM (4112 entries in
+    // 64 units: 16.6, 15.9, 21.3, 39.8 us with 1, 2, 4, 8; up to 32768 in 32: 50.0, 40.8, 36.5, 39.1)
     int cs = 1;
-    while (cs < 8 && a.cap / (2 * cs) >= kSelThreads && (long long)units * 2 * cs <= 2ll * device_sm_count())
+    while (cs < 8 && a.cap / (2 * cs) >= kSelThreads && (long long)units * 2 * cs <= device_sm_count())
         cs *= 2;
     while (cs < 8 && (a.cap + cs - 1) / cs > kSelItems * kSelThreads)
         cs *= 2;

@@ -82,8 +82,9 @@ struct PagedArgs {
     const float *ks, *vs;
     const int *block_table, *lens;
     float *part;     // [2 grid][rows][D] then m, l [rows]
+    long long *where;   // [0] the share, [1 + b] the first tile of sequence b (not of an empty one)
     float *scores;   // [sequence][KV head][row][cap]
-    int B, Hq, Hkv, G, Tq, M, rows, RB, causal, num_pages, max_pages, ps_shift, cap, grid;
+    int B, Hq, Hkv, G, Tq, M, rows, RB, causal, num_pages, max_pages, ps_shift, cap, grid, whole;
     float scale_log2;
     uint64_t timeout_ns;
 };
@@ -275,12 +276,26 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
         *abort_flag = 0;
         fence_mbar_init();
     }
-    const long long total = block_tiles(a, a.B, reinterpret_cast<volatile long long *>(smem + C::OFF_MISC + 16)) *
-                            a.Hkv * a.RB;
-    const long long share = share_of(a, total), t0 = share * blockIdx.x;
-    if (t0 >= total)
-        return;
-    Place p = place_of(a, t0, min(share, total - t0));
+    Place p;
+    long long share = 0, t0 = 0, mine_all;   // mine_all: tiles of this CTA
+    if (a.whole) {                           // one unit a CTA, however long
+        const int per = a.Hkv * a.RB, b = (int)blockIdx.x / per;
+        const int nt = tiles_of(a, b);
+        p = Place{b, (int)blockIdx.x - b * per, 0, nt, nt};
+        mine_all = nt;
+        __syncthreads();   // the barriers are there
+    } else {
+        const long long total = block_tiles(a, a.B, reinterpret_cast<volatile long long *>(smem + C::OFF_MISC + 16)) *
+                                a.Hkv * a.RB;
+        share = share_of(a, total);
+        t0 = share * blockIdx.x;
+        if (threadIdx.x == 0 && blockIdx.x == 0)
+            a.where[0] = share;
+        if (t0 >= total)
+            return;
+        mine_all = min(share, total - t0);
+        p = place_of(a, t0, mine_all);
+    }
     // rows of a page in one box, and boxes of a tile
     const int bp_shift = a.ps_shift < 6 ? a.ps_shift : 6, boxes = KT >> bp_shift;
 
@@ -347,8 +362,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
         const uint32_t q_lane = sbase + C::OFF_Q + (rt * 16 + (lane & 15)) * C::QPITCH + (lane >> 4) * 16;
         uint32_t n = 0;
         bool ok = true;
+        if (p.left == 0) {   // whole units: an empty sequence
+            const int h = p.ul % a.Hkv, row0 = p.ul / a.Hkv * a.rows, nrows = min(a.rows, a.M - row0);
+            const long long grow = ((long long)p.b * a.Hq + h * a.G) * a.Tq + row0;
+            for (int e = threadIdx.x; e < nrows * (D / 8); e += 32 * kMathWarps)
+                reinterpret_cast<uint4 *>(a.o + grow * D)[e] = make_uint4(0, 0, 0, 0);
+            for (int r = threadIdx.x; r < nrows; r += 32 * kMathWarps)
+                a.lse[grow + r] = -INFINITY;
+        }
         while (p.left > 0) {
             const int len = length_of(a, p.b), h = p.ul % a.Hkv, rb = p.ul / a.Hkv, cnt = segment(p);
+            if (threadIdx.x == 0 && p.tile == 0 && p.ul == 0 && !a.whole)
+                a.where[1 + p.b] = t0 + (mine_all - p.left);
             const int row0 = rb * a.rows, nrows = min(a.rows, a.M - row0);
             // ---- the unit's query rows: bf16, or f16 over the row's power of two with features in
             // the order in which the codes of four neighbours come out of a register
@@ -601,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
             auto weight = [](float m, float t) { return m == -INFINITY ? 0.f : ex2_approx(m - t); };
             const float f0 = weight(m0, top(rt, r0)), f1 = weight(m1, top(rt, r0 + 8));
             const bool whole = p.tile == 0 && cnt == p.nt;
-            const long long slot = 2ll * blockIdx.x + (t0 + (min(share, total - t0) - p.left) == t0 ? 0 : 1);
+            const long long slot = 2ll * blockIdx.x + (p.left == mine_all ? 0 : 1);
             float *part = a.part + slot * a.rows * (D + 2);
             const float vs = FP8 ? a.vs[h] : 1.f;
 #pragma unroll
@@ -676,28 +701,32 @@ struct Parts {
     bool none;   // no entry at all
 };
 
-__device__ __forceinline__ Parts parts_of(const PagedArgs &a, int b, int ul, volatile long long *scratch)
+__device__ __forceinline__ Parts parts_of(const PagedArgs &a, int b, int ul, int nt)
 {
-    const int per = a.Hkv * a.RB, nt = tiles_of(a, b);
-    const long long before = block_tiles(a, b, scratch) * per, total = block_tiles(a, a.B, scratch) * per;
-    const long long share = share_of(a, total), t = before + (long long)ul * nt;
-    Parts p;
-    p.none = nt == 0;
-    p.c0 = (int)(t / share);
-    p.c1 = (int)((t + nt - 1) / share);
-    p.s0 = 2ll * p.c0 + (t == p.c0 * share ? 0 : 1);
+    Parts p{0, 0, 0, nt == 0};
+    if (nt > 0) {
+        const long long share = a.where[0], t = a.where[1 + b] + (long long)ul * nt;
+        p.c0 = (int)(t / share);
+        p.c1 = (int)((t + nt - 1) / share);
+        p.s0 = 2ll * p.c0 + (t == p.c0 * share ? 0 : 1);
+    }
     return p;
 }
 
 // Blocks [0, units * rows): o and lse of one row of a unit whose entries were split (or of a
-// sequence without any).  Blocks from there: 256 entries' weights of one (sequence, KV head).
+// sequence without any).  Blocks from there: kWeightRun entries' weights of one (sequence, KV head).
+// The states of a row are read by D / 2 threads a state, two features each, so that several are
+// under way at once.
+constexpr int kJoinThreads = 128, kWeightRun = 4 * kJoinThreads;
+constexpr int kMaxParts = 2 * kSMs;
+
 template <int D>
-__global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ PagedArgs a, int wchunks)
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedArgs a, int wchunks)
 {
-    __shared__ long long scratch[4];
-    __shared__ float row_lse[kMaxRows];
+    __shared__ float wt[kMaxParts], row_lse[kMaxRows], sums[kJoinThreads * 2], red[8];
     const int tid = threadIdx.x, per = a.Hkv * a.RB;
     const long long rows_total = (long long)a.B * per * a.rows, blk = blockIdx.x;
+    const long long stride = (long long)a.rows * (D + 2);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (blk < rows_total) {
         const int row = (int)(blk % a.rows);
@@ -705,85 +734,120 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
         const int b = (int)(unit / per), ul = (int)(unit - (long long)b * per), h = ul % a.Hkv, rb = ul / a.Hkv;
         if (rb * a.rows + row >= a.M)
             return;
-        const Parts p = parts_of(a, b, ul, scratch);
+        const Parts p = parts_of(a, b, ul, tiles_of(a, b));
         if (!p.none && p.c0 == p.c1)
             return;
         const long long grow = ((long long)b * a.Hq + h * a.G) * a.Tq + rb * a.rows + row;
-        const long long stride = (long long)a.rows * (D + 2);
-        float m = -INFINITY, l = 0.f, x[D / 64] = {};
-        if (!p.none) {
-            auto slot = [&](int c) { return a.part + (c == p.c0 ? p.s0 : 2ll * c) * stride; };
-            for (int c = p.c0; c <= p.c1; ++c)
-                m = fmaxf(m, slot(c)[(long long)a.rows * D + row]);
-            if (m != -INFINITY)
-#pragma unroll 4
-                for (int c = p.c0; c <= p.c1; ++c) {
-                    const float *s = slot(c);
-                    const float mc = s[(long long)a.rows * D + row], w = mc == -INFINITY ? 0.f : ex2_approx(mc - m);
-                    l = fmaf(w, s[(long long)a.rows * (D + 1) + row], l);
-                    if (tid < 64)
-#pragma unroll
-                        for (int i = 0; i < D / 64; ++i)
-                            x[i] = fmaf(w, s[(long long)row * D + i * 64 + tid], x[i]);
-                }
+        auto slot = [&](int i) { return a.part + (i == 0 ? p.s0 : 2ll * (p.c0 + i)) * stride; };
+        const int n = p.none ? 0 : p.c1 - p.c0 + 1;
+        // the states' maxima, then their weights
+        float m = -INFINITY, l = 0.f;
+        for (int i = tid; i < n; i += kJoinThreads) {
+            wt[i] = slot(i)[(long long)a.rows * D + row];
+            m = fmaxf(m, wt[i]);
         }
-        if (tid < 64) {
-            const float k = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-            for (int i = 0; i < D / 64; ++i)
-                a.o[grow * D + i * 64 + tid] = __float2bfloat16(x[i] * k);
+        for (int off = 16; off > 0; off >>= 1)
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+        if (lane_id() == 0)
+            red[warp_id()] = m;
+        __syncthreads();
+        m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+        for (int i = tid; i < n; i += kJoinThreads) {
+            const float w = wt[i] == -INFINITY ? 0.f : ex2_approx(wt[i] - m);
+            l = fmaf(w, slot(i)[(long long)a.rows * (D + 1) + row], l);
+            wt[i] = w;
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1)
+            l += __shfl_xor_sync(0xffffffffu, l, off);
+        if (lane_id() == 0)
+            red[4 + warp_id()] = l;
+        __syncthreads();
+        l = (red[4] + red[5]) + (red[6] + red[7]);
+        constexpr int GROUPS = 2 * kJoinThreads / D;   // states under way
+        const int g = tid / (D / 2), f = 2 * (tid % (D / 2));
+        float2 x = make_float2(0.f, 0.f);
+#pragma unroll 8
+        for (int i = g; i < n; i += GROUPS) {
+            const float2 y = *reinterpret_cast<const float2 *>(slot(i) + (long long)row * D + f);
+            x.x = fmaf(wt[i], y.x, x.x);
+            x.y = fmaf(wt[i], y.y, x.y);
+        }
+        reinterpret_cast<float2 *>(sums)[tid] = x;
+        __syncthreads();
+        if (g == 0) {
+#pragma unroll
+            for (int w = 1; w < GROUPS; ++w) {
+                const float2 y = reinterpret_cast<const float2 *>(sums)[w * (D / 2) + tid];
+                x.x += y.x;
+                x.y += y.y;
+            }
+            const float k = l == 0.f ? 0.f : 1.f / l;
+            *reinterpret_cast<uint32_t *>(a.o + grow * D + f) = pack_bf16x2(x.x * k, x.y * k);
             if (tid == 0)
                 a.lse[grow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
         }
         return;
     }
-    // ---- weight_j += sum over the rows of p_j = 2^{s_j - lse}
+    // ---- weight_j += sum over the rows of p_j = 2^{s_j - lse}, four neighbours a thread
     const long long wb = blk - rows_total, uh = wb / wchunks;
     const int b = (int)(uh / a.Hkv), h = (int)(uh - (long long)b * a.Hkv), len = length_of(a, b);
-    const int first = (int)(wb - uh * wchunks) * 256;
-    if (first >= len)
+    const int j = (int)(wb - uh * wchunks) * kWeightRun + 4 * tid;
+    if (j - 4 * tid >= len)
         return;
-    float sum[2] = {0.f, 0.f};
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int rb = 0; rb < a.RB; ++rb) {
-        const Parts p = parts_of(a, b, rb * a.Hkv + h, scratch);
+        const Parts p = parts_of(a, b, rb * a.Hkv + h, (len + KT - 1) / KT);
         const int row0 = rb * a.rows, nrows = min(a.rows, a.M - row0);
-        const long long stride = (long long)a.rows * (D + 2);
-        for (int r = tid; r < nrows; r += 128) {
+        for (int r = tid; r < nrows; r += kJoinThreads) {
             float y;
             if (p.c0 == p.c1) {
                 y = a.lse[((long long)b * a.Hq + h * a.G) * a.Tq + row0 + r] * 1.4426950408889634f;
             } else {
                 float m = -INFINITY, l = 0.f;
-                auto slot = [&](int c) { return a.part + (c == p.c0 ? p.s0 : 2ll * c) * stride + (long long)a.rows * D + r; };
-                for (int c = p.c0; c <= p.c1; ++c)
-                    m = fmaxf(m, *slot(c));
-                if (m != -INFINITY)
-                    for (int c = p.c0; c <= p.c1; ++c) {
-                        const float *s = slot(c);
-                        l = fmaf(s[a.rows], s[0] == -INFINITY ? 0.f : ex2_approx(s[0] - m), l);
-                    }
+                const int n = p.c1 - p.c0 + 1;
+                auto slot = [&](int i) { return a.part + (i == 0 ? p.s0 : 2ll * (p.c0 + i)) * stride + (long long)a.rows * D + r; };
+#pragma unroll 4
+                for (int i = 0; i < n; ++i) {   // online, so that both loads of a state go together
+                    const float mi = *slot(i), li = slot(i)[a.rows], t = fmaxf(m, mi), z = t == -INFINITY ? 0.f : t;
+                    l = l * ex2_approx(m - z) + li * ex2_approx(mi - z);
+                    m = t;
+                }
                 y = l == 0.f ? -INFINITY : m + log2f(l);
             }
             // a row that saw nothing has no finite score either: 2^{-inf - 0}
             row_lse[r] = y == -INFINITY ? 0.f : y;
         }
         __syncthreads();
-        const float *sp = a.scores + (uh * a.M + row0) * a.cap;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int j = first + i * 128 + tid;
-            if (j < len)
+        // the stored scores reach to the end of the last group of 16 entries
+        if (j < len) {
+            const float *sp = a.scores + (uh * a.M + row0) * a.cap + j;
 #pragma unroll 4
-                for (int r = 0; r < nrows; ++r)
-                    sum[i] += ex2_approx(sp[(long long)r * a.cap + j] - row_lse[r]);
+            for (int r = 0; r < nrows; ++r) {
+                const float4 s = *reinterpret_cast<const float4 *>(sp + (long long)r * a.cap);
+                const float y = row_lse[r];
+                sum.x += ex2_approx(s.x - y);
+                sum.y += ex2_approx(s.y - y);
+                sum.z += ex2_approx(s.z - y);
+                sum.w += ex2_approx(s.w - y);
+            }
         }
         __syncthreads();
     }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int j = first + i * 128 + tid;
-        if (j < len)
-            a.weight[uh * a.cap + j] += sum[i];
+    if (j >= len)
+        return;
+    float *w = a.weight + uh * a.cap + j;
+    if (j + 4 <= len) {
+        float4 x = *reinterpret_cast<const float4 *>(w);
+        x.x += sum.x, x.y += sum.y, x.z += sum.z, x.w += sum.w;
+        *reinterpret_cast<float4 *>(w) = x;
+    } else {
+        w[0] += sum.x;
+        if (j + 1 < len)
+            w[1] += sum.y;
+        if (j + 2 < len)
+            w[2] += sum.z;
     }
 }
 
@@ -794,6 +858,10 @@ int rows_of(int M) { return M < kMaxRows ? M : kMaxRows; }
 int row_tiles(int M) { return M <= 16 ? 1 : M <= 32 ? 2 : 4; }
 int grid_of(int d) { return kSMs * (d == 256 ? 1 : 2); }
 
+// Tables of up to this many slots: one CTA a unit and no join.
+constexpr int kWholeSlots = 512;
+
+size_t where_bytes(int B) { return round256((size_t)(B + 1) * sizeof(long long)); }
 size_t part_bytes(int M, int d) { return round256((size_t)2 * grid_of(d) * rows_of(M) * (d + 2) * sizeof(float)); }
 
 // K or V pool as [page, KV head][column chunk][row][CB bytes]; a box is all chunks of a page's
@@ -832,7 +900,10 @@ int paged_run(const fa_kv_cache &c, PagedArgs &a, cudaStream_t s)
         const int box = c.page_size < KT ? c.page_size : KT;
         if ((st = encode_pool(&tk, c.k, c, box)) != OK || (st = encode_pool(&tv, c.v, c, box)) != OK)
             return st;
-        const int grid = (int)(most < a.grid ? most : a.grid);
+        const long long units = (long long)a.B * a.Hkv * a.RB;
+        if (a.whole && units > INT_MAX)
+            return ERR_UNSUPPORTED;
+        const int grid = (int)(a.whole ? units : most < a.grid ? most : a.grid);
         if (f8)
             st = rt == 1   ? launch_main<D, true, 1>(tk, tv, a, grid, s)
                  : rt == 2 ? launch_main<D, true, 2>(tk, tv, a, grid, s)
@@ -844,14 +915,16 @@ int paged_run(const fa_kv_cache &c, PagedArgs &a, cudaStream_t s)
         if (st != OK)
             return st;
     }
-    const int wchunks = a.scores ? (a.cap + 255) / 256 : 0;
+    if (a.whole && most > 0)
+        return OK;
+    const int wchunks = a.scores ? (a.cap + kWeightRun - 1) / kWeightRun : 0;
     const long long blocks = (long long)a.B * a.Hkv * a.RB * a.rows + (long long)a.B * a.Hkv * wchunks;
     if (blocks > INT_MAX)
         return ERR_UNSUPPORTED;
     // launched while the first kernel runs, waits for it inside
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)blocks);
-    cfg.blockDim = dim3(128);
+    cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = s;
     cudaLaunchAttribute at;
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -865,7 +938,7 @@ int paged_run(const fa_kv_cache &c, PagedArgs &a, cudaStream_t s)
 
 size_t paged_workspace_bytes(int B, int Hq, int Hkv, int Tq, int max_len, int d, int accumulate)
 {
-    return part_bytes(Hq / Hkv * Tq, d) + (accumulate ? round256((size_t)B * Hq * Tq * max_len * sizeof(float)) : 0);
+    return where_bytes(B) + part_bytes(Hq / Hkv * Tq, d) + (accumulate ? round256((size_t)B * Hq * Tq * max_len * sizeof(float)) : 0);
 }
 
 int paged_launch(const fa_kv_cache &c, const void *q, void *o, float *lse, int Hq, int Tq, int causal, float scale,
@@ -896,8 +969,11 @@ int paged_launch(const fa_kv_cache &c, const void *q, void *o, float *lse, int H
         ++a.ps_shift;
     a.cap = c.num_pages > 0 ? c.max_pages * c.page_size : 0;   // no pages: every length above 0 is out of range
     a.grid = grid_of(c.d);
-    a.part = static_cast<float *>(workspace);
-    a.scores = accumulate ? reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + part_bytes(a.M, c.d)) : nullptr;
+    a.whole = !accumulate && a.cap <= kWholeSlots;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    a.where = reinterpret_cast<long long *>(ws);
+    a.part = reinterpret_cast<float *>(ws + where_bytes(c.B));
+    a.scores = accumulate ? reinterpret_cast<float *>(ws + where_bytes(c.B) + part_bytes(a.M, c.d)) : nullptr;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.timeout_ns = wait_timeout_ns();
     return c.d == 64 ? paged_run<64>(c, a, s) : c.d == 128 ? paged_run<128>(c, a, s) : paged_run<256>(c, a, s);

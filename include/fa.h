@@ -232,7 +232,7 @@ int fa_rope(const fa_heads *x, const fa_heads *y, int n, const int *positions, c
 /*
  * A paged cache of B sequences, all pointers to device memory:
  *   k, v         [num_pages][Hkv][page_size][d], bf16 (FA_BF16) or e4m3 codes
- *                (FA_E4M3), 128-byte aligned
+ *                (FA_E4M3)
  *   k_scale, v_scale  [Hkv] f32, FA_E4M3 only: a code c of head h stands for
  *                c * scale[h] (positive, finite); NULL for FA_BF16
  *   block_table  [B][max_pages] int32: entry i of sequence b (its slot i) is
@@ -244,6 +244,7 @@ int fa_rope(const fa_heads *x, const fa_heads *y, int n, const int *positions, c
  *                weight of each entry, or NULL
  *   order        [B][Hkv][max_pages * page_size] int32: arrival number of each
  *                entry (the first token of a sequence has 0), or NULL
+ * k and v are 128-byte, weight and order 16-byte, the other arrays 4-byte aligned.
  * page_size is 16, 32, 64, 128 or 256; d 64, 128 or 256.  Only the pages and
  * rows in front of lens are read: what lies behind them may hold anything.
  * Sequences may share pages that none of them writes to (fa_cache_append and
