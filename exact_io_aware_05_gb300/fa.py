@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -56,9 +57,10 @@ _lib.fa_status_string.argtypes = [_i]
 _lib.fa_status_string.restype = ctypes.c_char_p
 
 
-class _Heads(ctypes.Structure):
-    _fields_ = [("data", _vp), ("stride_b", ctypes.c_longlong), ("stride_h", ctypes.c_longlong),
-                ("stride_t", ctypes.c_longlong), ("H", _i)]
+# one and two fa_heads (data, three strides, H), packed in one go: a step of a serving loop is a few
+# microseconds on the device, and a ctypes structure costs one to build
+_HEADS = struct.Struct("PqqqiI")
+_HEADS2 = struct.Struct("PqqqiIPqqqiI")
 
 
 class _RopeSpec(ctypes.Structure):
@@ -452,31 +454,27 @@ def rope_spec(d: int, sections=None, base: float = 10000.0, rot: int | None = No
     return RopeSpec(d, [base ** (-2.0 * i / rot) for i in range(rot // 2)], axis, interleaved)
 
 
-def _on(device: torch.device, stream):
-    """The stream to launch on: the given one, else the current stream of the tensors' device."""
-    if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
-    return _stream(stream)
+_current_stream = torch._C._cuda_getCurrentRawStream    # of a device index; torch.cuda's builds an object
+_current_device = torch._C._cuda_getDevice
 
 
-class _device_of:
-    """Makes the tensors' device current for a call, if it is not."""
-
-    __slots__ = ("want", "had")
-
-    def __init__(self, device: torch.device):
-        if device.type != "cuda":
-            raise ValueError(f"expected CUDA tensors, got {device}")
-        self.want = device.index if device.index is not None else torch.cuda.current_device()
-
-    def __enter__(self):
-        self.had = torch.cuda.current_device()
-        if self.had != self.want:
-            torch.cuda.set_device(self.want)
-
-    def __exit__(self, *exc):
-        if self.had != self.want:
-            torch.cuda.set_device(self.had)
+def _launch(fn: str, entry, index: int, stream, *args) -> None:
+    """Calls `entry` with the tensors' device current and a stream of that device: the given one, or
+    its current stream."""
+    if index < 0:
+        raise ValueError(f"{fn}: expected CUDA tensors")
+    stream = _current_stream(index) if stream is None else _stream(stream)
+    had = _current_device()
+    if had == index:
+        st = entry(*args, stream)
+    else:
+        torch.cuda.set_device(index)
+        try:
+            st = entry(*args, stream)
+        finally:
+            torch.cuda.set_device(had)
+    if st != FA_OK:
+        raise FAError(fn, st)
 
 
 def _record(stream, *tensors) -> None:
@@ -486,43 +484,47 @@ def _record(stream, *tensors) -> None:
             t.record_stream(stream)
 
 
-def _heads(t: torch.Tensor, name: str, dtype, shape, device) -> _Heads:
-    """A [B, H, T, d] tensor by strides; only the last dimension has to be contiguous."""
-    if t.dtype != dtype:
+def _heads(t: torch.Tensor, name: str, dtype, shape, index: int) -> tuple:
+    """The fields of fa_heads of a [B, H, T, d] tensor; only its last dimension has to be contiguous."""
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name}: expected device {device}, got {t.device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name}: expected a tensor on the others' device, got {t.device}")
     sb, sh, st, sd = t.stride()
     if sd != 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
     # the stride of a dimension of one entry is never used: torch leaves any value there
     B, H, T, _ = shape
-    return _Heads(t.data_ptr(), sb if B > 1 else 0, sh if H > 1 else 0, st if T > 1 else 0, H)
+    return t.data_ptr(), sb if B > 1 else 0, sh if H > 1 else 0, st if T > 1 else 0, H, 0
 
 
 def _rope(fn, q, q_out, positions, spec, k, k_out, inverse, stream):
-    if q.dim() != 4 or (k is None) != (k_out is None) or (k is not None and k.dim() != 4):
+    shape = q.shape
+    if len(shape) != 4 or (k is None) != (k_out is None):
         raise ValueError("q, k must be [B, H, T, d], with an output for each")
-    B, Hq, T, d = q.shape
-    dev = q.device
+    B, _, T, d = shape
     if d != spec.d:
         raise ValueError(f"q: expected head width {spec.d}, got {d}")
-    _need(positions, "positions", torch.int32, (spec.n_axes, B, T), dev)
-    n = 1 if k is None else 2
-    x, y = (_Heads * 2)(), (_Heads * 2)()
-    x[0] = _heads(q, "q", q.dtype, q.shape, dev)
-    y[0] = _heads(q_out, "q_out", q.dtype, q.shape, dev)
-    if k is not None:
-        shape = torch.Size((B, k.shape[1], T, d))
-        x[1] = _heads(k, "k", q.dtype, shape, dev)
-        y[1] = _heads(k_out, "k_out", q.dtype, shape, dev)
-    if q.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"q: expected torch.bfloat16 or torch.float32, got {q.dtype}")
-    with _device_of(dev):
-        _check(fn, _lib.fa_rope(x, y, n, positions.data_ptr(), spec._ref, B, T,
-                                FA_F32 if q.dtype == torch.float32 else FA_BF16, inverse, _on(dev, stream)))
+    dt, index = q.dtype, q.get_device()
+    if dt is not torch.bfloat16 and dt is not torch.float32:
+        raise TypeError(f"q: expected torch.bfloat16 or torch.float32, got {dt}")
+    if positions.dtype is not torch.int32 or positions.shape != (spec.n_axes, B, T) or \
+            positions.get_device() != index or not positions.is_contiguous():
+        _need(positions, "positions", torch.int32, (spec.n_axes, B, T), q.device)
+    x, y = _heads(q, "q", dt, shape, index), _heads(q_out, "q_out", dt, shape, index)
+    if k is None:
+        n, x, y = 1, _HEADS.pack(*x), _HEADS.pack(*y)
+    else:
+        if k.dim() != 4:
+            raise ValueError("q, k must be [B, H, T, d], with an output for each")
+        shape = (B, k.shape[1], T, d)
+        n = 2
+        x = _HEADS2.pack(*x, *_heads(k, "k", dt, shape, index))
+        y = _HEADS2.pack(*y, *_heads(k_out, "k_out", dt, shape, index))
+    _launch(fn, _lib.fa_rope, index, stream, x, y, n, positions.data_ptr(), spec._ref, B, T,
+            FA_BF16 if dt is torch.bfloat16 else FA_F32, inverse)
 
 
 def fa_rope(q, q_out, positions, spec: RopeSpec, k=None, k_out=None, stream=None) -> None:
@@ -590,7 +592,7 @@ class KVCache:
         self.k, self.v, self.block_table, self.lens = k, v, block_table, lens
         self.k_scale, self.v_scale, self.weight, self.order, self.seen = k_scale, v_scale, weight, order, seen
         self.B, self.Hkv, self.d, self.page_size, self.num_pages, self.max_pages = B, Hkv, d, ps, num_pages, max_pages
-        self.device = dev
+        self.device, self._index = dev, k.get_device()
         self._c = _KVCache(*(_ptr(t) for t in (k, v, k_scale, v_scale, block_table, lens, seen, weight, order)),
                            B, Hkv, d, ps, num_pages, max_pages, FA_E4M3 if codes else FA_BF16)
         self._ref = ctypes.addressof(self._c)
@@ -617,33 +619,33 @@ def fa_cache_append(cache: KVCache, k, v, positions=None, spec: RopeSpec | None 
     """Writes the first new_lens[b] (default: all) of the T rows of k and v [B, Hkv, T, d] as the
     last entries of sequence b; cache.lens (and seen) count them already.  With a spec, k is
     rotated by positions [n_axes, B, T] on the way, and q [B, Hq, T, d] into q_out."""
-    dev, B = cache.device, cache.B
+    index, B, d = cache._index, cache.B, cache.d
     if k.dim() != 4 or (q is not None and q.dim() != 4):
         raise ValueError("k, v, q must be [B, H, T, d]")
-    T = k.shape[2]
-    shape = torch.Size((B, cache.Hkv, T, cache.d))
-    kh, vh = _heads(k, "k", torch.bfloat16, shape, dev), _heads(v, "v", torch.bfloat16, shape, dev)
     if (positions is None) != (spec is None):
         raise ValueError("positions and spec come together")
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out come together")
     if q is not None and spec is None:
         raise ValueError("q is rotated: it needs a spec and positions")
-    pos = qh = oh = new = None
+    T = k.shape[2]
+    shape = (B, cache.Hkv, T, d)
+    bf16 = torch.bfloat16
+    kh, vh = _HEADS.pack(*_heads(k, "k", bf16, shape, index)), _HEADS.pack(*_heads(v, "v", bf16, shape, index))
+    pos = ref = qh = oh = new = None
     if spec is not None:
-        _need(positions, "positions", torch.int32, (spec.n_axes, B, T), dev)
-        pos = positions.data_ptr()
+        if positions.dtype is not torch.int32 or positions.shape != (spec.n_axes, B, T) or \
+                positions.get_device() != index or not positions.is_contiguous():
+            _need(positions, "positions", torch.int32, (spec.n_axes, B, T), cache.device)
+        pos, ref = positions.data_ptr(), spec._ref
     if q is not None:
-        qshape = torch.Size((B, q.shape[1], T, cache.d))
-        qh = ctypes.byref(_heads(q, "q", torch.bfloat16, qshape, dev))
-        oh = ctypes.byref(_heads(q_out, "q_out", torch.bfloat16, qshape, dev))
+        shape = (B, q.shape[1], T, d)
+        qh = _HEADS.pack(*_heads(q, "q", bf16, shape, index))
+        oh = _HEADS.pack(*_heads(q_out, "q_out", bf16, shape, index))
     if new_lens is not None:
-        _need(new_lens, "new_lens", torch.int32, (B,), dev)
+        _need(new_lens, "new_lens", torch.int32, (B,), cache.device)
         new = new_lens.data_ptr()
-    with _device_of(dev):
-        _check("fa_cache_append", _lib.fa_cache_append(
-            cache._ref, ctypes.byref(kh), ctypes.byref(vh), qh, oh, pos, None if spec is None else spec._ref, new, T,
-            _on(dev, stream)))
+    _launch("fa_cache_append", _lib.fa_cache_append, index, stream, cache._ref, kh, vh, qh, oh, pos, ref, new, T)
 
 
 def fa_decode_paged_workspace_bytes(cache: KVCache, Hq: int, Tq: int = 1, accumulate: bool = False) -> int:
@@ -656,21 +658,24 @@ def fa_decode_paged(cache: KVCache, q, o, lse, scale: float, workspace: torch.Te
                     accumulate: bool = False, stream=None) -> None:
     """O and lse of q [B, Hq, Tq, d] (the last Tq tokens of every sequence) over the cache; with
     `accumulate`, cache.weight grows by each entry's attention probabilities."""
-    dev = cache.device
-    if q.dim() != 4:
+    dev, index, shape = cache.device, cache._index, q.shape
+    if len(shape) != 4:
         raise ValueError("q must be [B, Hq, Tq, d]")
-    B, Hq, Tq, d = q.shape
-    shape = (cache.B, Hq, Tq, cache.d)
-    _need(q, "q", torch.bfloat16, shape, dev)
-    _need(o, "o", torch.bfloat16, shape, dev)
-    _need(lse, "lse", torch.float32, shape[:3], dev)
-    if workspace.device != dev or not workspace.is_contiguous():
+    _, Hq, Tq, _ = shape
+    bf16 = torch.bfloat16
+    if not (shape[0] == cache.B and shape[3] == cache.d and o.shape == shape and lse.shape == shape[:3] and
+            q.dtype is bf16 and o.dtype is bf16 and lse.dtype is torch.float32 and
+            q.get_device() == index and o.get_device() == index and lse.get_device() == index and
+            q.is_contiguous() and o.is_contiguous() and lse.is_contiguous()):
+        shape = (cache.B, Hq, Tq, cache.d)
+        _need(q, "q", bf16, shape, dev)
+        _need(o, "o", bf16, shape, dev)
+        _need(lse, "lse", torch.float32, shape[:3], dev)
+    if workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace: must be a contiguous tensor on the same device")
-    with _device_of(dev):
-        _check("fa_decode_paged", _lib.fa_decode_paged(
-            cache._ref, q.data_ptr(), o.data_ptr(), lse.data_ptr(), Hq, Tq, int(bool(causal)), float(scale),
-            int(bool(accumulate)), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-            _on(dev, stream)))
+    _launch("fa_decode_paged", _lib.fa_decode_paged, index, stream, cache._ref, q.data_ptr(), o.data_ptr(),
+            lse.data_ptr(), Hq, Tq, int(bool(causal)), scale, int(bool(accumulate)), workspace.data_ptr(),
+            workspace.nbytes)
 
 
 def attention_decode_paged(cache: KVCache, q, scale: float, causal: bool = True, accumulate: bool = False,
@@ -710,8 +715,6 @@ def fa_cache_evict(cache: KVCache, budget: int, weight_out=None, order_out=None,
         kept = torch.empty((cache.B, cache.Hkv, max(int(budget), 0)), dtype=torch.int32, device=dev)
         _record(stream, kept)
     _need(kept, "kept", torch.int32, (cache.B, cache.Hkv, budget), dev)
-    with _device_of(dev):
-        _check("fa_cache_evict", _lib.fa_cache_evict(
-            cache._ref, int(budget), int(n_first), int(n_recent), weight_out.data_ptr(), _ptr(order_out),
-            lens_out.data_ptr(), kept.data_ptr(), _on(dev, stream)))
+    _launch("fa_cache_evict", _lib.fa_cache_evict, cache._index, stream, cache._ref, int(budget), int(n_first),
+            int(n_recent), weight_out.data_ptr(), _ptr(order_out), lens_out.data_ptr(), kept.data_ptr())
     return kept

@@ -27,10 +27,22 @@ P = 1 << 24        # fake aligned addresses, a megabyte apart: never dereference
 MB = 1 << 20
 
 
+class Heads(ctypes.Structure):
+    _fields_ = [("data", vp), ("stride_b", ll), ("stride_h", ll), ("stride_t", ll), ("H", i)]
+
+
 def heads(fa, at, B=2, H=2, T=4, d=64, **kw):
     f = dict(data=P + at * MB, stride_b=H * T * d, stride_h=T * d, stride_t=d, H=H)
     f.update(kw)
-    return fa._Heads(**f)
+    return Heads(**f)
+
+
+def test_packed_heads_are_the_structure(fa):
+    """The binding packs fa_heads by a format string: the same bytes as the structure's."""
+    one = Heads(P, 1 << 40, 2, 3, 4)
+    assert fa._HEADS.size == ctypes.sizeof(Heads) and fa._HEADS2.size == 2 * ctypes.sizeof(Heads)
+    assert fa._HEADS.pack(P, 1 << 40, 2, 3, 4, 0) == bytes(one)
+    assert fa._HEADS2.pack(P, 1 << 40, 2, 3, 4, 0, P, 1 << 40, 2, 3, 4, 0) == bytes(one) * 2
 
 
 def cache(fa, **kw):
@@ -90,14 +102,14 @@ def test_spec_refusals(fa):
 # ---------------------------------------------------------------- rotation
 def test_rope_refusals(fa):
     f = fa.lib().fa_rope
-    x, y = (fa._Heads * 2)(heads(fa, 0), heads(fa, 1)), (fa._Heads * 2)(heads(fa, 2), heads(fa, 3))
+    x, y = (Heads * 2)(heads(fa, 0), heads(fa, 1)), (Heads * 2)(heads(fa, 2), heads(fa, 3))
     pos, sp = P + 5 * MB, spec(fa)
 
     def call(x=x, y=y, n=2, pos=pos, sp=sp, B=2, T=4, dtype=fa.FA_BF16, inverse=0):
         return f(x, y, n, pos, sp if isinstance(sp, int) or sp is None else sp._ref, B, T, dtype, inverse, None)
 
     def with_(arr, at, **kw):
-        out = (fa._Heads * 2)(*arr)
+        out = (Heads * 2)(*arr)
         for name, val in kw.items():
             setattr(out[at], name, val)
         return out
