@@ -8,7 +8,7 @@
 // What bounds it: K and V are read once, 4 d bytes an entry in bf16, and M = Hq / Hkv * Tq rows use
 // them: 2 M / 2 flops a byte, far below the device's ratio for M up to 64.  So the design is
 // about keeping loads in flight and spreading them evenly:
-//   * The batch's tiles of 64 entries (all sequences and KV heads in a row) are cut into equal
+//   * The batch's tiles of 64 to 256 entries (all sequences and KV heads in a row) are cut into equal
 //     shares, one per CTA, whatever the lengths: a share begins and ends anywhere, so at most its
 //     first and last head are partial, and a partial state (m, l, sum e^{s - m} v) goes to one of
 //     the CTA's two workspace slots.  A second kernel, launched early and waiting for the first,
@@ -38,7 +38,6 @@ __device__ int g_paged_status;   // device status word of the kernels in this fi
 namespace {
 
 constexpr int kStatusBadIndex = 5;
-constexpr int KT = 64;           // entries a tile
 constexpr int kMathWarps = 4;
 constexpr int kThreads = 32 * (kMathWarps + 1);
 constexpr int kSMs = 152;        // the grid is made for the GB300's; results depend on it, not on the device
@@ -52,8 +51,11 @@ struct Cfg {
     static constexpr int ELEM = FP8 ? 1 : 2;
     static constexpr int ROWB = D * ELEM;                          // bytes of an entry's K or V row
     static constexpr int CB = ROWB < 128 ? ROWB : 128;             // bytes of a column chunk
+    static constexpr int KT = ROWB <= 64 ? 256 : ROWB <= 128 ? 128 : 64;   // entries a tile: about 32 KB of K and V
     static constexpr int TILE = KT * ROWB;                         // K or V of a tile
     static constexpr int STAGE = 2 * TILE;
+    static constexpr int GW = KT / 16 * RT / kMathWarps;           // groups of 16 entries a warp has of a tile
+    static constexpr int GP = GW % 2 == 0 && D <= 128 ? 2 : 1;     // groups it takes at once
     static constexpr int QPITCH = D * 2 + 16;                      // bytes of a query row in shared memory
     static constexpr int OC = 32;                                  // features merged at a time
     static constexpr int OPITCH = OC + 4;                          // floats of a merge row
@@ -84,7 +86,7 @@ struct PagedArgs {
     float *part;     // [2 grid][rows][D] then m, l [rows]
     long long *where;   // [0] the share, [1 + b] the first tile of sequence b (not of an empty one)
     float *scores;   // [sequence][KV head][row][cap]
-    int B, Hq, Hkv, G, Tq, M, rows, RB, causal, num_pages, max_pages, ps_shift, cap, grid, whole;
+    int B, Hq, Hkv, G, Tq, M, rows, RB, causal, num_pages, max_pages, ps_shift, cap, grid, whole, kt;
     float scale_log2;
     uint64_t timeout_ns;
 };
@@ -160,14 +162,15 @@ __device__ __forceinline__ int length_of(const PagedArgs &a, int b)
     }
     return len;
 }
-__device__ __forceinline__ int tiles_of(const PagedArgs &a, int b) { return (length_of(a, b) + KT - 1) / KT; }
+__device__ __forceinline__ int tiles_of(const PagedArgs &a, int b) { return (length_of(a, b) + a.kt - 1) / a.kt; }
 
-// Tiles a CTA takes of the batch's `total`: equal shares, but at least 2, below which the
-// joining costs more than the tile.
+// Tiles a CTA takes of the batch's `total`: equal shares, but at least 128 entries, below which
+// the joining costs more than they do.
 __device__ __forceinline__ long long share_of(const PagedArgs &a, long long total)
 {
     const long long c = (total + a.grid - 1) / a.grid;
-    return c < 2 ? 2 : c;
+    const int least = a.kt < 128 ? 128 / a.kt : 1;
+    return c < least ? least : c;
 }
 
 __device__ __forceinline__ long long warp_sum64(long long x)
@@ -297,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
         p = place_of(a, t0, mine_all);
     }
     // rows of a page in one box, and boxes of a tile
-    const int bp_shift = a.ps_shift < 6 ? a.ps_shift : 6, boxes = KT >> bp_shift;
+    const int bp_shift = a.ps_shift < 6 ? a.ps_shift : 6, boxes = C::KT >> bp_shift;
 
     if (warp == kMathWarps) {
         // ---------------------------------------------------------- loads: lane 2 i is K of box i, 2 i + 1 V
@@ -314,12 +317,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
             const int len = length_of(a, p.b), h = p.ul % a.Hkv, cnt = segment(p);
             const int *table = a.block_table + (long long)p.b * a.max_pages;
             auto page_at = [&](int tile) {   // -1: nothing there
-                const int slot = tile * KT + (box << bp_shift);
+                const int slot = tile * C::KT + (box << bp_shift);
                 return mine && slot < len ? table[slot >> a.ps_shift] : -1;
             };
             int page = page_at(p.tile);
             for (int i = 0; i < cnt; ++i, ++n) {
-                const int tile = p.tile + i, slot = tile * KT + (box << bp_shift);
+                const int tile = p.tile + i, slot = tile * C::KT + (box << bp_shift);
                 const int next = i + 1 < cnt ? page_at(tile + 1) : -1;
                 const uint32_t st = n % C::NST;
                 if (n >= C::NST && !mbar_wait_warp(bar0 + 8u * (C::NST + st), (n / C::NST - 1) & 1u, ctx, SITE_PAGED_EMPTY)) {
@@ -359,6 +362,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
         const float *rs = reinterpret_cast<const float *>(smem + C::OFF_RS);
         float2 *ml = reinterpret_cast<float2 *>(smem + C::OFF_ML);
         float *ob = reinterpret_cast<float *>(smem + C::OFF_O);
+        constexpr int GP = C::GP;
+        // where a lane reads in a group's rows (ldmatrix): K in (entries, 16-byte units) order, V in
+        // (units, entries) order; unit u of a row lies at u ^ its swizzle
+        const int krow = (lane & 7) + ((lane >> 4) << 3), vrow = lane & 15;
+        auto swizzle_of = [](int row) { return C::CB == 128 ? row & 7 : (row >> 1) & 3; };
+        const uint32_t k_lane = (uint32_t)(krow * C::CB), k_unit = (uint32_t)((((lane >> 3) & 1) ^ swizzle_of(krow)) << 4);
+        const uint32_t v_lane = (uint32_t)(vrow * C::CB), v_unit = (uint32_t)(((lane >> 4) ^ swizzle_of(vrow)) << 4);
         const uint32_t q_lane = sbase + C::OFF_Q + (rt * 16 + (lane & 15)) * C::QPITCH + (lane >> 4) * 16;
         uint32_t n = 0;
         bool ok = true;
@@ -428,6 +438,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
             const bool st0 = a.scores && rt * 16 + r0 < nrows, st1 = a.scores && rt * 16 + r0 + 8 < nrows;
             float *sp = a.scores ? a.scores + (((long long)p.b * a.Hkv + h) * a.M + ra) * a.cap : nullptr;
 
+            auto put_scores = [&](int key, float x, float y, float z, float w) {   // of 8 entries, both rows
+                if (st0)
+                    *reinterpret_cast<float2 *>(sp + key + 2 * c4) = make_float2(x, y);
+                if (st1)
+                    *reinterpret_cast<float2 *>(sp + 8ll * a.cap + key + 2 * c4) = make_float2(z, w);
+            };
+
             float o[D / 8][4];
 #pragma unroll
             for (int i = 0; i < D / 8; ++i)
@@ -440,98 +457,103 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
                     ok = false;   // the CTA gives up: no more is computed or written, and its warps still meet
                 const uint32_t groups = ok ? there[st] : 0u;
 #pragma unroll 1
-                for (int j = 0; j < RT; ++j) {
-                    const int g = kw * RT + j, key0 = (p.tile + i) * KT + g * 16;
-                    if (!((groups >> g) & 1u)) {
-                        if (ok && key0 < len) {   // a page out of range: masked
-                            const float2 none = make_float2(-INFINITY, -INFINITY);
-#pragma unroll
-                            for (int t = 0; t < 2; ++t) {
-                                if (st0)
-                                    *reinterpret_cast<float2 *>(sp + key0 + 8 * t + 2 * c4) = none;
-                                if (st1)
-                                    *reinterpret_cast<float2 *>(sp + 8ll * a.cap + key0 + 8 * t + 2 * c4) = none;
-                            }
-                        }
+                for (int j = 0; j < C::GW; j += GP) {
+                    const int g = kw * C::GW + j, key0 = (p.tile + i) * C::KT + g * 16;
+                    const uint32_t have = (groups >> g) & ((1u << GP) - 1u);
+                    if (have == 0) {
+                        if (ok && a.scores)   // pages out of range: masked
+                            for (int t = 0; t < 2 * GP && key0 + 8 * (t & ~1) < len; ++t)
+                                put_scores(key0 + 8 * t, -INFINITY, -INFINITY, -INFINITY, -INFINITY);
                         continue;
                     }
-                    // the group's rows lie in one box: [chunk][row in box][CB bytes], swizzled
-                    const int gb = (g * 16) >> bp_shift, gr = (g * 16) & ((1 << bp_shift) - 1);
-                    const uint32_t base = sbase + st * C::STAGE + (uint32_t)((gb << bp_shift) * C::ROWB + gr * C::CB);
+                    // a group's rows lie in one box: [chunk][row in box][CB bytes], swizzled
                     const uint32_t chunk = (uint32_t)(C::CB << bp_shift);
-                    auto unit_at = [&](uint32_t from, int row, int unit) -> uint32_t {   // 16-byte unit of a row
-                        constexpr int UPC = C::CB / 16;
-                        const int sw = C::CB == 128 ? (row & 7) : ((row >> 1) & 3);
-                        return from + (unit / UPC) * chunk + row * C::CB + (((unit % UPC) ^ sw) << 4);
-                    };
-                    // ---- S = Q K^T: 16 rows x 16 entries, two accumulators for each 8 entries
-                    float s[2][4], s2[2][4];
+                    uint32_t base[GP];
 #pragma unroll
-                    for (int t = 0; t < 2; ++t)
-                        s[t][0] = s[t][1] = s[t][2] = s[t][3] = s2[t][0] = s2[t][1] = s2[t][2] = s2[t][3] = 0.f;
-                    const int krow = (lane & 7) + ((lane >> 4) << 3), kunit = (lane >> 3) & 1;
-                    if constexpr (!FP8) {
+                    for (int u = 0; u < GP; ++u) {
+                        const int at = (g + u) * 16;
+                        base[u] = sbase + st * C::STAGE + (uint32_t)((at >> bp_shift << bp_shift) * C::ROWB +
+                                                                     (at & ((1 << bp_shift) - 1)) * C::CB);
+                    }
+                    // ---- S = Q K^T: 16 rows x 16 entries a group; a single group has two accumulators for
+                    // each 8 entries, so that four products are always under way
+                    float s[4][4];
 #pragma unroll
-                        for (int k = 0; k < KSTEPS; ++k) {
-                            uint32_t kf[4], qa[4];
-                            ldsm4(kf, unit_at(base, krow, 2 * k + kunit));
-                            if constexpr (QREG) {
-                                qa[0] = qf[k][0], qa[1] = qf[k][1], qa[2] = qf[k][2], qa[3] = qf[k][3];
-                            } else {
-                                ldsm4(qa, q_lane + k * 32);
+                    for (int t = 0; t < 4; ++t)
+                        s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+#pragma unroll
+                    for (int k = 0; k < KSTEPS; k += FP8 ? 2 : 1) {
+                        uint32_t qa[4], qb[4];
+                        if constexpr (QREG) {
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                qa[x] = qf[k][x];
+                                qb[x] = qf[FP8 ? k + 1 : k][x];
                             }
-                            mma16816<false>(k & 1 ? s2[0] : s[0], qa, kf[0], kf[1]);
-                            mma16816<false>(k & 1 ? s2[1] : s[1], qa, kf[2], kf[3]);
-                        }
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < KSTEPS; k += 2) {   // a 16-byte unit is 16 features
-                            uint32_t kf[4], qa[4], qb[4];
-                            ldsm4(kf, unit_at(base, krow, k + kunit));
-                            if constexpr (QREG) {
-                                qa[0] = qf[k][0], qa[1] = qf[k][1], qa[2] = qf[k][2], qa[3] = qf[k][3];
-                                qb[0] = qf[k + 1][0], qb[1] = qf[k + 1][1], qb[2] = qf[k + 1][2], qb[3] = qf[k + 1][3];
-                            } else {
-                                ldsm4(qa, q_lane + k * 32);
+                        } else {
+                            ldsm4(qa, q_lane + k * 32);
+                            if constexpr (FP8)
                                 ldsm4(qb, q_lane + k * 32 + 32);
+                        }
+#pragma unroll
+                        for (int u = 0; u < GP; ++u) {
+                            uint32_t kf[4];
+                            if constexpr (!FP8) {   // a 16-byte unit is 8 features
+                                ldsm4(kf, base[u] + k_lane + (k / (C::CB / 32)) * chunk + (k_unit ^ ((k % (C::CB / 32)) << 5)));
+                                const int z = GP == 2 ? 2 * u : (k & 1) * 2;
+                                mma16816<false>(s[z], qa, kf[0], kf[1]);
+                                mma16816<false>(s[z + 1], qa, kf[2], kf[3]);
+                            } else {   // 16 features
+                                ldsm4(kf, base[u] + k_lane + (k / (C::CB / 16)) * chunk + (k_unit ^ ((k % (C::CB / 16)) << 4)));
+                                const int z = GP == 2 ? 2 * u : 2;
+                                mma16816<true>(s[2 * u], qa, e4m3x2_to_f16x2(kf[0]), e4m3x2_to_f16x2(kf[0] >> 16));
+                                mma16816<true>(s[2 * u + 1], qa, e4m3x2_to_f16x2(kf[2]), e4m3x2_to_f16x2(kf[2] >> 16));
+                                mma16816<true>(s[z], qb, e4m3x2_to_f16x2(kf[1]), e4m3x2_to_f16x2(kf[1] >> 16));
+                                mma16816<true>(s[z + 1], qb, e4m3x2_to_f16x2(kf[3]), e4m3x2_to_f16x2(kf[3] >> 16));
                             }
-                            mma16816<true>(s[0], qa, e4m3x2_to_f16x2(kf[0]), e4m3x2_to_f16x2(kf[0] >> 16));
-                            mma16816<true>(s[1], qa, e4m3x2_to_f16x2(kf[2]), e4m3x2_to_f16x2(kf[2] >> 16));
-                            mma16816<true>(s2[0], qb, e4m3x2_to_f16x2(kf[1]), e4m3x2_to_f16x2(kf[1] >> 16));
-                            mma16816<true>(s2[1], qb, e4m3x2_to_f16x2(kf[3]), e4m3x2_to_f16x2(kf[3] >> 16));
+                        }
+                    }
+                    if constexpr (GP == 1) {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            s[0][x] += s[2][x];
+                            s[1][x] += s[3][x];
                         }
                     }
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        s[t][0] = (s[t][0] + s2[t][0]) * sc0;
-                        s[t][1] = (s[t][1] + s2[t][1]) * sc0;
-                        s[t][2] = (s[t][2] + s2[t][2]) * sc1;
-                        s[t][3] = (s[t][3] + s2[t][3]) * sc1;
+                    for (int t = 0; t < 2 * GP; ++t) {
+                        s[t][0] *= sc0;
+                        s[t][1] *= sc0;
+                        s[t][2] *= sc1;
+                        s[t][3] *= sc1;
                     }
-                    if (key0 + 16 > all) {
+                    const bool clear = have == (1u << GP) - 1u && key0 + 16 * GP <= all;
+                    if (!clear) {
 #pragma unroll
-                        for (int t = 0; t < 2; ++t) {
+                        for (int t = 0; t < 2 * GP; ++t) {
+                            const bool in = (have >> (t >> 1)) & 1u;
                             const int key = key0 + 8 * t + 2 * c4;
-                            s[t][0] = key < lim0 ? s[t][0] : -INFINITY;
-                            s[t][1] = key + 1 < lim0 ? s[t][1] : -INFINITY;
-                            s[t][2] = key < lim1 ? s[t][2] : -INFINITY;
-                            s[t][3] = key + 1 < lim1 ? s[t][3] : -INFINITY;
+                            s[t][0] = in && key < lim0 ? s[t][0] : -INFINITY;
+                            s[t][1] = in && key + 1 < lim0 ? s[t][1] : -INFINITY;
+                            s[t][2] = in && key < lim1 ? s[t][2] : -INFINITY;
+                            s[t][3] = in && key + 1 < lim1 ? s[t][3] : -INFINITY;
                         }
                     }
                     if (a.scores) {
 #pragma unroll
-                        for (int t = 0; t < 2; ++t) {
-                            if (st0)
-                                *reinterpret_cast<float2 *>(sp + key0 + 8 * t + 2 * c4) = make_float2(s[t][0], s[t][1]);
-                            if (st1)
-                                *reinterpret_cast<float2 *>(sp + 8ll * a.cap + key0 + 8 * t + 2 * c4) =
-                                    make_float2(s[t][2], s[t][3]);
-                        }
+                        for (int t = 0; t < 2 * GP; ++t)
+                            if (key0 + 8 * (t & ~1) < len)
+                                put_scores(key0 + 8 * t, s[t][0], s[t][1], s[t][2], s[t][3]);
                     }
                     // ---- online softmax
                     constexpr float SH = FP8 ? kPShift : 0.f;
-                    const float n0 = fmaxf(m0, quad_max(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]))) - SH);
-                    const float n1 = fmaxf(m1, quad_max(fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]))) - SH);
+                    float x0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
+                    float x1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+                    if constexpr (GP == 2) {
+                        x0 = fmaxf(x0, fmaxf(fmaxf(s[2][0], s[2][1]), fmaxf(s[3][0], s[3][1])));
+                        x1 = fmaxf(x1, fmaxf(fmaxf(s[2][2], s[2][3]), fmaxf(s[3][2], s[3][3])));
+                    }
+                    const float n0 = fmaxf(m0, quad_max(x0) - SH), n1 = fmaxf(m1, quad_max(x1) - SH);
                     const float b0 = n0 == -INFINITY ? 0.f : n0, b1 = n1 == -INFINITY ? 0.f : n1;
                     if (__any_sync(0xffffffffu, n0 > m0 || n1 > m1)) {
                         const float f0 = ex2_approx(m0 - b0), f1 = ex2_approx(m1 - b1);
@@ -548,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
                         m1 = n1;
                     }
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
+                    for (int t = 0; t < 2 * GP; ++t) {
                         s[t][0] = ex2_approx(s[t][0] - b0);
                         s[t][1] = ex2_approx(s[t][1] - b0);
                         s[t][2] = ex2_approx(s[t][2] - b1);
@@ -556,49 +578,53 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
                         l0 += s[t][0] + s[t][1];
                         l1 += s[t][2] + s[t][3];
                     }
-                    // ---- O += P V; entries behind the length hold anything: their V reads as 0
-                    uint32_t v0 = 0xFFFFFFFFu, v1 = 0xFFFFFFFFu;
-                    if (key0 + 16 > len) {
-                        const int e = len - key0 - 2 * c4;
-                        v0 = (e > 0 ? 0xFFFFu : 0u) | (e > 1 ? 0xFFFF0000u : 0u);
-                        v1 = (e > 8 ? 0xFFFFu : 0u) | (e > 9 ? 0xFFFF0000u : 0u);
-                    }
-                    const uint32_t vbase = base + C::TILE;
-                    const int vrow = (lane & 7) + (((lane >> 3) & 1) << 3), vunit = lane >> 4;
-                    if constexpr (!FP8) {
-                        uint32_t hi[4], lo[4];
+                    // ---- O += P V, group by group; entries behind the length (and groups that are not
+                    // there) hold anything: their V reads as 0
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            const float pa = s[x >> 1][(x & 1) * 2], pb = s[x >> 1][(x & 1) * 2 + 1];
-                            hi[x] = pack_bf16x2(pa, pb);
-                            lo[x] = pack_bf16x2(pa - __uint_as_float(hi[x] << 16), pb - __uint_as_float(hi[x] & 0xFFFF0000u));
+                    for (int u = 0; u < GP; ++u) {
+                        uint32_t v0 = 0xFFFFFFFFu, v1 = 0xFFFFFFFFu;
+                        if (!clear) {
+                            const int e = (have >> u) & 1u ? len - (key0 + 16 * u) - 2 * c4 : 0;
+                            v0 = (e > 0 ? 0xFFFFu : 0u) | (e > 1 ? 0xFFFF0000u : 0u);
+                            v1 = (e > 8 ? 0xFFFFu : 0u) | (e > 9 ? 0xFFFF0000u : 0u);
                         }
+                        const uint32_t vbase = base[u] + C::TILE + v_lane;
+                        const float(&pu)[4] = s[2 * u], (&pw)[4] = s[2 * u + 1];
+                        if constexpr (!FP8) {
+                            uint32_t hi[4], lo[4];
 #pragma unroll
-                        for (int d = 0; d < D / 16; ++d) {
-                            uint32_t vf[4];
-                            ldsm4_t(vf, unit_at(vbase, vrow, 2 * d + vunit));
-                            vf[0] &= v0, vf[1] &= v1, vf[2] &= v0, vf[3] &= v1;
-                            mma16816<false>(o[2 * d], hi, vf[0], vf[1]);
-                            mma16816<false>(o[2 * d + 1], hi, vf[2], vf[3]);
-                            mma16816<false>(o[2 * d], lo, vf[0], vf[1]);
-                            mma16816<false>(o[2 * d + 1], lo, vf[2], vf[3]);
-                        }
-                    } else {
-                        uint32_t pf[4];
+                            for (int x = 0; x < 4; ++x) {
+                                const float pa = x < 2 ? pu[x * 2] : pw[(x - 2) * 2], pb = x < 2 ? pu[x * 2 + 1] : pw[(x - 2) * 2 + 1];
+                                hi[x] = pack_bf16x2(pa, pb);
+                                lo[x] = pack_bf16x2(pa - __uint_as_float(hi[x] << 16), pb - __uint_as_float(hi[x] & 0xFFFF0000u));
+                            }
 #pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            pf[x] = pack_f16x2(s[x >> 1][(x & 1) * 2], s[x >> 1][(x & 1) * 2 + 1]);
+                            for (int d = 0; d < D / 16; ++d) {
+                                uint32_t vf[4];
+                                ldsm4_t(vf, vbase + (d / (C::CB / 32)) * chunk + (v_unit ^ ((d % (C::CB / 32)) << 5)));
+                                vf[0] &= v0, vf[1] &= v1, vf[2] &= v0, vf[3] &= v1;
+                                mma16816<false>(o[2 * d], hi, vf[0], vf[1]);
+                                mma16816<false>(o[2 * d + 1], hi, vf[2], vf[3]);
+                                mma16816<false>(o[2 * d], lo, vf[0], vf[1]);
+                                mma16816<false>(o[2 * d + 1], lo, vf[2], vf[3]);
+                            }
+                        } else {
+                            uint32_t pf[4];
 #pragma unroll
-                        for (int d = 0; d < D / 32; ++d) {   // two 16-byte units: 32 features
-                            uint32_t vf[4];
-                            ldsm4_t(vf, unit_at(vbase, vrow, 2 * d + vunit));
-                            vf[0] &= v0, vf[1] &= v1, vf[2] &= v0, vf[3] &= v1;
+                            for (int x = 0; x < 4; ++x)
+                                pf[x] = x < 2 ? pack_f16x2(pu[x * 2], pu[x * 2 + 1]) : pack_f16x2(pw[(x - 2) * 2], pw[(x - 2) * 2 + 1]);
 #pragma unroll
-                            for (int u = 0; u < 2; ++u) {
-                                // a register holds features (f, f + 1) of entries 2 c and 2 c + 1: pair the entries
-                                const uint32_t x = __byte_perm(vf[2 * u], 0, 0x3120), y = __byte_perm(vf[2 * u + 1], 0, 0x3120);
-                                mma16816<true>(o[4 * d + 2 * u], pf, e4m3x2_to_f16x2(x), e4m3x2_to_f16x2(y));
-                                mma16816<true>(o[4 * d + 2 * u + 1], pf, e4m3x2_to_f16x2(x >> 16), e4m3x2_to_f16x2(y >> 16));
+                            for (int d = 0; d < D / 32; ++d) {   // two 16-byte units: 32 features
+                                uint32_t vf[4];
+                                ldsm4_t(vf, vbase + (d / (C::CB / 32)) * chunk + (v_unit ^ ((d % (C::CB / 32)) << 5)));
+                                vf[0] &= v0, vf[1] &= v1, vf[2] &= v0, vf[3] &= v1;
+#pragma unroll
+                                for (int w = 0; w < 2; ++w) {
+                                    // a register holds features (f, f + 1) of entries 2 c and 2 c + 1: pair the entries
+                                    const uint32_t x = __byte_perm(vf[2 * w], 0, 0x3120), y = __byte_perm(vf[2 * w + 1], 0, 0x3120);
+                                    mma16816<true>(o[4 * d + 2 * w], pf, e4m3x2_to_f16x2(x), e4m3x2_to_f16x2(y));
+                                    mma16816<true>(o[4 * d + 2 * w + 1], pf, e4m3x2_to_f16x2(x >> 16), e4m3x2_to_f16x2(y >> 16));
+                                }
                             }
                         }
                     }
@@ -798,7 +824,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
         return;
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int rb = 0; rb < a.RB; ++rb) {
-        const Parts p = parts_of(a, b, rb * a.Hkv + h, (len + KT - 1) / KT);
+        const Parts p = parts_of(a, b, rb * a.Hkv + h, (len + a.kt - 1) / a.kt);
         const int row0 = rb * a.rows, nrows = min(a.rows, a.M - row0);
         for (int r = tid; r < nrows; r += kJoinThreads) {
             float y;
@@ -893,11 +919,12 @@ int paged_run(const fa_kv_cache &c, PagedArgs &a, cudaStream_t s)
 {
     const bool f8 = c.dtype == FA_E4M3;
     const int rt = row_tiles(a.M);
-    const long long most = (long long)a.B * a.Hkv * a.RB * ((a.cap + KT - 1) / KT);   // tiles, at most
+    a.kt = f8 ? Cfg<D, true, 1>::KT : Cfg<D, false, 1>::KT;
+    const long long most = (long long)a.B * a.Hkv * a.RB * ((a.cap + a.kt - 1) / a.kt);   // tiles, at most
     int st = OK;
     if (most > 0) {
         CUtensorMap tk, tv;
-        const int box = c.page_size < KT ? c.page_size : KT;
+        const int box = c.page_size < 64 ? c.page_size : 64;
         if ((st = encode_pool(&tk, c.k, c, box)) != OK || (st = encode_pool(&tv, c.v, c, box)) != OK)
             return st;
         const long long units = (long long)a.B * a.Hkv * a.RB;
