@@ -51,7 +51,7 @@ struct Cfg {
     static constexpr int ELEM = FP8 ? 1 : 2;
     static constexpr int ROWB = D * ELEM;                          // bytes of an entry's K or V row
     static constexpr int CB = ROWB < 128 ? ROWB : 128;             // bytes of a column chunk
-    static constexpr int KT = ROWB <= 64 ? 256 : ROWB <= 128 ? 128 : 64;   // entries a tile: about 32 KB of K and V
+    static constexpr int KT = ROWB <= 128 ? 128 : 64;              // entries a tile
     static constexpr int TILE = KT * ROWB;                         // K or V of a tile
     static constexpr int STAGE = 2 * TILE;
     static constexpr int GW = KT / 16 * RT / kMathWarps;           // groups of 16 entries a warp has of a tile
@@ -61,9 +61,10 @@ struct Cfg {
     static constexpr int OPITCH = OC + 4;                          // floats of a merge row
     static constexpr int NQ = RT * 16 * QPITCH, NO = kMathWarps * 16 * OPITCH * 4, NML = kMathWarps * 16 * 8;
     static constexpr int SMALL = 1024 + NQ + NO + NML + RT * 16 * 4 + 24 * 12 + 64;
-    // two CTAs an SM where the accumulators leave registers for it; the ring takes what is left
-    static constexpr int CTAS = D == 256 ? 1 : 2;
-    static constexpr int FIT = ((CTAS == 2 ? 113 : 227) * 1024 - SMALL) / STAGE;
+    // as many CTAs an SM as the accumulators leave registers for and the ring has room; the
+    // ring takes what is left
+    static constexpr int CTAS = D == 256 ? 1 : FP8 && D == 64 && RT == 1 ? 3 : 2;
+    static constexpr int FIT = ((CTAS == 3 ? 75 : CTAS == 2 ? 113 : 227) * 1024 - SMALL) / STAGE;
     static constexpr int NST = FIT < 12 ? FIT : 12;
     static_assert(NST >= 2, "shared memory");
     static constexpr int OFF_Q = NST * STAGE;
@@ -139,6 +140,10 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map
         " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
         : "memory");
+}
+__device__ __forceinline__ void st_shared_zero16(uint32_t addr)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0) : "memory");
 }
 __device__ __forceinline__ void math_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kMathWarps) : "memory"); }
 __device__ __forceinline__ float quad_max(float x)
@@ -449,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
 #pragma unroll
             for (int i = 0; i < D / 8; ++i)
                 o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-            float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+            float m0 = -INFINITY, m1 = -INFINITY, l0[2] = {0.f, 0.f}, l1[2] = {0.f, 0.f};
 
             for (int i = 0; i < cnt; ++i, ++n) {
                 const uint32_t st = n % C::NST;
@@ -520,13 +525,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
                             s[1][x] += s[3][x];
                         }
                     }
-#pragma unroll
-                    for (int t = 0; t < 2 * GP; ++t) {
-                        s[t][0] *= sc0;
-                        s[t][1] *= sc0;
-                        s[t][2] *= sc1;
-                        s[t][3] *= sc1;
-                    }
                     const bool clear = have == (1u << GP) - 1u && key0 + 16 * GP <= all;
                     if (!clear) {
 #pragma unroll
@@ -543,22 +541,22 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
 #pragma unroll
                         for (int t = 0; t < 2 * GP; ++t)
                             if (key0 + 8 * (t & ~1) < len)
-                                put_scores(key0 + 8 * t, s[t][0], s[t][1], s[t][2], s[t][3]);
+                                put_scores(key0 + 8 * t, s[t][0] * sc0, s[t][1] * sc0, s[t][2] * sc1, s[t][3] * sc1);
                     }
                     // ---- online softmax
                     constexpr float SH = FP8 ? kPShift : 0.f;
-                    float x0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
-                    float x1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+                    float x0 = fmaxf(fmax3(s[0][0], s[0][1], s[1][0]), s[1][1]);
+                    float x1 = fmaxf(fmax3(s[0][2], s[0][3], s[1][2]), s[1][3]);
                     if constexpr (GP == 2) {
-                        x0 = fmaxf(x0, fmaxf(fmaxf(s[2][0], s[2][1]), fmaxf(s[3][0], s[3][1])));
-                        x1 = fmaxf(x1, fmaxf(fmaxf(s[2][2], s[2][3]), fmaxf(s[3][2], s[3][3])));
+                        x0 = fmax3(fmax3(x0, s[2][0], s[2][1]), s[3][0], s[3][1]);
+                        x1 = fmax3(fmax3(x1, s[2][2], s[2][3]), s[3][2], s[3][3]);
                     }
-                    const float n0 = fmaxf(m0, quad_max(x0) - SH), n1 = fmaxf(m1, quad_max(x1) - SH);
+                    const float n0 = fmaxf(m0, quad_max(x0) * sc0 - SH), n1 = fmaxf(m1, quad_max(x1) * sc1 - SH);
                     const float b0 = n0 == -INFINITY ? 0.f : n0, b1 = n1 == -INFINITY ? 0.f : n1;
                     if (__any_sync(0xffffffffu, n0 > m0 || n1 > m1)) {
                         const float f0 = ex2_approx(m0 - b0), f1 = ex2_approx(m1 - b1);
-                        l0 *= f0;
-                        l1 *= f1;
+                        l0[0] *= f0, l0[1] *= f0;
+                        l1[0] *= f1, l1[1] *= f1;
 #pragma unroll
                         for (int d = 0; d < D / 8; ++d) {
                             o[d][0] *= f0;
@@ -571,23 +569,31 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
                     }
 #pragma unroll
                     for (int t = 0; t < 2 * GP; ++t) {
-                        s[t][0] = ex2_approx(s[t][0] - b0);
-                        s[t][1] = ex2_approx(s[t][1] - b0);
-                        s[t][2] = ex2_approx(s[t][2] - b1);
-                        s[t][3] = ex2_approx(s[t][3] - b1);
-                        l0 += s[t][0] + s[t][1];
-                        l1 += s[t][2] + s[t][3];
+                        ffma2(s[t][0], s[t][1], s[t][0], s[t][1], sc0, sc0, -b0, -b0);
+                        ffma2(s[t][2], s[t][3], s[t][2], s[t][3], sc1, sc1, -b1, -b1);
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            s[t][x] = ex2_approx(s[t][x]);
+                        fadd2(l0[0], l0[1], l0[0], l0[1], s[t][0], s[t][1]);
+                        fadd2(l1[0], l1[1], l1[0], l1[1], s[t][2], s[t][3]);
                     }
-                    // ---- O += P V, group by group; entries behind the length (and groups that are not
-                    // there) hold anything: their V reads as 0
+                    // ---- O += P V, group by group.  Entries behind the length (and groups that are not
+                    // there) hold anything, and 0 times a NaN is one: their V rows become 0 first
+                    if (!clear) {
+#pragma unroll
+                        for (int u = 0; u < GP; ++u) {
+                            const int first = (have >> u) & 1u ? len - (key0 + 16 * u) : 0, row = lane & 15;
+                            if (row >= first)
+                                for (int x = lane >> 4; x < C::ROWB / 16; x += 2)
+                                    st_shared_zero16(base[u] + C::TILE + row * C::CB + (x / (C::CB / 16)) * chunk +
+                                                     (x % (C::CB / 16)) * 16);
+                        }
+                        // written through the generic proxy, and next by TMA
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                    }
 #pragma unroll
                     for (int u = 0; u < GP; ++u) {
-                        uint32_t v0 = 0xFFFFFFFFu, v1 = 0xFFFFFFFFu;
-                        if (!clear) {
-                            const int e = (have >> u) & 1u ? len - (key0 + 16 * u) - 2 * c4 : 0;
-                            v0 = (e > 0 ? 0xFFFFu : 0u) | (e > 1 ? 0xFFFF0000u : 0u);
-                            v1 = (e > 8 ? 0xFFFFu : 0u) | (e > 9 ? 0xFFFF0000u : 0u);
-                        }
                         const uint32_t vbase = base[u] + C::TILE + v_lane;
                         const float(&pu)[4] = s[2 * u], (&pw)[4] = s[2 * u + 1];
                         if constexpr (!FP8) {
@@ -602,7 +608,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
                             for (int d = 0; d < D / 16; ++d) {
                                 uint32_t vf[4];
                                 ldsm4_t(vf, vbase + (d / (C::CB / 32)) * chunk + (v_unit ^ ((d % (C::CB / 32)) << 5)));
-                                vf[0] &= v0, vf[1] &= v1, vf[2] &= v0, vf[3] &= v1;
                                 mma16816<false>(o[2 * d], hi, vf[0], vf[1]);
                                 mma16816<false>(o[2 * d + 1], hi, vf[2], vf[3]);
                                 mma16816<false>(o[2 * d], lo, vf[0], vf[1]);
@@ -617,7 +622,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
                             for (int d = 0; d < D / 32; ++d) {   // two 16-byte units: 32 features
                                 uint32_t vf[4];
                                 ldsm4_t(vf, vbase + (d / (C::CB / 32)) * chunk + (v_unit ^ ((d % (C::CB / 32)) << 5)));
-                                vf[0] &= v0, vf[1] &= v1, vf[2] &= v0, vf[3] &= v1;
 #pragma unroll
                                 for (int w = 0; w < 2; ++w) {
                                     // a register holds features (f, f + 1) of entries 2 c and 2 c + 1: pair the entries
@@ -635,11 +639,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
             }
 
             // ---- the warps' states of each row tile together, then out, 32 features at a time
-            l0 = quad_sum(l0);
-            l1 = quad_sum(l1);
+            const float s0 = quad_sum(l0[0] + l0[1]), s1 = quad_sum(l1[0] + l1[1]);
             if (c4 == 0) {
-                ml[warp * 16 + r0] = make_float2(m0, l0);
-                ml[warp * 16 + r0 + 8] = make_float2(m1, l1);
+                ml[warp * 16 + r0] = make_float2(m0, s0);
+                ml[warp * 16 + r0 + 8] = make_float2(m1, s1);
             }
             math_sync();
             auto top = [&](int rt_, int r) {   // largest of a row's maxima
@@ -744,7 +747,7 @@ __device__ __forceinline__ Parts parts_of(const PagedArgs &a, int b, int ul, int
 // The states of a row are read by D / 2 threads a state, two features each, so that several are
 // under way at once.
 constexpr int kJoinThreads = 128, kWeightRun = 4 * kJoinThreads;
-constexpr int kMaxParts = 2 * kSMs;
+constexpr int kMaxCtas = 3 * kSMs, kMaxParts = kMaxCtas;
 
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedArgs a, int wchunks)
@@ -882,13 +885,13 @@ size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 int rows_of(int M) { return M < kMaxRows ? M : kMaxRows; }
 int row_tiles(int M) { return M <= 16 ? 1 : M <= 32 ? 2 : 4; }
-int grid_of(int d) { return kSMs * (d == 256 ? 1 : 2); }
+
 
 // Tables of up to this many slots: one CTA a unit and no join.
 constexpr int kWholeSlots = 512;
 
 size_t where_bytes(int B) { return round256((size_t)(B + 1) * sizeof(long long)); }
-size_t part_bytes(int M, int d) { return round256((size_t)2 * grid_of(d) * rows_of(M) * (d + 2) * sizeof(float)); }
+size_t part_bytes(int M, int d) { return round256((size_t)2 * kMaxCtas * rows_of(M) * (d + 2) * sizeof(float)); }
 
 // K or V pool as [page, KV head][column chunk][row][CB bytes]; a box is all chunks of a page's
 // rows (64 at most).
@@ -920,6 +923,7 @@ int paged_run(const fa_kv_cache &c, PagedArgs &a, cudaStream_t s)
     const bool f8 = c.dtype == FA_E4M3;
     const int rt = row_tiles(a.M);
     a.kt = f8 ? Cfg<D, true, 1>::KT : Cfg<D, false, 1>::KT;
+    a.grid = kSMs * (rt == 1 ? (f8 ? Cfg<D, true, 1>::CTAS : Cfg<D, false, 1>::CTAS) : f8 ? Cfg<D, true, 2>::CTAS : Cfg<D, false, 2>::CTAS);
     const long long most = (long long)a.B * a.Hkv * a.RB * ((a.cap + a.kt - 1) / a.kt);   // tiles, at most
     int st = OK;
     if (most > 0) {
@@ -995,7 +999,6 @@ int paged_launch(const fa_kv_cache &c, const void *q, void *o, float *lse, int H
     while ((1 << a.ps_shift) < c.page_size)
         ++a.ps_shift;
     a.cap = c.num_pages > 0 ? c.max_pages * c.page_size : 0;   // no pages: every length above 0 is out of range
-    a.grid = grid_of(c.d);
     a.whole = !accumulate && a.cap <= kWholeSlots;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     a.where = reinterpret_cast<long long *>(ws);
