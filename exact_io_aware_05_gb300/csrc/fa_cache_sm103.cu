@@ -57,22 +57,36 @@ __device__ __forceinline__ void phase_sincos(unsigned long long turns, int pos, 
     cs = ((quad + 1) & 2) ? -b : b;
 }
 
-// 8 consecutive elements as fp32, from and to memory.
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&x)[8])
-{
-    const uint4 w = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+// 8 consecutive elements as they lie in memory, and as fp32.
+template <typename E>
+struct Raw8;
+template <>
+struct Raw8<__nv_bfloat16> {
+    uint4 w;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { w = *reinterpret_cast<const uint4 *>(p); }
+    __device__ __forceinline__ void get(float (&x)[8]) const
+    {
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(u[i] << 16);
-        x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(u[i] << 16);
+            x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+        }
     }
-}
-__device__ __forceinline__ void load8(const float *p, float (&x)[8])
-{
-    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
+};
+template <>
+struct Raw8<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float *p)
+    {
+        a = reinterpret_cast<const float4 *>(p)[0];
+        b = reinterpret_cast<const float4 *>(p)[1];
+    }
+    __device__ __forceinline__ void get(float (&x)[8]) const
+    {
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    }
+};
 __device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&x)[8])
 {
     *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
@@ -137,12 +151,15 @@ struct RopeArgs {
 };
 
 constexpr int kRopeThreads = 256;
+constexpr int kHeadsAhead = 4;    // heads whose loads a thread has in flight
 
 template <typename E, int D, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeTable tab,
                                                             const __grid_constant__ RopeArgs a)
 {
     constexpr int TPR = D / 16;                          // threads a row
+    pdl_launch();
+    pdl_wait();
     const int v = threadIdx.x % TPR;
     const long long tok = (long long)blockIdx.x * (kRopeThreads / TPR) + threadIdx.x / TPR;
     if (tok >= a.n)
@@ -159,19 +176,33 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
         }
     }
     const int h0 = blockIdx.y * a.heads_per_cta, h1 = min(a.H, h0 + a.heads_per_cta);
-    for (int h = h0; h < h1; ++h) {
-        const int w = h >= a.H0;
-        const Row3 &xi = a.x[w], &yi = a.y[w];
-        const int hh = h - (w ? a.H0 : 0);
-        const E *x = static_cast<const E *>(xi.p) + b * xi.sb + hh * xi.sh + t * xi.st;
-        E *y = static_cast<E *>(yi.p) + b * yi.sb + hh * yi.sh + t * yi.st;
-        float p[8], q[8];
-        load8(x + sl.e0, p);
-        load8(x + sl.e1, q);
-        if (sl.pair >= 0)
-            turn<INTER>(p, q, sn, cs);
-        store8(y + sl.e0, p);
-        store8(y + sl.e1, q);
+    for (int hb = h0; hb < h1; hb += kHeadsAhead) {
+        Raw8<E> p[kHeadsAhead], q[kHeadsAhead];
+#pragma unroll
+        for (int u = 0; u < kHeadsAhead; ++u) {
+            const int h = hb + u, w = h >= a.H0;
+            if (h < h1) {
+                const Row3 &xi = a.x[w];
+                const E *x = static_cast<const E *>(xi.p) + b * xi.sb + (h - (w ? a.H0 : 0)) * xi.sh + t * xi.st;
+                p[u].load(x + sl.e0);
+                q[u].load(x + sl.e1);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kHeadsAhead; ++u) {
+            const int h = hb + u, w = h >= a.H0;
+            if (h < h1) {
+                const Row3 &yi = a.y[w];
+                E *y = static_cast<E *>(yi.p) + b * yi.sb + (h - (w ? a.H0 : 0)) * yi.sh + t * yi.st;
+                float f[8], g[8];
+                p[u].get(f);
+                q[u].get(g);
+                if (sl.pair >= 0)
+                    turn<INTER>(f, g, sn, cs);
+                store8(y + sl.e0, f);
+                store8(y + sl.e1, g);
+            }
+        }
     }
 }
 
@@ -201,11 +232,7 @@ int rope_run(const RopeTable &t, const RopeArgs &a, int interleaved, cudaStream_
 {
     constexpr int TOK = kRopeThreads / (D / 16);
     const dim3 grid((unsigned)((a.n + TOK - 1) / TOK), (unsigned)((a.H + a.heads_per_cta - 1) / a.heads_per_cta));
-    if (interleaved)
-        rope_kernel<E, D, true><<<grid, kRopeThreads, 0, s>>>(t, a);
-    else
-        rope_kernel<E, D, false><<<grid, kRopeThreads, 0, s>>>(t, a);
-    return cudaGetLastError() == cudaSuccess ? OK : ERR_CUDA;
+    return launch_overlapped(interleaved ? rope_kernel<E, D, true> : rope_kernel<E, D, false>, grid, kRopeThreads, 0, 0, true, s, t, a);
 }
 
 template <typename E>
@@ -248,6 +275,8 @@ __global__ void __launch_bounds__(kRopeThreads) append_kernel(const __grid_const
                                                               const __grid_constant__ AppendArgs a)
 {
     constexpr int TPR = D / 16;
+    pdl_launch();
+    pdl_wait();
     const int vec = threadIdx.x % TPR;
     const long long n = (long long)a.B * a.T;
     const long long tok = (long long)blockIdx.x * (kRopeThreads / TPR) + threadIdx.x / TPR;
@@ -281,36 +310,48 @@ __global__ void __launch_bounds__(kRopeThreads) append_kernel(const __grid_const
             atomicCAS(&g_cache_status, 0, kStatusBadIndex);
     }
     const int row = slot & ((1 << a.ps_shift) - 1);
-    for (int h = h0; h < h1; ++h) {
-        float x[8], y[8];
-        if (h < a.Hq) {
-            const __nv_bfloat16 *p = static_cast<const __nv_bfloat16 *>(a.q.p) + b * a.q.sb + h * a.q.sh + t * a.q.st;
-            __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.qo.p) + b * a.qo.sb + h * a.qo.sh + t * a.qo.st;
-            load8(p + sl.e0, x);
-            load8(p + sl.e1, y);
-            if (sl.pair >= 0)
+    using E = __nv_bfloat16;
+    for (int hb = h0; hb < h1; hb += kHeadsAhead) {
+        Raw8<E> p[kHeadsAhead], q[kHeadsAhead];
+#pragma unroll
+        for (int u = 0; u < kHeadsAhead; ++u) {
+            const int h = hb + u, hk = h - a.Hq;
+            if (h < h1) {
+                const Row3 &r = hk < 0 ? a.q : hk < a.Hkv ? a.k : a.v;
+                const int in = hk < 0 ? h : hk < a.Hkv ? hk : hk - a.Hkv;
+                const E *x = static_cast<const E *>(r.p) + b * r.sb + in * r.sh + t * r.st;
+                p[u].load(x + sl.e0);
+                q[u].load(x + sl.e1);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kHeadsAhead; ++u) {
+            const int h = hb + u;
+            if (h >= h1)
+                break;
+            float x[8], y[8];
+            p[u].get(x);
+            q[u].get(y);
+            if (h < a.Hq + a.Hkv && sl.pair >= 0)
                 turn<INTER>(x, y, sn, cs);
-            store8(o + sl.e0, x);
-            store8(o + sl.e1, y);
-        } else if (page_ok) {
-            const bool isv = h >= a.Hq + a.Hkv;
-            const int hk = h - a.Hq - (isv ? a.Hkv : 0);
-            const Row3 &r = isv ? a.v : a.k;
-            const __nv_bfloat16 *p = static_cast<const __nv_bfloat16 *>(r.p) + b * r.sb + hk * r.sh + t * r.st;
-            load8(p + sl.e0, x);
-            load8(p + sl.e1, y);
-            if (!isv && sl.pair >= 0)
-                turn<INTER>(x, y, sn, cs);
-            const long long at = ((((long long)page * a.Hkv + hk) << a.ps_shift) + row) * D;
-            const float scale = FP8 ? (isv ? a.vs : a.ks)[hk] : 1.f;
-            put8<FP8>(isv ? a.vp : a.kp, at + sl.e0, x, scale);
-            put8<FP8>(isv ? a.vp : a.kp, at + sl.e1, y, scale);
-            if (!isv && vec == 0) {
-                const long long w = ((long long)b * a.Hkv + hk) * cap + slot;
-                if (a.weight)
-                    a.weight[w] = 0.f;
-                if (a.order)
-                    a.order[w] = (a.seen ? a.seen[b] - nb : len - nb) + t;
+            if (h < a.Hq) {
+                E *o = static_cast<E *>(a.qo.p) + b * a.qo.sb + h * a.qo.sh + t * a.qo.st;
+                store8(o + sl.e0, x);
+                store8(o + sl.e1, y);
+            } else if (page_ok) {
+                const bool isv = h >= a.Hq + a.Hkv;
+                const int hk = h - a.Hq - (isv ? a.Hkv : 0);
+                const long long at = ((((long long)page * a.Hkv + hk) << a.ps_shift) + row) * D;
+                const float scale = FP8 ? (isv ? a.vs : a.ks)[hk] : 1.f;
+                put8<FP8>(isv ? a.vp : a.kp, at + sl.e0, x, scale);
+                put8<FP8>(isv ? a.vp : a.kp, at + sl.e1, y, scale);
+                if (!isv && vec == 0) {
+                    const long long w = ((long long)b * a.Hkv + hk) * cap + slot;
+                    if (a.weight)
+                        a.weight[w] = 0.f;
+                    if (a.order)
+                        a.order[w] = (a.seen ? a.seen[b] - nb : len - nb) + t;
+                }
             }
         }
     }
@@ -323,11 +364,7 @@ int append_run(const RopeTable &t, const AppendArgs &a, int interleaved, cudaStr
     const long long n = (long long)a.B * a.T;
     const int H = a.Hq + 2 * a.Hkv;
     const dim3 grid((unsigned)((n + TOK - 1) / TOK), (unsigned)((H + a.heads_per_cta - 1) / a.heads_per_cta));
-    if (interleaved)
-        append_kernel<D, true, FP8><<<grid, kRopeThreads, 0, s>>>(t, a);
-    else
-        append_kernel<D, false, FP8><<<grid, kRopeThreads, 0, s>>>(t, a);
-    return cudaGetLastError() == cudaSuccess ? OK : ERR_CUDA;
+    return launch_overlapped(interleaved ? append_kernel<D, true, FP8> : append_kernel<D, false, FP8>, grid, kRopeThreads, 0, 0, true, s, t, a);
 }
 
 // ------------------------------------------------------------------ evict
@@ -431,7 +468,10 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
     int *copies = sel_smem, *hist = copies + kSelCopies * kSelBins, *scratch = hist + kSelPasses * kSelBins, *share = scratch + 32, *pick = share + 32;
     uint32_t *keys = reinterpret_cast<uint32_t *>(pick + 8);
     const int rank = (int)blockIdx.x % cs, unit = (int)blockIdx.x / cs, b = unit / a.Hkv, tid = threadIdx.x;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    pdl_launch();
+    for (int i = tid; i < (kSelCopies + kSelPasses) * kSelBins; i += kSelThreads)
+        copies[i] = 0;
+    pdl_wait();
     const int len = a.lens[b];
     int *kept = a.kept + (long long)unit * a.budget;
     const long long base = (long long)unit * a.cap;
@@ -454,8 +494,6 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
         }
         return;
     }
-    for (int i = tid; i < (kSelCopies + kSelPasses) * kSelBins; i += kSelThreads)
-        copies[i] = 0;
     const int per = (len + cs - 1) / cs, lo = min(len, rank * per), n = min(len, lo + per) - lo;
     const int recent = (a.seen ? a.seen[b] : len) - a.n_recent;
     const bool ages = order && (a.n_first > 0 || a.n_recent > 0);
@@ -603,6 +641,8 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_long_kernel(const __
 {
     __shared__ int hist[256], scratch[32], pick[2];
     const int unit = blockIdx.x, b = unit / a.Hkv, tid = threadIdx.x;
+    pdl_launch();
+    pdl_wait();
     const int len = a.lens[b];
     int *kept = a.kept + (long long)unit * a.budget;
     const long long base = (long long)unit * a.cap;
@@ -721,7 +761,8 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const __grid_constant__
     __shared__ long long list[8][32][2];
     const int unit = blockIdx.x, b = unit / a.Hkv, h = unit - b * a.Hkv, lane = threadIdx.x & 31;
     long long(*moves)[2] = list[threadIdx.x >> 5];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    pdl_launch();
+    pdl_wait();
     if (blockIdx.y == 0 && h == 0 && threadIdx.x == 0) {
         const int len = a.lens[b];
         a.lens_out[b] = min(len, a.budget);
@@ -892,37 +933,20 @@ int evict_launch(const fa_kv_cache &c, int budget, int n_first, int n_recent, fl
     while (cs < 8 && (a.cap + cs - 1) / cs > kSelItems * kSelThreads)
         cs *= 2;
     const int per = (a.cap + cs - 1) / cs;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute at;
-    cfg.stream = s;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
+    int st;
     if (per <= kSelItems * kSelThreads && (long long)units * cs <= INT_MAX) {
-        const int smem = kSelFixed + per * 4;
         if (cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  kSelFixed + kSelItems * kSelThreads * 4) != cudaSuccess)
             return ERR_CUDA;
-        cfg.gridDim = dim3((unsigned)(units * cs));
-        cfg.blockDim = dim3(kSelThreads);
-        cfg.dynamicSmemBytes = smem;
-        at.id = cudaLaunchAttributeClusterDimension;
-        at.val.clusterDim.x = cs;
-        at.val.clusterDim.y = at.val.clusterDim.z = 1;
-        if (cudaLaunchKernelEx(&cfg, evict_select_kernel, a, cs) != cudaSuccess)
-            return ERR_CUDA;
+        st = launch_overlapped(evict_select_kernel, dim3((unsigned)(units * cs)), kSelThreads, kSelFixed + per * 4, cs,
+                               false, s, a, cs);
     } else {
-        evict_select_long_kernel<<<units, kSelThreads, 0, s>>>(a);
-        if (cudaGetLastError() != cudaSuccess)
-            return ERR_CUDA;
+        st = launch_overlapped(evict_select_long_kernel, dim3((unsigned)units), kSelThreads, 0, 0, false, s, a);
     }
-    // launched while the selection runs, waits for it inside
+    if (st != OK)
+        return st;
     const int blocks = (budget + 255) / 256;
-    cfg.gridDim = dim3(units, blocks < 64 ? blocks : 64);
-    cfg.blockDim = dim3(256);
-    cfg.dynamicSmemBytes = 0;
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    return cudaLaunchKernelEx(&cfg, evict_move_kernel, a) == cudaSuccess ? OK : ERR_CUDA;
+    return launch_overlapped(evict_move_kernel, dim3((unsigned)units, blocks < 64 ? blocks : 64), 256, 0, 0, true, s, a);
 }
 
 int cache_status_fetch_clear(cudaStream_t s, int *host_word)

@@ -274,8 +274,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_MISC);
     const int lane = (int)lane_id(), warp = (int)warp_id();
     const WaitCtx ctx{abort_flag, &g_paged_status, a.timeout_ns};
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
+    pdl_launch();
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::NST; ++s) {
             mbar_init(bar0 + 8u * s, 1);
@@ -283,7 +282,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
         }
         *abort_flag = 0;
         fence_mbar_init();
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
     }
+    pdl_wait();
     Place p;
     long long share = 0, t0 = 0, mine_all;   // mine_all: tiles of this CTA
     if (a.whole) {                           // one unit a CTA, however long
@@ -314,8 +316,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
         const int box = lane >> 1;
         const uint32_t dst = (uint32_t)((lane & 1) * C::TILE + (box << bp_shift) * C::ROWB);
         const uint32_t box_bytes = (uint32_t)(C::ROWB << bp_shift);
-        if (lane < 2)
-            tma_prefetch_desc(map);
         uint32_t n = 0;
         bool ok = true;
         while (ok && p.left > 0) {
@@ -756,7 +756,8 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
     const int tid = threadIdx.x, per = a.Hkv * a.RB;
     const long long rows_total = (long long)a.B * per * a.rows, blk = blockIdx.x;
     const long long stride = (long long)a.rows * (D + 2);
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    pdl_launch();
+    pdl_wait();
     if (blk < rows_total) {
         const int row = (int)(blk % a.rows);
         const long long unit = blk / a.rows;
@@ -913,8 +914,7 @@ int launch_main(const CUtensorMap &tk, const CUtensorMap &tv, const PagedArgs &a
     using C = Cfg<D, FP8, RT>;
     if (cudaFuncSetAttribute(paged_kernel<D, FP8, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
         return ERR_CUDA;
-    paged_kernel<D, FP8, RT><<<grid, kThreads, C::SMEM, s>>>(tk, tv, a);
-    return cudaGetLastError() == cudaSuccess ? OK : ERR_CUDA;
+    return launch_overlapped(paged_kernel<D, FP8, RT>, dim3((unsigned)grid), kThreads, C::SMEM, 0, true, s, tk, tv, a);
 }
 
 template <int D>
@@ -952,17 +952,7 @@ int paged_run(const fa_kv_cache &c, PagedArgs &a, cudaStream_t s)
     const long long blocks = (long long)a.B * a.Hkv * a.RB * a.rows + (long long)a.B * a.Hkv * wchunks;
     if (blocks > INT_MAX)
         return ERR_UNSUPPORTED;
-    // launched while the first kernel runs, waits for it inside
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)blocks);
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = s;
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, paged_join_kernel<D>, a, wchunks) == cudaSuccess ? OK : ERR_CUDA;
+    return launch_overlapped(paged_join_kernel<D>, dim3((unsigned)blocks), kJoinThreads, 0, 0, true, s, a, wchunks);
 }
 
 }  // namespace
