@@ -118,25 +118,29 @@ __device__ __forceinline__ Slice slice_of(int v, int rot, int interleaved)
     return s;
 }
 
-// Turns the pairs held in (a, b): pair j is (a[j], b[j]), or, interleaved, two neighbours.
+// Turns the pairs held in (a, b): pair j is (a[j], b[j]), or, interleaved, two neighbours.  Two
+// pairs an instruction.
 template <bool INTER>
 __device__ __forceinline__ void turn(float (&a)[8], float (&b)[8], const float (&sn)[8], const float (&cs)[8])
 {
+    auto two = [&](float &x0, float &x1, float &y0, float &y1, int j) {
+        float u0, u1, w0, w1;
+        fmul2(u0, u1, x0, x1, cs[j], cs[j + 1]);
+        fmul2(w0, w1, y0, y1, cs[j], cs[j + 1]);
+        ffma2(w0, w1, x0, x1, sn[j], sn[j + 1], w0, w1);
+        ffma2(x0, x1, y0, y1, -sn[j], -sn[j + 1], u0, u1);
+        y0 = w0;
+        y1 = w1;
+    };
     if constexpr (!INTER) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float x = a[j], y = b[j];
-            a[j] = fmaf(-y, sn[j], x * cs[j]);
-            b[j] = fmaf(x, sn[j], y * cs[j]);
-        }
+        for (int j = 0; j < 8; j += 2)
+            two(a[j], a[j + 1], b[j], b[j + 1], j);
     } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float x = a[2 * j], y = a[2 * j + 1], u = b[2 * j], w = b[2 * j + 1];
-            a[2 * j] = fmaf(-y, sn[j], x * cs[j]);
-            a[2 * j + 1] = fmaf(x, sn[j], y * cs[j]);
-            b[2 * j] = fmaf(-w, sn[4 + j], u * cs[4 + j]);
-            b[2 * j + 1] = fmaf(u, sn[4 + j], w * cs[4 + j]);
+        for (int j = 0; j < 4; j += 2) {
+            two(a[2 * j], a[2 * j + 2], a[2 * j + 1], a[2 * j + 3], j);
+            two(b[2 * j], b[2 * j + 2], b[2 * j + 1], b[2 * j + 3], 4 + j);
         }
     }
 }
@@ -146,7 +150,7 @@ struct RopeArgs {
     int H0, H;            // heads of the first tensor, of both
     const int *pos;       // [axes][n]
     long long n;          // B * T
-    int T, rot, heads_per_cta;
+    int T, rot, heads_per_cta, groups;   // head groups
     float sign;
 };
 
@@ -161,7 +165,10 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     pdl_launch();
     pdl_wait();
     const int v = threadIdx.x % TPR;
-    const long long tok = (long long)blockIdx.x * (kRopeThreads / TPR) + threadIdx.x / TPR;
+    // head groups next to one another: CTAs that run together read whole token rows of a packed
+    // projection
+    const int tile = (int)(blockIdx.x / a.groups), group = (int)blockIdx.x - tile * a.groups;
+    const long long tok = (long long)tile * (kRopeThreads / TPR) + threadIdx.x / TPR;
     if (tok >= a.n)
         return;
     const long long b = tok / a.T, t = tok - b * a.T;
@@ -175,7 +182,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
             sn[j] *= a.sign;
         }
     }
-    const int h0 = blockIdx.y * a.heads_per_cta, h1 = min(a.H, h0 + a.heads_per_cta);
+    const int h0 = group * a.heads_per_cta, h1 = min(a.H, h0 + a.heads_per_cta);
     for (int hb = h0; hb < h1; hb += kHeadsAhead) {
         Raw8<E> p[kHeadsAhead], q[kHeadsAhead];
 #pragma unroll
@@ -218,20 +225,20 @@ RopeTable table_of(const fa_rope_spec &s)
 
 Row3 row3(const fa_heads &x) { return Row3{x.data, x.stride_b, x.stride_h, x.stride_t}; }
 
-// Heads one thread runs over: as many as leave enough threads to fill the device.
+// Heads one thread runs over: as few as let all CTAs be resident (two an SM), 32 at most.  With 4,
+// 8, 16, 32 and 64 heads the q and k of B8 H32 T4096 d128 take 229, 190, 174, 167 and 173 us.
 int heads_per_cta(long long tokens, int H, int d)
 {
-    const long long want = (long long)device_sm_count() * 1024;
-    const long long all = tokens * H * (d / 16);
-    const long long n = all / want;
-    return (int)(n < 1 ? 1 : n > 8 ? 8 : n);
+    const long long ctas = (tokens * (d / 16) + kRopeThreads - 1) / kRopeThreads * H, slots = 2 * device_sm_count();
+    const long long n = (ctas + slots - 1) / slots;
+    return (int)(n < 1 ? 1 : n > 32 ? 32 : n);
 }
 
 template <typename E, int D>
 int rope_run(const RopeTable &t, const RopeArgs &a, int interleaved, cudaStream_t s)
 {
     constexpr int TOK = kRopeThreads / (D / 16);
-    const dim3 grid((unsigned)((a.n + TOK - 1) / TOK), (unsigned)((a.H + a.heads_per_cta - 1) / a.heads_per_cta));
+    const dim3 grid((unsigned)((a.n + TOK - 1) / TOK * a.groups));
     return launch_overlapped(interleaved ? rope_kernel<E, D, true> : rope_kernel<E, D, false>, grid, kRopeThreads, 0, 0, true, s, t, a);
 }
 
@@ -245,7 +252,7 @@ int rope_width(int d, const RopeTable &t, const RopeArgs &a, int interleaved, cu
 // ------------------------------------------------------------------ append
 struct AppendArgs {
     Row3 q, qo, k, v;
-    int Hq, Hkv, B, T, rot, rotate, heads_per_cta;
+    int Hq, Hkv, B, T, rot, rotate, heads_per_cta, groups;
     const int *pos;
     const int *block_table, *lens, *seen, *new_lens;
     void *kp, *vp;
@@ -255,14 +262,35 @@ struct AppendArgs {
     int num_pages, max_pages, ps_shift;
 };
 
-// 8 values into the cache: bf16, or e4m3 codes of x / scale.
+// 8 values into the cache: bf16, or e4m3 codes of x / scale, the quotient rounded to nearest.  With
+// inv the rounded reciprocal of the scale, q = x inv is within one step of the quotient, and
+// q + (x - q scale) inv rounds it correctly (P. Markstein, 1990): three operations for two values
+// where the divide takes several each.  Values that would overflow on the way are divided.
 template <bool FP8>
-__device__ __forceinline__ void put8(void *base, long long at, const float (&x)[8], float scale)
+__device__ __forceinline__ void put8(void *base, long long at, const float (&x)[8], float scale, float inv)
 {
     if constexpr (FP8) {
+        float q[8];
+#pragma unroll
+        for (int j = 0; j < 8; j += 2)
+            fmul2(q[j], q[j + 1], x[j], x[j + 1], inv, inv);
+        const float big = fmax3(fmax3(fabsf(q[0]), fabsf(q[1]), fabsf(q[2])), fmax3(fabsf(q[3]), fabsf(q[4]), fabsf(q[5])),
+                                fmaxf(fabsf(q[6]), fabsf(q[7])));
+        if (big < 1e30f) {
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+                float r0, r1;
+                ffma2(r0, r1, q[j], q[j + 1], -scale, -scale, x[j], x[j + 1]);
+                ffma2(q[j], q[j + 1], r0, r1, inv, inv, q[j], q[j + 1]);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                q[j] = __fdiv_rn(x[j], scale);
+        }
         uint2 w;
-        w.x = pack_e4m3x4(__fdiv_rn(x[0], scale), __fdiv_rn(x[1], scale), __fdiv_rn(x[2], scale), __fdiv_rn(x[3], scale));
-        w.y = pack_e4m3x4(__fdiv_rn(x[4], scale), __fdiv_rn(x[5], scale), __fdiv_rn(x[6], scale), __fdiv_rn(x[7], scale));
+        w.x = pack_e4m3x4(q[0], q[1], q[2], q[3]);
+        w.y = pack_e4m3x4(q[4], q[5], q[6], q[7]);
         *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(base) + at) = w;
     } else {
         store8(static_cast<__nv_bfloat16 *>(base) + at, x);
@@ -279,14 +307,17 @@ __global__ void __launch_bounds__(kRopeThreads) append_kernel(const __grid_const
     pdl_wait();
     const int vec = threadIdx.x % TPR;
     const long long n = (long long)a.B * a.T;
-    const long long tok = (long long)blockIdx.x * (kRopeThreads / TPR) + threadIdx.x / TPR;
+    // head groups next to one another: CTAs that run together read whole token rows of a packed
+    // projection
+    const int tile = (int)(blockIdx.x / a.groups), group = (int)blockIdx.x - tile * a.groups;
+    const long long tok = (long long)tile * (kRopeThreads / TPR) + threadIdx.x / TPR;
     if (tok >= n)
         return;
     const int b = (int)(tok / a.T), t = (int)(tok - (long long)b * a.T);
     const int len = a.lens[b], cap = a.max_pages << a.ps_shift;
     const int nb = a.new_lens ? a.new_lens[b] : a.T;
     if (len < 0 || len > cap || nb < 0 || nb > a.T || nb > len) {
-        if (vec == 0 && t == 0 && blockIdx.y == 0)
+        if (vec == 0 && t == 0 && group == 0)
             atomicCAS(&g_cache_status, 0, kStatusBadIndex);
         return;
     }
@@ -294,7 +325,7 @@ __global__ void __launch_bounds__(kRopeThreads) append_kernel(const __grid_const
         return;
     const int slot = len - nb + t;
     const Slice sl = slice_of(vec, a.rotate ? a.rot : 0, INTER);
-    const int h0 = blockIdx.y * a.heads_per_cta, h1 = min(a.Hq + 2 * a.Hkv, h0 + a.heads_per_cta);
+    const int h0 = group * a.heads_per_cta, h1 = min(a.Hq + 2 * a.Hkv, h0 + a.heads_per_cta);
     float sn[8], cs[8];
     if (sl.pair >= 0 && h0 < a.Hq + a.Hkv) {
 #pragma unroll
@@ -342,9 +373,9 @@ __global__ void __launch_bounds__(kRopeThreads) append_kernel(const __grid_const
                 const bool isv = h >= a.Hq + a.Hkv;
                 const int hk = h - a.Hq - (isv ? a.Hkv : 0);
                 const long long at = ((((long long)page * a.Hkv + hk) << a.ps_shift) + row) * D;
-                const float scale = FP8 ? (isv ? a.vs : a.ks)[hk] : 1.f;
-                put8<FP8>(isv ? a.vp : a.kp, at + sl.e0, x, scale);
-                put8<FP8>(isv ? a.vp : a.kp, at + sl.e1, y, scale);
+                const float scale = FP8 ? (isv ? a.vs : a.ks)[hk] : 1.f, inv = FP8 ? __frcp_rn(scale) : 1.f;
+                put8<FP8>(isv ? a.vp : a.kp, at + sl.e0, x, scale, inv);
+                put8<FP8>(isv ? a.vp : a.kp, at + sl.e1, y, scale, inv);
                 if (!isv && vec == 0) {
                     const long long w = ((long long)b * a.Hkv + hk) * cap + slot;
                     if (a.weight)
@@ -362,8 +393,7 @@ int append_run(const RopeTable &t, const AppendArgs &a, int interleaved, cudaStr
 {
     constexpr int TOK = kRopeThreads / (D / 16);
     const long long n = (long long)a.B * a.T;
-    const int H = a.Hq + 2 * a.Hkv;
-    const dim3 grid((unsigned)((n + TOK - 1) / TOK), (unsigned)((H + a.heads_per_cta - 1) / a.heads_per_cta));
+    const dim3 grid((unsigned)((n + TOK - 1) / TOK * a.groups));
     return launch_overlapped(interleaved ? append_kernel<D, true, FP8> : append_kernel<D, false, FP8>, grid, kRopeThreads, 0, 0, true, s, t, a);
 }
 
@@ -843,8 +873,9 @@ int rope_launch(const fa_heads *x, const fa_heads *y, int n, const int *position
     a.T = T;
     a.rot = spec.rot;
     a.heads_per_cta = heads_per_cta(a.n, a.H, spec.d);
-    if ((a.H + a.heads_per_cta - 1) / a.heads_per_cta > 65535)
-        a.heads_per_cta = (a.H + 65534) / 65535;
+    a.groups = (a.H + a.heads_per_cta - 1) / a.heads_per_cta;
+    if ((a.n / 16 + 1) * a.groups > INT_MAX)
+        return ERR_UNSUPPORTED;
     a.sign = inverse ? -1.f : 1.f;
     const RopeTable t = table_of(spec);
     return dtype == FA_F32 ? rope_width<float>(spec.d, t, a, spec.interleaved, s)
@@ -882,8 +913,9 @@ int append_launch(const fa_kv_cache &c, const fa_heads &k, const fa_heads &v, co
     a.ps_shift = shift_of(c.page_size);
     const int H = a.Hq + 2 * a.Hkv;
     a.heads_per_cta = heads_per_cta((long long)c.B * T, H, c.d);
-    if ((H + a.heads_per_cta - 1) / a.heads_per_cta > 65535)
-        a.heads_per_cta = (H + 65534) / 65535;
+    a.groups = (H + a.heads_per_cta - 1) / a.heads_per_cta;
+    if (((long long)c.B * T / 16 + 1) * a.groups > INT_MAX)
+        return ERR_UNSUPPORTED;
     RopeTable t{};
     if (spec)
         t = table_of(*spec);

@@ -234,7 +234,7 @@ int fa_rope(const fa_heads *x, const fa_heads *y, int n, const int *positions, c
  *   k, v         [num_pages][Hkv][page_size][d], bf16 (FA_BF16) or e4m3 codes
  *                (FA_E4M3)
  *   k_scale, v_scale  [Hkv] f32, FA_E4M3 only: a code c of head h stands for
- *                c * scale[h] (positive, finite); NULL for FA_BF16
+ *                c * scale[h] (2^-64 to 2^64); NULL for FA_BF16
  *   block_table  [B][max_pages] int32: entry i of sequence b (its slot i) is
  *                row i % page_size of page block_table[b][i / page_size]
  *   lens         [B] int32: entries of each sequence, 0 to max_pages * page_size

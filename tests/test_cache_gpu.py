@@ -512,6 +512,24 @@ def test_append_rounds_like_the_type(fa):
     assert torch.equal(got[~torch.isnan(got)], k[0, 0, 0][~torch.isnan(got)]) and int(torch.isnan(got).sum()) == 1
 
 
+def test_append_codes_are_the_quotients(fa):
+    """Every code is the e4m3 value nearest to the fp32 quotient x / scale, whatever the scale."""
+    g = gen(43)
+    Hkv, T = 64, 256
+    cache = make_cache(fa, 44, [T], Hkv, 128, 256, fp8=True)
+    for t, lo, hi in ((cache.k_scale, -64, 64), (cache.v_scale, -6, 2)):
+        t.copy_(torch.exp2(lo + (hi - lo) * torch.rand(Hkv, generator=g, device=DEV)))
+    v = randn(g, 1, Hkv, T, 128)
+    # quotients on and next to the borders between codes, as bf16 allows
+    k = ((torch.randint(-480, 480, (1, Hkv, T, 128), generator=g, device=DEV) / 16) * cache.k_scale[:, None, None]).to(BF16)
+    fa.fa_cache_append(cache, k, v)
+    assert fa.fa_sync_status() == fa.FA_OK
+    page = int(cache.block_table[0, 0])
+    for pool, x, scale in ((cache.k, k, cache.k_scale), (cache.v, v, cache.v_scale)):
+        ref = (x[0].float() / scale[:, None, None]).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+        assert torch.equal(pool[page], ref)
+
+
 def test_append_bad_counts_and_pages(fa):
     cache = make_cache(fa, 42, [40, 40, 40, 40], 1, 64, 16, weight=True)
     cache.lens[0] = cache.max_pages * 16 + 1
