@@ -448,28 +448,41 @@ __device__ __forceinline__ int block_rank(bool p, int &total, int *scratch)
 
 // ---- selection by a cluster per (sequence, KV head)
 // The entries' ranks are read once and stay in shared memory, a contiguous run of slots per CTA.
-// Four passes of a radix select of 8 bits (counts of the whole cluster read over distributed
+// Up to four passes of a radix select of 8 bits (counts of the whole cluster read over distributed
 // shared memory, every CTA finds the digit for itself; fewer when all that match a prefix stay)
-// give the rank of the last entry that stays.  Digits of 11 bits save a pass but read 8 times the
-// counts from every CTA: 53 us for 32 units of up to 32768 entries, where this takes 19.  Then one
-// scan per question over runs of consecutive slots per thread: which
-// of several equals stay, and the numbers of the holes in front of the new length and of the kept
-// entries behind it.  The kept ones wait at the front of `kept` until every hole has read its own.
+// give the rank of the last entry that stays.  Then one scan over runs of consecutive slots per
+// thread numbers the holes in front of the new length and the kept entries behind it, which each
+// CTA lists; then the cluster's threads take hole and entry number g from whichever CTAs list them.
+// It is bound by latency, a chain of a dozen block- and cluster-wide steps, and not by its 20 bytes
+// an entry; what an entry that stays in its slot needs (kept, weight, order) is written when it is
+// read.  64 units of 4112 entries, and 32 of 9001 to 32768 with the rows' moves (17 us):
+//     threads a CTA      256, 4 and 8 CTAs a unit   512, 2 and 8   1024, 2 and 4
+//     us                 15.7 and 36.6              14.7 and 35.0  15.8 and 34.9
+constexpr int kPickThreads = 512;
 constexpr int kSelBins = 256, kSelPasses = 4;
-constexpr int kSelItems = 49;                                // entries a thread, at most (odd: see run)
+constexpr int kSelCap = 32768;                               // entries a CTA, at most (their numbers take 16 bits)
 constexpr int kSelCopies = 8;                                // of the first pass's counts: most ranks share a few digits
-constexpr int kSelFixed = (kSelPasses + kSelCopies) * kSelBins * 4 + 2 * 32 * 4 + 32;   // shared memory besides the ranks
+constexpr int kSelFixed = (kSelPasses + kSelCopies) * kSelBins * 4 + 32 * 4 + 32;   // shared memory besides the entries
+constexpr int kFewMoves = 128;                               // moved rows that the selection copies itself
 
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ int cluster_load(const int *p, int rank)   // the same word of another CTA
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ uint32_t cluster_addr(const void *p, int rank)   // the same place in another CTA
 {
     uint32_t addr;
-    int x;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(x) : "r"(addr) : "memory");
+    return addr;
+}
+__device__ __forceinline__ int cluster_load(const int *p, int rank)
+{
+    int x;
+    asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(x) : "r"(cluster_addr(p, rank)) : "memory");
+    return x;
+}
+__device__ __forceinline__ int cluster_load16(const uint16_t *p, int rank)
+{
+    uint16_t x;
+    asm volatile("ld.shared::cluster.u16 %0, [%1];" : "=h"(x) : "r"(cluster_addr(p, rank)) : "memory");
     return x;
 }
 
@@ -487,19 +500,32 @@ __device__ __forceinline__ int block_scan(int x, int &total, int *scratch)
     if (lane_id() == 31)
         scratch[warp_id()] = inc;
     __syncthreads();
-    const int c = scratch[lane_id()];
+    const int c = lane_id() < blockDim.x / 32 ? scratch[lane_id()] : 0;
     total = __reduce_add_sync(0xffffffffu, c);
     return __reduce_add_sync(0xffffffffu, lane_id() < warp_id() ? c : 0) + inc - x;
 }
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_constant__ EvictArgs a, int cs)
+// Byte offset of a slot's row in the pools, -1 if its page is out of range.
+__device__ __forceinline__ long long row_of(const EvictArgs &a, int b, int h, int slot)
 {
+    const int page = a.block_table[(long long)b * a.max_pages + (slot >> a.ps_shift)];
+    if (page < 0 || page >= a.num_pages)
+        return -1;
+    return ((((long long)page * a.Hkv + h) << a.ps_shift) + (slot & ((1 << a.ps_shift) - 1))) * a.row_bytes;
+}
+
+__global__ void __launch_bounds__(kPickThreads) evict_select_kernel(const __grid_constant__ EvictArgs a, int cs, int per, int few)
+{
+    constexpr int T = kPickThreads;
     extern __shared__ __align__(16) int sel_smem[];
-    int *copies = sel_smem, *hist = copies + kSelCopies * kSelBins, *scratch = hist + kSelPasses * kSelBins, *share = scratch + 32, *pick = share + 32;
-    uint32_t *keys = reinterpret_cast<uint32_t *>(pick + 8);
-    const int rank = (int)blockIdx.x % cs, unit = (int)blockIdx.x / cs, b = unit / a.Hkv, tid = threadIdx.x;
+    int *copies = sel_smem, *hist = copies + kSelCopies * kSelBins, *scratch = hist + kSelPasses * kSelBins;
+    int *share = scratch + 32, *pick = share + 4;
+    uint32_t *keys = reinterpret_cast<uint32_t *>(pick + 4);
+    uint16_t *list = reinterpret_cast<uint16_t *>(keys + per);   // holes, then movers
+    const int rank = (int)blockIdx.x % cs, unit = (int)blockIdx.x / cs, b = unit / a.Hkv, h = unit - b * a.Hkv;
+    const int tid = threadIdx.x;
     pdl_launch();
-    for (int i = tid; i < (kSelCopies + kSelPasses) * kSelBins; i += kSelThreads)
+    for (int i = tid; i < (kSelCopies + kSelPasses) * kSelBins; i += T)
         copies[i] = 0;
     pdl_wait();
     const int len = a.lens[b];
@@ -509,52 +535,53 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
     const int end = bad ? 0 : min(len, a.budget);
     if (bad && tid == 0)
         atomicCAS(&g_cache_status, 0, kStatusBadIndex);
-    for (int j = end + rank * kSelThreads + tid; j < a.budget; j += cs * kSelThreads)
+    for (int j = end + rank * T + tid; j < a.budget; j += cs * T)
         kept[j] = -1;
+    if (few && h == 0 && rank == 0 && tid == 0 && a.lens_out != a.lens)
+        a.lens_out[b] = min(len, a.budget);
     if (bad)
         return;   // the whole cluster
     const float *weight = a.weight + base;
     const int *order = a.order ? a.order + base : nullptr;
-    if (len <= a.budget) {
-        for (int j = rank * kSelThreads + tid; j < end; j += cs * kSelThreads) {
-            kept[j] = j;
-            a.weight_out[base + j] = weight[j];
-            if (order)
-                a.order_out[base + j] = order[j];
-        }
-        return;
-    }
-    const int per = (len + cs - 1) / cs, lo = min(len, rank * per), n = min(len, lo + per) - lo;
+    const int lo = min(len, rank * per), n = min(len, lo + per) - lo;
     const int recent = (a.seen ? a.seen[b] : len) - a.n_recent;
     const bool ages = order && (a.n_first > 0 || a.n_recent > 0);
     __syncthreads();
-    for (int i0 = tid; i0 < n; i0 += 4 * kSelThreads) {   // four loads in flight
-        float w[4];
-        int at[4];
+    for (int i0 = tid; i0 < n; i0 += 8 * T) {   // eight loads in flight
+        float w[8];
+        int at[8];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int i = i0 + u * kSelThreads;
+        for (int u = 0; u < 8; ++u) {
+            const int i = i0 + u * T;
             w[u] = i < n ? weight[lo + i] : 0.f;
-            at[u] = ages && i < n ? order[lo + i] : 0;
+            at[u] = order && i < n ? order[lo + i] : 0;
         }
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int i = i0 + u * kSelThreads;
-            if (i < n) {
-                const uint32_t k = rank_key(w[u], ages && (at[u] < a.n_first || (a.n_recent > 0 && at[u] >= recent)));
-                keys[i] = k;
-                atomicAdd(&copies[(k >> 24) * kSelCopies + (tid & (kSelCopies - 1))], 1);
+        for (int u = 0; u < 8; ++u) {
+            const int i = i0 + u * T, j = lo + i;
+            if (i >= n)
+                break;
+            if (j < end) {   // right for an entry that stays in its slot
+                kept[j] = j;
+                a.weight_out[base + j] = w[u];
+                if (order)
+                    a.order_out[base + j] = at[u];
             }
+            const uint32_t k = rank_key(w[u], ages && (at[u] < a.n_first || (a.n_recent > 0 && at[u] >= recent)));
+            keys[i] = k;
+            atomicAdd(&copies[(k >> 24) * kSelCopies + (tid & (kSelCopies - 1))], 1);
         }
     }
+    if (len <= a.budget)
+        return;   // all stay; the whole cluster
     uint32_t prefix = 0;
-    int need = end, equal = 0;   // still to be taken among those that match the prefix; how many do
+    int need = end, edge = INT_MAX;   // still to be taken among those that match the prefix; see below
 #pragma unroll 1
     for (int pass = 0; pass < kSelPasses; ++pass) {
         const int shift = 24 - 8 * pass;
         int *hp = hist + pass * kSelBins;
         if (pass > 0) {
-            for (int i = tid; i < n; i += kSelThreads) {
+            for (int i = tid; i < n; i += T) {
                 const uint32_t u = keys[i];
                 if ((u ^ prefix) >> (shift + 8) == 0)
                     atomicAdd(&hp[(u >> shift) & 255], 1);
@@ -566,17 +593,20 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
                 hp[tid] = x.x + x.y + x.z + x.w + y.x + y.y + y.z + y.w;
             }
         }
-        cluster_sync();
-        // four threads a bin, bins from the top
-        const int d = kSelBins - 1 - (tid >> 2);
+        cluster_arrive();
+        cluster_wait();
+        // T / 256 threads a bin, bins from the top
+        constexpr int TPB = T / kSelBins;
+        const int d = kSelBins - 1 - tid / TPB;
         int c = 0;
-        for (int r = tid & 3; r < cs; r += 4)
+        for (int r = tid % TPB; r < cs; r += TPB)
             c += cluster_load(hp + d, r);
-        c += __shfl_xor_sync(0xffffffffu, c, 1);
-        c += __shfl_xor_sync(0xffffffffu, c, 2);
+#pragma unroll
+        for (int off = 1; off < TPB; off <<= 1)
+            c += __shfl_xor_sync(0xffffffffu, c, off);
         int total;
-        const int before = block_scan((tid & 3) ? 0 : c, total, scratch);
-        if ((tid & 3) == 0 && before < need && need <= before + c) {
+        const int before = block_scan(tid % TPB ? 0 : c, total, scratch);
+        if (tid % TPB == 0 && before < need && need <= before + c) {
             pick[0] = d;
             pick[1] = need - before;
             pick[2] = c;
@@ -584,83 +614,117 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
         __syncthreads();
         prefix |= (uint32_t)pick[0] << shift;
         need = pick[1];
-        equal = pick[2];
+        const int equal = pick[2];
         if (equal == need)   // all that match stay: the lower digits do not matter
             break;
-    }
-    // an odd run of consecutive slots per thread: the runs of a warp lie in different banks
-    const int q = ((n + kSelThreads - 1) / kSelThreads) | 1, i0 = min(n, tid * q), i1 = min(n, i0 + q);
-    int edge = INT_MAX;   // slots below it stay among the entries whose rank is `prefix` itself
-    if (equal > need) {
-        int mine = 0, total;
-        for (int i = i0; i < i1; ++i)
-            mine += keys[i] == prefix;
-        int r = block_scan(mine, total, scratch);
-        if (tid == 0) {
-            share[0] = total;
-            pick[3] = INT_MAX;
+        if (pass == kSelPasses - 1) {   // of equal ranks the first `need` stay: those below slot `edge`
+            int done = 0;
+            for (int r = 0; r < rank; ++r)
+                done += cluster_load(hp + (prefix & 255), r);
+            edge = done >= need ? 0 : done + hp[prefix & 255] <= need ? INT_MAX : -1;
+            if (edge < 0) {   // this CTA has the last one
+                const int q = ((n + T - 1) / T) | 1, i0 = min(n, tid * q), i1 = min(n, i0 + q);
+                int mine = 0;
+                for (int i = i0; i < i1; ++i)
+                    mine += keys[i] == prefix;
+                int r = done + block_scan(mine, total, scratch);
+                for (int i = i0; i < i1; ++i)
+                    if (keys[i] == prefix && r++ == need - 1)
+                        pick[3] = i + 1;
+                __syncthreads();
+                edge = pick[3];
+            }
         }
-        cluster_sync();
-        for (int c = 0; c < rank; ++c)
-            r += cluster_load(share, c);
-        for (int i = i0; i < i1; ++i)
-            if (keys[i] == prefix && r++ == need - 1)
-                pick[3] = i + 1;
-        __syncthreads();
-        // this CTA's entries behind the last one to stay, wherever that is
-        int before = 0;
-        for (int c = 0; c < rank; ++c)
-            before += cluster_load(share, c);
-        edge = before >= need ? 0 : pick[3];
     }
     auto stays = [&](int i) {
         const uint32_t u = keys[i];
-        return u > prefix || (u == prefix && i < edge);
+        return u > prefix || (u == prefix && i < edge) || (edge == INT_MAX && u >= prefix);
     };
-    // holes in front of the new length in the low half, kept entries behind it in the high half
+    // holes in front of the new length in the low half, kept entries behind it in the high half; an
+    // odd run of consecutive slots per thread: the runs of a warp lie in different banks
+    const int q = ((n + T - 1) / T) | 1, i0 = min(n, tid * q), i1 = min(n, i0 + q);
     int mine = 0, total;
     for (int i = i0; i < i1; ++i)
         mine += lo + i < end ? (stays(i) ? 0 : 1) : (stays(i) ? 1 << 16 : 0);
     const int before = block_scan(mine, total, scratch);
-    if (tid == 0) {
-        share[1] = total & 0xFFFF;
-        share[2] = total >> 16;
-    }
-    cluster_sync();
-    int hole = before & 0xFFFF, mover = before >> 16;
-    for (int c = 0; c < rank; ++c) {
-        hole += cluster_load(share + 1, c);
-        mover += cluster_load(share + 2, c);
-    }
-    for (int i = i0, m = mover; i < i1; ++i)
-        if (lo + i >= end && stays(i))
-            kept[m++] = lo + i;
-    cluster_sync();
-    for (int i = i0; i < i1 && lo + i < end; ++i)
-        keys[i] = stays(i) ? lo + i : kept[hole++];
-    cluster_sync();
-    const int front = min(n, end - lo);
-    for (int i0 = tid; i0 < front; i0 += 4 * kSelThreads) {
-        float w[4];
-        int at[4], from[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int i = i0 + u * kSelThreads;
-            from[u] = i < front ? (int)keys[i] : 0;
-            w[u] = weight[from[u]];
-            at[u] = order ? order[from[u]] : 0;
+    if (mine) {
+        int x = before & 0xFFFF, m = (total & 0xFFFF) + (before >> 16);
+        for (int i = i0; i < i1; ++i) {
+            const bool stay = stays(i);
+            if (lo + i < end && !stay)
+                list[x++] = (uint16_t)i;
+            if (lo + i >= end && stay)
+                list[m++] = (uint16_t)i;
         }
+    }
+    if (tid == 0)
+        share[0] = total;
+    cluster_arrive();
+    cluster_wait();
+    int holes[8], moved[8], all = 0;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int i = i0 + u * kSelThreads, j = lo + i;
-            if (i < front) {
-                kept[j] = from[u];
-                a.weight_out[base + j] = w[u];
-                if (order)
-                    a.order_out[base + j] = at[u];
+    for (int r = 0; r < 8; ++r) {
+        const int x = r < cs ? cluster_load(share, r) : 0;
+        holes[r] = x & 0xFFFF;
+        moved[r] = x >> 16;
+        all += holes[r];
+    }
+    // hole and mover number g of the cluster, over all its threads; the lanes of a warp stay
+    // together, for it copies whole rows
+    for (int g0 = (rank * T + tid) & ~31; g0 < all; g0 += cs * T) {
+        const int g = g0 + (int)lane_id();
+        long long from = -1, to = -1;
+        if (g < all) {
+            int r = 0, m = g, c = 0, x = g;   // the CTAs that list them, and their places there
+#pragma unroll
+            for (int k = 0; k < 7; ++k) {
+                const bool past = r == k && m >= holes[k];
+                m -= past ? holes[k] : 0;
+                r += past;
+                const bool over = c == k && x >= moved[k];
+                x -= over ? moved[k] : 0;
+                c += over;
+            }
+            int skip = 0;   // holes of CTA c, in front of its movers
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                skip = c == k ? holes[k] : skip;
+            const int j = r * per + cluster_load16(list + m, r);
+            const int i = c * per + cluster_load16(list + skip + x, c);
+            kept[j] = i;
+            a.weight_out[base + j] = weight[i];
+            if (order)
+                a.order_out[base + j] = order[i];
+            if (few) {
+                from = row_of(a, b, h, i);
+                to = row_of(a, b, h, j);
+                if (from < 0 || to < 0) {
+                    atomicCAS(&g_cache_status, 0, kStatusBadIndex);
+                    from = -1;
+                }
+            }
+        }
+        for (uint32_t todo = __ballot_sync(0xffffffffu, from >= 0); todo; todo &= todo - 1) {
+            const int l = __ffs(todo) - 1, vecs = a.row_bytes / 16;
+            const long long f = __shfl_sync(0xffffffffu, from, l), t = __shfl_sync(0xffffffffu, to, l);
+            for (int e = (int)lane_id(); e < 2 * vecs; e += 32) {
+                uint8_t *pool = e < vecs ? a.k : a.v;
+                const int o = (e < vecs ? e : e - vecs) * 16;
+                *reinterpret_cast<uint4 *>(pool + t + o) = *reinterpret_cast<const uint4 *>(pool + f + o);
             }
         }
     }
+    cluster_arrive();   // no CTA ends while another may read its list
+    cluster_wait();
+}
+
+// lens_out = min(lens, budget), where the selection copied the rows and lens_out is lens.
+__global__ void __launch_bounds__(256) evict_lens_kernel(const __grid_constant__ EvictArgs a)
+{
+    pdl_launch();
+    pdl_wait();
+    for (int b = blockIdx.x * 256 + threadIdx.x; b < a.B; b += gridDim.x * 256)
+        a.lens_out[b] = min(a.lens[b], a.budget);
 }
 
 // The same for lengths whose ranks do not fit the shared memory of a cluster: one CTA per
@@ -797,21 +861,14 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const __grid_constant__
         const int len = a.lens[b];
         a.lens_out[b] = min(len, a.budget);
     }
-    const int *table = a.block_table + (long long)b * a.max_pages;
     const int vshift = 31 - __clz(a.row_bytes / 16), vecs = 1 << vshift;   // 16-byte vectors of a row
-    auto at = [&](int slot) -> long long {
-        const int page = table[slot >> a.ps_shift];
-        if (page < 0 || page >= a.num_pages)
-            return -1;
-        return ((((long long)page * a.Hkv + h) << a.ps_shift) + (slot & ((1 << a.ps_shift) - 1))) * a.row_bytes;
-    };
     for (int j0 = (blockIdx.y * 8 + (threadIdx.x >> 5)) * 32; j0 < a.budget; j0 += gridDim.y * 256) {
         const int j = j0 + lane;
         const int i = j < a.budget ? a.kept[(long long)unit * a.budget + j] : -1;
         long long from = -1, to = -1;
         if (i >= 0 && i != j) {
-            from = at(i);
-            to = at(j);
+            from = row_of(a, b, h, i);
+            to = row_of(a, b, h, j);
             if (from < 0 || to < 0) {
                 atomicCAS(&g_cache_status, 0, kStatusBadIndex);
                 from = -1;
@@ -957,26 +1014,35 @@ int evict_launch(const fa_kv_cache &c, int budget, int n_first, int n_recent, fl
     a.ps_shift = shift_of(c.page_size);
     a.row_bytes = c.d * (c.dtype == FA_E4M3 ? 1 : 2);
     const int units = c.B * c.Hkv;
-    // CTAs per (sequence, KV head): 1024 entries or more each, at most one CTA an SM (4112 entries in
-    // 64 units: 16.6, 15.9, 21.3, 39.8 us with 1, 2, 4, 8; up to 32768 in 32: 50.0, 40.8, 36.5, 39.1)
+    // CTAs per (sequence, KV head): 2048 entries or more each, all of them resident (two an SM); with
+    // half as many, and twice as many, 15.9 and 16.2 us for 64 units of 4112 entries instead of
+    // 14.7, and 37.0 for 32 units of up to 32768 instead of 35.0
     int cs = 1;
-    while (cs < 8 && a.cap / (2 * cs) >= kSelThreads && (long long)units * 2 * cs <= device_sm_count())
+    while (cs < 8 && a.cap / (2 * cs) >= 2048 && (long long)units * cs <= device_sm_count())
         cs *= 2;
-    while (cs < 8 && (a.cap + cs - 1) / cs > kSelItems * kSelThreads)
+    while (cs < 8 && (a.cap + cs - 1) / cs > kSelCap)
         cs *= 2;
     const int per = (a.cap + cs - 1) / cs;
+    const bool wide = per <= kSelCap && (long long)units * cs <= INT_MAX;
+    const int few = wide && a.cap - budget <= kFewMoves;
     int st;
-    if (per <= kSelItems * kSelThreads && (long long)units * cs <= INT_MAX) {
+    if (wide) {
         if (cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 kSelFixed + kSelItems * kSelThreads * 4) != cudaSuccess)
+                                 kSelFixed + kSelCap * 6) != cudaSuccess)
             return ERR_CUDA;
-        st = launch_overlapped(evict_select_kernel, dim3((unsigned)(units * cs)), kSelThreads, kSelFixed + per * 4, cs,
-                               false, s, a, cs);
+        // after the kernel before it: clusters that wait on the SMs delay the moves of the call before
+        // (20 us instead of 16.5 for the first case)
+        st = launch_overlapped(evict_select_kernel, dim3((unsigned)(units * cs)), kPickThreads, kSelFixed + per * 6, cs, false,
+                               s, a, cs, per, few);
     } else {
         st = launch_overlapped(evict_select_long_kernel, dim3((unsigned)units), kSelThreads, 0, 0, false, s, a);
     }
     if (st != OK)
         return st;
+    if (few)
+        return lens_out == c.lens
+                   ? launch_overlapped(evict_lens_kernel, dim3((unsigned)((c.B + 255) / 256)), 256, 0, 0, true, s, a)
+                   : OK;
     const int blocks = (budget + 255) / 256;
     return launch_overlapped(evict_move_kernel, dim3((unsigned)units, blocks < 64 ? blocks : 64), 256, 0, 0, true, s, a);
 }

@@ -627,7 +627,7 @@ def test_evict(fa, case, in_place):
 
 def test_evict_longest(fa):
     """More entries than fit a cluster's shared memory."""
-    n, budget = 402000, 100001
+    n, budget = 270000, 100001
     cache = make_cache(fa, 54, [n], 1, 64, 256, weight=True)
     cache.weight.copy_(weights_of("few", gen(55), tuple(cache.weight.shape)) + (cache.weight < 0.5))
     w0, k0 = cache.weight.clone(), cache.k.clone()
