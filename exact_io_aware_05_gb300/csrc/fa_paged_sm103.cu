@@ -73,8 +73,8 @@ struct Cfg {
     static constexpr int OFF_RS = OFF_ML + NML;                    // scale of each row's scores
     static constexpr int OFF_BAR = OFF_RS + RT * 16 * 4;           // full[NST], empty[NST]
     static constexpr int OFF_OK = OFF_BAR + 16 * NST;              // per stage: which 16-entry groups are there
-    static constexpr int OFF_MISC = (OFF_OK + 4 * NST + 15) / 16 * 16;   // abort flag, reduction scratch
-    static constexpr int SMEM = OFF_MISC + 16 + 8 * (kMathWarps + 1) + 1024;
+    static constexpr int OFF_MISC = (OFF_OK + 4 * NST + 15) / 16 * 16;   // abort flag
+    static constexpr int SMEM = OFF_MISC + 16 + 1024;
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
@@ -178,28 +178,18 @@ __device__ __forceinline__ long long share_of(const PagedArgs &a, long long tota
     return c < least ? least : c;
 }
 
-__device__ __forceinline__ long long warp_sum64(long long x)
+// Tiles of the batch per KV head and row block.  Every warp adds them up for itself: the loads of
+// the others are in the same cache lines, and a block-wide sum would cost two barriers at a time
+// when nothing is under way.
+__device__ __forceinline__ long long warp_tiles(const PagedArgs &a)
 {
+    long long x = 0;
+#pragma unroll 4
+    for (int b = (int)lane_id(); b < a.B; b += 32)
+        x += tiles_of(a, b);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1)
         x += __shfl_xor_sync(0xffffffffu, x, off);
-    return x;
-}
-
-// Tiles of sequences [0, n) per KV head and row block, over the whole block of threads.
-__device__ __forceinline__ long long block_tiles(const PagedArgs &a, int n, volatile long long *scratch)
-{
-    long long x = 0;
-    for (int b = threadIdx.x; b < n; b += blockDim.x)
-        x += tiles_of(a, b);
-    x = warp_sum64(x);
-    if (lane_id() == 0)
-        scratch[warp_id()] = x;
-    __syncthreads();
-    x = 0;
-    for (int w = 0; w < (int)blockDim.x / 32; ++w)
-        x += scratch[w];
-    __syncthreads();
     return x;
 }
 
@@ -293,10 +283,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
         const int nt = tiles_of(a, b);
         p = Place{b, (int)blockIdx.x - b * per, 0, nt, nt};
         mine_all = nt;
-        __syncthreads();   // the barriers are there
     } else {
-        const long long total = block_tiles(a, a.B, reinterpret_cast<volatile long long *>(smem + C::OFF_MISC + 16)) *
-                                a.Hkv * a.RB;
+        const long long total = warp_tiles(a) * a.Hkv * a.RB;
         share = share_of(a, total);
         t0 = share * blockIdx.x;
         if (threadIdx.x == 0 && blockIdx.x == 0)
@@ -306,6 +294,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
         mine_all = min(share, total - t0);
         p = place_of(a, t0, mine_all);
     }
+    __syncthreads();   // the barriers are there
     // rows of a page in one box, and boxes of a tile
     const int bp_shift = a.ps_shift < 6 ? a.ps_shift : 6, boxes = C::KT >> bp_shift;
 
