@@ -171,26 +171,12 @@ __device__ __forceinline__ int tiles_of(const PagedArgs &a, int b) { return (len
 
 // Tiles a CTA takes of the batch's `total`: equal shares, but at least 128 entries, below which
 // the joining costs more than they do.
-__device__ __forceinline__ long long share_of(const PagedArgs &a, long long total)
+template <typename I>
+__device__ __forceinline__ I share_of(const PagedArgs &a, I total)
 {
-    const long long c = (total + a.grid - 1) / a.grid;
+    const I c = (total + a.grid - 1) / a.grid;
     const int least = a.kt < 128 ? 128 / a.kt : 1;
     return c < least ? least : c;
-}
-
-// Tiles of the batch per KV head and row block.  Every warp adds them up for itself: the loads of
-// the others are in the same cache lines, and a block-wide sum would cost two barriers at a time
-// when nothing is under way.
-__device__ __forceinline__ long long warp_tiles(const PagedArgs &a)
-{
-    long long x = 0;
-#pragma unroll 4
-    for (int b = (int)lane_id(); b < a.B; b += 32)
-        x += tiles_of(a, b);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1)
-        x += __shfl_xor_sync(0xffffffffu, x, off);
-    return x;
 }
 
 // A CTA's place in the batch's tiles: sequence b, unit ul (row block, KV head) in it, tile.
@@ -199,20 +185,48 @@ struct Place {
     long long left;   // tiles still to do
 };
 
-__device__ __forceinline__ Place place_of(const PagedArgs &a, long long t0, long long left)
+__device__ __forceinline__ long long warp_scan(long long x)   // sum over the lanes up to this one
+{
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, off);
+        if ((int)lane_id() >= off)
+            x += y;
+    }
+    return x;
+}
+
+// Finds the CTA's place; p.left: its tiles, 0 if there is nothing for it.  Every warp does it for
+// itself: the loads of the others are in the same cache lines, and a block-wide sum would cost
+// barriers at a time when nothing is under way.
+__device__ __forceinline__ Place place_of(const PagedArgs &a, long long &share, long long &t0)
 {
     const int per = a.Hkv * a.RB, lane = (int)lane_id();
-    Place p{a.B, 0, 0, 0, left};
-    long long base = 0;
-    for (int b0 = 0; b0 < a.B; b0 += 32) {
-        const int b = b0 + lane;
-        const int nt = b < a.B ? tiles_of(a, b) : 0;
-        long long inc = (long long)nt * per;
+    const int nt0 = lane < a.B ? tiles_of(a, lane) : 0;
+    const long long inc0 = warp_scan((long long)nt0 * per);
+    long long total = __shfl_sync(0xffffffffu, inc0, 31);
+    if (a.B > 32) {
+        long long x = 0;
+#pragma unroll 4
+        for (int b = 32 + lane; b < a.B; b += 32)
+            x += tiles_of(a, b);
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, inc, off);
-            if (lane >= off)
-                inc += y;
+        for (int off = 16; off > 0; off >>= 1)
+            x += __shfl_xor_sync(0xffffffffu, x, off);
+        total += x * per;
+    }
+    share = total < INT_MAX ? share_of(a, (int)total) : share_of(a, total);
+    t0 = share * blockIdx.x;
+    Place p{a.B, 0, 0, 0, 0};
+    if (t0 >= total)
+        return p;
+    p.left = min(share, total - t0);
+    long long base = 0, inc = inc0;
+    int nt = nt0;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+        if (b0 > 0) {
+            nt = b0 + lane < a.B ? tiles_of(a, b0 + lane) : 0;
+            inc = warp_scan((long long)nt * per);
         }
         const uint32_t past = __ballot_sync(0xffffffffu, base + inc > t0);
         if (past) {
@@ -221,12 +235,13 @@ __device__ __forceinline__ Place place_of(const PagedArgs &a, long long t0, long
             p.nt = __shfl_sync(0xffffffffu, nt, src);
             p.b = b0 + src;
             const long long in = t0 - (end - (long long)p.nt * per);
-            p.ul = (int)(in / p.nt);
+            p.ul = in < INT_MAX ? (int)in / p.nt : (int)(in / p.nt);
             p.tile = (int)(in - (long long)p.ul * p.nt);
             return p;
         }
         base += __shfl_sync(0xffffffffu, inc, 31);
     }
+    p.left = 0;   // lengths that change under the call: nothing out of range is read
     return p;
 }
 
@@ -239,7 +254,10 @@ __device__ __forceinline__ void next_unit(const PagedArgs &a, Place &p, int done
     if (p.left > 0 && ++p.ul == a.Hkv * a.RB) {
         p.ul = 0;
         do {
-            ++p.b;
+            if (++p.b >= a.B) {
+                p.left = 0;
+                return;
+            }
             p.nt = tiles_of(a, p.b);
         } while (p.nt == 0);
     }
@@ -264,7 +282,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_MISC);
     const int lane = (int)lane_id(), warp = (int)warp_id();
     const WaitCtx ctx{abort_flag, &g_paged_status, a.timeout_ns};
-    pdl_launch();
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::NST; ++s) {
             mbar_init(bar0 + 8u * s, 1);
@@ -284,15 +301,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
         p = Place{b, (int)blockIdx.x - b * per, 0, nt, nt};
         mine_all = nt;
     } else {
-        const long long total = warp_tiles(a) * a.Hkv * a.RB;
-        share = share_of(a, total);
-        t0 = share * blockIdx.x;
+        p = place_of(a, share, t0);
         if (threadIdx.x == 0 && blockIdx.x == 0)
             a.where[0] = share;
-        if (t0 >= total)
-            return;
-        mine_all = min(share, total - t0);
-        p = place_of(a, t0, mine_all);
+        if (p.left == 0)
+            return;   // the whole CTA
+        mine_all = p.left;
     }
     __syncthreads();   // the barriers are there
     // rows of a page in one box, and boxes of a tile
@@ -627,6 +641,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
                     mbar_arrive(bar0 + 8u * (C::NST + st));
             }
 
+            // the join's blocks may come now: earlier they would take registers that CTAs of the next
+            // call want
+            pdl_launch();
             // ---- the warps' states of each row tile together, then out, 32 features at a time
             const float s0 = quad_sum(l0[0] + l0[1]), s1 = quad_sum(l1[0] + l1[1]);
             if (c4 == 0) {
@@ -646,7 +663,29 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
             const bool whole = p.tile == 0 && cnt == p.nt;
             const long long slot = 2ll * blockIdx.x + (p.left == mine_all ? 0 : 1);
             float *part = a.part + slot * a.rows * (D + 2);
+            // a thread puts out four features of the same RT rows in every slice
             const float vs = FP8 ? a.vs[h] : 1.f;
+            float factor[RT];
+#pragma unroll
+            for (int e = 0; e < RT; ++e) {
+                const int row = (e * 128 + (int)threadIdx.x) >> 3;
+                const float t = top(row >> 4, row & 15);
+                float l = 0.f;
+#pragma unroll
+                for (int w = 0; w < KW; ++w) {
+                    const float2 y = ml[(w * RT + (row >> 4)) * 16 + (row & 15)];
+                    l = fmaf(y.y, weight(y.x, t), l);
+                }
+                factor[e] = whole ? (l == 0.f ? 0.f : vs / l) : vs;
+                if ((threadIdx.x & 7) == 0 && row < nrows && ok) {
+                    if (whole) {
+                        a.lse[grow + row] = l == 0.f ? -INFINITY : (t + log2f(l)) * 0.69314718055994530942f;
+                    } else {
+                        part[(long long)a.rows * D + row] = t;
+                        part[(long long)a.rows * (D + 1) + row] = l;
+                    }
+                }
+            }
 #pragma unroll
             for (int sl = 0; sl < D / C::OC; ++sl) {
                 float *mine = ob + (warp * 16 + r0) * C::OPITCH;
@@ -677,30 +716,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
                     }
                     if (row >= nrows || !ok)
                         continue;
-                    const float t = top(rt_, r);
-                    float l = 0.f;
-#pragma unroll
-                    for (int w = 0; w < KW; ++w) {
-                        const float2 y = ml[(w * RT + rt_) * 16 + r];
-                        l = fmaf(y.y, weight(y.x, t), l);
-                    }
-                    const float k = whole ? (l == 0.f ? 0.f : vs / l) : vs;
+                    const float k = factor[e];
                     if (whole) {
                         uint2 y;
                         y.x = pack_bf16x2(x.x * k, x.y * k);
                         y.y = pack_bf16x2(x.z * k, x.w * k);
                         *reinterpret_cast<uint2 *>(a.o + (grow + row) * D + sl * C::OC + col) = y;
-                        if (sl == 0 && col == 0)
-                            a.lse[grow + row] = l == 0.f ? -INFINITY : (t + log2f(l)) * 0.69314718055994530942f;
                     } else {
                         // 8-byte stores: a slot of `rows` (D + 2) floats is a multiple of 8 bytes
                         float2 *dst = reinterpret_cast<float2 *>(part + (long long)row * D + sl * C::OC + col);
                         dst[0] = make_float2(x.x * k, x.y * k);
                         dst[1] = make_float2(x.z * k, x.w * k);
-                        if (sl == 0 && col == 0) {
-                            part[(long long)a.rows * D + row] = t;
-                            part[(long long)a.rows * (D + 1) + row] = l;
-                        }
                     }
                 }
                 math_sync();
