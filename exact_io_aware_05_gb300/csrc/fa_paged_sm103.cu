@@ -24,6 +24,7 @@
 //     2^-17 and not 2^-9, which would be as large as the output's own rounding.  e4m3 codes become
 //     f16 exactly; there q is scaled by a power of two per row and P by 2^15, which keeps
 //     probabilities down to 2^-29 in f16's normal range, with 11 bits.
+#include <algorithm>
 #include <climits>
 
 #include <cuda_fp16.h>
@@ -57,9 +58,9 @@ struct Cfg {
     static constexpr int GW = KT / 16 * RT / kMathWarps;           // groups of 16 entries a warp has of a tile
     static constexpr int GP = GW % 2 == 0 && D <= 128 ? 2 : 1;     // groups it takes at once
     static constexpr int QPITCH = D * 2 + 16;                      // bytes of a query row in shared memory
-    static constexpr int OC = 32;                                  // features merged at a time
-    static constexpr int OPITCH = OC + 4;                          // floats of a merge row
-    static constexpr int NQ = RT * 16 * QPITCH, NO = kMathWarps * 16 * OPITCH * 4, NML = kMathWarps * 16 * 8;
+    static constexpr int MR = 512 / D;                             // rows of a row tile merged at a time
+    static constexpr int OPITCH = D + 4;                           // floats of a merge row
+    static constexpr int NQ = RT * 16 * QPITCH, NO = kMathWarps * MR * OPITCH * 4, NML = kMathWarps * 16 * 8;
     static constexpr int SMALL = 1024 + NQ + NO + NML + RT * 16 * 4 + 24 * 12 + 64;
     // as many CTAs an SM as the accumulators leave registers for and the ring has room; the
     // ring takes what is left
@@ -378,8 +379,63 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
         const uint32_t k_lane = (uint32_t)(krow * C::CB), k_unit = (uint32_t)((((lane >> 3) & 1) ^ swizzle_of(krow)) << 4);
         const uint32_t v_lane = (uint32_t)(vrow * C::CB), v_unit = (uint32_t)(((lane >> 4) ^ swizzle_of(vrow)) << 4);
         const uint32_t q_lane = sbase + C::OFF_Q + (rt * 16 + (lane & 15)) * C::QPITCH + (lane >> 4) * 16;
+        // The unit's query rows: a warp's share of them into registers, from there to shared memory as
+        // bf16, or as f16 over the row's power of two with features in the order in which the codes of
+        // four neighbours come out of a register.
+        uint32_t qw[RT * 4][D / 64];
+        float qks = 1.f;
+        auto fetch_q = [&](const Place &at) {
+            const int h = at.ul % a.Hkv, row0 = at.ul / a.Hkv * a.rows, nrows = min(a.rows, a.M - row0);
+            const __nv_bfloat16 *q = a.q + (((long long)at.b * a.Hq + h * a.G) * a.Tq + row0) * D;
+#pragma unroll
+            for (int j = 0; j < RT * 4; ++j) {
+                const int r = warp + kMathWarps * j;
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i)
+                    qw[j][i] = r < nrows ? reinterpret_cast<const uint32_t *>(q + (long long)r * D)[i * 32 + lane] : 0u;
+            }
+            if constexpr (FP8)
+                qks = a.ks[h];
+        };
+        auto put_q = [&]() {
+#pragma unroll
+            for (int j = 0; j < RT * 4; ++j) {
+                const int r = warp + kMathWarps * j;
+                uint8_t *qr = smem + C::OFF_Q + r * C::QPITCH;
+                float scale = a.scale_log2;
+                if constexpr (FP8) {
+                    float big = 0.f;
+#pragma unroll
+                    for (int i = 0; i < D / 64; ++i)
+                        big = fmax3(big, fabsf(__uint_as_float(qw[j][i] << 16)), fabsf(__uint_as_float(qw[j][i] & 0xFFFF0000u)));
+#pragma unroll
+                    for (int off = 16; off > 0; off >>= 1)
+                        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
+                    // 2^-e brings the row's largest value into [1, 4); zeros and infinities stay
+                    const int x = (int)(__float_as_uint(big) >> 23);
+                    const int e = x == 255 || x == 0 ? 0 : min(x - 127, 126);
+                    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+                    scale *= qks / down;
+#pragma unroll
+                    for (int i = 0; i < D / 64; ++i) {
+                        const int f = i * 64 + 2 * lane, c = (f & 15) >> 2;   // features f, f + 1
+                        const int at = (f & ~15) + 2 * c + ((f & 2) ? 8 : 0);
+                        reinterpret_cast<uint32_t *>(qr)[at / 2] =
+                            pack_f16x2(__uint_as_float(qw[j][i] << 16) * down, __uint_as_float(qw[j][i] & 0xFFFF0000u) * down);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < D / 64; ++i)
+                        reinterpret_cast<uint32_t *>(qr)[i * 32 + lane] = qw[j][i];
+                }
+                if (lane == 0)
+                    reinterpret_cast<float *>(smem + C::OFF_RS)[r] = scale;
+            }
+        };
         uint32_t n = 0;
         bool ok = true;
+        if (RT == 1 && p.left > 0)
+            fetch_q(p);
         if (p.left == 0) {   // whole units: an empty sequence
             const int h = p.ul % a.Hkv, row0 = p.ul / a.Hkv * a.rows, nrows = min(a.rows, a.M - row0);
             const long long grow = ((long long)p.b * a.Hq + h * a.G) * a.Tq + row0;
@@ -393,43 +449,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
             if (threadIdx.x == 0 && p.tile == 0 && p.ul == 0 && !a.whole)
                 a.where[1 + p.b] = t0 + (mine_all - p.left);
             const int row0 = rb * a.rows, nrows = min(a.rows, a.M - row0);
-            // ---- the unit's query rows: bf16, or f16 over the row's power of two with features in
-            // the order in which the codes of four neighbours come out of a register
             const long long grow = ((long long)p.b * a.Hq + h * a.G) * a.Tq + row0;   // first row of q and o
-            for (int r = warp; r < RT * 16; r += kMathWarps) {
-                uint32_t w[D / 64];
-                float big = 0.f;
-#pragma unroll
-                for (int i = 0; i < D / 64; ++i) {
-                    w[i] = r < nrows ? reinterpret_cast<const uint32_t *>(a.q + (grow + r) * D)[i * 32 + lane] : 0u;
-                    big = fmaxf(big, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xFFFF0000u))));
-                }
-                uint8_t *qr = smem + C::OFF_Q + r * C::QPITCH;
-                float scale = a.scale_log2;
-                if constexpr (FP8) {
-#pragma unroll
-                    for (int off = 16; off > 0; off >>= 1)
-                        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
-                    // 2^-e brings the row's largest value into [1, 4); zeros and infinities stay
-                    const int x = (int)(__float_as_uint(big) >> 23);
-                    const int e = x == 255 || x == 0 ? 0 : min(x - 127, 126);
-                    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-                    scale *= a.ks[h] / down;
-#pragma unroll
-                    for (int i = 0; i < D / 64; ++i) {
-                        const int f = i * 64 + 2 * lane, c = (f & 15) >> 2;   // features f, f + 1
-                        const int at = (f & ~15) + 2 * c + ((f & 2) ? 8 : 0);
-                        reinterpret_cast<uint32_t *>(qr)[at / 2] =
-                            pack_f16x2(__uint_as_float(w[i] << 16) * down, __uint_as_float(w[i] & 0xFFFF0000u) * down);
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < D / 64; ++i)
-                        reinterpret_cast<uint32_t *>(qr)[i * 32 + lane] = w[i];
-                }
-                if (lane == 0)
-                    reinterpret_cast<float *>(smem + C::OFF_RS)[r] = scale;
-            }
+            if constexpr (RT > 1)
+                fetch_q(p);
+            put_q();
             math_sync();
             uint32_t qf[QREG ? KSTEPS : 1][4];
             if constexpr (QREG) {
@@ -644,7 +667,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
             // the join's blocks may come now: earlier they would take registers that CTAs of the next
             // call want
             pdl_launch();
-            // ---- the warps' states of each row tile together, then out, 32 features at a time
+            // the next unit's query rows, under way while this one is put together
+            Place next = p;
+            next_unit(a, next, cnt);
+            if (RT == 1 && next.left > 0)
+                fetch_q(next);
+            // ---- the warps' states of each row tile together, then out, MR rows of each at a time
             const float s0 = quad_sum(l0[0] + l0[1]), s1 = quad_sum(l1[0] + l1[1]);
             if (c4 == 0) {
                 ml[warp * 16 + r0] = make_float2(m0, s0);
@@ -663,75 +691,65 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
             const bool whole = p.tile == 0 && cnt == p.nt;
             const long long slot = 2ll * blockIdx.x + (p.left == mine_all ? 0 : 1);
             float *part = a.part + slot * a.rows * (D + 2);
-            // a thread puts out four features of the same RT rows in every slice
             const float vs = FP8 ? a.vs[h] : 1.f;
-            float factor[RT];
+            constexpr int MR = C::MR;
+#pragma unroll 1
+            for (int first = 0; first < min(16, nrows); first += MR) {
+                if (r0 / MR == (first & 7) / MR) {
+                    float *mine = ob + (warp * MR + r0 % MR) * C::OPITCH;
+                    const bool low = first < 8;
+                    const float f = low ? f0 : f1;
 #pragma unroll
-            for (int e = 0; e < RT; ++e) {
-                const int row = (e * 128 + (int)threadIdx.x) >> 3;
-                const float t = top(row >> 4, row & 15);
-                float l = 0.f;
-#pragma unroll
-                for (int w = 0; w < KW; ++w) {
-                    const float2 y = ml[(w * RT + (row >> 4)) * 16 + (row & 15)];
-                    l = fmaf(y.y, weight(y.x, t), l);
-                }
-                factor[e] = whole ? (l == 0.f ? 0.f : vs / l) : vs;
-                if ((threadIdx.x & 7) == 0 && row < nrows && ok) {
-                    if (whole) {
-                        a.lse[grow + row] = l == 0.f ? -INFINITY : (t + log2f(l)) * 0.69314718055994530942f;
-                    } else {
-                        part[(long long)a.rows * D + row] = t;
-                        part[(long long)a.rows * (D + 1) + row] = l;
-                    }
-                }
-            }
-#pragma unroll
-            for (int sl = 0; sl < D / C::OC; ++sl) {
-                float *mine = ob + (warp * 16 + r0) * C::OPITCH;
-#pragma unroll
-                for (int x = 0; x < 4; x += 2) {
-                    const float(&p0)[4] = o[sl * 4 + x], (&p1)[4] = o[sl * 4 + x + 1];
-                    if constexpr (!FP8) {
-                        *reinterpret_cast<float2 *>(mine + 8 * x + 2 * c4) = make_float2(p0[0] * f0, p0[1] * f0);
-                        *reinterpret_cast<float2 *>(mine + 8 * x + 8 + 2 * c4) = make_float2(p1[0] * f0, p1[1] * f0);
-                        *reinterpret_cast<float2 *>(mine + 8 * C::OPITCH + 8 * x + 2 * c4) = make_float2(p0[2] * f1, p0[3] * f1);
-                        *reinterpret_cast<float2 *>(mine + 8 * C::OPITCH + 8 * x + 8 + 2 * c4) = make_float2(p1[2] * f1, p1[3] * f1);
-                    } else {   // even and odd features of a 16-feature unit
-                        *reinterpret_cast<float4 *>(mine + 8 * x + 4 * c4) = make_float4(p0[0] * f0, p1[0] * f0, p0[1] * f0, p1[1] * f0);
-                        *reinterpret_cast<float4 *>(mine + 8 * C::OPITCH + 8 * x + 4 * c4) =
-                            make_float4(p0[2] * f1, p1[2] * f1, p0[3] * f1, p1[3] * f1);
+                    for (int x = 0; x < D / 8; x += 2) {
+                        const float a0 = (low ? o[x][0] : o[x][2]) * f, a1 = (low ? o[x][1] : o[x][3]) * f;
+                        const float b0 = (low ? o[x + 1][0] : o[x + 1][2]) * f, b1 = (low ? o[x + 1][1] : o[x + 1][3]) * f;
+                        if constexpr (!FP8) {
+                            *reinterpret_cast<float2 *>(mine + 8 * x + 2 * c4) = make_float2(a0, a1);
+                            *reinterpret_cast<float2 *>(mine + 8 * x + 8 + 2 * c4) = make_float2(b0, b1);
+                        } else {   // even and odd features of a 16-feature unit
+                            *reinterpret_cast<float4 *>(mine + 8 * x + 4 * c4) = make_float4(a0, b0, a1, b1);
+                        }
                     }
                 }
                 math_sync();
 #pragma unroll
-                for (int e = 0; e < RT; ++e) {
-                    const int at = e * 128 + (int)threadIdx.x, row = at >> 3, col = (at & 7) * 4;
-                    const int rt_ = row >> 4, r = row & 15;
-                    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                    for (int w = 0; w < KW; ++w) {
-                        const float4 y = *reinterpret_cast<const float4 *>(ob + ((w * RT + rt_) * 16 + r) * C::OPITCH + col);
-                        x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
-                    }
+                for (int e = 0; e < RT; ++e) {   // four features of one row a thread: RT * MR rows of D
+                    const int at = e * 128 + (int)threadIdx.x, k = at / (D / 4), col = (at % (D / 4)) * 4;
+                    const int rt_ = k / MR, r = first + k % MR, row = rt_ * 16 + r;
                     if (row >= nrows || !ok)
                         continue;
-                    const float k = factor[e];
+                    const float t = top(rt_, r);
+                    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                    float l = 0.f;
+#pragma unroll
+                    for (int w = 0; w < KW; ++w) {
+                        const float4 y = *reinterpret_cast<const float4 *>(ob + ((w * RT + rt_) * MR + k % MR) * C::OPITCH + col);
+                        x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+                        const float2 z = ml[(w * RT + rt_) * 16 + r];
+                        l = fmaf(z.y, weight(z.x, t), l);
+                    }
+                    const float g = whole ? (l == 0.f ? 0.f : vs / l) : vs;
                     if (whole) {
                         uint2 y;
-                        y.x = pack_bf16x2(x.x * k, x.y * k);
-                        y.y = pack_bf16x2(x.z * k, x.w * k);
-                        *reinterpret_cast<uint2 *>(a.o + (grow + row) * D + sl * C::OC + col) = y;
+                        y.x = pack_bf16x2(x.x * g, x.y * g);
+                        y.y = pack_bf16x2(x.z * g, x.w * g);
+                        *reinterpret_cast<uint2 *>(a.o + (grow + row) * D + col) = y;
+                        if (col == 0)
+                            a.lse[grow + row] = l == 0.f ? -INFINITY : (t + log2f(l)) * 0.69314718055994530942f;
                     } else {
                         // 8-byte stores: a slot of `rows` (D + 2) floats is a multiple of 8 bytes
-                        float2 *dst = reinterpret_cast<float2 *>(part + (long long)row * D + sl * C::OC + col);
-                        dst[0] = make_float2(x.x * k, x.y * k);
-                        dst[1] = make_float2(x.z * k, x.w * k);
+                        float2 *dst = reinterpret_cast<float2 *>(part + (long long)row * D + col);
+                        dst[0] = make_float2(x.x * g, x.y * g);
+                        dst[1] = make_float2(x.z * g, x.w * g);
+                        if (col == 0) {
+                            part[(long long)a.rows * D + row] = t;
+                            part[(long long)a.rows * (D + 1) + row] = l;
+                        }
                     }
                 }
                 math_sync();
             }
-            next_unit(a, p, cnt);
+            p = next;
         }
     }
 }
@@ -757,81 +775,83 @@ __device__ __forceinline__ Parts parts_of(const PagedArgs &a, int b, int ul, int
     return p;
 }
 
-// Blocks [0, units * rows): o and lse of one row of a unit whose entries were split (or of a
-// sequence without any).  Blocks from there: kWeightRun entries' weights of one (sequence, KV head).
+// The first blocks: o and lse of rpb rows of a unit whose entries were split (or of a sequence
+// without any).  Blocks from there: kWeightRun entries' weights of one (sequence, KV head).
 // The states of a row are read by D / 2 threads a state, two features each, so that several are
 // under way at once.
 constexpr int kJoinThreads = 128, kWeightRun = 4 * kJoinThreads;
 constexpr int kMaxCtas = 3 * kSMs, kMaxParts = kMaxCtas;
 
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedArgs a, int wchunks)
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedArgs a, int wchunks, int rpb)
 {
     __shared__ float wt[kMaxParts], row_lse[kMaxRows], sums[kJoinThreads * 2], red[8];
     const int tid = threadIdx.x, per = a.Hkv * a.RB;
-    const long long rows_total = (long long)a.B * per * a.rows, blk = blockIdx.x;
+    const int bpu = (a.rows + rpb - 1) / rpb;   // blocks a unit
+    const long long rows_total = (long long)a.B * per * bpu, blk = blockIdx.x;
     const long long stride = (long long)a.rows * (D + 2);
     pdl_launch();
     pdl_wait();
     if (blk < rows_total) {
-        const int row = (int)(blk % a.rows);
-        const long long unit = blk / a.rows;
+        const long long unit = blk / bpu;
+        const int first = (int)(blk - unit * bpu) * rpb;
         const int b = (int)(unit / per), ul = (int)(unit - (long long)b * per), h = ul % a.Hkv, rb = ul / a.Hkv;
-        if (rb * a.rows + row >= a.M)
-            return;
         const Parts p = parts_of(a, b, ul, tiles_of(a, b));
         if (!p.none && p.c0 == p.c1)
             return;
-        const long long grow = ((long long)b * a.Hq + h * a.G) * a.Tq + rb * a.rows + row;
-        auto slot = [&](int i) { return a.part + (i == 0 ? p.s0 : 2ll * (p.c0 + i)) * stride; };
-        const int n = p.none ? 0 : p.c1 - p.c0 + 1;
-        // the states' maxima, then their weights
-        float m = -INFINITY, l = 0.f;
-        for (int i = tid; i < n; i += kJoinThreads) {
-            wt[i] = slot(i)[(long long)a.rows * D + row];
-            m = fmaxf(m, wt[i]);
-        }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1)
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-        if (lane_id() == 0)
-            red[warp_id()] = m;
-        __syncthreads();
-        m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-        for (int i = tid; i < n; i += kJoinThreads) {
-            const float w = wt[i] == -INFINITY ? 0.f : ex2_approx(wt[i] - m);
-            l = fmaf(w, slot(i)[(long long)a.rows * (D + 1) + row], l);
-            wt[i] = w;
-        }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1)
-            l += __shfl_xor_sync(0xffffffffu, l, off);
-        if (lane_id() == 0)
-            red[4 + warp_id()] = l;
-        __syncthreads();
-        l = (red[4] + red[5]) + (red[6] + red[7]);
-        constexpr int GROUPS = 2 * kJoinThreads / D;   // states under way
-        const int g = tid / (D / 2), f = 2 * (tid % (D / 2));
-        float2 x = make_float2(0.f, 0.f);
-#pragma unroll 8
-        for (int i = g; i < n; i += GROUPS) {
-            const float2 y = *reinterpret_cast<const float2 *>(slot(i) + (long long)row * D + f);
-            x.x = fmaf(wt[i], y.x, x.x);
-            x.y = fmaf(wt[i], y.y, x.y);
-        }
-        reinterpret_cast<float2 *>(sums)[tid] = x;
-        __syncthreads();
-        if (g == 0) {
-#pragma unroll
-            for (int w = 1; w < GROUPS; ++w) {
-                const float2 y = reinterpret_cast<const float2 *>(sums)[w * (D / 2) + tid];
-                x.x += y.x;
-                x.y += y.y;
+        for (int row = first; row < min(first + rpb, min(a.rows, a.M - rb * a.rows)); ++row) {
+            const long long grow = ((long long)b * a.Hq + h * a.G) * a.Tq + rb * a.rows + row;
+            auto slot = [&](int i) { return a.part + (i == 0 ? p.s0 : 2ll * (p.c0 + i)) * stride; };
+            const int n = p.none ? 0 : p.c1 - p.c0 + 1;
+            // the states' maxima, then their weights
+            float m = -INFINITY, l = 0.f;
+            for (int i = tid; i < n; i += kJoinThreads) {
+                wt[i] = slot(i)[(long long)a.rows * D + row];
+                m = fmaxf(m, wt[i]);
             }
-            const float k = l == 0.f ? 0.f : 1.f / l;
-            *reinterpret_cast<uint32_t *>(a.o + grow * D + f) = pack_bf16x2(x.x * k, x.y * k);
-            if (tid == 0)
-                a.lse[grow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1)
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+            if (lane_id() == 0)
+                red[warp_id()] = m;
+            __syncthreads();
+            m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+            for (int i = tid; i < n; i += kJoinThreads) {
+                const float w = wt[i] == -INFINITY ? 0.f : ex2_approx(wt[i] - m);
+                l = fmaf(w, slot(i)[(long long)a.rows * (D + 1) + row], l);
+                wt[i] = w;
+            }
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1)
+                l += __shfl_xor_sync(0xffffffffu, l, off);
+            if (lane_id() == 0)
+                red[4 + warp_id()] = l;
+            __syncthreads();
+            l = (red[4] + red[5]) + (red[6] + red[7]);
+            constexpr int GROUPS = 2 * kJoinThreads / D;   // states under way
+            const int g = tid / (D / 2), f = 2 * (tid % (D / 2));
+            float2 x = make_float2(0.f, 0.f);
+#pragma unroll 8
+            for (int i = g; i < n; i += GROUPS) {
+                const float2 y = *reinterpret_cast<const float2 *>(slot(i) + (long long)row * D + f);
+                x.x = fmaf(wt[i], y.x, x.x);
+                x.y = fmaf(wt[i], y.y, x.y);
+            }
+            reinterpret_cast<float2 *>(sums)[tid] = x;
+            __syncthreads();
+            if (g == 0) {
+#pragma unroll
+                for (int w = 1; w < GROUPS; ++w) {
+                    const float2 y = reinterpret_cast<const float2 *>(sums)[w * (D / 2) + tid];
+                    x.x += y.x;
+                    x.y += y.y;
+                }
+                const float k = l == 0.f ? 0.f : 1.f / l;
+                *reinterpret_cast<uint32_t *>(a.o + grow * D + f) = pack_bf16x2(x.x * k, x.y * k);
+                if (tid == 0)
+                    a.lse[grow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
+            }
+            __syncthreads();   // before the next row's states
         }
         return;
     }
@@ -964,10 +984,13 @@ int paged_run(const fa_kv_cache &c, PagedArgs &a, cudaStream_t s)
     if (a.whole && most > 0)
         return OK;
     const int wchunks = a.scores ? (a.cap + kWeightRun - 1) / kWeightRun : 0;
-    const long long blocks = (long long)a.B * a.Hkv * a.RB * a.rows + (long long)a.B * a.Hkv * wchunks;
+    // rows a block: one, unless that makes more blocks than the device holds at a time
+    const long long units = (long long)a.B * a.Hkv * a.RB, held = 8 * kSMs;
+    const int rpb = (int)std::min<long long>(a.rows, (units * a.rows + held - 1) / held);
+    const long long blocks = units * ((a.rows + rpb - 1) / rpb) + (long long)a.B * a.Hkv * wchunks;
     if (blocks > INT_MAX)
         return ERR_UNSUPPORTED;
-    return launch_overlapped(paged_join_kernel<D>, dim3((unsigned)blocks), kJoinThreads, 0, 0, true, s, a, wchunks);
+    return launch_overlapped(paged_join_kernel<D>, dim3((unsigned)blocks), kJoinThreads, 0, 0, true, s, a, wchunks, rpb);
 }
 
 }  // namespace
