@@ -88,7 +88,7 @@ struct PagedArgs {
     float *part;     // [2 grid][rows][D] then m, l [rows]
     long long *where;   // [0] the share, [1 + b] the first tile of sequence b (not of an empty one)
     float *scores;   // [sequence][KV head][row][cap]
-    int B, Hq, Hkv, G, Tq, M, rows, RB, causal, num_pages, max_pages, ps_shift, cap, grid, whole, kt;
+    int B, Hq, Hkv, G, Tq, M, rows, RB, causal, num_pages, max_pages, ps_shift, cap, grid, whole, may_whole, kt;
     float scale_log2;
     uint64_t timeout_ns;
 };
@@ -200,25 +200,44 @@ __device__ __forceinline__ long long warp_scan(long long x)   // sum over the la
 // Finds the CTA's place; p.left: its tiles, 0 if there is nothing for it.  Every warp does it for
 // itself: the loads of the others are in the same cache lines, and a block-wide sum would cost
 // barriers at a time when nothing is under way.
-__device__ __forceinline__ Place place_of(const PagedArgs &a, long long &share, long long &t0)
+// whole: every unit is one CTA's, because there are enough CTAs and the longest unit is at most a
+// quarter and 4 tiles longer than an equal share: a CTA whose neighbours have ended gets more of the
+// bandwidth, and there are no second units to start and nothing to join (256 units of 1024, 2048 and
+// 4096 entries, d 128: 26.5, 45.3 and 83.4 us against 30.8, 50.2 and 89.2; but 144 units of 1000 to 3000,
+// d 256, half longer than a share: 61.6 against 56.1).
+__device__ __forceinline__ Place place_of(const PagedArgs &a, long long &share, long long &t0, bool &whole)
 {
     const int per = a.Hkv * a.RB, lane = (int)lane_id();
     const int nt0 = lane < a.B ? tiles_of(a, lane) : 0;
     const long long inc0 = warp_scan((long long)nt0 * per);
     long long total = __shfl_sync(0xffffffffu, inc0, 31);
+    int longest = nt0;
     if (a.B > 32) {
         long long x = 0;
 #pragma unroll 4
-        for (int b = 32 + lane; b < a.B; b += 32)
-            x += tiles_of(a, b);
+        for (int b = 32 + lane; b < a.B; b += 32) {
+            const int nt = tiles_of(a, b);
+            x += nt;
+            longest = max(longest, nt);
+        }
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1)
             x += __shfl_xor_sync(0xffffffffu, x, off);
         total += x * per;
     }
+    longest = __reduce_max_sync(0xffffffffu, longest);
     share = total < INT_MAX ? share_of(a, (int)total) : share_of(a, total);
-    t0 = share * blockIdx.x;
     Place p{a.B, 0, 0, 0, 0};
+    if (a.may_whole && longest <= share + share / 4 + 4) {
+        whole = true;
+        if ((int)blockIdx.x < a.B * per) {
+            p.b = (int)blockIdx.x / per;
+            p.ul = (int)blockIdx.x - p.b * per;
+            p.left = p.nt = tiles_of(a, p.b);
+        }
+        return p;
+    }
+    t0 = share * blockIdx.x;
     if (t0 >= total)
         return p;
     p.left = min(share, total - t0);
@@ -264,6 +283,38 @@ __device__ __forceinline__ void next_unit(const PagedArgs &a, Place &p, int done
     }
 }
 
+// sum + the probabilities 2^{s - lse} of four neighbouring entries over nrows rows of stored scores
+// (which reach to the end of the last group of 16 entries); `last`: adds them to the weights at
+// `at`, of which `left` or more are entries.
+__device__ __forceinline__ float4 add_weights(const PagedArgs &a, long long at, int left, const float *sp, int nrows,
+                                              const float *row_lse, float4 sum, bool last)
+{
+#pragma unroll 4
+    for (int r = 0; r < nrows; ++r) {
+        const float4 s = *reinterpret_cast<const float4 *>(sp + (long long)r * a.cap);
+        const float y = row_lse[r];
+        sum.x += ex2_approx(s.x - y);
+        sum.y += ex2_approx(s.y - y);
+        sum.z += ex2_approx(s.z - y);
+        sum.w += ex2_approx(s.w - y);
+    }
+    if (!last)
+        return sum;
+    float *w = a.weight + at;
+    if (left >= 4) {
+        float4 x = *reinterpret_cast<const float4 *>(w);
+        x.x += sum.x, x.y += sum.y, x.z += sum.z, x.w += sum.w;
+        *reinterpret_cast<float4 *>(w) = x;
+    } else {
+        w[0] += sum.x;
+        if (left > 1)
+            w[1] += sum.y;
+        if (left > 2)
+            w[2] += sum.z;
+    }
+    return sum;
+}
+
 // ------------------------------------------------------------------ attention
 template <int D, bool FP8, int RT>
 __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
@@ -295,20 +346,20 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
     }
     pdl_wait();
     Place p;
-    long long share = 0, t0 = 0, mine_all;   // mine_all: tiles of this CTA
-    if (a.whole) {                           // one unit a CTA, however long
+    long long share = 0, t0 = 0;
+    bool whole = a.whole;
+    if (whole) {   // one unit a CTA, however long
         const int per = a.Hkv * a.RB, b = (int)blockIdx.x / per;
         const int nt = tiles_of(a, b);
         p = Place{b, (int)blockIdx.x - b * per, 0, nt, nt};
-        mine_all = nt;
     } else {
-        p = place_of(a, share, t0);
+        p = place_of(a, share, t0, whole);
         if (threadIdx.x == 0 && blockIdx.x == 0)
-            a.where[0] = share;
-        if (p.left == 0)
+            a.where[0] = whole ? 0 : share;
+        if (p.left == 0 && !(whole && p.b < a.B))
             return;   // the whole CTA
-        mine_all = p.left;
     }
+    const long long mine_all = p.left;   // tiles of this CTA
     __syncthreads();   // the barriers are there
     // rows of a page in one box, and boxes of a tile
     const int bp_shift = a.ps_shift < 6 ? a.ps_shift : 6, boxes = C::KT >> bp_shift;
@@ -368,7 +419,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
     } else {
         // ---------------------------------------------------------- math
         const int rt = warp % RT, kw = warp / RT, c4 = lane & 3, r0 = lane >> 2;
+        // the rows' scales; once they are read, the place of the rows' lse
         const float *rs = reinterpret_cast<const float *>(smem + C::OFF_RS);
+        float *row_lse = reinterpret_cast<float *>(smem + C::OFF_RS);
         float2 *ml = reinterpret_cast<float2 *>(smem + C::OFF_ML);
         float *ob = reinterpret_cast<float *>(smem + C::OFF_O);
         constexpr int GP = C::GP;
@@ -446,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
         }
         while (p.left > 0) {
             const int len = length_of(a, p.b), h = p.ul % a.Hkv, rb = p.ul / a.Hkv, cnt = segment(p);
-            if (threadIdx.x == 0 && p.tile == 0 && p.ul == 0 && !a.whole)
+            if (threadIdx.x == 0 && p.tile == 0 && p.ul == 0 && !whole)
                 a.where[1 + p.b] = t0 + (mine_all - p.left);
             const int row0 = rb * a.rows, nrows = min(a.rows, a.M - row0);
             const long long grow = ((long long)p.b * a.Hq + h * a.G) * a.Tq + row0;   // first row of q and o
@@ -688,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
             };
             auto weight = [](float m, float t) { return m == -INFINITY ? 0.f : ex2_approx(m - t); };
             const float f0 = weight(m0, top(rt, r0)), f1 = weight(m1, top(rt, r0 + 8));
-            const bool whole = p.tile == 0 && cnt == p.nt;
+            const bool entire = p.tile == 0 && cnt == p.nt;   // all of the unit
             const long long slot = 2ll * blockIdx.x + (p.left == mine_all ? 0 : 1);
             float *part = a.part + slot * a.rows * (D + 2);
             const float vs = FP8 ? a.vs[h] : 1.f;
@@ -728,14 +781,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
                         const float2 z = ml[(w * RT + rt_) * 16 + r];
                         l = fmaf(z.y, weight(z.x, t), l);
                     }
-                    const float g = whole ? (l == 0.f ? 0.f : vs / l) : vs;
-                    if (whole) {
+                    const float g = entire ? (l == 0.f ? 0.f : vs / l) : vs;
+                    if (entire) {
                         uint2 y;
                         y.x = pack_bf16x2(x.x * g, x.y * g);
                         y.y = pack_bf16x2(x.z * g, x.w * g);
                         *reinterpret_cast<uint2 *>(a.o + (grow + row) * D + col) = y;
-                        if (col == 0)
-                            a.lse[grow + row] = l == 0.f ? -INFINITY : (t + log2f(l)) * 0.69314718055994530942f;
+                        if (col == 0) {
+                            const float y = t + log2f(l);   // -inf if l is 0
+                            a.lse[grow + row] = l == 0.f ? -INFINITY : y * 0.69314718055994530942f;
+                            row_lse[row] = l == 0.f ? 0.f : y;   // a row that saw nothing has no finite score either
+                        }
                     } else {
                         // 8-byte stores: a slot of `rows` (D + 2) floats is a multiple of 8 bytes
                         float2 *dst = reinterpret_cast<float2 *>(part + (long long)row * D + col);
@@ -749,6 +805,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
                 }
                 math_sync();
             }
+            // ---- one CTA has the whole unit, its scores too: weight_j += sum over the rows of
+            // p_j = 2^{s_j - lse}, four neighbours a thread
+            if (whole && a.scores && ok)
+                for (int j = 4 * (int)threadIdx.x; j < len; j += 4 * 32 * kMathWarps)
+                    add_weights(a, ((long long)p.b * a.Hkv + h) * a.cap + j, len - j,
+                                a.scores + ((long long)p.b * a.Hkv + h) * a.M * a.cap + j, nrows, row_lse,
+                                make_float4(0.f, 0.f, 0.f, 0.f), true);
             p = next;
         }
     }
@@ -792,6 +855,8 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
     const long long stride = (long long)a.rows * (D + 2);
     pdl_launch();
     pdl_wait();
+    if (a.may_whole && a.where[0] == 0)
+        return;   // whole units: nothing is left to do
     if (blk < rows_total) {
         const long long unit = blk / bpu;
         const int first = (int)(blk - unit * bpu) * rpb;
@@ -885,34 +950,10 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
             row_lse[r] = y == -INFINITY ? 0.f : y;
         }
         __syncthreads();
-        // the stored scores reach to the end of the last group of 16 entries
-        if (j < len) {
-            const float *sp = a.scores + (uh * a.M + row0) * a.cap + j;
-#pragma unroll 4
-            for (int r = 0; r < nrows; ++r) {
-                const float4 s = *reinterpret_cast<const float4 *>(sp + (long long)r * a.cap);
-                const float y = row_lse[r];
-                sum.x += ex2_approx(s.x - y);
-                sum.y += ex2_approx(s.y - y);
-                sum.z += ex2_approx(s.z - y);
-                sum.w += ex2_approx(s.w - y);
-            }
-        }
+        if (j < len)
+            sum = add_weights(a, uh * a.cap + j, len - j, a.scores + (uh * a.M + row0) * a.cap + j, nrows, row_lse, sum,
+                              rb == a.RB - 1);
         __syncthreads();
-    }
-    if (j >= len)
-        return;
-    float *w = a.weight + uh * a.cap + j;
-    if (j + 4 <= len) {
-        float4 x = *reinterpret_cast<const float4 *>(w);
-        x.x += sum.x, x.y += sum.y, x.z += sum.z, x.w += sum.w;
-        *reinterpret_cast<float4 *>(w) = x;
-    } else {
-        w[0] += sum.x;
-        if (j + 1 < len)
-            w[1] += sum.y;
-        if (j + 2 < len)
-            w[2] += sum.z;
     }
 }
 
@@ -923,7 +964,9 @@ int rows_of(int M) { return M < kMaxRows ? M : kMaxRows; }
 int row_tiles(int M) { return M <= 16 ? 1 : M <= 32 ? 2 : 4; }
 
 
-// Tables of up to this many slots: one CTA a unit and no join.
+// Tables of up to this many slots (half at d 256): one CTA a unit and no join.  8 units of 256, 512 and
+// 1024 entries, d 128: 5.7, 8.5 and 13.9 us against 8.2, 8.5 and 8.9 in shares; d 256: 7.6, 11.7 and
+// 20.0 against 9.4, 10.2 and 9.9.
 constexpr int kWholeSlots = 512;
 
 size_t where_bytes(int B) { return round256((size_t)(B + 1) * sizeof(long long)); }
@@ -960,6 +1003,7 @@ int paged_run(const fa_kv_cache &c, PagedArgs &a, cudaStream_t s)
     a.kt = f8 ? Cfg<D, true, 1>::KT : Cfg<D, false, 1>::KT;
     a.grid = kSMs * (rt == 1 ? (f8 ? Cfg<D, true, 1>::CTAS : Cfg<D, false, 1>::CTAS) : f8 ? Cfg<D, true, 2>::CTAS : Cfg<D, false, 2>::CTAS);
     const long long most = (long long)a.B * a.Hkv * a.RB * ((a.cap + a.kt - 1) / a.kt);   // tiles, at most
+    a.may_whole = a.may_whole && most > 0 && (long long)a.B * a.Hkv * a.RB <= a.grid;
     int st = OK;
     if (most > 0) {
         CUtensorMap tk, tv;
@@ -1027,7 +1071,10 @@ int paged_launch(const fa_kv_cache &c, const void *q, void *o, float *lse, int H
     while ((1 << a.ps_shift) < c.page_size)
         ++a.ps_shift;
     a.cap = c.num_pages > 0 ? c.max_pages * c.page_size : 0;   // no pages: every length above 0 is out of range
-    a.whole = !accumulate && a.cap <= kWholeSlots;
+    // several row blocks of a unit: only the join can add their weights
+    const bool can = !accumulate || a.RB == 1;
+    a.whole = can && a.cap <= (c.d == 256 ? kWholeSlots / 2 : kWholeSlots);
+    a.may_whole = can;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     a.where = reinterpret_cast<long long *>(ws);
     a.part = reinterpret_cast<float *>(ws + where_bytes(c.B));
