@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
     using C = Cfg<D, FP8, RT>;
     constexpr int KW = kMathWarps / RT;             // warps that share a row tile's entries
     constexpr int KSTEPS = D / 16;                  // products along the head width, per 8 entries
-    constexpr bool QREG = D <= 64;                  // query fragments stay in registers
+    constexpr bool QREG = D <= 64 && !(FP8 && RT == 1);                  // query fragments stay in registers
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t sbase = (raw + 1023u) & ~1023u;
