@@ -455,15 +455,14 @@ __device__ __forceinline__ int block_rank(bool p, int &total, int *scratch)
 // CTA lists; then the cluster's threads take hole and entry number g from whichever CTAs list them.
 // It is bound by latency, a chain of a dozen block- and cluster-wide steps, and not by its 20 bytes
 // an entry; what an entry that stays in its slot needs (kept, weight, order) is written when it is
-// read.  64 units of 4112 entries, and 32 of 9001 to 32768 with the rows' moves (17 us):
-//     threads a CTA      256, 4 and 8 CTAs a unit   512, 2 and 8   1024, 2 and 4
-//     us                 15.7 and 36.6              14.7 and 35.0  15.8 and 34.9
+// read.  With 512 threads a CTA the selection of 64 units of 4112 entries and of 32 of up to 32768 took 14.7
+// and 18 us, with 256 15.7 and 19.5, with 1024 15.8 and 18.  The cluster then moves the rows itself:
+// a second kernel for them cost 3 us more.
 constexpr int kPickThreads = 512;
 constexpr int kSelBins = 256, kSelPasses = 4;
 constexpr int kSelCap = 32768;                               // entries a CTA, at most (their numbers take 16 bits)
 constexpr int kSelCopies = 8;                                // of the first pass's counts: most ranks share a few digits
 constexpr int kSelFixed = (kSelPasses + kSelCopies) * kSelBins * 4 + 32 * 4 + 32;   // shared memory besides the entries
-constexpr int kFewMoves = 128;                               // moved rows that the selection copies itself
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
@@ -505,6 +504,12 @@ __device__ __forceinline__ int block_scan(int x, int &total, int *scratch)
     return __reduce_add_sync(0xffffffffu, lane_id() < warp_id() ? c : 0) + inc - x;
 }
 
+// The length after eviction; one out of range stays as it is.
+__device__ __forceinline__ int new_length(const EvictArgs &a, int len)
+{
+    return len < 0 || len > a.cap ? len : min(len, a.budget);
+}
+
 // Byte offset of a slot's row in the pools, -1 if its page is out of range.
 __device__ __forceinline__ long long row_of(const EvictArgs &a, int b, int h, int slot)
 {
@@ -514,9 +519,59 @@ __device__ __forceinline__ long long row_of(const EvictArgs &a, int b, int h, in
     return ((((long long)page * a.Hkv + h) << a.ps_shift) + (slot & ((1 << a.ps_shift) - 1))) * a.row_bytes;
 }
 
-__global__ void __launch_bounds__(kPickThreads) evict_select_kernel(const __grid_constant__ EvictArgs a, int cs, int per, int few)
+// Copies the K and V rows of `n` moves (byte offsets from, to), one warp, eight 16-byte loads in
+// flight a lane.  Sources lie behind the new length and targets in front of it.
+__device__ __forceinline__ void copy_rows(const EvictArgs &a, const long long (*moves)[2], int n)
+{
+    const int vshift = 31 - __clz(a.row_bytes / 16), vecs = 1 << vshift;   // 16-byte vectors of a row
+    const int count = n << (vshift + 1);                                   // of K and V
+    for (int e0 = (int)lane_id(); e0 < count; e0 += 32 * 8) {
+        uint4 x[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int e = e0 + 32 * u;
+            if (e < count)
+                x[u] = *reinterpret_cast<const uint4 *>((e & vecs ? a.v : a.k) + moves[e >> (vshift + 1)][0] + (e & (vecs - 1)) * 16);
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int e = e0 + 32 * u;
+            if (e < count)
+                *reinterpret_cast<uint4 *>((e & vecs ? a.v : a.k) + moves[e >> (vshift + 1)][1] + (e & (vecs - 1)) * 16) = x[u];
+        }
+    }
+}
+
+// Lists the moves of a warp's lanes (from < 0: none) and copies them.
+__device__ __forceinline__ void move_rows(const EvictArgs &a, long long (*moves)[2], long long from, long long to)
+{
+    const uint32_t todo = __ballot_sync(0xffffffffu, from >= 0);
+    if (from >= 0) {
+        const int r = __popc(todo & ((1u << lane_id()) - 1u));
+        moves[r][0] = from;
+        moves[r][1] = to;
+    }
+    __syncwarp();
+    copy_rows(a, moves, __popc(todo));
+    __syncwarp();
+}
+
+// Byte offsets of a move's rows; from < 0 if a page is out of range.
+__device__ __forceinline__ void move_of(const EvictArgs &a, int b, int h, int i, int j, long long &from, long long &to)
+{
+    from = row_of(a, b, h, i);
+    to = row_of(a, b, h, j);
+    if (from < 0 || to < 0) {
+        atomicCAS(&g_cache_status, 0, kStatusBadIndex);
+        from = -1;
+    }
+}
+
+__global__ void __launch_bounds__(kPickThreads) evict_select_kernel(const __grid_constant__ EvictArgs a, int cs, int per)
 {
     constexpr int T = kPickThreads;
+    __shared__ long long moves[T / 32][32][2];
+    __shared__ int lists[8];   // of each CTA: holes in the low half, entries behind the new length in the high half
     extern __shared__ __align__(16) int sel_smem[];
     int *copies = sel_smem, *hist = copies + kSelCopies * kSelBins, *scratch = hist + kSelPasses * kSelBins;
     int *share = scratch + 32, *pick = share + 4;
@@ -537,8 +592,8 @@ __global__ void __launch_bounds__(kPickThreads) evict_select_kernel(const __grid
         atomicCAS(&g_cache_status, 0, kStatusBadIndex);
     for (int j = end + rank * T + tid; j < a.budget; j += cs * T)
         kept[j] = -1;
-    if (few && h == 0 && rank == 0 && tid == 0 && a.lens_out != a.lens)
-        a.lens_out[b] = min(len, a.budget);
+    if (h == 0 && rank == 0 && tid == 0 && a.lens_out != a.lens)
+        a.lens_out[b] = new_length(a, len);
     if (bad)
         return;   // the whole cluster
     const float *weight = a.weight + base;
@@ -661,70 +716,44 @@ __global__ void __launch_bounds__(kPickThreads) evict_select_kernel(const __grid
         share[0] = total;
     cluster_arrive();
     cluster_wait();
-    int holes[8], moved[8], all = 0;
-#pragma unroll
-    for (int r = 0; r < 8; ++r) {
-        const int x = r < cs ? cluster_load(share, r) : 0;
-        holes[r] = x & 0xFFFF;
-        moved[r] = x >> 16;
-        all += holes[r];
-    }
-    // hole and mover number g of the cluster, over all its threads; the lanes of a warp stay
-    // together, for it copies whole rows
-    for (int g0 = (rank * T + tid) & ~31; g0 < all; g0 += cs * T) {
+    if (tid < 8)
+        lists[tid] = tid < cs ? cluster_load(share, tid) : 0;
+    __syncthreads();
+    int all = 0;
+    for (int r = 0; r < cs; ++r)
+        all += lists[r] & 0xFFFF;
+    // hole and entry number g of the cluster; each of its warps takes up to 32 of them
+    const int warps = cs * T / 32, chunk = min(32, (all + warps - 1) / warps);
+    for (int g0 = (rank * (T / 32) + (int)warp_id()) * chunk; g0 < all; g0 += warps * chunk) {
         const int g = g0 + (int)lane_id();
         long long from = -1, to = -1;
-        if (g < all) {
+        if ((int)lane_id() < chunk && g < all) {
             int r = 0, m = g, c = 0, x = g;   // the CTAs that list them, and their places there
-#pragma unroll
-            for (int k = 0; k < 7; ++k) {
-                const bool past = r == k && m >= holes[k];
-                m -= past ? holes[k] : 0;
-                r += past;
-                const bool over = c == k && x >= moved[k];
-                x -= over ? moved[k] : 0;
-                c += over;
-            }
-            int skip = 0;   // holes of CTA c, in front of its movers
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                skip = c == k ? holes[k] : skip;
+            while (m >= (lists[r] & 0xFFFF))
+                m -= lists[r++] & 0xFFFF;
+            while (x >= lists[c] >> 16)
+                x -= lists[c++] >> 16;
             const int j = r * per + cluster_load16(list + m, r);
-            const int i = c * per + cluster_load16(list + skip + x, c);
+            const int i = c * per + cluster_load16(list + (lists[c] & 0xFFFF) + x, c);
             kept[j] = i;
             a.weight_out[base + j] = weight[i];
             if (order)
                 a.order_out[base + j] = order[i];
-            if (few) {
-                from = row_of(a, b, h, i);
-                to = row_of(a, b, h, j);
-                if (from < 0 || to < 0) {
-                    atomicCAS(&g_cache_status, 0, kStatusBadIndex);
-                    from = -1;
-                }
-            }
+            move_of(a, b, h, i, j, from, to);
         }
-        for (uint32_t todo = __ballot_sync(0xffffffffu, from >= 0); todo; todo &= todo - 1) {
-            const int l = __ffs(todo) - 1, vecs = a.row_bytes / 16;
-            const long long f = __shfl_sync(0xffffffffu, from, l), t = __shfl_sync(0xffffffffu, to, l);
-            for (int e = (int)lane_id(); e < 2 * vecs; e += 32) {
-                uint8_t *pool = e < vecs ? a.k : a.v;
-                const int o = (e < vecs ? e : e - vecs) * 16;
-                *reinterpret_cast<uint4 *>(pool + t + o) = *reinterpret_cast<const uint4 *>(pool + f + o);
-            }
-        }
+        move_rows(a, moves[warp_id()], from, to);
     }
     cluster_arrive();   // no CTA ends while another may read its list
     cluster_wait();
 }
 
-// lens_out = min(lens, budget), where the selection copied the rows and lens_out is lens.
+// The lengths, where lens_out is lens, which every CTA of the selection reads.
 __global__ void __launch_bounds__(256) evict_lens_kernel(const __grid_constant__ EvictArgs a)
 {
     pdl_launch();
     pdl_wait();
     for (int b = blockIdx.x * 256 + threadIdx.x; b < a.B; b += gridDim.x * 256)
-        a.lens_out[b] = min(a.lens[b], a.budget);
+        a.lens_out[b] = new_length(a, a.lens[b]);
 }
 
 // The same for lengths whose ranks do not fit the shared memory of a cluster: one CTA per
@@ -847,61 +876,23 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_long_kernel(const __
     }
 }
 
-// Rows of the moved entries: each warp takes 32 entries of one (sequence, KV head), lists those
-// that moved and copies their K and V rows, eight 16-byte loads in flight a lane.  Sources lie
-// behind the new length and targets in front of it.
+// Rows of the moved entries after the selection of long lengths: each warp takes 32 entries of one
+// (sequence, KV head).
 __global__ void __launch_bounds__(256) evict_move_kernel(const __grid_constant__ EvictArgs a)
 {
-    __shared__ long long list[8][32][2];
-    const int unit = blockIdx.x, b = unit / a.Hkv, h = unit - b * a.Hkv, lane = threadIdx.x & 31;
-    long long(*moves)[2] = list[threadIdx.x >> 5];
+    __shared__ long long moves[8][32][2];
+    const int unit = blockIdx.x, b = unit / a.Hkv, h = unit - b * a.Hkv;
     pdl_launch();
     pdl_wait();
-    if (blockIdx.y == 0 && h == 0 && threadIdx.x == 0) {
-        const int len = a.lens[b];
-        a.lens_out[b] = min(len, a.budget);
-    }
-    const int vshift = 31 - __clz(a.row_bytes / 16), vecs = 1 << vshift;   // 16-byte vectors of a row
-    for (int j0 = (blockIdx.y * 8 + (threadIdx.x >> 5)) * 32; j0 < a.budget; j0 += gridDim.y * 256) {
-        const int j = j0 + lane;
+    if (blockIdx.y == 0 && h == 0 && threadIdx.x == 0)
+        a.lens_out[b] = new_length(a, a.lens[b]);
+    for (int j0 = (blockIdx.y * 8 + (int)warp_id()) * 32; j0 < a.budget; j0 += gridDim.y * 256) {
+        const int j = j0 + (int)lane_id();
         const int i = j < a.budget ? a.kept[(long long)unit * a.budget + j] : -1;
         long long from = -1, to = -1;
-        if (i >= 0 && i != j) {
-            from = row_of(a, b, h, i);
-            to = row_of(a, b, h, j);
-            if (from < 0 || to < 0) {
-                atomicCAS(&g_cache_status, 0, kStatusBadIndex);
-                from = -1;
-            }
-        }
-        const uint32_t todo = __ballot_sync(0xffffffffu, from >= 0);
-        if (from >= 0) {
-            const int r = __popc(todo & ((1u << lane) - 1u));
-            moves[r][0] = from;
-            moves[r][1] = to;
-        }
-        __syncwarp();
-        const int count = __popc(todo) << (vshift + 1);   // vectors of K and V
-        for (int e0 = lane; e0 < count; e0 += 32 * 8) {
-            uint4 x[8];
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const int e = e0 + 32 * u;
-                if (e < count) {
-                    const int m = e >> (vshift + 1), o = e & (vecs - 1);
-                    x[u] = *reinterpret_cast<const uint4 *>((e & vecs ? a.v : a.k) + moves[m][0] + o * 16);
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const int e = e0 + 32 * u;
-                if (e < count) {
-                    const int m = e >> (vshift + 1), o = e & (vecs - 1);
-                    *reinterpret_cast<uint4 *>((e & vecs ? a.v : a.k) + moves[m][1] + o * 16) = x[u];
-                }
-            }
-        }
-        __syncwarp();
+        if (i >= 0 && i != j)
+            move_of(a, b, h, i, j, from, to);
+        move_rows(a, moves[warp_id()], from, to);
     }
 }
 
@@ -1014,35 +1005,38 @@ int evict_launch(const fa_kv_cache &c, int budget, int n_first, int n_recent, fl
     a.ps_shift = shift_of(c.page_size);
     a.row_bytes = c.d * (c.dtype == FA_E4M3 ? 1 : 2);
     const int units = c.B * c.Hkv;
-    // CTAs per (sequence, KV head): 2048 entries or more each, all of them resident (two an SM); with
-    // half as many, and twice as many, 15.9 and 16.2 us for 64 units of 4112 entries instead of
-    // 14.7, and 37.0 for 32 units of up to 32768 instead of 35.0
+    // CTAs per (sequence, KV head): as many as there are SMs for, with 512 entries or more each (the
+    // rows are moved by as many), or two an SM with 2048 or more.  us with 1, 2, 4 and 8 of them:
+    //   64 units of 4112 entries, 16 evicted                   13.2  12.1  14.4  29.5   (2)
+    //   32 units of up to 32768, 4096 stay                    110    55.0  37.3  32.1   (8)
+    //   1 unit of 5935, d 256, 3851 stay                       42.2  29.1  16.8  13.3   (8)
+    //   256 units of 2100, 2000 stay                           14.7  23.2  42.8  80.1   (1)
     int cs = 1;
-    while (cs < 8 && a.cap / (2 * cs) >= 2048 && (long long)units * cs <= device_sm_count())
+    auto worth = [&](int n) {
+        return (long long)units * n <= device_sm_count() ? a.cap / n >= 512
+                                                         : (long long)units * n <= 2 * device_sm_count() && a.cap / n >= 2048;
+    };
+    while (cs < 8 && worth(2 * cs))
         cs *= 2;
     while (cs < 8 && (a.cap + cs - 1) / cs > kSelCap)
         cs *= 2;
     const int per = (a.cap + cs - 1) / cs;
     const bool wide = per <= kSelCap && (long long)units * cs <= INT_MAX;
-    const int few = wide && a.cap - budget <= kFewMoves;
-    int st;
     if (wide) {
         if (cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  kSelFixed + kSelCap * 6) != cudaSuccess)
             return ERR_CUDA;
-        // after the kernel before it: clusters that wait on the SMs delay the moves of the call before
-        // (20 us instead of 16.5 for the first case)
-        st = launch_overlapped(evict_select_kernel, dim3((unsigned)(units * cs)), kPickThreads, kSelFixed + per * 6, cs, false,
-                               s, a, cs, per, few);
-    } else {
-        st = launch_overlapped(evict_select_long_kernel, dim3((unsigned)units), kSelThreads, 0, 0, false, s, a);
+        // not overlapped with the kernel before it: clusters that wait on the SMs were in its way (20 us
+        // instead of 16.5 for the first case above)
+        const int st = launch_overlapped(evict_select_kernel, dim3((unsigned)(units * cs)), kPickThreads, kSelFixed + per * 6,
+                                         cs, false, s, a, cs, per);
+        if (st != OK || lens_out != c.lens)
+            return st;
+        return launch_overlapped(evict_lens_kernel, dim3((unsigned)((c.B + 255) / 256)), 256, 0, 0, true, s, a);
     }
+    const int st = launch_overlapped(evict_select_long_kernel, dim3((unsigned)units), kSelThreads, 0, 0, false, s, a);
     if (st != OK)
         return st;
-    if (few)
-        return lens_out == c.lens
-                   ? launch_overlapped(evict_lens_kernel, dim3((unsigned)((c.B + 255) / 256)), 256, 0, 0, true, s, a)
-                   : OK;
     const int blocks = (budget + 255) / 256;
     return launch_overlapped(evict_move_kernel, dim3((unsigned)units, blocks < 64 ? blocks : 64), 256, 0, 0, true, s, a);
 }

@@ -290,7 +290,8 @@ int fa_cache_append(const fa_kv_cache *cache, const fa_heads *k, const fa_heads 
  * of Hkv; query head h reads KV head h / (Hq / Hkv).  With causal != 0 row t sees
  * slots up to lens[b] - Tq + t (bottom-right, as fa_decode; the Tq rows' own
  * tokens are the last entries), else every slot.  A row that sees nothing gets
- * O = 0 and lse = -inf.  Scores, statistics and the row sums are fp32; the
+ * O = 0 and lse = -inf.  An infinity or NaN in an entry that any row of the
+ * call sees may reach every row of its head group.  Scores, statistics and the row sums are fp32; the
  * keys are split over the thread blocks in equal shares of the whole batch, and
  * partial results are joined in a fixed order: the same call gives the same
  * bits, but a sequence's last bits may depend on the other lengths.
@@ -319,7 +320,8 @@ int fa_decode_paged(const fa_kv_cache *cache, const void *q, void *o, float *lse
  *   weight_out, order_out  like cache->weight and cache->order (which they may
  *              be), the entries in front of the new length only; order_out NULL
  *              exactly when cache->order is;
- *   lens_out   [B] int32 (may be cache->lens): min(lens, budget).
+ *   lens_out   [B] int32 (may be cache->lens): min(lens, budget), or lens where it
+ *              is out of range.
  * n_first, n_recent >= 0 with n_first + n_recent <= budget; either one > 0 needs
  * cache->order.  cache->weight is needed.  A sequence with a length out of range
  * is left alone; so is a row whose page is out of range.

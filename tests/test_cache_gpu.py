@@ -653,6 +653,19 @@ def test_evict_without_order(fa):
             assert kept[b, h, :len(src)].tolist() == src
 
 
+@pytest.mark.parametrize("budget", [90, 20])
+def test_evict_bad_lengths(fa, budget):
+    """Few moves (copied by the selection) and many: a length out of range stays as it is."""
+    for in_place in (False, True):
+        cache = make_cache(fa, 56, [100, 100, 60], 1, 64, 16, weight=True, width=13 if budget == 20 else 8)
+        cache.lens[0] = -1
+        cache.lens[1] = cache.max_pages * 16 + 5
+        out = cache.lens if in_place else torch.zeros_like(cache.lens)
+        fa.fa_cache_evict(cache, budget, lens_out=out)
+        assert fa.fa_sync_status() == fa.FA_ERR_BAD_INDEX
+        assert out.tolist() == [-1, cache.max_pages * 16 + 5, min(60, budget)]
+
+
 def test_evict_bad_lengths_and_pages(fa):
     cache = make_cache(fa, 53, [100, 100, 100], 1, 64, 16, weight=True)
     cache.lens[0] = -1
