@@ -145,6 +145,33 @@ __device__ __forceinline__ void turn(float (&a)[8], float (&b)[8], const float (
     }
 }
 
+// Runs over `n` heads of one token: x points at the first one's row, sx elements apart.  The loads
+// of kHeadsAhead heads are under way at once; put(head, values at e0, values at e1) takes them.
+constexpr int kHeadsAhead = 4;
+template <typename E, typename Put>
+__device__ __forceinline__ void each_head(const E *x, long long sx, int n, const Slice &sl, Put put)
+{
+    x += sl.e0;
+    const int gap = sl.e1 - sl.e0;
+    for (int i = 0; i < n; i += kHeadsAhead, x += kHeadsAhead * sx) {
+        Raw8<E> p[kHeadsAhead], q[kHeadsAhead];
+#pragma unroll
+        for (int u = 0; u < kHeadsAhead; ++u)
+            if (i + u < n) {
+                p[u].load(x + u * sx);
+                q[u].load(x + u * sx + gap);
+            }
+#pragma unroll
+        for (int u = 0; u < kHeadsAhead; ++u)
+            if (i + u < n) {
+                float f[8], g[8];
+                p[u].get(f);
+                q[u].get(g);
+                put(i + u, f, g);
+            }
+    }
+}
+
 struct RopeArgs {
     Row3 x[2], y[2];
     int H0, H;            // heads of the first tensor, of both
@@ -155,7 +182,6 @@ struct RopeArgs {
 };
 
 constexpr int kRopeThreads = 256;
-constexpr int kHeadsAhead = 4;    // heads whose loads a thread has in flight
 
 template <typename E, int D, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeTable tab,
@@ -171,7 +197,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     const long long tok = (long long)tile * (kRopeThreads / TPR) + threadIdx.x / TPR;
     if (tok >= a.n)
         return;
-    const long long b = tok / a.T, t = tok - b * a.T;
+    const int b = (int)tok / a.T, t = (int)tok - b * a.T;
     const Slice sl = slice_of(v, a.rot, INTER);
     float sn[8], cs[8];
     if (sl.pair >= 0) {
@@ -183,33 +209,22 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
         }
     }
     const int h0 = group * a.heads_per_cta, h1 = min(a.H, h0 + a.heads_per_cta);
-    for (int hb = h0; hb < h1; hb += kHeadsAhead) {
-        Raw8<E> p[kHeadsAhead], q[kHeadsAhead];
 #pragma unroll
-        for (int u = 0; u < kHeadsAhead; ++u) {
-            const int h = hb + u, w = h >= a.H0;
-            if (h < h1) {
-                const Row3 &xi = a.x[w];
-                const E *x = static_cast<const E *>(xi.p) + b * xi.sb + (h - (w ? a.H0 : 0)) * xi.sh + t * xi.st;
-                p[u].load(x + sl.e0);
-                q[u].load(x + sl.e1);
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < kHeadsAhead; ++u) {
-            const int h = hb + u, w = h >= a.H0;
-            if (h < h1) {
-                const Row3 &yi = a.y[w];
-                E *y = static_cast<E *>(yi.p) + b * yi.sb + (h - (w ? a.H0 : 0)) * yi.sh + t * yi.st;
-                float f[8], g[8];
-                p[u].get(f);
-                q[u].get(g);
-                if (sl.pair >= 0)
-                    turn<INTER>(f, g, sn, cs);
-                store8(y + sl.e0, f);
-                store8(y + sl.e1, g);
-            }
-        }
+    for (int w = 0; w < 2; ++w) {   // the group's heads of either tensor
+        const int first = max(h0 - (w ? a.H0 : 0), 0), last = min(h1 - (w ? a.H0 : 0), w ? a.H - a.H0 : a.H0);
+        if (first >= last)
+            continue;
+        const Row3 &xi = a.x[w], &yi = a.y[w];
+        const E *x = static_cast<const E *>(xi.p) + b * xi.sb + first * xi.sh + t * xi.st;
+        E *y = static_cast<E *>(yi.p) + b * yi.sb + first * yi.sh + t * yi.st + sl.e0;
+        const int gap = sl.e1 - sl.e0;
+        each_head(x, xi.sh, last - first, sl, [&](int, float(&f)[8], float(&g)[8]) {
+            if (sl.pair >= 0)
+                turn<INTER>(f, g, sn, cs);
+            store8(y, f);
+            store8(y + gap, g);
+            y += yi.sh;
+        });
     }
 }
 
@@ -313,9 +328,18 @@ __global__ void __launch_bounds__(kRopeThreads) append_kernel(const __grid_const
     const long long tok = (long long)tile * (kRopeThreads / TPR) + threadIdx.x / TPR;
     if (tok >= n)
         return;
-    const int b = (int)(tok / a.T), t = (int)(tok - (long long)b * a.T);
+    const int b = (int)tok / a.T, t = (int)tok - b * a.T;
     const int len = a.lens[b], cap = a.max_pages << a.ps_shift;
     const int nb = a.new_lens ? a.new_lens[b] : a.T;
+    const Slice sl = slice_of(vec, a.rotate ? a.rot : 0, INTER);
+    const int h0 = group * a.heads_per_cta, h1 = min(a.Hq + 2 * a.Hkv, h0 + a.heads_per_cta);
+    const bool turns = sl.pair >= 0 && h0 < a.Hq + a.Hkv;
+    int pos[8];
+    if (turns) {   // with the lengths, not after them
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            pos[j] = a.pos[(long long)tab.axis[sl.pair + j] * n + tok];
+    }
     if (len < 0 || len > cap || nb < 0 || nb > a.T || nb > len) {
         if (vec == 0 && t == 0 && group == 0)
             atomicCAS(&g_cache_status, 0, kStatusBadIndex);
@@ -324,67 +348,69 @@ __global__ void __launch_bounds__(kRopeThreads) append_kernel(const __grid_const
     if (t >= nb)
         return;
     const int slot = len - nb + t;
-    const Slice sl = slice_of(vec, a.rotate ? a.rot : 0, INTER);
-    const int h0 = group * a.heads_per_cta, h1 = min(a.Hq + 2 * a.Hkv, h0 + a.heads_per_cta);
+    int page = 0;
+    if (h1 > a.Hq)
+        page = a.block_table[(long long)b * a.max_pages + (slot >> a.ps_shift)];
     float sn[8], cs[8];
-    if (sl.pair >= 0 && h0 < a.Hq + a.Hkv) {
+    if (turns) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            phase_sincos(tab.turns[sl.pair + j], a.pos[(long long)tab.axis[sl.pair + j] * n + tok], sn[j], cs[j]);
+            phase_sincos(tab.turns[sl.pair + j], pos[j], sn[j], cs[j]);
     }
-    int page = 0;
-    bool page_ok = true;
-    if (h1 > a.Hq) {
-        page = a.block_table[(long long)b * a.max_pages + (slot >> a.ps_shift)];
-        page_ok = page >= 0 && page < a.num_pages;
-        if (!page_ok && vec == 0)
-            atomicCAS(&g_cache_status, 0, kStatusBadIndex);
-    }
-    const int row = slot & ((1 << a.ps_shift) - 1);
+    const bool page_ok = page >= 0 && page < a.num_pages;
+    if (h1 > a.Hq && !page_ok && vec == 0)
+        atomicCAS(&g_cache_status, 0, kStatusBadIndex);
     using E = __nv_bfloat16;
-    for (int hb = h0; hb < h1; hb += kHeadsAhead) {
-        Raw8<E> p[kHeadsAhead], q[kHeadsAhead];
-#pragma unroll
-        for (int u = 0; u < kHeadsAhead; ++u) {
-            const int h = hb + u, hk = h - a.Hq;
-            if (h < h1) {
-                const Row3 &r = hk < 0 ? a.q : hk < a.Hkv ? a.k : a.v;
-                const int in = hk < 0 ? h : hk < a.Hkv ? hk : hk - a.Hkv;
-                const E *x = static_cast<const E *>(r.p) + b * r.sb + in * r.sh + t * r.st;
-                p[u].load(x + sl.e0);
-                q[u].load(x + sl.e1);
+    const int gap = sl.e1 - sl.e0;
+    auto part = [&](int from, int n, int &first, int &count) {   // the group's heads among n from `from` on
+        first = max(h0 - from, 0);
+        count = min(h1 - from, n) - first;
+        return count > 0;
+    };
+    int first, count;
+    if (part(0, a.Hq, first, count)) {
+        const E *x = static_cast<const E *>(a.q.p) + b * a.q.sb + first * a.q.sh + t * a.q.st;
+        E *o = static_cast<E *>(a.qo.p) + b * a.qo.sb + first * a.qo.sh + t * a.qo.st + sl.e0;
+        each_head(x, a.q.sh, count, sl, [&](int, float(&f)[8], float(&g)[8]) {
+            if (turns)
+                turn<INTER>(f, g, sn, cs);
+            store8(o, f);
+            store8(o + gap, g);
+            o += a.qo.sh;
+        });
+    }
+    if (!page_ok)
+        return;
+    const long long row_at = (((long long)page * a.Hkv << a.ps_shift) + (slot & ((1 << a.ps_shift) - 1))) * D + sl.e0;
+    const long long step = (long long)D << a.ps_shift;   // from head to head in a page
+    if (part(a.Hq, a.Hkv, first, count)) {
+        const E *x = static_cast<const E *>(a.k.p) + b * a.k.sb + first * a.k.sh + t * a.k.st;
+        long long at = row_at + first * step;
+        each_head(x, a.k.sh, count, sl, [&](int i, float(&f)[8], float(&g)[8]) {
+            if (turns)
+                turn<INTER>(f, g, sn, cs);
+            const float scale = FP8 ? a.ks[first + i] : 1.f, inv = FP8 ? __frcp_rn(scale) : 1.f;
+            put8<FP8>(a.kp, at, f, scale, inv);
+            put8<FP8>(a.kp, at + gap, g, scale, inv);
+            at += step;
+            if (vec == 0) {
+                const long long w = ((long long)b * a.Hkv + first + i) * cap + slot;
+                if (a.weight)
+                    a.weight[w] = 0.f;
+                if (a.order)
+                    a.order[w] = (a.seen ? a.seen[b] - nb : len - nb) + t;
             }
-        }
-#pragma unroll
-        for (int u = 0; u < kHeadsAhead; ++u) {
-            const int h = hb + u;
-            if (h >= h1)
-                break;
-            float x[8], y[8];
-            p[u].get(x);
-            q[u].get(y);
-            if (h < a.Hq + a.Hkv && sl.pair >= 0)
-                turn<INTER>(x, y, sn, cs);
-            if (h < a.Hq) {
-                E *o = static_cast<E *>(a.qo.p) + b * a.qo.sb + h * a.qo.sh + t * a.qo.st;
-                store8(o + sl.e0, x);
-                store8(o + sl.e1, y);
-            } else if (page_ok) {
-                const bool isv = h >= a.Hq + a.Hkv;
-                const int hk = h - a.Hq - (isv ? a.Hkv : 0);
-                const long long at = ((((long long)page * a.Hkv + hk) << a.ps_shift) + row) * D;
-                const float scale = FP8 ? (isv ? a.vs : a.ks)[hk] : 1.f, inv = FP8 ? __frcp_rn(scale) : 1.f;
-                put8<FP8>(isv ? a.vp : a.kp, at + sl.e0, x, scale, inv);
-                put8<FP8>(isv ? a.vp : a.kp, at + sl.e1, y, scale, inv);
-                if (!isv && vec == 0) {
-                    const long long w = ((long long)b * a.Hkv + hk) * cap + slot;
-                    if (a.weight)
-                        a.weight[w] = 0.f;
-                    if (a.order)
-                        a.order[w] = (a.seen ? a.seen[b] - nb : len - nb) + t;
-                }
-            }
-        }
+        });
+    }
+    if (part(a.Hq + a.Hkv, a.Hkv, first, count)) {
+        const E *x = static_cast<const E *>(a.v.p) + b * a.v.sb + first * a.v.sh + t * a.v.st;
+        long long at = row_at + first * step;
+        each_head(x, a.v.sh, count, sl, [&](int i, float(&f)[8], float(&g)[8]) {
+            const float scale = FP8 ? a.vs[first + i] : 1.f, inv = FP8 ? __frcp_rn(scale) : 1.f;
+            put8<FP8>(a.vp, at, f, scale, inv);
+            put8<FP8>(a.vp, at + gap, g, scale, inv);
+            at += step;
+        });
     }
 }
 
