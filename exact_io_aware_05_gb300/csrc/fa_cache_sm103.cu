@@ -15,6 +15,7 @@
 
 #include "fa_common.cuh"
 #include "fa_internal.h"
+#include "fa_pdl.cuh"
 
 namespace fa {
 
@@ -240,8 +241,9 @@ RopeTable table_of(const fa_rope_spec &s)
 
 Row3 row3(const fa_heads &x) { return Row3{x.data, x.stride_b, x.stride_h, x.stride_t}; }
 
-// Heads one thread runs over: as few as let all CTAs be resident (two an SM), 32 at most.  With 4,
-// 8, 16, 32 and 64 heads the q and k of B8 H32 T4096 d128 take 229, 190, 174, 167 and 173 us.
+// Heads one thread runs over: as few as let all CTAs be resident (two an SM), 32 at most.  With 8, 16,
+// 32 and 48 heads the q and k of B8 H32 T4096 d128 take 175, 163, 162 and 163 us, and 4193 new tokens of
+// 32 + 16 heads 24.6, 24.1, 21.1 and 26.7.
 int heads_per_cta(long long tokens, int H, int d)
 {
     const long long ctas = (tokens * (d / 16) + kRopeThreads - 1) / kRopeThreads * H, slots = 2 * device_sm_count();

@@ -38,14 +38,6 @@ __device__ __forceinline__ uint64_t globaltimer_ns()
 __device__ __forceinline__ uint32_t lane_id() { return threadIdx.x & 31u; }
 __device__ __forceinline__ uint32_t warp_id() { return threadIdx.x >> 5; }
 
-// Programmatic dependent launch.  pdl_launch(): the next kernel of the stream may be launched once
-// every CTA of this one has said so (or ended); it runs its prologue and stops at its pdl_wait().
-// pdl_wait(): returns when the kernels before this one have ended and their writes are visible.
-// Every CTA of such a kernel calls it before its first access to device memory, so that the end
-// of a kernel still means the end of all before it.
-__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // ------------------------------------------------------------------ mbarrier
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count)
 {

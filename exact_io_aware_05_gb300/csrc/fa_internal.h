@@ -145,29 +145,6 @@ int dec_status_fetch_clear(cudaStream_t s, int *host_word);
 int encode_tmap(CUtensorMap *map, const void *base, CUtensorMapDataType dtype, int rank, const uint64_t *dims,
                 const uint64_t *strides, const uint32_t *box, CUtensorMapSwizzle swizzle);
 
-// Launches a kernel that may start while the one before it in the stream still runs: it calls
-// pdl_wait() (fa_common.cuh) before it touches device memory, and the launch latency is hidden.
-// cluster > 0: CTAs of a cluster.  overlap = false: after the one before it, as usual.
-template <typename... P, typename... A>
-int launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, size_t smem, int cluster, bool overlap, cudaStream_t s,
-                      const A &...args)
-{
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = overlap ? 1 : 0;
-    at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = (unsigned)cluster;
-    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cfg.attrs = at;
-    cfg.numAttrs = cluster > 0 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? OK : ERR_CUDA;
-}
-
 // Rotary positions and the paged cache (fa_cache_sm103.cu, fa_paged_sm103.cu); arguments
 // already validated by fa_cache_api.cu.  Structures as in include/fa.h.
 int rope_launch(const fa_heads *x, const fa_heads *y, int n, const int *positions, const fa_rope_spec &spec, int B,

@@ -31,6 +31,7 @@
 
 #include "fa_common.cuh"
 #include "fa_internal.h"
+#include "fa_pdl.cuh"
 
 namespace fa {
 
