@@ -135,13 +135,20 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int y, int z, int w)
+__device__ __forceinline__ void tma_load_4d_hint(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int y, int z, int w,
+                                                 uint64_t policy)
 {
     asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w), "l"(policy)
         : "memory");
+}
+__device__ __forceinline__ uint64_t policy_evict_normal()
+{
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+    return p;
 }
 __device__ __forceinline__ void st_shared_zero16(uint32_t addr)
 {
@@ -372,6 +379,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
         const int box = lane >> 1;
         const uint32_t dst = (uint32_t)((lane & 1) * C::TILE + (box << bp_shift) * C::ROWB);
         const uint32_t box_bytes = (uint32_t)(C::ROWB << bp_shift);
+        // K and V are read once, unless several row blocks read them: they leave the L2 to what is written
+        // and read again (e4m3 d 64 58.5 -> 57.1 us, with stored scores 30.3 -> 28.2)
+        const uint64_t policy = a.RB == 1 ? policy_evict_first() : policy_evict_normal();
         uint32_t n = 0;
         bool ok = true;
         while (ok && p.left > 0) {
@@ -407,8 +417,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
                 }
                 __syncwarp();
                 if (good)
-                    tma_load_4d(sbase + st * C::STAGE + dst, map, bar0 + 8u * st, 0, slot & ((1 << a.ps_shift) - 1), 0,
-                                page * a.Hkv + h);
+                    tma_load_4d_hint(sbase + st * C::STAGE + dst, map, bar0 + 8u * st, 0, slot & ((1 << a.ps_shift) - 1), 0,
+                                     page * a.Hkv + h, policy);
                 page = next;
             }
             if (ok)
