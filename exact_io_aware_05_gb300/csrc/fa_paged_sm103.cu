@@ -69,6 +69,10 @@ struct Cfg {
     static constexpr int FIT = ((CTAS == 3 ? 75 : CTAS == 2 ? 113 : 227) * 1024 - SMALL) / STAGE;
     static constexpr int NST = FIT < 12 ? FIT : 12;
     static_assert(NST >= 2, "shared memory");
+    // Stages in use where every SM has its CTAs: with 64 KB a CTA under way the memory is busy, and
+    // more only queues (64 sequences, d 128 and 64: 164.9 and 164.4 us with two stages, 167.5 and 170.7
+    // with three); where the products take longer the third hides them (e4m3 d 128: 101 against 107).
+    static constexpr int DEPTH = !FP8 && D <= 128 && RT == 1 ? 2 : NST;
     static constexpr int OFF_Q = NST * STAGE;
     static constexpr int OFF_O = OFF_Q + NQ;
     static constexpr int OFF_ML = OFF_O + NO;
@@ -368,6 +372,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
             return;   // the whole CTA
     }
     const long long mine_all = p.left;   // tiles of this CTA
+    const uint32_t depth = whole ? C::NST : C::DEPTH;   // stages in use
     __syncthreads();   // the barriers are there
     // rows of a page in one box, and boxes of a tile
     const int bp_shift = a.ps_shift < 6 ? a.ps_shift : 6, boxes = C::KT >> bp_shift;
@@ -382,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
         // K and V are read once, unless several row blocks read them: they leave the L2 to what is written
         // and read again (e4m3 d 64 58.5 -> 57.1 us, with stored scores 30.3 -> 28.2)
         const uint64_t policy = a.RB == 1 ? policy_evict_first() : policy_evict_normal();
-        uint32_t n = 0;
+        uint32_t n = 0, st = 0, round = 0;   // tiles so far; the stage of the next one, and its round
         bool ok = true;
         while (ok && p.left > 0) {
             const int len = length_of(a, p.b), h = p.ul % a.Hkv, cnt = segment(p);
@@ -395,8 +400,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
             for (int i = 0; i < cnt; ++i, ++n) {
                 const int tile = p.tile + i, slot = tile * C::KT + (box << bp_shift);
                 const int next = i + 1 < cnt ? page_at(tile + 1) : -1;
-                const uint32_t st = n % C::NST;
-                if (n >= C::NST && !mbar_wait_warp(bar0 + 8u * (C::NST + st), (n / C::NST - 1) & 1u, ctx, SITE_PAGED_EMPTY)) {
+                if (round > 0 && !mbar_wait_warp(bar0 + 8u * (C::NST + st), (round - 1) & 1u, ctx, SITE_PAGED_EMPTY)) {
                     ok = false;
                     break;
                 }
@@ -420,13 +424,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
                     tma_load_4d_hint(sbase + st * C::STAGE + dst, map, bar0 + 8u * st, 0, slot & ((1 << a.ps_shift) - 1), 0,
                                      page * a.Hkv + h, policy);
                 page = next;
+                if (++st == depth) {
+                    st = 0;
+                    ++round;
+                }
             }
             if (ok)
                 next_unit(a, p, cnt);
         }
         if (!ok)   // copies already issued land before the CTA exits
-            for (uint32_t s = n < C::NST ? 0 : n - C::NST; s < n; ++s)
-                mbar_wait_drain(bar0 + 8u * (s % C::NST), (s / C::NST) & 1u);
+            for (uint32_t s = n < depth ? 0 : n - depth; s < n; ++s)
+                mbar_wait_drain(bar0 + 8u * (s % depth), (s / depth) & 1u);
     } else {
         // ---------------------------------------------------------- math
         const int rt = warp % RT, kw = warp / RT, c4 = lane & 3, r0 = lane >> 2;
@@ -496,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
                     reinterpret_cast<float *>(smem + C::OFF_RS)[r] = scale;
             }
         };
-        uint32_t n = 0;
+        uint32_t st = 0, round = 0;   // the next tile's stage, and its round
         bool ok = true;
         if (RT == 1 && p.left > 0)
             fetch_q(p);
@@ -546,9 +554,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
                 o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
             float m0 = -INFINITY, m1 = -INFINITY, l0[2] = {0.f, 0.f}, l1[2] = {0.f, 0.f};
 
-            for (int i = 0; i < cnt; ++i, ++n) {
-                const uint32_t st = n % C::NST;
-                if (!mbar_wait_warp(bar0 + 8u * st, (n / C::NST) & 1u, ctx, SITE_PAGED_FULL))
+            for (int i = 0; i < cnt; ++i) {
+                if (!mbar_wait_warp(bar0 + 8u * st, round & 1u, ctx, SITE_PAGED_FULL))
                     ok = false;   // the CTA gives up: no more is computed or written, and its warps still meet
                 const uint32_t groups = ok ? there[st] : 0u;
 #pragma unroll 1
@@ -726,6 +733,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(bar0 + 8u * (C::NST + st));
+                if (++st == depth) {
+                    st = 0;
+                    ++round;
+                }
             }
 
             // the join's blocks may come now: earlier they would take registers that CTAs of the next
