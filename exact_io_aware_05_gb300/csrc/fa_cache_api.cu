@@ -10,6 +10,8 @@
 
 namespace {
 
+constexpr long long kMaxSlots = 1ll << 30;   // of a sequence: slot numbers past the end of a tile fit an int
+
 bool width_ok(int d) { return d == 64 || d == 128 || d == 256; }
 
 // A strided [B][H][T][d] tensor: present, 16-byte aligned rows, strides in range.
@@ -86,7 +88,7 @@ int cache_check(const fa_kv_cache *c)
     if (ps != 16 && ps != 32 && ps != 64 && ps != 128 && ps != 256)
         return FA_ERR_UNSUPPORTED;
     if ((long long)c->num_pages * c->Hkv > INT_MAX || (long long)c->B * c->Hkv > INT_MAX ||
-        (long long)c->max_pages * ps > INT_MAX)
+        (long long)c->max_pages * ps > kMaxSlots)
         return FA_ERR_INVALID_ARG;
     if (c->B == 0)
         return FA_OK;
@@ -290,7 +292,7 @@ static bool paged_sizes_ok(int B, int Hq, int Hkv, int Tq, int max_pages, int pa
 {
     if (B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Tq < 1 || Tq > 16 || max_pages < 0 || page_size < 1)
         return false;
-    if (!width_ok(d) || (long long)max_pages * page_size > INT_MAX)
+    if (!width_ok(d) || (long long)max_pages * page_size > kMaxSlots)
         return false;
     // row indexes of q, and units of (sequence, KV head, 64 rows of a head group), in 31 bits
     return (long long)B * Hq * Tq <= INT_MAX;

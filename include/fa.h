@@ -248,8 +248,8 @@ int fa_rope(const fa_heads *x, const fa_heads *y, int n, const int *positions, c
  * page_size is 16, 32, 64, 128 or 256; d 64, 128 or 256.  Only the pages and
  * rows in front of lens are read: what lies behind them may hold anything.
  * Sequences may share pages that none of them writes to (fa_cache_append and
- * fa_cache_evict write).  num_pages * Hkv and B * Hkv must fit in 31 bits, and
- * max_pages * page_size too.  The struct is read during the call only; a page
+ * fa_cache_evict write).  num_pages * Hkv and B * Hkv must fit in 31 bits;
+ * max_pages * page_size is at most 2^30.  The struct is read during the call only; a page
  * number outside 0 .. num_pages - 1 in front of lens, or a length outside its
  * range, is FA_ERR_BAD_INDEX from fa_sync_status and is never dereferenced.
  */
@@ -290,11 +290,12 @@ int fa_cache_append(const fa_kv_cache *cache, const fa_heads *k, const fa_heads 
  * of Hkv; query head h reads KV head h / (Hq / Hkv).  With causal != 0 row t sees
  * slots up to lens[b] - Tq + t (bottom-right, as fa_decode; the Tq rows' own
  * tokens are the last entries), else every slot.  A row that sees nothing gets
- * O = 0 and lse = -inf.  An infinity or NaN in an entry that any row of the
- * call sees may reach every row of its head group.  Scores, statistics and the row sums are fp32; the
- * keys are split over the thread blocks in equal shares of the whole batch, and
- * partial results are joined in a fixed order: the same call gives the same
- * bits, but a sequence's last bits may depend on the other lengths.
+ * O = 0 and lse = -inf.  An infinity or NaN in the v of an entry that any row of
+ * the call sees may reach every row of its head group.  Scores, statistics and
+ * the row sums are fp32; the keys are split over the thread blocks in equal
+ * shares of the whole batch, and partial results are joined in a fixed order:
+ * the same call gives the same bits, but a sequence's last bits may depend on
+ * the other lengths.
  * accumulate = 1 adds, for every entry, the sum of its probabilities over the
  * head group's rows (Hq / Hkv heads x Tq) to cache->weight.
  * workspace: fa_decode_paged_workspace_bytes bytes, 256-byte aligned, contents

@@ -625,9 +625,9 @@ def test_evict(fa, case, in_place):
     assert torch.equal(cache.v.view(torch.uint8), ev.view(torch.uint8))
 
 
-def test_evict_longest(fa):
-    """More entries than fit a cluster's shared memory."""
-    n, budget = 270000, 100001
+@pytest.mark.parametrize("n,budget", [(261000, 130000), (270000, 100001)])
+def test_evict_longest(fa, n, budget):
+    """The most entries that fit a cluster's shared memory, and more."""
     cache = make_cache(fa, 54, [n], 1, 64, 256, weight=True)
     cache.weight.copy_(weights_of("few", gen(55), tuple(cache.weight.shape)) + (cache.weight < 0.5))
     w0, k0 = cache.weight.clone(), cache.k.clone()

@@ -146,7 +146,7 @@ BAD_CACHES = [
     (dict(B=-1), INVALID), (dict(Hkv=0), INVALID), (dict(num_pages=-1), INVALID), (dict(max_pages=-1), INVALID),
     (dict(dtype=1), INVALID), (dict(dtype=9), INVALID), (dict(d=96), UNSUPPORTED), (dict(page_size=8), UNSUPPORTED),
     (dict(page_size=48), UNSUPPORTED), (dict(page_size=512), UNSUPPORTED), (dict(num_pages=1 << 30, Hkv=4), INVALID),
-    (dict(max_pages=1 << 28, page_size=16), INVALID), (dict(k=None), INVALID), (dict(v=None), INVALID),
+    (dict(max_pages=1 << 28, page_size=16), INVALID), (dict(max_pages=(1 << 22) + 1, page_size=256), INVALID), (dict(k=None), INVALID), (dict(v=None), INVALID),
     (dict(lens=None), INVALID), (dict(block_table=None), INVALID), (dict(k=P + 64), INVALID), (dict(weight=P + 4 * MB + 4), INVALID), (dict(order=P + 5 * MB + 8), INVALID), (dict(lens=P + 3 * MB + 2), INVALID),
     (dict(k_scale=P + 6 * MB, v_scale=P + 6 * MB), INVALID), (dict(dtype=2), INVALID), (dict(dtype=2, k_scale=P + 6 * MB), INVALID),
 ]
