@@ -488,12 +488,17 @@ __device__ __forceinline__ int block_rank(bool p, int &total, int *scratch)
 // a second kernel for them cost 3 us more.
 constexpr int kPickThreads = 512;
 constexpr int kSelBins = 256, kSelPasses = 4;
-constexpr int kSelCap = 32768;                               // entries a CTA, at most (their numbers take 16 bits)
+constexpr int kSelCap = 32767;                               // entries a CTA, at most (two counts share an int)
 constexpr int kSelCopies = 8;                                // of the first pass's counts: most ranks share a few digits
 constexpr int kSelFixed = (kSelPasses + kSelCopies) * kSelBins * 4 + 32 * 4 + 32;   // shared memory besides the entries
 
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// All threads of the cluster meet; not the .aligned form, which wants whole warps: the loops before it
+// go by the data.
+__device__ __forceinline__ void cluster_sync()
+{
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
 __device__ __forceinline__ uint32_t cluster_addr(const void *p, int rank)   // the same place in another CTA
 {
     uint32_t addr;
@@ -676,8 +681,7 @@ __global__ void __launch_bounds__(kPickThreads) evict_select_kernel(const __grid
                 hp[tid] = x.x + x.y + x.z + x.w + y.x + y.y + y.z + y.w;
             }
         }
-        cluster_arrive();
-        cluster_wait();
+        cluster_sync();
         // T / 256 threads a bin, bins from the top
         constexpr int TPB = T / kSelBins;
         const int d = kSelBins - 1 - tid / TPB;
@@ -742,14 +746,22 @@ __global__ void __launch_bounds__(kPickThreads) evict_select_kernel(const __grid
     }
     if (tid == 0)
         share[0] = total;
-    cluster_arrive();
-    cluster_wait();
+    cluster_sync();
     if (tid < 8)
         lists[tid] = tid < cs ? cluster_load(share, tid) : 0;
     __syncthreads();
-    int all = 0;
-    for (int r = 0; r < cs; ++r)
+    int all = 0, behind = 0;
+    for (int r = 0; r < cs; ++r) {
         all += lists[r] & 0xFFFF;
+        behind += lists[r] >> 16;
+    }
+    // as many holes as entries for them: anything else means that the lengths changed under the call,
+    // and nothing is moved
+    if (all != behind) {
+        if (tid == 0)
+            atomicCAS(&g_cache_status, 0, kStatusBadIndex);
+        all = 0;
+    }
     // hole and entry number g of the cluster; each of its warps takes up to 32 of them
     const int warps = cs * T / 32, chunk = min(32, (all + warps - 1) / warps);
     for (int g0 = (rank * (T / 32) + (int)warp_id()) * chunk; g0 < all; g0 += warps * chunk) {
@@ -763,16 +775,17 @@ __global__ void __launch_bounds__(kPickThreads) evict_select_kernel(const __grid
                 x -= lists[c++] >> 16;
             const int j = r * per + cluster_load16(list + m, r);
             const int i = c * per + cluster_load16(list + (lists[c] & 0xFFFF) + x, c);
-            kept[j] = i;
-            a.weight_out[base + j] = weight[i];
-            if (order)
-                a.order_out[base + j] = order[i];
-            move_of(a, b, h, i, j, from, to);
+            if (j < end && i < len) {   // the same
+                kept[j] = i;
+                a.weight_out[base + j] = weight[i];
+                if (order)
+                    a.order_out[base + j] = order[i];
+                move_of(a, b, h, i, j, from, to);
+            }
         }
         move_rows(a, moves[warp_id()], from, to);
     }
-    cluster_arrive();   // no CTA ends while another may read its list
-    cluster_wait();
+    cluster_sync();   // no CTA ends while another may read its list
 }
 
 // The lengths, where lens_out is lens, which every CTA of the selection reads.

@@ -683,6 +683,54 @@ def test_evict_bad_lengths_and_pages(fa):
     assert torch.equal(moved[1], k0[p[6], 0, :4])
 
 
+# ---------------------------------------------------------------- nothing outside the buffers
+class Guarded:
+    """Buffers in the middle of larger ones; `intact()`: nothing around them was written."""
+
+    def __init__(self):
+        self.all = []
+
+    def like(self, t, fill=None):
+        n, pad = t.numel() * t.element_size(), 1 << 16
+        raw = torch.full((n + 2 * pad,), 0xA5, dtype=torch.uint8, device=DEV)
+        self.all.append((raw, n, pad))
+        view = raw[pad:pad + n].view(t.dtype).view(t.shape)
+        if fill is None:
+            view.copy_(t)
+        return view
+
+    def intact(self):
+        return all(bool((raw[:pad] == 0xA5).all()) and bool((raw[pad + n:] == 0xA5).all()) for raw, n, pad in self.all)
+
+
+@pytest.mark.parametrize("lens,Hq,Hkv,d,ps,Tq,fp8", [
+    ([1, 63, 2049, 0], 8, 2, 128, 16, 1, False), ([5000], 16, 1, 64, 64, 7, True), ([130, 700], 4, 4, 256, 32, 3, False),
+    ([900] * 40, 32, 8, 128, 16, 1, False), ([9001, 12000, 20000, 32768], 8, 8, 128, 64, 1, False)])
+def test_nothing_outside_the_buffers(fa, lens, Hq, Hkv, d, ps, Tq, fp8):
+    g, rnd = Guarded(), gen(70)
+    base = make_cache(fa, 71, lens, Hkv, d, ps, fp8, weight=True, extra_pages=0)
+    B = base.B
+    cache = fa.KVCache(g.like(base.k), g.like(base.v), g.like(base.block_table), g.like(base.lens), base.k_scale, base.v_scale,
+                       g.like(base.weight), g.like(base.order), g.like(base.lens))
+    q = randn(rnd, B, Hq, Tq, d)
+    qo, o, lse = g.like(q), g.like(q), g.like(torch.empty((B, Hq, Tq), device=DEV))
+    spec = fa.rope_spec(d)
+    pos = torch.randint(0, 9999, (1, B, Tq), generator=rnd, device=DEV).to(I32)
+    new = torch.minimum(cache.lens, torch.full_like(cache.lens, Tq))
+    fa.fa_cache_append(cache, randn(rnd, B, Hkv, Tq, d), randn(rnd, B, Hkv, Tq, d), pos, spec, q=q, q_out=qo, new_lens=new)
+    fa.fa_rope(q, g.like(q), pos, spec, k=q, k_out=g.like(q))
+    for acc in (False, True):
+        ws = g.like(torch.empty(fa.fa_decode_paged_workspace_bytes(cache, Hq, Tq, acc), dtype=torch.uint8, device=DEV), fill=0)
+        fa.fa_decode_paged(cache, qo, o, lse, 0.1, ws, accumulate=acc)
+    assert fa.fa_sync_status() == fa.FA_OK and g.intact()
+    for budget in (max(max(lens) - 16, 1), max(max(lens) // 3, 1)):
+        kept = g.like(torch.empty((B, Hkv, budget), dtype=I32, device=DEV))
+        fa.fa_cache_evict(cache, budget, g.like(cache.weight), g.like(cache.order), g.like(cache.lens), kept, n_recent=1)
+        assert fa.fa_sync_status() == fa.FA_OK and g.intact()
+        fa.fa_cache_evict(cache, budget, kept=kept, n_first=1)
+        assert fa.fa_sync_status() == fa.FA_OK and g.intact()
+
+
 # ---------------------------------------------------------------- together
 @pytest.mark.parametrize("fp8", [False, True])
 def test_serving_steps(fa, fp8):
