@@ -167,7 +167,11 @@ __device__ __forceinline__ void st_shared_zero16(uint32_t addr)
 {
     asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0) : "memory");
 }
-__device__ __forceinline__ void math_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kMathWarps) : "memory"); }
+__device__ __forceinline__ void math_sync()   // the math warps meet, each one whole
+{
+    __syncwarp();
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * kMathWarps) : "memory");
+}
 __device__ __forceinline__ float quad_max(float x)
 {
     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
