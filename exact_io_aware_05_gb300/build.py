@@ -3,6 +3,8 @@
 Each translation unit compiles in parallel into ``_build/`` and links into
 ``exact_io_aware_05_gb300/libfa.so`` with the static CUDA runtime.  No torch
 types or headers are involved: the library is a plain C ABI (include/fa.h).
+The host compiler also builds ``_fa_py.so``, a CPython module with the binding's
+argument checks for the rotary and cache calls (csrc/fa_py.c).
 
 With ``test_variant=True`` the same pool also compiles the API and the two
 tile-loop units with ``FA_TEST_WITHHOLD=1`` into ``_build/waittest/`` and links
@@ -16,6 +18,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -24,6 +27,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 SO = os.path.join(PKG, "libfa.so")
 TEST_SO = os.path.join(PKG, "libfa_waittest.so")
+PY_SO = os.path.join(PKG, "_fa_py.so")     # CPython module: the cache calls' argument marshalling
 SOURCES = ["fa_api.cu", "fa_fwd_sm103.cu", "fa_fwd_f32.cu", "fa_bwd_sm103.cu", "fa_bwd_noalloc.cu",
            "fa_decode_sm103.cu", "fa_fp8_sm103.cu", "fa_cache_api.cu", "fa_cache_sm103.cu",
            "fa_paged_sm103.cu"]
@@ -54,7 +58,7 @@ def up_to_date(so: str = SO) -> bool:
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False, test_variant: bool = False) -> str:
     """Builds libfa.so (and, with test_variant, libfa_waittest.so) unless up to date."""
-    if not force and up_to_date() and (not test_variant or up_to_date(TEST_SO)):
+    if not force and up_to_date() and up_to_date(PY_SO) and (not test_variant or up_to_date(TEST_SO)):
         return SO
     os.makedirs(os.path.join(BUILD, "waittest"), exist_ok=True)
     cc = nvcc()
@@ -62,6 +66,15 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False, 
                     "-I", os.path.join(ROOT, "include"), "-I", CSRC]
     if ptxas_info:
         flags += ["-Xptxas", "-v"]
+
+    def compile_py() -> None:
+        tmp = PY_SO + f".tmp{os.getpid()}"
+        cmd = [os.environ.get("CC") or shutil.which("gcc") or "cc", "-O2", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"],
+               os.path.join(CSRC, "fa_py.c"), "-o", tmp]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"the host compiler failed on fa_py.c:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, PY_SO)
 
     def compile_one(job: tuple[str, bool]) -> str:
         src, test = job
@@ -75,8 +88,10 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False, 
         return obj
 
     jobs = [(src, False) for src in SOURCES] + ([(src, True) for src in TEST_SOURCES] if test_variant else [])
-    with ThreadPoolExecutor(max_workers=len(jobs)) as ex:
+    with ThreadPoolExecutor(max_workers=len(jobs) + 1) as ex:
+        py = ex.submit(compile_py)
         objs = list(ex.map(compile_one, jobs))
+        py.result()
     prod = objs[:len(SOURCES)]
     _link(cc, prod, SO)
     if test_variant:

@@ -1,10 +1,13 @@
-"""ctypes binding of libfa.so (include/fa.h): argument marshalling only.
+"""Binding of libfa.so (include/fa.h): argument marshalling only.
 
 Every function here checks tensor dtypes, shapes, devices and contiguity,
 reads the current CUDA stream, and calls the C entry point of the same name
-with raw device pointers.  No attention arithmetic happens in Python and
-there is no fallback: importing this module fails if libfa.so is missing,
-and every nonzero status raises ``FAError``.
+with raw device pointers, through ctypes.  The rotary and cache calls, which
+take a few microseconds on the device, are checked and made by the CPython
+module _fa_py (csrc/fa_py.c); where a check of its does not pass, the checks
+here say why.  No attention arithmetic happens in Python and there is no
+fallback: importing this module fails if libfa.so or _fa_py.so is missing, and
+every nonzero status raises ``FAError``.
 """
 from __future__ import annotations
 
@@ -20,6 +23,12 @@ LIB_PATH = os.path.join(_HERE, "libfa.so")
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is not built; run exact_io_aware_05_gb300.build.build() "
                       "(or __graft_entry__.build()) first")
+
+try:
+    from . import _fa_py
+except ImportError as e:
+    raise ImportError("_fa_py.so is not built for this Python; run exact_io_aware_05_gb300.build.build() "
+                      "(or __graft_entry__.build()) first") from e
 
 _lib = ctypes.CDLL(LIB_PATH)
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
@@ -456,6 +465,9 @@ def rope_spec(d: int, sections=None, base: float = 10000.0, rot: int | None = No
 
 _current_stream = torch._C._cuda_getCurrentRawStream    # of a device index; torch.cuda's builds an object
 _current_device = torch._C._cuda_getDevice
+_fa_py.setup(torch.bfloat16, torch.float32, torch.int32, _current_stream, _current_device,
+             *(ctypes.cast(f, _vp).value for f in (_lib.fa_rope, _lib.fa_cache_append, _lib.fa_decode_paged,
+                                                   _lib.fa_cache_evict)))
 
 
 def _launch(fn: str, entry, index: int, stream, *args) -> None:
@@ -475,6 +487,13 @@ def _launch(fn: str, entry, index: int, stream, *args) -> None:
             torch.cuda.set_device(had)
     if st != FA_OK:
         raise FAError(fn, st)
+
+
+def _again(status, fn: str, call, *args) -> None:
+    """After _fa_py: its nonzero status as an error, or, for None, the call with the checks here."""
+    if status is not None:
+        raise FAError(fn, status)
+    call(*args)
 
 
 def _record(stream, *tensors) -> None:
@@ -531,13 +550,17 @@ def fa_rope(q, q_out, positions, spec: RopeSpec, k=None, k_out=None, stream=None
     """q_out = q [B, Hq, T, d] (and k_out = k [B, Hk, T, d]) with their pairs turned by the
     positions, int32 [n_axes, B, T].  bf16 or float32; strided views with contiguous rows are
     taken as they are; an output may be its input."""
-    _rope("fa_rope", q, q_out, positions, spec, k, k_out, 0, stream)
+    st = _fa_py.rope(spec._ref, q, q_out, k, k_out, positions, 0, stream)
+    if st != FA_OK:
+        _again(st, "fa_rope", _rope, "fa_rope", q, q_out, positions, spec, k, k_out, 0, stream)
 
 
 def fa_rope_bwd(dq_out, dq, positions, spec: RopeSpec, k=None, k_out=None, stream=None) -> None:
     """Backward of fa_rope: dq, the gradient of q, from dq_out, the gradient of q_out (and
     k_out from k, the gradients of k and of the rotated k)."""
-    _rope("fa_rope_bwd", dq_out, dq, positions, spec, k, k_out, 1, stream)
+    st = _fa_py.rope(spec._ref, dq_out, dq, k, k_out, positions, 1, stream)
+    if st != FA_OK:
+        _again(st, "fa_rope_bwd", _rope, "fa_rope_bwd", dq_out, dq, positions, spec, k, k_out, 1, stream)
 
 
 def rope_forward(q, k, positions, spec: RopeSpec, stream=None):
@@ -619,6 +642,13 @@ def fa_cache_append(cache: KVCache, k, v, positions=None, spec: RopeSpec | None 
     """Writes the first new_lens[b] (default: all) of the T rows of k and v [B, Hkv, T, d] as the
     last entries of sequence b; cache.lens (and seen) count them already.  With a spec, k is
     rotated by positions [n_axes, B, T] on the way, and q [B, Hq, T, d] into q_out."""
+    st = _fa_py.append(cache._ref, cache._index, k, v, positions, None if spec is None else spec._ref, q, q_out, new_lens,
+                       stream)
+    if st != FA_OK:
+        _again(st, "fa_cache_append", _append, cache, k, v, positions, spec, q, q_out, new_lens, stream)
+
+
+def _append(cache, k, v, positions, spec, q, q_out, new_lens, stream) -> None:
     index, B, d = cache._index, cache.B, cache.d
     if k.dim() != 4 or (q is not None and q.dim() != 4):
         raise ValueError("k, v, q must be [B, H, T, d]")
@@ -658,6 +688,12 @@ def fa_decode_paged(cache: KVCache, q, o, lse, scale: float, workspace: torch.Te
                     accumulate: bool = False, stream=None) -> None:
     """O and lse of q [B, Hq, Tq, d] (the last Tq tokens of every sequence) over the cache; with
     `accumulate`, cache.weight grows by each entry's attention probabilities."""
+    st = _fa_py.decode(cache._ref, cache._index, q, o, lse, scale, workspace, causal, accumulate, stream)
+    if st != FA_OK:
+        _again(st, "fa_decode_paged", _decode, cache, q, o, lse, scale, workspace, causal, accumulate, stream)
+
+
+def _decode(cache, q, o, lse, scale, workspace, causal, accumulate, stream) -> None:
     dev, index, shape = cache.device, cache._index, q.shape
     if len(shape) != 4:
         raise ValueError("q must be [B, Hq, Tq, d]")
@@ -699,22 +735,28 @@ def fa_cache_evict(cache: KVCache, budget: int, weight_out=None, order_out=None,
     n_recent tokens, then those of the largest cache.weight.  K and V rows move in place; weight,
     order and lens are updated in place unless outputs are given.  Returns kept, int32
     [B, Hkv, budget]: the old slot of each entry, -1 behind the new length."""
-    dev = cache.device
     if cache.weight is None:
         raise ValueError("the cache has no weight")
     weight_out = cache.weight if weight_out is None else weight_out
     order_out = cache.order if order_out is None else order_out
     lens_out = cache.lens if lens_out is None else lens_out
+    if kept is None:
+        kept = torch.empty((cache.B, cache.Hkv, max(int(budget), 0)), dtype=torch.int32, device=cache.device)
+        _record(stream, kept)
+    st = _fa_py.evict(cache._ref, cache._index, budget, weight_out, order_out, lens_out, kept, n_first, n_recent, stream)
+    if st != FA_OK:
+        _again(st, "fa_cache_evict", _evict, cache, budget, weight_out, order_out, lens_out, kept, n_first, n_recent, stream)
+    return kept
+
+
+def _evict(cache, budget, weight_out, order_out, lens_out, kept, n_first, n_recent, stream) -> None:
+    dev = cache.device
     _need(weight_out, "weight_out", torch.float32, cache.weight.shape, dev)
     if (order_out is None) != (cache.order is None):
         raise ValueError("order_out: needed with a cache that has an order and only with it")
     if order_out is not None:
         _need(order_out, "order_out", torch.int32, cache.weight.shape, dev)
     _need(lens_out, "lens_out", torch.int32, (cache.B,), dev)
-    if kept is None:
-        kept = torch.empty((cache.B, cache.Hkv, max(int(budget), 0)), dtype=torch.int32, device=dev)
-        _record(stream, kept)
     _need(kept, "kept", torch.int32, (cache.B, cache.Hkv, budget), dev)
     _launch("fa_cache_evict", _lib.fa_cache_evict, cache._index, stream, cache._ref, int(budget), int(n_first),
             int(n_recent), weight_out.data_ptr(), _ptr(order_out), lens_out.data_ptr(), kept.data_ptr())
-    return kept

@@ -683,6 +683,50 @@ def test_evict_bad_lengths_and_pages(fa):
     assert torch.equal(moved[1], k0[p[6], 0, :4])
 
 
+# ---------------------------------------------------------------- the binding's two ways
+def test_both_ways_of_calling(fa):
+    """The compiled checks and the ones that say what is wrong make the same calls."""
+    g = gen(80)
+    spec = fa.rope_spec(64, (8, 24))
+    q, k = randn(g, 2, 4, 3, 64), randn(g, 2, 2, 3, 64)
+    pos = torch.randint(0, 99, (2, 2, 3), generator=g, device=DEV).to(I32)
+    out = []
+    for way in (0, 1):
+        cache = make_cache(fa, 81, [200, 77], 2, 64, 16, weight=True)
+        qo, ko, q2 = torch.empty_like(q), torch.empty_like(k), torch.empty_like(q)
+        o, lse = torch.empty_like(q), torch.empty((2, 4, 3), device=DEV)
+        ws = torch.empty(fa.fa_decode_paged_workspace_bytes(cache, 4, 3, True), dtype=torch.uint8, device=DEV)
+        kept = torch.empty((2, 2, 64), dtype=I32, device=DEV)
+        if way == 0:
+            fa.fa_rope(q, qo, pos, spec, k=k, k_out=ko)
+            fa.fa_cache_append(cache, k, k, pos, spec, q=q, q_out=q2)
+            fa.fa_decode_paged(cache, q2, o, lse, 0.125, ws, accumulate=True)
+            fa.fa_cache_evict(cache, 64, kept=kept, n_recent=3)
+        else:
+            fa._rope("fa_rope", q, qo, pos, spec, k, ko, 0, None)
+            fa._append(cache, k, k, pos, spec, q, q2, None, torch.cuda.current_stream())
+            fa._decode(cache, q2, o, lse, 0.125, ws, True, True, torch.cuda.current_stream().cuda_stream)
+            fa._evict(cache, 64, cache.weight, cache.order, cache.lens, kept, 0, 3, None)
+        assert fa.fa_sync_status() == fa.FA_OK
+        out.append([qo, ko, q2, o, lse, kept, cache.k.view(torch.uint8), cache.weight, cache.order, cache.lens])
+    assert all(torch.equal(a, b) for a, b in zip(*out))
+    # the compiled way refuses by None, not by a wrong call; a status comes back as an error
+    assert fa._fa_py.rope(spec._ref, q.half(), q, None, None, pos, 0, None) is None
+    assert fa._fa_py.rope(spec._ref, q, q[:, :3], None, None, pos, 0, None) is None
+    assert fa._fa_py.rope(spec._ref, q, q, None, None, pos.long(), 0, None) is None
+    assert fa._fa_py.rope(spec._ref, q.cpu(), q.cpu(), None, None, pos.cpu(), 0, None) is None
+    assert fa._fa_py.append(cache._ref, cache._index, k, q, None, None, None, None, None, None) is None
+    assert fa._fa_py.decode(cache._ref, cache._index, q, o, lse.half(), 0.1, ws, True, False, None) is None
+    assert fa._fa_py.decode(cache._ref, cache._index, q, o, lse, 0.1, "no", True, False, None) is None
+    assert fa._fa_py.evict(cache._ref, cache._index, 63, cache.weight, cache.order, cache.lens, kept, 0, 0, None) is None
+    with pytest.raises(fa.FAError):
+        fa.fa_decode_paged(cache, q, o, lse, -1.0, ws)
+    with pytest.raises(TypeError):
+        fa.fa_rope(q.half(), qo, pos, spec)
+    with pytest.raises(ValueError):
+        fa.fa_cache_append(cache, k, q)
+
+
 # ---------------------------------------------------------------- nothing outside the buffers
 class Guarded:
     """Buffers in the middle of larger ones; `intact()`: nothing around them was written."""
