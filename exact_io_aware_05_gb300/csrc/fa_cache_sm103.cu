@@ -1067,10 +1067,8 @@ int evict_launch(const fa_kv_cache &c, int budget, int n_first, int n_recent, fl
         if (cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  kSelFixed + kSelCap * 6) != cudaSuccess)
             return ERR_CUDA;
-        // not overlapped with the kernel before it: clusters that wait on the SMs were in its way (20 us
-        // instead of 16.5 for the first case above)
         const int st = launch_overlapped(evict_select_kernel, dim3((unsigned)(units * cs)), kPickThreads, kSelFixed + per * 6,
-                                         cs, false, s, a, cs, per);
+                                         cs, true, s, a, cs, per);
         if (st != OK || lens_out != c.lens)
             return st;
         return launch_overlapped(evict_lens_kernel, dim3((unsigned)((c.B + 255) / 256)), 256, 0, 0, true, s, a);
