@@ -496,11 +496,21 @@ def _again(status, fn: str, call, *args) -> None:
     call(*args)
 
 
-def _record(stream, *tensors) -> None:
-    """Tells the allocator that tensors allocated here are used on `stream`."""
-    if stream is not None and hasattr(stream, "cuda_stream"):
-        for t in tensors:
-            t.record_stream(stream)
+def _empties(stream, device, *specs) -> list:
+    """torch.empty of each (shape, dtype), for a call on `stream`.  They are of that stream's memory: a
+    block that was freed on the current stream may still be in use there.  The caller goes on with them
+    on the current stream, so that one is recorded."""
+    if stream is None or device.type != "cuda":
+        return [torch.empty(shape, dtype=dtype, device=device) for shape, dtype in specs]
+    if not isinstance(stream, torch.cuda.Stream):
+        raw = _stream(stream)
+        stream = torch.cuda.ExternalStream(raw, device=device) if raw else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        out = [torch.empty(shape, dtype=dtype, device=device) for shape, dtype in specs]
+    here = torch.cuda.current_stream(device)
+    for t in out:
+        t.record_stream(here)
+    return out
 
 
 def _heads(t: torch.Tensor, name: str, dtype, shape, index: int) -> tuple:
@@ -565,17 +575,15 @@ def fa_rope_bwd(dq_out, dq, positions, spec: RopeSpec, k=None, k_out=None, strea
 
 def rope_forward(q, k, positions, spec: RopeSpec, stream=None):
     """Allocates contiguous outputs and runs fa_rope on q and k: what fa_fwd takes."""
-    q_out, k_out = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k))
+    q_out, k_out = _empties(stream, q.device, (q.shape, q.dtype), (k.shape, k.dtype))
     fa_rope(q, q_out, positions, spec, k, k_out, stream)
-    _record(stream, q_out, k_out)
     return q_out, k_out
 
 
 def rope_backward(dq_out, dk_out, positions, spec: RopeSpec, stream=None):
     """Allocates and returns the gradients of q and k from those of rope_forward's outputs."""
-    dq, dk = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (dq_out, dk_out))
+    dq, dk = _empties(stream, dq_out.device, (dq_out.shape, dq_out.dtype), (dk_out.shape, dk_out.dtype))
     fa_rope_bwd(dq_out, dq, positions, spec, dk_out, dk, stream)
-    _record(stream, dq, dk)
     return dq, dk
 
 
@@ -719,13 +727,12 @@ def attention_decode_paged(cache: KVCache, q, scale: float, causal: bool = True,
     """Allocates O, lse (and the workspace if not given) and runs fa_decode_paged."""
     if q.dim() != 4:
         raise ValueError("q must be [B, Hq, Tq, d]")
-    o = torch.empty_like(q)
-    lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+    specs = [(q.shape, q.dtype), (q.shape[:3], torch.float32)]
     if workspace is None:
         n = fa_decode_paged_workspace_bytes(cache, q.shape[1], q.shape[2], accumulate)
-        workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
-    fa_decode_paged(cache, q, o, lse, scale, workspace, causal, accumulate, stream)
-    _record(stream, o, lse, workspace)
+        specs.append(((max(n, 256),), torch.uint8))
+    o, lse, *own = _empties(stream, q.device, *specs)
+    fa_decode_paged(cache, q, o, lse, scale, own[0] if own else workspace, causal, accumulate, stream)
     return o, lse
 
 
@@ -741,8 +748,7 @@ def fa_cache_evict(cache: KVCache, budget: int, weight_out=None, order_out=None,
     order_out = cache.order if order_out is None else order_out
     lens_out = cache.lens if lens_out is None else lens_out
     if kept is None:
-        kept = torch.empty((cache.B, cache.Hkv, max(int(budget), 0)), dtype=torch.int32, device=cache.device)
-        _record(stream, kept)
+        kept, = _empties(stream, cache.device, ((cache.B, cache.Hkv, max(int(budget), 0)), torch.int32))
     st = _fa_py.evict(cache._ref, cache._index, budget, weight_out, order_out, lens_out, kept, n_first, n_recent, stream)
     if st != FA_OK:
         _again(st, "fa_cache_evict", _evict, cache, budget, weight_out, order_out, lens_out, kept, n_first, n_recent, stream)

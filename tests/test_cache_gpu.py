@@ -378,6 +378,36 @@ def test_decode_two_streams(fa):
         assert all(torch.equal(x, y) for x, y in zip(ga + gb, ref_a + ref_b))
 
 
+@pytest.mark.parametrize("raw", [False, True])
+def test_allocating_calls_on_another_stream(fa, raw):
+    """The current stream still works on blocks that it has freed: what a call on another stream
+    allocates must not be one of them."""
+    cache = make_cache(fa, 5, [70, 33], 2, 64, 16, weight=True)
+    q = randn(gen(6), 2, 8, 1, 64)
+    k = randn(gen(7), 2, 2, 1, 64)
+    spec = fa.rope_spec(64)
+    pos = torch.arange(2, dtype=torch.int32, device="cuda").view(1, 2, 1)
+    want = [*fa.attention_decode_paged(cache, q, 0.1), *fa.rope_forward(q, k, pos, spec), *fa.rope_backward(q, k, pos, spec)]
+    other = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for run in (lambda s: fa.attention_decode_paged(cache, q, 0.1, stream=s),
+                lambda s: fa.rope_forward(q, k, pos, spec, stream=s), lambda s: fa.rope_backward(q, k, pos, spec, stream=s)):
+        torch.cuda._sleep(20_000_000)
+        junk = [torch.full((n,), 0x55, dtype=torch.uint8, device="cuda") for n in (128, 512, 2048) for _ in range(20)]
+        del junk   # the blocks are free again, and the fills still wait
+        got = run(other.cuda_stream if raw else other)
+        torch.cuda.current_stream().wait_stream(other)
+        torch.cuda.synchronize()
+        for x in got:
+            assert torch.equal(x, want.pop(0))
+    torch.cuda._sleep(20_000_000)
+    junk = [torch.full((64,), 0x55, dtype=torch.uint8, device="cuda") for _ in range(20)]
+    del junk
+    kept = fa.fa_cache_evict(cache, 3, stream=other.cuda_stream if raw else other)
+    torch.cuda.synchronize()
+    assert int(kept.min()) >= 0 and int(kept.max()) < 70 and cache.lens.tolist() == [3, 3]
+
+
 def test_decode_bad_lengths_and_pages(fa):
     """A length outside the table counts as empty, a page outside the pool as masked; both are
     reported and never read."""
