@@ -184,15 +184,15 @@ __device__ __forceinline__ float quad_sum(float x)
 }
 
 // ------------------------------------------------------------------ shares
-__device__ __forceinline__ int length_of(const PagedArgs &a, int b)
+__device__ __forceinline__ int length_in_range(const PagedArgs &a, int len)
 {
-    const int len = a.lens[b];
     if (len < 0 || len > a.cap) {
         atomicCAS(&g_paged_status, 0, kStatusBadIndex);
         return 0;
     }
     return len;
 }
+__device__ __forceinline__ int length_of(const PagedArgs &a, int b) { return length_in_range(a, a.lens[b]); }
 __device__ __forceinline__ int tiles_of(const PagedArgs &a, int b) { return (length_of(a, b) + a.kt - 1) / a.kt; }
 
 // Tiles a CTA takes of the batch's `total`: equal shares, but at least 128 entries, below which
@@ -861,11 +861,11 @@ struct Parts {
     bool none;   // no entry at all
 };
 
-__device__ __forceinline__ Parts parts_of(const PagedArgs &a, int b, int ul, int nt)
+__device__ __forceinline__ Parts parts_of(long long share, long long first, int ul, int nt)   // a.where[0], [1 + b]
 {
     Parts p{0, 0, 0, nt == 0};
     if (nt > 0) {
-        const long long share = a.where[0], t = a.where[1 + b] + (long long)ul * nt;
+        const long long t = first + (long long)ul * nt;
         p.c0 = (int)(t / share);
         p.c1 = (int)((t + nt - 1) / share);
         p.s0 = 2ll * p.c0 + (t == p.c0 * share ? 0 : 1);
@@ -881,7 +881,7 @@ constexpr int kJoinThreads = 128, kWeightRun = 4 * kJoinThreads;
 constexpr int kMaxCtas = 3 * kSMs, kMaxParts = kMaxCtas;
 
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedArgs a, int wchunks, int rpb)
+__global__ void __launch_bounds__(kJoinThreads, 8) paged_join_kernel(const __grid_constant__ PagedArgs a, int wchunks, int rpb)
 {
     __shared__ float wt[kMaxParts], row_lse[kMaxRows], sums[kJoinThreads * 2], red[8];
     const int tid = threadIdx.x, per = a.Hkv * a.RB;
@@ -889,26 +889,48 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
     const long long rows_total = (long long)a.B * per * bpu, blk = blockIdx.x;
     const long long stride = (long long)a.rows * (D + 2);
     pdl_launch();
+    const bool joins = blk < rows_total;
+    const long long unit = joins ? blk / bpu : (blk - rows_total) / wchunks;   // or, for weights, (sequence, KV head)
+    const int b = (int)(unit / (joins ? per : a.Hkv)), ul = (int)(unit - (long long)b * (joins ? per : a.Hkv)), h = ul % a.Hkv;
+    // The lengths may be read in front of the wait: this kernel is launched when every CTA of the
+    // attention is past its own wait (or after the kernel before this one has ended).  All that it wrote is read behind
+    // the wait, in two steps: the place, then everything of the states at once (loads that wait for one
+    // another cost 0.7 us each).
+    const int len = length_in_range(a, __ldcg(a.lens + b)), nt = (len + a.kt - 1) / a.kt;
     pdl_wait();
-    if (a.may_whole && a.where[0] == 0)
+    const long long share = a.where[0], place = a.where[1 + b];
+    if (a.may_whole && share == 0)
         return;   // whole units: nothing is left to do
-    if (blk < rows_total) {
-        const long long unit = blk / bpu;
-        const int first = (int)(blk - unit * bpu) * rpb;
-        const int b = (int)(unit / per), ul = (int)(unit - (long long)b * per), h = ul % a.Hkv, rb = ul / a.Hkv;
-        const Parts p = parts_of(a, b, ul, tiles_of(a, b));
+    if (joins) {
+        const int first = (int)(blk - unit * bpu) * rpb, rb = ul / a.Hkv;
+        const Parts p = parts_of(share, place, ul, nt);
         if (!p.none && p.c0 == p.c1)
             return;
         for (int row = first; row < min(first + rpb, min(a.rows, a.M - rb * a.rows)); ++row) {
             const long long grow = ((long long)b * a.Hq + h * a.G) * a.Tq + rb * a.rows + row;
             auto slot = [&](int i) { return a.part + (i == 0 ? p.s0 : 2ll * (p.c0 + i)) * stride; };
             const int n = p.none ? 0 : p.c1 - p.c0 + 1;
+            constexpr int GROUPS = 2 * kJoinThreads / D;   // states under way
+            constexpr int PER = (kMaxParts + kJoinThreads - 1) / kJoinThreads, AHEAD = 8;
+            const int g = tid / (D / 2), f = 2 * (tid % (D / 2));
+            float mi[PER], li[PER];
+            float2 y[AHEAD];
+#pragma unroll
+            for (int u = 0; u < PER; ++u) {
+                const int i = tid + u * kJoinThreads;
+                mi[u] = i < n ? slot(i)[(long long)a.rows * D + row] : -INFINITY;
+                li[u] = i < n ? slot(i)[(long long)a.rows * (D + 1) + row] : 0.f;
+            }
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u) {
+                const int i = g + u * GROUPS;
+                y[u] = i < n ? *reinterpret_cast<const float2 *>(slot(i) + (long long)row * D + f) : make_float2(0.f, 0.f);
+            }
             // the states' maxima, then their weights
             float m = -INFINITY, l = 0.f;
-            for (int i = tid; i < n; i += kJoinThreads) {
-                wt[i] = slot(i)[(long long)a.rows * D + row];
-                m = fmaxf(m, wt[i]);
-            }
+#pragma unroll
+            for (int u = 0; u < PER; ++u)
+                m = fmaxf(m, mi[u]);
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1)
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
@@ -916,10 +938,13 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
                 red[warp_id()] = m;
             __syncthreads();
             m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-            for (int i = tid; i < n; i += kJoinThreads) {
-                const float w = wt[i] == -INFINITY ? 0.f : ex2_approx(wt[i] - m);
-                l = fmaf(w, slot(i)[(long long)a.rows * (D + 1) + row], l);
-                wt[i] = w;
+#pragma unroll
+            for (int u = 0; u < PER; ++u) {
+                const int i = tid + u * kJoinThreads;
+                const float w = mi[u] == -INFINITY ? 0.f : ex2_approx(mi[u] - m);
+                l = fmaf(w, li[u], l);
+                if (i < n)
+                    wt[i] = w;
             }
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1)
@@ -928,23 +953,28 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
                 red[4 + warp_id()] = l;
             __syncthreads();
             l = (red[4] + red[5]) + (red[6] + red[7]);
-            constexpr int GROUPS = 2 * kJoinThreads / D;   // states under way
-            const int g = tid / (D / 2), f = 2 * (tid % (D / 2));
             float2 x = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u) {
+                const int i = g + u * GROUPS;
+                const float w = i < n ? wt[i] : 0.f;
+                x.x = fmaf(w, y[u].x, x.x);
+                x.y = fmaf(w, y[u].y, x.y);
+            }
 #pragma unroll 8
-            for (int i = g; i < n; i += GROUPS) {
-                const float2 y = *reinterpret_cast<const float2 *>(slot(i) + (long long)row * D + f);
-                x.x = fmaf(wt[i], y.x, x.x);
-                x.y = fmaf(wt[i], y.y, x.y);
+            for (int i = g + AHEAD * GROUPS; i < n; i += GROUPS) {
+                const float2 z = *reinterpret_cast<const float2 *>(slot(i) + (long long)row * D + f);
+                x.x = fmaf(wt[i], z.x, x.x);
+                x.y = fmaf(wt[i], z.y, x.y);
             }
             reinterpret_cast<float2 *>(sums)[tid] = x;
             __syncthreads();
             if (g == 0) {
 #pragma unroll
                 for (int w = 1; w < GROUPS; ++w) {
-                    const float2 y = reinterpret_cast<const float2 *>(sums)[w * (D / 2) + tid];
-                    x.x += y.x;
-                    x.y += y.y;
+                    const float2 z = reinterpret_cast<const float2 *>(sums)[w * (D / 2) + tid];
+                    x.x += z.x;
+                    x.y += z.y;
                 }
                 const float k = l == 0.f ? 0.f : 1.f / l;
                 *reinterpret_cast<uint32_t *>(a.o + grow * D + f) = pack_bf16x2(x.x * k, x.y * k);
@@ -956,14 +986,13 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
         return;
     }
     // ---- weight_j += sum over the rows of p_j = 2^{s_j - lse}, four neighbours a thread
-    const long long wb = blk - rows_total, uh = wb / wchunks;
-    const int b = (int)(uh / a.Hkv), h = (int)(uh - (long long)b * a.Hkv), len = length_of(a, b);
-    const int j = (int)(wb - uh * wchunks) * kWeightRun + 4 * tid;
+    const long long uh = unit;
+    const int j = (int)(blk - rows_total - uh * wchunks) * kWeightRun + 4 * tid;
     if (j - 4 * tid >= len)
         return;
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int rb = 0; rb < a.RB; ++rb) {
-        const Parts p = parts_of(a, b, rb * a.Hkv + h, (len + a.kt - 1) / a.kt);
+        const Parts p = parts_of(share, place, rb * a.Hkv + h, nt);
         const int row0 = rb * a.rows, nrows = min(a.rows, a.M - row0);
         for (int r = tid; r < nrows; r += kJoinThreads) {
             float y;
@@ -1069,7 +1098,7 @@ int paged_run(const fa_kv_cache &c, PagedArgs &a, cudaStream_t s)
     const long long blocks = units * ((a.rows + rpb - 1) / rpb) + (long long)a.B * a.Hkv * wchunks;
     if (blocks > INT_MAX)
         return ERR_UNSUPPORTED;
-    return launch_overlapped(paged_join_kernel<D>, dim3((unsigned)blocks), kJoinThreads, 0, 0, true, s, a, wchunks, rpb);
+    return launch_overlapped(paged_join_kernel<D>, dim3((unsigned)blocks), kJoinThreads, 0, 0, most > 0, s, a, wchunks, rpb);
 }
 
 }  // namespace
