@@ -70,7 +70,7 @@ struct Cfg {
     static constexpr int QPITCH = D * 2 + 16;                      // bytes of a query row in shared memory
     static constexpr int MR = 512 / D;                             // rows of a row tile merged at a time
     static constexpr int OPITCH = D + 4;                           // floats of a merge row
-    static constexpr int NQ = RT * 16 * QPITCH, NO = kMathWarps * MR * OPITCH * 4, NML = kMathWarps * 16 * 8;
+    static constexpr int NQ = RT * 16 * QPITCH, NO = RT < kMathWarps ? kMathWarps * MR * OPITCH * 4 : 0, NML = kMathWarps * 16 * 8;
     static constexpr int SMALL = 1024 + NQ + NO + NML + RT * 16 * 4 + 24 * 12 + 64;
     // as many CTAs an SM as the accumulators leave registers for and the ring has room; the
     // ring takes what is left
@@ -767,78 +767,114 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
                 ml[warp * 16 + r0 + 8] = make_float2(m1, s1);
             }
             math_sync();
-            auto top = [&](int rt_, int r) {   // largest of a row's maxima
-                float x = -INFINITY;
-#pragma unroll
-                for (int w = 0; w < KW; ++w)
-                    x = fmaxf(x, ml[(w * RT + rt_) * 16 + r].x);
-                return x;
-            };
-            auto weight = [](float m, float t) { return m == -INFINITY ? 0.f : ex2_approx(m - t); };
-            const float f0 = weight(m0, top(rt, r0)), f1 = weight(m1, top(rt, r0 + 8));
             const bool entire = p.tile == 0 && cnt == p.nt;   // all of the unit
             const long long slot = 2ll * blockIdx.x + (p.left == mine_all ? 0 : 1);
             float *part = a.part + slot * a.rows * (D + 2);
             const float vs = FP8 ? a.vs[h] : 1.f;
-            constexpr int MR = C::MR;
-#pragma unroll 1
-            for (int first = 0; first < min(16, nrows); first += MR) {
-                if (r0 / MR == (first & 7) / MR) {
-                    float *mine = ob + (warp * MR + r0 % MR) * C::OPITCH;
-                    const bool low = first < 8;
-                    const float f = low ? f0 : f1;
+            // the factor of this warp's sums in row r's output (or, scaled by vs, in its partial state); one
+            // warp of the row tile writes the row's statistics
+            auto factor = [&](int r, float m) {
+                float t = -INFINITY, l = 0.f;
 #pragma unroll
-                    for (int x = 0; x < D / 8; x += 2) {
-                        const float a0 = (low ? o[x][0] : o[x][2]) * f, a1 = (low ? o[x][1] : o[x][3]) * f;
-                        const float b0 = (low ? o[x + 1][0] : o[x + 1][2]) * f, b1 = (low ? o[x + 1][1] : o[x + 1][3]) * f;
-                        if constexpr (!FP8) {
-                            *reinterpret_cast<float2 *>(mine + 8 * x + 2 * c4) = make_float2(a0, a1);
-                            *reinterpret_cast<float2 *>(mine + 8 * x + 8 + 2 * c4) = make_float2(b0, b1);
-                        } else {   // even and odd features of a 16-feature unit
-                            *reinterpret_cast<float4 *>(mine + 8 * x + 4 * c4) = make_float4(a0, b0, a1, b1);
-                        }
+                for (int w = 0; w < KW; ++w)
+                    t = fmaxf(t, ml[(w * RT + rt) * 16 + r].x);
+                const float z = t == -INFINITY ? 0.f : t;
+#pragma unroll
+                for (int w = 0; w < KW; ++w) {
+                    const float2 y = ml[(w * RT + rt) * 16 + r];
+                    l = fmaf(y.y, ex2_approx(y.x - z), l);
+                }
+                const int row = rt * 16 + r;
+                if (kw == 0 && c4 == 0 && row < nrows && ok) {
+                    if (entire) {
+                        const float y = t + log2f(l);   // -inf if l is 0
+                        a.lse[grow + row] = l == 0.f ? -INFINITY : y * 0.69314718055994530942f;
+                        row_lse[row] = l == 0.f ? 0.f : y;   // a row that saw nothing has no finite score either
+                    } else {
+                        part[(long long)a.rows * D + row] = t;
+                        part[(long long)a.rows * (D + 1) + row] = l;
                     }
                 }
-                math_sync();
+                return ex2_approx(m - z) * (entire ? (l == 0.f ? 0.f : vs / l) : vs);
+            };
+            const float f0 = factor(r0, m0), f1 = factor(r0 + 8, m1);
+            if constexpr (KW == 1) {   // a row is one warp's: out of its registers
 #pragma unroll
-                for (int e = 0; e < RT; ++e) {   // four features of one row a thread: RT * MR rows of D
-                    const int at = e * 128 + (int)threadIdx.x, k = at / (D / 4), col = (at % (D / 4)) * 4;
-                    const int rt_ = k / MR, r = first + k % MR, row = rt_ * 16 + r;
+                for (int half = 0; half < 2; ++half) {
+                    const int row = rt * 16 + r0 + 8 * half;
                     if (row >= nrows || !ok)
                         continue;
-                    const float t = top(rt_, r);
-                    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-                    float l = 0.f;
+                    const float f = half ? f1 : f0;
+                    uint32_t *dst = reinterpret_cast<uint32_t *>(a.o + (grow + row) * D) + (FP8 ? 2 * c4 : c4);
+                    // 8-byte stores: a slot of `rows` (D + 2) floats is a multiple of 8 bytes
+                    float2 *pd = reinterpret_cast<float2 *>(part + (long long)row * D) + (FP8 ? 2 * c4 : c4);
 #pragma unroll
-                    for (int w = 0; w < KW; ++w) {
-                        const float4 y = *reinterpret_cast<const float4 *>(ob + ((w * RT + rt_) * MR + k % MR) * C::OPITCH + col);
-                        x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
-                        const float2 z = ml[(w * RT + rt_) * 16 + r];
-                        l = fmaf(z.y, weight(z.x, t), l);
-                    }
-                    const float g = entire ? (l == 0.f ? 0.f : vs / l) : vs;
-                    if (entire) {
-                        uint2 y;
-                        y.x = pack_bf16x2(x.x * g, x.y * g);
-                        y.y = pack_bf16x2(x.z * g, x.w * g);
-                        *reinterpret_cast<uint2 *>(a.o + (grow + row) * D + col) = y;
-                        if (col == 0) {
-                            const float y = t + log2f(l);   // -inf if l is 0
-                            a.lse[grow + row] = l == 0.f ? -INFINITY : y * 0.69314718055994530942f;
-                            row_lse[row] = l == 0.f ? 0.f : y;   // a row that saw nothing has no finite score either
-                        }
-                    } else {
-                        // 8-byte stores: a slot of `rows` (D + 2) floats is a multiple of 8 bytes
-                        float2 *dst = reinterpret_cast<float2 *>(part + (long long)row * D + col);
-                        dst[0] = make_float2(x.x * g, x.y * g);
-                        dst[1] = make_float2(x.z * g, x.w * g);
-                        if (col == 0) {
-                            part[(long long)a.rows * D + row] = t;
-                            part[(long long)a.rows * (D + 1) + row] = l;
+                    for (int x = 0; x < D / 8; x += 2) {
+                        const float a0 = o[x][2 * half] * f, a1 = o[x][2 * half + 1] * f;
+                        const float b0 = o[x + 1][2 * half] * f, b1 = o[x + 1][2 * half + 1] * f;
+                        if constexpr (!FP8) {
+                            if (entire) {
+                                dst[4 * x] = pack_bf16x2(a0, a1);
+                                dst[4 * x + 4] = pack_bf16x2(b0, b1);
+                            } else {
+                                pd[4 * x] = make_float2(a0, a1);
+                                pd[4 * x + 4] = make_float2(b0, b1);
+                            }
+                        } else {   // even and odd features of a 16-feature unit
+                            if (entire) {
+                                *reinterpret_cast<uint2 *>(dst + 4 * x) = make_uint2(pack_bf16x2(a0, b0), pack_bf16x2(a1, b1));
+                            } else {
+                                pd[4 * x] = make_float2(a0, b0);
+                                pd[4 * x + 1] = make_float2(a1, b1);
+                            }
                         }
                     }
                 }
-                math_sync();
+                math_sync();   // before the next unit's rows and states
+            } else {
+                constexpr int MR = C::MR;
+#pragma unroll 1
+                for (int first = 0; first < min(16, nrows); first += MR) {
+                    if (r0 / MR == (first & 7) / MR) {
+                        float *mine = ob + (warp * MR + r0 % MR) * C::OPITCH;
+                        const bool low = first < 8;
+                        const float f = low ? f0 : f1;
+#pragma unroll
+                        for (int x = 0; x < D / 8; x += 2) {
+                            const float a0 = (low ? o[x][0] : o[x][2]) * f, a1 = (low ? o[x][1] : o[x][3]) * f;
+                            const float b0 = (low ? o[x + 1][0] : o[x + 1][2]) * f, b1 = (low ? o[x + 1][1] : o[x + 1][3]) * f;
+                            if constexpr (!FP8) {
+                                *reinterpret_cast<float2 *>(mine + 8 * x + 2 * c4) = make_float2(a0, a1);
+                                *reinterpret_cast<float2 *>(mine + 8 * x + 8 + 2 * c4) = make_float2(b0, b1);
+                            } else {
+                                *reinterpret_cast<float4 *>(mine + 8 * x + 4 * c4) = make_float4(a0, b0, a1, b1);
+                            }
+                        }
+                    }
+                    math_sync();
+#pragma unroll
+                    for (int e = 0; e < RT; ++e) {   // four features of one row a thread: RT * MR rows of D
+                        const int at = e * 128 + (int)threadIdx.x, k = at / (D / 4), col = (at % (D / 4)) * 4;
+                        const int rt_ = k / MR, row = rt_ * 16 + first + k % MR;
+                        if (row >= nrows || !ok)
+                            continue;
+                        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                        for (int w = 0; w < KW; ++w) {
+                            const float4 y = *reinterpret_cast<const float4 *>(ob + ((w * RT + rt_) * MR + k % MR) * C::OPITCH + col);
+                            x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+                        }
+                        if (entire) {
+                            *reinterpret_cast<uint2 *>(a.o + (grow + row) * D + col) =
+                                make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+                        } else {
+                            float2 *dst = reinterpret_cast<float2 *>(part + (long long)row * D + col);
+                            dst[0] = make_float2(x.x, x.y);
+                            dst[1] = make_float2(x.z, x.w);
+                        }
+                    }
+                    math_sync();
+                }
             }
             // ---- one CTA has the whole unit, its scores too: weight_j += sum over the rows of
             // p_j = 2^{s_j - lse}, four neighbours a thread
