@@ -29,9 +29,9 @@
 //
 // Measured: 8 sequences of 32768 entries, 32 KV heads, d 128 (4.3 GB) 589 us, 7.3 TB/s; 64 sequences of 200 to
 // 8000, 8 KV heads (1.1 GB) 165 us, 6.5 TB/s; 17 entries of one sequence 3.6 us.  Of the second, 3 us pass
-// before the first load, 5 with the join, and the CTAs end within 10 % of one another, with the
-// tensor pipe 28 % and the issue slots 22 % busy.  By rows (160 units of 2048 to 4096, d 128): 48, 54, 65 and
-// 106 us with 4, 16, 32 and 64; e4m3, twice as long: 50, 58, 97 and 176, its codes being converted by
+// before the first load, 3 to 4 with the join, and the CTAs end within 10 % of one another, with the
+// tensor pipe 28 % and the issue slots 22 % busy.  By rows (160 units of 2048 to 4096, d 128): 46, 51, 61 and
+// 101 us with 4, 16, 32 and 64; e4m3, twice as long: 48, 54, 91 and 163, its codes being converted by
 // every row tile.
 #include <algorithm>
 #include <climits>
@@ -226,10 +226,13 @@ __device__ __forceinline__ long long warp_scan(long long x)   // sum over the la
 // itself: the loads of the others are in the same cache lines, and a block-wide sum would cost
 // barriers at a time when nothing is under way.
 // whole: every unit is one CTA's, because there are enough CTAs and the longest unit is at most a
-// quarter and 4 tiles longer than an equal share: a CTA whose neighbours have ended gets more of the
-// bandwidth, and there are no second units to start and nothing to join (256 units of 1024, 2048 and
-// 4096 entries, d 128: 26.5, 45.3 and 83.4 us against 30.8, 50.2 and 89.2; but 144 units of 1000 to 3000,
-// d 256, half longer than a share: 61.6 against 56.1).
+// quarter, or 7 tiles (4 with three CTAs an SM, where one by itself gains less), longer than an equal share,
+// and not twice as long: a CTA whose neighbours have ended gets more
+// of the bandwidth, and there are no second units to start and nothing to join.  us whole and in shares, by
+// tiles of the longest unit / of a share: 296 units, d 128, 16/9 21.8 and 29.9, 18/16 29.6 and 32.4, 27/17 33.6 and
+// 33.4, 63/33 63.8 and 57.9; 256 units, 64/54 82.9 and 87.5; 120 units, 18/7 20.7 and 18.0; 8 units, 4/2 7.6
+// and 7.9, 6/2 9.0 and 8.0; e4m3, 296 units, 9/9 19.8 and 25.0, 200 units, 12/6 21.5 and 20.2; 144 units, d 256,
+// 21/16 30.8 and 31.6, 63/46 77.8 and 72.3; 240 units, e4m3 d 64, 16/9 27.2 and 22.8, 296 units, 9/6 18.2 and 19.5.
 __device__ __forceinline__ Place place_of(const PagedArgs &a, long long &share, long long &t0, bool &whole)
 {
     const int per = a.Hkv * a.RB, lane = (int)lane_id();
@@ -253,7 +256,8 @@ __device__ __forceinline__ Place place_of(const PagedArgs &a, long long &share, 
     longest = __reduce_max_sync(0xffffffffu, longest);
     share = total < INT_MAX ? share_of(a, (int)total) : share_of(a, total);
     Place p{a.B, 0, 0, 0, 0};
-    if (a.may_whole && longest <= share + share / 4 + 4) {
+    const long long more = max(share >> 2, a.grid > 2 * kSMs ? 4ll : 7ll), most = (share * 13 >> 4) + 1;
+    if (a.may_whole && longest <= share + min(more, most)) {
         whole = true;
         if ((int)blockIdx.x < a.B * per) {
             p.b = (int)blockIdx.x / per;
@@ -519,6 +523,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
         };
         uint32_t st = 0, round = 0;   // the next tile's stage, and its round
         bool ok = true;
+        // All CTAs are there, and the join's blocks take nothing from them (0.2 to 0.4 us); where no join
+        // follows, the next call's do (240 units of 512 14.1 us instead of 13.2)
+        if (whole && !a.whole)
+            pdl_launch();
         if (RT == 1 && p.left > 0)
             fetch_q(p);
         if (p.left == 0) {   // whole units: an empty sequence
@@ -1065,8 +1073,9 @@ int row_tiles(int M) { return M <= 16 ? 1 : M <= 32 ? 2 : 4; }
 
 
 // Tables of up to this many slots (half at d 256): one CTA a unit and no join.  8 units of 256, 512 and
-// 1024 entries, d 128: 5.7, 8.5 and 13.9 us against 8.2, 8.5 and 8.9 in shares; d 256: 7.6, 11.7 and
-// 20.0 against 9.4, 10.2 and 9.9.
+// 1024 entries, d 64: 4.7, 6.7 and 10.4 us against 7.2, 7.2 and 7.2 in shares; d 128: 6.0, 8.5 and 14.0
+// against 7.9, 8.0 and 8.0; d 256: 7.5, 11.5 and 19.3 against 8.7, 8.7 and 8.9.  240 units of 512, d 128: 13.2
+// against 20.1.
 constexpr int kWholeSlots = 512;
 
 size_t where_bytes(int B) { return round256((size_t)(B + 1) * sizeof(long long)); }
