@@ -16,22 +16,25 @@
 //     as even as shares would be, are taken a unit a CTA, and nothing is left to join.
 //   * One warp fills a ring of tiles by TMA, a box per page (all 128-byte column chunks of its
 //     rows at once, swizzled); page numbers are read one tile ahead.
-//   * Four warps compute with m16n8k16 products out of registers (ldmatrix): a warp owns 16 query
-//     rows and a quarter, half or all of a tile's entries (1, 2 or 4 row tiles).  The tensor cores
-//     of the fifth generation want 128 rows a product: with up to 16 rows, the usual case, they
-//     would run nearly empty, and their accumulators would have to come back for the softmax, where
-//     the warp-level products leave S in the registers that P V takes.  At 64 rows these products
-//     are the bound (see below).
+//   * Four warps compute with m16n8k16 products out of registers (ldmatrix): a warp owns up to 16 query
+//     rows and a quarter, half or all of a tile's entries (1, 2 or 4 row tiles).  They reach 200 to 270
+//     TFLOP/s in all, about what e4m3 needs with 16 rows a product.  So up to 8 rows the operands
+//     change places, K and V^T being the 16 rows and the queries the 8 columns, and half the products
+//     do (e4m3, 16 sequences of 1001 to 65536, d 64 55.5 -> 53.6 us; 160 units of 2048 to 4096, d 256 65 -> 52).
+//     The tensor cores of the fifth generation want 128 rows a product: with up to 16 rows, the usual
+//     case, they would run nearly empty, and their accumulators would have to come back for the
+//     softmax, where the warp-level products leave S in the registers that P V takes.  At 64 rows
+//     these products are the bound (see below).
 //   * P enters its product as two bf16 numbers (its leading 8 bits and the rest), so its error is
 //     2^-17 and not 2^-9, which would be as large as the output's own rounding.  e4m3 codes become
 //     f16 exactly; there q is scaled by a power of two per row and P by 2^15, which keeps
 //     probabilities down to 2^-29 in f16's normal range, with 11 bits.
 //
-// Measured: 8 sequences of 32768 entries, 32 KV heads, d 128 (4.3 GB) 589 us, 7.3 TB/s; 64 sequences of 200 to
-// 8000, 8 KV heads (1.1 GB) 165 us, 6.5 TB/s; 17 entries of one sequence 3.6 us.  Of the second, 3 us pass
+// Measured: 8 sequences of 32768 entries, 32 KV heads, d 128 (4.3 GB) 594 us, 7.2 TB/s; 64 sequences of 200 to
+// 8000, 8 KV heads (1.1 GB) 164 us, 6.6 TB/s; 17 entries of one sequence 3.7 us.  Of the second, 3 us pass
 // before the first load, 3 to 4 with the join, and the CTAs end within 10 % of one another, with the
-// tensor pipe 28 % and the issue slots 22 % busy.  By rows (160 units of 2048 to 4096, d 128): 46, 51, 61 and
-// 101 us with 4, 16, 32 and 64; e4m3, twice as long: 48, 54, 91 and 163, its codes being converted by
+// issue slots a fifth busy.  By rows (160 units of 2048 to 4096, d 128): 45, 47, 51, 61 and 103 us
+// with 4, 8, 16, 32 and 64; e4m3, twice as long: 46, 47, 54, 96 and 162, its codes being converted by
 // every row tile.
 #include <algorithm>
 #include <climits>
@@ -57,8 +60,12 @@ constexpr float kPShift = 15.f;  // e4m3: probabilities are scaled by 2^15
 
 enum PagedSite : int { SITE_PAGED_FULL = 1, SITE_PAGED_EMPTY = 2 };
 
-template <int D, bool FP8, int RT>
+// ROWS: query rows of a CTA.  With 16 and more a warp's products have 16 query rows and 8 entries (or
+// features); with 8 they are turned round (TURNED): 16 entries, or features, and 8 query rows, half as many.
+template <int D, bool FP8, int ROWS>
 struct Cfg {
+    static constexpr bool TURNED = ROWS == 8;
+    static constexpr int RT = TURNED ? 1 : ROWS / 16;              // row tiles
     static constexpr int ELEM = FP8 ? 1 : 2;
     static constexpr int ROWB = D * ELEM;                          // bytes of an entry's K or V row
     static constexpr int CB = ROWB < 128 ? ROWB : 128;             // bytes of a column chunk
@@ -70,7 +77,7 @@ struct Cfg {
     static constexpr int QPITCH = D * 2 + 16;                      // bytes of a query row in shared memory
     static constexpr int MR = 512 / D;                             // rows of a row tile merged at a time
     static constexpr int OPITCH = D + 4;                           // floats of a merge row
-    static constexpr int NQ = RT * 16 * QPITCH, NO = RT < kMathWarps ? kMathWarps * MR * OPITCH * 4 : 0, NML = kMathWarps * 16 * 8;
+    static constexpr int NQ = ROWS * QPITCH, NO = RT < kMathWarps ? kMathWarps * MR * OPITCH * 4 : 0, NML = kMathWarps * 16 * 8;
     static constexpr int SMALL = 1024 + NQ + NO + NML + RT * 16 * 4 + 24 * 12 + 64;
     // as many CTAs an SM as the accumulators leave registers for and the ring has room; the
     // ring takes what is left
@@ -136,6 +143,13 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// An 8 x 8 block of 16-bit values, two of a row a lane, turned round.
+__device__ __forceinline__ uint32_t turn8x8(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
 // Two e4m3 codes (in the low or high half of x) as two f16.
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t x)
 {
@@ -176,11 +190,6 @@ __device__ __forceinline__ float quad_max(float x)
 {
     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
     return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-}
-__device__ __forceinline__ float quad_sum(float x)
-{
-    x += __shfl_xor_sync(0xffffffffu, x, 1);
-    return x + __shfl_xor_sync(0xffffffffu, x, 2);
 }
 
 // ------------------------------------------------------------------ shares
@@ -345,15 +354,17 @@ __device__ __forceinline__ float4 add_weights(const PagedArgs &a, long long at, 
 }
 
 // ------------------------------------------------------------------ attention
-template <int D, bool FP8, int RT>
-__global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
+template <int D, bool FP8, int ROWS>
+__global__ void __launch_bounds__(kThreads, Cfg<D, FP8, ROWS>::CTAS)
     paged_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                  const __grid_constant__ PagedArgs a)
 {
-    using C = Cfg<D, FP8, RT>;
+    using C = Cfg<D, FP8, ROWS>;
+    constexpr bool TURNED = C::TURNED;
+    constexpr int RT = C::RT;
     constexpr int KW = kMathWarps / RT;             // warps that share a row tile's entries
     constexpr int KSTEPS = D / 16;                  // products along the head width, per 8 entries
-    constexpr bool QREG = D <= 64 && !(FP8 && RT == 1);   // query fragments stay in registers
+    constexpr bool QREG = TURNED || (D <= 64 && !(FP8 && RT == 1));   // query fragments stay in registers
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t sbase = (raw + 1023u) & ~1023u;
@@ -389,7 +400,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
             return;   // the whole CTA
     }
     const long long mine_all = p.left;   // tiles of this CTA
-    const uint32_t depth = whole ? C::NST : C::DEPTH;   // stages in use
+    // Stages in use.  Long whole units that run in step do better with fewer, unless their pages are small (256
+    // units, d 128: 32768 entries 594 us with two and 605 with three, 16384 299 and 305, in pages of 16 305 and
+    // 301; 4096 82.1 and 80.1)
+    const uint32_t depth = whole && (a.ps_shift < 6 || p.nt < 256) ? C::NST : C::DEPTH;
     __syncthreads();   // the barriers are there
     // rows of a page in one box, and boxes of a tile
     const int bp_shift = a.ps_shift < 6 ? a.ps_shift : 6, boxes = C::KT >> bp_shift;
@@ -471,13 +485,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
         // The unit's query rows: a warp's share of them into registers, from there to shared memory as
         // bf16, or as f16 over the row's power of two with features in the order in which the codes of
         // four neighbours come out of a register.
-        uint32_t qw[RT * 4][D / 64];
+        constexpr int QROWS = ROWS / kMathWarps;
+        uint32_t qw[QROWS][D / 64];
         float qks = 1.f;
         auto fetch_q = [&](const Place &at) {
             const int h = at.ul % a.Hkv, row0 = at.ul / a.Hkv * a.rows, nrows = min(a.rows, a.M - row0);
             const __nv_bfloat16 *q = a.q + (((long long)at.b * a.Hq + h * a.G) * a.Tq + row0) * D;
 #pragma unroll
-            for (int j = 0; j < RT * 4; ++j) {
+            for (int j = 0; j < QROWS; ++j) {
                 const int r = warp + kMathWarps * j;
 #pragma unroll
                 for (int i = 0; i < D / 64; ++i)
@@ -488,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
         };
         auto put_q = [&]() {
 #pragma unroll
-            for (int j = 0; j < RT * 4; ++j) {
+            for (int j = 0; j < QROWS; ++j) {
                 const int r = warp + kMathWarps * j;
                 uint8_t *qr = smem + C::OFF_Q + r * C::QPITCH;
                 float scale = a.scale_log2;
@@ -547,31 +562,43 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
                 fetch_q(p);
             put_q();
             math_sync();
-            uint32_t qf[QREG ? KSTEPS : 1][4];
-            if constexpr (QREG) {
+            uint32_t qf[QREG ? (TURNED ? KSTEPS / 2 : KSTEPS) : 1][4];   // turned: of two steps
+            if constexpr (TURNED) {
+#pragma unroll
+                for (int k = 0; k < KSTEPS / 2; ++k)
+                    ldsm4(qf[k], sbase + C::OFF_Q + (lane & 7) * C::QPITCH + (lane >> 3) * 16 + k * 64);
+            } else if constexpr (QREG) {
 #pragma unroll
                 for (int k = 0; k < KSTEPS; ++k)
                     ldsm4(qf[k], q_lane + k * 32);
             }
-            const float sc0 = rs[rt * 16 + r0], sc1 = rs[rt * 16 + r0 + 8];
-            // slots that the thread's two rows see; a row past the last sees what the others may
-            const int ra = row0 + rt * 16 + r0, rz = ra + 8;
+            // the thread's two rows, and the slots that they see; a row past the last sees what the others may
+            const int la = TURNED ? 2 * c4 : rt * 16 + r0, lz = la + (TURNED ? 1 : 8), ra = row0 + la, rz = row0 + lz;
+            const float sc0 = rs[la], sc1 = rs[lz];
             const int all = a.causal ? len - a.Tq + 1 : len;   // slots that every row sees
             const int lim0 = a.causal && ra < a.M ? len - a.Tq + ra % a.Tq + 1 : len;
             const int lim1 = a.causal && rz < a.M ? len - a.Tq + rz % a.Tq + 1 : len;
-            const bool st0 = a.scores && rt * 16 + r0 < nrows, st1 = a.scores && rt * 16 + r0 + 8 < nrows;
+            const bool st0 = a.scores && la < nrows, st1 = a.scores && lz < nrows;
             float *sp = a.scores ? a.scores + (((long long)p.b * a.Hkv + h) * a.M + ra) * a.cap : nullptr;
 
             auto put_scores = [&](int key, float x, float y, float z, float w) {   // of 8 entries, both rows
+                if constexpr (TURNED) {   // x, y: entry r0; z, w: entry r0 + 8
+                    if (st0)
+                        sp[key + r0] = x, sp[key + r0 + 8] = z;
+                    if (st1)
+                        sp[(long long)a.cap + key + r0] = y, sp[(long long)a.cap + key + r0 + 8] = w;
+                    return;
+                }
                 if (st0)
                     *reinterpret_cast<float2 *>(sp + key + 2 * c4) = make_float2(x, y);
                 if (st1)
                     *reinterpret_cast<float2 *>(sp + 8ll * a.cap + key + 2 * c4) = make_float2(z, w);
             };
 
-            float o[D / 8][4];
+            constexpr int OT = D / (TURNED ? 16 : 8);   // accumulators: of 16 or 8 features
+            float o[OT][4];
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i)
+            for (int i = 0; i < OT; ++i)
                 o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
             float m0 = -INFINITY, m1 = -INFINITY, l0[2] = {0.f, 0.f}, l1[2] = {0.f, 0.f};
 
@@ -585,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
                     const uint32_t have = (groups >> g) & ((1u << GP) - 1u);
                     if (have == 0) {
                         if (ok && a.scores)   // pages out of range: masked
-                            for (int t = 0; t < 2 * GP && key0 + 8 * (t & ~1) < len; ++t)
+                            for (int t = 0; t < 2 * GP && key0 + 8 * (t & ~1) < len; t += TURNED ? 2 : 1)
                                 put_scores(key0 + 8 * t, -INFINITY, -INFINITY, -INFINITY, -INFINITY);
                         continue;
                     }
@@ -598,106 +625,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
                         base[u] = sbase + st * C::STAGE + (uint32_t)((at >> bp_shift << bp_shift) * C::ROWB +
                                                                      (at & ((1 << bp_shift) - 1)) * C::CB);
                     }
-                    // ---- S = Q K^T: 16 rows x 16 entries a group; a single group has two accumulators for
-                    // each 8 entries, so that four products are always under way
-                    float s[4][4];
-#pragma unroll
-                    for (int t = 0; t < 4; ++t)
-                        s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
-#pragma unroll
-                    for (int k = 0; k < KSTEPS; k += FP8 ? 2 : 1) {
-                        uint32_t qa[4], qb[4];
-                        if constexpr (QREG) {
-#pragma unroll
-                            for (int x = 0; x < 4; ++x) {
-                                qa[x] = qf[k][x];
-                                qb[x] = qf[FP8 ? k + 1 : k][x];
-                            }
-                        } else {
-                            ldsm4(qa, q_lane + k * 32);
-                            if constexpr (FP8)
-                                ldsm4(qb, q_lane + k * 32 + 32);
-                        }
-#pragma unroll
-                        for (int u = 0; u < GP; ++u) {
-                            uint32_t kf[4];
-                            if constexpr (!FP8) {   // a 16-byte unit is 8 features
-                                ldsm4(kf, base[u] + k_lane + (k / (C::CB / 32)) * chunk + (k_unit ^ ((k % (C::CB / 32)) << 5)));
-                                const int z = GP == 2 ? 2 * u : (k & 1) * 2;
-                                mma16816<false>(s[z], qa, kf[0], kf[1]);
-                                mma16816<false>(s[z + 1], qa, kf[2], kf[3]);
-                            } else {   // 16 features
-                                ldsm4(kf, base[u] + k_lane + (k / (C::CB / 16)) * chunk + (k_unit ^ ((k % (C::CB / 16)) << 4)));
-                                const int z = GP == 2 ? 2 * u : 2;
-                                mma16816<true>(s[2 * u], qa, e4m3x2_to_f16x2(kf[0]), e4m3x2_to_f16x2(kf[0] >> 16));
-                                mma16816<true>(s[2 * u + 1], qa, e4m3x2_to_f16x2(kf[2]), e4m3x2_to_f16x2(kf[2] >> 16));
-                                mma16816<true>(s[z], qb, e4m3x2_to_f16x2(kf[1]), e4m3x2_to_f16x2(kf[1] >> 16));
-                                mma16816<true>(s[z + 1], qb, e4m3x2_to_f16x2(kf[3]), e4m3x2_to_f16x2(kf[3] >> 16));
-                            }
-                        }
-                    }
-                    if constexpr (GP == 1) {
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            s[0][x] += s[2][x];
-                            s[1][x] += s[3][x];
-                        }
-                    }
                     const bool clear = have == (1u << GP) - 1u && key0 + 16 * GP <= all;
-                    if (!clear) {
-#pragma unroll
-                        for (int t = 0; t < 2 * GP; ++t) {
-                            const bool in = (have >> (t >> 1)) & 1u;
-                            const int key = key0 + 8 * t + 2 * c4;
-                            s[t][0] = in && key < lim0 ? s[t][0] : -INFINITY;
-                            s[t][1] = in && key + 1 < lim0 ? s[t][1] : -INFINITY;
-                            s[t][2] = in && key < lim1 ? s[t][2] : -INFINITY;
-                            s[t][3] = in && key + 1 < lim1 ? s[t][3] : -INFINITY;
-                        }
-                    }
-                    if (a.scores) {
-#pragma unroll
-                        for (int t = 0; t < 2 * GP; ++t)
-                            if (key0 + 8 * (t & ~1) < len)
-                                put_scores(key0 + 8 * t, s[t][0] * sc0, s[t][1] * sc0, s[t][2] * sc1, s[t][3] * sc1);
-                    }
-                    // ---- online softmax
-                    constexpr float SH = FP8 ? kPShift : 0.f;
-                    float x0 = fmaxf(fmax3(s[0][0], s[0][1], s[1][0]), s[1][1]);
-                    float x1 = fmaxf(fmax3(s[0][2], s[0][3], s[1][2]), s[1][3]);
-                    if constexpr (GP == 2) {
-                        x0 = fmax3(fmax3(x0, s[2][0], s[2][1]), s[3][0], s[3][1]);
-                        x1 = fmax3(fmax3(x1, s[2][2], s[2][3]), s[3][2], s[3][3]);
-                    }
-                    const float n0 = fmaxf(m0, quad_max(x0) * sc0 - SH), n1 = fmaxf(m1, quad_max(x1) * sc1 - SH);
-                    const float b0 = n0 == -INFINITY ? 0.f : n0, b1 = n1 == -INFINITY ? 0.f : n1;
-                    if (__any_sync(0xffffffffu, n0 > m0 || n1 > m1)) {
-                        const float f0 = ex2_approx(m0 - b0), f1 = ex2_approx(m1 - b1);
-                        l0[0] *= f0, l0[1] *= f0;
-                        l1[0] *= f1, l1[1] *= f1;
-#pragma unroll
-                        for (int d = 0; d < D / 8; ++d) {
-                            o[d][0] *= f0;
-                            o[d][1] *= f0;
-                            o[d][2] *= f1;
-                            o[d][3] *= f1;
-                        }
-                        m0 = n0;
-                        m1 = n1;
-                    }
-#pragma unroll
-                    for (int t = 0; t < 2 * GP; ++t) {
-                        ffma2(s[t][0], s[t][1], s[t][0], s[t][1], sc0, sc0, -b0, -b0);
-                        ffma2(s[t][2], s[t][3], s[t][2], s[t][3], sc1, sc1, -b1, -b1);
-#pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            s[t][x] = ex2_approx(s[t][x]);
-                        fadd2(l0[0], l0[1], l0[0], l0[1], s[t][0], s[t][1]);
-                        fadd2(l1[0], l1[1], l1[0], l1[1], s[t][2], s[t][3]);
-                    }
-                    // ---- O += P V, group by group.  Entries behind the length (and groups that are not
-                    // there) hold anything, and 0 times a NaN is one: their V rows become 0 first
-                    if (!clear) {
+                    // Entries behind the length (and groups that are not there) hold anything, and 0 times a
+                    // NaN is one: their V rows become 0 before P V
+                    auto zero_behind = [&]() {
+                        if (clear)
+                            return;
 #pragma unroll
                         for (int u = 0; u < GP; ++u) {
                             const int first = (have >> u) & 1u ? len - (key0 + 16 * u) : 0, row = lane & 15;
@@ -709,43 +642,275 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
                         // written through the generic proxy, and next by TMA
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                         __syncwarp();
-                    }
+                    };
+                    if constexpr (TURNED) {
+                        // ---- S^T = K Q^T: 16 entries x 8 rows a group, in two accumulators
+                        float s[GP][2][4];
 #pragma unroll
-                    for (int u = 0; u < GP; ++u) {
-                        const uint32_t vbase = base[u] + C::TILE + v_lane;
-                        const float(&pu)[4] = s[2 * u], (&pw)[4] = s[2 * u + 1];
-                        if constexpr (!FP8) {
-                            uint32_t hi[4], lo[4];
-#pragma unroll
-                            for (int x = 0; x < 4; ++x) {
-                                const float pa = x < 2 ? pu[x * 2] : pw[(x - 2) * 2], pb = x < 2 ? pu[x * 2 + 1] : pw[(x - 2) * 2 + 1];
-                                hi[x] = pack_bf16x2(pa, pb);
-                                lo[x] = pack_bf16x2(pa - __uint_as_float(hi[x] << 16), pb - __uint_as_float(hi[x] & 0xFFFF0000u));
-                            }
-#pragma unroll
-                            for (int d = 0; d < D / 16; ++d) {
-                                uint32_t vf[4];
-                                ldsm4_t(vf, vbase + (d / (C::CB / 32)) * chunk + (v_unit ^ ((d % (C::CB / 32)) << 5)));
-                                mma16816<false>(o[2 * d], hi, vf[0], vf[1]);
-                                mma16816<false>(o[2 * d + 1], hi, vf[2], vf[3]);
-                                mma16816<false>(o[2 * d], lo, vf[0], vf[1]);
-                                mma16816<false>(o[2 * d + 1], lo, vf[2], vf[3]);
-                            }
-                        } else {
-                            uint32_t pf[4];
+                        for (int u = 0; u < GP; ++u)
 #pragma unroll
                             for (int x = 0; x < 4; ++x)
-                                pf[x] = x < 2 ? pack_f16x2(pu[x * 2], pu[x * 2 + 1]) : pack_f16x2(pw[(x - 2) * 2], pw[(x - 2) * 2 + 1]);
+                                s[u][0][x] = s[u][1][x] = 0.f;
 #pragma unroll
-                            for (int d = 0; d < D / 32; ++d) {   // two 16-byte units: 32 features
-                                uint32_t vf[4];
-                                ldsm4_t(vf, vbase + (d / (C::CB / 32)) * chunk + (v_unit ^ ((d % (C::CB / 32)) << 5)));
+                        for (int k = 0; k < KSTEPS; k += 2) {
+                            const uint32_t(&qk)[4] = qf[k / 2];
 #pragma unroll
-                                for (int w = 0; w < 2; ++w) {
-                                    // a register holds features (f, f + 1) of entries 2 c and 2 c + 1: pair the entries
-                                    const uint32_t x = __byte_perm(vf[2 * w], 0, 0x3120), y = __byte_perm(vf[2 * w + 1], 0, 0x3120);
-                                    mma16816<true>(o[4 * d + 2 * w], pf, e4m3x2_to_f16x2(x), e4m3x2_to_f16x2(y));
-                                    mma16816<true>(o[4 * d + 2 * w + 1], pf, e4m3x2_to_f16x2(x >> 16), e4m3x2_to_f16x2(y >> 16));
+                            for (int u = 0; u < GP; ++u) {
+                                uint32_t kf[4];
+                                if constexpr (!FP8) {   // a 16-byte unit is 8 features
+#pragma unroll
+                                    for (int w = 0; w < 2; ++w) {
+                                        const int kk = k + w;
+                                        ldsm4(kf, base[u] + k_lane + (kk / (C::CB / 32)) * chunk + (k_unit ^ ((kk % (C::CB / 32)) << 5)));
+                                        mma16816<false>(s[u][w], {kf[0], kf[2], kf[1], kf[3]}, qk[2 * w], qk[2 * w + 1]);
+                                    }
+                                } else {   // 16 features
+                                    ldsm4(kf, base[u] + k_lane + (k / (C::CB / 16)) * chunk + (k_unit ^ ((k % (C::CB / 16)) << 4)));
+                                    mma16816<true>(s[u][0], {e4m3x2_to_f16x2(kf[0]), e4m3x2_to_f16x2(kf[2]),
+                                                             e4m3x2_to_f16x2(kf[0] >> 16), e4m3x2_to_f16x2(kf[2] >> 16)}, qk[0], qk[1]);
+                                    mma16816<true>(s[u][1], {e4m3x2_to_f16x2(kf[1]), e4m3x2_to_f16x2(kf[3]),
+                                                             e4m3x2_to_f16x2(kf[1] >> 16), e4m3x2_to_f16x2(kf[3] >> 16)}, qk[2], qk[3]);
+                                }
+                            }
+                        }
+                        // t: (entry, first row), (entry, second), (entry + 8, first), (entry + 8, second)
+                        float t[GP][4];
+#pragma unroll
+                        for (int u = 0; u < GP; ++u) {
+                            fadd2(t[u][0], t[u][1], s[u][0][0], s[u][0][1], s[u][1][0], s[u][1][1]);
+                            fadd2(t[u][2], t[u][3], s[u][0][2], s[u][0][3], s[u][1][2], s[u][1][3]);
+                        }
+                        if (!clear) {
+#pragma unroll
+                            for (int u = 0; u < GP; ++u) {
+                                const bool in = (have >> u) & 1u;
+                                const int key = key0 + 16 * u + r0;
+                                t[u][0] = in && key < lim0 ? t[u][0] : -INFINITY;
+                                t[u][1] = in && key < lim1 ? t[u][1] : -INFINITY;
+                                t[u][2] = in && key + 8 < lim0 ? t[u][2] : -INFINITY;
+                                t[u][3] = in && key + 8 < lim1 ? t[u][3] : -INFINITY;
+                            }
+                        }
+                        if (a.scores) {
+#pragma unroll
+                            for (int u = 0; u < GP; ++u)
+                                if (key0 + 16 * u < len)
+                                    put_scores(key0 + 16 * u, t[u][0] * sc0, t[u][1] * sc1, t[u][2] * sc0, t[u][3] * sc1);
+                        }
+                        // ---- online softmax; the rows' maxima are put together only when one of them grows
+                        constexpr float SH = FP8 ? kPShift : 0.f;
+                        float x0 = fmaxf(t[0][0], t[0][2]), x1 = fmaxf(t[0][1], t[0][3]);
+                        if constexpr (GP == 2) {
+                            x0 = fmax3(x0, t[1][0], t[1][2]);
+                            x1 = fmax3(x1, t[1][1], t[1][3]);
+                        }
+                        float n0 = x0 * sc0 - SH, n1 = x1 * sc1 - SH;
+                        if (__any_sync(0xffffffffu, n0 > m0 || n1 > m1)) {
+#pragma unroll
+                            for (int off = 4; off < 32; off <<= 1) {
+                                n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, off));
+                                n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, off));
+                            }
+                            n0 = fmaxf(n0, m0);
+                            n1 = fmaxf(n1, m1);
+                            const float f0 = ex2_approx(m0 - (n0 == -INFINITY ? 0.f : n0));
+                            const float f1 = ex2_approx(m1 - (n1 == -INFINITY ? 0.f : n1));
+                            l0[0] *= f0;
+                            l1[0] *= f1;
+#pragma unroll
+                            for (int d = 0; d < OT; ++d) {
+                                o[d][0] *= f0;
+                                o[d][1] *= f1;
+                                o[d][2] *= f0;
+                                o[d][3] *= f1;
+                            }
+                            m0 = n0;
+                            m1 = n1;
+                        }
+                        const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;
+#pragma unroll
+                        for (int u = 0; u < GP; ++u)
+#pragma unroll
+                            for (int x = 0; x < 4; x += 2) {
+                                ffma2(t[u][x], t[u][x + 1], t[u][x], t[u][x + 1], sc0, sc1, -b0, -b1);
+                                t[u][x] = ex2_approx(t[u][x]);
+                                t[u][x + 1] = ex2_approx(t[u][x + 1]);
+                                fadd2(l0[0], l1[0], l0[0], l1[0], t[u][x], t[u][x + 1]);
+                            }
+                        zero_behind();
+                        // ---- O^T += V^T P^T, group by group; P's 8 x 8 blocks (entries, rows) turned round
+#pragma unroll
+                        for (int u = 0; u < GP; ++u) {
+                            const uint32_t vbase = base[u] + C::TILE + v_lane;
+                            if constexpr (!FP8) {
+                                uint32_t hi[2], lo[2];
+#pragma unroll
+                                for (int x = 0; x < 2; ++x) {
+                                    const float pa = t[u][2 * x], pb = t[u][2 * x + 1];
+                                    const uint32_t h = pack_bf16x2(pa, pb);
+                                    hi[x] = turn8x8(h);
+                                    lo[x] = turn8x8(pack_bf16x2(pa - __uint_as_float(h << 16), pb - __uint_as_float(h & 0xFFFF0000u)));
+                                }
+#pragma unroll
+                                for (int d = 0; d < D / 16; ++d) {
+                                    uint32_t vf[4];
+                                    ldsm4_t(vf, vbase + (d / (C::CB / 32)) * chunk + (v_unit ^ ((d % (C::CB / 32)) << 5)));
+                                    mma16816<false>(o[d], {vf[0], vf[2], vf[1], vf[3]}, hi[0], hi[1]);
+                                    mma16816<false>(o[d], {vf[0], vf[2], vf[1], vf[3]}, lo[0], lo[1]);
+                                }
+                            } else {
+                                const uint32_t p0 = turn8x8(pack_f16x2(t[u][0], t[u][1])), p1 = turn8x8(pack_f16x2(t[u][2], t[u][3]));
+#pragma unroll
+                                for (int d = 0; d < D / 32; ++d) {   // two 16-byte units: 32 features
+                                    uint32_t vf[4];
+                                    ldsm4_t(vf, vbase + (d / (C::CB / 32)) * chunk + (v_unit ^ ((d % (C::CB / 32)) << 5)));
+#pragma unroll
+                                    for (int w = 0; w < 2; ++w) {
+                                        // a register holds features (f, f + 1) of entries 2 c and 2 c + 1: pair the entries;
+                                        // even features are the product's first 8 rows, odd ones the others
+                                        const uint32_t x = __byte_perm(vf[2 * w], 0, 0x3120), y = __byte_perm(vf[2 * w + 1], 0, 0x3120);
+                                        mma16816<true>(o[2 * d + w], {e4m3x2_to_f16x2(x), e4m3x2_to_f16x2(x >> 16),
+                                                                      e4m3x2_to_f16x2(y), e4m3x2_to_f16x2(y >> 16)}, p0, p1);
+                                    }
+                                }
+                            }
+                        }
+                        continue;
+                    } else {
+                        // ---- S = Q K^T: 16 rows x 16 entries a group; a single group has two accumulators for
+                        // each 8 entries, so that four products are always under way
+                        float s[4][4];
+#pragma unroll
+                        for (int t = 0; t < 4; ++t)
+                            s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+#pragma unroll
+                        for (int k = 0; k < KSTEPS; k += FP8 ? 2 : 1) {
+                            uint32_t qa[4], qb[4];
+                            if constexpr (QREG) {
+#pragma unroll
+                                for (int x = 0; x < 4; ++x) {
+                                    qa[x] = qf[k][x];
+                                    qb[x] = qf[FP8 ? k + 1 : k][x];
+                                }
+                            } else {
+                                ldsm4(qa, q_lane + k * 32);
+                                if constexpr (FP8)
+                                    ldsm4(qb, q_lane + k * 32 + 32);
+                            }
+#pragma unroll
+                            for (int u = 0; u < GP; ++u) {
+                                uint32_t kf[4];
+                                if constexpr (!FP8) {   // a 16-byte unit is 8 features
+                                    ldsm4(kf, base[u] + k_lane + (k / (C::CB / 32)) * chunk + (k_unit ^ ((k % (C::CB / 32)) << 5)));
+                                    const int z = GP == 2 ? 2 * u : (k & 1) * 2;
+                                    mma16816<false>(s[z], qa, kf[0], kf[1]);
+                                    mma16816<false>(s[z + 1], qa, kf[2], kf[3]);
+                                } else {   // 16 features
+                                    ldsm4(kf, base[u] + k_lane + (k / (C::CB / 16)) * chunk + (k_unit ^ ((k % (C::CB / 16)) << 4)));
+                                    const int z = GP == 2 ? 2 * u : 2;
+                                    mma16816<true>(s[2 * u], qa, e4m3x2_to_f16x2(kf[0]), e4m3x2_to_f16x2(kf[0] >> 16));
+                                    mma16816<true>(s[2 * u + 1], qa, e4m3x2_to_f16x2(kf[2]), e4m3x2_to_f16x2(kf[2] >> 16));
+                                    mma16816<true>(s[z], qb, e4m3x2_to_f16x2(kf[1]), e4m3x2_to_f16x2(kf[1] >> 16));
+                                    mma16816<true>(s[z + 1], qb, e4m3x2_to_f16x2(kf[3]), e4m3x2_to_f16x2(kf[3] >> 16));
+                                }
+                            }
+                        }
+                        if constexpr (GP == 1) {
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                s[0][x] += s[2][x];
+                                s[1][x] += s[3][x];
+                            }
+                        }
+                        if (!clear) {
+#pragma unroll
+                            for (int t = 0; t < 2 * GP; ++t) {
+                                const bool in = (have >> (t >> 1)) & 1u;
+                                const int key = key0 + 8 * t + 2 * c4;
+                                s[t][0] = in && key < lim0 ? s[t][0] : -INFINITY;
+                                s[t][1] = in && key + 1 < lim0 ? s[t][1] : -INFINITY;
+                                s[t][2] = in && key < lim1 ? s[t][2] : -INFINITY;
+                                s[t][3] = in && key + 1 < lim1 ? s[t][3] : -INFINITY;
+                            }
+                        }
+                        if (a.scores) {
+#pragma unroll
+                            for (int t = 0; t < 2 * GP; ++t)
+                                if (key0 + 8 * (t & ~1) < len)
+                                    put_scores(key0 + 8 * t, s[t][0] * sc0, s[t][1] * sc0, s[t][2] * sc1, s[t][3] * sc1);
+                        }
+                        // ---- online softmax
+                        constexpr float SH = FP8 ? kPShift : 0.f;
+                        float x0 = fmaxf(fmax3(s[0][0], s[0][1], s[1][0]), s[1][1]);
+                        float x1 = fmaxf(fmax3(s[0][2], s[0][3], s[1][2]), s[1][3]);
+                        if constexpr (GP == 2) {
+                            x0 = fmax3(fmax3(x0, s[2][0], s[2][1]), s[3][0], s[3][1]);
+                            x1 = fmax3(fmax3(x1, s[2][2], s[2][3]), s[3][2], s[3][3]);
+                        }
+                        const float n0 = fmaxf(m0, quad_max(x0) * sc0 - SH), n1 = fmaxf(m1, quad_max(x1) * sc1 - SH);
+                        const float b0 = n0 == -INFINITY ? 0.f : n0, b1 = n1 == -INFINITY ? 0.f : n1;
+                        if (__any_sync(0xffffffffu, n0 > m0 || n1 > m1)) {
+                            const float f0 = ex2_approx(m0 - b0), f1 = ex2_approx(m1 - b1);
+                            l0[0] *= f0, l0[1] *= f0;
+                            l1[0] *= f1, l1[1] *= f1;
+#pragma unroll
+                            for (int d = 0; d < D / 8; ++d) {
+                                o[d][0] *= f0;
+                                o[d][1] *= f0;
+                                o[d][2] *= f1;
+                                o[d][3] *= f1;
+                            }
+                            m0 = n0;
+                            m1 = n1;
+                        }
+#pragma unroll
+                        for (int t = 0; t < 2 * GP; ++t) {
+                            ffma2(s[t][0], s[t][1], s[t][0], s[t][1], sc0, sc0, -b0, -b0);
+                            ffma2(s[t][2], s[t][3], s[t][2], s[t][3], sc1, sc1, -b1, -b1);
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                s[t][x] = ex2_approx(s[t][x]);
+                            fadd2(l0[0], l0[1], l0[0], l0[1], s[t][0], s[t][1]);
+                            fadd2(l1[0], l1[1], l1[0], l1[1], s[t][2], s[t][3]);
+                        }
+                        zero_behind();
+#pragma unroll
+                        for (int u = 0; u < GP; ++u) {
+                            const uint32_t vbase = base[u] + C::TILE + v_lane;
+                            const float(&pu)[4] = s[2 * u], (&pw)[4] = s[2 * u + 1];
+                            if constexpr (!FP8) {
+                                uint32_t hi[4], lo[4];
+#pragma unroll
+                                for (int x = 0; x < 4; ++x) {
+                                    const float pa = x < 2 ? pu[x * 2] : pw[(x - 2) * 2], pb = x < 2 ? pu[x * 2 + 1] : pw[(x - 2) * 2 + 1];
+                                    hi[x] = pack_bf16x2(pa, pb);
+                                    lo[x] = pack_bf16x2(pa - __uint_as_float(hi[x] << 16), pb - __uint_as_float(hi[x] & 0xFFFF0000u));
+                                }
+#pragma unroll
+                                for (int d = 0; d < D / 16; ++d) {
+                                    uint32_t vf[4];
+                                    ldsm4_t(vf, vbase + (d / (C::CB / 32)) * chunk + (v_unit ^ ((d % (C::CB / 32)) << 5)));
+                                    mma16816<false>(o[2 * d], hi, vf[0], vf[1]);
+                                    mma16816<false>(o[2 * d + 1], hi, vf[2], vf[3]);
+                                    mma16816<false>(o[2 * d], lo, vf[0], vf[1]);
+                                    mma16816<false>(o[2 * d + 1], lo, vf[2], vf[3]);
+                                }
+                            } else {
+                                uint32_t pf[4];
+#pragma unroll
+                                for (int x = 0; x < 4; ++x)
+                                    pf[x] = x < 2 ? pack_f16x2(pu[x * 2], pu[x * 2 + 1]) : pack_f16x2(pw[(x - 2) * 2], pw[(x - 2) * 2 + 1]);
+#pragma unroll
+                                for (int d = 0; d < D / 32; ++d) {   // two 16-byte units: 32 features
+                                    uint32_t vf[4];
+                                    ldsm4_t(vf, vbase + (d / (C::CB / 32)) * chunk + (v_unit ^ ((d % (C::CB / 32)) << 5)));
+#pragma unroll
+                                    for (int w = 0; w < 2; ++w) {
+                                        // a register holds features (f, f + 1) of entries 2 c and 2 c + 1: pair the entries
+                                        const uint32_t x = __byte_perm(vf[2 * w], 0, 0x3120), y = __byte_perm(vf[2 * w + 1], 0, 0x3120);
+                                        mma16816<true>(o[4 * d + 2 * w], pf, e4m3x2_to_f16x2(x), e4m3x2_to_f16x2(y));
+                                        mma16816<true>(o[4 * d + 2 * w + 1], pf, e4m3x2_to_f16x2(x >> 16), e4m3x2_to_f16x2(y >> 16));
+                                    }
                                 }
                             }
                         }
@@ -769,31 +934,36 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
             if (RT == 1 && next.left > 0)
                 fetch_q(next);
             // ---- the warps' states of each row tile together, then out, MR rows of each at a time
-            const float s0 = quad_sum(l0[0] + l0[1]), s1 = quad_sum(l1[0] + l1[1]);
-            if (c4 == 0) {
-                ml[warp * 16 + r0] = make_float2(m0, s0);
-                ml[warp * 16 + r0 + 8] = make_float2(m1, s1);
+            float s0 = l0[0] + l0[1], s1 = l1[0] + l1[1];
+#pragma unroll
+            for (int off = TURNED ? 4 : 1; off < (TURNED ? 32 : 4); off <<= 1) {
+                s0 += __shfl_xor_sync(0xffffffffu, s0, off);
+                s1 += __shfl_xor_sync(0xffffffffu, s1, off);
+            }
+            const bool first_lane = TURNED ? r0 == 0 : c4 == 0;   // of those that have the same rows
+            if (first_lane) {
+                ml[kw * RT * 16 + la] = make_float2(m0, s0);
+                ml[kw * RT * 16 + lz] = make_float2(m1, s1);
             }
             math_sync();
             const bool entire = p.tile == 0 && cnt == p.nt;   // all of the unit
             const long long slot = 2ll * blockIdx.x + (p.left == mine_all ? 0 : 1);
             float *part = a.part + slot * a.rows * (D + 2);
             const float vs = FP8 ? a.vs[h] : 1.f;
-            // the factor of this warp's sums in row r's output (or, scaled by vs, in its partial state); one
+            // the factor of this warp's sums in a row's output (or, scaled by vs, in its partial state); one
             // warp of the row tile writes the row's statistics
-            auto factor = [&](int r, float m) {
+            auto factor = [&](int row, float m) {
                 float t = -INFINITY, l = 0.f;
 #pragma unroll
                 for (int w = 0; w < KW; ++w)
-                    t = fmaxf(t, ml[(w * RT + rt) * 16 + r].x);
+                    t = fmaxf(t, ml[w * RT * 16 + row].x);
                 const float z = t == -INFINITY ? 0.f : t;
 #pragma unroll
                 for (int w = 0; w < KW; ++w) {
-                    const float2 y = ml[(w * RT + rt) * 16 + r];
+                    const float2 y = ml[w * RT * 16 + row];
                     l = fmaf(y.y, ex2_approx(y.x - z), l);
                 }
-                const int row = rt * 16 + r;
-                if (kw == 0 && c4 == 0 && row < nrows && ok) {
+                if (kw == 0 && first_lane && row < nrows && ok) {
                     if (entire) {
                         const float y = t + log2f(l);   // -inf if l is 0
                         a.lse[grow + row] = l == 0.f ? -INFINITY : y * 0.69314718055994530942f;
@@ -805,7 +975,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
                 }
                 return ex2_approx(m - z) * (entire ? (l == 0.f ? 0.f : vs / l) : vs);
             };
-            const float f0 = factor(r0, m0), f1 = factor(r0 + 8, m1);
+            const float f0 = factor(la, m0), f1 = factor(lz, m1);
             if constexpr (KW == 1) {   // a row is one warp's: out of its registers
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
@@ -843,12 +1013,27 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, RT>::CTAS)
                 constexpr int MR = C::MR;
 #pragma unroll 1
                 for (int first = 0; first < min(16, nrows); first += MR) {
-                    if (r0 / MR == (first & 7) / MR) {
+                    if (TURNED && la / MR == first / MR) {
+                        float *mine = ob + (kw * MR + la % MR) * C::OPITCH;
+#pragma unroll
+                        for (int x = 0; x < OT; ++x) {
+                            if constexpr (!FP8) {
+                                mine[16 * x + r0] = o[x][0] * f0;
+                                mine[16 * x + 8 + r0] = o[x][2] * f0;
+                                mine[C::OPITCH + 16 * x + r0] = o[x][1] * f1;
+                                mine[C::OPITCH + 16 * x + 8 + r0] = o[x][3] * f1;
+                            } else {
+                                *reinterpret_cast<float2 *>(mine + 16 * x + 2 * r0) = make_float2(o[x][0] * f0, o[x][2] * f0);
+                                *reinterpret_cast<float2 *>(mine + C::OPITCH + 16 * x + 2 * r0) = make_float2(o[x][1] * f1, o[x][3] * f1);
+                            }
+                        }
+                    }
+                    if (!TURNED && r0 / MR == (first & 7) / MR) {
                         float *mine = ob + (warp * MR + r0 % MR) * C::OPITCH;
                         const bool low = first < 8;
                         const float f = low ? f0 : f1;
 #pragma unroll
-                        for (int x = 0; x < D / 8; x += 2) {
+                        for (int x = 0; x < (TURNED ? 0 : D / 8); x += 2) {
                             const float a0 = (low ? o[x][0] : o[x][2]) * f, a1 = (low ? o[x][1] : o[x][3]) * f;
                             const float b0 = (low ? o[x + 1][0] : o[x + 1][2]) * f, b1 = (low ? o[x + 1][1] : o[x + 1][3]) * f;
                             if constexpr (!FP8) {
@@ -1069,7 +1254,7 @@ __global__ void __launch_bounds__(kJoinThreads, 8) paged_join_kernel(const __gri
 size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 int rows_of(int M) { return M < kMaxRows ? M : kMaxRows; }
-int row_tiles(int M) { return M <= 16 ? 1 : M <= 32 ? 2 : 4; }
+int tile_rows(int M) { return M <= 8 ? 8 : M <= 16 ? 16 : M <= 32 ? 32 : 64; }   // of the instance
 
 
 // Tables of up to this many slots (half at d 256): one CTA a unit and no join.  8 units of 256, 512 and
@@ -1095,22 +1280,25 @@ int encode_pool(CUtensorMap *map, const void *base, const fa_kv_cache &c, int bo
                        box, cb == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
-template <int D, bool FP8, int RT>
+template <int D, bool FP8, int ROWS>
 int launch_main(const CUtensorMap &tk, const CUtensorMap &tv, const PagedArgs &a, int grid, cudaStream_t s)
 {
-    using C = Cfg<D, FP8, RT>;
-    if (cudaFuncSetAttribute(paged_kernel<D, FP8, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
+    using C = Cfg<D, FP8, ROWS>;
+    if (cudaFuncSetAttribute(paged_kernel<D, FP8, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
         return ERR_CUDA;
-    return launch_overlapped(paged_kernel<D, FP8, RT>, dim3((unsigned)grid), kThreads, C::SMEM, 0, true, s, tk, tv, a);
+    return launch_overlapped(paged_kernel<D, FP8, ROWS>, dim3((unsigned)grid), kThreads, C::SMEM, 0, true, s, tk, tv, a);
 }
 
 template <int D>
 int paged_run(const fa_kv_cache &c, PagedArgs &a, cudaStream_t s)
 {
     const bool f8 = c.dtype == FA_E4M3;
-    const int rt = row_tiles(a.M);
-    a.kt = f8 ? Cfg<D, true, 1>::KT : Cfg<D, false, 1>::KT;
-    a.grid = kSMs * (rt == 1 ? (f8 ? Cfg<D, true, 1>::CTAS : Cfg<D, false, 1>::CTAS) : f8 ? Cfg<D, true, 2>::CTAS : Cfg<D, false, 2>::CTAS);
+    const int rows = tile_rows(a.M);
+    a.kt = f8 ? Cfg<D, true, 8>::KT : Cfg<D, false, 8>::KT;
+    const int ctas = rows == 8    ? (f8 ? Cfg<D, true, 8>::CTAS : Cfg<D, false, 8>::CTAS)
+                     : rows == 16 ? (f8 ? Cfg<D, true, 16>::CTAS : Cfg<D, false, 16>::CTAS)
+                                  : f8 ? Cfg<D, true, 32>::CTAS : Cfg<D, false, 32>::CTAS;
+    a.grid = kSMs * ctas;
     const long long most = (long long)a.B * a.Hkv * a.RB * ((a.cap + a.kt - 1) / a.kt);   // tiles, at most
     a.may_whole = a.may_whole && most > 0 && (long long)a.B * a.Hkv * a.RB <= a.grid;
     int st = OK;
@@ -1124,13 +1312,15 @@ int paged_run(const fa_kv_cache &c, PagedArgs &a, cudaStream_t s)
             return ERR_UNSUPPORTED;
         const int grid = (int)(a.whole ? units : most < a.grid ? most : a.grid);
         if (f8)
-            st = rt == 1   ? launch_main<D, true, 1>(tk, tv, a, grid, s)
-                 : rt == 2 ? launch_main<D, true, 2>(tk, tv, a, grid, s)
-                           : launch_main<D, true, 4>(tk, tv, a, grid, s);
+            st = rows == 8    ? launch_main<D, true, 8>(tk, tv, a, grid, s)
+                 : rows == 16 ? launch_main<D, true, 16>(tk, tv, a, grid, s)
+                 : rows == 32 ? launch_main<D, true, 32>(tk, tv, a, grid, s)
+                              : launch_main<D, true, 64>(tk, tv, a, grid, s);
         else
-            st = rt == 1   ? launch_main<D, false, 1>(tk, tv, a, grid, s)
-                 : rt == 2 ? launch_main<D, false, 2>(tk, tv, a, grid, s)
-                           : launch_main<D, false, 4>(tk, tv, a, grid, s);
+            st = rows == 8    ? launch_main<D, false, 8>(tk, tv, a, grid, s)
+                 : rows == 16 ? launch_main<D, false, 16>(tk, tv, a, grid, s)
+                 : rows == 32 ? launch_main<D, false, 32>(tk, tv, a, grid, s)
+                              : launch_main<D, false, 64>(tk, tv, a, grid, s);
         if (st != OK)
             return st;
     }
