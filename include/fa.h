@@ -292,10 +292,11 @@ int fa_cache_append(const fa_kv_cache *cache, const fa_heads *k, const fa_heads 
  * tokens are the last entries), else every slot.  A row that sees nothing gets
  * O = 0 and lse = -inf.  An infinity or NaN in the v of an entry that any row of
  * the call sees may reach every row of its head group.  Scores, statistics and
- * the row sums are fp32; the keys are split over the thread blocks in equal
- * shares of the whole batch, and partial results are joined in a fixed order:
- * the same call gives the same bits, but a sequence's last bits may depend on
- * the other lengths.
+ * the row sums are fp32; a probability meets v with 16 bits, in an FA_E4M3 cache
+ * with 11, or, below 2^-29 of the row's largest, to a multiple of 2^-39 of it.
+ * The keys are split over the thread blocks in equal shares of the whole batch,
+ * and partial results are joined in a fixed order: the same call gives the same
+ * bits, but a sequence's last bits may depend on the other lengths.
  * accumulate = 1 adds, for every entry, the sum of its probabilities over the
  * head group's rows (Hq / Hkv heads x Tq) to cache->weight.
  * workspace: fa_decode_paged_workspace_bytes bytes, 256-byte aligned, contents

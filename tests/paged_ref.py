@@ -11,7 +11,10 @@ absolute below e4m3's smallest normal number).
   Attention: a score is off by at most e = (d + 4) u c sum_i |q_i k_i| (fp32 sums of exact
     products, in any order), a probability by a factor e^{2e} and 2^-20 (exp2, the joins), so with
     A = sum p |v| an output is off by (2 e + 2^-18) A; probabilities that enter the second product
-    with 11 bits or more add 2^-12 A, the bf16 output 2^-8 |o|.  lse: e + 2^-20 (1 + |lse|).
+    with 11 bits or more add 2^-12 A, the bf16 output 2^-8 |o|.  In an e4m3 cache they enter as f16 after
+    a factor of 2^15 on e^{s - m}: below 2^-14 f16 goes in steps of 2^-24, so that each e^{s - m} is off by up to
+    2^-25 2^-15 = 2^-40 instead, where 2^-12 of it is less.  m only grows, and a later m scales the error down with
+    the value; the sum l >= 1 divides it.  That adds 2^-40 sum |v|, over the entries that the row sees.  lse: e + 2^-20 (1 + |lse|).
     weight: (2 e + 2^-18) sum p, and u (M + 1) |w| for the additions.
 """
 from __future__ import annotations
@@ -43,9 +46,9 @@ def rotate(x: np.ndarray, pos: np.ndarray, freqs, axis, interleaved=False, inver
     return y, tol
 
 
-def attend(q, k, v, scale, causal, group):
+def attend(q, k, v, scale, causal, group, codes=False):
     """q [Hq][Tq][d], k, v [Hkv][n][d] float64 -> o, lse, weight sums [Hkv][n] and the tolerances
-    of the three (module docstring), without the rounding of o to bf16."""
+    of the three (module docstring; codes: of an e4m3 cache), without the rounding of o to bf16."""
     Hq, Tq, d = q.shape
     n = k.shape[1]
     o, lse = np.zeros_like(q), np.full((Hq, Tq), -np.inf)
@@ -65,6 +68,8 @@ def attend(q, k, v, scale, causal, group):
             o[h, t], lse[h, t] = p @ v[kv, :m], mx + np.log(z)
             w[kv, :m] += p
             to[h, t] = (2 * e + 2.0 ** -18 + 2.0 ** -12) * (p @ np.abs(v[kv, :m]))
+            if codes:
+                to[h, t] += 2.0 ** -40 * np.abs(v[kv, :m]).sum(0)
             tl[h, t] = e + 2.0 ** -20 * (1 + abs(lse[h, t]))
             tw[kv, :m] += (2 * e + 2.0 ** -18) * p
     return o, lse, w, to, tl, tw

@@ -200,7 +200,7 @@ def check_decode(fa, cache, Hq, Tq, causal=True, accumulate=False, seed=1, seque
     G = Hq // cache.Hkv
     for b in (range(cache.B) if sequences is None else sequences):
         k, v = entries(cache, b)
-        ro, rl, rw, to, tl, tw = R.attend(to64(q[b]), k, v, scale, causal, G)
+        ro, rl, rw, to, tl, tw = R.attend(to64(q[b]), k, v, scale, causal, G, cache.k_scale is not None)
         dead = np.isneginf(rl)
         assert np.array_equal(np.isneginf(to64(lse[b])), dead)
         within(to64(lse[b])[~dead], rl[~dead], tl[~dead])
@@ -241,6 +241,26 @@ def test_decode_paged(fa, case):
     lens, Hq, Hkv, d, ps, Tq, causal, fp8, acc = case
     cache = make_cache(fa, sum(lens) + d, lens, Hkv, d, ps, fp8, weight=acc)
     check_decode(fa, cache, Hq, Tq, causal, acc)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_decode_rows_of_a_head_group(fa, d, fp8):
+    """Every instance by rows (up to 8, 16, 32 and 64 at a time, and more), at both ends of each; units whole
+    and in shares, with weights."""
+    for M in (1, 7, 8, 9, 16, 17, 32, 33, 64, 70):
+        cache = make_cache(fa, 300 + M, [350, 0, 1, 2900], 2, d, 32, fp8, weight=True)
+        check_decode(fa, cache, 2 * M, 1, accumulate=True, seed=M)
+        cache = make_cache(fa, 400 + M, [130, 75, 16], 1, d, 16, fp8, weight=True)
+        check_decode(fa, cache, M, 1, accumulate=True, seed=M)
+
+
+@pytest.mark.parametrize("d,fp8,ps", [(64, False, 16), (128, False, 64), (128, True, 16), (64, True, 64)])
+def test_decode_even_lengths_in_a_long_table(fa, d, fp8, ps):
+    """Units as even as shares: taken whole by the lengths, though the table allows more."""
+    lens = [700, 650, 0, 720] + [690] * 24
+    cache = make_cache(fa, 33, lens, 8, d, ps, fp8, weight=True, width=4096 // ps)
+    check_decode(fa, cache, 24, 1, accumulate=True, sequences=[0, 1, 2, 3, 27])
 
 
 def test_decode_batch_of_many_lengths(fa):
