@@ -1066,10 +1066,10 @@ int evict_launch(const fa_kv_cache &c, int budget, int n_first, int n_recent, fl
     const int per = (a.cap + cs - 1) / cs;
     const bool wide = per <= kSelCap && (long long)units * cs <= INT_MAX;
     if (wide) {
-        if (cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 kSelFixed + kSelCap * 6) != cudaSuccess)
-            return ERR_CUDA;
-        const int st = launch_overlapped(evict_select_kernel, dim3((unsigned)(units * cs)), kPickThreads, kSelFixed + per * 6,
+        int st = allow_smem<evict_select_kernel>(kSelFixed + kSelCap * 6);
+        if (st != OK)
+            return st;
+        st = launch_overlapped(evict_select_kernel, dim3((unsigned)(units * cs)), kPickThreads, kSelFixed + per * 6,
                                          cs, true, s, a, cs, per);
         if (st != OK || lens_out != c.lens)
             return st;

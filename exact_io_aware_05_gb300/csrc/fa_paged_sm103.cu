@@ -1284,8 +1284,8 @@ template <int D, bool FP8, int ROWS>
 int launch_main(const CUtensorMap &tk, const CUtensorMap &tv, const PagedArgs &a, int grid, cudaStream_t s)
 {
     using C = Cfg<D, FP8, ROWS>;
-    if (cudaFuncSetAttribute(paged_kernel<D, FP8, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
-        return ERR_CUDA;
+    if (const int st = allow_smem<paged_kernel<D, FP8, ROWS>>(C::SMEM); st != OK)
+        return st;
     return launch_overlapped(paged_kernel<D, FP8, ROWS>, dim3((unsigned)grid), kThreads, C::SMEM, 0, true, s, tk, tv, a);
 }
 

@@ -2,6 +2,8 @@
 // short kernels that follow one another in a serving step.
 #pragma once
 
+#include <atomic>
+
 #include <cuda_runtime.h>
 
 #include "fa_internal.h"
@@ -15,6 +17,23 @@ namespace fa {
 // end of all before it.
 __device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Allows a kernel its dynamic shared memory (more than 48 KB), once on each device: 0.2 us a call otherwise.
+template <auto Kernel>
+int allow_smem(size_t bytes)
+{
+    static std::atomic<unsigned long long> done{0};   // a bit a device
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess)
+        return ERR_CUDA;
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit)
+        return OK;
+    if (cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess)
+        return ERR_CUDA;
+    done.fetch_or(bit, std::memory_order_relaxed);
+    return OK;
+}
 
 // Launches a kernel; with overlap, one that calls pdl_wait() and may start while the one before it
 // still runs, so that the launch latency is hidden.  cluster > 0: CTAs of a cluster.
