@@ -106,15 +106,11 @@ static int plain(PyObject *t, PyObject *dtype, int n, const long long *shape, lo
     return data_of(t, p);
 }
 
-/* A [B, H, T, d] tensor by strides; H < 0: any number of heads. */
-static int heads(PyObject *t, PyObject *dtype, long long B, long long H, long long T, long long d, long long index,
-                 fa_heads *out)
+/* The strides and the address of a tensor of shape s. */
+static int strided(PyObject *t, const long long *s, fa_heads *out)
 {
-    long long s[4], st[4];
-    if (!has_dtype(t, dtype) || !tuple_of(t, n_shape, 0, 4, s) || !on_device(t, index) ||
-        !tuple_of(t, n_stride, 1, 4, st))
-        return 0;
-    if (s[0] != B || (H >= 0 && s[1] != H) || s[2] != T || s[3] != d || st[3] != 1 || s[1] > INT_MAX)
+    long long st[4];
+    if (!tuple_of(t, n_stride, 1, 4, st) || st[3] != 1 || s[1] > INT_MAX)
         return 0;
     /* the stride of a dimension of one entry is never used: torch leaves any value there */
     out->stride_b = s[0] > 1 ? st[0] : 0;
@@ -122,6 +118,18 @@ static int heads(PyObject *t, PyObject *dtype, long long B, long long H, long lo
     out->stride_t = s[2] > 1 ? st[2] : 0;
     out->H = (int)s[1];
     return data_of(t, &out->data);
+}
+
+/* A [B, H, T, d] tensor by strides; H < 0: any number of heads. */
+static int heads(PyObject *t, PyObject *dtype, long long B, long long H, long long T, long long d, long long index,
+                 fa_heads *out)
+{
+    long long s[4];
+    if (!has_dtype(t, dtype) || !tuple_of(t, n_shape, 0, 4, s) || !on_device(t, index))
+        return 0;
+    if (s[0] != B || (H >= 0 && s[1] != H) || s[2] != T || s[3] != d)
+        return 0;
+    return strided(t, s, out);
 }
 
 /* The stream to launch on, if `index` is the current device. */
@@ -173,16 +181,16 @@ static PyObject *py_rope(PyObject *self, PyObject *const *a, Py_ssize_t n)
     fa_stream_t s;
     long long shape[4];
     int ok = 1, inverse;
-    PyObject *dtype = has_dtype(a[1], t_bf16) ? t_bf16 : t_f32;
+    PyObject *dtype = has_dtype(a[1], t_bf16) ? t_bf16 : has_dtype(a[1], t_f32) ? t_f32 : NULL;
     PyObject *index = PyObject_CallMethodNoArgs(a[1], n_get_device);
     Py_XINCREF(index);
     const long long dev = taken_int(index, &ok);
-    if (!ok || !tuple_of(a[1], n_shape, 0, 4, shape))
+    if (!dtype || !ok || !tuple_of(a[1], n_shape, 0, 4, shape))
         goto no;
     const long long B = shape[0], T = shape[2], d = shape[3], at[3] = {spec->n_axes, B, T};
     const int two = a[3] != Py_None;
     if (d != spec->d || two != (a[4] != Py_None) || B > INT_MAX || T > INT_MAX || !int_arg(a[6], &inverse) ||
-        !plain(a[5], t_i32, 3, at, dev, &pos) || !heads(a[1], dtype, B, -1, T, d, dev, &x[0]) ||
+        !plain(a[5], t_i32, 3, at, dev, &pos) || !strided(a[1], shape, &x[0]) ||
         !heads(a[2], dtype, B, x[0].H, T, d, dev, &y[0]))
         goto no;
     if (two && (!heads(a[3], dtype, B, -1, T, d, dev, &x[1]) || !heads(a[4], dtype, B, x[1].H, T, d, dev, &y[1])))
@@ -222,7 +230,8 @@ static PyObject *py_append(PyObject *self, PyObject *const *a, Py_ssize_t n)
     const long long B = c->B, T = shape[2], d = c->d, lens[1] = {B};
     const int rotate = spec != NULL, with_q = a[6] != Py_None;
     if (rotate != (a[4] != Py_None) || with_q != (a[7] != Py_None) || (with_q && !rotate) ||
-        !heads(a[2], t_bf16, B, c->Hkv, T, d, dev, &k) || !heads(a[3], t_bf16, B, c->Hkv, T, d, dev, &v))
+        shape[0] != B || shape[1] != c->Hkv || shape[3] != d || !has_dtype(a[2], t_bf16) || !on_device(a[2], dev) ||
+        !strided(a[2], shape, &k) || !heads(a[3], t_bf16, B, c->Hkv, T, d, dev, &v))
         return slow();
     if (rotate) {
         const long long at[3] = {spec->n_axes, B, T};
@@ -258,13 +267,12 @@ static PyObject *py_decode(PyObject *self, PyObject *const *a, Py_ssize_t n)
     void *q, *o, *lse, *ws;
     fa_stream_t s;
     long long shape[4];
-    if (!ok || !tuple_of(a[2], n_shape, 0, 4, shape) || shape[1] > INT_MAX || shape[2] > INT_MAX)
+    if (!ok || !tuple_of(a[2], n_shape, 0, 4, shape) || shape[0] != c->B || shape[1] > INT_MAX || shape[2] > INT_MAX ||
+        shape[3] != c->d || !has_dtype(a[2], t_bf16) || !on_device(a[2], dev) || !is_contiguous(a[2]) || !data_of(a[2], &q))
         return slow();
-    shape[0] = c->B;
-    shape[3] = c->d;
     const double scale = PyFloat_AsDouble(a[5]);
     const int causal = PyObject_IsTrue(a[7]), accumulate = PyObject_IsTrue(a[8]);
-    if (PyErr_Occurred() || !plain(a[2], t_bf16, 4, shape, dev, &q) || !plain(a[3], t_bf16, 4, shape, dev, &o) ||
+    if (PyErr_Occurred() || !plain(a[3], t_bf16, 4, shape, dev, &o) ||
         !plain(a[4], t_f32, 3, shape, dev, &lse) || !on_device(a[6], dev) || !is_contiguous(a[6]) || !data_of(a[6], &ws))
         return slow();
     const long long bytes = taken_int(PyObject_GetAttr(a[6], n_nbytes), &ok);
