@@ -17,14 +17,14 @@
 //   * One warp fills a ring of tiles by TMA, a box per page (all 128-byte column chunks of its
 //     rows at once, swizzled); page numbers are read one tile ahead.
 //   * Four warps compute with m16n8k16 products out of registers (ldmatrix): a warp owns up to 16 query
-//     rows and a quarter, half or all of a tile's entries (1, 2 or 4 row tiles).  They reach 200 to 270
-//     TFLOP/s in all, about what e4m3 needs with 16 rows a product.  So up to 8 rows the operands
-//     change places, K and V^T being the 16 rows and the queries the 8 columns, and half the products
-//     do (e4m3, 16 sequences of 1001 to 65536, d 64 55.5 -> 53.6 us; 160 units of 2048 to 4096, d 256 65 -> 52).
+//     rows and a quarter, half or all of a tile's entries (1, 2 or 4 row tiles).  Up to 8 rows the
+//     operands change places, K and V^T being the 16 rows and the queries the 8 columns: half the
+//     products and half the accumulators do, which e4m3 needs most, two entries of which come with the bytes of
+//     one (16 sequences of 1001 to 65536, d 64 55.5 -> 53.6 us; 160 units of 2048 to 4096, d 256 65 -> 52).
 //     The tensor cores of the fifth generation want 128 rows a product: with up to 16 rows, the usual
 //     case, they would run nearly empty, and their accumulators would have to come back for the
 //     softmax, where the warp-level products leave S in the registers that P V takes.  At 64 rows
-//     these products are the bound (see below).
+//     the bound are the math warps, two a scheduler, with the product pipe 40 % busy (see below).
 //   * P enters its product as two bf16 numbers (its leading 8 bits and the rest), so its error is
 //     2^-17 and not 2^-9, which would be as large as the output's own rounding.  e4m3 codes become
 //     f16 exactly; there q is scaled by a power of two per row and P by 2^15, which keeps
