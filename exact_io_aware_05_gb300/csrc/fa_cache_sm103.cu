@@ -284,7 +284,8 @@ struct AppendArgs {
 // 8 values into the cache: bf16, or e4m3 codes of x / scale, the quotient rounded to nearest.  With
 // inv the rounded reciprocal of the scale, q = x inv is within one step of the quotient, and
 // q + (x - q scale) inv rounds it correctly (P. Markstein, 1990): three operations for two values
-// where the divide takes several each.  Values that would overflow on the way are divided.
+// where the divide takes several each.  A quotient that could overflow
+// on the way is far beyond the largest code, and stays as it is.
 template <bool FP8>
 __device__ __forceinline__ void put8(void *base, long long at, const float (&x)[8], float scale, float inv)
 {
@@ -304,8 +305,10 @@ __device__ __forceinline__ void put8(void *base, long long at, const float (&x)[
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                q[j] = __fdiv_rn(x[j], scale);
+            for (int j = 0; j < 8; ++j) {
+                const float y = fmaf(fmaf(q[j], -scale, x[j]), inv, q[j]);
+                q[j] = fabsf(q[j]) < 1e30f ? y : q[j];
+            }
         }
         uint2 w;
         w.x = pack_e4m3x4(q[0], q[1], q[2], q[3]);
