@@ -27,8 +27,9 @@
 //     the bound are the math warps, two a scheduler, with the product pipe 40 % busy (see below).
 //   * P enters its product as two bf16 numbers (its leading 8 bits and the rest), so its error is
 //     2^-17 and not 2^-9, which would be as large as the output's own rounding.  e4m3 codes become
-//     f16 exactly; there q is scaled by a power of two per row and P by 2^15, which keeps
-//     probabilities down to 2^-29 in f16's normal range, with 11 bits.
+//     f16 exactly; there P is scaled by 2^15, which keeps probabilities down to 2^-29 in f16's normal
+//     range, with 11 bits, and a row of q by the power of two that puts its largest value next to
+//     f16's end: bf16's 8 bits are exact down to 2^-31 of that value.
 //
 // Measured: 8 sequences of 32768 entries, 32 KV heads, d 128 (4.3 GB) 594 us, 7.2 TB/s; 64 sequences of 200 to
 // 8000, 8 KV heads (1.1 GB) 164 us, 6.6 TB/s; 17 entries of one sequence 3.7 us.  Of the second, 3 us pass
@@ -515,10 +516,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, ROWS>::CTAS)
 #pragma unroll
                     for (int off = 16; off > 0; off >>= 1)
                         big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
-                    // 2^-e brings the row's largest value into [1, 4); zeros and infinities stay
-                    const int x = (int)(__float_as_uint(big) >> 23);
-                    const int e = x == 255 || x == 0 ? 0 : min(x - 127, 126);
-                    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+                    // a power of two, `down`, brings the row's largest value into [2^14, 2^15) (as far as 2^127
+                    // does): what a bf16 value of 2^-31 of it or more holds stays whole, below that a multiple of
+                    // 2^-38 of it; sums of d products with codes stay below 2^15 448 d < 2^32.  Zeros and
+                    // infinities stay
+                    const int x = (int)(__float_as_uint(big) >> 23), de = x == 255 || x == 0 ? 127 : min(268 - x, 254);
+                    const float down = __uint_as_float((uint32_t)de << 23);
                     scale *= qks / down;
 #pragma unroll
                     for (int i = 0; i < D / 64; ++i) {

@@ -294,6 +294,8 @@ int fa_cache_append(const fa_kv_cache *cache, const fa_heads *k, const fa_heads 
  * the call sees may reach every row of its head group.  Scores, statistics and
  * the row sums are fp32; a probability meets v with 16 bits, in an FA_E4M3 cache
  * with 11, or, below 2^-29 of the row's largest, to a multiple of 2^-39 of it.
+ * There q meets the codes exactly, but a feature below 2^-31 of its row's largest
+ * to a multiple of 2^-38 of that.
  * The keys are split over the thread blocks in equal shares of the whole batch,
  * and partial results are joined in a fixed order: the same call gives the same
  * bits, but a sequence's last bits may depend on the other lengths.
