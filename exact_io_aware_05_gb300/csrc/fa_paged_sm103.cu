@@ -38,6 +38,7 @@
 // with 4, 8, 16, 32 and 64; e4m3, twice as long: 46, 47, 54, 96 and 162, its codes being converted by
 // every row tile.
 #include <algorithm>
+#include <cfloat>
 #include <climits>
 
 #include <cuda_fp16.h>
@@ -191,6 +192,17 @@ __device__ __forceinline__ float quad_max(float x)
 {
     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
     return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+}
+
+// The product of three positive factors, the largest and the smallest first, so that no part of it
+// leaves fp32's range where the whole does not.  What is too small becomes the smallest normal number: a
+// factor of 0 would make a NaN of a masked entry's -inf, and 2^32 times it is still nothing as a score.  In
+// the same way what is too large stays finite, for sums of 0.
+__device__ __forceinline__ float score_scale(float a, float b, float c)
+{
+    const float hi = fmaxf(a, b), lo = fminf(a, b);
+    const float x = fmaxf(hi, c) * fminf(lo, c) * fmaxf(lo, fminf(hi, c));
+    return fminf(fmaxf(x, FLT_MIN), FLT_MAX);
 }
 
 // ------------------------------------------------------------------ shares
@@ -522,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, ROWS>::CTAS)
                     // infinities stay
                     const int x = (int)(__float_as_uint(big) >> 23), de = x == 255 || x == 0 ? 127 : min(268 - x, 254);
                     const float down = __uint_as_float((uint32_t)de << 23);
-                    scale *= qks / down;
+                    scale = score_scale(scale, qks, 1.f / down);
 #pragma unroll
                     for (int i = 0; i < D / 64; ++i) {
                         const int f = i * 64 + 2 * lane, c = (f & 15) >> 2;   // features f, f + 1
@@ -1381,7 +1393,7 @@ int paged_launch(const fa_kv_cache &c, const void *q, void *o, float *lse, int H
     a.where = reinterpret_cast<long long *>(ws);
     a.part = reinterpret_cast<float *>(ws + where_bytes(c.B));
     a.scores = accumulate ? reinterpret_cast<float *>(ws + where_bytes(c.B) + part_bytes(a.M, c.d)) : nullptr;
-    a.scale_log2 = scale * 1.4426950408889634f;
+    a.scale_log2 = std::min(scale * 1.4426950408889634f, FLT_MAX);   // finite, for sums of 0
     a.timeout_ns = wait_timeout_ns();
     return c.d == 64 ? paged_run<64>(c, a, s) : c.d == 128 ? paged_run<128>(c, a, s) : paged_run<256>(c, a, s);
 }

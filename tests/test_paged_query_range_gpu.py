@@ -55,3 +55,30 @@ def test_one_large_feature_against_zero_keys(fa, d, rows, below):
     q[..., 0] = 4096.0
     # scores of a few units: keys are about 40 k_scale
     check(fa, cache, q.to(BF16), 2.0 ** (below - 12) / (40 * float(cache.k_scale.max()) * d ** 0.5), 2)
+
+
+@pytest.mark.parametrize("rows", [1, 16, 40])
+@pytest.mark.parametrize("q_exp,k_exp", [(-100, -64), (-126, 0), (-130, -30), (-60, -64), (0, -64), (60, -60), (-70, 64)])
+def test_scores_of_small_and_large_scales(fa, rows, q_exp, k_exp):
+    """Queries and key scales from end to end of their ranges, entries masked by length and by row: what
+    underflows is 0, and masked entries stay masked."""
+    cache = make_cache(fa, 95, [37, 100, 5], 1, 64, 16, fp8=True, weight=True)
+    cache.k_scale.fill_(2.0 ** k_exp)
+    q = (randn(gen(96), 3, rows, 3, 64, dtype=F32).double() * 2.0 ** q_exp).to(BF16)
+    c = 1.0 if q_exp + k_exp < -20 else 2.0 ** -10
+    check(fa, cache, q, c, 1)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("rows", [1, 16, 40])
+def test_zero_scores_of_the_largest_scales(fa, rows, fp8):
+    """Keys of 0 under the largest query, key scale and softmax scale: every entry counts alike."""
+    cache = make_cache(fa, 97, [37, 100, 5], 1, 64, 16, fp8=fp8, weight=True)
+    for b in range(3):
+        cache.k[cache.block_table[b, :-(-int(cache.lens[b]) // 16)].long()] = 0
+    if fp8:
+        cache.k_scale.fill_(2.0 ** 64)
+    q = (randn(gen(98), 3, rows, 1, 64, dtype=F32).clamp(-2, 2) * 2.0 ** 100).to(BF16)
+    check(fa, cache, q, 3.0e38, 1)
+    q.zero_()
+    check(fa, cache, q, 1e-44, 1)
