@@ -589,44 +589,58 @@ def rope_backward(dq_out, dk_out, positions, spec: RopeSpec, stream=None):
 
 # ---------------------------------------------------------------- paged key/value cache
 class KVCache:
-    """Handle of a paged cache (fa_kv_cache in include/fa.h): checks the tensors once and keeps
+    """Handle of a paged cache (fa_kv_cache in include/fa.h): checks its tensors once and keeps
     them.  k, v: [num_pages, Hkv, page_size, d] bf16, or uint8 e4m3 codes with k_scale and
     v_scale [Hkv] float32; block_table [B, max_pages] int32; lens [B] int32 (entries of each
     sequence, updated by the caller and by fa_cache_evict); seen [B] int32 (tokens ever
     appended; default: lens); weight float32 and order int32 [B, Hkv, max_pages * page_size],
-    both optional.  The contents are read at each call, so tensors are changed in place."""
+    both optional.  The contents are read at each call.  A tensor assigned to one of these names is
+    checked and takes the place of the one before, for calls from then on (a captured graph keeps the
+    one that it was captured with); sizes stay as they are."""
+
+    _TENSORS = ("k", "v", "block_table", "lens", "k_scale", "v_scale", "seen", "weight", "order")
+    _FIXED = ("B", "Hkv", "d", "page_size", "num_pages", "max_pages", "device")
 
     def __init__(self, k, v, block_table, lens, k_scale=None, v_scale=None, weight=None, order=None, seen=None):
         if k.dim() != 4 or block_table.dim() != 2:
             raise ValueError("k must be [num_pages, Hkv, page_size, d] and block_table [B, max_pages]")
-        dev = k.device
-        num_pages, Hkv, ps, d = k.shape
-        B, max_pages = block_table.shape
         if k.dtype not in (torch.bfloat16, torch.uint8):
             raise TypeError(f"k: expected torch.bfloat16 or torch.uint8 (e4m3 codes), got {k.dtype}")
-        _need(k, "k", k.dtype, (num_pages, Hkv, ps, d), dev)
-        _need(v, "v", k.dtype, (num_pages, Hkv, ps, d), dev)
-        _need(block_table, "block_table", torch.int32, (B, max_pages), dev)
-        _need(lens, "lens", torch.int32, (B,), dev)
+        num_pages, Hkv, ps, d = k.shape
+        B, max_pages = block_table.shape
         codes = k.dtype == torch.uint8
-        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-            if (t is not None) != codes:
-                raise ValueError(f"{name}: needed with e4m3 codes and only with them")
+        f32, i32, pool, slots = torch.float32, torch.int32, (k.dtype, (num_pages, Hkv, ps, d)), (B, Hkv, max_pages * ps)
+        self.__dict__.update(
+            B=B, Hkv=Hkv, d=d, page_size=ps, num_pages=num_pages, max_pages=max_pages, device=k.device, _index=k.get_device(),
+            _c=_KVCache(B=B, Hkv=Hkv, d=d, page_size=ps, num_pages=num_pages, max_pages=max_pages,
+                        dtype=FA_E4M3 if codes else FA_BF16),
+            # type and shape of each tensor, and whether it is there: always, never or as the caller likes (None)
+            _want=dict(k=(*pool, True), v=(*pool, True), block_table=(i32, (B, max_pages), True), lens=(i32, (B,), True),
+                       k_scale=(f32, (Hkv,), codes), v_scale=(f32, (Hkv,), codes), seen=(i32, (B,), None),
+                       weight=(f32, slots, None), order=(i32, slots, None)))
+        self.__dict__["_ref"] = ctypes.addressof(self._c)
+        for name, t in zip(self._TENSORS, (k, v, block_table, lens, k_scale, v_scale, seen, weight, order)):
+            setattr(self, name, t)
+
+    def __setattr__(self, name, t):
+        if name in self._FIXED:
+            raise AttributeError(f"{name} of a KVCache is fixed: its tensors' sizes and the structure say so")
+        if name in self._TENSORS:
+            dtype, shape, there = self._want[name]
+            if there is not None and (t is not None) != there:
+                raise ValueError(f"{name}: needed" if there and "scale" not in name else
+                                 f"{name}: needed with e4m3 codes and only with them")
             if t is not None:
-                _need(t, name, torch.float32, (Hkv,), dev)
-        if seen is not None:
-            _need(seen, "seen", torch.int32, (B,), dev)
-        if weight is not None:
-            _need(weight, "weight", torch.float32, (B, Hkv, max_pages * ps), dev)
-        if order is not None:
-            _need(order, "order", torch.int32, (B, Hkv, max_pages * ps), dev)
-        self.k, self.v, self.block_table, self.lens = k, v, block_table, lens
-        self.k_scale, self.v_scale, self.weight, self.order, self.seen = k_scale, v_scale, weight, order, seen
-        self.B, self.Hkv, self.d, self.page_size, self.num_pages, self.max_pages = B, Hkv, d, ps, num_pages, max_pages
-        self.device, self._index = dev, k.get_device()
-        self._c = _KVCache(*(_ptr(t) for t in (k, v, k_scale, v_scale, block_table, lens, seen, weight, order)),
-                           B, Hkv, d, ps, num_pages, max_pages, FA_E4M3 if codes else FA_BF16)
-        self._ref = ctypes.addressof(self._c)
+                if not isinstance(t, torch.Tensor):
+                    raise TypeError(f"{name}: expected a tensor, got {type(t).__name__}")
+                _need(t, name, dtype, shape, self.device)
+            setattr(self._c, name, _ptr(t))   # what the calls read
+        self.__dict__[name] = t
+
+    def __delattr__(self, name):
+        if name in self._FIXED or name in self._TENSORS:
+            raise AttributeError(f"{name} of a KVCache cannot be deleted")
+        object.__delattr__(self, name)
 
 
 def alloc_kv_cache(B: int, Hkv: int, d: int, max_len: int, page_size: int = 16, k_scale=None, v_scale=None,
