@@ -450,6 +450,10 @@ class RopeSpec:
             (ctypes.c_ubyte * len(axis))(*axis), int(self.interleaved)))
         self._ref = ctypes.addressof(self._c)
 
+    def __setstate__(self, state):   # of a copy or a pickle: the address is of its own structure
+        self.__dict__.update(state)
+        self._ref = ctypes.addressof(self._c)
+
 
 def rope_spec(d: int, sections=None, base: float = 10000.0, rot: int | None = None,
               interleaved: bool = False) -> RopeSpec:
@@ -641,6 +645,10 @@ class KVCache:
         if name in self._FIXED or name in self._TENSORS:
             raise AttributeError(f"{name} of a KVCache cannot be deleted")
         object.__delattr__(self, name)
+
+    def __reduce__(self):   # copies and pickles are handles of their own, with a structure of their own
+        return type(self), (self.k, self.v, self.block_table, self.lens, self.k_scale, self.v_scale, self.weight, self.order,
+                            self.seen)
 
 
 def alloc_kv_cache(B: int, Hkv: int, d: int, max_len: int, page_size: int = 16, k_scale=None, v_scale=None,

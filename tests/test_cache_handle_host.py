@@ -1,5 +1,9 @@
 """The handles KVCache and RopeSpec on the host: what the structure that the C calls read holds after
 their attributes change.  Tensors are on the CPU and nothing is launched."""
+import copy
+import ctypes
+import pickle
+
 import pytest
 import torch
 
@@ -81,3 +85,30 @@ def test_what_does_not_fit_is_refused_and_changes_nothing(fa):
         del cache.lens
     cache.note = "a name of the caller's own"
     assert held(cache)
+
+
+def test_copies_of_a_spec_have_their_own_table(fa):
+    """A copy (deep, or from a pickle) reads its own structure, which lives as long as it does."""
+    spec = fa.rope_spec(64, (8, 12, 12), interleaved=True)
+    for copied in (copy.deepcopy(spec), copy.copy(spec), pickle.loads(pickle.dumps(spec))):
+        assert copied._ref == ctypes.addressof(copied._c)
+        assert bytes(copied._c) == bytes(spec._c)
+        assert (copied.d, copied.rot, copied.n_axes, copied.interleaved) == (64, 64, 3, True)
+    assert copy.deepcopy(spec)._ref != spec._ref
+
+
+@pytest.mark.parametrize("codes", [False, True])
+def test_copies_of_a_cache_are_handles_of_their_own(fa, codes):
+    """A shallow copy shares the tensors, not the structure; a deep copy or a pickle has tensors of its own."""
+    cache = fa.KVCache(**tensors(codes))
+    cache.order = None
+    shallow = copy.copy(cache)
+    assert held(shallow) and shallow._ref != cache._ref and shallow._ref == ctypes.addressof(shallow._c)
+    assert all(getattr(shallow, n) is getattr(cache, n) for n in cache._TENSORS)
+    shallow.lens = shallow.lens + 5
+    assert held(shallow) and held(cache) and cache.lens.tolist() == [0, 0, 0]
+    for own in (copy.deepcopy(cache), pickle.loads(pickle.dumps(cache))):
+        assert held(own) and own._ref == ctypes.addressof(own._c)
+        for n in cache._TENSORS:
+            a, b = getattr(own, n), getattr(cache, n)
+            assert (a is None) == (b is None) and (a is None or (a.data_ptr() != b.data_ptr() and torch.equal(a, b)))
