@@ -6,8 +6,8 @@ types or headers are involved: the library is a plain C ABI (include/fa.h).
 The host compiler also builds ``_fa_py.so``, a CPython module with the binding's
 argument checks for the rotary and cache calls (csrc/fa_py.c).
 
-With ``test_variant=True`` the same pool also compiles the API and the two
-tile-loop units with ``FA_TEST_WITHHOLD=1`` into ``_build/waittest/`` and links
+With ``test_variant=True`` the same pool also compiles the API, the two
+tile-loop units and the paged decode with ``FA_TEST_WITHHOLD=1`` into ``_build/waittest/`` and links
 them with the other product objects into ``libfa_waittest.so``: a library for
 the tests of the bounded-wait timeout path only (one launch may leave out one
 mbarrier arrive).  Nothing in the package loads it; libfa.so never contains it.
@@ -32,7 +32,7 @@ SOURCES = ["fa_api.cu", "fa_fwd_sm103.cu", "fa_fwd_f32.cu", "fa_bwd_sm103.cu", "
            "fa_decode_sm103.cu", "fa_fp8_sm103.cu", "fa_cache_api.cu", "fa_cache_sm103.cu",
            "fa_paged_sm103.cu"]
 # the units that read FA_TEST_WITHHOLD; the test library takes the others from the product build
-TEST_SOURCES = ["fa_api.cu", "fa_fwd_sm103.cu", "fa_bwd_sm103.cu"]
+TEST_SOURCES = ["fa_api.cu", "fa_fwd_sm103.cu", "fa_bwd_sm103.cu", "fa_paged_sm103.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -570,20 +570,26 @@ int fa_bwd_stage(int stage, const void *q, const void *k, const void *v, const v
                       workspace_bytes, 1 << (stage - 1), stream);
 }
 
+// The status word of the first kernel file that has one (all are read and cleared).
+static int fetch_status(cudaStream_t s, int *word)
+{
+    int w[5] = {0, 0, 0, 0, 0};
+    if (fa::fwd_status_fetch_clear(s, &w[0]) != fa::OK || fa::bwd_status_fetch_clear(s, &w[1]) != fa::OK ||
+        fa::dec_status_fetch_clear(s, &w[2]) != fa::OK || fa::paged_status_fetch_clear(s, &w[3]) != fa::OK ||
+        fa::cache_status_fetch_clear(s, &w[4]) != fa::OK)
+        return fa::ERR_CUDA;
+    for (int i = 0; i < 5 && *word == 0; ++i)
+        *word = w[i];
+    return fa::OK;
+}
+
 int fa_sync_status(fa_stream_t stream)
 {
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (cudaStreamSynchronize(s) != cudaSuccess)
         return FA_ERR_CUDA;
-    int w[5] = {0, 0, 0, 0, 0};
-    if (fa::fwd_status_fetch_clear(s, &w[0]) != fa::OK || fa::bwd_status_fetch_clear(s, &w[1]) != fa::OK ||
-        fa::dec_status_fetch_clear(s, &w[2]) != fa::OK || fa::paged_status_fetch_clear(s, &w[3]) != fa::OK ||
-        fa::cache_status_fetch_clear(s, &w[4]) != fa::OK)
-        return FA_ERR_CUDA;
-    for (int i = 0; i < 5; ++i)
-        if (w[i])
-            return w[i] & 0xFF;
-    return FA_OK;
+    int word = 0;
+    return fetch_status(s, &word) == fa::OK ? (word & 0xFF) : FA_ERR_CUDA;
 }
 
 const char *fa_status_string(int status)
@@ -620,11 +626,8 @@ int fa_test_status_word(fa_stream_t stream)
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (cudaStreamSynchronize(s) != cudaSuccess)
         return -1;
-    int wf = 0, wb = 0, wd = 0;
-    if (fa::fwd_status_fetch_clear(s, &wf) != fa::OK || fa::bwd_status_fetch_clear(s, &wb) != fa::OK ||
-        fa::dec_status_fetch_clear(s, &wd) != fa::OK)
-        return -1;
-    return wf ? wf : (wb ? wb : wd);
+    int word = 0;
+    return fetch_status(s, &word) == fa::OK ? word : -1;
 }
 #endif
 

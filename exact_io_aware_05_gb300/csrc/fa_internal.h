@@ -44,10 +44,12 @@ uint64_t wait_timeout_ns();     // bounded-wait limit for device spin waits
 //                     unit; only that tile's softmax waits for it (epilogue)
 //   WITHHOLD_BWD_DKV  backward tile loop, CTA 0: the "dK, dV complete" signal of its
 //                     first unit; only the drain warpgroup waits for it
+//   WITHHOLD_PAGED_FULL  paged decode, CTA 0: the loader's arrive for its first tile; the math
+//                     warps wait for it, and in a unit longer than the ring the loader for them
 #ifndef FA_TEST_WITHHOLD
 #define FA_TEST_WITHHOLD 0
 #endif
-enum : int { WITHHOLD_NONE = 0, WITHHOLD_FWD_KV = 1, WITHHOLD_FWD_EPI = 2, WITHHOLD_BWD_DKV = 3 };
+enum : int { WITHHOLD_NONE = 0, WITHHOLD_FWD_KV = 1, WITHHOLD_FWD_EPI = 2, WITHHOLD_BWD_DKV = 3, WITHHOLD_PAGED_FULL = 4 };
 #if FA_TEST_WITHHOLD
 int test_withhold_take(int lo, int hi);   // the armed case if in [lo, hi] (then disarmed), else 0
 #endif

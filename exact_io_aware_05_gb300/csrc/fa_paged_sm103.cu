@@ -112,6 +112,7 @@ struct PagedArgs {
     long long *where;   // [0] the share, [1 + b] the first tile of sequence b (not of an empty one)
     float *scores;   // [sequence][KV head][row][cap]
     int B, Hq, Hkv, G, Tq, M, rows, RB, causal, num_pages, max_pages, ps_shift, cap, grid, whole, may_whole, kt;
+    int withhold;   // test builds: the arrive that is left out
     float scale_log2;
     uint64_t timeout_ns;
 };
@@ -172,6 +173,11 @@ __device__ __forceinline__ void tma_load_4d_hint(uint32_t dst, const CUtensorMap
         " [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w), "l"(policy)
         : "memory");
+}
+// Bytes that a phase waits for, without the arrive (test builds).
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ uint64_t policy_evict_normal()
 {
@@ -444,7 +450,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, ROWS>::CTAS)
             for (int i = 0; i < cnt; ++i, ++n) {
                 const int tile = p.tile + i, slot = tile * C::KT + (box << bp_shift);
                 const int next = i + 1 < cnt ? page_at(tile + 1) : -1;
-                if (round > 0 && !mbar_wait_warp(bar0 + 8u * (C::NST + st), (round - 1) & 1u, ctx, SITE_PAGED_EMPTY)) {
+                // A math warp that has given up releases its stages unread, after raising the abort flag: such a
+                // stage is not filled again, so that each full barrier's phase is that of its last fill
+                if (round > 0 && (!mbar_wait_warp(bar0 + 8u * (C::NST + st), (round - 1) & 1u, ctx, SITE_PAGED_EMPTY) ||
+                                  __any_sync(0xffffffffu, *abort_flag))) {
                     ok = false;
                     break;
                 }
@@ -461,7 +470,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, ROWS>::CTAS)
                 const uint32_t loads = __popc(__ballot_sync(0xffffffffu, good));
                 if (lane == 0) {
                     there[st] = groups;
-                    mbar_arrive_expect_tx(bar0 + 8u * st, loads * box_bytes);
+#if FA_TEST_WITHHOLD
+                    const bool hold = a.withhold == WITHHOLD_PAGED_FULL && blockIdx.x == 0 && n == 0;
+#else
+                    constexpr bool hold = false;
+#endif
+                    if (hold)
+                        mbar_expect_tx(bar0 + 8u * st, loads * box_bytes);
+                    else
+                        mbar_arrive_expect_tx(bar0 + 8u * st, loads * box_bytes);
                 }
                 __syncwarp();
                 if (good)
@@ -476,9 +493,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, ROWS>::CTAS)
             if (ok)
                 next_unit(a, p, cnt);
         }
-        if (!ok)   // copies already issued land before the CTA exits
-            for (uint32_t s = n < depth ? 0 : n - depth; s < n; ++s)
-                mbar_wait_drain(bar0 + 8u * (s % depth), (s / depth) & 1u);
+        // Every copy lands before the CTA exits, whoever gave up: the math warps may have done so after the
+        // last copy was issued
+        for (uint32_t s = n < depth ? 0 : n - depth; s < n; ++s)
+            mbar_wait_drain(bar0 + 8u * (s % depth), (s / depth) & 1u);
     } else {
         // ---------------------------------------------------------- math
         const int rt = warp % RT, kw = warp / RT, c4 = lane & 3, r0 = lane >> 2;
@@ -618,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, ROWS>::CTAS)
             float m0 = -INFINITY, m1 = -INFINITY, l0[2] = {0.f, 0.f}, l1[2] = {0.f, 0.f};
 
             for (int i = 0; i < cnt; ++i) {
-                if (!mbar_wait_warp(bar0 + 8u * st, round & 1u, ctx, SITE_PAGED_FULL))
+                if (ok && !mbar_wait_warp(bar0 + 8u * st, round & 1u, ctx, SITE_PAGED_FULL))
                     ok = false;   // the CTA gives up: no more is computed or written, and its warps still meet
                 const uint32_t groups = ok ? there[st] : 0u;
 #pragma unroll 1
@@ -1395,6 +1413,10 @@ int paged_launch(const fa_kv_cache &c, const void *q, void *o, float *lse, int H
     a.scores = accumulate ? reinterpret_cast<float *>(ws + where_bytes(c.B) + part_bytes(a.M, c.d)) : nullptr;
     a.scale_log2 = std::min(scale * 1.4426950408889634f, FLT_MAX);   // finite, for sums of 0
     a.timeout_ns = wait_timeout_ns();
+    a.withhold = WITHHOLD_NONE;
+#if FA_TEST_WITHHOLD
+    a.withhold = test_withhold_take(WITHHOLD_PAGED_FULL, WITHHOLD_PAGED_FULL);
+#endif
     return c.d == 64 ? paged_run<64>(c, a, s) : c.d == 128 ? paged_run<128>(c, a, s) : paged_run<256>(c, a, s);
 }
 
