@@ -570,7 +570,8 @@ int fa_bwd_stage(int stage, const void *q, const void *k, const void *v, const v
                       workspace_bytes, 1 << (stage - 1), stream);
 }
 
-// The status word of the first kernel file that has one (all are read and cleared).
+// The status word of the first kernel file that has one (all are read and cleared): those with waits come
+// before those that report indexes alone, so that a timeout is told first.
 static int fetch_status(cudaStream_t s, int *word)
 {
     int w[5] = {0, 0, 0, 0, 0};

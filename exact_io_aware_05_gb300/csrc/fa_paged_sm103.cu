@@ -49,7 +49,9 @@
 
 namespace fa {
 
-__device__ int g_paged_status;   // device status word of the kernels in this file
+// Device status words of the kernels in this file: a wait that ran out, and an index out of range.  Two, because
+// indexes are checked first, and a timeout, after which nothing of the call is valid, must not be lost to one.
+__device__ int g_paged_status, g_paged_index;
 
 namespace {
 
@@ -215,7 +217,7 @@ __device__ __forceinline__ float score_scale(float a, float b, float c)
 __device__ __forceinline__ int length_in_range(const PagedArgs &a, int len)
 {
     if (len < 0 || len > a.cap) {
-        atomicCAS(&g_paged_status, 0, kStatusBadIndex);
+        atomicCAS(&g_paged_index, 0, kStatusBadIndex);
         return 0;
     }
     return len;
@@ -459,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, ROWS>::CTAS)
                 }
                 const bool inside = mine && slot < len, good = inside && page >= 0 && page < a.num_pages;
                 if (inside && !good)
-                    atomicCAS(&g_paged_status, 0, kStatusBadIndex);
+                    atomicCAS(&g_paged_index, 0, kStatusBadIndex);
                 // groups of 16 entries whose page is there and that begin in front of the length
                 uint32_t groups = 0;
                 if (good && !(lane & 1))
@@ -1422,11 +1424,15 @@ int paged_launch(const fa_kv_cache &c, const void *q, void *o, float *lse, int H
 
 int paged_status_fetch_clear(cudaStream_t s, int *host_word)
 {
-    int zero = 0;
+    int zero = 0, index = 0;
     if (cudaMemcpyFromSymbolAsync(host_word, g_paged_status, sizeof(int), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
         cudaMemcpyToSymbolAsync(g_paged_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s) != cudaSuccess ||
+        cudaMemcpyFromSymbolAsync(&index, g_paged_index, sizeof(int), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+        cudaMemcpyToSymbolAsync(g_paged_index, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s) != cudaSuccess ||
         cudaStreamSynchronize(s) != cudaSuccess)
         return ERR_CUDA;
+    if (*host_word == 0)
+        *host_word = index;
     return OK;
 }
 

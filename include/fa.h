@@ -451,8 +451,8 @@ int fa_bwd_noalloc(const void *q, const void *k, const void *v, const void *o, c
 /*
  * Synchronises `stream`, then returns and clears the device status word of
  * the current device: FA_OK, FA_ERR_TIMEOUT (a kernel's bounded wait ran out;
- * its outputs are invalid), FA_ERR_BAD_INDEX (see fa_kv_cache) or FA_ERR_CUDA
- * (the synchronise failed).
+ * its outputs are invalid), FA_ERR_BAD_INDEX (see fa_kv_cache; where both
+ * happened, FA_ERR_TIMEOUT) or FA_ERR_CUDA (the synchronise failed).
  */
 int fa_sync_status(fa_stream_t stream);
 

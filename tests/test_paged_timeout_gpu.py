@@ -39,3 +39,12 @@ def test_tile_never_signalled(results, name, sites):
     assert res["launch"] == 0 and res["word"] & 0xFF == FA_ERR_TIMEOUT and (res["word"] >> 8) in sites, res
     assert res["again_launch"] == 0 and res["again_status"] == 0
     assert res["again_excess"] <= 0
+
+
+def test_timeout_beside_a_bad_length(results):
+    """A length out of range is reported first, and its sequence alone is left out; the timeout, after which
+    no output of the call is valid, is what the caller has to hear of."""
+    res = results["beside_a_bad_length"]
+    assert res["launch"] == 0 and res["status"] == FA_ERR_TIMEOUT
+    assert res["again_launch"] == 0 and res["again_status"] == 0
+    assert res["again_excess"] <= 0
