@@ -2,6 +2,7 @@
 // validation, TMA descriptor encoding, kernel dispatch and the device status
 // word.  No compute happens here; every step of the path runs in the kernels
 // of fa_fwd_sm103.cu, fa_fwd_f32.cu and fa_bwd_sm103.cu.
+#include <atomic>
 #include <climits>
 #include <cmath>
 #include <cstdlib>
@@ -163,6 +164,28 @@ int fill_empty_launch(void *o, float *lse, size_t rows, int d, int elem_bytes, c
     const int grid = device_sm_count() * 4;
     fill_empty_kernel<<<grid, 256, 0, s>>>(static_cast<uint8_t *>(o), lse, rows, d * elem_bytes);
     return cudaGetLastError() == cudaSuccess ? OK : ERR_CUDA;
+}
+
+// ------------------------------------------------------------ status words in use
+namespace {
+std::atomic<unsigned> g_status_in_use{0};   // a bit a StatusWords
+#if FA_TEST_WITHHOLD
+std::atomic<int> g_status_reads{0};         // of the cache kernels' words
+#endif
+bool status_is_in_use(StatusWords w)
+{
+    const bool in_use = g_status_in_use.load(std::memory_order_relaxed) >> w & 1u;
+#if FA_TEST_WITHHOLD
+    g_status_reads += in_use;
+#endif
+    return in_use;
+}
+}  // namespace
+
+void status_in_use(StatusWords w)
+{
+    if (!(g_status_in_use.load(std::memory_order_relaxed) >> w & 1u))
+        g_status_in_use.fetch_or(1u << w, std::memory_order_relaxed);
 }
 
 // ------------------------------------------------------------ validation
@@ -576,8 +599,11 @@ static int fetch_status(cudaStream_t s, int *word)
 {
     int w[5] = {0, 0, 0, 0, 0};
     if (fa::fwd_status_fetch_clear(s, &w[0]) != fa::OK || fa::bwd_status_fetch_clear(s, &w[1]) != fa::OK ||
-        fa::dec_status_fetch_clear(s, &w[2]) != fa::OK || fa::paged_status_fetch_clear(s, &w[3]) != fa::OK ||
-        fa::cache_status_fetch_clear(s, &w[4]) != fa::OK)
+        fa::dec_status_fetch_clear(s, &w[2]) != fa::OK)
+        return fa::ERR_CUDA;
+    if (fa::status_is_in_use(fa::STATUS_PAGED) && fa::paged_status_fetch_clear(s, &w[3]) != fa::OK)
+        return fa::ERR_CUDA;
+    if (fa::status_is_in_use(fa::STATUS_CACHE) && fa::cache_status_fetch_clear(s, &w[4]) != fa::OK)
         return fa::ERR_CUDA;
     for (int i = 0; i < 5 && *word == 0; ++i)
         *word = w[i];
@@ -615,12 +641,15 @@ const char *fa_status_string(int status)
 
 #if FA_TEST_WITHHOLD
 // Test-only exports (absent from the product library): arm one withheld arrive for the
-// next matching launch, and read the raw status word (wait site << 8 | status).
+// next matching launch, count the reads of the cache kernels' status words, and read the raw status word
+// (wait site << 8 | status).
 void fa_test_withhold(int which)
 {
     std::lock_guard<std::mutex> lock(fa::g_withhold_mu);
     fa::g_withhold = which;
 }
+
+int fa_test_status_reads(void) { return fa::g_status_reads; }
 
 int fa_test_status_word(fa_stream_t stream)
 {

@@ -980,6 +980,7 @@ int append_launch(const fa_kv_cache &c, const fa_heads &k, const fa_heads &v, co
                   const fa_heads *q_out, const int *positions, const fa_rope_spec *spec, const int *new_lens, int T,
                   cudaStream_t s)
 {
+    status_in_use(STATUS_CACHE);
     AppendArgs a;
     a.k = row3(k);
     a.v = row3(v);
@@ -1028,6 +1029,7 @@ int append_launch(const fa_kv_cache &c, const fa_heads &k, const fa_heads &v, co
 int evict_launch(const fa_kv_cache &c, int budget, int n_first, int n_recent, float *weight_out, int *order_out,
                  int *lens_out, int *kept, cudaStream_t s)
 {
+    status_in_use(STATUS_CACHE);
     EvictArgs a;
     a.weight = c.weight;
     a.order = c.order;
@@ -1089,8 +1091,11 @@ int cache_status_fetch_clear(cudaStream_t s, int *host_word)
 {
     int zero = 0;
     if (cudaMemcpyFromSymbolAsync(host_word, g_cache_status, sizeof(int), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
-        cudaMemcpyToSymbolAsync(g_cache_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s) != cudaSuccess ||
         cudaStreamSynchronize(s) != cudaSuccess)
+        return ERR_CUDA;
+    if (*host_word != 0 &&
+        (cudaMemcpyToSymbolAsync(g_cache_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s) != cudaSuccess ||
+         cudaStreamSynchronize(s) != cudaSuccess))
         return ERR_CUDA;
     return OK;
 }

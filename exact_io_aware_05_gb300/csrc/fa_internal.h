@@ -162,4 +162,9 @@ int paged_launch(const fa_kv_cache &c, const void *q, void *o, float *lse, int H
 int cache_status_fetch_clear(cudaStream_t s, int *host_word);
 int paged_status_fetch_clear(cudaStream_t s, int *host_word);
 
+// The status words of the cache kernels are read from the first launch of one of them in this process
+// on (a captured one may run again at any time): fa_sync_status of a program that has no cache costs no more for them.
+enum StatusWords : int { STATUS_CACHE = 0, STATUS_PAGED = 1 };
+void status_in_use(StatusWords w);
+
 }  // namespace fa

@@ -49,9 +49,9 @@
 
 namespace fa {
 
-// Device status words of the kernels in this file: a wait that ran out, and an index out of range.  Two, because
+// Device status words of the kernels in this file: [0] a wait that ran out, [1] an index out of range.  Two, because
 // indexes are checked first, and a timeout, after which nothing of the call is valid, must not be lost to one.
-__device__ int g_paged_status, g_paged_index;
+__device__ int g_paged_status[2];
 
 namespace {
 
@@ -217,7 +217,7 @@ __device__ __forceinline__ float score_scale(float a, float b, float c)
 __device__ __forceinline__ int length_in_range(const PagedArgs &a, int len)
 {
     if (len < 0 || len > a.cap) {
-        atomicCAS(&g_paged_index, 0, kStatusBadIndex);
+        atomicCAS(&g_paged_status[1], 0, kStatusBadIndex);
         return 0;
     }
     return len;
@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, ROWS>::CTAS)
     volatile uint32_t *there = reinterpret_cast<volatile uint32_t *>(smem + C::OFF_OK);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_MISC);
     const int lane = (int)lane_id(), warp = (int)warp_id();
-    const WaitCtx ctx{abort_flag, &g_paged_status, a.timeout_ns};
+    const WaitCtx ctx{abort_flag, &g_paged_status[0], a.timeout_ns};
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::NST; ++s) {
             mbar_init(bar0 + 8u * s, 1);
@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, ROWS>::CTAS)
                 }
                 const bool inside = mine && slot < len, good = inside && page >= 0 && page < a.num_pages;
                 if (inside && !good)
-                    atomicCAS(&g_paged_index, 0, kStatusBadIndex);
+                    atomicCAS(&g_paged_status[1], 0, kStatusBadIndex);
                 // groups of 16 entries whose page is there and that begin in front of the length
                 uint32_t groups = 0;
                 if (good && !(lane & 1))
@@ -1381,6 +1381,7 @@ size_t paged_workspace_bytes(int B, int Hq, int Hkv, int Tq, int max_len, int d,
 int paged_launch(const fa_kv_cache &c, const void *q, void *o, float *lse, int Hq, int Tq, int causal, float scale,
                  int accumulate, void *workspace, cudaStream_t s)
 {
+    status_in_use(STATUS_PAGED);
     PagedArgs a;
     a.q = static_cast<const __nv_bfloat16 *>(q);
     a.o = static_cast<__nv_bfloat16 *>(o);
@@ -1424,15 +1425,16 @@ int paged_launch(const fa_kv_cache &c, const void *q, void *o, float *lse, int H
 
 int paged_status_fetch_clear(cudaStream_t s, int *host_word)
 {
-    int zero = 0, index = 0;
-    if (cudaMemcpyFromSymbolAsync(host_word, g_paged_status, sizeof(int), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
-        cudaMemcpyToSymbolAsync(g_paged_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s) != cudaSuccess ||
-        cudaMemcpyFromSymbolAsync(&index, g_paged_index, sizeof(int), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
-        cudaMemcpyToSymbolAsync(g_paged_index, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s) != cudaSuccess ||
+    int word[2] = {0, 0};
+    if (cudaMemcpyFromSymbolAsync(word, g_paged_status, sizeof(word), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
         cudaStreamSynchronize(s) != cudaSuccess)
         return ERR_CUDA;
-    if (*host_word == 0)
-        *host_word = index;
+    *host_word = word[0] ? word[0] : word[1];
+    const int zero[2] = {0, 0};
+    if (*host_word != 0 &&
+        (cudaMemcpyToSymbolAsync(g_paged_status, zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s) != cudaSuccess ||
+         cudaStreamSynchronize(s) != cudaSuccess))
+        return ERR_CUDA;
     return OK;
 }
 

@@ -36,7 +36,8 @@ def main():
     lib.fa_test_withhold.argtypes = [ctypes.c_int]
     lib.fa_test_status_word.argtypes = [ctypes.c_void_p]
     stream = torch.cuda.current_stream().cuda_stream
-    out = {}
+    assert lib.fa_sync_status(stream) == 0
+    out = {"reads_before_any_cache_call": lib.fa_test_status_reads()}
     for name, (lens, Hq, fp8, bad) in CASES.items():
         cache = make_cache(fa, 5, lens, 2, 128, 16, fp8)
         q = randn(gen(6), len(lens), Hq, 1, 128)
@@ -68,6 +69,9 @@ def main():
                          float((np.abs(to64(lse[b]) - rl) - tl).max()))
         res["again_excess"] = excess
         out[name] = res
+    n = lib.fa_test_status_reads()
+    assert lib.fa_sync_status(stream) == 0
+    out["reads_after_decodes"] = lib.fa_test_status_reads() - n
     print(json.dumps(out))
 
 

@@ -48,3 +48,9 @@ def test_timeout_beside_a_bad_length(results):
     assert res["launch"] == 0 and res["status"] == FA_ERR_TIMEOUT
     assert res["again_launch"] == 0 and res["again_status"] == 0
     assert res["again_excess"] <= 0
+
+
+def test_status_words_are_read_once_they_are_in_use(results):
+    """fa_sync_status reads the words of the cache kernels only after one of them was launched."""
+    assert results["reads_before_any_cache_call"] == 0
+    assert results["reads_after_decodes"] == 1      # the paged decode's, not append's and evict's
