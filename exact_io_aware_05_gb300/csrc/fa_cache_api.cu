@@ -10,7 +10,9 @@
 
 namespace {
 
-constexpr long long kMaxSlots = 1ll << 30;   // of a sequence: slot numbers past the end of a tile fit an int
+// Slots of a sequence, and the budget of an eviction: slot numbers past the end of a tile, and a loop's step
+// past the budget, fit an int.
+constexpr long long kMaxSlots = 1ll << 30;
 
 bool width_ok(int d) { return d == 64 || d == 128 || d == 256; }
 
@@ -355,7 +357,7 @@ int fa_cache_evict(const fa_kv_cache *cache, int budget, int n_first, int n_rece
     int st = cache_check(cache);
     if (st != FA_OK)
         return st;
-    if (budget < 1 || n_first < 0 || n_recent < 0 || (long long)n_first + n_recent > budget)
+    if (budget < 1 || budget > kMaxSlots || n_first < 0 || n_recent < 0 || (long long)n_first + n_recent > budget)
         return FA_ERR_INVALID_ARG;
     const int B = cache->B;
     if (B == 0)

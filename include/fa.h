@@ -311,7 +311,7 @@ int fa_decode_paged(const fa_kv_cache *cache, const void *q, void *o, float *lse
                     float scale, int accumulate, void *workspace, size_t workspace_bytes, fa_stream_t stream);
 
 /*
- * Evicts, for every sequence and KV head on its own, down to `budget` (>= 1)
+ * Evicts, for every sequence and KV head on its own, down to `budget` (1 to 2^30)
  * entries.  Kept are the min(lens, budget) first ones in this order: protected
  * entries (arrival number below n_first, or at least seen - n_recent), then by
  * larger weight, a NaN counting as the least; of equals the lower slot.  The
