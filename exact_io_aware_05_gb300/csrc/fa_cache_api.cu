@@ -15,6 +15,7 @@ namespace {
 constexpr long long kMaxSlots = 1ll << 30;
 
 bool width_ok(int d) { return d == 64 || d == 128 || d == 256; }
+bool page_size_ok(int ps) { return ps == 16 || ps == 32 || ps == 64 || ps == 128 || ps == 256; }
 
 // A strided [B][H][T][d] tensor: present, 16-byte aligned rows, strides in range.
 bool heads_ok(const fa_heads *x, int elem)
@@ -87,7 +88,7 @@ int cache_check(const fa_kv_cache *c)
     if (!width_ok(c->d))
         return FA_ERR_UNSUPPORTED;
     const int ps = c->page_size;
-    if (ps != 16 && ps != 32 && ps != 64 && ps != 128 && ps != 256)
+    if (!page_size_ok(ps))
         return FA_ERR_UNSUPPORTED;
     if ((long long)c->num_pages * c->Hkv > INT_MAX || (long long)c->B * c->Hkv > INT_MAX ||
         (long long)c->max_pages * ps > kMaxSlots)
@@ -292,12 +293,12 @@ int fa_cache_append(const fa_kv_cache *cache, const fa_heads *k, const fa_heads 
 // Sizes of a paged decode: 0 for what fa_decode_paged refuses.
 static bool paged_sizes_ok(int B, int Hq, int Hkv, int Tq, int max_pages, int page_size, int d)
 {
-    if (B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Tq < 1 || Tq > 16 || max_pages < 0 || page_size < 1)
+    if (B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Tq < 1 || Tq > 16 || max_pages < 0 || !page_size_ok(page_size))
         return false;
     if (!width_ok(d) || (long long)max_pages * page_size > kMaxSlots)
         return false;
     // row indexes of q, and units of (sequence, KV head, 64 rows of a head group), in 31 bits
-    return (long long)B * Hq * Tq <= INT_MAX;
+    return (long long)B * Hq <= INT_MAX / Tq;
 }
 
 size_t fa_decode_paged_workspace_bytes(int B, int Hq, int Hkv, int Tq, int max_pages, int page_size, int d,

@@ -30,3 +30,24 @@ def test_evict_budgets(fa):
     assert evict(fa, 1 << 30) in NO_GPU
     for budget in ((1 << 30) + 1, 2 ** 31 - 1):
         assert evict(fa, budget) == INVALID
+
+
+def test_workspace_sizes_of_refused_calls(fa):
+    """0 for every size that fa_decode_paged refuses: page sizes, and products beyond 31 and 63 bits."""
+    size = fa.lib().fa_decode_paged_workspace_bytes
+    for ps in (16, 32, 64, 128, 256):
+        assert size(2, 4, 2, 1, 4, ps, 64, 0) > 0
+    for ps in (1, 8, 17, 48, 512):
+        assert size(2, 4, 2, 1, 4, ps, 64, 0) == 0
+        c = cache(fa, page_size=ps)
+        assert fa.lib().fa_decode_paged(ctypes.byref(c), P + 8 * MB, P + 9 * MB, P + 10 * MB, 4, 1, 1, 0.1, 0, P + 16 * MB,
+                                        64 * MB, None) == UNSUPPORTED
+    assert size(1 << 30, 1 << 30, 1, 16, 4, 16, 64, 0) == 0      # 2^64 rows
+    assert size(1 << 30, 1 << 29, 1, 16, 4, 16, 64, 1) == 0      # 2^63
+    assert size(1 << 27, 1, 1, 16, 4, 16, 64, 0) == 0            # 2^31
+
+
+def test_binding_workspace_of_a_refused_page_size(fa):
+    z = torch.zeros((4, 2, 48, 64), dtype=torch.bfloat16)
+    c = fa.KVCache(z, z.clone(), torch.zeros((2, 3), dtype=torch.int32), torch.zeros(2, dtype=torch.int32))
+    assert fa.fa_decode_paged_workspace_bytes(c, 4) == 0
