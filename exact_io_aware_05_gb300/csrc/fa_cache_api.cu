@@ -323,7 +323,7 @@ int fa_decode_paged(const fa_kv_cache *cache, const void *q, void *o, float *lse
     const int B = cache->B, d = cache->d;
     if (!paged_sizes_ok(B, Hq, cache->Hkv, Tq, cache->max_pages, cache->page_size, d))
         return FA_ERR_INVALID_ARG;
-    if (accumulate && !cache->weight)
+    if (accumulate && !cache->weight && slots_bytes(cache) > 0)
         return FA_ERR_INVALID_ARG;
     if (B == 0)
         return FA_OK;
@@ -363,16 +363,19 @@ int fa_cache_evict(const fa_kv_cache *cache, int budget, int n_first, int n_rece
     const int B = cache->B;
     if (B == 0)
         return FA_OK;
-    if (!cache->weight || ((n_first > 0 || n_recent > 0) && !cache->order) || (order_out != nullptr) != (cache->order != nullptr))
+    const size_t ns = slots_bytes(cache);
+    // without a slot the arrays have no element, and no address need be given
+    if (ns > 0 && (!cache->weight || !weight_out || ((n_first > 0 || n_recent > 0) && !cache->order) ||
+                   (order_out != nullptr) != (cache->order != nullptr)))
         return FA_ERR_INVALID_ARG;
-    if (!weight_out || !lens_out || !kept)
+    if (!lens_out || !kept)
         return FA_ERR_INVALID_ARG;
     if (!fa::aligned16(weight_out) || !fa::aligned16(order_out) || !fa::aligned16(kept) ||
         (reinterpret_cast<uintptr_t>(lens_out) & 3u))
         return FA_ERR_INVALID_ARG;
     if (!cache_disjoint(cache))
         return FA_ERR_INVALID_ARG;
-    const size_t ns = slots_bytes(cache), nb = (size_t)B * 4, nk = (size_t)B * cache->Hkv * budget * 4;
+    const size_t nb = (size_t)B * 4, nk = (size_t)B * cache->Hkv * budget * 4;
     const void *outs[4] = {weight_out, order_out, lens_out, kept};
     const size_t out_n[4] = {ns, ns, nb, nk};
     const void *same[4] = {cache->weight, cache->order, cache->lens, nullptr};

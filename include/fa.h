@@ -244,7 +244,8 @@ int fa_rope(const fa_heads *x, const fa_heads *y, int n, const int *positions, c
  *                weight of each entry, or NULL
  *   order        [B][Hkv][max_pages * page_size] int32: arrival number of each
  *                entry (the first token of a sequence has 0), or NULL
- * k and v are 128-byte, weight and order 16-byte, the other arrays 4-byte aligned.
+ * k and v are 128-byte, weight and order 16-byte, the other arrays 4-byte aligned;
+ * an array without an element may be NULL.
  * page_size is 16, 32, 64, 128 or 256; d 64, 128 or 256.  Only the pages and
  * rows in front of lens are read: what lies behind them may hold anything.
  * Sequences may share pages that none of them writes to (fa_cache_append and

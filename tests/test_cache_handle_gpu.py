@@ -43,3 +43,17 @@ def test_assigned_tensors_are_read_and_written(fa):
     check_decode(fa, cache, 4, 1, accumulate=True)
     for n, t in old.items():
         assert torch.equal(t.view(torch.uint8), marks[n].view(torch.uint8)), n
+
+
+def test_empty_caches_with_weights(fa):
+    """No sequences, and sequences without a slot: nothing to attend to, to add up or to evict."""
+    for B, pages in ((0, 3), (2, 0)):
+        cache = fa.alloc_kv_cache(B, 2, 64, 16 * pages, 16, weight=True)
+        q = torch.ones((B, 4, 1, 64), device=DEV, dtype=BF16)
+        o, lse = fa.attention_decode_paged(cache, q, 0.1, accumulate=True)
+        kept = fa.fa_cache_evict(cache, 5, n_first=1, n_recent=2)
+        assert fa.fa_sync_status() == fa.FA_OK
+        assert torch.all(o == 0) and torch.all(torch.isneginf(lse)) and torch.all(kept == -1) and cache.lens.tolist() == [0] * B
+        no = torch.zeros((B, 2, 0, 64), device=DEV, dtype=BF16)
+        fa.fa_cache_append(cache, no, no)
+        assert fa.fa_sync_status() == fa.FA_OK

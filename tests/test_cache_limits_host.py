@@ -51,3 +51,35 @@ def test_binding_workspace_of_a_refused_page_size(fa):
     z = torch.zeros((4, 2, 48, 64), dtype=torch.bfloat16)
     c = fa.KVCache(z, z.clone(), torch.zeros((2, 3), dtype=torch.int32), torch.zeros(2, dtype=torch.int32))
     assert fa.fa_decode_paged_workspace_bytes(c, 4) == 0
+
+
+def test_empty_caches_are_empty_calls(fa):
+    """No sequences, or no slots: arrays without an element have no address (torch gives 0), and the calls are
+    those of a cache that has some, with nothing to do."""
+    lib = fa.lib()
+
+    def decode(acc, **kw):
+        c = cache(fa, **kw)
+        return lib.fa_decode_paged(ctypes.byref(c), P + 8 * MB, P + 9 * MB, P + 10 * MB, 4, 1, 1, 0.1, acc, P + 16 * MB, 64 * MB, None)
+
+    for acc in (0, 1):
+        assert decode(acc, B=0, weight=None, order=None, lens=None, block_table=None) == 0
+        assert decode(acc, max_pages=0, weight=None, order=None, block_table=None) in NO_GPU
+    assert decode(1, weight=None) == INVALID                                  # slots without weights
+
+    def evict(w, o, n_recent=2, **kw):
+        c = cache(fa, **kw)
+        return lib.fa_cache_evict(ctypes.byref(c), 8, 1, n_recent, w, o, P + 10 * MB, P + 11 * MB, None)
+
+    assert evict(None, None, B=0, weight=None, order=None, lens=None, block_table=None) == 0
+    assert evict(None, None, max_pages=0, weight=None, order=None, block_table=None) in NO_GPU
+    assert evict(P + 8 * MB, None, order=None) == INVALID                     # slots, and recent without an order
+    assert evict(None, P + 9 * MB) == INVALID
+
+
+def test_binding_of_empty_caches(fa):
+    """The same through the handle: weights and an order of no element are there."""
+    for B, pages in ((0, 3), (2, 0)):
+        c = fa.alloc_kv_cache(B, 2, 64, 16 * pages, 16, weight=True, device="cpu")
+        assert c.weight.numel() == 0 and c.order.numel() == 0
+        assert fa.fa_decode_paged_workspace_bytes(c, 4, accumulate=True) > 0
