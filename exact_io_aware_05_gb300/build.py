@@ -3,8 +3,9 @@
 Each translation unit compiles in parallel into ``_build/`` and links into
 ``exact_io_aware_05_gb300/libfa.so`` with the static CUDA runtime.  No torch
 types or headers are involved: the library is a plain C ABI (include/fa.h).
-The host compiler also builds ``_fa_py.so``, a CPython module with the binding's
-argument checks for the rotary and cache calls (csrc/fa_py.c).
+The host compiler also builds ``_fa_py``, a CPython module with the binding's
+argument checks for the rotary and cache calls (csrc/fa_py.c), under the running
+interpreter's file name.
 
 With ``test_variant=True`` the same pool also compiles the API, the two
 tile-loop units and the paged decode with ``FA_TEST_WITHHOLD=1`` into ``_build/waittest/`` and links
@@ -27,7 +28,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 SO = os.path.join(PKG, "libfa.so")
 TEST_SO = os.path.join(PKG, "libfa_waittest.so")
-PY_SO = os.path.join(PKG, "_fa_py.so")     # CPython module: the cache calls' argument marshalling
+# CPython module: the cache calls' argument marshalling.  It uses the C API of one version of Python
+PY_SO = os.path.join(PKG, "_fa_py" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 SOURCES = ["fa_api.cu", "fa_fwd_sm103.cu", "fa_fwd_f32.cu", "fa_bwd_sm103.cu", "fa_bwd_noalloc.cu",
            "fa_decode_sm103.cu", "fa_fp8_sm103.cu", "fa_cache_api.cu", "fa_cache_sm103.cu",
            "fa_paged_sm103.cu"]
@@ -58,6 +60,9 @@ def up_to_date(so: str = SO) -> bool:
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False, test_variant: bool = False) -> str:
     """Builds libfa.so (and, with test_variant, libfa_waittest.so) unless up to date."""
+    untagged = os.path.join(PKG, "_fa_py.so")   # a name that every Python would load
+    if untagged != PY_SO and os.path.exists(untagged):
+        os.remove(untagged)
     if not force and up_to_date() and up_to_date(PY_SO) and (not test_variant or up_to_date(TEST_SO)):
         return SO
     os.makedirs(os.path.join(BUILD, "waittest"), exist_ok=True)
