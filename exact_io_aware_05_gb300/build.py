@@ -5,7 +5,8 @@ Each translation unit compiles in parallel into ``_build/`` and links into
 types or headers are involved: the library is a plain C ABI (include/fa.h).
 The host compiler also builds ``_fa_py``, a CPython module with the binding's
 argument checks for the rotary and cache calls (csrc/fa_py.c), under the running
-interpreter's file name.
+interpreter's file name; without Python's headers it is left out, and those calls go
+through ctypes.
 
 With ``test_variant=True`` the same pool also compiles the API, the two
 tile-loop units and the paged decode with ``FA_TEST_WITHHOLD=1`` into ``_build/waittest/`` and links
@@ -58,12 +59,16 @@ def up_to_date(so: str = SO) -> bool:
     return all(os.path.getmtime(f) <= t for f in _deps())
 
 
+def _has_python_headers() -> bool:
+    return os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h"))
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False, test_variant: bool = False) -> str:
     """Builds libfa.so (and, with test_variant, libfa_waittest.so) unless up to date."""
     untagged = os.path.join(PKG, "_fa_py.so")   # a name that every Python would load
     if untagged != PY_SO and os.path.exists(untagged):
         os.remove(untagged)
-    if not force and up_to_date() and up_to_date(PY_SO) and (not test_variant or up_to_date(TEST_SO)):
+    if not force and up_to_date() and (up_to_date(PY_SO) or not _has_python_headers()) and (not test_variant or up_to_date(TEST_SO)):
         return SO
     os.makedirs(os.path.join(BUILD, "waittest"), exist_ok=True)
     cc = nvcc()
@@ -73,6 +78,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False, 
         flags += ["-Xptxas", "-v"]
 
     def compile_py() -> None:
+        if not _has_python_headers():
+            return
         tmp = PY_SO + f".tmp{os.getpid()}"
         cmd = [os.environ.get("CC") or shutil.which("gcc") or "cc", "-O2", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"],
                os.path.join(CSRC, "fa_py.c"), "-o", tmp]

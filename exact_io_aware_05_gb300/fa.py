@@ -5,8 +5,9 @@ reads the current CUDA stream, and calls the C entry point of the same name
 with raw device pointers, through ctypes.  The rotary and cache calls, which
 take a few microseconds on the device, are checked and made by the CPython
 module _fa_py (csrc/fa_py.c); where a check of its does not pass, the checks
-here say why.  No attention arithmetic happens in Python and there is no
-fallback: importing this module fails if libfa.so or _fa_py.so is missing, and
+here say why, and where it was not built for the running interpreter, they and
+ctypes make the call, 3 to 4 us slower.  No attention arithmetic happens in Python and
+there is no fallback: importing this module fails if libfa.so is missing, and
 every nonzero status raises ``FAError``.
 """
 from __future__ import annotations
@@ -26,9 +27,8 @@ if not os.path.exists(LIB_PATH):
 
 try:
     from . import _fa_py
-except ImportError as e:
-    raise ImportError("_fa_py.so is not built for this Python; run exact_io_aware_05_gb300.build.build() "
-                      "(or __graft_entry__.build()) first") from e
+except ImportError:
+    _fa_py = None
 
 _lib = ctypes.CDLL(LIB_PATH)
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
@@ -469,9 +469,20 @@ def rope_spec(d: int, sections=None, base: float = 10000.0, rot: int | None = No
 
 _current_stream = torch._C._cuda_getCurrentRawStream    # of a device index; torch.cuda's builds an object
 _current_device = torch._C._cuda_getDevice
-_fa_py.setup(torch.bfloat16, torch.float32, torch.int32, _current_stream, _current_device,
-             *(ctypes.cast(f, _vp).value for f in (_lib.fa_rope, _lib.fa_cache_append, _lib.fa_decode_paged,
-                                                   _lib.fa_cache_evict)))
+
+
+class _Without:
+    """Stands for _fa_py where it is missing: no call passes its checks."""
+    rope = append = decode = evict = staticmethod(lambda *args: None)
+
+
+if _fa_py is None:
+    _fast = _Without
+else:
+    _fast = _fa_py
+    _fa_py.setup(torch.bfloat16, torch.float32, torch.int32, _current_stream, _current_device,
+                 *(ctypes.cast(f, _vp).value for f in (_lib.fa_rope, _lib.fa_cache_append, _lib.fa_decode_paged,
+                                                       _lib.fa_cache_evict)))
 
 
 def _launch(fn: str, entry, index: int, stream, *args) -> None:
@@ -564,7 +575,7 @@ def fa_rope(q, q_out, positions, spec: RopeSpec, k=None, k_out=None, stream=None
     """q_out = q [B, Hq, T, d] (and k_out = k [B, Hk, T, d]) with their pairs turned by the
     positions, int32 [n_axes, B, T].  bf16 or float32; strided views with contiguous rows are
     taken as they are; an output may be its input."""
-    st = _fa_py.rope(spec._ref, q, q_out, k, k_out, positions, 0, stream)
+    st = _fast.rope(spec._ref, q, q_out, k, k_out, positions, 0, stream)
     if st != FA_OK:
         _again(st, "fa_rope", _rope, "fa_rope", q, q_out, positions, spec, k, k_out, 0, stream)
 
@@ -572,7 +583,7 @@ def fa_rope(q, q_out, positions, spec: RopeSpec, k=None, k_out=None, stream=None
 def fa_rope_bwd(dq_out, dq, positions, spec: RopeSpec, k=None, k_out=None, stream=None) -> None:
     """Backward of fa_rope: dq, the gradient of q, from dq_out, the gradient of q_out (and
     k_out from k, the gradients of k and of the rotated k)."""
-    st = _fa_py.rope(spec._ref, dq_out, dq, k, k_out, positions, 1, stream)
+    st = _fast.rope(spec._ref, dq_out, dq, k, k_out, positions, 1, stream)
     if st != FA_OK:
         _again(st, "fa_rope_bwd", _rope, "fa_rope_bwd", dq_out, dq, positions, spec, k, k_out, 1, stream)
 
@@ -672,7 +683,7 @@ def fa_cache_append(cache: KVCache, k, v, positions=None, spec: RopeSpec | None 
     """Writes the first new_lens[b] (default: all) of the T rows of k and v [B, Hkv, T, d] as the
     last entries of sequence b; cache.lens (and seen) count them already.  With a spec, k is
     rotated by positions [n_axes, B, T] on the way, and q [B, Hq, T, d] into q_out."""
-    st = _fa_py.append(cache._ref, cache._index, k, v, positions, None if spec is None else spec._ref, q, q_out, new_lens,
+    st = _fast.append(cache._ref, cache._index, k, v, positions, None if spec is None else spec._ref, q, q_out, new_lens,
                        stream)
     if st != FA_OK:
         _again(st, "fa_cache_append", _append, cache, k, v, positions, spec, q, q_out, new_lens, stream)
@@ -718,7 +729,7 @@ def fa_decode_paged(cache: KVCache, q, o, lse, scale: float, workspace: torch.Te
                     accumulate: bool = False, stream=None) -> None:
     """O and lse of q [B, Hq, Tq, d] (the last Tq tokens of every sequence) over the cache; with
     `accumulate`, cache.weight grows by each entry's attention probabilities."""
-    st = _fa_py.decode(cache._ref, cache._index, q, o, lse, scale, workspace, causal, accumulate, stream)
+    st = _fast.decode(cache._ref, cache._index, q, o, lse, scale, workspace, causal, accumulate, stream)
     if st != FA_OK:
         _again(st, "fa_decode_paged", _decode, cache, q, o, lse, scale, workspace, causal, accumulate, stream)
 
@@ -771,7 +782,7 @@ def fa_cache_evict(cache: KVCache, budget: int, weight_out=None, order_out=None,
     lens_out = cache.lens if lens_out is None else lens_out
     if kept is None:
         kept, = _empties(stream, cache.device, ((cache.B, cache.Hkv, max(int(budget), 0)), torch.int32))
-    st = _fa_py.evict(cache._ref, cache._index, budget, weight_out, order_out, lens_out, kept, n_first, n_recent, stream)
+    st = _fast.evict(cache._ref, cache._index, budget, weight_out, order_out, lens_out, kept, n_first, n_recent, stream)
     if st != FA_OK:
         _again(st, "fa_cache_evict", _evict, cache, budget, weight_out, order_out, lens_out, kept, n_first, n_recent, stream)
     return kept
