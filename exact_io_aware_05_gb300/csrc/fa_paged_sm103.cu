@@ -24,18 +24,18 @@
 //     The tensor cores of the fifth generation want 128 rows a product: with up to 16 rows, the usual
 //     case, they would run nearly empty, and their accumulators would have to come back for the
 //     softmax, where the warp-level products leave S in the registers that P V takes.  At 64 rows
-//     the bound are the math warps, two a scheduler, with the product pipe 40 % busy (see below).
+//     the bound are the math warps, two a scheduler, with the product pipe 46 % busy (see below).
 //   * P enters its product as two bf16 numbers (its leading 8 bits and the rest), so its error is
 //     2^-17 and not 2^-9, which would be as large as the output's own rounding.  e4m3 codes become
 //     f16 exactly; there P is scaled by 2^15, which keeps probabilities down to 2^-29 in f16's normal
 //     range, with 11 bits, and a row of q by the power of two that puts its largest value next to
 //     f16's end: bf16's 8 bits are exact down to 2^-31 of that value.
 //
-// Measured: 8 sequences of 32768 entries, 32 KV heads, d 128 (4.3 GB) 594 us, 7.2 TB/s; 64 sequences of 200 to
+// Measured: 8 sequences of 32768 entries, 32 KV heads, d 128 (4.3 GB) 598 us, 7.2 TB/s; 64 sequences of 200 to
 // 8000, 8 KV heads (1.1 GB) 164 us, 6.6 TB/s; 17 entries of one sequence 3.7 us.  Of the second, 3 us pass
 // before the first load, 3 to 4 with the join, and the CTAs end within 10 % of one another, with the
-// issue slots a fifth busy.  By rows (160 units of 2048 to 4096, d 128): 45, 47, 51, 61 and 103 us
-// with 4, 8, 16, 32 and 64; e4m3, twice as long: 46, 47, 54, 96 and 162, its codes being converted by
+// issue slots a fifth busy.  By rows (160 units of 2048 to 4096, d 128): 46, 47, 52, 62 and 103 us
+// with 4, 8, 16, 32 and 64; e4m3, twice as long: 48, 50, 55, 87 and 159, its codes being converted by
 // every row tile.
 #include <algorithm>
 #include <cfloat>
