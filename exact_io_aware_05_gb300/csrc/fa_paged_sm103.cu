@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, ROWS>::CTAS)
                     // does): what a bf16 value of 2^-31 of it or more holds stays whole, below that a multiple of
                     // 2^-38 of it; sums of d products with codes stay below 2^15 448 d < 2^32.  Zeros and
                     // infinities stay
-                    const int x = (int)(__float_as_uint(big) >> 23), de = x == 255 || x == 0 ? 127 : min(268 - x, 254);
+                    const int x = (int)(__float_as_uint(big) >> 23), de = x == 255 || big == 0.f ? 127 : min(268 - x, 254);
                     const float down = __uint_as_float((uint32_t)de << 23);
                     scale = score_scale(scale, qks, 1.f / down);
 #pragma unroll

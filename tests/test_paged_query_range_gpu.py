@@ -82,3 +82,13 @@ def test_zero_scores_of_the_largest_scales(fa, rows, fp8):
     check(fa, cache, q, 3.0e38, 1)
     q.zero_()
     check(fa, cache, q, 1e-44, 1)
+
+
+@pytest.mark.parametrize("rows", [1, 16, 40])
+def test_subnormal_queries_count(fa, rows):
+    """Queries below bf16's normal range under a softmax scale that makes scores of a few units of them."""
+    cache = make_cache(fa, 99, [37, 100, 5], 1, 64, 16, fp8=True, weight=True)
+    cache.k_scale.fill_(1.0)
+    q = (randn(gen(100), 3, rows, 1, 64, dtype=F32).double() * 2.0 ** -129).to(BF16)
+    assert float(q.double().abs().max()) < 2.0 ** -126 and bool((q != 0).any())
+    check(fa, cache, q, 2.0 ** 122, 1)
