@@ -205,12 +205,13 @@ __device__ __forceinline__ float quad_max(float x)
 // The product of three positive factors, the largest and the smallest first, so that no part of it
 // leaves fp32's range where the whole does not.  What is too small becomes the smallest normal number: a
 // factor of 0 would make a NaN of a masked entry's -inf, and 2^32 times it is still nothing as a score.  In
-// the same way what is too large stays finite, for sums of 0.
+// the same way what is too large stays finite, for sums of 0.  A NaN of b, the cache's scale, stays one (the
+// minima and maxima drop it).
 __device__ __forceinline__ float score_scale(float a, float b, float c)
 {
     const float hi = fmaxf(a, b), lo = fminf(a, b);
     const float x = fmaxf(hi, c) * fminf(lo, c) * fmaxf(lo, fminf(hi, c));
-    return fminf(fmaxf(x, FLT_MIN), FLT_MAX);
+    return isnan(b) ? b : fminf(fmaxf(x, FLT_MIN), FLT_MAX);
 }
 
 // ------------------------------------------------------------------ shares

@@ -92,3 +92,14 @@ def test_subnormal_queries_count(fa, rows):
     q = (randn(gen(100), 3, rows, 1, 64, dtype=F32).double() * 2.0 ** -129).to(BF16)
     assert float(q.double().abs().max()) < 2.0 ** -126 and bool((q != 0).any())
     check(fa, cache, q, 2.0 ** 122, 1)
+
+
+def test_an_undefined_key_scale_shows(fa):
+    """A NaN among the key scales makes NaN of its head's rows, and of no others."""
+    cache = make_cache(fa, 101, [37, 100], 2, 64, 16, fp8=True)
+    q = randn(gen(102), 2, 4, 1, 64)
+    want, _ = fa.attention_decode_paged(cache, q, 0.1)
+    cache.k_scale[1] = float("nan")
+    o, lse = fa.attention_decode_paged(cache, q, 0.1)
+    assert fa.fa_sync_status() == fa.FA_OK
+    assert torch.isnan(o[:, 2:]).all() and torch.isnan(lse[:, 2:]).all() and torch.equal(o[:, :2], want[:, :2])
