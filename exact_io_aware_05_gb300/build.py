@@ -16,6 +16,7 @@ mbarrier arrive).  Nothing in the package loads it; libfa.so never contains it.
 """
 from __future__ import annotations
 
+import contextlib
 import os
 import shutil
 import subprocess
@@ -66,8 +67,9 @@ def _has_python_headers() -> bool:
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False, test_variant: bool = False) -> str:
     """Builds libfa.so (and, with test_variant, libfa_waittest.so) unless up to date."""
     untagged = os.path.join(PKG, "_fa_py.so")   # a name that every Python would load
-    if untagged != PY_SO and os.path.exists(untagged):
-        os.remove(untagged)
+    if untagged != PY_SO:
+        with contextlib.suppress(FileNotFoundError):
+            os.remove(untagged)
     if not force and up_to_date() and (up_to_date(PY_SO) or not _has_python_headers()) and (not test_variant or up_to_date(TEST_SO)):
         return SO
     os.makedirs(os.path.join(BUILD, "waittest"), exist_ok=True)

@@ -302,6 +302,8 @@ int fa_cache_append(const fa_kv_cache *cache, const fa_heads *k, const fa_heads 
  * bits, but a sequence's last bits may depend on the other lengths.
  * accumulate = 1 adds, for every entry, the sum of its probabilities over the
  * head group's rows (Hq / Hkv heads x Tq) to cache->weight.
+ * Its time and workspace, and the time of fa_cache_evict, grow with the table's
+ * max_pages * page_size and not with lens alone.
  * workspace: fa_decode_paged_workspace_bytes bytes, 256-byte aligned, contents
  * on entry ignored, not shared by calls that may overlap in time.  A sequence
  * with a length out of range counts as empty, a page out of range as masked.
