@@ -141,6 +141,69 @@ bool cache_disjoint(const fa_kv_cache *c)
            !fa::overlaps(c->order, ns, c->lens, (size_t)c->B * 4);
 }
 
+// What fa_rope and the norms with a rotation check of their tensors; the number of rows in *rows_out.
+int rope_check(const fa_heads *x, const fa_heads *y, int n, const int *positions, const fa_rope_spec *spec, int B, int T,
+               int dtype, long long *rows_out)
+{
+    if (!x || !y || n < 1 || n > 2 || B < 0 || T < 0)
+        return FA_ERR_INVALID_ARG;
+    if (dtype != FA_BF16 && dtype != FA_F32)
+        return FA_ERR_INVALID_ARG;
+    if (!spec_ok(spec))
+        return FA_ERR_INVALID_ARG;
+    const int elem = dtype == FA_F32 ? 4 : 2, d = spec->d;
+    const size_t np = (size_t)spec->n_axes * B * T * 4;
+    if ((long long)B * T > INT_MAX)
+        return FA_ERR_INVALID_ARG;
+    long long rows = 0, heads = 0;
+    for (int i = 0; i < n; ++i) {
+        if (!heads_ok(&x[i], elem) || !heads_ok(&y[i], elem) || x[i].H != y[i].H)
+            return FA_ERR_INVALID_ARG;
+        const size_t rows_i = (size_t)B * x[i].H * T;
+        if (!heads_present(&x[i], rows_i) || !heads_present(&y[i], rows_i))
+            return FA_ERR_INVALID_ARG;
+        if (rows_i > 0 && !self_disjoint(&y[i], B, T, d))
+            return FA_ERR_INVALID_ARG;
+        rows += (long long)rows_i;
+        heads += x[i].H;
+    }
+    if (heads > INT_MAX)
+        return FA_ERR_INVALID_ARG;
+    *rows_out = rows;
+    if (rows == 0)
+        return FA_OK;
+    if (!positions || (reinterpret_cast<uintptr_t>(positions) & 3u))
+        return FA_ERR_INVALID_ARG;
+    for (int i = 0; i < n; ++i) {
+        if (!contiguous(&y[i], B, T, d))
+            continue;
+        const size_t ny = (size_t)B * y[i].H * T * d * elem;
+        if (fa::overlaps(y[i].data, ny, positions, np))
+            return FA_ERR_INVALID_ARG;
+        for (int j = 0; j < n; ++j) {
+            const size_t nx = (size_t)B * x[j].H * T * d * elem;
+            if (contiguous(&x[j], B, T, d) && !(i == j && same_place(&x[j], &y[i], B, T)) &&
+                fa::overlaps(y[i].data, ny, x[j].data, nx))
+                return FA_ERR_INVALID_ARG;
+            if (j != i && contiguous(&y[j], B, T, d) && fa::overlaps(y[i].data, ny, y[j].data, nx))
+                return FA_ERR_INVALID_ARG;
+        }
+    }
+    return FA_OK;
+}
+
+bool norm_ok(const fa_head_norm *m, const fa_rope_spec *spec)
+{
+    return m && spec && m->d == spec->d && width_ok(m->d) && (m->dtype == FA_BF16 || m->dtype == FA_F32) &&
+           std::isfinite(m->eps) && m->eps > 0.0f && fa::aligned16(m->q_weight) && fa::aligned16(m->k_weight);
+}
+
+bool touches_weights(const fa_head_norm *m, const void *p, size_t n)
+{
+    const size_t nw = (size_t)m->d * (m->dtype == FA_F32 ? 4 : 2);
+    return fa::overlaps(p, n, m->q_weight, nw) || fa::overlaps(p, n, m->k_weight, nw);
+}
+
 }  // namespace
 
 extern "C" {
@@ -187,58 +250,95 @@ int fa_rope_spec_init(fa_rope_spec *spec, int d, int rot, int n_axes, const doub
 int fa_rope(const fa_heads *x, const fa_heads *y, int n, const int *positions, const fa_rope_spec *spec, int B, int T,
             int dtype, int inverse, fa_stream_t stream)
 {
-    if (!x || !y || n < 1 || n > 2 || B < 0 || T < 0 || inverse < 0 || inverse > 1)
+    if (inverse < 0 || inverse > 1)
         return FA_ERR_INVALID_ARG;
-    if (dtype != FA_BF16 && dtype != FA_F32)
-        return FA_ERR_INVALID_ARG;
-    if (!spec_ok(spec))
-        return FA_ERR_INVALID_ARG;
-    const int elem = dtype == FA_F32 ? 4 : 2, d = spec->d;
-    const size_t np = (size_t)spec->n_axes * B * T * 4;
-    if ((long long)B * T > INT_MAX)
-        return FA_ERR_INVALID_ARG;
-    long long rows = 0, heads = 0;
-    for (int i = 0; i < n; ++i) {
-        if (!heads_ok(&x[i], elem) || !heads_ok(&y[i], elem) || x[i].H != y[i].H)
-            return FA_ERR_INVALID_ARG;
-        const size_t rows_i = (size_t)B * x[i].H * T;
-        if (!heads_present(&x[i], rows_i) || !heads_present(&y[i], rows_i))
-            return FA_ERR_INVALID_ARG;
-        if (rows_i > 0 && !self_disjoint(&y[i], B, T, d))
-            return FA_ERR_INVALID_ARG;
-        rows += (long long)rows_i;
-        heads += x[i].H;
-    }
-    if (heads > INT_MAX)
-        return FA_ERR_INVALID_ARG;
-    if (rows == 0)
-        return FA_OK;
-    if (!positions || (reinterpret_cast<uintptr_t>(positions) & 3u))
-        return FA_ERR_INVALID_ARG;
-    for (int i = 0; i < n; ++i) {
-        if (!contiguous(&y[i], B, T, d))
-            continue;
-        const size_t ny = (size_t)B * y[i].H * T * d * elem;
-        if (fa::overlaps(y[i].data, ny, positions, np))
-            return FA_ERR_INVALID_ARG;
-        for (int j = 0; j < n; ++j) {
-            const size_t nx = (size_t)B * x[j].H * T * d * elem;
-            if (contiguous(&x[j], B, T, d) && !(i == j && same_place(&x[j], &y[i], B, T)) &&
-                fa::overlaps(y[i].data, ny, x[j].data, nx))
-                return FA_ERR_INVALID_ARG;
-            if (j != i && contiguous(&y[j], B, T, d) && fa::overlaps(y[i].data, ny, y[j].data, nx))
-                return FA_ERR_INVALID_ARG;
-        }
-    }
-    const int st = fa::check_device();
-    if (st != fa::OK)
+    long long rows = 0;
+    int st = rope_check(x, y, n, positions, spec, B, T, dtype, &rows);
+    if (st != FA_OK || rows == 0)
+        return st;
+    if ((st = fa::check_device()) != fa::OK)
         return st;
     return fa::rope_launch(x, y, n, positions, *spec, B, T, dtype, inverse, reinterpret_cast<cudaStream_t>(stream));
 }
 
-int fa_cache_append(const fa_kv_cache *cache, const fa_heads *k, const fa_heads *v, const fa_heads *q,
-                    const fa_heads *q_out, const int *positions, const fa_rope_spec *spec, const int *new_lens, int T,
-                    fa_stream_t stream)
+int fa_norm_rope(const fa_heads *x, const fa_heads *y, int n, const fa_head_norm *norm, const int *positions,
+                 const fa_rope_spec *spec, int B, int T, int dtype, fa_stream_t stream)
+{
+    if (!norm_ok(norm, spec))
+        return FA_ERR_INVALID_ARG;
+    long long rows = 0;
+    int st = rope_check(x, y, n, positions, spec, B, T, dtype, &rows);
+    if (st != FA_OK || rows == 0)
+        return st;
+    for (int i = 0; i < n; ++i)
+        if (touches_weights(norm, contiguous(&y[i], B, T, spec->d) ? y[i].data : nullptr,
+                            (size_t)B * y[i].H * T * spec->d * (dtype == FA_F32 ? 4 : 2)))
+            return FA_ERR_INVALID_ARG;
+    if ((st = fa::check_device()) != fa::OK)
+        return st;
+    return fa::norm_rope_launch(x, y, n, *norm, positions, *spec, B, T, dtype, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t fa_norm_rope_bwd_workspace_bytes(int d) { return width_ok(d) ? fa::norm_bwd_workspace_bytes(d) : 0; }
+
+int fa_norm_rope_bwd(const fa_heads *dy, const fa_heads *x, const fa_heads *dx, int n, const fa_head_norm *norm,
+                     const int *positions, const fa_rope_spec *spec, int B, int T, int dtype, float *dq_weight,
+                     float *dk_weight, void *workspace, size_t workspace_bytes, fa_stream_t stream)
+{
+    if (!norm_ok(norm, spec) || !x)
+        return FA_ERR_INVALID_ARG;
+    long long rows = 0;
+    int st = rope_check(dy, dx, n, positions, spec, B, T, dtype, &rows);
+    if (st != FA_OK)
+        return st;
+    const int d = spec->d, elem = dtype == FA_F32 ? 4 : 2;
+    const size_t np = (size_t)spec->n_axes * B * T * 4, nw = (size_t)d * 4, need = fa::norm_bwd_workspace_bytes(d);
+    auto bytes = [&](const fa_heads &h) { return (size_t)B * h.H * T * d * elem; };
+    for (int i = 0; i < n; ++i)
+        if (!heads_ok(&x[i], elem) || x[i].H != dy[i].H || !heads_present(&x[i], (size_t)B * x[i].H * T))
+            return FA_ERR_INVALID_ARG;
+    if ((dk_weight && n < 2) || (dq_weight && !norm->q_weight) || (dk_weight && !norm->k_weight) || !fa::aligned16(dq_weight) ||
+        !fa::aligned16(dk_weight))
+        return FA_ERR_INVALID_ARG;
+    const bool sums = dq_weight || dk_weight;
+    if (sums && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0))
+        return FA_ERR_INVALID_ARG;
+    // the gradients of x beside what is read; those of the weights and the workspace beside everything
+    for (int i = 0; i < n; ++i) {
+        if (!contiguous(&dx[i], B, T, d))
+            continue;
+        if (touches_weights(norm, dx[i].data, bytes(dx[i])))
+            return FA_ERR_INVALID_ARG;
+        for (int j = 0; j < n; ++j)
+            if (contiguous(&x[j], B, T, d) && fa::overlaps(dx[i].data, bytes(dx[i]), x[j].data, bytes(x[j])))
+                return FA_ERR_INVALID_ARG;
+    }
+    if (sums) {
+        const void *outs[3] = {dq_weight, dk_weight, workspace};
+        const size_t out_n[3] = {dq_weight ? nw : 0, dk_weight ? nw : 0, need};
+        for (int i = 0; i < 3; ++i) {
+            if (touches_weights(norm, outs[i], out_n[i]) || fa::overlaps(outs[i], out_n[i], positions, np))
+                return FA_ERR_INVALID_ARG;
+            for (int j = 0; j < n; ++j)
+                for (const fa_heads *h : {&x[j], &dy[j], &dx[j]})
+                    if (contiguous(h, B, T, d) && fa::overlaps(outs[i], out_n[i], h->data, bytes(*h)))
+                        return FA_ERR_INVALID_ARG;
+            for (int j = i + 1; j < 3; ++j)
+                if (fa::overlaps(outs[i], out_n[i], outs[j], out_n[j]))
+                    return FA_ERR_INVALID_ARG;
+        }
+    }
+    if (rows == 0 && !sums)
+        return FA_OK;
+    if ((st = fa::check_device()) != fa::OK)
+        return st;
+    return fa::norm_rope_bwd_launch(x, dy, dx, n, *norm, positions, *spec, B, rows == 0 ? 0 : T, dtype, dq_weight, dk_weight,
+                                    workspace, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int fa_cache_append_norm(const fa_kv_cache *cache, const fa_heads *k, const fa_heads *v, const fa_heads *q,
+                         const fa_heads *q_out, const int *positions, const fa_rope_spec *spec, const fa_head_norm *norm,
+                         const int *new_lens, int T, fa_stream_t stream)
 {
     int st = cache_check(cache);
     if (st != FA_OK)
@@ -249,7 +349,7 @@ int fa_cache_append(const fa_kv_cache *cache, const fa_heads *k, const fa_heads 
         return FA_ERR_INVALID_ARG;
     if (spec ? (!spec_ok(spec) || spec->d != d) : (positions || q || q_out))
         return FA_ERR_INVALID_ARG;
-    if ((q != nullptr) != (q_out != nullptr))
+    if ((q != nullptr) != (q_out != nullptr) || (norm && !norm_ok(norm, spec)))
         return FA_ERR_INVALID_ARG;
     if (q && (!heads_ok(q, 2) || !heads_ok(q_out, 2) || q->H != q_out->H || (long long)q->H + 2ll * cache->Hkv > INT_MAX))
         return FA_ERR_INVALID_ARG;
@@ -269,6 +369,12 @@ int fa_cache_append(const fa_kv_cache *cache, const fa_heads *k, const fa_heads 
         fa::overlaps(new_lens, (size_t)B * 4, cache->weight, slots_bytes(cache)) ||
         fa::overlaps(new_lens, (size_t)B * 4, cache->order, slots_bytes(cache)))
         return FA_ERR_INVALID_ARG;
+    if (norm) {
+        const size_t nw = (size_t)d * (norm->dtype == FA_F32 ? 4 : 2);
+        if ((norm->q_weight && touches_cache(cache, norm->q_weight, nw, true)) ||
+            (norm->k_weight && touches_cache(cache, norm->k_weight, nw, true)))
+            return FA_ERR_INVALID_ARG;
+    }
     if (q && q->H > 0) {
         const size_t nq = rows * q->H * d * 2;
         if (!heads_present(q, rows) || !heads_present(q_out, rows) || !self_disjoint(q_out, B, T, d))
@@ -276,7 +382,7 @@ int fa_cache_append(const fa_kv_cache *cache, const fa_heads *k, const fa_heads 
         if (contiguous(q, B, T, d) && touches_cache(cache, q->data, nq, true))
             return FA_ERR_INVALID_ARG;
         if (contiguous(q_out, B, T, d)) {
-            if (touches_cache(cache, q_out->data, nq, true) || fa::overlaps(q_out->data, nq, positions, npos) ||
+            if ((norm && touches_weights(norm, q_out->data, nq)) || touches_cache(cache, q_out->data, nq, true) || fa::overlaps(q_out->data, nq, positions, npos) ||
                 fa::overlaps(q_out->data, nq, new_lens, new_lens ? (size_t)B * 4 : 0) ||
                 (contiguous(q, B, T, d) && !same_place(q, q_out, B, T) && fa::overlaps(q_out->data, nq, q->data, nq)) ||
                 (contiguous(k, B, T, d) && fa::overlaps(q_out->data, nq, k->data, nk)) ||
@@ -286,8 +392,15 @@ int fa_cache_append(const fa_kv_cache *cache, const fa_heads *k, const fa_heads 
     }
     if ((st = fa::check_device()) != fa::OK)
         return st;
-    return fa::append_launch(*cache, *k, *v, q && q->H > 0 ? q : nullptr, q_out, positions, spec, new_lens, T,
+    return fa::append_launch(*cache, *k, *v, q && q->H > 0 ? q : nullptr, q_out, positions, spec, norm, new_lens, T,
                              reinterpret_cast<cudaStream_t>(stream));
+}
+
+int fa_cache_append(const fa_kv_cache *cache, const fa_heads *k, const fa_heads *v, const fa_heads *q,
+                    const fa_heads *q_out, const int *positions, const fa_rope_spec *spec, const int *new_lens, int T,
+                    fa_stream_t stream)
+{
+    return fa_cache_append_norm(cache, k, v, q, q_out, positions, spec, nullptr, new_lens, T, stream);
 }
 
 // Sizes of a paged decode: 0 for what fa_decode_paged refuses.

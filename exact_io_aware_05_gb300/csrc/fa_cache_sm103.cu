@@ -16,6 +16,7 @@
 #include "fa_common.cuh"
 #include "fa_internal.h"
 #include "fa_pdl.cuh"
+#include "fa_rope.cuh"
 
 namespace fa {
 
@@ -26,155 +27,6 @@ namespace {
 constexpr int kStatusBadIndex = 5;
 
 // ------------------------------------------------------------------ rotation
-struct RopeTable {
-    unsigned long long turns[128];
-    unsigned char axis[128];
-};
-
-struct Row3 {   // one strided [B][H][T][d] tensor
-    void *p;
-    long long sb, sh, st;
-};
-
-__device__ __forceinline__ void phase_sincos(unsigned long long turns, int pos, float &sn, float &cs)
-{
-    const unsigned long long ph = turns * (unsigned long long)(long long)pos;
-    const unsigned long long up = ph + (1ull << 61);      // to the nearest quarter turn
-    const uint32_t quad = (uint32_t)(up >> 62);
-    const int rest = (int)((long long)(ph - ((up >> 62) << 62)) >> 30);   // units of 2^-34 turns
-    const float x = (float)rest * 3.6572952e-10f;         // 2 pi 2^-34: |x| <= pi / 4
-    const float z = x * x;
-    float s = fmaf(z, 2.7557319e-6f, -1.9841270e-4f);
-    s = fmaf(z, s, 8.3333333e-3f);
-    s = fmaf(z, s, -1.6666667e-1f);
-    s = fmaf(x * z, s, x);
-    float c = fmaf(z, -2.7557319e-7f, 2.4801587e-5f);
-    c = fmaf(z, c, -1.3888889e-3f);
-    c = fmaf(z, c, 4.1666667e-2f);
-    c = fmaf(z, c, -0.5f);
-    c = fmaf(z, c, 1.0f);
-    const float a = (quad & 1) ? c : s, b = (quad & 1) ? s : c;
-    sn = (quad & 2) ? -a : a;
-    cs = ((quad + 1) & 2) ? -b : b;
-}
-
-// 8 consecutive elements as they lie in memory, and as fp32.
-template <typename E>
-struct Raw8;
-template <>
-struct Raw8<__nv_bfloat16> {
-    uint4 w;
-    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { w = *reinterpret_cast<const uint4 *>(p); }
-    __device__ __forceinline__ void get(float (&x)[8]) const
-    {
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = __uint_as_float(u[i] << 16);
-            x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-        }
-    }
-};
-template <>
-struct Raw8<float> {
-    float4 a, b;
-    __device__ __forceinline__ void load(const float *p)
-    {
-        a = reinterpret_cast<const float4 *>(p)[0];
-        b = reinterpret_cast<const float4 *>(p)[1];
-    }
-    __device__ __forceinline__ void get(float (&x)[8]) const
-    {
-        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-    }
-};
-__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&x)[8])
-{
-    *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                               pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
-}
-__device__ __forceinline__ void store8(float *p, const float (&x)[8])
-{
-    reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-}
-
-// The 16 features of one thread: two runs of 8 at e0 and e1.  Thread v < rot / 16 has pairs
-// 8 v .. 8 v + 7; the others 16 features that pass through.
-struct Slice {
-    int e0, e1, pair;   // pair < 0: pass through
-};
-__device__ __forceinline__ Slice slice_of(int v, int rot, int interleaved)
-{
-    Slice s;
-    if (v < rot / 16) {
-        s.pair = 8 * v;
-        s.e0 = interleaved ? 16 * v : 8 * v;
-        s.e1 = interleaved ? 16 * v + 8 : rot / 2 + 8 * v;
-    } else {
-        s.pair = -1;
-        s.e0 = 16 * v;
-        s.e1 = 16 * v + 8;
-    }
-    return s;
-}
-
-// Turns the pairs held in (a, b): pair j is (a[j], b[j]), or, interleaved, two neighbours.  Two
-// pairs an instruction.
-template <bool INTER>
-__device__ __forceinline__ void turn(float (&a)[8], float (&b)[8], const float (&sn)[8], const float (&cs)[8])
-{
-    auto two = [&](float &x0, float &x1, float &y0, float &y1, int j) {
-        float u0, u1, w0, w1;
-        fmul2(u0, u1, x0, x1, cs[j], cs[j + 1]);
-        fmul2(w0, w1, y0, y1, cs[j], cs[j + 1]);
-        ffma2(w0, w1, x0, x1, sn[j], sn[j + 1], w0, w1);
-        ffma2(x0, x1, y0, y1, -sn[j], -sn[j + 1], u0, u1);
-        y0 = w0;
-        y1 = w1;
-    };
-    if constexpr (!INTER) {
-#pragma unroll
-        for (int j = 0; j < 8; j += 2)
-            two(a[j], a[j + 1], b[j], b[j + 1], j);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; j += 2) {
-            two(a[2 * j], a[2 * j + 2], a[2 * j + 1], a[2 * j + 3], j);
-            two(b[2 * j], b[2 * j + 2], b[2 * j + 1], b[2 * j + 3], 4 + j);
-        }
-    }
-}
-
-// Runs over `n` heads of one token: x points at the first one's row, sx elements apart.  The loads
-// of AHEAD heads are under way at once; put(head, values at e0, values at e1) takes them.  q and k of B8 H32 T4096
-// d128 with 4, 6 and 8 heads ahead: 162.4, 160.9 and 160.1 us; prompts of 4193 tokens in e4m3 21.1, 20.5 and 20.2;
-// 512 tokens 5.5, 5.8 and 6.3.  fp32 rows are twice as long.
-template <typename E, typename Put>
-__device__ __forceinline__ void each_head(const E *x, long long sx, int n, const Slice &sl, Put put)
-{
-    constexpr int AHEAD = sizeof(E) == 2 ? 6 : 3;
-    x += sl.e0;
-    const int gap = sl.e1 - sl.e0;
-    for (int i = 0; i < n; i += AHEAD, x += AHEAD * sx) {
-        Raw8<E> p[AHEAD], q[AHEAD];
-#pragma unroll
-        for (int u = 0; u < AHEAD; ++u)
-            if (i + u < n) {
-                p[u].load(x + u * sx);
-                q[u].load(x + u * sx + gap);
-            }
-#pragma unroll
-        for (int u = 0; u < AHEAD; ++u)
-            if (i + u < n) {
-                float f[8], g[8];
-                p[u].get(f);
-                q[u].get(g);
-                put(i + u, f, g);
-            }
-    }
-}
-
 struct RopeArgs {
     Row3 x[2], y[2];
     int H0, H;            // heads of the first tensor, of both
@@ -183,8 +35,6 @@ struct RopeArgs {
     int T, rot, heads_per_cta, groups;   // head groups
     float sign;
 };
-
-constexpr int kRopeThreads = 256;
 
 template <typename E, int D, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads, 2) rope_kernel(const __grid_constant__ RopeTable tab,
@@ -231,28 +81,6 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_kernel(const __grid_cons
     }
 }
 
-RopeTable table_of(const fa_rope_spec &s)
-{
-    RopeTable t;
-    for (int i = 0; i < 128; ++i) {
-        t.turns[i] = s.turns[i];
-        t.axis[i] = s.axis[i];
-    }
-    return t;
-}
-
-Row3 row3(const fa_heads &x) { return Row3{x.data, x.stride_b, x.stride_h, x.stride_t}; }
-
-// Heads one thread runs over: as few as let all CTAs be resident (two an SM), 32 at most.  With 8, 16,
-// 32 and 48 heads the q and k of B8 H32 T4096 d128 take 175, 163, 162 and 163 us, and 4193 new tokens of
-// 32 + 16 heads 24.6, 24.1, 21.1 and 26.7.
-int heads_per_cta(long long tokens, int H, int d)
-{
-    const long long ctas = (tokens * (d / 16) + kRopeThreads - 1) / kRopeThreads * H, slots = 2 * device_sm_count();
-    const long long n = (ctas + slots - 1) / slots;
-    return (int)(n < 1 ? 1 : n > 32 ? 32 : n);
-}
-
 template <typename E, int D>
 int rope_run(const RopeTable &t, const RopeArgs &a, int interleaved, cudaStream_t s)
 {
@@ -271,6 +99,7 @@ int rope_width(int d, const RopeTable &t, const RopeArgs &a, int interleaved, cu
 // ------------------------------------------------------------------ append
 struct AppendArgs {
     Row3 q, qo, k, v;
+    NormArgs norm;        // of q's and k's heads (NORM)
     int Hq, Hkv, B, T, rot, rotate, heads_per_cta, groups;
     const int *pos;
     const int *block_table, *lens, *seen, *new_lens;
@@ -319,8 +148,9 @@ __device__ __forceinline__ void put8(void *base, long long at, const float (&x)[
     }
 }
 
-// Heads run q, then k, then v; a token's slot and page are looked up once per thread.
-template <int D, bool INTER, bool FP8>
+// Heads run q, then k, then v; a token's slot and page are looked up once per thread.  NORM: the rows of q
+// and k are normed before they turn.
+template <int D, bool INTER, bool FP8, bool NORM>
 __global__ void __launch_bounds__(kRopeThreads, 2) append_kernel(const __grid_constant__ RopeTable tab,
                                                               const __grid_constant__ AppendArgs a)
 {
@@ -347,6 +177,13 @@ __global__ void __launch_bounds__(kRopeThreads, 2) append_kernel(const __grid_co
         for (int j = 0; j < 8; ++j)
             pos[j] = a.pos[(long long)tab.axis[sl.pair + j] * n + tok];
     }
+    float wf[8], wg[8];   // of the first tensor that the group has
+    auto weights = [&](int which) {
+        norm_weights(a.norm, which, sl.e0, wf);
+        norm_weights(a.norm, which, sl.e1, wg);
+    };
+    if (NORM && h0 < a.Hq + a.Hkv)
+        weights(h0 < a.Hq ? 0 : 1);
     if (len < 0 || len > cap || nb < 0 || nb > a.T || nb > len) {
         if (vec == 0 && t == 0 && group == 0)
             atomicCAS(&g_cache_status, 0, kStatusBadIndex);
@@ -378,13 +215,17 @@ __global__ void __launch_bounds__(kRopeThreads, 2) append_kernel(const __grid_co
     if (part(0, a.Hq, first, count)) {
         const E *x = static_cast<const E *>(a.q.p) + b * a.q.sb + first * a.q.sh + t * a.q.st;
         E *o = static_cast<E *>(a.qo.p) + b * a.qo.sb + first * a.qo.sh + t * a.qo.st + sl.e0;
-        each_head(x, a.q.sh, count, sl, [&](int, float(&f)[8], float(&g)[8]) {
+        auto put = [&](int, float(&f)[8], float(&g)[8]) {
             if (turns)
                 turn<INTER>(f, g, sn, cs);
             store8(o, f);
             store8(o + gap, g);
             o += a.qo.sh;
-        });
+        };
+        if constexpr (NORM)
+            each_head_normed<E, D>(x, a.q.sh, count, sl, wf, wg, a.norm.eps, put);
+        else
+            each_head(x, a.q.sh, count, sl, put);
     }
     if (!page_ok)
         return;
@@ -393,7 +234,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) append_kernel(const __grid_co
     if (part(a.Hq, a.Hkv, first, count)) {
         const E *x = static_cast<const E *>(a.k.p) + b * a.k.sb + first * a.k.sh + t * a.k.st;
         long long at = row_at + first * step;
-        each_head(x, a.k.sh, count, sl, [&](int i, float(&f)[8], float(&g)[8]) {
+        auto put = [&](int i, float(&f)[8], float(&g)[8]) {
             if (turns)
                 turn<INTER>(f, g, sn, cs);
             const float scale = FP8 ? a.ks[first + i] : 1.f, inv = FP8 ? __frcp_rn(scale) : 1.f;
@@ -407,7 +248,14 @@ __global__ void __launch_bounds__(kRopeThreads, 2) append_kernel(const __grid_co
                 if (a.order)
                     a.order[w] = (a.seen ? a.seen[b] - nb : len - nb) + t;
             }
-        });
+        };
+        if constexpr (NORM) {
+            if (h0 < a.Hq)
+                weights(1);
+            each_head_normed<E, D>(x, a.k.sh, count, sl, wf, wg, a.norm.eps, put);
+        } else {
+            each_head(x, a.k.sh, count, sl, put);
+        }
     }
     if (part(a.Hq + a.Hkv, a.Hkv, first, count)) {
         const E *x = static_cast<const E *>(a.v.p) + b * a.v.sb + first * a.v.sh + t * a.v.st;
@@ -421,13 +269,20 @@ __global__ void __launch_bounds__(kRopeThreads, 2) append_kernel(const __grid_co
     }
 }
 
-template <int D, bool FP8>
-int append_run(const RopeTable &t, const AppendArgs &a, int interleaved, cudaStream_t s)
+template <int D, bool FP8, bool NORM>
+int append_with(const RopeTable &t, const AppendArgs &a, int interleaved, cudaStream_t s)
 {
     constexpr int TOK = kRopeThreads / (D / 16);
     const long long n = (long long)a.B * a.T;
     const dim3 grid((unsigned)((n + TOK - 1) / TOK * a.groups));
-    return launch_overlapped(interleaved ? append_kernel<D, true, FP8> : append_kernel<D, false, FP8>, grid, kRopeThreads, 0, 0, true, s, t, a);
+    return launch_overlapped(interleaved ? append_kernel<D, true, FP8, NORM> : append_kernel<D, false, FP8, NORM>, grid, kRopeThreads, 0, 0,
+                             true, s, t, a);
+}
+
+template <int D, bool FP8>
+int append_run(const RopeTable &t, const AppendArgs &a, int interleaved, bool norm, cudaStream_t s)
+{
+    return norm ? append_with<D, FP8, true>(t, a, interleaved, s) : append_with<D, FP8, false>(t, a, interleaved, s);
 }
 
 // ------------------------------------------------------------------ evict
@@ -977,11 +832,12 @@ int rope_launch(const fa_heads *x, const fa_heads *y, int n, const int *position
 }
 
 int append_launch(const fa_kv_cache &c, const fa_heads &k, const fa_heads &v, const fa_heads *q,
-                  const fa_heads *q_out, const int *positions, const fa_rope_spec *spec, const int *new_lens, int T,
-                  cudaStream_t s)
+                  const fa_heads *q_out, const int *positions, const fa_rope_spec *spec, const fa_head_norm *norm,
+                  const int *new_lens, int T, cudaStream_t s)
 {
     status_in_use(STATUS_CACHE);
     AppendArgs a;
+    a.norm = norm ? norm_args(*norm) : NormArgs{};
     a.k = row3(k);
     a.v = row3(v);
     a.q = q ? row3(*q) : Row3{nullptr, 0, 0, 0};
@@ -1018,11 +874,11 @@ int append_launch(const fa_kv_cache &c, const fa_heads &k, const fa_heads &v, co
     const bool f8 = c.dtype == FA_E4M3;
     switch (c.d) {
     case 64:
-        return f8 ? append_run<64, true>(t, a, inter, s) : append_run<64, false>(t, a, inter, s);
+        return f8 ? append_run<64, true>(t, a, inter, norm, s) : append_run<64, false>(t, a, inter, norm, s);
     case 128:
-        return f8 ? append_run<128, true>(t, a, inter, s) : append_run<128, false>(t, a, inter, s);
+        return f8 ? append_run<128, true>(t, a, inter, norm, s) : append_run<128, false>(t, a, inter, norm, s);
     default:
-        return f8 ? append_run<256, true>(t, a, inter, s) : append_run<256, false>(t, a, inter, s);
+        return f8 ? append_run<256, true>(t, a, inter, norm, s) : append_run<256, false>(t, a, inter, norm, s);
     }
 }
 

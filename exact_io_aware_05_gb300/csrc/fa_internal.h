@@ -152,8 +152,15 @@ int encode_tmap(CUtensorMap *map, const void *base, CUtensorMapDataType dtype, i
 int rope_launch(const fa_heads *x, const fa_heads *y, int n, const int *positions, const fa_rope_spec &spec, int B,
                 int T, int dtype, int inverse, cudaStream_t s);
 int append_launch(const fa_kv_cache &c, const fa_heads &k, const fa_heads &v, const fa_heads *q,
-                  const fa_heads *q_out, const int *positions, const fa_rope_spec *spec, const int *new_lens, int T,
-                  cudaStream_t s);
+                  const fa_heads *q_out, const int *positions, const fa_rope_spec *spec, const fa_head_norm *norm,
+                  const int *new_lens, int T, cudaStream_t s);
+// Head norms with the rotation (fa_norm_sm103.cu).  rows of n tensors; the gradients of the weights may be null.
+int norm_rope_launch(const fa_heads *x, const fa_heads *y, int n, const fa_head_norm &norm, const int *positions,
+                     const fa_rope_spec &spec, int B, int T, int dtype, cudaStream_t s);
+size_t norm_bwd_workspace_bytes(int d);
+int norm_rope_bwd_launch(const fa_heads *x, const fa_heads *dy, const fa_heads *dx, int n, const fa_head_norm &norm,
+                         const int *positions, const fa_rope_spec &spec, int B, int T, int dtype, float *dq_weight,
+                         float *dk_weight, void *workspace, cudaStream_t s);
 int evict_launch(const fa_kv_cache &c, int budget, int n_first, int n_recent, float *weight_out, int *order_out,
                  int *lens_out, int *kept, cudaStream_t s);
 size_t paged_workspace_bytes(int B, int Hq, int Hkv, int Tq, int max_len, int d, int accumulate);

@@ -1,0 +1,347 @@
+// fa_norm_sm103.cu -- norms of query and key heads with the rotation in the same pass, and their
+// gradients (sm_103a).
+//
+// Formulas, per row of d features: r = (mean x^2 + eps)^(-1/2), u = x r, y = R(w u), where R turns the
+// pairs by the token's positions (fa_cache_sm103.cu).  Backward, with g = R^T dy:
+//     dw = sum over all rows of g u,    dx = r (w g - u mean(w g u)).
+// r is found again from x: it is one sum more, and nothing has to be kept between the passes.
+//
+// What bounds them is memory: forward reads and writes each element once, backward reads x and dy and
+// writes dx.  A thread has 16 features of one token (8 pairs) and runs over heads with the token's
+// sines and cosines and the weights in registers; the D / 16 threads of a row put their sums together by
+// shuffles, those of all heads under way at a time, so that a shuffle's latency is paid once for several
+// rows.  dw: each thread adds up its features over all its rows, each CTA its threads, and a second
+// kernel the CTAs, in a fixed order: the same bits on every run.
+#include <climits>
+
+#include "fa_common.cuh"
+#include "fa_internal.h"
+#include "fa_pdl.cuh"
+#include "fa_rope.cuh"
+
+namespace fa {
+namespace {
+
+struct NormRopeArgs {
+    Row3 x[2], y[2];
+    NormArgs norm;
+    int H0, H;            // heads of the first tensor, of both
+    const int *pos;       // [axes][n]
+    long long n;          // B * T
+    int T, rot, heads_per_cta, groups;
+};
+
+template <typename E, int D, bool INTER>
+__global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_kernel(const __grid_constant__ RopeTable tab,
+                                                                 const __grid_constant__ NormRopeArgs a)
+{
+    constexpr int TPR = D / 16;                          // threads a row
+    pdl_launch();
+    pdl_wait();
+    const int v = threadIdx.x % TPR;
+    // head groups next to one another: CTAs that run together read whole token rows of a packed
+    // projection
+    const int tile = (int)(blockIdx.x / a.groups), group = (int)blockIdx.x - tile * a.groups;
+    const long long tok = (long long)tile * (kRopeThreads / TPR) + threadIdx.x / TPR;
+    if (tok >= a.n)
+        return;
+    const int b = (int)tok / a.T, t = (int)tok - b * a.T;
+    const Slice sl = slice_of(v, a.rot, INTER);
+    float sn[8], cs[8];
+    if (sl.pair >= 0) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int p = a.pos[(long long)tab.axis[sl.pair + j] * a.n + tok];
+            phase_sincos(tab.turns[sl.pair + j], p, sn[j], cs[j]);
+        }
+    }
+    const int h0 = group * a.heads_per_cta, h1 = min(a.H, h0 + a.heads_per_cta);
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {   // the group's heads of either tensor
+        const int first = max(h0 - (w ? a.H0 : 0), 0), last = min(h1 - (w ? a.H0 : 0), w ? a.H - a.H0 : a.H0);
+        if (first >= last)
+            continue;
+        float wf[8], wg[8];
+        norm_weights(a.norm, w, sl.e0, wf);
+        norm_weights(a.norm, w, sl.e1, wg);
+        const Row3 &xi = a.x[w], &yi = a.y[w];
+        const E *x = static_cast<const E *>(xi.p) + b * xi.sb + first * xi.sh + t * xi.st;
+        E *y = static_cast<E *>(yi.p) + b * yi.sb + first * yi.sh + t * yi.st + sl.e0;
+        const int gap = sl.e1 - sl.e0;
+        each_head_normed<E, D>(x, xi.sh, last - first, sl, wf, wg, a.norm.eps, [&](int, float(&f)[8], float(&g)[8]) {
+            if (sl.pair >= 0)
+                turn<INTER>(f, g, sn, cs);
+            store8(y, f);
+            store8(y + gap, g);
+            y += yi.sh;
+        });
+    }
+}
+
+// ------------------------------------------------------------------ backward
+struct NormBwdArgs {
+    Row3 x[2], dy[2], dx[2];
+    NormArgs norm;
+    int H[2], G0;         // heads of either tensor; head groups of the first
+    const int *pos;       // [axes][n]
+    long long n;          // B * T
+    int T, rot, heads_per_cta, groups, tiles;
+    float *part;          // [CTA][d], or null: no gradients of the weights
+    float *dw[2];         // or null
+    int ctas;
+};
+
+constexpr int kNormCtas = 304;   // two an SM; the sums' order depends on it, not on the device
+
+// A CTA has one head group, of one tensor, and every ctas / groups-th tile of tokens.
+template <typename E, int D, bool INTER>
+__global__ void __launch_bounds__(kRopeThreads, 2) norm_bwd_kernel(const __grid_constant__ RopeTable tab,
+                                                                const __grid_constant__ NormBwdArgs a)
+{
+    constexpr int TPR = D / 16, TOK = kRopeThreads / TPR;
+    constexpr int AHEAD = sizeof(E) == 2 ? 2 : 1;        // heads under way: two streams of 16 features each
+    __shared__ float sums[TOK * D];
+    pdl_wait();
+    const int v = threadIdx.x % TPR, row = threadIdx.x / TPR;
+    const int group = (int)blockIdx.x % a.groups, w = group >= a.G0;
+    const int h0 = (group - (w ? a.G0 : 0)) * a.heads_per_cta, nh = min(a.heads_per_cta, a.H[w] - h0);
+    const Slice sl = slice_of(v, a.rot, INTER);
+    const int gap = sl.e1 - sl.e0;
+    float wf[8], wg[8], af[8], ag[8];
+    norm_weights(a.norm, w, sl.e0, wf);
+    norm_weights(a.norm, w, sl.e1, wg);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        af[j] = ag[j] = 0.f;
+    const Row3 &xi = a.x[w], &gi = a.dy[w], &oi = a.dx[w];
+    for (int tile = (int)blockIdx.x / a.groups; tile < a.tiles; tile += a.ctas / a.groups) {
+        const long long tok = (long long)tile * TOK + row;
+        if (tok >= a.n)
+            break;
+        const int b = (int)tok / a.T, t = (int)tok - b * a.T;
+        float sn[8], cs[8];
+        if (sl.pair >= 0) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int p = a.pos[(long long)tab.axis[sl.pair + j] * a.n + tok];
+                phase_sincos(tab.turns[sl.pair + j], p, sn[j], cs[j]);
+                sn[j] = -sn[j];   // the transpose turns the other way
+            }
+        }
+        const E *x = static_cast<const E *>(xi.p) + b * xi.sb + h0 * xi.sh + t * xi.st + sl.e0;
+        const E *dy = static_cast<const E *>(gi.p) + b * gi.sb + h0 * gi.sh + t * gi.st + sl.e0;
+        E *dx = static_cast<E *>(oi.p) + b * oi.sb + h0 * oi.sh + t * oi.st + sl.e0;
+        for (int i = 0; i < nh; i += AHEAD) {
+            Raw8<E> px[AHEAD][2] = {}, pg[AHEAD][2] = {};
+            float s[AHEAD], z[AHEAD];   // sums of x^2 and of w g x
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u)
+                if (i + u < nh) {
+                    px[u][0].load(x + u * xi.sh);
+                    px[u][1].load(x + u * xi.sh + gap);
+                    pg[u][0].load(dy + u * gi.sh);
+                    pg[u][1].load(dy + u * gi.sh + gap);
+                }
+            x += AHEAD * xi.sh;
+            dy += AHEAD * gi.sh;
+            // R^T dy is found twice, for the sums and behind them: kept, its registers would be one head less
+            auto turned = [&](int u, float(&f)[8], float(&g)[8]) {
+                pg[u][0].get(f);
+                pg[u][1].get(g);
+                if (sl.pair >= 0)
+                    turn<INTER>(f, g, sn, cs);
+            };
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u) {
+                float xf[8], xg[8], f[8], g[8];
+                px[u][0].get(xf);
+                px[u][1].get(xg);
+                turned(u, f, g);
+                s[u] = sum_squares(xf, xg);
+                float z0 = 0.f, z1 = 0.f;
+#pragma unroll
+                for (int j = 0; j < 8; j += 2) {
+                    float t0, t1;
+                    fmul2(t0, t1, f[j], f[j + 1], wf[j], wf[j + 1]);
+                    ffma2(z0, z1, t0, t1, xf[j], xf[j + 1], z0, z1);
+                    fmul2(t0, t1, g[j], g[j + 1], wg[j], wg[j + 1]);
+                    ffma2(z0, z1, t0, t1, xg[j], xg[j + 1], z0, z1);
+                }
+                z[u] = z0 + z1;
+            }
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u) {
+                s[u] = row_sum<TPR>(s[u]);
+                z[u] = row_sum<TPR>(z[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u)
+                if (i + u < nh) {
+                    const float r = __frsqrt_rn(fmaf(s[u], 1.f / D, a.norm.eps));
+                    const float m = -z[u] * (1.f / D) * r * r;   // dx = r (w g - x (r^2 mean(w g x)))
+                    float x0[8], x1[8], f[8], g[8];
+                    turned(u, f, g);
+                    px[u][0].get(x0);
+                    px[u][1].get(x1);
+                    auto half = [&](float(&gy)[8], const float(&xx)[8], const float(&ww)[8], float(&acc)[8]) {
+#pragma unroll
+                        for (int j = 0; j < 8; j += 2) {
+                            float t0, t1;
+                            fmul2(t0, t1, xx[j], xx[j + 1], r, r);
+                            ffma2(acc[j], acc[j + 1], gy[j], gy[j + 1], t0, t1, acc[j], acc[j + 1]);
+                            fmul2(t0, t1, gy[j], gy[j + 1], ww[j], ww[j + 1]);
+                            ffma2(t0, t1, xx[j], xx[j + 1], m, m, t0, t1);
+                            fmul2(gy[j], gy[j + 1], t0, t1, r, r);
+                        }
+                    };
+                    half(f, x0, wf, af);
+                    half(g, x1, wg, ag);
+                    store8(dx, f);
+                    store8(dx + gap, g);
+                    dx += oi.sh;
+                }
+        }
+    }
+    pdl_launch();
+    if (!a.part)
+        return;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        sums[row * D + sl.e0 + j] = af[j];
+        sums[row * D + sl.e1 + j] = ag[j];
+    }
+    __syncthreads();
+    for (int f = threadIdx.x; f < D; f += kRopeThreads) {
+        float x = 0.f;
+#pragma unroll 8
+        for (int i = 0; i < TOK; ++i)
+            x += sums[i * D + f];
+        a.part[(long long)blockIdx.x * D + f] = x;
+    }
+}
+
+// dw[tensor][32 features of a block]: the CTAs' sums, eight runs of CTAs side by side.
+__global__ void __launch_bounds__(256) norm_dweight_kernel(const __grid_constant__ NormBwdArgs a, int d)
+{
+    __shared__ float red[8][32];
+    pdl_launch();
+    pdl_wait();
+    const int w = (int)blockIdx.y, f = (int)blockIdx.x * 32 + (threadIdx.x & 31), run = threadIdx.x >> 5;
+    if (!a.dw[w])
+        return;
+    const int from = w ? a.G0 : 0, count = w ? a.groups - a.G0 : a.G0;   // its head groups
+    const int total = count * (a.ctas / a.groups);
+    float x = 0.f;
+#pragma unroll 4
+    for (int i = run; i < total; i += 8)
+        x += __ldcg(a.part + (long long)(i / count * a.groups + from + i % count) * d + f);
+    red[run][threadIdx.x & 31] = x;
+    __syncthreads();
+    if (run == 0) {
+        for (int i = 1; i < 8; ++i)
+            x += red[i][threadIdx.x];
+        a.dw[w][f] = x;
+    }
+}
+
+template <typename E, int D>
+int norm_run(const RopeTable &t, const NormRopeArgs &a, int interleaved, cudaStream_t s)
+{
+    constexpr int TOK = kRopeThreads / (D / 16);
+    const dim3 grid((unsigned)((a.n + TOK - 1) / TOK * a.groups));
+    return launch_overlapped(interleaved ? norm_rope_kernel<E, D, true> : norm_rope_kernel<E, D, false>, grid, kRopeThreads, 0, 0,
+                             true, s, t, a);
+}
+
+template <typename E, int D>
+int norm_bwd_run(const RopeTable &t, NormBwdArgs &a, int interleaved, cudaStream_t s)
+{
+    constexpr int TOK = kRopeThreads / (D / 16);
+    a.tiles = (int)((a.n + TOK - 1) / TOK);
+    const int runs = kNormCtas / a.groups;   // CTAs of a head group
+    a.ctas = a.groups * (a.tiles < runs ? a.tiles : runs);
+    if (a.ctas == 0)   // no row: the sums are 0
+        return launch_overlapped(norm_dweight_kernel, dim3(D / 32, 2), 256, 0, 0, true, s, a, D);
+    const int st = launch_overlapped(interleaved ? norm_bwd_kernel<E, D, true> : norm_bwd_kernel<E, D, false>, dim3((unsigned)a.ctas),
+                                     kRopeThreads, 0, 0, true, s, t, a);
+    if (st != OK || !a.part)
+        return st;
+    return launch_overlapped(norm_dweight_kernel, dim3(D / 32, 2), 256, 0, 0, true, s, a, D);
+}
+
+template <typename E>
+int norm_width(int d, const RopeTable &t, const NormRopeArgs &a, int interleaved, cudaStream_t s)
+{
+    return d == 64 ? norm_run<E, 64>(t, a, interleaved, s)
+                   : d == 128 ? norm_run<E, 128>(t, a, interleaved, s) : norm_run<E, 256>(t, a, interleaved, s);
+}
+
+template <typename E>
+int norm_bwd_width(int d, const RopeTable &t, NormBwdArgs &a, int interleaved, cudaStream_t s)
+{
+    return d == 64 ? norm_bwd_run<E, 64>(t, a, interleaved, s)
+                   : d == 128 ? norm_bwd_run<E, 128>(t, a, interleaved, s) : norm_bwd_run<E, 256>(t, a, interleaved, s);
+}
+
+}  // namespace
+
+int norm_rope_launch(const fa_heads *x, const fa_heads *y, int n, const fa_head_norm &norm, const int *positions,
+                     const fa_rope_spec &spec, int B, int T, int dtype, cudaStream_t s)
+{
+    NormRopeArgs a{};
+    a.H = 0;
+    for (int i = 0; i < n; ++i) {
+        a.x[i] = row3(x[i]);
+        a.y[i] = row3(y[i]);
+        a.H += x[i].H;
+    }
+    a.H0 = x[0].H;
+    a.norm = norm_args(norm);
+    a.pos = positions;
+    a.n = (long long)B * T;
+    a.T = T;
+    a.rot = spec.rot;
+    a.heads_per_cta = heads_per_cta(a.n, a.H, spec.d);
+    a.groups = (a.H + a.heads_per_cta - 1) / a.heads_per_cta;
+    if ((a.n / 16 + 1) * a.groups > INT_MAX)
+        return ERR_UNSUPPORTED;
+    const RopeTable t = table_of(spec);
+    return dtype == FA_F32 ? norm_width<float>(spec.d, t, a, spec.interleaved, s)
+                           : norm_width<__nv_bfloat16>(spec.d, t, a, spec.interleaved, s);
+}
+
+size_t norm_bwd_workspace_bytes(int d) { return (size_t)kNormCtas * d * sizeof(float); }
+
+int norm_rope_bwd_launch(const fa_heads *x, const fa_heads *dy, const fa_heads *dx, int n, const fa_head_norm &norm,
+                         const int *positions, const fa_rope_spec &spec, int B, int T, int dtype, float *dq_weight,
+                         float *dk_weight, void *workspace, cudaStream_t s)
+{
+    NormBwdArgs a{};
+    long long H = 0;
+    for (int i = 0; i < n; ++i) {
+        a.x[i] = row3(x[i]);
+        a.dy[i] = row3(dy[i]);
+        a.dx[i] = row3(dx[i]);
+        a.H[i] = x[i].H;
+        H += x[i].H;
+    }
+    a.norm = norm_args(norm);
+    a.pos = positions;
+    a.n = (long long)B * T;
+    a.T = T;
+    a.rot = spec.rot;
+    // as in the forward, and so many that every head group has a CTA
+    const int hpc = H > 0 ? heads_per_cta(a.n, (int)H, spec.d) : 1, least = (int)((H + kNormCtas - 3) / (kNormCtas - 2));
+    a.heads_per_cta = hpc > least ? hpc : least;
+    a.G0 = (a.H[0] + a.heads_per_cta - 1) / a.heads_per_cta;
+    a.groups = a.G0 + (a.H[1] + a.heads_per_cta - 1) / a.heads_per_cta;
+    a.groups = a.groups > 0 ? a.groups : 1;
+    a.dw[0] = dq_weight;
+    a.dw[1] = dk_weight;
+    a.part = dq_weight || dk_weight ? static_cast<float *>(workspace) : nullptr;
+    const RopeTable t = table_of(spec);
+    return dtype == FA_F32 ? norm_bwd_width<float>(spec.d, t, a, spec.interleaved, s)
+                           : norm_bwd_width<__nv_bfloat16>(spec.d, t, a, spec.interleaved, s);
+}
+
+}  // namespace fa

@@ -16,13 +16,16 @@
 
 typedef int (*rope_fn)(const fa_heads *, const fa_heads *, int, const int *, const fa_rope_spec *, int, int, int, int,
                        fa_stream_t);
+typedef int (*norm_rope_fn)(const fa_heads *, const fa_heads *, int, const fa_head_norm *, const int *, const fa_rope_spec *, int,
+                            int, int, fa_stream_t);
 typedef int (*append_fn)(const fa_kv_cache *, const fa_heads *, const fa_heads *, const fa_heads *, const fa_heads *,
-                         const int *, const fa_rope_spec *, const int *, int, fa_stream_t);
+                         const int *, const fa_rope_spec *, const fa_head_norm *, const int *, int, fa_stream_t);
 typedef int (*decode_fn)(const fa_kv_cache *, const void *, void *, float *, int, int, int, float, int, void *, size_t,
                          fa_stream_t);
 typedef int (*evict_fn)(const fa_kv_cache *, int, int, int, float *, int *, int *, int *, fa_stream_t);
 
 static rope_fn call_rope;
+static norm_rope_fn call_norm_rope;
 static append_fn call_append;
 static decode_fn call_decode;
 static evict_fn call_evict;
@@ -167,6 +170,46 @@ static int int_arg(PyObject *x, int *out)
     return 1;
 }
 
+/* The tensors of a rotary call: a[0] .. a[4] are q, q_out, k, k_out and positions. */
+typedef struct {
+    fa_heads x[2], y[2];
+    void *pos;
+    fa_stream_t stream;
+    int n, B, T, dtype;
+    long long dev;
+} rotary;
+
+static int rotary_of(const fa_rope_spec *spec, PyObject *const *a, PyObject *stream, rotary *r)
+{
+    long long shape[4];
+    int ok = 1;
+    PyObject *dtype = has_dtype(a[0], t_bf16) ? t_bf16 : has_dtype(a[0], t_f32) ? t_f32 : NULL;
+    PyObject *index = PyObject_CallMethodNoArgs(a[0], n_get_device);
+    Py_XINCREF(index);
+    const long long dev = taken_int(index, &ok);
+    if (!dtype || !ok || !tuple_of(a[0], n_shape, 0, 4, shape))
+        goto no;
+    const long long B = shape[0], T = shape[2], d = shape[3], at[3] = {spec->n_axes, B, T};
+    const int two = a[2] != Py_None;
+    if (d != spec->d || two != (a[3] != Py_None) || B > INT_MAX || T > INT_MAX || !plain(a[4], t_i32, 3, at, dev, &r->pos) ||
+        !strided(a[0], shape, &r->x[0]) || !heads(a[1], dtype, B, r->x[0].H, T, d, dev, &r->y[0]))
+        goto no;
+    if (two && (!heads(a[2], dtype, B, -1, T, d, dev, &r->x[1]) || !heads(a[3], dtype, B, r->x[1].H, T, d, dev, &r->y[1])))
+        goto no;
+    if (!stream_of(stream, index, dev, &r->stream))
+        goto no;
+    Py_DECREF(index);
+    r->n = two ? 2 : 1;
+    r->B = (int)B;
+    r->T = (int)T;
+    r->dtype = dtype == t_bf16 ? FA_BF16 : FA_F32;
+    r->dev = dev;
+    return 1;
+no:
+    Py_XDECREF(index);
+    return 0;
+}
+
 /* rope(spec, q, q_out, k, k_out, positions, inverse, stream) */
 static PyObject *py_rope(PyObject *self, PyObject *const *a, Py_ssize_t n)
 {
@@ -174,46 +217,50 @@ static PyObject *py_rope(PyObject *self, PyObject *const *a, Py_ssize_t n)
     if (n != 8)
         return PyErr_Format(PyExc_TypeError, "rope: 8 arguments");
     const fa_rope_spec *spec = (const fa_rope_spec *)PyLong_AsVoidPtr(a[0]);
-    if (!spec)
+    rotary r;
+    int inverse;
+    if (!spec || !int_arg(a[6], &inverse) || !rotary_of(spec, a + 1, a[7], &r))
         return slow();
-    fa_heads x[2], y[2];
-    void *pos;
-    fa_stream_t s;
-    long long shape[4];
-    int ok = 1, inverse;
-    PyObject *dtype = has_dtype(a[1], t_bf16) ? t_bf16 : has_dtype(a[1], t_f32) ? t_f32 : NULL;
-    PyObject *index = PyObject_CallMethodNoArgs(a[1], n_get_device);
-    Py_XINCREF(index);
-    const long long dev = taken_int(index, &ok);
-    if (!dtype || !ok || !tuple_of(a[1], n_shape, 0, 4, shape))
-        goto no;
-    const long long B = shape[0], T = shape[2], d = shape[3], at[3] = {spec->n_axes, B, T};
-    const int two = a[3] != Py_None;
-    if (d != spec->d || two != (a[4] != Py_None) || B > INT_MAX || T > INT_MAX || !int_arg(a[6], &inverse) ||
-        !plain(a[5], t_i32, 3, at, dev, &pos) || !strided(a[1], shape, &x[0]) ||
-        !heads(a[2], dtype, B, x[0].H, T, d, dev, &y[0]))
-        goto no;
-    if (two && (!heads(a[3], dtype, B, -1, T, d, dev, &x[1]) || !heads(a[4], dtype, B, x[1].H, T, d, dev, &y[1])))
-        goto no;
-    if (!stream_of(a[7], index, dev, &s))
-        goto no;
-    Py_DECREF(index);
     int st;
     Py_BEGIN_ALLOW_THREADS;
-    st = call_rope(x, y, two ? 2 : 1, (const int *)pos, spec, (int)B, (int)T, dtype == t_bf16 ? FA_BF16 : FA_F32, inverse, s);
+    st = call_rope(r.x, r.y, r.n, (const int *)r.pos, spec, r.B, r.T, r.dtype, inverse, r.stream);
     Py_END_ALLOW_THREADS;
     return PyLong_FromLong(st);
-no:
-    Py_XDECREF(index);
-    return slow();
 }
 
-/* append(cache, index, k, v, positions, spec, q, q_out, new_lens, stream); spec None or an address */
+/* A norm's address and its weights' device (-1: it has none) beside tensors on `dev`. */
+static int norm_of(PyObject *ref, PyObject *index, long long dev, const fa_head_norm **out)
+{
+    int at;
+    *out = (const fa_head_norm *)PyLong_AsVoidPtr(ref);
+    return *out && int_arg(index, &at) && (at == dev || (!(*out)->q_weight && !(*out)->k_weight));
+}
+
+/* norm_rope(spec, norm, norm's index, q, q_out, k, k_out, positions, stream) */
+static PyObject *py_norm_rope(PyObject *self, PyObject *const *a, Py_ssize_t n)
+{
+    (void)self;
+    if (n != 9)
+        return PyErr_Format(PyExc_TypeError, "norm_rope: 9 arguments");
+    const fa_rope_spec *spec = (const fa_rope_spec *)PyLong_AsVoidPtr(a[0]);
+    const fa_head_norm *norm;
+    rotary r;
+    if (!spec || !rotary_of(spec, a + 3, a[8], &r) || !norm_of(a[1], a[2], r.dev, &norm) || norm->d != spec->d)
+        return slow();
+    int st;
+    Py_BEGIN_ALLOW_THREADS;
+    st = call_norm_rope(r.x, r.y, r.n, norm, (const int *)r.pos, spec, r.B, r.T, r.dtype, r.stream);
+    Py_END_ALLOW_THREADS;
+    return PyLong_FromLong(st);
+}
+
+/* append(cache, index, k, v, positions, spec, q, q_out, new_lens, stream[, norm, norm's index]); spec and norm None
+ * or an address */
 static PyObject *py_append(PyObject *self, PyObject *const *a, Py_ssize_t n)
 {
     (void)self;
-    if (n != 10)
-        return PyErr_Format(PyExc_TypeError, "append: 10 arguments");
+    if (n != 10 && n != 12)
+        return PyErr_Format(PyExc_TypeError, "append: 10 or 12 arguments");
     const fa_kv_cache *c = (const fa_kv_cache *)PyLong_AsVoidPtr(a[0]);
     if (!c)
         return slow();
@@ -242,11 +289,14 @@ static PyObject *py_append(PyObject *self, PyObject *const *a, Py_ssize_t n)
         return slow();
     if (a[8] != Py_None && !plain(a[8], t_i32, 1, lens, dev, &new_lens))
         return slow();
+    const fa_head_norm *norm = NULL;
+    if (n == 12 && a[10] != Py_None && (!rotate || !norm_of(a[10], a[11], dev, &norm) || norm->d != d))
+        return slow();
     if (!stream_of(a[9], a[1], dev, &s))
         return slow();
     int st;
     Py_BEGIN_ALLOW_THREADS;
-    st = call_append(c, &k, &v, with_q ? &q : NULL, with_q ? &qo : NULL, (const int *)pos, spec, (const int *)new_lens,
+    st = call_append(c, &k, &v, with_q ? &q : NULL, with_q ? &qo : NULL, (const int *)pos, spec, norm, (const int *)new_lens,
                      (int)T, s);
     Py_END_ALLOW_THREADS;
     return PyLong_FromLong(st);
@@ -315,15 +365,17 @@ static PyObject *py_evict(PyObject *self, PyObject *const *a, Py_ssize_t n)
     return PyLong_FromLong(st);
 }
 
-/* setup(bfloat16, float32, int32, stream function, device function, addresses of the four entry points) */
+enum { ENTRIES = 5 };
+
+/* setup(bfloat16, float32, int32, stream function, device function, addresses of the entry points) */
 static PyObject *py_setup(PyObject *self, PyObject *const *a, Py_ssize_t n)
 {
     (void)self;
-    if (n != 9)
-        return PyErr_Format(PyExc_TypeError, "setup: 9 arguments");
+    if (n != 5 + ENTRIES)
+        return PyErr_Format(PyExc_TypeError, "setup: %d arguments", 5 + ENTRIES);
     PyObject **keep[5] = {&t_bf16, &t_f32, &t_i32, &f_stream, &f_device};
-    void *fn[4];
-    for (int i = 0; i < 4; ++i) {
+    void *fn[ENTRIES];
+    for (int i = 0; i < ENTRIES; ++i) {
         fn[i] = PyLong_AsVoidPtr(a[5 + i]);
         if (!fn[i])
             return PyErr_Occurred() ? NULL : PyErr_Format(PyExc_ValueError, "setup: a null entry point");
@@ -333,15 +385,17 @@ static PyObject *py_setup(PyObject *self, PyObject *const *a, Py_ssize_t n)
         Py_XSETREF(*keep[i], a[i]);
     }
     call_rope = (rope_fn)fn[0];
-    call_append = (append_fn)fn[1];
-    call_decode = (decode_fn)fn[2];
-    call_evict = (evict_fn)fn[3];
+    call_norm_rope = (norm_rope_fn)fn[1];
+    call_append = (append_fn)fn[2];
+    call_decode = (decode_fn)fn[3];
+    call_evict = (evict_fn)fn[4];
     Py_RETURN_NONE;
 }
 
 static PyMethodDef methods[] = {
     {"setup", (PyCFunction)(void (*)(void))py_setup, METH_FASTCALL, NULL},
     {"rope", (PyCFunction)(void (*)(void))py_rope, METH_FASTCALL, NULL},
+    {"norm_rope", (PyCFunction)(void (*)(void))py_norm_rope, METH_FASTCALL, NULL},
     {"append", (PyCFunction)(void (*)(void))py_append, METH_FASTCALL, NULL},
     {"decode", (PyCFunction)(void (*)(void))py_decode, METH_FASTCALL, NULL},
     {"evict", (PyCFunction)(void (*)(void))py_evict, METH_FASTCALL, NULL},

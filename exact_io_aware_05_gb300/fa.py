@@ -82,12 +82,24 @@ class _KVCache(ctypes.Structure):
                [(n, _i) for n in ("B", "Hkv", "d", "page_size", "num_pages", "max_pages", "dtype")]
 
 
+class _HeadNorm(ctypes.Structure):
+    _fields_ = [("q_weight", _vp), ("k_weight", _vp), ("d", _i), ("dtype", _i), ("eps", _f)]
+
+
 _lib.fa_rope_spec_init.argtypes = [_vp, _i, _i, _i, _vp, _vp, _i]
 _lib.fa_rope_spec_init.restype = _i
 _lib.fa_rope.argtypes = [_vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _vp]
 _lib.fa_rope.restype = _i
+_lib.fa_norm_rope.argtypes = [_vp, _vp, _i, _vp, _vp, _vp, _i, _i, _i, _vp]
+_lib.fa_norm_rope.restype = _i
+_lib.fa_norm_rope_bwd_workspace_bytes.argtypes = [_i]
+_lib.fa_norm_rope_bwd_workspace_bytes.restype = _sz
+_lib.fa_norm_rope_bwd.argtypes = [_vp, _vp, _vp, _i, _vp, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _sz, _vp]
+_lib.fa_norm_rope_bwd.restype = _i
 _lib.fa_cache_append.argtypes = [_vp] * 8 + [_i, _vp]
 _lib.fa_cache_append.restype = _i
+_lib.fa_cache_append_norm.argtypes = [_vp] * 9 + [_i, _vp]
+_lib.fa_cache_append_norm.restype = _i
 _lib.fa_decode_paged_workspace_bytes.argtypes = [_i] * 8
 _lib.fa_decode_paged_workspace_bytes.restype = _sz
 _lib.fa_decode_paged.argtypes = [_vp, _vp, _vp, _vp, _i, _i, _i, _f, _i, _vp, _sz, _vp]
@@ -473,7 +485,7 @@ _current_device = torch._C._cuda_getDevice
 
 class _Without:
     """Stands for _fa_py where it is missing: no call passes its checks."""
-    rope = append = decode = evict = staticmethod(lambda *args: None)
+    rope = norm_rope = append = decode = evict = staticmethod(lambda *args: None)
 
 
 if _fa_py is None:
@@ -481,7 +493,7 @@ if _fa_py is None:
 else:
     _fast = _fa_py
     _fa_py.setup(torch.bfloat16, torch.float32, torch.int32, _current_stream, _current_device,
-                 *(ctypes.cast(f, _vp).value for f in (_lib.fa_rope, _lib.fa_cache_append, _lib.fa_decode_paged,
+                 *(ctypes.cast(f, _vp).value for f in (_lib.fa_rope, _lib.fa_norm_rope, _lib.fa_cache_append_norm, _lib.fa_decode_paged,
                                                        _lib.fa_cache_evict)))
 
 
@@ -544,7 +556,9 @@ def _heads(t: torch.Tensor, name: str, dtype, shape, index: int) -> tuple:
     return t.data_ptr(), sb if B > 1 else 0, sh if H > 1 else 0, st if T > 1 else 0, H, 0
 
 
-def _rope(fn, q, q_out, positions, spec, k, k_out, inverse, stream):
+def _rope_heads(q, q_out, positions, spec, k, k_out) -> tuple:
+    """Checks of the rotary calls: the number of tensors, their fa_heads and those of the outputs, B, T, the
+    element type and the device's index."""
     shape = q.shape
     if len(shape) != 4 or (k is None) != (k_out is None):
         raise ValueError("q, k must be [B, H, T, d], with an output for each")
@@ -567,8 +581,12 @@ def _rope(fn, q, q_out, positions, spec, k, k_out, inverse, stream):
         n = 2
         x = _HEADS2.pack(*x, *_heads(k, "k", dt, shape, index))
         y = _HEADS2.pack(*y, *_heads(k_out, "k_out", dt, shape, index))
-    _launch(fn, _lib.fa_rope, index, stream, x, y, n, positions.data_ptr(), spec._ref, B, T,
-            FA_BF16 if dt is torch.bfloat16 else FA_F32, inverse)
+    return n, x, y, B, T, FA_BF16 if dt is torch.bfloat16 else FA_F32, index
+
+
+def _rope(fn, q, q_out, positions, spec, k, k_out, inverse, stream):
+    n, x, y, B, T, dt, index = _rope_heads(q, q_out, positions, spec, k, k_out)
+    _launch(fn, _lib.fa_rope, index, stream, x, y, n, positions.data_ptr(), spec._ref, B, T, dt, inverse)
 
 
 def fa_rope(q, q_out, positions, spec: RopeSpec, k=None, k_out=None, stream=None) -> None:
@@ -600,6 +618,127 @@ def rope_backward(dq_out, dk_out, positions, spec: RopeSpec, stream=None):
     dq, dk = _empties(stream, dq_out.device, (dq_out.shape, dq_out.dtype), (dk_out.shape, dk_out.dtype))
     fa_rope_bwd(dq_out, dq, positions, spec, dk_out, dk, stream)
     return dq, dk
+
+
+# ---------------------------------------------------------------- norms of heads, with the rotation
+class HeadNorm:
+    """Norms of query and key heads of width d (fa_head_norm in include/fa.h): a row x becomes
+    weight x / sqrt(mean(x^2) + eps).  q_weight and k_weight: [d] bf16 or float32, both of one type, or None
+    (ones).  Checks its tensors once and keeps them; their contents are read at each call, so a weight that an
+    optimizer changes in place is taken as it is.  A tensor assigned to q_weight or k_weight is checked
+    and takes the place of the one before (a captured graph keeps the one that it was captured with)."""
+
+    _WEIGHTS = ("q_weight", "k_weight")
+
+    def __init__(self, d: int, q_weight=None, k_weight=None, eps: float = 1e-6):
+        if d not in (64, 128, 256):
+            raise ValueError(f"d: expected 64, 128 or 256, got {d}")
+        if not 0.0 < float(eps) < float("inf"):
+            raise ValueError(f"eps: expected a finite value above 0, got {eps}")
+        self.__dict__.update(d=int(d), eps=float(eps), q_weight=None, k_weight=None, _index=-1,
+                             _c=_HeadNorm(d=int(d), dtype=FA_BF16, eps=float(eps)))
+        if self._c.eps == 0.0:
+            raise ValueError(f"eps: {eps} is 0 in fp32")
+        self.__dict__["_ref"] = ctypes.addressof(self._c)
+        self.q_weight, self.k_weight = q_weight, k_weight
+
+    def __setattr__(self, name, t):
+        if name not in self._WEIGHTS:
+            raise AttributeError(f"{name} of a HeadNorm is fixed")
+        other = self.__dict__["k_weight" if name == "q_weight" else "q_weight"]
+        if t is not None:
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{name}: expected a tensor, got {type(t).__name__}")
+            if t.dtype not in (torch.bfloat16, torch.float32):
+                raise TypeError(f"{name}: expected torch.bfloat16 or torch.float32, got {t.dtype}")
+            _need(t, name, t.dtype if other is None else other.dtype, (self.d,), t.device if other is None else other.device)
+        there = other if t is None else t
+        self.__dict__[name] = t
+        self.__dict__["_index"] = -1 if there is None else there.get_device()
+        setattr(self._c, name, _ptr(t))
+        self._c.dtype = FA_F32 if there is not None and there.dtype is torch.float32 else FA_BF16
+
+    def __delattr__(self, name):
+        raise AttributeError(f"{name} of a HeadNorm cannot be deleted")
+
+    def __reduce__(self):   # copies and pickles are handles of their own, with a structure of their own
+        return type(self), (self.d, self.q_weight, self.k_weight, self.eps)
+
+
+def _need_norm(norm, spec, index) -> None:
+    if not isinstance(norm, HeadNorm):
+        raise TypeError(f"norm: expected a HeadNorm, got {type(norm).__name__}")
+    if norm.d != spec.d:
+        raise ValueError(f"norm: expected head width {spec.d}, got {norm.d}")
+    if (norm.q_weight is not None or norm.k_weight is not None) and norm._index != index:
+        raise ValueError("norm: expected weights on the others' device")
+
+
+def fa_norm_rope(q, q_out, positions, spec: RopeSpec, norm: HeadNorm, k=None, k_out=None, stream=None) -> None:
+    """q_out = q [B, Hq, T, d] (and k_out = k [B, Hk, T, d]) normed by head and then rotated as by fa_rope, in
+    one pass; tensors as there.  An output may be its input where no gradient is wanted."""
+    st = _fast.norm_rope(spec._ref, norm._ref, norm._index, q, q_out, k, k_out, positions, stream)
+    if st != FA_OK:
+        _again(st, "fa_norm_rope", _norm_rope, q, q_out, positions, spec, norm, k, k_out, stream)
+
+
+def _norm_rope(q, q_out, positions, spec, norm, k, k_out, stream) -> None:
+    n, x, y, B, T, dt, index = _rope_heads(q, q_out, positions, spec, k, k_out)
+    _need_norm(norm, spec, index)
+    _launch("fa_norm_rope", _lib.fa_norm_rope, index, stream, x, y, n, norm._ref, positions.data_ptr(), spec._ref, B, T, dt)
+
+
+def fa_norm_rope_bwd_workspace_bytes(d: int) -> int:
+    return int(_lib.fa_norm_rope_bwd_workspace_bytes(d))
+
+
+def fa_norm_rope_bwd(dq_out, q, dq, positions, spec: RopeSpec, norm: HeadNorm, dk_out=None, k=None, dk=None, dq_weight=None,
+                     dk_weight=None, workspace: torch.Tensor = None, stream=None) -> None:
+    """Backward of fa_norm_rope: dq from dq_out, the gradient of q_out, and q (dk from dk_out and k); dq_weight
+    and dk_weight, float32 [d], if given, are set to the gradients of the weights, for which a workspace of
+    fa_norm_rope_bwd_workspace_bytes(d) bytes is needed.  dq may be dq_out."""
+    if (k is None) != (dk_out is None):
+        raise ValueError("k, dk_out and dk come together")
+    n, g, dx, B, T, dt, index = _rope_heads(dq_out, dq, positions, spec, dk_out, dk)
+    _need_norm(norm, spec, index)
+    x = _heads(q, "q", dq_out.dtype, dq_out.shape, index)
+    x = _HEADS.pack(*x) if k is None else _HEADS2.pack(*x, *_heads(k, "k", dq_out.dtype, dk_out.shape, index))
+    for name, t, w, there in (("dq_weight", dq_weight, norm.q_weight, True), ("dk_weight", dk_weight, norm.k_weight, k is not None)):
+        if t is not None:
+            if w is None or not there:
+                raise ValueError(f"{name}: there is no {name[1:]}")
+            _need(t, name, torch.float32, (spec.d,), dq_out.device)
+    ws = nbytes = 0
+    if dq_weight is not None or dk_weight is not None:
+        if workspace is None or workspace.get_device() != index or not workspace.is_contiguous():
+            raise ValueError("workspace: a contiguous tensor on the same device")
+        ws, nbytes = workspace.data_ptr(), workspace.nbytes
+    _launch("fa_norm_rope_bwd", _lib.fa_norm_rope_bwd, index, stream, g, x, dx, n, norm._ref, positions.data_ptr(), spec._ref, B, T, dt,
+            _ptr(dq_weight), _ptr(dk_weight), ws, nbytes)
+
+
+def norm_rope_forward(q, k, positions, spec: RopeSpec, norm: HeadNorm, stream=None):
+    """Allocates contiguous outputs and runs fa_norm_rope on q and k: what fa_fwd takes."""
+    q_out, k_out = _empties(stream, q.device, (q.shape, q.dtype), (k.shape, k.dtype))
+    fa_norm_rope(q, q_out, positions, spec, norm, k, k_out, stream)
+    return q_out, k_out
+
+
+def norm_rope_backward(dq_out, dk_out, q, k, positions, spec: RopeSpec, norm: HeadNorm, workspace=None, stream=None):
+    """Allocates and returns the gradients of q, k, q_weight and k_weight (None where the norm has no
+    weight) from those of norm_rope_forward's outputs."""
+    f32 = torch.float32
+    specs = [(dq_out.shape, dq_out.dtype), (dk_out.shape, dk_out.dtype)]
+    specs += [((spec.d,), f32) for w in (norm.q_weight, norm.k_weight) if w is not None]
+    if workspace is None:
+        specs.append(((fa_norm_rope_bwd_workspace_bytes(spec.d),), torch.uint8))
+    dq, dk, *rest = _empties(stream, dq_out.device, *specs)
+    if workspace is None:
+        workspace = rest.pop()
+    dqw = None if norm.q_weight is None else rest.pop(0)
+    dkw = None if norm.k_weight is None else rest.pop(0)
+    fa_norm_rope_bwd(dq_out, q, dq, positions, spec, norm, dk_out, k, dk, dqw, dkw, workspace, stream)
+    return dq, dk, dqw, dkw
 
 
 # ---------------------------------------------------------------- paged key/value cache
@@ -679,17 +818,18 @@ def alloc_kv_cache(B: int, Hkv: int, d: int, max_len: int, page_size: int = 16, 
 
 
 def fa_cache_append(cache: KVCache, k, v, positions=None, spec: RopeSpec | None = None, q=None, q_out=None,
-                    new_lens=None, stream=None) -> None:
+                    new_lens=None, stream=None, norm: HeadNorm | None = None) -> None:
     """Writes the first new_lens[b] (default: all) of the T rows of k and v [B, Hkv, T, d] as the
     last entries of sequence b; cache.lens (and seen) count them already.  With a spec, k is
-    rotated by positions [n_axes, B, T] on the way, and q [B, Hq, T, d] into q_out."""
+    rotated by positions [n_axes, B, T] on the way, and q [B, Hq, T, d] into q_out; with a norm
+    too (it needs a spec), the heads of q and k are normed before they are rotated."""
     st = _fast.append(cache._ref, cache._index, k, v, positions, None if spec is None else spec._ref, q, q_out, new_lens,
-                       stream)
+                       stream, None if norm is None else norm._ref, -1 if norm is None else norm._index)
     if st != FA_OK:
-        _again(st, "fa_cache_append", _append, cache, k, v, positions, spec, q, q_out, new_lens, stream)
+        _again(st, "fa_cache_append", _append, cache, k, v, positions, spec, q, q_out, new_lens, stream, norm)
 
 
-def _append(cache, k, v, positions, spec, q, q_out, new_lens, stream) -> None:
+def _append(cache, k, v, positions, spec, q, q_out, new_lens, stream, norm=None) -> None:
     index, B, d = cache._index, cache.B, cache.d
     if k.dim() != 4 or (q is not None and q.dim() != 4):
         raise ValueError("k, v, q must be [B, H, T, d]")
@@ -699,6 +839,10 @@ def _append(cache, k, v, positions, spec, q, q_out, new_lens, stream) -> None:
         raise ValueError("q and q_out come together")
     if q is not None and spec is None:
         raise ValueError("q is rotated: it needs a spec and positions")
+    if norm is not None:
+        if spec is None:
+            raise ValueError("norm: needs a spec and positions")
+        _need_norm(norm, spec, index)
     T = k.shape[2]
     shape = (B, cache.Hkv, T, d)
     bf16 = torch.bfloat16
@@ -716,7 +860,8 @@ def _append(cache, k, v, positions, spec, q, q_out, new_lens, stream) -> None:
     if new_lens is not None:
         _need(new_lens, "new_lens", torch.int32, (B,), cache.device)
         new = new_lens.data_ptr()
-    _launch("fa_cache_append", _lib.fa_cache_append, index, stream, cache._ref, kh, vh, qh, oh, pos, ref, new, T)
+    _launch("fa_cache_append", _lib.fa_cache_append_norm, index, stream, cache._ref, kh, vh, qh, oh, pos, ref,
+            None if norm is None else norm._ref, new, T)
 
 
 def fa_decode_paged_workspace_bytes(cache: KVCache, Hq: int, Tq: int = 1, accumulate: bool = False) -> int:

@@ -230,6 +230,39 @@ int fa_rope(const fa_heads *x, const fa_heads *y, int n, const int *positions, c
             int B, int T, int dtype, int inverse, fa_stream_t stream);
 
 /*
+ * Norms of query and key heads with the rotation in the same pass.  A row x of d features becomes the
+ * rotation of w x / sqrt(mean(x^2) + eps): x[0] (such as q) with weights q_weight, x[1] (such as k)
+ * with k_weight, [d] each for all heads, bf16 or f32 (dtype), 16-byte aligned; NULL: ones.  eps finite
+ * and > 0.  The arithmetic is fp32, rounded once; the squares' sum must not leave fp32.
+ */
+typedef struct {
+    const void *q_weight, *k_weight;
+    int d, dtype;
+    float eps;
+} fa_head_norm;
+
+/*
+ * y = x normed and rotated: tensors, positions, spec and errors as in fa_rope (norm->d == spec->d; no
+ * output shares memory with the weights).
+ */
+int fa_norm_rope(const fa_heads *x, const fa_heads *y, int n, const fa_head_norm *norm, const int *positions,
+                 const fa_rope_spec *spec, int B, int T, int dtype, fa_stream_t stream);
+
+/*
+ * Backward of fa_norm_rope: dx[i], the gradient of x[i], from dy[i], the gradient of y[i], and x[i]
+ * itself (not y[i]: where fa_norm_rope's output took its input's place there is no backward).  dx[i]
+ * may be dy[i]; otherwise no output shares memory with an input.  dq_weight and dk_weight: f32 [d],
+ * 16-byte aligned, the gradients of the weights (of either type), summed in fp32 over all rows in a fixed order;
+ * each may be NULL, and is where its weight is.  They are written, not added to: zeros where there are
+ * no rows.  workspace: fa_norm_rope_bwd_workspace_bytes(d) bytes, 256-byte aligned, contents on entry
+ * ignored, not shared by calls that may overlap in time; not needed without gradients of weights.
+ */
+size_t fa_norm_rope_bwd_workspace_bytes(int d);   /* 0: unsupported width */
+int fa_norm_rope_bwd(const fa_heads *dy, const fa_heads *x, const fa_heads *dx, int n, const fa_head_norm *norm,
+                     const int *positions, const fa_rope_spec *spec, int B, int T, int dtype, float *dq_weight,
+                     float *dk_weight, void *workspace, size_t workspace_bytes, fa_stream_t stream);
+
+/*
  * A paged cache of B sequences, all pointers to device memory:
  *   k, v         [num_pages][Hkv][page_size][d], bf16 (FA_BF16) or e4m3 codes
  *                (FA_E4M3)
@@ -284,6 +317,15 @@ typedef struct {
 int fa_cache_append(const fa_kv_cache *cache, const fa_heads *k, const fa_heads *v, const fa_heads *q,
                     const fa_heads *q_out, const int *positions, const fa_rope_spec *spec,
                     const int *new_lens, int T, fa_stream_t stream);
+
+/*
+ * fa_cache_append with the rows of q and k normed before they are rotated (fa_head_norm above; v is
+ * written as it is).  norm needs a spec with norm->d == spec->d; NULL: fa_cache_append.  The weights lie
+ * outside of the cache and of q_out.
+ */
+int fa_cache_append_norm(const fa_kv_cache *cache, const fa_heads *k, const fa_heads *v, const fa_heads *q,
+                         const fa_heads *q_out, const int *positions, const fa_rope_spec *spec, const fa_head_norm *norm,
+                         const int *new_lens, int T, fa_stream_t stream);
 
 /*
  * Attention of the last Tq (1 to 16) tokens of every sequence over the cache:
