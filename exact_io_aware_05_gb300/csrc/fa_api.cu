@@ -299,7 +299,7 @@ int bwd_check_args(const void *q, const void *k, const void *v, const void *o, c
     int st = check_sizes(B, H, Tq, Tk, d, 0, scale);
     if (st != OK)
         return st;
-    if (mask.left < -1 || mask.right < -1 || mask.per_head < 0 || mask.per_head > 1)
+    if (mask.left < -1 || mask.right < -1 || mask.per_head < 0 || mask.per_head > 1 || mask.sinks < 0)
         return ERR_INVALID_ARG;
     if (d == 256)
         return ERR_UNSUPPORTED;
@@ -372,6 +372,24 @@ int fa_fwd_masked(const void *q, const void *k, const void *v, void *o, float *l
     if (Tk == 0)
         return fa::fill_empty_launch(o, lse, (size_t)BH * Tq, d, 2, s);
     const fa::MaskSpec m{window_left, window_right, block_mask, mask_per_head};
+    return fa::fwd_bf16_launch(q, k, v, o, lse, BH, Tq, Tk, d, m, scale, s);
+}
+
+int fa_fwd_sinks(const void *q, const void *k, const void *v, void *o, float *lse, int B, int H, int Tq, int Tk, int d,
+                 int window_left, int n_sinks, float scale, fa_stream_t stream)
+{
+    if (window_left < -1 || n_sinks < 0)
+        return FA_ERR_INVALID_ARG;
+    int st = fa::check_fwd(q, k, v, o, lse, B, H, Tq, Tk, d, 0, scale, 2);
+    if (st != fa::OK)
+        return st;
+    const int BH = B * H;
+    if ((size_t)BH * Tq == 0)
+        return FA_OK;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (Tk == 0)
+        return fa::fill_empty_launch(o, lse, (size_t)BH * Tq, d, 2, s);
+    const fa::MaskSpec m{window_left, 0, nullptr, 0, n_sinks};
     return fa::fwd_bf16_launch(q, k, v, o, lse, BH, Tq, Tk, d, m, scale, s);
 }
 
@@ -519,7 +537,7 @@ static int bwd_common(const void *q, const void *k, const void *v, const void *o
     if (bh == 0 || (Tq == 0 && Tk == 0))
         return FA_OK;
     const size_t nq = bh * Tq * d * 2, nk = bh * Tk * d * 2, nl = bh * Tq * sizeof(float);
-    const size_t need = fa::bwd_workspace_bytes(bh, Tq, d);
+    const size_t base = fa::bwd_workspace_bytes(bh, Tq, d), need = base + fa::bwd_sink_bytes(bh, Tq, Tk, d, mask);
     if (need > 0 && (!workspace || workspace_bytes < need))
         return FA_ERR_INVALID_ARG;
     if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
@@ -545,7 +563,8 @@ static int bwd_common(const void *q, const void *k, const void *v, const void *o
     if (st != fa::OK)
         return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const fa::BwdWorkspace ws = fa::bwd_workspace_carve(workspace, (int)bh, Tq, d);
+    fa::BwdWorkspace ws = fa::bwd_workspace_carve(workspace, (int)bh, Tq, d);
+    ws.sink_part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + base);
     return fa::bwd_launch(q, k, v, o, lse, dO, dq, dk, dv, (int)bh, Tq, Tk, d, mask, scale, ws, stages, s);
 }
 
@@ -569,6 +588,25 @@ int fa_bwd_masked(const void *q, const void *k, const void *v, const void *o, co
     if (deterministic < 0 || deterministic > 1)
         return FA_ERR_INVALID_ARG;
     const fa::MaskSpec m{window_left, window_right, block_mask, mask_per_head};
+    return bwd_common(q, k, v, o, lse, dO, dq, dk, dv, B, H, Tq, Tk, d, m, scale, workspace, workspace_bytes,
+                      7 | (deterministic ? fa::kBwdDeterministic : 0), stream);
+}
+
+size_t fa_bwd_sinks_workspace_bytes(int B, int H, int Tq, int Tk, int d, int window_left, int n_sinks)
+{
+    const size_t base = fa_bwd_workspace_bytes(B, H, Tq, Tk, d);
+    if (base == 0 || window_left < -1 || n_sinks < 0)
+        return 0;
+    return base + fa::bwd_sink_bytes((size_t)B * H, Tq, Tk, d, fa::MaskSpec{window_left, 0, nullptr, 0, n_sinks});
+}
+
+int fa_bwd_sinks(const void *q, const void *k, const void *v, const void *o, const float *lse, const void *dO, void *dq,
+                 void *dk, void *dv, int B, int H, int Tq, int Tk, int d, int window_left, int n_sinks, int deterministic,
+                 float scale, void *workspace, size_t workspace_bytes, fa_stream_t stream)
+{
+    if (deterministic < 0 || deterministic > 1)
+        return FA_ERR_INVALID_ARG;
+    const fa::MaskSpec m{window_left, 0, nullptr, 0, n_sinks};
     return bwd_common(q, k, v, o, lse, dO, dq, dk, dv, B, H, Tq, Tk, d, m, scale, workspace, workspace_bytes,
                       7 | (deterministic ? fa::kBwdDeterministic : 0), stream);
 }

@@ -33,6 +33,8 @@
 //     read dP^T from them; for d = 64, dQ = dS K_j has two buffers of its own;
 //   * every MMA that overwrites a tensor-memory region waits for the MMA (or
 //     the drain) that last read it, and every wait is bounded.
+#include <algorithm>
+
 #include "fa_common.cuh"
 #include "fa_internal.h"
 
@@ -118,7 +120,16 @@ struct BwdArgs {
     int left, right;
     const uint8_t *bmask;
     int bm_per_head, nqbm, nkbm;
+    // sinks instance: the left bound does not hold for keys below sinks.  Their nsb key blocks see every
+    // query block behind them, the others a window's: with parts > 1 each of them is so many units, which
+    // leave fp32 dV and dK (x scale) in sink_part, [head][sink block][part][dV, dK][128][D]
+    int sinks, nsb, parts;
+    float *sink_part;
 };
+
+// Instances by mask: causal or none; a window and/or a block mask; a window whose left bound spares the first
+// keys (sinks).
+enum : int { kPlain = 0, kWindow = 1, kSinks = 2 };
 
 // Deterministic mode.  dQ_i is a sum over key blocks whose terms arrive in any
 // order; held as int32 fixed point their sum is the same in every order.  The
@@ -142,6 +153,7 @@ struct Unit {
     int i0, nq;    // first query block, number of query blocks visited
     int i1;        // last query block visited
     const uint8_t *bm;   // masked instance: the key block's mask column (stride nkbm), or null
+    int part;      // sinks instance: which part of a split key block, or -1: the unit is all of it
 };
 
 // The first query block at or after i that unit x visits (i1 + 1 if none).
@@ -152,11 +164,12 @@ __device__ __forceinline__ int unit_next(const Unit &x, int i, int nkbm)
     return i;
 }
 
-// MASKED = false: causal or not, every unit visits a contiguous run of query blocks.
-template <bool MASKED>
+// kPlain: causal or not, every unit visits a contiguous run of query blocks.
+template <int MASK>
 __device__ __forceinline__ Unit make_unit(int u, const BwdArgs &a)
 {
-    const int per_group = a.group * a.nkb;
+    constexpr bool MASKED = MASK != kPlain;
+    const int per_group = a.group * (MASK == kSinks ? a.nkb + a.nsb * (a.parts - 1) : a.nkb);
     const int g = u / per_group;
     const int w = u - g * per_group;
     const int heads_here = min(a.group, a.BH - g * a.group);
@@ -164,6 +177,13 @@ __device__ __forceinline__ Unit make_unit(int u, const BwdArgs &a)
     Unit x;
     x.bh = g * a.group + (w - lvl * heads_here);
     x.j = lvl;
+    x.part = -1;
+    if constexpr (MASK == kSinks) {
+        const int split = a.nsb * a.parts;   // the sinks' parts come first
+        x.j = lvl < split ? lvl / a.parts : lvl - a.nsb * (a.parts - 1);
+        if (lvl < split && a.parts > 1)
+            x.part = lvl - x.j * a.parts;
+    }
     const int nqb = (a.Tq + BQ - 1) / BQ;
     int first_row = 0;
     if (a.causal) {
@@ -182,7 +202,7 @@ __device__ __forceinline__ Unit make_unit(int u, const BwdArgs &a)
         const long off = (long)a.Tk - a.Tq;
         const long kf = (long)x.j * BK, kl = min((long)a.Tk - 1, kf + BK - 1);
         const long rlo = a.right >= 0 ? max(0L, kf - off - a.right) : 0L;
-        const long rhi = a.left >= 0 ? min((long)a.Tq - 1, kl - off + a.left) : (long)a.Tq - 1;
+        const long rhi = a.left >= 0 && !(MASK == kSinks && kf < a.sinks) ? min((long)a.Tq - 1, kl - off + a.left) : (long)a.Tq - 1;
         if (rlo > rhi) {
             x.nq = 0;
             x.i1 = x.i0 - 1;
@@ -203,6 +223,14 @@ __device__ __forceinline__ Unit make_unit(int u, const BwdArgs &a)
             x.i1 = last;
         } else {
             x.nq = x.i1 - x.i0 + 1;
+        }
+        if constexpr (MASK == kSinks) {
+            if (x.part >= 0) {   // an equal share of the query blocks (none, where there are fewer than parts)
+                const int from = (int)((long)x.nq * x.part / a.parts), to = (int)((long)x.nq * (x.part + 1) / a.parts);
+                x.i1 = x.i0 + to - 1;
+                x.i0 += from;
+                x.nq = to - from;
+            }
         }
     }
     return x;
@@ -261,7 +289,7 @@ __device__ __forceinline__ void softmax_p32(uint32_t (&sv)[32], const float4 *nl
     }
 }
 
-template <int D, bool MASKED>
+template <int D, int MASK>
 __global__ void __launch_bounds__(512, 1)
     bwd_main_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
@@ -269,6 +297,7 @@ __global__ void __launch_bounds__(512, 1)
                     const __grid_constant__ CUtensorMap tm_acc, const BwdArgs a)
 {
     using L = BwdLayout<D>;
+    constexpr bool MASKED = MASK != kPlain;
     constexpr int NST = L::NST;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -335,7 +364,7 @@ __global__ void __launch_bounds__(512, 1)
             uint32_t n_kv = 0, n_st = 0, n_do = 0;   // K/V, stage (Q, and dO unless BULK) and BULK dO loads issued
             bool ok = true;
             for (int pass = 0, u = snake_unit<!MASKED>(0); u < a.units && ok; u = snake_unit<!MASKED>(++pass)) {
-                const Unit x = make_unit<MASKED>(u, a);
+                const Unit x = make_unit<MASK>(u, a);
                 if (x.nq == 0)
                     continue;
                 if (n_kv > 0 && !mbar_wait<true>(bar(L::B_KVEMPTY), (n_kv - 1) & 1, ctx, SITE_P_KVEMPTY))
@@ -427,7 +456,7 @@ __global__ void __launch_bounds__(512, 1)
                 return true;
             };
             for (int pass = 0, u = snake_unit<!MASKED>(0); u < a.units && ok; u = snake_unit<!MASKED>(++pass)) {
-                const Unit x = make_unit<MASKED>(u, a);
+                const Unit x = make_unit<MASK>(u, a);
                 if (x.nq == 0)
                     continue;
                 if (!wait(bar(L::B_KVFULL), nu & 1, SITE_M_KVFULL) || !issue_s(g))
@@ -537,7 +566,7 @@ __global__ void __launch_bounds__(512, 1)
             uint32_t g = 0;
             bool ok = true;
             for (int pass = 0, u = snake_unit<!MASKED>(0); u < a.units && ok; u = snake_unit<!MASKED>(++pass)) {
-                const Unit x = make_unit<MASKED>(u, a);
+                const Unit x = make_unit<MASK>(u, a);
                 for (int i = 0, qi = x.i0; i < x.nq; ++i, ++g, qi = MASKED ? unit_next(x, qi + 1, a.nkbm) : qi + 1) {
                     const size_t roff = (size_t)x.bh * a.Tq_pad + (size_t)qi * BQ;
                     if (g > 0 && !mbar_wait<true>(bar(L::B_PFULL), (g - 1) & 1, ctx, SITE_L_PFULL)) {
@@ -571,7 +600,7 @@ __global__ void __launch_bounds__(512, 1)
         uint32_t g = 0;
         bool ok = true;
         for (int pass = 0, u = snake_unit<!MASKED>(0); u < a.units && ok; u = snake_unit<!MASKED>(++pass)) {
-            const Unit x = make_unit<MASKED>(u, a);
+            const Unit x = make_unit<MASK>(u, a);
             const int l = x.j * BK + key_in_blk;         // this thread's key
             for (int i = 0, qi = x.i0; i < x.nq; ++i, ++g, qi = MASKED ? unit_next(x, qi + 1, a.nkbm) : qi + 1) {
                 const int qb = qi * BQ + half * 64;   // first query row of this half
@@ -585,7 +614,7 @@ __global__ void __launch_bounds__(512, 1)
                     const long off = (long)a.Tk - a.Tq;
                     if (a.right >= 0)
                         qmin = (int)max(0L, min(64L, (long)l - off - a.right - qb));
-                    if (a.left >= 0)
+                    if (a.left >= 0 && !(MASK == kSinks && l < a.sinks))
                         qmax = (int)max(0L, min(64L, (long)l - off + a.left - qb + 1));
                 }
                 const bool mask = __any_sync(0xffffffffu, qmin > 0 || qmax < 64);
@@ -673,9 +702,19 @@ __global__ void __launch_bounds__(512, 1)
         uint32_t stg_n = 0;                          // dQ boxes this warp has staged (d = 128)
         bool ok = true;
         for (int pass = 0, u = snake_unit<!MASKED>(0); u < a.units && ok; u = snake_unit<!MASKED>(++pass)) {
-            const Unit x = make_unit<MASKED>(u, a);
+            const Unit x = make_unit<MASK>(u, a);
             const int l = x.j * BK + row;
             const size_t krow = (size_t)x.bh * a.Tk + l;
+            // a part's rows of dV, and of dK 128 rows on
+            float *part = MASK == kSinks && x.part >= 0
+                              ? a.sink_part + (((((size_t)x.bh * a.nsb + x.j) * a.parts + x.part) * 2) * BK + row) * D
+                              : nullptr;
+            if (MASK == kSinks && x.nq == 0 && x.part >= 0) {
+                for (int e = 0; e < D / 4; ++e)
+                    reinterpret_cast<float4 *>(part)[e] = reinterpret_cast<float4 *>(part + (size_t)BK * D)[e] =
+                        make_float4(0.f, 0.f, 0.f, 0.f);
+                continue;
+            }
             if (x.nq == 0) {
                 if (l < a.Tk) {
                     uint4 *pk_ = reinterpret_cast<uint4 *>(a.dk + krow * D);
@@ -798,6 +837,25 @@ __global__ void __launch_bounds__(512, 1)
             if (!kv_ok)
                 break;
             tc_fence_after();
+            if (MASK == kSinks && x.part >= 0) {   // fp32, for the sum over the parts
+#pragma unroll
+                for (int w = 0; w < 2; ++w)
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t v[32];
+                        tmem_ld_x32(lane_base + (w ? L::T_DK : L::T_DV) + c * 32, v);
+                        const float f = w ? a.scale : 1.f;
+                        float4 *dst = reinterpret_cast<float4 *>(part + (size_t)w * BK * D + c * 32);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            dst[e] = make_float4(__uint_as_float(v[4 * e]) * f, __uint_as_float(v[4 * e + 1]) * f,
+                                                 __uint_as_float(v[4 * e + 2]) * f, __uint_as_float(v[4 * e + 3]) * f);
+                    }
+                tc_fence_before();
+                mbar_arrive(bar(L::B_DKVEMPTY));
+                ++nu;
+                continue;
+            }
             // dV, then dK (x c): each warp packs its 32 key rows (the TMEM lanes it reads) to bf16
             // into its own 8 KB of shared memory (d = 128: a quarter of the two staging buffers,
             // free once the last dQ chunk has been read; d = 64: the warp's own buffer) as boxes of
@@ -1041,6 +1099,30 @@ __global__ void __launch_bounds__(256) bwd_dq_kernel(const float *__restrict__ d
     }
 }
 
+// dV and dK of the key blocks that were split: the sum of their parts, in order.  A thread has four features.
+template <int D>
+__global__ void __launch_bounds__(256) bwd_sink_join_kernel(const float *__restrict__ part, __nv_bfloat16 *__restrict__ dv,
+                                                            __nv_bfloat16 *__restrict__ dk, int BH, int Tk, int nsb, int parts)
+{
+    const size_t i = blockIdx.x * (size_t)blockDim.x + threadIdx.x, n = (size_t)BH * nsb * 2 * BK * (D / 4);
+    if (i >= n)
+        return;
+    const int col = (int)(i % (D / 4)) * 4, row = (int)(i / (D / 4) % BK), w = (int)(i / (D / 4) / BK % 2);
+    const size_t blk = i / (D / 4) / BK / 2;   // head and sink block
+    const int l = (int)(blk % nsb) * BK + row;
+    if (l >= Tk)
+        return;
+    const float *p = part + ((blk * parts * 2 + w) * BK + row) * D + col;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = 0; k < parts; ++k) {
+        const float4 y = *reinterpret_cast<const float4 *>(p + (size_t)k * 2 * BK * D);
+        x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+    }
+    *reinterpret_cast<uint2 *>((w ? dk : dv) + ((blk / nsb) * Tk + l) * D + col) =
+        make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+}
+
 template <int D>
 int launch_bwd(const void *q, const void *k, const void *v, const void *o, const float *lse, const void *dO,
                void *dq, void *dk, void *dv, int BH, int Tq, int Tk, const MaskSpec &mask, float scale,
@@ -1121,7 +1203,15 @@ int launch_bwd(const void *q, const void *k, const void *v, const void *o, const
         a.scale = scale;
         a.scale_log2 = scale * 1.4426950408889634f;
         a.nkb = (Tk + BK - 1) / BK;
-        a.units = BH * a.nkb;
+        a.sinks = mask.sinks < Tk ? mask.sinks : Tk;
+        const bool sinks = mask.left >= 0 && a.sinks > 0;
+        a.nsb = sinks ? (a.sinks + BK - 1) / BK : 0;
+        a.parts = sinks ? bwd_sink_parts(BH, Tq, Tk, mask) : 1;
+        a.sink_part = ws.sink_part;
+        const long long units = (long long)BH * (a.nkb + (long long)a.nsb * (a.parts - 1));
+        if (units > 0x7fffffffll)
+            return ERR_UNSUPPORTED;
+        a.units = (int)units;
         // heads per group: Q, dO, K, V of the group within ~80 MB of L2, a whole number of
         // passes where possible (B8 H32 N4096 d128: 19 heads; measured faster than 12).  The
         // masked instance keeps ~48 MB groups and same-direction passes (measured faster
@@ -1142,13 +1232,19 @@ int launch_bwd(const void *q, const void *k, const void *v, const void *o, const
         a.bm_per_head = mask.per_head;
         a.nqbm = (Tq + 127) / 128;
         a.nkbm = (Tk + 127) / 128;
-        auto kernel = masked ? bwd_main_kernel<D, true> : bwd_main_kernel<D, false>;
+        auto kernel = sinks ? bwd_main_kernel<D, kSinks> : masked ? bwd_main_kernel<D, kWindow> : bwd_main_kernel<D, kPlain>;
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM_BYTES) != cudaSuccess)
             return ERR_CUDA;
         const int grid = a.units < sms ? a.units : sms;
         kernel<<<grid, L::NTHREADS, L::SMEM_BYTES, s>>>(tq, tk, tv, tdo, tdk, tdv, tacc, a);
         if (cudaGetLastError() != cudaSuccess)
             return ERR_CUDA;
+        if (a.parts > 1) {
+            const size_t blocks = ((size_t)BH * a.nsb * 2 * BK * (D / 4) + 255) / 256;
+            bwd_sink_join_kernel<D><<<(unsigned)blocks, 256, 0, s>>>(ws.sink_part, a.dv, a.dk, BH, Tk, a.nsb, a.parts);
+            if (cudaGetLastError() != cudaSuccess)
+                return ERR_CUDA;
+        }
     }
     // 3. dQ
     if ((stages & 4) && Tq > 0) {
@@ -1164,6 +1260,31 @@ int launch_bwd(const void *q, const void *k, const void *v, const void *o, const
 }
 
 }  // namespace
+
+// Units that a key block with sinks is cut into.  It sees all nqb query blocks behind it, a window's block about
+// wq: in one piece it would keep one CTA busy when the others have ended, so a part is at most a window's
+// block or an eighth of a CTA's whole share, whichever is more.  Of sizes only: the sums' order, and the
+// workspace, do not depend on the device.
+int bwd_sink_parts(int BH, int Tq, int Tk, const MaskSpec &mask)
+{
+    const long long nqb = (Tq + BQ - 1) / BQ, nkb = (Tk + BK - 1) / BK;
+    const int sinks = mask.sinks < Tk ? mask.sinks : Tk;
+    if (mask.left < 0 || sinks <= 0)
+        return 1;
+    const long long nsb = (sinks + BK - 1) / BK, wq = std::min<long long>(mask.left / BQ + 2, nqb);
+    const long long share = BH * (nkb * wq + nsb * nqb) / 152;
+    const long long most = std::max(std::max(wq, share / 8), 1ll);
+    return (int)std::min<long long>(std::max((nqb + most - 1) / most, 1ll), 64);
+}
+
+size_t bwd_sink_bytes(size_t BH, int Tq, int Tk, int d, const MaskSpec &mask)
+{
+    const int parts = bwd_sink_parts((int)BH, Tq, Tk, mask);
+    if (parts == 1)
+        return 0;
+    const int sinks = mask.sinks < Tk ? mask.sinks : Tk;
+    return BH * ((sinks + BK - 1) / BK) * parts * 2 * BK * d * sizeof(float);
+}
 
 int bwd_launch(const void *q, const void *k, const void *v, const void *o, const float *lse, const void *dO, void *dq,
                void *dk, void *dv, int BH, int Tq, int Tk, int d, const MaskSpec &mask, float scale,

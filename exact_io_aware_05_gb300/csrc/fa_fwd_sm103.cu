@@ -149,7 +149,8 @@ struct FwdArgs {
     const uint8_t *bmask;   // null, or [heads][nqbm][nkbm], nonzero = visit
     int bm_per_head;        // one mask per head (else one for all heads)
     int nqbm, nkbm;         // ceil(Tq / 128), ceil(Tk / 128)
-    int masked;             // a left bound or a block mask: the MASKED instance runs
+    int masked;             // kWindow: a left bound or a block mask; kSinks: a left bound and sinks
+    int sinks;              // kSinks: keys 0 .. sinks - 1 are outside of the left bound (1 to Tk)
     float scale_log2;    // scale * log2(e)
     // FP8: dequantization factors of the e4m3 operands: Q per 128-row block, K per
     // 128-key block, V per channel ([heads][nqd], [heads][nkd], [heads][D])
@@ -162,10 +163,15 @@ struct FwdArgs {
     int withhold;        // test-only build: the arrive this launch leaves out (else 0, unused)
 };
 
+// Instances by mask: none or a right bound alone; a window and/or a block mask; a window whose left bound
+// spares the first keys (sinks).
+enum : int { kPlain = 0, kWindow = 1, kSinks = 2 };
+
 // One unit = NQ consecutive 128-row query tiles of one (b, h).  Tile t visits the KV
 // blocks j in [lo, hi] (its rows' window) whose 128-key block its mask row marks.
 struct TileRange {
     int lo, hi;              // KV block range (lo > hi: none)
+    int ns;                  // kSinks: blocks 0 .. ns - 1 (ns <= lo) are visited too
     const uint8_t *bm;       // mask row of the tile's 128 rows, or null
     int n;                   // KV blocks the tile visits (0: none)
     int first, last;         // first and last of them
@@ -182,26 +188,30 @@ struct Plan {
 // Tile t's range, chosen with a select (no run-time array indexing).
 __device__ __forceinline__ TileRange tile_of(const Plan &p, int t) { return t ? p.tr1 : p.tr0; }
 
-template <int BC>
+template <int BC, int MASK>
 __device__ __forceinline__ bool tile_active(const TileRange &r, int j)
 {
+    if constexpr (MASK == kSinks)
+        return r.n > 0 && j <= r.hi && (j >= r.lo || j < r.ns);
     if (!r.rows || j < r.lo || j > r.hi)
         return false;
     return !r.bm || r.bm[(j * BC) >> 7] != 0;
 }
 
 // The first KV block at or after j that the tile visits (hi + 1 if none).
-template <int BC>
+template <int BC, int MASK>
 __device__ __forceinline__ int next_active(const TileRange &r, int j)
 {
-    while (j <= r.hi && !tile_active<BC>(r, j))
+    if constexpr (MASK == kSinks)   // over the blocks between the sinks and the window in one step
+        return j >= r.ns && j < r.lo ? r.lo : j;
+    while (j <= r.hi && !tile_active<BC, MASK>(r, j))
         ++j;
     return j;
 }
 
-// MASKED = false: no left bound and no block mask, so every tile visits a prefix
+// kPlain: no left bound and no block mask, so every tile visits a prefix
 // 0 .. n-1 of the KV blocks (causal, non-causal, right-bounded windows).
-template <int D, bool MASKED>
+template <int D, int MASK>
 __device__ __forceinline__ Plan make_plan(int u, const FwdArgs &a)
 {
     using L = FwdLayout<D>;
@@ -218,7 +228,7 @@ __device__ __forceinline__ Plan make_plan(int u, const FwdArgs &a)
     p.J = 0;
     p.js = 1 << 30;
     p.je = -1;
-    if constexpr (!MASKED) {
+    if constexpr (MASK == kPlain) {
         const int nkv = (a.Tk + L::BC - 1) / L::BC;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -255,6 +265,7 @@ __device__ __forceinline__ Plan make_plan(int u, const FwdArgs &a)
             tr.rows = (t < L::NQ) && (r_first < a.Tq);
             tr.lo = 0;
             tr.hi = -1;
+            tr.ns = 0;
             tr.bm = nullptr;
             if (tr.rows) {
                 const int r_last = min(r_first + BR - 1, a.Tq - 1);
@@ -265,19 +276,23 @@ __device__ __forceinline__ Plan make_plan(int u, const FwdArgs &a)
                     tr.lo = (int)(klo / L::BC);
                     tr.hi = (int)(khi / L::BC);
                 }
-                if (a.bmask)
+                if constexpr (MASK == kSinks) {
+                    // and the sinks that the last row sees, in blocks in front of the window's
+                    tr.ns = klo <= khi ? min(tr.lo, (int)(min(khi, (long)a.sinks - 1) / L::BC) + 1) : 0;
+                }
+                if (MASK != kSinks && a.bmask)
                     tr.bm = a.bmask + ((size_t)(a.bm_per_head ? p.bh : 0) * a.nqbm + (r_first >> 7)) * a.nkbm;
             }
             int n = 0;
             if (!tr.bm) {
-                n = tr.hi - tr.lo + 1;
-                tr.first = tr.lo;
+                n = tr.hi - tr.lo + 1 + tr.ns;
+                tr.first = tr.ns > 0 ? 0 : tr.lo;
                 tr.last = tr.hi;
             } else {
                 tr.first = tr.hi + 1;
                 tr.last = tr.lo - 1;
                 for (int j = tr.lo; j <= tr.hi; ++j)
-                    if (tile_active<L::BC>(tr, j)) {
+                    if (tile_active<L::BC, MASK>(tr, j)) {
                         tr.first = min(tr.first, j);
                         tr.last = j;
                         ++n;
@@ -301,22 +316,28 @@ __device__ __forceinline__ Plan make_plan(int u, const FwdArgs &a)
 // Two tiles: the K/V blocks either tile of the unit visits (both walk them, each
 // skipping the blocks that are not its own).  union_next gives the first such block at
 // or after j (je + 1 if none), union_count their number.
-template <int BC, bool MASKED>
+template <int BC, int MASK>
 __device__ __forceinline__ int union_next(const Plan &p, int j)
 {
-    if constexpr (MASKED)
-        while (j <= p.je && !tile_active<BC>(p.tr0, j) && !tile_active<BC>(p.tr1, j))
+    if constexpr (MASK == kSinks) {
+        // the tile below has the later window; a tile without a block visits none
+        const int j0 = next_active<BC, MASK>(p.tr0, j), j1 = next_active<BC, MASK>(p.tr1, j);
+        const int x = p.tr0.n > 0 && j0 <= p.tr0.hi ? j0 : p.je + 1, y = p.tr1.n > 0 && j1 <= p.tr1.hi ? j1 : p.je + 1;
+        return min(x, y);
+    }
+    if constexpr (MASK != kPlain)
+        while (j <= p.je && !tile_active<BC, MASK>(p.tr0, j) && !tile_active<BC, MASK>(p.tr1, j))
             ++j;
     return j;
 }
 
-template <int BC, bool MASKED>
+template <int BC, int MASK>
 __device__ __forceinline__ int union_count(const Plan &p)
 {
-    if constexpr (!MASKED)
+    if constexpr (MASK == kPlain)
         return p.je - p.js + 1;
     int n = 0;
-    for (int j = union_next<BC, MASKED>(p, p.js); j <= p.je; j = union_next<BC, MASKED>(p, j + 1))
+    for (int j = union_next<BC, MASK>(p, p.js); j <= p.je; j = union_next<BC, MASK>(p, j + 1))
         ++n;
     return n;
 }
@@ -342,12 +363,13 @@ __device__ __forceinline__ bool walk_ops(int J, FS &&fs, FPV &&fpv)
     return true;
 }
 
-template <int D, bool MASKED, bool F8 = false>
+template <int D, int MASK, bool F8 = false>
 __global__ void __launch_bounds__(FwdLayout<D, F8>::NTHREADS, 1)
     fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                const __grid_constant__ CUtensorMap tm_v, const FwdArgs a)
 {
     using L = FwdLayout<D, F8>;
+    constexpr bool MASKED = MASK != kPlain;
     static_assert(!(F8 && MASKED), "the FP8 forward takes no window or block mask");
     constexpr int BC = L::BC, NQ = L::NQ, NSLOT = L::NSLOT;
     constexpr bool INL = NQ == 2;   // register split below: bounded waits inlined (no calls)
@@ -417,7 +439,7 @@ __global__ void __launch_bounds__(FwdLayout<D, F8>::NTHREADS, 1)
                 const uint64_t pol_kv = policy_evict_last();
                 const uint64_t pol_q = policy_evict_first();
                 for (int pass = 0, u = snake_unit<!MASKED>(0); u < a.units; u = snake_unit<!MASKED>(++pass)) {
-                    const Plan p = make_plan<D, MASKED>(u, a);
+                    const Plan p = make_plan<D, MASK>(u, a);
                     if (p.J == 0)
                         continue;
                     if (n_q > 0 && !mbar_wait<INL, HN>(bar(L::B_QEMPTY), (n_q - 1) & 1, ctx, SITE_P_QEMPTY))
@@ -471,17 +493,17 @@ __global__ void __launch_bounds__(FwdLayout<D, F8>::NTHREADS, 1)
                     if constexpr (NQ == 2) {
                         // each tile's MMA warp consumes K_j, V_j of every block either tile visits,
                         // in the order S(0), S(1), PV(0), S(2), PV(1), ...
-                        int kj = union_next<BC, MASKED>(p, p.js), vj = kj;
+                        int kj = union_next<BC, MASK>(p, p.js), vj = kj;
                         ok = walk_ops(
-                            union_count<BC, MASKED>(p),
+                            union_count<BC, MASK>(p),
                             [&](int) {
                                 const bool r = load(&tm_k, kj);
-                                kj = union_next<BC, MASKED>(p, kj + 1);
+                                kj = union_next<BC, MASK>(p, kj + 1);
                                 return r;
                             },
                             [&](int) {
                                 const bool r = load(&tm_v, vj);
-                                vj = union_next<BC, MASKED>(p, vj + 1);
+                                vj = union_next<BC, MASK>(p, vj + 1);
                                 return r;
                             });
                     } else {
@@ -491,12 +513,12 @@ __global__ void __launch_bounds__(FwdLayout<D, F8>::NTHREADS, 1)
                             p.J,
                             [&](int) {
                                 const bool r = load_chunks(true, kj);
-                                kj = next_active<BC>(p.tr0, kj + 1);
+                                kj = next_active<BC, MASK>(p.tr0, kj + 1);
                                 return r;
                             },
                             [&](int) {
                                 const bool r = load_chunks(false, vj);
-                                vj = next_active<BC>(p.tr0, vj + 1);
+                                vj = next_active<BC, MASK>(p.tr0, vj + 1);
                                 return r;
                             });
                     }
@@ -526,7 +548,7 @@ __global__ void __launch_bounds__(FwdLayout<D, F8>::NTHREADS, 1)
                 uint32_t ld = 0, q_seen = 0, sn = 0, pvn = 0, epi = 0;
                 bool ok = true;
                 for (int pass = 0, u = snake_unit<!MASKED>(0); u < a.units && ok; u = snake_unit<!MASKED>(++pass)) {
-                    const Plan p = make_plan<D, MASKED>(u, a);
+                    const Plan p = make_plan<D, MASK>(u, a);
                     if (p.J == 0)
                         continue;
                     if (!mbar_wait<INL, HN>(bar(L::B_QFULL), q_seen & 1, ctx, SITE_M_QFULL))
@@ -535,23 +557,23 @@ __global__ void __launch_bounds__(FwdLayout<D, F8>::NTHREADS, 1)
                     const TileRange me = tile_of(p, t);
                     if (me.n == 0)
                         mbar_arrive(bar(L::B_QEMPTY));      // this tile reads no Q in this unit
-                    auto mine = [&](int j) { return MASKED ? tile_active<BC>(me, j) : j < me.n; };
+                    auto mine = [&](int j) { return MASKED ? tile_active<BC, MASK>(me, j) : j < me.n; };
                     auto acquire = [&](uint32_t &slot) -> bool {
                         slot = ld % NSLOT;
                         const bool r = mbar_wait<INL, HN>(bar(L::B_FULL + slot), (ld / NSLOT) & 1, ctx, SITE_M_FULL);
                         ++ld;
                         return r;
                     };
-                    int kj = union_next<BC, MASKED>(p, p.js), vj = kj;
+                    int kj = union_next<BC, MASK>(p, p.js), vj = kj;
                     ok = walk_ops(
-                        union_count<BC, MASKED>(p),
+                        union_count<BC, MASK>(p),
                         [&](int) -> bool {
                             // K_j: S_t = Q_t K_j^T
                             uint32_t ks;
                             if (!acquire(ks))
                                 return false;
                             const int j = kj;
-                            kj = union_next<BC, MASKED>(p, kj + 1);
+                            kj = union_next<BC, MASK>(p, kj + 1);
                             if (!mine(j)) {
                                 mbar_arrive(bar(L::B_EMPTY + ks));   // K_j is only for the other tile
                                 return true;
@@ -591,7 +613,7 @@ __global__ void __launch_bounds__(FwdLayout<D, F8>::NTHREADS, 1)
                             if (!acquire(vs))
                                 return false;
                             const int j = vj;
-                            vj = union_next<BC, MASKED>(p, vj + 1);
+                            vj = union_next<BC, MASK>(p, vj + 1);
                             if (!mine(j)) {
                                 mbar_arrive(bar(L::B_EMPTY + vs));
                                 return true;
@@ -654,7 +676,7 @@ __global__ void __launch_bounds__(FwdLayout<D, F8>::NTHREADS, 1)
                 bool ok = true;
                 const uint64_t qd = sdesc_sw128(sbase + L::OFF_Q, 16, 1024);
                 for (int pass = 0, u = snake_unit<!MASKED>(0); u < a.units && ok; u = snake_unit<!MASKED>(++pass)) {
-                    const Plan p = make_plan<D, MASKED>(u, a);
+                    const Plan p = make_plan<D, MASK>(u, a);
                     const int J = p.J;
                     if (J == 0)
                         continue;
@@ -759,7 +781,7 @@ __global__ void __launch_bounds__(FwdLayout<D, F8>::NTHREADS, 1)
         uint32_t pv = 0, ep = 0;   // jobs and epilogues of this tile so far
         // The two softmax warpgroups run unsynchronised: each follows its own tile's S.
         for (int pass = 0, u = snake_unit<!MASKED>(0); u < a.units; u = snake_unit<!MASKED>(++pass)) {
-            const Plan p = make_plan<D, MASKED>(u, a);
+            const Plan p = make_plan<D, MASK>(u, a);
             const int r = p.row0 + t * BR + rit;
             const TileRange me = tile_of(p, t);
             const bool row_ok = r < a.Tq;
@@ -784,7 +806,7 @@ __global__ void __launch_bounds__(FwdLayout<D, F8>::NTHREADS, 1)
             bool ok = true;
             // jj: job index of this tile; j: the KV block it visits
             for (int jj = 0, j = MASKED ? me.first : 0; jj < me.n && ok;
-                 ++jj, j = MASKED ? next_active<BC>(me, j + 1) : jj) {
+                 ++jj, j = MASKED ? next_active<BC, MASK>(me, j + 1) : jj) {
                 // two tiles: S buffer t, one phase per job of this tile; one tile: the NSB
                 // S buffers take consecutive jobs in turn
                 const uint32_t b = NQ == 2 ? (uint32_t)t : (pv % L::NSB);
@@ -820,7 +842,8 @@ __global__ void __launch_bounds__(FwdLayout<D, F8>::NTHREADS, 1)
                 const long off = (long)a.Tk - a.Tq;
                 const bool need_mask = (kv0 + BC > a.Tk) ||
                                        (a.right >= 0 && (long)kv0 + BC - 1 > (long)first_row + off + a.right) ||
-                                       (MASKED && a.left >= 0 && (long)kv0 < (long)last_row + off - a.left);
+                                       (MASKED && a.left >= 0 && (long)kv0 < (long)last_row + off - a.left &&
+                                        !(MASK == kSinks && kv0 + BC <= a.sinks));
                 if (need_mask) {
                     long hi = a.Tk;   // allowed keys of row r: [lo, hi)
                     if (a.right >= 0)
@@ -828,9 +851,10 @@ __global__ void __launch_bounds__(FwdLayout<D, F8>::NTHREADS, 1)
                     const long lo = (MASKED && a.left >= 0) ? (long)r + off - a.left : 0L;
                     const int ch = (int)max(0L, min((long)BC, hi - kv0));
                     const int cl = MASKED ? (int)max(0L, min((long)BC, lo - kv0)) : 0;
+                    const int cs = MASK == kSinks ? a.sinks - kv0 : 0;   // keys in front of it are seen, up to ch
 #pragma unroll
                     for (int i = 0; i < BC; ++i)
-                        if (i < cl || i >= ch)
+                        if ((i < cl && i >= cs) || i >= ch)
                             s[i] = -INFINITY;
                 }
                 // row max: four independent chains of three-input max
@@ -1060,7 +1084,8 @@ int launch(const void *q, const void *k, const void *v, void *o, float *lse, int
     a.bm_per_head = mask.per_head;
     a.nqbm = (Tq + 127) / 128;
     a.nkbm = (Tk + 127) / 128;
-    a.masked = (mask.left >= 0 || mask.block) ? 1 : 0;
+    a.sinks = mask.sinks < Tk ? mask.sinks : Tk;
+    a.masked = mask.left >= 0 && a.sinks > 0 ? kSinks : mask.left >= 0 || mask.block ? kWindow : kPlain;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.qd = a.kd = a.vd = nullptr;
     a.nqd = a.nkd = 0;
@@ -1081,7 +1106,7 @@ int launch(const void *q, const void *k, const void *v, void *o, float *lse, int
     if (L::NQ == 2)
         a.withhold = test_withhold_take(WITHHOLD_FWD_KV, WITHHOLD_FWD_EPI);
 #endif
-    auto kernel = a.masked ? fwd_kernel<D, true> : fwd_kernel<D, false>;
+    auto kernel = a.masked == kSinks ? fwd_kernel<D, kSinks> : a.masked == kWindow ? fwd_kernel<D, kWindow> : fwd_kernel<D, kPlain>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM_BYTES) != cudaSuccess)
         return ERR_CUDA;
     kernel<<<grid, L::NTHREADS, L::SMEM_BYTES, s>>>(tq, tk, tv, a);
@@ -1116,7 +1141,8 @@ int launch_f8(const void *q8, const void *k8, const void *vt8, const float *qd, 
     a.bm_per_head = 0;
     a.nqbm = (Tq + 127) / 128;
     a.nkbm = (Tk + 127) / 128;
-    a.masked = 0;
+    a.masked = kPlain;
+    a.sinks = 0;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.qd = qd;
     a.kd = kd;
@@ -1132,7 +1158,7 @@ int launch_f8(const void *q8, const void *k8, const void *vt8, const float *qd, 
     a.group = grid_aligned_group(g < 1 ? 1 : (g > BH ? BH : g), a.nqb, grid);
     a.timeout_ns = wait_timeout_ns();
     a.withhold = WITHHOLD_NONE;
-    auto kernel = fwd_kernel<D, false, true>;
+    auto kernel = fwd_kernel<D, kPlain, true>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM_BYTES) != cudaSuccess)
         return ERR_CUDA;
     kernel<<<grid, L::NTHREADS, L::SMEM_BYTES, s>>>(tq, tk, tv, a);

@@ -71,11 +71,13 @@ inline int grid_aligned_group(int gmax, int levels, int grid)
 //   r + Tk - Tq - left <= l <= r + Tk - Tq + right   (left, right = -1: that side unbounded)
 // and, with a block mask, block[(r / 128) * nkbm + l / 128] != 0 for the head's mask
 // ([heads][ceil(Tq / 128)][ceil(Tk / 128)] bytes in device memory, one mask per head when
-// per_head, else one for all heads).  Causal is left = -1, right = 0.
+// per_head, else one for all heads).  Causal is left = -1, right = 0.  The left bound does not hold for keys
+// below sinks (right = 0 and no block mask with them).
 struct MaskSpec {
     int left, right;
     const uint8_t *block;
     int per_head;
+    int sinks = 0;
 };
 inline MaskSpec causal_spec(int causal) { return MaskSpec{-1, causal ? 0 : -1, nullptr, 0}; }
 
@@ -111,7 +113,10 @@ struct BwdWorkspace {
     // and |K_lc| (float bits), and per 128-row query block a bound on |dq_acc| (float bits)
     float *kvmax;    // [BH][2]
     int *bound;      // [BH][Tq_pad / 128]
+    float *sink_part = nullptr;   // behind them: partial dV, dK of split key blocks (bwd_sink_bytes; 0: none)
 };
+int bwd_sink_parts(int BH, int Tq, int Tk, const MaskSpec &mask);
+size_t bwd_sink_bytes(size_t BH, int Tq, int Tk, int d, const MaskSpec &mask);
 size_t bwd_row_stride(int Tq);
 size_t bwd_workspace_bytes(size_t BH, int Tq, int d);
 BwdWorkspace bwd_workspace_carve(void *ws, int BH, int Tq, int d);

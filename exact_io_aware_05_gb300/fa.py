@@ -40,6 +40,12 @@ _lib.fa_fwd_masked.argtypes = [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, 
 _lib.fa_fwd_masked.restype = _i
 _lib.fa_bwd_masked.argtypes = [_vp] * 9 + [_i] * 7 + [_vp, _i, _i, _f, _vp, _sz, _vp]
 _lib.fa_bwd_masked.restype = _i
+_lib.fa_fwd_sinks.argtypes = [_vp] * 5 + [_i] * 7 + [_f, _vp]
+_lib.fa_fwd_sinks.restype = _i
+_lib.fa_bwd_sinks_workspace_bytes.argtypes = [_i] * 7
+_lib.fa_bwd_sinks_workspace_bytes.restype = _sz
+_lib.fa_bwd_sinks.argtypes = [_vp] * 9 + [_i] * 8 + [_f, _vp, _sz, _vp]
+_lib.fa_bwd_sinks.restype = _i
 _lib.fa_fp8_vt_stride.argtypes = [_i]
 _lib.fa_fp8_vt_stride.restype = _sz
 _lib.fa_fp8_quantize.argtypes = [_vp] * 4 + [_i] * 5 + [_vp] * 6 + [_vp]
@@ -200,6 +206,20 @@ def fa_fwd_masked(q, k, v, o, lse, window=(-1, -1), block_mask=None, scale: floa
                                                _stream(stream)))
 
 
+def fa_fwd_sinks(q, k, v, o, lse, window_left: int, n_sinks: int, scale: float, stream=None) -> None:
+    """fa_fwd under a causal window of window_left + 1 keys (-1: no left bound) and the first n_sinks keys, which
+    stay visible to every row behind them."""
+    B, H, Tq, Tk, d = _shapes(q, k)
+    dev = q.device
+    _need(q, "q", torch.bfloat16, (B, H, Tq, d), dev)
+    _need(k, "k", torch.bfloat16, (B, H, Tk, d), dev)
+    _need(v, "v", torch.bfloat16, (B, H, Tk, d), dev)
+    _need(o, "o", torch.bfloat16, (B, H, Tq, d), dev)
+    _need(lse, "lse", torch.float32, (B, H, Tq), dev)
+    _launch("fa_fwd_sinks", _lib.fa_fwd_sinks, q.get_device(), stream, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, H, Tq,
+            Tk, d, int(window_left), int(n_sinks), float(scale))
+
+
 def fa_decode_workspace_bytes(B: int, H: int, Tq: int, Tk: int, d: int) -> int:
     return int(_lib.fa_decode_workspace_bytes(B, H, Tq, Tk, d))
 
@@ -308,13 +328,26 @@ def fa_status_string(status: int) -> str:
 
 
 # ---------------------------------------------------------------- conveniences
-def attention_forward(q, k, v, causal: bool, scale: float, stream=None, window=None, block_mask=None):
+def _sink_window(causal, window, block_mask) -> int:
+    """The left bound of a call with sinks."""
+    if causal == (window is not None):
+        raise ValueError("sinks: give either causal or a window")
+    left, right = (-1, 0) if window is None else window
+    if right != 0 or block_mask is not None:
+        raise ValueError("sinks: a causal window (left, 0) without a block mask")
+    return left
+
+
+def attention_forward(q, k, v, causal: bool, scale: float, stream=None, window=None, block_mask=None, sinks: int = 0):
     """Allocates O and lse with torch and runs fa_fwd (bf16) or fa_fwd_f32 (float32); with a
-    window (which replaces `causal`) or a block mask, fa_fwd_masked."""
+    window (which replaces `causal`) or a block mask, fa_fwd_masked; with a window (left, 0) and sinks,
+    fa_fwd_sinks."""
     B, H, Tq, Tk, d = _shapes(q, k)
     o = torch.empty_like(q)
     lse = torch.empty((B, H, Tq), dtype=torch.float32, device=q.device)
-    if window is not None or block_mask is not None:
+    if sinks:
+        fa_fwd_sinks(q, k, v, o, lse, _sink_window(causal, window, block_mask), sinks, scale, stream)
+    elif window is not None or block_mask is not None:
         if window is None:
             window = (-1, 0 if causal else -1)
         elif causal:
@@ -421,12 +454,41 @@ def fa_bwd_masked(q, k, v, o, lse, dO, dq, dk, dv, window=(-1, -1), block_mask=N
                                                _ptr(workspace), nbytes, _stream(stream)))
 
 
+def fa_bwd_sinks_workspace_bytes(B: int, H: int, Tq: int, Tk: int, d: int, window_left: int, n_sinks: int) -> int:
+    return int(_lib.fa_bwd_sinks_workspace_bytes(B, H, Tq, Tk, d, window_left, n_sinks))
+
+
+def fa_bwd_sinks(q, k, v, o, lse, dO, dq, dk, dv, window_left: int, n_sinks: int, scale: float, workspace: torch.Tensor,
+                 deterministic: bool = False, stream=None) -> None:
+    """Backward of fa_fwd_sinks under the same window and sinks; workspace of fa_bwd_sinks_workspace_bytes."""
+    B, H, Tq, Tk, d = _shapes(q, k)
+    dev = q.device
+    for name, t, shp in (("q", q, (B, H, Tq, d)), ("k", k, (B, H, Tk, d)), ("v", v, (B, H, Tk, d)),
+                         ("o", o, (B, H, Tq, d)), ("dO", dO, (B, H, Tq, d)), ("dq", dq, (B, H, Tq, d)),
+                         ("dk", dk, (B, H, Tk, d)), ("dv", dv, (B, H, Tk, d))):
+        _need(t, name, torch.bfloat16, shp, dev)
+    _need(lse, "lse", torch.float32, (B, H, Tq), dev)
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace: must be a contiguous tensor on the same device")
+    _launch("fa_bwd_sinks", _lib.fa_bwd_sinks, q.get_device(), stream, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dO),
+            _ptr(dq), _ptr(dk), _ptr(dv), B, H, Tq, Tk, d, int(window_left), int(n_sinks), int(bool(deterministic)), float(scale),
+            _ptr(workspace), workspace.nbytes)
+
+
 def attention_backward(q, k, v, o, lse, dO, causal: bool, scale: float, workspace=None, stream=None,
-                       deterministic: bool = False, window=None, block_mask=None):
+                       deterministic: bool = False, window=None, block_mask=None, sinks: int = 0):
     """Allocates dQ, dK, dV (and the workspace if not given) and runs fa_bwd
     (fa_bwd_deterministic when `deterministic`; fa_bwd_masked with a window, which
-    replaces `causal`, or a block mask)."""
+    replaces `causal`, or a block mask; fa_bwd_sinks with a window (left, 0) and sinks)."""
     B, H, Tq, Tk, d = _shapes(q, k)
+    if sinks:
+        left = _sink_window(causal, window, block_mask)
+        specs = [(t.shape, t.dtype) for t in (q, k, v)]
+        if workspace is None:
+            specs.append(((max(fa_bwd_sinks_workspace_bytes(B, H, Tq, Tk, d, left, sinks), 256),), torch.uint8))
+        dq, dk, dv, *own = _empties(stream, q.device, *specs)
+        fa_bwd_sinks(q, k, v, o, lse, dO, dq, dk, dv, left, sinks, scale, own[0] if own else workspace, deterministic, stream)
+        return dq, dk, dv
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     ws = alloc_workspace(B, H, Tq, Tk, d, q.device) if workspace is None else workspace
     if window is not None or block_mask is not None:

@@ -99,6 +99,17 @@ int fa_fwd_masked(const void *q, const void *k, const void *v, void *o, float *l
                   fa_stream_t stream);
 
 /*
+ * fa_fwd under a causal sliding window with sinks: key l is allowed for query row r, at position
+ * p = r + Tk - Tq, iff
+ *     l <= p  and  (l >= p - window_left  or  l < n_sinks)
+ * so that the first n_sinks keys stay visible to every row behind them, however far (window_left -1:
+ * no left bound, plain causal).  Tiles between the sinks and the window are never loaded.  Other arguments and
+ * errors as fa_fwd_masked; n_sinks >= 0, any number.
+ */
+int fa_fwd_sinks(const void *q, const void *k, const void *v, void *o, float *lse, int B, int H, int Tq, int Tk,
+                 int d, int window_left, int n_sinks, float scale, fa_stream_t stream);
+
+/*
  * FP8 forward (atlas.blal.pro "FlashAttention -- IO-Aware Exact Attention",
  * "The version ladder: FA1 -> FA2 -> FA3", the FA3 entry: e4m3 tensor-core
  * products with block quantization and incoherent processing; "Honest caveats &
@@ -436,6 +447,19 @@ int fa_bwd_masked(const void *q, const void *k, const void *v, const void *o,
                   int B, int H, int Tq, int Tk, int d, int window_left, int window_right,
                   const unsigned char *block_mask, int mask_per_head, int deterministic,
                   float scale, void *workspace, size_t workspace_bytes, fa_stream_t stream);
+
+/*
+ * Backward of fa_fwd_sinks (o and lse from it, with the same window and sinks).  Each 128-key block visits
+ * the query blocks of its window; blocks with sinks, which every query block behind them sees, are
+ * cut into parts where one of them would outlast the rest, with fp32 sums joined in a fixed order: the workspace is
+ * fa_bwd_sinks_workspace_bytes(...) (at least fa_bwd_workspace_bytes; 0 for invalid sizes).
+ * deterministic = 1 selects fa_bwd_deterministic's order-independent dQ.  Other arguments and errors as
+ * fa_bwd.
+ */
+size_t fa_bwd_sinks_workspace_bytes(int B, int H, int Tq, int Tk, int d, int window_left, int n_sinks);
+int fa_bwd_sinks(const void *q, const void *k, const void *v, const void *o, const float *lse, const void *dO,
+                 void *dq, void *dk, void *dv, int B, int H, int Tq, int Tk, int d, int window_left, int n_sinks,
+                 int deterministic, float scale, void *workspace, size_t workspace_bytes, fa_stream_t stream);
 
 /*
  * One stage of fa_bwd, for callers that schedule or time the three kernels

@@ -1,0 +1,42 @@
+"""Refusals of the attention under a window with sinks on the host, before any CUDA call, and the size of its
+workspace.  The addresses are made up: the refusals run only where there is no GPU."""
+import pytest
+import torch
+
+from test_cache_host import INVALID, MB, NO_GPU, P, UNSUPPORTED, fa  # noqa: F401  (fa: a fixture)
+
+made_up = pytest.mark.skipif(torch.cuda.is_available(), reason="made-up addresses: only without a GPU")
+
+
+@made_up
+def test_refusals(fa):
+    f, g = fa.lib().fa_fwd_sinks, fa.lib().fa_bwd_sinks
+    t = [P + i * MB for i in range(10)]
+
+    def fwd(left=5, sinks=2, d=64, scale=0.1, o=t[3]):
+        return f(t[0], t[1], t[2], o, t[4], 1, 1, 100, 100, d, left, sinks, scale, None)
+
+    def bwd(left=5, sinks=2, d=64, det=0, ws=t[9], dq=t[6], nbytes=None):
+        need = fa.fa_bwd_sinks_workspace_bytes(1, 1, 100, 100, d, left, sinks)
+        return g(t[0], t[1], t[2], t[3], t[4], t[5], dq, t[7], t[8], 1, 1, 100, 100, d, left, sinks, det, 0.1, ws,
+                 need if nbytes is None else nbytes, None)
+    assert fwd() in NO_GPU and fwd(left=-1) in NO_GPU and fwd(left=2 ** 31 - 1, sinks=2 ** 31 - 1) in NO_GPU
+    assert fwd(left=-2) == INVALID and fwd(sinks=-1) == INVALID and fwd(scale=0.0) == INVALID and fwd(o=t[0]) == INVALID
+    assert fwd(d=96) == UNSUPPORTED
+    assert bwd() in NO_GPU and bwd(left=2 ** 31 - 1, sinks=2 ** 31 - 1) in NO_GPU
+    assert bwd(left=-2) == INVALID and bwd(sinks=-1) == INVALID and bwd(det=2) == INVALID and bwd(ws=None) == INVALID
+    assert bwd(dq=t[0]) == INVALID and bwd(d=256) == UNSUPPORTED and bwd(ws=P + 9 * MB + 16) == INVALID
+    assert bwd(nbytes=fa.fa_bwd_sinks_workspace_bytes(1, 1, 100, 100, 64, 5, 2) - 1) == INVALID
+
+
+def test_workspace(fa):
+    """The partial sums: per head and key block with sinks, parts x (dV and dK) x 128 rows of d floats; none without
+    a left bound or sinks."""
+    size, base = fa.fa_bwd_sinks_workspace_bytes, fa.fa_bwd_workspace_bytes
+    for args in ((1, 1, 3000, 3000, 128), (2, 3, 777, 5000, 64), (8, 32, 4096, 4096, 128)):
+        assert size(*args, -1, 4) == size(*args, 100, 0) == base(*args)
+        for left, sinks in ((0, 1), (100, 4), (100, 300), (10 ** 9, 10 ** 9)):
+            extra, unit = size(*args, left, sinks) - base(*args), args[0] * args[1] * -(-min(sinks, args[3]) // 128) * 2 * 128 * args[4] * 4
+            assert extra % unit == 0 and extra // unit in (0, *range(2, 65))
+    assert size(1, 1, 3000, 3000, 128, 255, 4) - base(1, 1, 3000, 3000, 128) == 8 * 2 * 128 * 128 * 4   # 24 query blocks, 3 a window
+    assert size(1, 1, 100, 100, 64, -2, 0) == 0 and size(1, 1, 100, 100, 64, 0, -1) == 0 and size(1, 1, 100, 100, 96, 0, 1) == 0
