@@ -631,20 +631,23 @@ int fa_bwd_stage(int stage, const void *q, const void *k, const void *v, const v
                       workspace_bytes, 1 << (stage - 1), stream);
 }
 
-// The status word of the first kernel file that has one (all are read and cleared): those with waits come
-// before those that report indexes alone, so that a timeout is told first.
+// The status word of the first kernel file that has one (all are read and cleared), a timeout before an index
+// out of range.
 static int fetch_status(cudaStream_t s, int *word)
 {
-    int w[5] = {0, 0, 0, 0, 0};
+    int w[6] = {0, 0, 0, 0, 0, 0};
     if (fa::fwd_status_fetch_clear(s, &w[0]) != fa::OK || fa::bwd_status_fetch_clear(s, &w[1]) != fa::OK ||
         fa::dec_status_fetch_clear(s, &w[2]) != fa::OK)
         return fa::ERR_CUDA;
     if (fa::status_is_in_use(fa::STATUS_PAGED) && fa::paged_status_fetch_clear(s, &w[3]) != fa::OK)
         return fa::ERR_CUDA;
+    if (fa::status_is_in_use(fa::STATUS_RANGE) && fa::paged_range_status_fetch_clear(s, &w[5]) != fa::OK)
+        return fa::ERR_CUDA;
     if (fa::status_is_in_use(fa::STATUS_CACHE) && fa::cache_status_fetch_clear(s, &w[4]) != fa::OK)
         return fa::ERR_CUDA;
-    for (int i = 0; i < 5 && *word == 0; ++i)
-        *word = w[i];
+    for (int i = 0; i < 6; ++i)
+        if (*word == 0 || ((w[i] & 0xFF) == fa::ERR_TIMEOUT && (*word & 0xFF) != fa::ERR_TIMEOUT))
+            *word = w[i];
     return fa::OK;
 }
 

@@ -204,6 +204,59 @@ bool touches_weights(const fa_head_norm *m, const void *p, size_t n)
     return fa::overlaps(p, n, m->q_weight, nw) || fa::overlaps(p, n, m->k_weight, nw);
 }
 
+// Sizes of a paged decode: 0 for what fa_decode_paged refuses.
+bool paged_sizes_ok(int B, int Hq, int Hkv, int Tq, int max_pages, int page_size, int d)
+{
+    if (B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Tq < 1 || Tq > 16 || max_pages < 0 || !page_size_ok(page_size))
+        return false;
+    if (!width_ok(d) || (long long)max_pages * page_size > kMaxSlots)
+        return false;
+    // row indexes of q, and units of (sequence, KV head, 64 rows of a head group), in 31 bits
+    return (long long)B * Hq <= INT_MAX / Tq;
+}
+
+// What the decodes over a cache check; *empty: nothing to do.  need(): the workspace's size, for sizes in range.
+template <typename Need>
+int decode_check(const fa_kv_cache *cache, const void *q, void *o, float *lse, int Hq, int Tq, float scale, int accumulate,
+                        void *workspace, size_t workspace_bytes, Need &&need_of, bool *empty)
+{
+    int st = cache_check(cache);
+    if (st != FA_OK)
+        return st;
+    if (!std::isfinite(scale) || !(scale > 0.0f))
+        return FA_ERR_INVALID_ARG;
+    if (Tq > 16)
+        return FA_ERR_UNSUPPORTED;
+    const int B = cache->B, d = cache->d;
+    if (!paged_sizes_ok(B, Hq, cache->Hkv, Tq, cache->max_pages, cache->page_size, d))
+        return FA_ERR_INVALID_ARG;
+    if (accumulate && !cache->weight && slots_bytes(cache) > 0)
+        return FA_ERR_INVALID_ARG;
+    *empty = B == 0;
+    if (B == 0)
+        return FA_OK;
+    const size_t rows = (size_t)B * Hq * Tq, nq = rows * d * 2, nl = rows * 4;
+    if (!q || !o || !lse || !fa::aligned16(q) || !fa::aligned16(o) || !fa::aligned16(lse))
+        return FA_ERR_INVALID_ARG;
+    const size_t need = need_of();
+    if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+        return FA_ERR_INVALID_ARG;
+    if (!cache_disjoint(cache) && accumulate)
+        return FA_ERR_INVALID_ARG;
+    void *outs[3] = {o, lse, workspace};
+    const size_t out_n[3] = {nq, nl, need};
+    for (int i = 0; i < 3; ++i) {
+        if (fa::overlaps(outs[i], out_n[i], q, nq) || touches_cache(cache, outs[i], out_n[i], true))
+            return FA_ERR_INVALID_ARG;
+        for (int j = i + 1; j < 3; ++j)
+            if (fa::overlaps(outs[i], out_n[i], outs[j], out_n[j]))
+                return FA_ERR_INVALID_ARG;
+    }
+    if (accumulate && fa::overlaps(cache->weight, slots_bytes(cache), q, nq))
+        return FA_ERR_INVALID_ARG;
+    return FA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -403,17 +456,6 @@ int fa_cache_append(const fa_kv_cache *cache, const fa_heads *k, const fa_heads 
     return fa_cache_append_norm(cache, k, v, q, q_out, positions, spec, nullptr, new_lens, T, stream);
 }
 
-// Sizes of a paged decode: 0 for what fa_decode_paged refuses.
-static bool paged_sizes_ok(int B, int Hq, int Hkv, int Tq, int max_pages, int page_size, int d)
-{
-    if (B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Tq < 1 || Tq > 16 || max_pages < 0 || !page_size_ok(page_size))
-        return false;
-    if (!width_ok(d) || (long long)max_pages * page_size > kMaxSlots)
-        return false;
-    // row indexes of q, and units of (sequence, KV head, 64 rows of a head group), in 31 bits
-    return (long long)B * Hq <= INT_MAX / Tq;
-}
-
 size_t fa_decode_paged_workspace_bytes(int B, int Hq, int Hkv, int Tq, int max_pages, int page_size, int d,
                                        int accumulate)
 {
@@ -426,43 +468,40 @@ size_t fa_decode_paged_workspace_bytes(int B, int Hq, int Hkv, int Tq, int max_p
 int fa_decode_paged(const fa_kv_cache *cache, const void *q, void *o, float *lse, int Hq, int Tq, int causal,
                     float scale, int accumulate, void *workspace, size_t workspace_bytes, fa_stream_t stream)
 {
-    int st = cache_check(cache);
-    if (st != FA_OK)
+    if (causal < 0 || causal > 1 || accumulate < 0 || accumulate > 1)
+        return cache_check(cache) == FA_ERR_UNSUPPORTED ? FA_ERR_UNSUPPORTED : FA_ERR_INVALID_ARG;
+    bool empty = false;
+    int st = decode_check(cache, q, o, lse, Hq, Tq, scale, accumulate, workspace, workspace_bytes,
+                          [&] { return fa::paged_workspace_bytes(cache->B, Hq, cache->Hkv, Tq, cache->max_pages * cache->page_size,
+                                                                 cache->d, accumulate); },
+                          &empty);
+    if (st != FA_OK || empty)
         return st;
-    if (causal < 0 || causal > 1 || accumulate < 0 || accumulate > 1 || !std::isfinite(scale) || !(scale > 0.0f))
-        return FA_ERR_INVALID_ARG;
-    if (Tq > 16)
-        return FA_ERR_UNSUPPORTED;
-    const int B = cache->B, d = cache->d;
-    if (!paged_sizes_ok(B, Hq, cache->Hkv, Tq, cache->max_pages, cache->page_size, d))
-        return FA_ERR_INVALID_ARG;
-    if (accumulate && !cache->weight && slots_bytes(cache) > 0)
-        return FA_ERR_INVALID_ARG;
-    if (B == 0)
-        return FA_OK;
-    const size_t rows = (size_t)B * Hq * Tq, nq = rows * d * 2, nl = rows * 4;
-    if (!q || !o || !lse || !fa::aligned16(q) || !fa::aligned16(o) || !fa::aligned16(lse))
-        return FA_ERR_INVALID_ARG;
-    const size_t need = fa::paged_workspace_bytes(B, Hq, cache->Hkv, Tq, cache->max_pages * cache->page_size, d, accumulate);
-    if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
-        return FA_ERR_INVALID_ARG;
-    if (!cache_disjoint(cache) && accumulate)
-        return FA_ERR_INVALID_ARG;
-    void *outs[3] = {o, lse, workspace};
-    const size_t out_n[3] = {nq, nl, need};
-    for (int i = 0; i < 3; ++i) {
-        if (fa::overlaps(outs[i], out_n[i], q, nq) || touches_cache(cache, outs[i], out_n[i], true))
-            return FA_ERR_INVALID_ARG;
-        for (int j = i + 1; j < 3; ++j)
-            if (fa::overlaps(outs[i], out_n[i], outs[j], out_n[j]))
-                return FA_ERR_INVALID_ARG;
-    }
-    if (accumulate && fa::overlaps(cache->weight, slots_bytes(cache), q, nq))
-        return FA_ERR_INVALID_ARG;
     if ((st = fa::check_device()) != fa::OK)
         return st;
     return fa::paged_launch(*cache, q, o, lse, Hq, Tq, causal, scale, accumulate, workspace,
                             reinterpret_cast<cudaStream_t>(stream));
+}
+
+int fa_decode_paged_window(const fa_kv_cache *cache, const void *q, void *o, float *lse, int Hq, int Tq, int window_left,
+                           int n_sinks, float scale, void *workspace, size_t workspace_bytes, fa_stream_t stream)
+{
+    bool empty = false;
+    int st = decode_check(cache, q, o, lse, Hq, Tq, scale, 0, workspace, workspace_bytes,
+                          [&] { return fa::paged_workspace_bytes(cache->B, Hq, cache->Hkv, Tq, cache->max_pages * cache->page_size,
+                                                                 cache->d, 0); },
+                          &empty);
+    if (st != FA_OK)
+        return st;
+    if (window_left < -1 || n_sinks < 0)
+        return FA_ERR_INVALID_ARG;
+    if (empty)
+        return FA_OK;
+    if ((st = fa::check_device()) != fa::OK)
+        return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return window_left < 0 ? fa::paged_launch(*cache, q, o, lse, Hq, Tq, 1, scale, 0, workspace, s)
+                           : fa::paged_window_launch(*cache, q, o, lse, Hq, Tq, window_left, n_sinks, scale, workspace, s);
 }
 
 int fa_cache_evict(const fa_kv_cache *cache, int budget, int n_first, int n_recent, float *weight_out, int *order_out,

@@ -46,10 +46,11 @@ uint64_t wait_timeout_ns();     // bounded-wait limit for device spin waits
 //                     first unit; only the drain warpgroup waits for it
 //   WITHHOLD_PAGED_FULL  paged decode, CTA 0: the loader's arrive for its first tile; the math
 //                     warps wait for it, and in a unit longer than the ring the loader for them
+//   WITHHOLD_RANGE_FULL  the same of the paged decode over a part of the entries
 #ifndef FA_TEST_WITHHOLD
 #define FA_TEST_WITHHOLD 0
 #endif
-enum : int { WITHHOLD_NONE = 0, WITHHOLD_FWD_KV = 1, WITHHOLD_FWD_EPI = 2, WITHHOLD_BWD_DKV = 3, WITHHOLD_PAGED_FULL = 4 };
+enum : int { WITHHOLD_NONE = 0, WITHHOLD_FWD_KV = 1, WITHHOLD_FWD_EPI = 2, WITHHOLD_BWD_DKV = 3, WITHHOLD_PAGED_FULL = 4, WITHHOLD_RANGE_FULL = 5 };
 #if FA_TEST_WITHHOLD
 int test_withhold_take(int lo, int hi);   // the armed case if in [lo, hi] (then disarmed), else 0
 #endif
@@ -171,12 +172,15 @@ int evict_launch(const fa_kv_cache &c, int budget, int n_first, int n_recent, fl
 size_t paged_workspace_bytes(int B, int Hq, int Hkv, int Tq, int max_len, int d, int accumulate);
 int paged_launch(const fa_kv_cache &c, const void *q, void *o, float *lse, int Hq, int Tq, int causal, float scale,
                  int accumulate, void *workspace, cudaStream_t s);
+int paged_window_launch(const fa_kv_cache &c, const void *q, void *o, float *lse, int Hq, int Tq, int left, int sinks,
+                        float scale, void *workspace, cudaStream_t s);
 int cache_status_fetch_clear(cudaStream_t s, int *host_word);
 int paged_status_fetch_clear(cudaStream_t s, int *host_word);
+int paged_range_status_fetch_clear(cudaStream_t s, int *host_word);
 
 // The status words of the cache kernels are read from the first launch of one of them in this process
 // on (a captured one may run again at any time): fa_sync_status of a program that has no cache costs no more for them.
-enum StatusWords : int { STATUS_CACHE = 0, STATUS_PAGED = 1 };
+enum StatusWords : int { STATUS_CACHE = 0, STATUS_PAGED = 1, STATUS_RANGE = 2 };
 void status_in_use(StatusWords w);
 
 }  // namespace fa

@@ -22,6 +22,8 @@ typedef int (*append_fn)(const fa_kv_cache *, const fa_heads *, const fa_heads *
                          const int *, const fa_rope_spec *, const fa_head_norm *, const int *, int, fa_stream_t);
 typedef int (*decode_fn)(const fa_kv_cache *, const void *, void *, float *, int, int, int, float, int, void *, size_t,
                          fa_stream_t);
+typedef int (*decode_window_fn)(const fa_kv_cache *, const void *, void *, float *, int, int, int, int, float, void *, size_t,
+                                fa_stream_t);
 typedef int (*evict_fn)(const fa_kv_cache *, int, int, int, float *, int *, int *, int *, fa_stream_t);
 
 static rope_fn call_rope;
@@ -29,6 +31,7 @@ static norm_rope_fn call_norm_rope;
 static append_fn call_append;
 static decode_fn call_decode;
 static evict_fn call_evict;
+static decode_window_fn call_decode_window;
 
 /* torch's dtypes and two of its functions, and the names of attributes */
 static PyObject *t_bf16, *t_f32, *t_i32, *f_stream, *f_device;
@@ -302,36 +305,68 @@ static PyObject *py_append(PyObject *self, PyObject *const *a, Py_ssize_t n)
     return PyLong_FromLong(st);
 }
 
+/* The tensors of a decode over a cache. */
+typedef struct {
+    const fa_kv_cache *c;
+    void *q, *o, *lse, *ws;
+    long long shape[4], bytes, dev;
+    float scale;
+    fa_stream_t stream;
+} decoding;
+
+/* a: cache, index, q, o, lse */
+static int decoding_of(PyObject *const *a, PyObject *scale, PyObject *workspace, PyObject *stream, decoding *r)
+{
+    int ok = 1;
+    r->c = (const fa_kv_cache *)PyLong_AsVoidPtr(a[0]);
+    if (!r->c)
+        return 0;
+    Py_INCREF(a[1]);
+    const long long dev = r->dev = taken_int(a[1], &ok);
+    long long *shape = r->shape;
+    if (!ok || !tuple_of(a[2], n_shape, 0, 4, shape) || shape[0] != r->c->B || shape[1] > INT_MAX || shape[2] > INT_MAX ||
+        shape[3] != r->c->d || !has_dtype(a[2], t_bf16) || !on_device(a[2], dev) || !is_contiguous(a[2]) || !data_of(a[2], &r->q))
+        return 0;
+    r->scale = (float)PyFloat_AsDouble(scale);
+    if (PyErr_Occurred() || !plain(a[3], t_bf16, 4, shape, dev, &r->o) || !plain(a[4], t_f32, 3, shape, dev, &r->lse) ||
+        !on_device(workspace, dev) || !is_contiguous(workspace) || !data_of(workspace, &r->ws))
+        return 0;
+    r->bytes = taken_int(PyObject_GetAttr(workspace, n_nbytes), &ok);
+    return ok && stream_of(stream, a[1], dev, &r->stream);
+}
+
 /* decode(cache, index, q, o, lse, scale, workspace, causal, accumulate, stream) */
 static PyObject *py_decode(PyObject *self, PyObject *const *a, Py_ssize_t n)
 {
     (void)self;
     if (n != 10)
         return PyErr_Format(PyExc_TypeError, "decode: 10 arguments");
-    const fa_kv_cache *c = (const fa_kv_cache *)PyLong_AsVoidPtr(a[0]);
-    if (!c)
-        return slow();
-    int ok = 1;
-    Py_INCREF(a[1]);
-    const long long dev = taken_int(a[1], &ok);
-    void *q, *o, *lse, *ws;
-    fa_stream_t s;
-    long long shape[4];
-    if (!ok || !tuple_of(a[2], n_shape, 0, 4, shape) || shape[0] != c->B || shape[1] > INT_MAX || shape[2] > INT_MAX ||
-        shape[3] != c->d || !has_dtype(a[2], t_bf16) || !on_device(a[2], dev) || !is_contiguous(a[2]) || !data_of(a[2], &q))
-        return slow();
-    const double scale = PyFloat_AsDouble(a[5]);
+    decoding r;
     const int causal = PyObject_IsTrue(a[7]), accumulate = PyObject_IsTrue(a[8]);
-    if (PyErr_Occurred() || !plain(a[3], t_bf16, 4, shape, dev, &o) ||
-        !plain(a[4], t_f32, 3, shape, dev, &lse) || !on_device(a[6], dev) || !is_contiguous(a[6]) || !data_of(a[6], &ws))
-        return slow();
-    const long long bytes = taken_int(PyObject_GetAttr(a[6], n_nbytes), &ok);
-    if (!ok || !stream_of(a[9], a[1], dev, &s))
+    if (causal < 0 || accumulate < 0 || !decoding_of(a, a[5], a[6], a[9], &r))
         return slow();
     int st;
     Py_BEGIN_ALLOW_THREADS;
-    st = call_decode(c, q, o, (float *)lse, (int)shape[1], (int)shape[2], causal, (float)scale, accumulate, ws,
-                     (size_t)bytes, s);
+    st = call_decode(r.c, r.q, r.o, (float *)r.lse, (int)r.shape[1], (int)r.shape[2], causal, r.scale, accumulate, r.ws,
+                     (size_t)r.bytes, r.stream);
+    Py_END_ALLOW_THREADS;
+    return PyLong_FromLong(st);
+}
+
+/* decode_window(cache, index, q, o, lse, window_left, n_sinks, scale, workspace, stream) */
+static PyObject *py_decode_window(PyObject *self, PyObject *const *a, Py_ssize_t n)
+{
+    (void)self;
+    if (n != 10)
+        return PyErr_Format(PyExc_TypeError, "decode_window: 10 arguments");
+    decoding r;
+    int left, sinks;
+    if (!int_arg(a[5], &left) || !int_arg(a[6], &sinks) || !decoding_of(a, a[7], a[8], a[9], &r))
+        return slow();
+    int st;
+    Py_BEGIN_ALLOW_THREADS;
+    st = call_decode_window(r.c, r.q, r.o, (float *)r.lse, (int)r.shape[1], (int)r.shape[2], left, sinks, r.scale, r.ws,
+                            (size_t)r.bytes, r.stream);
     Py_END_ALLOW_THREADS;
     return PyLong_FromLong(st);
 }
@@ -365,7 +400,7 @@ static PyObject *py_evict(PyObject *self, PyObject *const *a, Py_ssize_t n)
     return PyLong_FromLong(st);
 }
 
-enum { ENTRIES = 5 };
+enum { ENTRIES = 6 };
 
 /* setup(bfloat16, float32, int32, stream function, device function, addresses of the entry points) */
 static PyObject *py_setup(PyObject *self, PyObject *const *a, Py_ssize_t n)
@@ -389,6 +424,7 @@ static PyObject *py_setup(PyObject *self, PyObject *const *a, Py_ssize_t n)
     call_append = (append_fn)fn[2];
     call_decode = (decode_fn)fn[3];
     call_evict = (evict_fn)fn[4];
+    call_decode_window = (decode_window_fn)fn[5];
     Py_RETURN_NONE;
 }
 
@@ -398,6 +434,7 @@ static PyMethodDef methods[] = {
     {"norm_rope", (PyCFunction)(void (*)(void))py_norm_rope, METH_FASTCALL, NULL},
     {"append", (PyCFunction)(void (*)(void))py_append, METH_FASTCALL, NULL},
     {"decode", (PyCFunction)(void (*)(void))py_decode, METH_FASTCALL, NULL},
+    {"decode_window", (PyCFunction)(void (*)(void))py_decode_window, METH_FASTCALL, NULL},
     {"evict", (PyCFunction)(void (*)(void))py_evict, METH_FASTCALL, NULL},
     {NULL, NULL, 0, NULL},
 };

@@ -110,6 +110,8 @@ _lib.fa_decode_paged_workspace_bytes.argtypes = [_i] * 8
 _lib.fa_decode_paged_workspace_bytes.restype = _sz
 _lib.fa_decode_paged.argtypes = [_vp, _vp, _vp, _vp, _i, _i, _i, _f, _i, _vp, _sz, _vp]
 _lib.fa_decode_paged.restype = _i
+_lib.fa_decode_paged_window.argtypes = [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _f, _vp, _sz, _vp]
+_lib.fa_decode_paged_window.restype = _i
 _lib.fa_cache_evict.argtypes = [_vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp]
 _lib.fa_cache_evict.restype = _i
 
@@ -547,7 +549,7 @@ _current_device = torch._C._cuda_getDevice
 
 class _Without:
     """Stands for _fa_py where it is missing: no call passes its checks."""
-    rope = norm_rope = append = decode = evict = staticmethod(lambda *args: None)
+    rope = norm_rope = append = decode = decode_window = evict = staticmethod(lambda *args: None)
 
 
 if _fa_py is None:
@@ -556,7 +558,7 @@ else:
     _fast = _fa_py
     _fa_py.setup(torch.bfloat16, torch.float32, torch.int32, _current_stream, _current_device,
                  *(ctypes.cast(f, _vp).value for f in (_lib.fa_rope, _lib.fa_norm_rope, _lib.fa_cache_append_norm, _lib.fa_decode_paged,
-                                                       _lib.fa_cache_evict)))
+                                                       _lib.fa_cache_evict, _lib.fa_decode_paged_window)))
 
 
 def _launch(fn: str, entry, index: int, stream, *args) -> None:
@@ -941,7 +943,8 @@ def fa_decode_paged(cache: KVCache, q, o, lse, scale: float, workspace: torch.Te
         _again(st, "fa_decode_paged", _decode, cache, q, o, lse, scale, workspace, causal, accumulate, stream)
 
 
-def _decode(cache, q, o, lse, scale, workspace, causal, accumulate, stream) -> None:
+def _need_decode(cache, q, o, lse, workspace) -> tuple:
+    """Checks of the decodes' tensors; Hq and Tq."""
     dev, index, shape = cache.device, cache._index, q.shape
     if len(shape) != 4:
         raise ValueError("q must be [B, Hq, Tq, d]")
@@ -957,22 +960,56 @@ def _decode(cache, q, o, lse, scale, workspace, causal, accumulate, stream) -> N
         _need(lse, "lse", torch.float32, shape[:3], dev)
     if workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace: must be a contiguous tensor on the same device")
-    _launch("fa_decode_paged", _lib.fa_decode_paged, index, stream, cache._ref, q.data_ptr(), o.data_ptr(),
+    return Hq, Tq
+
+
+def _decode(cache, q, o, lse, scale, workspace, causal, accumulate, stream) -> None:
+    Hq, Tq = _need_decode(cache, q, o, lse, workspace)
+    _launch("fa_decode_paged", _lib.fa_decode_paged, cache._index, stream, cache._ref, q.data_ptr(), o.data_ptr(),
             lse.data_ptr(), Hq, Tq, int(bool(causal)), scale, int(bool(accumulate)), workspace.data_ptr(),
             workspace.nbytes)
 
 
+def fa_decode_paged_window_workspace_bytes(cache: KVCache, Hq: int, Tq: int = 1) -> int:
+    """Workspace of fa_decode_paged_window for these sizes, 0 for sizes that it refuses."""
+    return fa_decode_paged_workspace_bytes(cache, Hq, Tq)
+
+
+def fa_decode_paged_window(cache: KVCache, q, o, lse, window_left: int, n_sinks: int, scale: float, workspace: torch.Tensor,
+                           stream=None) -> None:
+    """fa_decode_paged (causal) under a window of window_left + 1 slots (-1: no left bound) and the first n_sinks
+    slots; pages that no row sees are not read."""
+    st = _fast.decode_window(cache._ref, cache._index, q, o, lse, window_left, n_sinks, scale, workspace, stream)
+    if st != FA_OK:
+        _again(st, "fa_decode_paged_window", _decode_window, cache, q, o, lse, window_left, n_sinks, scale, workspace, stream)
+
+
+def _decode_window(cache, q, o, lse, window_left, n_sinks, scale, workspace, stream) -> None:
+    Hq, Tq = _need_decode(cache, q, o, lse, workspace)
+    _launch("fa_decode_paged_window", _lib.fa_decode_paged_window, cache._index, stream, cache._ref, q.data_ptr(), o.data_ptr(),
+            lse.data_ptr(), Hq, Tq, int(window_left), int(n_sinks), scale, workspace.data_ptr(), workspace.nbytes)
+
+
 def attention_decode_paged(cache: KVCache, q, scale: float, causal: bool = True, accumulate: bool = False,
-                           workspace=None, stream=None):
-    """Allocates O, lse (and the workspace if not given) and runs fa_decode_paged."""
+                           workspace=None, stream=None, window=None, sinks: int = 0):
+    """Allocates O, lse (and the workspace if not given) and runs fa_decode_paged; with a window (left, 0),
+    and sinks, fa_decode_paged_window."""
     if q.dim() != 4:
         raise ValueError("q must be [B, Hq, Tq, d]")
+    if window is None and sinks and not causal:
+        raise ValueError("sinks: give a window, or causal rows")
+    if window is not None and (window[1] != 0 or not causal or accumulate):
+        raise ValueError("window: (left, 0) with causal rows and without accumulated weights")
     specs = [(q.shape, q.dtype), (q.shape[:3], torch.float32)]
     if workspace is None:
         n = fa_decode_paged_workspace_bytes(cache, q.shape[1], q.shape[2], accumulate)
         specs.append(((max(n, 256),), torch.uint8))
     o, lse, *own = _empties(stream, q.device, *specs)
-    fa_decode_paged(cache, q, o, lse, scale, own[0] if own else workspace, causal, accumulate, stream)
+    workspace = own[0] if own else workspace
+    if window is None:   # sinks are part of what causal rows see
+        fa_decode_paged(cache, q, o, lse, scale, workspace, causal, accumulate, stream)
+    else:
+        fa_decode_paged_window(cache, q, o, lse, window[0], sinks, scale, workspace, stream)
     return o, lse
 
 

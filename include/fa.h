@@ -367,6 +367,19 @@ int fa_decode_paged(const fa_kv_cache *cache, const void *q, void *o, float *lse
                     float scale, int accumulate, void *workspace, size_t workspace_bytes, fa_stream_t stream);
 
 /*
+ * fa_decode_paged, causal, under a sliding window with sinks: the row at position p = lens[b] - Tq + t sees
+ * slot j iff
+ *     j <= p  and  (j >= p - window_left  or  j < n_sinks)
+ * (window_left -1: no left bound).  Slots, not arrival numbers: in a cache that fa_cache_evict has reordered
+ * the two differ.  Time goes with the visible slots, not with lens.  Pages without a slot that some row sees are not
+ * read and their table entries not looked at: they may have been given back.  No accumulated weights.
+ * workspace: fa_decode_paged_workspace_bytes(..., accumulate = 0); other arguments, results and errors as there.
+ */
+int fa_decode_paged_window(const fa_kv_cache *cache, const void *q, void *o, float *lse, int Hq, int Tq,
+                           int window_left, int n_sinks, float scale, void *workspace, size_t workspace_bytes,
+                           fa_stream_t stream);
+
+/*
  * Evicts, for every sequence and KV head on its own, down to `budget` (1 to 2^30)
  * entries.  Kept are the min(lens, budget) first ones in this order: protected
  * entries (arrival number below n_first, or at least seen - n_recent), then by
