@@ -635,7 +635,7 @@ int fa_bwd_stage(int stage, const void *q, const void *k, const void *v, const v
 // out of range.
 static int fetch_status(cudaStream_t s, int *word)
 {
-    int w[6] = {0, 0, 0, 0, 0, 0};
+    int w[7] = {0, 0, 0, 0, 0, 0, 0};
     if (fa::fwd_status_fetch_clear(s, &w[0]) != fa::OK || fa::bwd_status_fetch_clear(s, &w[1]) != fa::OK ||
         fa::dec_status_fetch_clear(s, &w[2]) != fa::OK)
         return fa::ERR_CUDA;
@@ -643,9 +643,11 @@ static int fetch_status(cudaStream_t s, int *word)
         return fa::ERR_CUDA;
     if (fa::status_is_in_use(fa::STATUS_RANGE) && fa::paged_range_status_fetch_clear(s, &w[5]) != fa::OK)
         return fa::ERR_CUDA;
+    if (fa::status_is_in_use(fa::STATUS_PREFIX) && fa::prefix_status_fetch_clear(s, &w[6]) != fa::OK)
+        return fa::ERR_CUDA;
     if (fa::status_is_in_use(fa::STATUS_CACHE) && fa::cache_status_fetch_clear(s, &w[4]) != fa::OK)
         return fa::ERR_CUDA;
-    for (int i = 0; i < 6; ++i)
+    for (int i = 0; i < 7; ++i)
         if (*word == 0 || ((w[i] & 0xFF) == fa::ERR_TIMEOUT && (*word & 0xFF) != fa::ERR_TIMEOUT))
             *word = w[i];
     return fa::OK;

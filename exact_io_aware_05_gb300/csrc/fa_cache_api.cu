@@ -504,6 +504,48 @@ int fa_decode_paged_window(const fa_kv_cache *cache, const void *q, void *o, flo
                            : fa::paged_window_launch(*cache, q, o, lse, Hq, Tq, window_left, n_sinks, scale, workspace, s);
 }
 
+size_t fa_decode_paged_shared_workspace_bytes(int B, int Hq, int Hkv, int Tq, int max_pages, int page_size, int d, int dtype,
+                                              int n_prefix_pages)
+{
+    if (!paged_sizes_ok(B, Hq, Hkv, Tq, max_pages, page_size, d) || (dtype != FA_BF16 && dtype != FA_E4M3) || n_prefix_pages < 0 ||
+        n_prefix_pages > max_pages)
+        return 0;
+    const size_t n = fa::prefix_workspace_bytes(B, Hq, Hkv, Tq, max_pages * page_size, d, dtype == FA_E4M3, n_prefix_pages, page_size);
+    return n > 256 ? n : 256;
+}
+
+int fa_decode_paged_shared(const fa_kv_cache *cache, const void *q, void *o, float *lse, int Hq, int Tq, int causal,
+                           const int *prefix_pages, int n_prefix_pages, float scale, void *workspace, size_t workspace_bytes,
+                           fa_stream_t stream)
+{
+    bool empty = false;
+    int st = decode_check(cache, q, o, lse, Hq, Tq, scale, 0, workspace, workspace_bytes,
+                          [&] {
+                              return n_prefix_pages < 0 || n_prefix_pages > cache->max_pages
+                                         ? ~(size_t)0
+                                         : fa::prefix_workspace_bytes(cache->B, Hq, cache->Hkv, Tq, cache->max_pages * cache->page_size,
+                                                                      cache->d, cache->dtype == FA_E4M3, n_prefix_pages, cache->page_size);
+                          },
+                          &empty);
+    if (st != FA_OK)
+        return st;
+    if (causal < 0 || causal > 1 || n_prefix_pages < 0 || n_prefix_pages > cache->max_pages)
+        return FA_ERR_INVALID_ARG;
+    if (empty)
+        return FA_OK;
+    const size_t np = (size_t)n_prefix_pages * 4, rows = (size_t)cache->B * Hq * Tq;
+    if ((n_prefix_pages > 0 && !prefix_pages) || (reinterpret_cast<uintptr_t>(prefix_pages) & 3u) ||
+        fa::overlaps(prefix_pages, np, o, rows * cache->d * 2) || fa::overlaps(prefix_pages, np, lse, rows * 4) ||
+        fa::overlaps(prefix_pages, np, workspace, workspace_bytes))
+        return FA_ERR_INVALID_ARG;
+    if ((st = fa::check_device()) != fa::OK)
+        return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return n_prefix_pages == 0 || cache->num_pages == 0
+               ? fa::paged_launch(*cache, q, o, lse, Hq, Tq, causal, scale, 0, workspace, s)
+               : fa::prefix_launch(*cache, q, o, lse, Hq, Tq, causal, prefix_pages, n_prefix_pages, scale, workspace, s);
+}
+
 int fa_cache_evict(const fa_kv_cache *cache, int budget, int n_first, int n_recent, float *weight_out, int *order_out,
                    int *lens_out, int *kept, fa_stream_t stream)
 {

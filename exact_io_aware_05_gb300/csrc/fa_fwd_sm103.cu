@@ -202,11 +202,13 @@ __device__ __forceinline__ bool tile_active(const TileRange &r, int j)
 template <int BC, int MASK>
 __device__ __forceinline__ int next_active(const TileRange &r, int j)
 {
-    if constexpr (MASK == kSinks)   // over the blocks between the sinks and the window in one step
+    if constexpr (MASK == kSinks) {   // over the blocks between the sinks and the window in one step
         return j >= r.ns && j < r.lo ? r.lo : j;
-    while (j <= r.hi && !tile_active<BC, MASK>(r, j))
-        ++j;
-    return j;
+    } else {
+        while (j <= r.hi && !tile_active<BC, MASK>(r, j))
+            ++j;
+        return j;
+    }
 }
 
 // kPlain: no left bound and no block mask, so every tile visits a prefix

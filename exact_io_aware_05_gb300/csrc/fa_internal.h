@@ -47,10 +47,12 @@ uint64_t wait_timeout_ns();     // bounded-wait limit for device spin waits
 //   WITHHOLD_PAGED_FULL  paged decode, CTA 0: the loader's arrive for its first tile; the math
 //                     warps wait for it, and in a unit longer than the ring the loader for them
 //   WITHHOLD_RANGE_FULL  the same of the paged decode over a part of the entries
+//   WITHHOLD_PREFIX_FULL  the same of the shared prefix's attention
 #ifndef FA_TEST_WITHHOLD
 #define FA_TEST_WITHHOLD 0
 #endif
-enum : int { WITHHOLD_NONE = 0, WITHHOLD_FWD_KV = 1, WITHHOLD_FWD_EPI = 2, WITHHOLD_BWD_DKV = 3, WITHHOLD_PAGED_FULL = 4, WITHHOLD_RANGE_FULL = 5 };
+enum : int { WITHHOLD_NONE = 0, WITHHOLD_FWD_KV = 1, WITHHOLD_FWD_EPI = 2, WITHHOLD_BWD_DKV = 3, WITHHOLD_PAGED_FULL = 4, WITHHOLD_RANGE_FULL = 5,
+                 WITHHOLD_PREFIX_FULL = 6 };
 #if FA_TEST_WITHHOLD
 int test_withhold_take(int lo, int hi);   // the armed case if in [lo, hi] (then disarmed), else 0
 #endif
@@ -174,13 +176,20 @@ int paged_launch(const fa_kv_cache &c, const void *q, void *o, float *lse, int H
                  int accumulate, void *workspace, cudaStream_t s);
 int paged_window_launch(const fa_kv_cache &c, const void *q, void *o, float *lse, int Hq, int Tq, int left, int sinks,
                         float scale, void *workspace, cudaStream_t s);
+int paged_behind_launch(const fa_kv_cache &c, const void *q, float *o, float *lse, int Hq, int Tq, int causal, int base, float scale,
+                        void *workspace, cudaStream_t s);
+// Attention over a shared prefix and the entries behind it (fa_prefix_sm103.cu); n_pages > 0, pages of the prefix.
+size_t prefix_workspace_bytes(int B, int Hq, int Hkv, int Tq, int max_len, int d, int codes, int n_pages, int page_size);
+int prefix_launch(const fa_kv_cache &c, const void *q, void *o, float *lse, int Hq, int Tq, int causal, const int *pages,
+                  int n_pages, float scale, void *workspace, cudaStream_t s);
 int cache_status_fetch_clear(cudaStream_t s, int *host_word);
 int paged_status_fetch_clear(cudaStream_t s, int *host_word);
 int paged_range_status_fetch_clear(cudaStream_t s, int *host_word);
+int prefix_status_fetch_clear(cudaStream_t s, int *host_word);
 
 // The status words of the cache kernels are read from the first launch of one of them in this process
 // on (a captured one may run again at any time): fa_sync_status of a program that has no cache costs no more for them.
-enum StatusWords : int { STATUS_CACHE = 0, STATUS_PAGED = 1, STATUS_RANGE = 2 };
+enum StatusWords : int { STATUS_CACHE = 0, STATUS_PAGED = 1, STATUS_RANGE = 2, STATUS_PREFIX = 3 };
 void status_in_use(StatusWords w);
 
 }  // namespace fa

@@ -34,6 +34,20 @@ int paged_window_launch(const fa_kv_cache &c, const void *q, void *o, float *lse
     return run(c, a, s);
 }
 
+// The entries from slot `base` on; o in fp32.
+int paged_behind_launch(const fa_kv_cache &c, const void *q, float *o, float *lse, int Hq, int Tq, int causal, int base, float scale,
+                        void *workspace, cudaStream_t s)
+{
+    status_in_use(STATUS_RANGE);
+    PagedArgs a = paged_args(c, q, nullptr, lse, Hq, Tq, causal, scale, workspace);
+    a.left = -1;
+    a.sinks = 0;
+    a.base = std::min(base, a.cap);
+    a.span = a.cap - a.base;
+    a.o32 = o;
+    return run(c, a, s);
+}
+
 int paged_range_status_fetch_clear(cudaStream_t s, int *host_word) { return paged_words_fetch_clear(s, host_word); }
 
 }  // namespace fa

@@ -24,6 +24,8 @@ typedef int (*decode_fn)(const fa_kv_cache *, const void *, void *, float *, int
                          fa_stream_t);
 typedef int (*decode_window_fn)(const fa_kv_cache *, const void *, void *, float *, int, int, int, int, float, void *, size_t,
                                 fa_stream_t);
+typedef int (*decode_shared_fn)(const fa_kv_cache *, const void *, void *, float *, int, int, int, const int *, int, float, void *,
+                                size_t, fa_stream_t);
 typedef int (*evict_fn)(const fa_kv_cache *, int, int, int, float *, int *, int *, int *, fa_stream_t);
 
 static rope_fn call_rope;
@@ -32,6 +34,7 @@ static append_fn call_append;
 static decode_fn call_decode;
 static evict_fn call_evict;
 static decode_window_fn call_decode_window;
+static decode_shared_fn call_decode_shared;
 
 /* torch's dtypes and two of its functions, and the names of attributes */
 static PyObject *t_bf16, *t_f32, *t_i32, *f_stream, *f_device;
@@ -371,6 +374,27 @@ static PyObject *py_decode_window(PyObject *self, PyObject *const *a, Py_ssize_t
     return PyLong_FromLong(st);
 }
 
+/* decode_shared(cache, index, q, o, lse, prefix_pages, scale, workspace, causal, stream) */
+static PyObject *py_decode_shared(PyObject *self, PyObject *const *a, Py_ssize_t n)
+{
+    (void)self;
+    if (n != 10)
+        return PyErr_Format(PyExc_TypeError, "decode_shared: 10 arguments");
+    decoding r;
+    void *pages;
+    long long count[1];
+    const int causal = PyObject_IsTrue(a[8]);
+    if (causal < 0 || !decoding_of(a, a[6], a[7], a[9], &r) || !tuple_of(a[5], n_shape, 0, 1, count) || count[0] > INT_MAX ||
+        !plain(a[5], t_i32, 1, count, r.dev, &pages))
+        return slow();
+    int st;
+    Py_BEGIN_ALLOW_THREADS;
+    st = call_decode_shared(r.c, r.q, r.o, (float *)r.lse, (int)r.shape[1], (int)r.shape[2], causal, (const int *)pages, (int)count[0],
+                            r.scale, r.ws, (size_t)r.bytes, r.stream);
+    Py_END_ALLOW_THREADS;
+    return PyLong_FromLong(st);
+}
+
 /* evict(cache, index, budget, weight_out, order_out, lens_out, kept, n_first, n_recent, stream) */
 static PyObject *py_evict(PyObject *self, PyObject *const *a, Py_ssize_t n)
 {
@@ -400,7 +424,7 @@ static PyObject *py_evict(PyObject *self, PyObject *const *a, Py_ssize_t n)
     return PyLong_FromLong(st);
 }
 
-enum { ENTRIES = 6 };
+enum { ENTRIES = 7 };
 
 /* setup(bfloat16, float32, int32, stream function, device function, addresses of the entry points) */
 static PyObject *py_setup(PyObject *self, PyObject *const *a, Py_ssize_t n)
@@ -425,6 +449,7 @@ static PyObject *py_setup(PyObject *self, PyObject *const *a, Py_ssize_t n)
     call_decode = (decode_fn)fn[3];
     call_evict = (evict_fn)fn[4];
     call_decode_window = (decode_window_fn)fn[5];
+    call_decode_shared = (decode_shared_fn)fn[6];
     Py_RETURN_NONE;
 }
 
@@ -435,6 +460,7 @@ static PyMethodDef methods[] = {
     {"append", (PyCFunction)(void (*)(void))py_append, METH_FASTCALL, NULL},
     {"decode", (PyCFunction)(void (*)(void))py_decode, METH_FASTCALL, NULL},
     {"decode_window", (PyCFunction)(void (*)(void))py_decode_window, METH_FASTCALL, NULL},
+    {"decode_shared", (PyCFunction)(void (*)(void))py_decode_shared, METH_FASTCALL, NULL},
     {"evict", (PyCFunction)(void (*)(void))py_evict, METH_FASTCALL, NULL},
     {NULL, NULL, 0, NULL},
 };

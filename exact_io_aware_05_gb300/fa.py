@@ -112,6 +112,10 @@ _lib.fa_decode_paged.argtypes = [_vp, _vp, _vp, _vp, _i, _i, _i, _f, _i, _vp, _s
 _lib.fa_decode_paged.restype = _i
 _lib.fa_decode_paged_window.argtypes = [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _f, _vp, _sz, _vp]
 _lib.fa_decode_paged_window.restype = _i
+_lib.fa_decode_paged_shared_workspace_bytes.argtypes = [_i] * 9
+_lib.fa_decode_paged_shared_workspace_bytes.restype = _sz
+_lib.fa_decode_paged_shared.argtypes = [_vp, _vp, _vp, _vp, _i, _i, _i, _vp, _i, _f, _vp, _sz, _vp]
+_lib.fa_decode_paged_shared.restype = _i
 _lib.fa_cache_evict.argtypes = [_vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp]
 _lib.fa_cache_evict.restype = _i
 
@@ -549,7 +553,7 @@ _current_device = torch._C._cuda_getDevice
 
 class _Without:
     """Stands for _fa_py where it is missing: no call passes its checks."""
-    rope = norm_rope = append = decode = decode_window = evict = staticmethod(lambda *args: None)
+    rope = norm_rope = append = decode = decode_window = decode_shared = evict = staticmethod(lambda *args: None)
 
 
 if _fa_py is None:
@@ -558,7 +562,7 @@ else:
     _fast = _fa_py
     _fa_py.setup(torch.bfloat16, torch.float32, torch.int32, _current_stream, _current_device,
                  *(ctypes.cast(f, _vp).value for f in (_lib.fa_rope, _lib.fa_norm_rope, _lib.fa_cache_append_norm, _lib.fa_decode_paged,
-                                                       _lib.fa_cache_evict, _lib.fa_decode_paged_window)))
+                                                       _lib.fa_cache_evict, _lib.fa_decode_paged_window, _lib.fa_decode_paged_shared)))
 
 
 def _launch(fn: str, entry, index: int, stream, *args) -> None:
@@ -990,23 +994,53 @@ def _decode_window(cache, q, o, lse, window_left, n_sinks, scale, workspace, str
             lse.data_ptr(), Hq, Tq, int(window_left), int(n_sinks), scale, workspace.data_ptr(), workspace.nbytes)
 
 
+def fa_decode_paged_shared_workspace_bytes(cache: KVCache, Hq: int, Tq: int, prefix_pages: torch.Tensor) -> int:
+    """Workspace of fa_decode_paged_shared for these sizes, 0 for sizes that it refuses."""
+    return int(_lib.fa_decode_paged_shared_workspace_bytes(cache.B, Hq, cache.Hkv, Tq, cache.max_pages, cache.page_size, cache.d,
+                                                           cache._c.dtype, prefix_pages.numel()))
+
+
+def fa_decode_paged_shared(cache: KVCache, q, o, lse, prefix_pages: torch.Tensor, scale: float, workspace: torch.Tensor,
+                           causal: bool = True, stream=None) -> None:
+    """fa_decode_paged for a batch whose sequences all begin with the same full pages, prefix_pages (int32 [n], the first
+    n entries of each sequence's block table): they are read once for all of them."""
+    st = _fast.decode_shared(cache._ref, cache._index, q, o, lse, prefix_pages, scale, workspace, causal, stream)
+    if st != FA_OK:
+        _again(st, "fa_decode_paged_shared", _decode_shared, cache, q, o, lse, prefix_pages, scale, workspace, causal, stream)
+
+
+def _decode_shared(cache, q, o, lse, prefix_pages, scale, workspace, causal, stream) -> None:
+    Hq, Tq = _need_decode(cache, q, o, lse, workspace)
+    if prefix_pages.dim() != 1:
+        raise ValueError("prefix_pages: expected one dimension")
+    _need(prefix_pages, "prefix_pages", torch.int32, prefix_pages.shape, cache.device)
+    _launch("fa_decode_paged_shared", _lib.fa_decode_paged_shared, cache._index, stream, cache._ref, q.data_ptr(), o.data_ptr(),
+            lse.data_ptr(), Hq, Tq, int(bool(causal)), prefix_pages.data_ptr(), prefix_pages.shape[0], scale, workspace.data_ptr(),
+            workspace.nbytes)
+
+
 def attention_decode_paged(cache: KVCache, q, scale: float, causal: bool = True, accumulate: bool = False,
-                           workspace=None, stream=None, window=None, sinks: int = 0):
+                           workspace=None, stream=None, window=None, sinks: int = 0, prefix_pages=None):
     """Allocates O, lse (and the workspace if not given) and runs fa_decode_paged; with a window (left, 0),
-    and sinks, fa_decode_paged_window."""
+    and sinks, fa_decode_paged_window; with prefix_pages, fa_decode_paged_shared."""
     if q.dim() != 4:
         raise ValueError("q must be [B, Hq, Tq, d]")
     if window is None and sinks and not causal:
         raise ValueError("sinks: give a window, or causal rows")
     if window is not None and (window[1] != 0 or not causal or accumulate):
         raise ValueError("window: (left, 0) with causal rows and without accumulated weights")
+    if prefix_pages is not None and (window is not None or accumulate):
+        raise ValueError("prefix_pages: without a window and accumulated weights")
     specs = [(q.shape, q.dtype), (q.shape[:3], torch.float32)]
     if workspace is None:
-        n = fa_decode_paged_workspace_bytes(cache, q.shape[1], q.shape[2], accumulate)
+        n = (fa_decode_paged_workspace_bytes(cache, q.shape[1], q.shape[2], accumulate) if prefix_pages is None else
+             fa_decode_paged_shared_workspace_bytes(cache, q.shape[1], q.shape[2], prefix_pages))
         specs.append(((max(n, 256),), torch.uint8))
     o, lse, *own = _empties(stream, q.device, *specs)
     workspace = own[0] if own else workspace
-    if window is None:   # sinks are part of what causal rows see
+    if prefix_pages is not None:
+        fa_decode_paged_shared(cache, q, o, lse, prefix_pages, scale, workspace, causal, stream)
+    elif window is None:   # sinks are part of what causal rows see
         fa_decode_paged(cache, q, o, lse, scale, workspace, causal, accumulate, stream)
     else:
         fa_decode_paged_window(cache, q, o, lse, window[0], sinks, scale, workspace, stream)
