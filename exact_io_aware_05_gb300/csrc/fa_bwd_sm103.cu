@@ -123,7 +123,7 @@ struct BwdArgs {
     // sinks instance: the left bound does not hold for keys below sinks.  Their nsb key blocks see every
     // query block behind them, the others a window's: with parts > 1 each of them is so many units, which
     // leave fp32 dV and dK (x scale) in sink_part, [head][sink block][part][dV, dK][128][D]
-    int sinks, nsb, parts;
+    int sinks, nsb, parts, part_len;
     float *sink_part;
 };
 
@@ -179,10 +179,14 @@ __device__ __forceinline__ Unit make_unit(int u, const BwdArgs &a)
     x.j = lvl;
     x.part = -1;
     if constexpr (MASK == kSinks) {
-        const int split = a.nsb * a.parts;   // the sinks' parts come first
-        x.j = lvl < split ? lvl / a.parts : lvl - a.nsb * (a.parts - 1);
-        if (lvl < split && a.parts > 1)
+        // The sinks' parts come first.  No division in the usual case, and none of 64 bits: every role
+        // finds its units by itself, and between units they wait for it (B8 H32 T1152 d128 284 us with them, 251)
+        if (lvl >= a.nsb * a.parts) {
+            x.j = lvl - a.nsb * (a.parts - 1);
+        } else if (a.parts > 1) {
+            x.j = a.nsb == 1 ? 0 : lvl / a.parts;
             x.part = lvl - x.j * a.parts;
+        }
     }
     const int nqb = (a.Tq + BQ - 1) / BQ;
     int first_row = 0;
@@ -225,11 +229,10 @@ __device__ __forceinline__ Unit make_unit(int u, const BwdArgs &a)
             x.nq = x.i1 - x.i0 + 1;
         }
         if constexpr (MASK == kSinks) {
-            if (x.part >= 0) {   // an equal share of the query blocks (none, where there are fewer than parts)
-                const int from = (int)((long)x.nq * x.part / a.parts), to = (int)((long)x.nq * (x.part + 1) / a.parts);
-                x.i1 = x.i0 + to - 1;
-                x.i0 += from;
-                x.nq = to - from;
+            if (x.part >= 0) {   // part_len query blocks of them (fewer, or none, at the end)
+                x.i0 += x.part * a.part_len;
+                x.nq = max(0, min(x.nq - x.part * a.part_len, a.part_len));
+                x.i1 = x.i0 + x.nq - 1;
             }
         }
     }
@@ -631,7 +634,27 @@ __global__ void __launch_bounds__(512, 1)
                 tmem_wait_ld_x32(p0);
                 tmem_wait_ld_x32(p1);
                 const float4 *nl4 = reinterpret_cast<const float4 *>(smem + L::OFF_LSE) + half * 16;
-                if (mask) {
+                if (MASK == kSinks && mask) {
+                    // 32 queries at a time: all keys of the warp are seen by all of them, none by any, or in part
+                    auto part = [&](uint32_t(&p)[32], const float4 *nl, int q0) {
+                        if (__all_sync(0xffffffffu, qmin >= q0 + 32 || qmax <= q0)) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                p[e] = 0u;
+                        } else if (__all_sync(0xffffffffu, qmin <= q0 && qmax >= q0 + 32)) {
+                            softmax_p32<false>(p, nl, sl2, 0, 0, 64);
+                        } else {   // a bit a query: one select each in place of two comparisons
+                            auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
+                            const uint32_t w = below(qmax - q0) & ~below(qmin - q0);
+                            softmax_p32<false>(p, nl, sl2, 0, 0, 64);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                p[e] = (w & (1u << e)) ? p[e] : 0u;
+                        }
+                    };
+                    part(p0, nl4, 0);
+                    part(p1, nl4 + 8, 32);
+                } else if (mask) {
                     softmax_p32<true>(p0, nl4, sl2, 0, qmin, qmax);
                     softmax_p32<true>(p1, nl4 + 8, sl2, 32, qmin, qmax);
                 } else {
@@ -705,11 +728,11 @@ __global__ void __launch_bounds__(512, 1)
             const Unit x = make_unit<MASK>(u, a);
             const int l = x.j * BK + row;
             const size_t krow = (size_t)x.bh * a.Tk + l;
-            // a part's rows of dV, and of dK 128 rows on
-            float *part = MASK == kSinks && x.part >= 0
-                              ? a.sink_part + (((((size_t)x.bh * a.nsb + x.j) * a.parts + x.part) * 2) * BK + row) * D
-                              : nullptr;
+            auto part_of = [&]() {   // a part's rows of dV, and of dK 128 rows on: this thread's
+                return a.sink_part + (((((size_t)x.bh * a.nsb + x.j) * a.parts + x.part) * 2) * BK + row) * D;
+            };
             if (MASK == kSinks && x.nq == 0 && x.part >= 0) {
+                float *part = part_of();
                 for (int e = 0; e < D / 4; ++e)
                     reinterpret_cast<float4 *>(part)[e] = reinterpret_cast<float4 *>(part + (size_t)BK * D)[e] =
                         make_float4(0.f, 0.f, 0.f, 0.f);
@@ -837,22 +860,40 @@ __global__ void __launch_bounds__(512, 1)
             if (!kv_ok)
                 break;
             tc_fence_after();
-            if (MASK == kSinks && x.part >= 0) {   // fp32, for the sum over the parts
+            if (MASK == kSinks && x.part >= 0) {
+                // fp32, for the sum over the parts: 32 rows x 32 features at a time through the warp's staging
+                // buffer, so that its stores are whole lines (a thread's own row would be 32 lines a store)
+                if (lane == 0)
+                    bulk_wait_read_all();   // this warp's dQ chunks have been read
+                __syncwarp();
+                uint8_t *stage = smem + L::OFF_STG + quarter * 8192u;
+                float *part = part_of() - (size_t)lane * D;   // the warp's first row
 #pragma unroll
                 for (int w = 0; w < 2; ++w)
 #pragma unroll
                     for (int c = 0; c < D / 32; ++c) {
                         uint32_t v[32];
                         tmem_ld_x32(lane_base + (w ? L::T_DK : L::T_DV) + c * 32, v);
+                        if (w == 1 && c == D / 32 - 1) {
+                            tc_fence_before();
+                            mbar_arrive(bar(L::B_DKVEMPTY));   // dV and dK are out of tensor memory
+                        }
+                        uint8_t *buf = stage + (c & 1) * 4096;
                         const float f = w ? a.scale : 1.f;
-                        float4 *dst = reinterpret_cast<float4 *>(part + (size_t)w * BK * D + c * 32);
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
-                            dst[e] = make_float4(__uint_as_float(v[4 * e]) * f, __uint_as_float(v[4 * e + 1]) * f,
-                                                 __uint_as_float(v[4 * e + 2]) * f, __uint_as_float(v[4 * e + 3]) * f);
+                            *reinterpret_cast<float4 *>(buf + lane * 128 + ((e ^ (lane & 7)) << 4)) =
+                                make_float4(__uint_as_float(v[4 * e]) * f, __uint_as_float(v[4 * e + 1]) * f,
+                                            __uint_as_float(v[4 * e + 2]) * f, __uint_as_float(v[4 * e + 3]) * f);
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int r = 4 * i + (int)(lane >> 3), e = (int)(lane & 7);
+                            *reinterpret_cast<float4 *>(part + ((size_t)w * BK + r) * D + c * 32 + 4 * e) =
+                                *reinterpret_cast<const float4 *>(buf + r * 128 + ((e ^ (r & 7)) << 4));
+                        }
                     }
-                tc_fence_before();
-                mbar_arrive(bar(L::B_DKVEMPTY));
+                __syncwarp();   // the buffer is free again for the next unit's dQ
                 ++nu;
                 continue;
             }
@@ -1206,7 +1247,8 @@ int launch_bwd(const void *q, const void *k, const void *v, const void *o, const
         a.sinks = mask.sinks < Tk ? mask.sinks : Tk;
         const bool sinks = mask.left >= 0 && a.sinks > 0;
         a.nsb = sinks ? (a.sinks + BK - 1) / BK : 0;
-        a.parts = sinks ? bwd_sink_parts(BH, Tq, Tk, mask) : 1;
+        a.parts = sinks ? bwd_sink_parts(Tq, Tk, mask) : 1;
+        a.part_len = ((Tq + BQ - 1) / BQ + a.parts - 1) / a.parts;
         a.sink_part = ws.sink_part;
         const long long units = (long long)BH * (a.nkb + (long long)a.nsb * (a.parts - 1));
         if (units > 0x7fffffffll)
@@ -1262,24 +1304,23 @@ int launch_bwd(const void *q, const void *k, const void *v, const void *o, const
 }  // namespace
 
 // Units that a key block with sinks is cut into.  It sees all nqb query blocks behind it, a window's block about
-// wq: in one piece it would keep one CTA busy when the others have ended, so a part is at most a window's
-// block or an eighth of a CTA's whole share, whichever is more.  Of sizes only: the sums' order, and the
-// workspace, do not depend on the device.
-int bwd_sink_parts(int BH, int Tq, int Tk, const MaskSpec &mask)
+// wq: in one piece it would keep one CTA busy when the others have ended (65536 rows, 6 heads of 64, window 512: 1417 us
+// in one piece, 373 in 64), so a part is as long as a window's block, but not shorter than 8, below which its
+// start and its sums cost more (B2 H16 T8192 d128, window 256: 329 us by 3, 308 by 8, 328 by 16).  Of sizes only: the
+// sums' order, and the workspace, do not depend on the device.
+int bwd_sink_parts(int Tq, int Tk, const MaskSpec &mask)
 {
-    const long long nqb = (Tq + BQ - 1) / BQ, nkb = (Tk + BK - 1) / BK;
+    const long long nqb = (Tq + BQ - 1) / BQ;
     const int sinks = mask.sinks < Tk ? mask.sinks : Tk;
     if (mask.left < 0 || sinks <= 0)
         return 1;
-    const long long nsb = (sinks + BK - 1) / BK, wq = std::min<long long>(mask.left / BQ + 2, nqb);
-    const long long share = BH * (nkb * wq + nsb * nqb) / 152;
-    const long long most = std::max(std::max(wq, share / 8), 1ll);
+    const long long wq = std::min<long long>(mask.left / BQ + 2, nqb), most = std::max(wq, 8ll);
     return (int)std::min<long long>(std::max((nqb + most - 1) / most, 1ll), 64);
 }
 
 size_t bwd_sink_bytes(size_t BH, int Tq, int Tk, int d, const MaskSpec &mask)
 {
-    const int parts = bwd_sink_parts((int)BH, Tq, Tk, mask);
+    const int parts = bwd_sink_parts(Tq, Tk, mask);
     if (parts == 1)
         return 0;
     const int sinks = mask.sinks < Tk ? mask.sinks : Tk;

@@ -183,6 +183,7 @@ struct Plan {
     TileRange tr0, tr1;      // tiles 0 and 1
     int J;                   // jobs (one S and one PV MMA each) in the unit
     int js, je;              // first and last KV block any tile visits
+    int us, ul;              // kSinks: they are blocks 0 .. us - 1 and ul .. je
 };
 
 // Tile t's range, chosen with a select (no run-time array indexing).
@@ -311,6 +312,13 @@ __device__ __forceinline__ Plan make_plan(int u, const FwdArgs &a)
             else
                 p.tr1 = tr;
         }
+        if constexpr (MASK == kSinks) {
+            // the tiles' windows follow one another without a gap, and so do the sinks of the later one; a tile
+            // without a block (rows in front of every key, or none) has no part in it
+            const bool a0 = p.tr0.n > 0, a1 = p.tr1.n > 0;
+            p.us = max(a0 ? p.tr0.ns : 0, a1 ? p.tr1.ns : 0);
+            p.ul = min(a0 ? p.tr0.lo : 1 << 30, a1 ? p.tr1.lo : 1 << 30);
+        }
         return p;
     }
 }
@@ -321,13 +329,9 @@ __device__ __forceinline__ Plan make_plan(int u, const FwdArgs &a)
 template <int BC, int MASK>
 __device__ __forceinline__ int union_next(const Plan &p, int j)
 {
-    if constexpr (MASK == kSinks) {
-        // the tile below has the later window; a tile without a block visits none
-        const int j0 = next_active<BC, MASK>(p.tr0, j), j1 = next_active<BC, MASK>(p.tr1, j);
-        const int x = p.tr0.n > 0 && j0 <= p.tr0.hi ? j0 : p.je + 1, y = p.tr1.n > 0 && j1 <= p.tr1.hi ? j1 : p.je + 1;
-        return min(x, y);
-    }
-    if constexpr (MASK != kPlain)
+    if constexpr (MASK == kSinks)
+        return j >= p.us && j < p.ul ? p.ul : j;
+    if constexpr (MASK == kWindow)
         while (j <= p.je && !tile_active<BC, MASK>(p.tr0, j) && !tile_active<BC, MASK>(p.tr1, j))
             ++j;
     return j;
@@ -338,6 +342,8 @@ __device__ __forceinline__ int union_count(const Plan &p)
 {
     if constexpr (MASK == kPlain)
         return p.je - p.js + 1;
+    if constexpr (MASK == kSinks)
+        return p.je + 1 - max(0, p.ul - p.us);
     int n = 0;
     for (int j = union_next<BC, MASK>(p, p.js); j <= p.je; j = union_next<BC, MASK>(p, j + 1))
         ++n;
@@ -853,11 +859,24 @@ __global__ void __launch_bounds__(FwdLayout<D, F8>::NTHREADS, 1)
                     const long lo = (MASKED && a.left >= 0) ? (long)r + off - a.left : 0L;
                     const int ch = (int)max(0L, min((long)BC, hi - kv0));
                     const int cl = MASKED ? (int)max(0L, min((long)BC, lo - kv0)) : 0;
-                    const int cs = MASK == kSinks ? a.sinks - kv0 : 0;   // keys in front of it are seen, up to ch
+                    if constexpr (MASK == kSinks) {
+                        // 32 keys a word: those in front of ch, and of them those from cl on or in front of cs (the
+                        // sinks); one select a key in place of three comparisons
+                        const int cs = a.sinks - kv0;
+                        auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
 #pragma unroll
-                    for (int i = 0; i < BC; ++i)
-                        if ((i < cl && i >= cs) || i >= ch)
-                            s[i] = -INFINITY;
+                        for (int c = 0; c < BC / 32; ++c) {
+                            const uint32_t w = below(ch - 32 * c) & (~below(cl - 32 * c) | below(cs - 32 * c));
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                s[c * 32 + i] = (w & (1u << i)) ? s[c * 32 + i] : -INFINITY;
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < BC; ++i)
+                            if (i < cl || i >= ch)
+                                s[i] = -INFINITY;
+                    }
                 }
                 // row max: four independent chains of three-input max
                 float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;

@@ -92,24 +92,37 @@ struct NormBwdArgs {
 };
 
 constexpr int kNormCtas = 304;   // two an SM; the sums' order depends on it, not on the device
+// Threads of a CTA: 168 registers each are enough for two heads ahead without a spill.  q and k of B8 H32
+// T4096 d128, us by threads, CTAs an SM and heads ahead: 192 2 2 256, 128 3 2 257, 256 1 4 267, 256 2 1 272, 192 2 3
+// (60 bytes of spills) 301, 256 2 2 (200) 381.
+constexpr int kNormThreads = 192;
 
-// A CTA has one head group, of one tensor, and every ctas / groups-th tile of tokens.
+// A CTA has one head group, of one tensor, and every ctas / groups-th tile of tokens.  A thread's loads run one
+// or two heads ahead: a head's values go to fp32 registers, its buffer is filled again, and only then they are
+// used.  The weights stay in shared memory.
 template <typename E, int D, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads, 2) norm_bwd_kernel(const __grid_constant__ RopeTable tab,
+__global__ void __launch_bounds__(kNormThreads, 2) norm_bwd_kernel(const __grid_constant__ RopeTable tab,
                                                                 const __grid_constant__ NormBwdArgs a)
 {
-    constexpr int TPR = D / 16, TOK = kRopeThreads / TPR;
-    constexpr int AHEAD = sizeof(E) == 2 ? 2 : 1;        // heads under way: two streams of 16 features each
+    constexpr int TPR = D / 16, TOK = kNormThreads / TPR;
+    constexpr int AHEAD = sizeof(E) == 2 ? 2 : 1;
     __shared__ float sums[TOK * D];
+    __shared__ __align__(16) float weight[D];
     pdl_wait();
     const int v = threadIdx.x % TPR, row = threadIdx.x / TPR;
     const int group = (int)blockIdx.x % a.groups, w = group >= a.G0;
     const int h0 = (group - (w ? a.G0 : 0)) * a.heads_per_cta, nh = min(a.heads_per_cta, a.H[w] - h0);
     const Slice sl = slice_of(v, a.rot, INTER);
     const int gap = sl.e1 - sl.e0;
-    float wf[8], wg[8], af[8], ag[8];
-    norm_weights(a.norm, w, sl.e0, wf);
-    norm_weights(a.norm, w, sl.e1, wg);
+    if (row == 0) {
+        float t[8];
+        norm_weights(a.norm, w, sl.e0, t);
+        store8(weight + sl.e0, t);
+        norm_weights(a.norm, w, sl.e1, t);
+        store8(weight + sl.e1, t);
+    }
+    __syncthreads();
+    float af[8], ag[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j)
         af[j] = ag[j] = 0.f;
@@ -119,6 +132,22 @@ __global__ void __launch_bounds__(kRopeThreads, 2) norm_bwd_kernel(const __grid_
         if (tok >= a.n)
             break;
         const int b = (int)tok / a.T, t = (int)tok - b * a.T;
+        const E *x = static_cast<const E *>(xi.p) + b * xi.sb + h0 * xi.sh + t * xi.st + sl.e0;
+        const E *dy = static_cast<const E *>(gi.p) + b * gi.sb + h0 * gi.sh + t * gi.st + sl.e0;
+        E *dx = static_cast<E *>(oi.p) + b * oi.sb + h0 * oi.sh + t * oi.st + sl.e0;
+        Raw8<E> px[AHEAD][2], pg[AHEAD][2];
+        auto fill = [&](int u) {
+            px[u][0].load(x);
+            px[u][1].load(x + gap);
+            pg[u][0].load(dy);
+            pg[u][1].load(dy + gap);
+            x += xi.sh;
+            dy += gi.sh;
+        };
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u)
+            if (u < nh)
+                fill(u);
         float sn[8], cs[8];
         if (sl.pair >= 0) {
 #pragma unroll
@@ -128,78 +157,61 @@ __global__ void __launch_bounds__(kRopeThreads, 2) norm_bwd_kernel(const __grid_
                 sn[j] = -sn[j];   // the transpose turns the other way
             }
         }
-        const E *x = static_cast<const E *>(xi.p) + b * xi.sb + h0 * xi.sh + t * xi.st + sl.e0;
-        const E *dy = static_cast<const E *>(gi.p) + b * gi.sb + h0 * gi.sh + t * gi.st + sl.e0;
-        E *dx = static_cast<E *>(oi.p) + b * oi.sb + h0 * oi.sh + t * oi.st + sl.e0;
         for (int i = 0; i < nh; i += AHEAD) {
-            Raw8<E> px[AHEAD][2] = {}, pg[AHEAD][2] = {};
-            float s[AHEAD], z[AHEAD];   // sums of x^2 and of w g x
 #pragma unroll
-            for (int u = 0; u < AHEAD; ++u)
-                if (i + u < nh) {
-                    px[u][0].load(x + u * xi.sh);
-                    px[u][1].load(x + u * xi.sh + gap);
-                    pg[u][0].load(dy + u * gi.sh);
-                    pg[u][1].load(dy + u * gi.sh + gap);
-                }
-            x += AHEAD * xi.sh;
-            dy += AHEAD * gi.sh;
-            // R^T dy is found twice, for the sums and behind them: kept, its registers would be one head less
-            auto turned = [&](int u, float(&f)[8], float(&g)[8]) {
+            for (int u = 0; u < AHEAD; ++u) {
+                if (i + u >= nh)
+                    break;
+                float x0[8], x1[8], f[8], g[8];   // x, and R^T dy
+                px[u][0].get(x0);
+                px[u][1].get(x1);
                 pg[u][0].get(f);
                 pg[u][1].get(g);
+                if (i + u + AHEAD < nh)
+                    fill(u);
                 if (sl.pair >= 0)
                     turn<INTER>(f, g, sn, cs);
-            };
-#pragma unroll
-            for (int u = 0; u < AHEAD; ++u) {
-                float xf[8], xg[8], f[8], g[8];
-                px[u][0].get(xf);
-                px[u][1].get(xg);
-                turned(u, f, g);
-                s[u] = sum_squares(xf, xg);
+                // sums of x^2 and of w g x
+                const float s = row_sum<TPR>(sum_squares(x0, x1));
                 float z0 = 0.f, z1 = 0.f;
+                auto dots = [&](const float(&gy)[8], const float(&xx)[8], int e) {
+                    Raw8<float> r;
+                    float ww[8];
+                    r.load(weight + e);
+                    r.get(ww);
 #pragma unroll
-                for (int j = 0; j < 8; j += 2) {
-                    float t0, t1;
-                    fmul2(t0, t1, f[j], f[j + 1], wf[j], wf[j + 1]);
-                    ffma2(z0, z1, t0, t1, xf[j], xf[j + 1], z0, z1);
-                    fmul2(t0, t1, g[j], g[j + 1], wg[j], wg[j + 1]);
-                    ffma2(z0, z1, t0, t1, xg[j], xg[j + 1], z0, z1);
-                }
-                z[u] = z0 + z1;
+                    for (int j = 0; j < 8; j += 2) {
+                        float t0, t1;
+                        fmul2(t0, t1, gy[j], gy[j + 1], ww[j], ww[j + 1]);
+                        ffma2(z0, z1, t0, t1, xx[j], xx[j + 1], z0, z1);
+                    }
+                };
+                dots(f, x0, sl.e0);
+                dots(g, x1, sl.e1);
+                const float z = row_sum<TPR>(z0 + z1);
+                const float r = __frsqrt_rn(fmaf(s, 1.f / D, a.norm.eps));
+                const float m = -z * (1.f / D) * r * r;   // dx = r (w g - x (r^2 mean(w g x)))
+                auto half = [&](float(&gy)[8], const float(&xx)[8], int e, float(&acc)[8]) {
+                    Raw8<float> rw;
+                    float ww[8];
+                    rw.load(weight + e);
+                    rw.get(ww);
+#pragma unroll
+                    for (int j = 0; j < 8; j += 2) {
+                        float t0, t1;
+                        fmul2(t0, t1, xx[j], xx[j + 1], r, r);
+                        ffma2(acc[j], acc[j + 1], gy[j], gy[j + 1], t0, t1, acc[j], acc[j + 1]);
+                        fmul2(t0, t1, gy[j], gy[j + 1], ww[j], ww[j + 1]);
+                        ffma2(t0, t1, xx[j], xx[j + 1], m, m, t0, t1);
+                        fmul2(gy[j], gy[j + 1], t0, t1, r, r);
+                    }
+                };
+                half(f, x0, sl.e0, af);
+                half(g, x1, sl.e1, ag);
+                store8(dx, f);
+                store8(dx + gap, g);
+                dx += oi.sh;
             }
-#pragma unroll
-            for (int u = 0; u < AHEAD; ++u) {
-                s[u] = row_sum<TPR>(s[u]);
-                z[u] = row_sum<TPR>(z[u]);
-            }
-#pragma unroll
-            for (int u = 0; u < AHEAD; ++u)
-                if (i + u < nh) {
-                    const float r = __frsqrt_rn(fmaf(s[u], 1.f / D, a.norm.eps));
-                    const float m = -z[u] * (1.f / D) * r * r;   // dx = r (w g - x (r^2 mean(w g x)))
-                    float x0[8], x1[8], f[8], g[8];
-                    turned(u, f, g);
-                    px[u][0].get(x0);
-                    px[u][1].get(x1);
-                    auto half = [&](float(&gy)[8], const float(&xx)[8], const float(&ww)[8], float(&acc)[8]) {
-#pragma unroll
-                        for (int j = 0; j < 8; j += 2) {
-                            float t0, t1;
-                            fmul2(t0, t1, xx[j], xx[j + 1], r, r);
-                            ffma2(acc[j], acc[j + 1], gy[j], gy[j + 1], t0, t1, acc[j], acc[j + 1]);
-                            fmul2(t0, t1, gy[j], gy[j + 1], ww[j], ww[j + 1]);
-                            ffma2(t0, t1, xx[j], xx[j + 1], m, m, t0, t1);
-                            fmul2(gy[j], gy[j + 1], t0, t1, r, r);
-                        }
-                    };
-                    half(f, x0, wf, af);
-                    half(g, x1, wg, ag);
-                    store8(dx, f);
-                    store8(dx + gap, g);
-                    dx += oi.sh;
-                }
         }
     }
     pdl_launch();
@@ -211,7 +223,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) norm_bwd_kernel(const __grid_
         sums[row * D + sl.e1 + j] = ag[j];
     }
     __syncthreads();
-    for (int f = threadIdx.x; f < D; f += kRopeThreads) {
+    for (int f = threadIdx.x; f < D; f += kNormThreads) {
         float x = 0.f;
 #pragma unroll 8
         for (int i = 0; i < TOK; ++i)
@@ -256,14 +268,14 @@ int norm_run(const RopeTable &t, const NormRopeArgs &a, int interleaved, cudaStr
 template <typename E, int D>
 int norm_bwd_run(const RopeTable &t, NormBwdArgs &a, int interleaved, cudaStream_t s)
 {
-    constexpr int TOK = kRopeThreads / (D / 16);
+    constexpr int TOK = kNormThreads / (D / 16);
     a.tiles = (int)((a.n + TOK - 1) / TOK);
     const int runs = kNormCtas / a.groups;   // CTAs of a head group
     a.ctas = a.groups * (a.tiles < runs ? a.tiles : runs);
     if (a.ctas == 0)   // no row: the sums are 0
         return launch_overlapped(norm_dweight_kernel, dim3(D / 32, 2), 256, 0, 0, true, s, a, D);
     const int st = launch_overlapped(interleaved ? norm_bwd_kernel<E, D, true> : norm_bwd_kernel<E, D, false>, dim3((unsigned)a.ctas),
-                                     kRopeThreads, 0, 0, true, s, t, a);
+                                     kNormThreads, 0, 0, true, s, t, a);
     if (st != OK || !a.part)
         return st;
     return launch_overlapped(norm_dweight_kernel, dim3(D / 32, 2), 256, 0, 0, true, s, a, D);

@@ -38,5 +38,5 @@ def test_workspace(fa):
         for left, sinks in ((0, 1), (100, 4), (100, 300), (10 ** 9, 10 ** 9)):
             extra, unit = size(*args, left, sinks) - base(*args), args[0] * args[1] * -(-min(sinks, args[3]) // 128) * 2 * 128 * args[4] * 4
             assert extra % unit == 0 and extra // unit in (0, *range(2, 65))
-    assert size(1, 1, 3000, 3000, 128, 255, 4) - base(1, 1, 3000, 3000, 128) == 8 * 2 * 128 * 128 * 4   # 24 query blocks, 3 a window
+    assert size(1, 1, 3000, 3000, 128, 255, 4) - base(1, 1, 3000, 3000, 128) == 3 * 2 * 128 * 128 * 4   # 24 query blocks, 8 a part
     assert size(1, 1, 100, 100, 64, -2, 0) == 0 and size(1, 1, 100, 100, 64, 0, -1) == 0 and size(1, 1, 100, 100, 96, 0, 1) == 0
