@@ -176,10 +176,20 @@ int paged_launch(const fa_kv_cache &c, const void *q, void *o, float *lse, int H
                  int accumulate, void *workspace, cudaStream_t s);
 int paged_window_launch(const fa_kv_cache &c, const void *q, void *o, float *lse, int Hq, int Tq, int left, int sinks,
                         float scale, void *workspace, cudaStream_t s);
+// Where the states of the entries behind a prefix are, for the kernel that joins them with the prefix's.
+struct OwnStates {
+    const float *o, *lse;      // of units that one CTA had
+    const float *part;         // of the others: two slots a CTA, [rows][d] then m, l [rows]
+    const long long *where;    // the share of a CTA (0: whole units), and the first tile of each sequence
+    const int *lens;
+    int whole;                 // whole units, whatever `where` says
+    int rows, RB, Hkv, kt, base, cap;
+};
 int paged_behind_launch(const fa_kv_cache &c, const void *q, float *o, float *lse, int Hq, int Tq, int causal, int base, float scale,
-                        void *workspace, cudaStream_t s);
+                        void *workspace, OwnStates *states, cudaStream_t s);
 // Attention over a shared prefix and the entries behind it (fa_prefix_sm103.cu); n_pages > 0, pages of the prefix.
 size_t prefix_workspace_bytes(int B, int Hq, int Hkv, int Tq, int max_len, int d, int codes, int n_pages, int page_size);
+bool prefix_pays(const fa_kv_cache &c, int Hq, int Tq, int n_pages);
 int prefix_launch(const fa_kv_cache &c, const void *q, void *o, float *lse, int Hq, int Tq, int causal, const int *pages,
                   int n_pages, float scale, void *workspace, cudaStream_t s);
 int cache_status_fetch_clear(cudaStream_t s, int *host_word);

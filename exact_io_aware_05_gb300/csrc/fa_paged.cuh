@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, ROWS>::CTAS)
                 if (lane == 0) {
                     there[st] = groups;
 #if FA_TEST_WITHHOLD
-                    const bool hold = a.withhold == WITHHOLD_PAGED_FULL && blockIdx.x == 0 && n == 0;
+                    const bool hold = a.withhold == (RANGED ? WITHHOLD_RANGE_FULL : WITHHOLD_PAGED_FULL) && blockIdx.x == 0 && n == 0;
 #else
                     constexpr bool hold = false;
 #endif
@@ -614,7 +614,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, ROWS>::CTAS)
         bool ok = true;
         // All CTAs are there, and the join's blocks take nothing from them (0.2 to 0.4 us); where no join
         // follows, the next call's do (240 units of 512 14.1 us instead of 13.2)
-        if (whole && !a.whole)
+        // (own entries behind a shared prefix: its kernel does not wait for this one, and takes the SMs that are done)
+        if ((whole && !a.whole) || (RANGED && a.o32))
             pdl_launch();
         if (RT == 1 && p.left > 0)
             fetch_q(p);
@@ -1395,7 +1396,8 @@ int paged_run(const fa_kv_cache &c, PagedArgs &a, cudaStream_t s)
     a.grid = kSMs * ctas;
     // tiles, at most: those of a window begin and end anywhere, and so do the sinks'
     const long long most = (long long)a.B * a.Hkv * a.RB * std::min((a.cap + a.kt - 1) / a.kt, RANGED ? a.span / a.kt + 3 : INT_MAX);
-    a.may_whole = a.may_whole && most > 0 && (long long)a.B * a.Hkv * a.RB <= a.grid;
+    // RANGED: more units than CTAs at a time may be whole ones too, taken by CTAs as others end
+    a.may_whole = a.may_whole && most > 0 && (long long)a.B * a.Hkv * a.RB <= (RANGED ? 8 : 1) * a.grid;
     int st = OK;
     if (most > 0) {
         CUtensorMap tk, tv;
@@ -1405,7 +1407,7 @@ int paged_run(const fa_kv_cache &c, PagedArgs &a, cudaStream_t s)
         const long long units = (long long)a.B * a.Hkv * a.RB;
         if (a.whole && units > INT_MAX)
             return ERR_UNSUPPORTED;
-        const int grid = (int)(a.whole ? units : most < a.grid ? most : a.grid);
+        const int grid = (int)(a.whole || (RANGED && a.may_whole && units > a.grid) ? units : most < a.grid ? most : a.grid);
         if (f8)
             st = rows == 8    ? launch_main<D, true, 8, RANGED>(tk, tv, a, grid, s)
                  : rows == 16 ? launch_main<D, true, 16, RANGED>(tk, tv, a, grid, s)
@@ -1419,7 +1421,7 @@ int paged_run(const fa_kv_cache &c, PagedArgs &a, cudaStream_t s)
         if (st != OK)
             return st;
     }
-    if (a.whole && most > 0)
+    if ((a.whole && most > 0) || (RANGED && a.o32))
         return OK;
     const int wchunks = a.scores ? (a.cap + kWeightRun - 1) / kWeightRun : 0;
     // rows a block: one, unless that makes more blocks than the device holds at a time

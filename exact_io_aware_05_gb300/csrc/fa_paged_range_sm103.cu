@@ -34,9 +34,9 @@ int paged_window_launch(const fa_kv_cache &c, const void *q, void *o, float *lse
     return run(c, a, s);
 }
 
-// The entries from slot `base` on; o in fp32.
+// The entries from slot `base` on: o in fp32, and no join.
 int paged_behind_launch(const fa_kv_cache &c, const void *q, float *o, float *lse, int Hq, int Tq, int causal, int base, float scale,
-                        void *workspace, cudaStream_t s)
+                        void *workspace, OwnStates *states, cudaStream_t s)
 {
     status_in_use(STATUS_RANGE);
     PagedArgs a = paged_args(c, q, nullptr, lse, Hq, Tq, causal, scale, workspace);
@@ -45,7 +45,9 @@ int paged_behind_launch(const fa_kv_cache &c, const void *q, float *o, float *ls
     a.base = std::min(base, a.cap);
     a.span = a.cap - a.base;
     a.o32 = o;
-    return run(c, a, s);
+    const int st = run(c, a, s);
+    *states = OwnStates{o, lse, a.part, a.where, a.lens, a.whole, a.rows, a.RB, a.Hkv, a.kt, a.base, a.cap};
+    return st;
 }
 
 int paged_range_status_fetch_clear(cudaStream_t s, int *host_word) { return paged_words_fetch_clear(s, host_word); }

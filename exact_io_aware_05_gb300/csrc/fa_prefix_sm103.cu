@@ -10,7 +10,7 @@
 // What bounds it: each entry's 4 d bytes (bf16) serve B G Tq rows at 4 d flops each, so that with 128 rows a KV
 // head the tensor cores and the memory take about the same time, and with more the products do.  So they
 // are tcgen05 products of 128 query rows by a tile of entries, with S and O~ in tensor memory:
-//   * A CTA has one KV head's 128 or (bf16, d 64 and 128) 256 rows, in one or two query tiles, and one run of the
+//   * A CTA has one KV head's 128 (d 256) or 256 rows, in one or two query tiles, and one run of the
 //     prefix's tiles of 128 entries (64 at d 256).  The runs are as many as fill the SMs.
 //   * Warp 0 loads K and V tiles by TMA, a box for each page and 64 features, into 128-byte swizzled
 //     tiles; pages that are not there, and what lies behind the prefix, come as zeros (a box behind the
@@ -20,7 +20,7 @@
 //   * Query rows are gathered by the softmax warps, straight into the swizzled tile: they lie scattered over the
 //     batch, B runs of G Tq rows.  Warps whose 32 rows lie behind the last one take no part.
 //   * e4m3: four more warps turn the tiles' codes into bf16, which holds every code exactly, so that q stays
-//     as it is; one query tile a CTA, whose room the codes take.
+//     as it is.
 //   * P enters its product as bf16, as in the forward pass: 2^-8 of each probability.
 #include <algorithm>
 #include <cfloat>
@@ -49,7 +49,7 @@ enum PrefixSite : int { SITE_X_EMPTY = 1, SITE_X_REMPTY, SITE_X_RFULL, SITE_X_QF
 
 template <int D, bool FP8>
 struct XCfg {
-    static constexpr int NQ = D == 256 || FP8 ? 1 : 2;          // query tiles of a CTA
+    static constexpr int NQ = D == 256 ? 1 : 2;                 // query tiles of a CTA
     static constexpr int BC = D == 256 ? 64 : 128;              // entries a tile
     static constexpr int KCH = D / 64;                          // 128-byte chunks of a bf16 row
     static constexpr int Q_CHUNK = BR * 128, Q_TILE = KCH * Q_CHUNK;
@@ -59,10 +59,10 @@ struct XCfg {
     static constexpr int OFF_Q = 0, OFF_P = NQ * Q_TILE, OFF_SLOT = OFF_P + NQ * P_TILE;
     static constexpr int AVAIL = 227 * 1024 - 1024 - 512 - OFF_SLOT;
     static constexpr int FIT = AVAIL / KV_TILE;
-    static constexpr int NSLOT = FP8 ? (D == 64 ? 4 : 3) : FIT < 8 ? FIT : 8;
+    static constexpr int NSLOT = FP8 ? (D == 64 ? 4 : D == 128 ? 2 : 3) : FIT < 8 ? FIT : 8;
     static constexpr int RFIT = (AVAIL - NSLOT * KV_TILE) / RAW_TILE;
     static constexpr int NRAW = FP8 ? (RFIT < 8 ? RFIT : 8) : 0;
-    static_assert(NSLOT >= 3 && (!FP8 || NRAW >= 3), "K/V rings");
+    static_assert(NSLOT >= (FP8 ? 2 : 3) && (!FP8 || NRAW >= 2), "K/V rings");
     static constexpr int OFF_RAW = OFF_SLOT + NSLOT * KV_TILE;
     static constexpr int OFF_BAR = OFF_RAW + NRAW * RAW_TILE;
     static constexpr int B_FULL = 0, B_EMPTY = NSLOT, B_RFULL = 2 * NSLOT, B_REMPTY = B_RFULL + NRAW, B_QFULL = B_REMPTY + NRAW,
@@ -137,7 +137,9 @@ __global__ void __launch_bounds__(XCfg<D, FP8>::NTHREADS, 1)
 {
     using C = XCfg<D, FP8>;
     constexpr int BC = C::BC, NQ = C::NQ, NSLOT = C::NSLOT, NRAW = FP8 ? C::NRAW : 1;
-    constexpr bool SPLIT = C::NTHREADS == 384;   // registers move from warps 0 to 3 to the softmax
+    // Registers move from warps 0 to 3 (and those that convert) to the softmax: of three warpgroups with 168 each 104
+    // and 200, or 104, 200 and 168; of four with 128 each 64, 176 twice and 96
+    constexpr bool SPLIT = C::NTHREADS >= 384, FOUR = C::NTHREADS == 512;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t sbase = (raw + 1023u) & ~1023u;
@@ -184,12 +186,13 @@ __global__ void __launch_bounds__(XCfg<D, FP8>::NTHREADS, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const WaitCtx ctx{abort_flag, &g_prefix_status[0], a.timeout_ns};
-    pdl_wait();
+    // No wait here: the kernel before this one, that of the sequences' own entries, lets this one start only once
+    // all of it is past its own wait, and nothing that it writes is read.  The wait is at the end
     pdl_launch();
 
     if (warp < 4) {
         if constexpr (SPLIT)
-            regs_dealloc<104>();
+            regs_dealloc<FOUR ? 64 : 104>();
         if (warp == 0) {
             // ---------------------------------------------------- loads: lane = box (page, and 64 features in bf16)
             const int bp_shift = min(a.ps_shift, BC == 64 ? 6 : 7), boxes = BC >> bp_shift;   // rows of a box; boxes of a tile
@@ -301,9 +304,11 @@ __global__ void __launch_bounds__(XCfg<D, FP8>::NTHREADS, 1)
             mbar_wait_drain(bar(C::B_DRAIN + t), 0);
         }
         __syncwarp();
-    } else if (FP8 && warp >= 8) {
+    } else if (FP8 && warp >= 4 + 4 * NQ) {
+        if constexpr (FOUR)
+            regs_dealloc<96>();
         // -------------------------------------------------------- codes to bf16, in the loads' order
-        const int tid = (int)threadIdx.x - 256;
+        const int tid = (int)threadIdx.x - (128 + 128 * NQ);
         constexpr int UNITS = D / 16;   // 16-code pieces of a row
         for (uint32_t i = 0; i < 2u * (uint32_t)n; ++i) {
             const uint32_t r = i % NRAW, s = i % NSLOT;
@@ -327,7 +332,7 @@ __global__ void __launch_bounds__(XCfg<D, FP8>::NTHREADS, 1)
         }
     } else if ((int)(warp - 4) / 4 < nq) {
         if constexpr (SPLIT)
-            regs_alloc<200>();
+            regs_alloc<FOUR ? 176 : 200>();
         // -------------------------------------------------------- softmax of query tile t: a thread a row
         const int t = (int)(warp - 4) >> 2;
         const uint32_t quarter = warp & 3u;
@@ -337,22 +342,21 @@ __global__ void __launch_bounds__(XCfg<D, FP8>::NTHREADS, 1)
         int lim = 0;   // entries of the prefix that the row sees
         {
             const int b = r / a.GT, i = r - b * a.GT;   // sequence, and row of its head group
-            uint8_t *qrow = smem + C::OFF_Q + t * C::Q_TILE + rit * 128;
-            const uint4 *src = nullptr;
+            long long src = -1;
             if (r < a.R) {
                 const int len = a.lens[b];
                 lim = len < 0 || len > a.cap ? 0 : min(a.P, max(0, a.causal ? len - a.Tq + i % a.Tq + 1 : len));
-                src = reinterpret_cast<const uint4 *>(a.q + (((long long)b * a.Hq + (long long)h * a.G) * a.Tq + i) * D);
+                src = (((long long)b * a.Hq + (long long)h * a.G) * a.Tq + i) * D;
             }
-#pragma unroll
-            for (int c = 0; c < C::KCH; ++c) {
-                uint4 v[8];
-#pragma unroll
-                for (int u = 0; u < 8; ++u)
-                    v[u] = src ? src[c * 8 + u] : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                for (int u = 0; u < 8; ++u)
-                    *reinterpret_cast<uint4 *>(qrow + c * C::Q_CHUNK + ((u ^ (rit & 7)) << 4)) = v[u];
+            // the warp's rows, D / 8 lanes a row: whole lines (a thread's own row would be 32 lines a load)
+            constexpr int LPR = D / 8, RPL = 32 / LPR;
+            uint8_t *qt = smem + C::OFF_Q + t * C::Q_TILE;
+#pragma unroll 8
+            for (int k = 0; k < LPR; ++k) {
+                const int row = k * RPL + (int)lane / LPR, u = (int)lane % LPR, at = (int)quarter * 32 + row;
+                const long long from = __shfl_sync(0xffffffffu, src, row);
+                const uint4 v = from >= 0 ? *reinterpret_cast<const uint4 *>(a.q + from + u * 8) : make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4 *>(qt + (u >> 3) * C::Q_CHUNK + at * 128 + (((u & 7) ^ (at & 7)) << 4)) = v;
             }
             fence_smem_to_async();
             mbar_arrive(bar(C::B_QFULL + t));
@@ -515,84 +519,162 @@ __global__ void __launch_bounds__(XCfg<D, FP8>::NTHREADS, 1)
         tc_fence_after();
         tmem_dealloc(tmem, C::TMEM_COLS);
     }
+    pdl_wait();   // the end of this kernel means the end of the one before it
 }
 
 // ------------------------------------------------------------------ join
 struct PrefixJoinArgs {
-    const float *part, *own, *own_lse;   // states of the runs; o and lse of the sequences' own entries
+    const float *part;     // states of the runs
     long long ml_at;
+    OwnStates own;
     __nv_bfloat16 *o;
     float *lse;
     int Hq, G, Tq, GT, RP, runs, rows;   // rows: of a CTA of the attention
+    long long n;           // rows of o
 };
 
-// One row a block of four warps: each takes every fourth run, a lane D / 32 features; then the warps' sums and the
-// own entries.
-template <int D>
+// W warps a row: each takes every W-th state (the runs', then the own entries'), a lane D / 32 features; then the
+// warps' sums.  The first states of each warp are under way before anything is known of them.
+template <int D, int W>
 __global__ void __launch_bounds__(128) prefix_join_kernel(const __grid_constant__ PrefixJoinArgs a)
 {
-    constexpr int F = D / 32, AHEAD = 5;
-    __shared__ float sum[4][D], ml[4][2];
+    constexpr int F = D / 32, AHEAD = D == 256 ? 4 : 8;   // divides 32
+    __shared__ float sum[W == 1 ? 1 : 4][D], red[4];
     pdl_launch();
-    pdl_wait();
-    const int warp = (int)warp_id(), lane = (int)lane_id();
-    const long long row = blockIdx.x;                 // (b Hq + head) Tq + t
+    const int warp = (int)warp_id() % W, lane = (int)lane_id();
+    const long long row = (long long)blockIdx.x * (4 / W) + warp_id() / W;   // (b Hq + head) Tq + t
+    if (row >= a.n) {
+        pdl_wait();
+        return;
+    }
     const int t = (int)(row % a.Tq), head = (int)(row / a.Tq % a.Hq), b = (int)(row / a.Tq / a.Hq);
-    const int h = head / a.G, r = b * a.GT + (head - h * a.G) * a.Tq + t;   // KV head, and row of its matrix
+    const int h = head / a.G, i = (head - h * a.G) * a.Tq + t, r = b * a.GT + i;   // KV head, row of its group, of its matrix
     const long long at = (long long)(h * a.RP + r / a.rows) * a.runs * a.rows + r % a.rows;
-    const float2 *states = reinterpret_cast<const float2 *>(a.part + a.ml_at);
-    // the runs' maximum: every warp reads all of them
+    // The lengths may be read in front of the wait: all kernels before the attention's had ended when this one
+    // was launched.  Behind it, everything whose place is known goes together, the own entries' state as if it were whole
+    int len = a.own.lens[b];
+    len = len < 0 || len > a.own.cap ? 0 : len;
+    pdl_wait();
+    const long long where0 = a.own.whole ? 0 : __ldcg(a.own.where), where1 = a.own.whole ? 0 : __ldcg(a.own.where + 1 + b);
+    const float lse0 = __ldcg(a.own.lse + row);
+    float z[F];
+#pragma unroll
+    for (int f = 0; f < F; f += 2)
+        *reinterpret_cast<float2 *>(&z[f]) = __ldcg(reinterpret_cast<const float2 *>(a.own.o + row * D + lane * F + f));
+    const float2 *ml = reinterpret_cast<const float2 *>(a.part + a.ml_at) + at;
+    auto run_o = [&](int s) { return a.part + (at + (long long)s * a.rows) * D + lane * F; };
+    // this warp's states are the runs warp, warp + W, ...; lane j has (m, l) of the j-th of 32 at a time
+    const int mine = (a.runs - warp + W - 1) / W;
+    float y[AHEAD][F];
+    auto fetch = [&](int u, int k) {   // the k-th of them
+        if (k < mine)
+#pragma unroll
+            for (int f = 0; f < F; f += 2)
+                *reinterpret_cast<float2 *>(&y[u][f]) = __ldcg(reinterpret_cast<const float2 *>(run_o(warp + W * k) + f));
+    };
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u)
+        fetch(u, u);
+    const float2 none = make_float2(-INFINITY, 0.f);
+    const float2 st0 = lane < mine ? __ldcg(&ml[(long long)(warp + W * lane) * a.rows]) : none;
     float m = -INFINITY;
-    for (int i = lane; i < a.runs; i += 32)
-        m = fmaxf(m, __ldcg(&states[at + (long long)i * a.rows]).x);
+    for (int s = lane; s < a.runs; s += 32)
+        m = fmaxf(m, __ldcg(&ml[(long long)s * a.rows]).x);
+    // the own entries' states: none, one that is whole, or those of CTAs c0 .. c0 + own - 1
+    int own = 0;
+    bool whole = false;
+    const float *first = nullptr, *rest = nullptr;    // slots of the first CTA and, two apart, of those behind it
+    const int rb = i / a.own.rows, ri = i - rb * a.own.rows;
+    const long long stride = (long long)a.own.rows * (D + 2);
+    const int from = min(a.own.base, len) / a.own.kt, nt = a.own.base < len ? (len + a.own.kt - 1) / a.own.kt - from : 0;
+    if (nt > 0) {
+        const long long share = where0;
+        whole = share == 0;
+        if (!whole) {
+            const long long tile = where1 + (long long)(rb * a.own.Hkv + h) * nt, c0 = tile / share, c1 = (tile + nt - 1) / share;
+            whole = c0 == c1;
+            own = (int)(c1 - c0) + 1;
+            first = a.own.part + (2 * c0 + (tile == c0 * share ? 0 : 1)) * stride;
+            rest = a.own.part + 2 * c0 * stride;
+        }
+        if (whole)
+            own = 1;
+    }
+    auto own_slot = [&](int s) { return s == 0 ? first : rest + 2 * s * stride; };
+    auto own_ml = [&](int s) {
+        return whole ? make_float2(lse0 * 1.4426950408889634f, 1.f)
+                     : make_float2(own_slot(s)[(long long)a.own.rows * D + ri], own_slot(s)[(long long)a.own.rows * (D + 1) + ri]);
+    };
+    for (int s = lane; s < own; s += 32)
+        m = fmaxf(m, own_ml(s).x);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1)
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-    const float own = a.own_lse[row] * 1.4426950408889634f;
-    m = fmaxf(m, own);
     const float ref = m == -INFINITY ? 0.f : m;
     float l = 0.f, x[F];
 #pragma unroll
     for (int f = 0; f < F; ++f)
         x[f] = 0.f;
-    for (int i0 = warp; i0 < a.runs; i0 += 4 * AHEAD) {
-        float y[AHEAD][F];
-        float2 st[AHEAD];
+    for (int base = 0; base < mine; base += 32) {
+        const float2 st = base == 0 ? st0 : base + lane < mine ? __ldcg(&ml[(long long)(warp + W * (base + lane)) * a.rows]) : none;
+        const float w = st.x == -INFINITY ? 0.f : ex2_approx(st.x - ref);
+        l = fmaf(w, st.y, l);   // each lane its states'; put together below
+        for (int k0 = base; k0 < min(base + 32, mine); k0 += AHEAD) {
 #pragma unroll
-        for (int u = 0; u < AHEAD; ++u)
-            if (i0 + 4 * u < a.runs) {
-                const long long p = at + (long long)(i0 + 4 * u) * a.rows;
-                st[u] = __ldcg(&states[p]);
+            for (int u = 0; u < AHEAD; ++u) {
+                const float wu = __shfl_sync(0xffffffffu, w, (k0 + u) & 31);
+                // a state that saw nothing may hold anything
+                if (k0 + u < min(base + 32, mine) && wu != 0.f)
 #pragma unroll
-                for (int f = 0; f < F; f += 2)
-                    *reinterpret_cast<float2 *>(&y[u][f]) = __ldcg(reinterpret_cast<const float2 *>(a.part + p * D + lane * F + f));
+                    for (int f = 0; f < F; ++f)
+                        x[f] = fmaf(wu, y[u][f], x[f]);
             }
 #pragma unroll
-        for (int u = 0; u < AHEAD; ++u)
-            if (i0 + 4 * u < a.runs && st[u].x != -INFINITY) {
-                const float w = ex2_approx(st[u].x - ref);
-                l = fmaf(w, st[u].y, l);
-#pragma unroll
-                for (int f = 0; f < F; ++f)
-                    x[f] = fmaf(w, y[u][f], x[f]);
-            }
+            for (int u = 0; u < AHEAD; ++u)
+                fetch(u, k0 + AHEAD + u);
+        }
     }
 #pragma unroll
-    for (int f = 0; f < F; ++f)
-        sum[warp][lane * F + f] = x[f];
-    if (lane == 0)
-        ml[warp][0] = l;
-    __syncthreads();
-    const float wo = own == -INFINITY ? 0.f : ex2_approx(own - ref);
-    l = (ml[0][0] + ml[1][0]) + (ml[2][0] + ml[3][0]) + wo;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    for (int f = 2 * (int)threadIdx.x; f < D; f += 256) {
-        const float2 y = wo == 0.f ? make_float2(0.f, 0.f) : *reinterpret_cast<const float2 *>(a.own + row * D + f);
-        const float u = (sum[0][f] + sum[1][f]) + (sum[2][f] + sum[3][f]) + wo * y.x;
-        const float v = (sum[0][f + 1] + sum[1][f + 1]) + (sum[2][f + 1] + sum[3][f + 1]) + wo * y.y;
-        *reinterpret_cast<uint32_t *>(a.o + row * D + f) = pack_bf16x2(u * inv, v * inv);
+    for (int off = 16; off > 0; off >>= 1)
+        l += __shfl_xor_sync(0xffffffffu, l, off);
+    for (int s = warp; s < own; s += W) {
+        const float2 st = own_ml(s);
+        if (st.x == -INFINITY)
+            continue;
+        const float w = ex2_approx(st.x - ref);
+        l = fmaf(w, st.y, l);
+        if (!whole) {
+            const float *src = own_slot(s) + (long long)ri * D + lane * F;
+#pragma unroll
+            for (int f = 0; f < F; f += 2)
+                *reinterpret_cast<float2 *>(&z[f]) = __ldcg(reinterpret_cast<const float2 *>(src + f));
+        }
+#pragma unroll
+        for (int f = 0; f < F; ++f)
+            x[f] = fmaf(w, z[f], x[f]);
     }
-    if (threadIdx.x == 0)
+    if constexpr (W == 1) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        uint32_t *dst = reinterpret_cast<uint32_t *>(a.o + row * D) + lane * (F / 2);
+#pragma unroll
+        for (int f = 0; f < F; f += 2)
+            dst[f / 2] = pack_bf16x2(x[f] * inv, x[f + 1] * inv);
+    } else {
+#pragma unroll
+        for (int f = 0; f < F; ++f)
+            sum[warp][lane * F + f] = x[f];
+        if (lane == 0)
+            red[warp] = l;
+        __syncthreads();
+        l = (red[0] + red[1]) + (red[2] + red[3]);
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        for (int f = 2 * (int)threadIdx.x; f < D; f += 256) {
+            const float u = (sum[0][f] + sum[1][f]) + (sum[2][f] + sum[3][f]);
+            const float v = (sum[0][f + 1] + sum[1][f + 1]) + (sum[2][f + 1] + sum[3][f + 1]);
+            *reinterpret_cast<uint32_t *>(a.o + row * D + f) = pack_bf16x2(u * inv, v * inv);
+        }
+    }
+    if (warp == 0 && lane == 0)
         a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
 }
 
@@ -604,10 +686,10 @@ struct Cut {
     int rows, rp, tiles, runs;
 };
 
-Cut cut_of(int B, int Hq, int Hkv, int Tq, int d, bool f8, long long P)
+Cut cut_of(int B, int Hq, int Hkv, int Tq, int d, long long P)
 {
     Cut c;
-    c.rows = d == 256 || f8 ? BR : 2 * BR;
+    c.rows = d == 256 ? BR : 2 * BR;
     const long long R = (long long)B * (Hq / Hkv) * Tq;
     c.rp = (int)((R + c.rows - 1) / c.rows);
     const int bc = d == 256 ? 64 : 128;
@@ -659,13 +741,39 @@ int prefix_run(const fa_kv_cache &c, const PrefixArgs &a, cudaStream_t s)
     return launch_overlapped(prefix_kernel<D, FP8>, dim3((unsigned)(a.Hkv * a.runs * a.RP)), C::NTHREADS, C::SMEM, 0, true, s, tk, tv, a);
 }
 
+// A warp a row where it has few states or where there are rows for all SMs.
+template <int D>
+int join_run(const PrefixJoinArgs &j, cudaStream_t s)
+{
+    const bool one = j.runs <= 8 || j.n >= 2048;
+    return launch_overlapped(one ? prefix_join_kernel<D, 1> : prefix_join_kernel<D, 4>, dim3((unsigned)(one ? (j.n + 3) / 4 : j.n)), 128, 0, 0, true, s,
+                             j);
+}
+
 }  // namespace
+
+// Whether the prefix by itself is faster than every sequence reading it: an estimate of both, in us.  Without it each
+// sequence's P entries come from HBM or L2 at about 6.5 TB/s; with it the three kernels take 10.5 (14 at d 256), the
+// states 4.4 for 1000 rows of d 128, the prefix itself 5 TB/s.  us without and with, 8 KV heads of 128 and 4 query heads each,
+// batch x entries: 2 x 8192 15.1 and 17.3, 4 x 512 10.2 and 11.9, 4 x 2048 11.9 and 14.6, 4 x 8192 20.5 and 18.5,
+// 8 x 512 11.3 and 10.9, 8 x 2048 15.4 and 14.8, 16 x 512 13.5 and 11.5, 16 x 2048 21.1 and 15.0, 32 x 512 12.6 and
+// 14.5, 32 x 2048 30.6 and 18.4, 64 x 128 11.5 and 19.7, 64 x 512 26.1 and 20.4, 64 x 8192 177 and 31; 4 KV heads of 64,
+// 16 x 512 9.9 and 10.7, 16 x 2048 12.7 and 10.9; 8 of 256, 16 x 512 13.1 and 18.2, 16 x 2048 30.8 and 22.1.
+// (The test library computes it by itself whatever the sizes.)
+bool prefix_pays(const fa_kv_cache &c, int Hq, int Tq, int n_pages)
+{
+    if (FA_TEST_WITHHOLD)
+        return true;
+    const double entry = (double)c.Hkv * 2 * c.d * (c.dtype == FA_E4M3 ? 1 : 2), once = entry * n_pages * c.page_size * 1e-6;   // MB
+    const double rows = (double)c.B * Hq * Tq * c.d / 128e3;
+    return 7.0 + c.B * once / 6.5 >= (c.d == 256 ? 14.0 : 10.5) + 4.4 * rows + once / 5.0;
+}
 
 // Behind one another: the own entries' workspace, their o (fp32) and lse, the runs' states.
 size_t prefix_workspace_bytes(int B, int Hq, int Hkv, int Tq, int max_len, int d, int codes, int n_pages, int page_size)
 {
     const size_t rows = (size_t)B * Hq * Tq;
-    const Cut c = cut_of(B, Hq, Hkv, Tq, d, codes != 0, (long long)n_pages * page_size);
+    const Cut c = cut_of(B, Hq, Hkv, Tq, d, (long long)n_pages * page_size);
     return round256(paged_workspace_bytes(B, Hq, Hkv, Tq, max_len, d, 0)) + round256(rows * d * 4) + round256(rows * 4) +
            (n_pages > 0 ? round256(part_floats(c, Hkv, d) * 4) : 0);
 }
@@ -676,7 +784,7 @@ int prefix_launch(const fa_kv_cache &c, const void *q, void *o, float *lse, int 
     const int P = n_pages * c.page_size, B = c.B;
     const size_t rows = (size_t)B * Hq * Tq;
     const bool f8 = c.dtype == FA_E4M3;
-    const Cut cut = cut_of(B, Hq, c.Hkv, Tq, c.d, f8, P);
+    const Cut cut = cut_of(B, Hq, c.Hkv, Tq, c.d, P);
     if ((long long)c.Hkv * cut.rp * cut.runs > INT_MAX || rows > INT_MAX)
         return ERR_UNSUPPORTED;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
@@ -714,17 +822,18 @@ int prefix_launch(const fa_kv_cache &c, const void *q, void *o, float *lse, int 
 #if FA_TEST_WITHHOLD
     a.withhold = test_withhold_take(WITHHOLD_PREFIX_FULL, WITHHOLD_PREFIX_FULL);
 #endif
-    int st = c.d == 64    ? (f8 ? prefix_run<64, true>(c, a, s) : prefix_run<64, false>(c, a, s))
+    // the own entries first: the memory bounds them, and the prefix's CTAs take the SMs as they are done
+    OwnStates states;
+    int st = paged_behind_launch(c, q, reinterpret_cast<float *>(own), own_lse, Hq, Tq, causal, P, scale, workspace, &states, s);
+    if (st == OK)
+        st = c.d == 64    ? (f8 ? prefix_run<64, true>(c, a, s) : prefix_run<64, false>(c, a, s))
              : c.d == 128 ? (f8 ? prefix_run<128, true>(c, a, s) : prefix_run<128, false>(c, a, s))
                           : (f8 ? prefix_run<256, true>(c, a, s) : prefix_run<256, false>(c, a, s));
-    if (st == OK)
-        st = paged_behind_launch(c, q, reinterpret_cast<float *>(own), own_lse, Hq, Tq, causal, P, scale, workspace, s);
     if (st != OK)
         return st;
-    PrefixJoinArgs j{part, reinterpret_cast<const float *>(own), own_lse, a.ml_at, static_cast<__nv_bfloat16 *>(o), lse, Hq, a.G, Tq, a.GT,
-                     a.RP, a.runs, cut.rows};
-    auto kernel = c.d == 64 ? prefix_join_kernel<64> : c.d == 128 ? prefix_join_kernel<128> : prefix_join_kernel<256>;
-    return launch_overlapped(kernel, dim3((unsigned)rows), 128, 0, 0, true, s, j);
+    PrefixJoinArgs j{part, a.ml_at, states, static_cast<__nv_bfloat16 *>(o), lse, Hq, a.G, Tq, a.GT, a.RP, a.runs, cut.rows,
+                     (long long)rows};
+    return c.d == 64 ? join_run<64>(j, s) : c.d == 128 ? join_run<128>(j, s) : join_run<256>(j, s);
 }
 
 int prefix_status_fetch_clear(cudaStream_t s, int *host_word)

@@ -381,9 +381,10 @@ int fa_decode_paged_window(const fa_kv_cache *cache, const void *q, void *o, flo
 
 /*
  * fa_decode_paged for a batch whose sequences all begin with the same n_prefix_pages full pages,
- * prefix_pages (int32, device memory): the first entries of each sequence's row of the block table, as far
+ * prefix_pages (int32, device memory): the first entries of each sequence's row of the block table too, as far
  * as its length reaches.  The prefix is read once for the rows of all sequences, in matrix products of
- * 128 rows; each sequence's own entries, behind it, as by fa_decode_paged; and the two are joined.  Results as
+ * 128 rows; each sequence's own entries, behind it, as by fa_decode_paged; and the two are joined.  (Where the sizes
+ * say that reading so little for every sequence is faster, it is fa_decode_paged.)  Results as
  * fa_decode_paged's, except that a probability meets a v of the prefix as bf16, 2^-8 of it off at most, and that
  * an infinity or NaN in the v of a prefix's entry may reach every row of its KV head in the batch.  A sequence
  * may be shorter than the prefix (one of length 0, a place of the batch without a request, sees
