@@ -232,10 +232,12 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_bwd_kernel(const __grid_
     }
 }
 
-// dw[tensor][32 features of a block]: the CTAs' sums, eight runs of CTAs side by side.
-__global__ void __launch_bounds__(256) norm_dweight_kernel(const __grid_constant__ NormBwdArgs a, int d)
+// dw[tensor][32 features of a block]: the CTAs' sums, kRuns runs of CTAs side by side, so that a warp's loads are two
+// or three rounds (5.1 us with eight runs and four loads at once, at 228 CTAs).
+constexpr int kRuns = 16;
+__global__ void __launch_bounds__(32 * kRuns) norm_dweight_kernel(const __grid_constant__ NormBwdArgs a, int d)
 {
-    __shared__ float red[8][32];
+    __shared__ float red[kRuns][32];
     pdl_launch();
     pdl_wait();
     const int w = (int)blockIdx.y, f = (int)blockIdx.x * 32 + (threadIdx.x & 31), run = threadIdx.x >> 5;
@@ -244,13 +246,14 @@ __global__ void __launch_bounds__(256) norm_dweight_kernel(const __grid_constant
     const int from = w ? a.G0 : 0, count = w ? a.groups - a.G0 : a.G0;   // its head groups
     const int total = count * (a.ctas / a.groups);
     float x = 0.f;
-#pragma unroll 4
-    for (int i = run; i < total; i += 8)
+#pragma unroll 8
+    for (int i = run; i < total; i += kRuns)
         x += __ldcg(a.part + (long long)(i / count * a.groups + from + i % count) * d + f);
     red[run][threadIdx.x & 31] = x;
     __syncthreads();
     if (run == 0) {
-        for (int i = 1; i < 8; ++i)
+#pragma unroll
+        for (int i = 1; i < kRuns; ++i)
             x += red[i][threadIdx.x];
         a.dw[w][f] = x;
     }
@@ -273,12 +276,12 @@ int norm_bwd_run(const RopeTable &t, NormBwdArgs &a, int interleaved, cudaStream
     const int runs = kNormCtas / a.groups;   // CTAs of a head group
     a.ctas = a.groups * (a.tiles < runs ? a.tiles : runs);
     if (a.ctas == 0)   // no row: the sums are 0
-        return launch_overlapped(norm_dweight_kernel, dim3(D / 32, 2), 256, 0, 0, true, s, a, D);
+        return launch_overlapped(norm_dweight_kernel, dim3(D / 32, 2), 32 * kRuns, 0, 0, true, s, a, D);
     const int st = launch_overlapped(interleaved ? norm_bwd_kernel<E, D, true> : norm_bwd_kernel<E, D, false>, dim3((unsigned)a.ctas),
                                      kNormThreads, 0, 0, true, s, t, a);
     if (st != OK || !a.part)
         return st;
-    return launch_overlapped(norm_dweight_kernel, dim3(D / 32, 2), 256, 0, 0, true, s, a, D);
+    return launch_overlapped(norm_dweight_kernel, dim3(D / 32, 2), 32 * kRuns, 0, 0, true, s, a, D);
 }
 
 template <typename E>
@@ -342,10 +345,15 @@ int norm_rope_bwd_launch(const fa_heads *x, const fa_heads *dy, const fa_heads *
     a.n = (long long)B * T;
     a.T = T;
     a.rot = spec.rot;
-    // as in the forward, and so many that every head group has a CTA
-    const int hpc = H > 0 ? heads_per_cta(a.n, (int)H, spec.d) : 1, least = (int)((H + kNormCtas - 3) / (kNormCtas - 2));
-    a.heads_per_cta = hpc > least ? hpc : least;
-    a.G0 = (a.H[0] + a.heads_per_cta - 1) / a.heads_per_cta;
+    // Heads of a group: as few as let every tile of every group have a CTA of its own, up to 32, and so many that every
+    // group has a CTA.  B2 T1021 of 6 + 2 heads of 64, fp32: a head a group is 344 tiles, two of them for some CTAs
+    const int tok = kNormThreads / (spec.d / 16), least = (int)((H + kNormCtas - 3) / (kNormCtas - 2));
+    const long long tiles = (a.n + tok - 1) / tok;
+    auto groups_of = [&](int hpc) { return (a.H[0] + hpc - 1) / hpc; };
+    a.heads_per_cta = least > 1 ? least : 1;
+    while (a.heads_per_cta < 32 && (groups_of(a.heads_per_cta) + (a.H[1] + a.heads_per_cta - 1) / a.heads_per_cta) * tiles > kNormCtas)
+        ++a.heads_per_cta;
+    a.G0 = groups_of(a.heads_per_cta);
     a.groups = a.G0 + (a.H[1] + a.heads_per_cta - 1) / a.heads_per_cta;
     a.groups = a.groups > 0 ? a.groups : 1;
     a.dw[0] = dq_weight;

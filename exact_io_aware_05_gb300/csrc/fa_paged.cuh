@@ -1201,7 +1201,7 @@ __device__ __forceinline__ Parts parts_of(long long share, long long first, int 
 constexpr int kJoinThreads = 128, kWeightRun = 4 * kJoinThreads;
 constexpr int kMaxCtas = 3 * kSMs, kMaxParts = kMaxCtas;
 
-template <int D, bool RANGED>
+template <int D>
 __global__ void __launch_bounds__(kJoinThreads, 8) paged_join_kernel(const __grid_constant__ PagedArgs a, int wchunks, int rpb)
 {
     __shared__ float wt[kMaxParts], row_lse[kMaxRows], sums[kJoinThreads * 2], red[8];
@@ -1217,7 +1217,7 @@ __global__ void __launch_bounds__(kJoinThreads, 8) paged_join_kernel(const __gri
     // attention is past its own wait (or after the kernel before this one has ended).  All that it wrote is read behind
     // the wait, in two steps: the place, then everything of the states at once (loads that wait for one
     // another cost 0.7 us each).
-    const int len = length_in_range(a, __ldcg(a.lens + b)), nt = tiles_in<RANGED>(a, len);
+    const int len = length_in_range(a, __ldcg(a.lens + b)), nt = tiles_in<false>(a, len);
     pdl_wait();
     const long long share = a.where[0], place = a.where[1 + b];
     if (a.may_whole && share == 0)
@@ -1298,10 +1298,7 @@ __global__ void __launch_bounds__(kJoinThreads, 8) paged_join_kernel(const __gri
                     x.y += z.y;
                 }
                 const float k = l == 0.f ? 0.f : 1.f / l;
-                if (RANGED && a.o32)
-                    *reinterpret_cast<float2 *>(a.o32 + grow * D + f) = make_float2(x.x * k, x.y * k);
-                else
-                    *reinterpret_cast<uint32_t *>(a.o + grow * D + f) = pack_bf16x2(x.x * k, x.y * k);
+                *reinterpret_cast<uint32_t *>(a.o + grow * D + f) = pack_bf16x2(x.x * k, x.y * k);
                 if (tid == 0)
                     a.lse[grow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
             }
@@ -1343,6 +1340,84 @@ __global__ void __launch_bounds__(kJoinThreads, 8) paged_join_kernel(const __gri
                               rb == a.RB - 1);
         __syncthreads();
     }
+}
+
+// RANGED: a warp a row, which has few states; the first AHEAD of them are read whole at once, behind the place and
+// nothing else.
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) range_join_kernel(const __grid_constant__ PagedArgs a)
+{
+    constexpr int F = D / 32, AHEAD = 4;
+    pdl_launch();
+    const int lane = (int)lane_id();
+    const long long row = (long long)blockIdx.x * (kJoinThreads / 32) + warp_id();   // (b Hq + head) Tq + t
+    const bool here = row < (long long)a.B * a.Hq * a.Tq;
+    const int t = (int)(row % a.Tq), head = (int)(row / a.Tq % a.Hq), b = (int)(row / a.Tq / a.Hq);
+    const int h = head / a.G, i = (head - h * a.G) * a.Tq + t, rb = i / a.rows, ri = i - rb * a.rows;
+    // the lengths in front of the wait, as in paged_join_kernel
+    const int len = here ? length_in_range(a, __ldcg(a.lens + b)) : 0, nt = here ? tiles_in<true>(a, len) : 0;
+    pdl_wait();
+    if (!here)
+        return;
+    const long long share = __ldcg(a.where), place = __ldcg(a.where + 1 + b);
+    if (share == 0)
+        return;   // whole units: nothing is left to do
+    const Parts p = parts_of(share, place, rb * a.Hkv + h, nt);
+    if (!p.none && p.c0 == p.c1)
+        return;
+    const long long stride = (long long)a.rows * (D + 2);
+    const int n = p.none ? 0 : p.c1 - p.c0 + 1;
+    auto slot = [&](int s) { return a.part + (s == 0 ? p.s0 : 2ll * (p.c0 + s)) * stride; };
+    auto state = [&](int s) {
+        return s < n ? make_float2(__ldcg(slot(s) + (long long)a.rows * D + ri), __ldcg(slot(s) + (long long)a.rows * (D + 1) + ri))
+                     : make_float2(-INFINITY, 0.f);
+    };
+    float y[AHEAD][F];
+    float2 st[AHEAD];
+#pragma unroll
+    for (int s = 0; s < AHEAD; ++s) {
+        st[s] = state(s);
+#pragma unroll
+        for (int f = 0; f < F; f += 2) {
+            const float2 z = s < n ? __ldcg(reinterpret_cast<const float2 *>(slot(s) + (long long)ri * D + lane * F + f)) : make_float2(0.f, 0.f);
+            y[s][f] = z.x, y[s][f + 1] = z.y;
+        }
+    }
+    float m = -INFINITY, l = 0.f, x[F];
+    for (int s = lane; s < n; s += 32)
+        m = fmaxf(m, state(s).x);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+#pragma unroll
+    for (int f = 0; f < F; ++f)
+        x[f] = 0.f;
+#pragma unroll
+    for (int s = 0; s < AHEAD; ++s) {
+        const float w = st[s].x == -INFINITY ? 0.f : ex2_approx(st[s].x - m);
+        l = fmaf(w, st[s].y, l);
+#pragma unroll
+        for (int f = 0; f < F; ++f)
+            x[f] = fmaf(w, y[s][f], x[f]);
+    }
+#pragma unroll 4
+    for (int s = AHEAD; s < n; ++s) {
+        const float2 z = state(s);
+        const float w = z.x == -INFINITY ? 0.f : ex2_approx(z.x - m);
+        l = fmaf(w, z.y, l);
+#pragma unroll
+        for (int f = 0; f < F; f += 2) {
+            const float2 u = __ldcg(reinterpret_cast<const float2 *>(slot(s) + (long long)ri * D + lane * F + f));
+            x[f] = fmaf(w, u.x, x[f]);
+            x[f + 1] = fmaf(w, u.y, x[f + 1]);
+        }
+    }
+    const float k = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+    for (int f = 0; f < F; f += 2)
+        *reinterpret_cast<uint32_t *>(a.o + row * D + lane * F + f) = pack_bf16x2(x[f] * k, x[f + 1] * k);
+    if (lane == 0)
+        a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
 }
 
 // ------------------------------------------------------------------ host
@@ -1396,8 +1471,11 @@ int paged_run(const fa_kv_cache &c, PagedArgs &a, cudaStream_t s)
     a.grid = kSMs * ctas;
     // tiles, at most: those of a window begin and end anywhere, and so do the sinks'
     const long long most = (long long)a.B * a.Hkv * a.RB * std::min((a.cap + a.kt - 1) / a.kt, RANGED ? a.span / a.kt + 3 : INT_MAX);
-    // RANGED: more units than CTAs at a time may be whole ones too, taken by CTAs as others end
-    a.may_whole = a.may_whole && most > 0 && (long long)a.B * a.Hkv * a.RB <= (RANGED ? 8 : 1) * a.grid;
+    // RANGED: up to two whole units for each CTA at a time, taken as others end.  us whole and in shares, 8 KV heads of
+    // 128: 64 sequences of 20 to 700 entries 26.8 and 35.1 (a share of many short units has many starts), of 360 23.6 and
+    // 24.6, of 1024 48.9 and 49.9, of 100 to 2000 under a window of 700 34.4 and 38.4; with more units a CTA
+    // shares are better: 96 of 20 to 3000 107.9 and 103.3, 128 of 512 58.2 and 49.5, 200 of 300 69.6 and 53.2
+    a.may_whole = a.may_whole && most > 0 && (long long)a.B * a.Hkv * a.RB <= (RANGED ? 2 : 1) * a.grid;
     int st = OK;
     if (most > 0) {
         CUtensorMap tk, tv;
@@ -1423,14 +1501,21 @@ int paged_run(const fa_kv_cache &c, PagedArgs &a, cudaStream_t s)
     }
     if ((a.whole && most > 0) || (RANGED && a.o32))
         return OK;
-    const int wchunks = a.scores ? (a.cap + kWeightRun - 1) / kWeightRun : 0;
-    // rows a block: one, unless that makes more blocks than the device holds at a time
-    const long long units = (long long)a.B * a.Hkv * a.RB, held = 8 * kSMs;
-    const int rpb = (int)std::min<long long>(a.rows, (units * a.rows + held - 1) / held);
-    const long long blocks = units * ((a.rows + rpb - 1) / rpb) + (long long)a.B * a.Hkv * wchunks;
-    if (blocks > INT_MAX)
-        return ERR_UNSUPPORTED;
-    return launch_overlapped(paged_join_kernel<D, RANGED>, dim3((unsigned)blocks), kJoinThreads, 0, 0, most > 0, s, a, wchunks, rpb);
+    if constexpr (RANGED) {
+        const long long blocks = ((long long)a.B * a.Hq * a.Tq + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
+        if (blocks > INT_MAX)
+            return ERR_UNSUPPORTED;
+        return launch_overlapped(range_join_kernel<D>, dim3((unsigned)blocks), kJoinThreads, 0, 0, most > 0, s, a);
+    } else {
+        const int wchunks = a.scores ? (a.cap + kWeightRun - 1) / kWeightRun : 0;
+        // rows a block: one, unless that makes more blocks than the device holds at a time
+        const long long units = (long long)a.B * a.Hkv * a.RB, held = 8 * kSMs;
+        const int rpb = (int)std::min<long long>(a.rows, (units * a.rows + held - 1) / held);
+        const long long blocks = units * ((a.rows + rpb - 1) / rpb) + (long long)a.B * a.Hkv * wchunks;
+        if (blocks > INT_MAX)
+            return ERR_UNSUPPORTED;
+        return launch_overlapped(paged_join_kernel<D>, dim3((unsigned)blocks), kJoinThreads, 0, 0, most > 0, s, a, wchunks, rpb);
+    }
 }
 
 // The arguments that both files' launches share.

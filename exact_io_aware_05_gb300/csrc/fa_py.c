@@ -18,6 +18,8 @@ typedef int (*rope_fn)(const fa_heads *, const fa_heads *, int, const int *, con
                        fa_stream_t);
 typedef int (*norm_rope_fn)(const fa_heads *, const fa_heads *, int, const fa_head_norm *, const int *, const fa_rope_spec *, int,
                             int, int, fa_stream_t);
+typedef int (*norm_rope_bwd_fn)(const fa_heads *, const fa_heads *, const fa_heads *, int, const fa_head_norm *, const int *,
+                                const fa_rope_spec *, int, int, int, float *, float *, void *, size_t, fa_stream_t);
 typedef int (*append_fn)(const fa_kv_cache *, const fa_heads *, const fa_heads *, const fa_heads *, const fa_heads *,
                          const int *, const fa_rope_spec *, const fa_head_norm *, const int *, int, fa_stream_t);
 typedef int (*decode_fn)(const fa_kv_cache *, const void *, void *, float *, int, int, int, float, int, void *, size_t,
@@ -30,6 +32,7 @@ typedef int (*evict_fn)(const fa_kv_cache *, int, int, int, float *, int *, int 
 
 static rope_fn call_rope;
 static norm_rope_fn call_norm_rope;
+static norm_rope_bwd_fn call_norm_rope_bwd;
 static append_fn call_append;
 static decode_fn call_decode;
 static evict_fn call_evict;
@@ -260,6 +263,45 @@ static PyObject *py_norm_rope(PyObject *self, PyObject *const *a, Py_ssize_t n)
     return PyLong_FromLong(st);
 }
 
+/* norm_rope_bwd(spec, norm, norm's index, dq_out, dq, dk_out, dk, positions, stream, q, k, dq_weight, dk_weight, workspace) */
+static PyObject *py_norm_rope_bwd(PyObject *self, PyObject *const *a, Py_ssize_t n)
+{
+    (void)self;
+    if (n != 14)
+        return PyErr_Format(PyExc_TypeError, "norm_rope_bwd: 14 arguments");
+    const fa_rope_spec *spec = (const fa_rope_spec *)PyLong_AsVoidPtr(a[0]);
+    const fa_head_norm *norm;
+    rotary r;
+    if (!spec || !rotary_of(spec, a + 3, a[8], &r) || !norm_of(a[1], a[2], r.dev, &norm) || norm->d != spec->d ||
+        (a[10] != Py_None) != (r.n == 2))
+        return slow();
+    PyObject *dtype = r.dtype == FA_BF16 ? t_bf16 : t_f32;
+    const long long width[1] = {spec->d};
+    fa_heads x[2];
+    void *dw[2] = {NULL, NULL}, *ws = NULL;
+    long long bytes = 0;
+    int ok = 1;
+    for (int i = 0; i < r.n; ++i)
+        if (!heads(a[9 + i], dtype, r.B, r.x[i].H, r.T, spec->d, r.dev, &x[i]))
+            return slow();
+    for (int i = 0; i < 2; ++i)
+        if (a[11 + i] != Py_None && (i >= r.n || !(i ? norm->k_weight : norm->q_weight) || !plain(a[11 + i], t_f32, 1, width, r.dev, &dw[i])))
+            return slow();
+    if (dw[0] || dw[1]) {
+        if (a[13] == Py_None || !on_device(a[13], r.dev) || !is_contiguous(a[13]) || !data_of(a[13], &ws))
+            return slow();
+        bytes = taken_int(PyObject_GetAttr(a[13], n_nbytes), &ok);
+        if (!ok)
+            return slow();
+    }
+    int st;
+    Py_BEGIN_ALLOW_THREADS;
+    st = call_norm_rope_bwd(r.x, x, r.y, r.n, norm, (const int *)r.pos, spec, r.B, r.T, r.dtype, (float *)dw[0], (float *)dw[1], ws,
+                            (size_t)bytes, r.stream);
+    Py_END_ALLOW_THREADS;
+    return PyLong_FromLong(st);
+}
+
 /* append(cache, index, k, v, positions, spec, q, q_out, new_lens, stream[, norm, norm's index]); spec and norm None
  * or an address */
 static PyObject *py_append(PyObject *self, PyObject *const *a, Py_ssize_t n)
@@ -424,7 +466,7 @@ static PyObject *py_evict(PyObject *self, PyObject *const *a, Py_ssize_t n)
     return PyLong_FromLong(st);
 }
 
-enum { ENTRIES = 7 };
+enum { ENTRIES = 8 };
 
 /* setup(bfloat16, float32, int32, stream function, device function, addresses of the entry points) */
 static PyObject *py_setup(PyObject *self, PyObject *const *a, Py_ssize_t n)
@@ -450,6 +492,7 @@ static PyObject *py_setup(PyObject *self, PyObject *const *a, Py_ssize_t n)
     call_evict = (evict_fn)fn[4];
     call_decode_window = (decode_window_fn)fn[5];
     call_decode_shared = (decode_shared_fn)fn[6];
+    call_norm_rope_bwd = (norm_rope_bwd_fn)fn[7];
     Py_RETURN_NONE;
 }
 
@@ -457,6 +500,7 @@ static PyMethodDef methods[] = {
     {"setup", (PyCFunction)(void (*)(void))py_setup, METH_FASTCALL, NULL},
     {"rope", (PyCFunction)(void (*)(void))py_rope, METH_FASTCALL, NULL},
     {"norm_rope", (PyCFunction)(void (*)(void))py_norm_rope, METH_FASTCALL, NULL},
+    {"norm_rope_bwd", (PyCFunction)(void (*)(void))py_norm_rope_bwd, METH_FASTCALL, NULL},
     {"append", (PyCFunction)(void (*)(void))py_append, METH_FASTCALL, NULL},
     {"decode", (PyCFunction)(void (*)(void))py_decode, METH_FASTCALL, NULL},
     {"decode_window", (PyCFunction)(void (*)(void))py_decode_window, METH_FASTCALL, NULL},

@@ -553,7 +553,7 @@ _current_device = torch._C._cuda_getDevice
 
 class _Without:
     """Stands for _fa_py where it is missing: no call passes its checks."""
-    rope = norm_rope = append = decode = decode_window = decode_shared = evict = staticmethod(lambda *args: None)
+    rope = norm_rope = norm_rope_bwd = append = decode = decode_window = decode_shared = evict = staticmethod(lambda *args: None)
 
 
 if _fa_py is None:
@@ -562,7 +562,8 @@ else:
     _fast = _fa_py
     _fa_py.setup(torch.bfloat16, torch.float32, torch.int32, _current_stream, _current_device,
                  *(ctypes.cast(f, _vp).value for f in (_lib.fa_rope, _lib.fa_norm_rope, _lib.fa_cache_append_norm, _lib.fa_decode_paged,
-                                                       _lib.fa_cache_evict, _lib.fa_decode_paged_window, _lib.fa_decode_paged_shared)))
+                                                       _lib.fa_cache_evict, _lib.fa_decode_paged_window, _lib.fa_decode_paged_shared,
+                                                       _lib.fa_norm_rope_bwd)))
 
 
 def _launch(fn: str, entry, index: int, stream, *args) -> None:
@@ -765,6 +766,14 @@ def fa_norm_rope_bwd(dq_out, q, dq, positions, spec: RopeSpec, norm: HeadNorm, d
     """Backward of fa_norm_rope: dq from dq_out, the gradient of q_out, and q (dk from dk_out and k); dq_weight
     and dk_weight, float32 [d], if given, are set to the gradients of the weights, for which a workspace of
     fa_norm_rope_bwd_workspace_bytes(d) bytes is needed.  dq may be dq_out."""
+    st = _fast.norm_rope_bwd(spec._ref, norm._ref, norm._index, dq_out, dq, dk_out, dk, positions, stream, q, k, dq_weight, dk_weight,
+                             workspace)
+    if st != FA_OK:
+        _again(st, "fa_norm_rope_bwd", _norm_rope_bwd, dq_out, q, dq, positions, spec, norm, dk_out, k, dk, dq_weight, dk_weight,
+               workspace, stream)
+
+
+def _norm_rope_bwd(dq_out, q, dq, positions, spec, norm, dk_out, k, dk, dq_weight, dk_weight, workspace, stream) -> None:
     if (k is None) != (dk_out is None):
         raise ValueError("k, dk_out and dk come together")
     n, g, dx, B, T, dt, index = _rope_heads(dq_out, dq, positions, spec, dk_out, dk)

@@ -234,6 +234,19 @@ def test_both_ways_of_calling(fa):
         assert call(spec._ref, norm._ref, norm._index + 1, q, qo, k, ko, pos, None) is None
         assert call(spec._ref, norm._ref, norm._index, q, qo.float(), k, ko, pos, None) is None
         assert call(spec._ref, norm._ref, norm._index, q, qo, k, None, pos, None) is None
+    g = torch.empty((2, 2, 128), device=DEV)
+    ws = torch.empty(fa.fa_norm_rope_bwd_workspace_bytes(128), dtype=torch.uint8, device=DEV)
+    got = []
+    for way, f in enumerate((fa.fa_norm_rope_bwd, fa._norm_rope_bwd)):
+        dq, dk = torch.empty_like(q), torch.empty_like(k)
+        f(qo, q, dq, pos, spec, norm, ko, k, dk, g[way, 0], g[way, 1], ws, None)
+        got.append((dq, dk))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1]) and torch.equal(g[0], g[1])
+    if fa._fa_py is not None:
+        call, args = fa._fa_py.norm_rope_bwd, [spec._ref, norm._ref, norm._index, qo, dq, ko, dk, pos, None, q, k, g[0, 0], g[0, 1], ws]
+        assert call(*args) == fa.FA_OK
+        for at, bad in ((9, q.float()), (10, None), (11, g[0]), (13, None), (2, norm._index + 1)):
+            assert call(*args[:at], bad, *args[at + 1:]) is None
     with pytest.raises(ValueError):
         fa.fa_norm_rope(q, qo, pos, spec, fa.HeadNorm(64), k, ko)
     with pytest.raises(ValueError):
