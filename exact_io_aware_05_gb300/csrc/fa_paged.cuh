@@ -1360,7 +1360,7 @@ __global__ void __launch_bounds__(kJoinThreads) range_join_kernel(const __grid_c
     if (!here)
         return;
     const long long share = __ldcg(a.where), place = __ldcg(a.where + 1 + b);
-    if (share == 0)
+    if (a.may_whole && share == 0)
         return;   // whole units: nothing is left to do
     const Parts p = parts_of(share, place, rb * a.Hkv + h, nt);
     if (!p.none && p.c0 == p.c1)

@@ -172,6 +172,24 @@ def test_both_ways_captured_and_shared_workspace(fa):
     assert fa.fa_sync_status() == fa.FA_OK
 
 
+def test_without_slots_pages_or_entries(fa):
+    """Tables without a slot, pools without a page, batches without an entry or a sequence: zeros, whatever the
+    workspace held."""
+    for pages, width, lens in ((0, 0, [0, 0]), (0, 3, [0, 0]), (4, 0, [0]), (4, 2, [0, 0, 0]), (4, 700, [0] * 70), (4, 2, [])):
+        k = torch.zeros((pages, 2, 16, 64), dtype=BF16, device=DEV)
+        cache = fa.KVCache(k, k.clone(), torch.zeros((len(lens), width), dtype=I32, device=DEV), torch.tensor(lens, dtype=I32, device=DEV))
+        q = randn(gen(1), len(lens), 4, 2, 64)
+        o, lse = torch.full_like(q, 7), torch.full(q.shape[:3], 7.0, device=DEV)
+        for fill in (0, 255):
+            ws = torch.full((max(fa.fa_decode_paged_window_workspace_bytes(cache, 4, 2), 256),), fill, dtype=torch.uint8, device=DEV)
+            fa.fa_decode_paged_window(cache, q, o.fill_(7), lse.fill_(7), 3, 4, 0.1, ws)
+            assert fa.fa_sync_status() == fa.FA_OK and torch.all(o == 0) and torch.all(lse == -np.inf)
+        none = torch.zeros(0, dtype=I32, device=DEV)
+        ws = torch.zeros(max(fa.fa_decode_paged_shared_workspace_bytes(cache, 4, 2, none), 256), dtype=torch.uint8, device=DEV)
+        fa.fa_decode_paged_shared(cache, q, o.fill_(7), lse.fill_(7), none, 0.1, ws)
+        assert fa.fa_sync_status() == fa.FA_OK and torch.all(o == 0) and torch.all(lse == -np.inf)
+
+
 def test_bad_lengths_and_pages(fa):
     cache = make_cache(fa, 12, [500, 500, 500, 500], 2, 64, 16)
     q = randn(gen(13), 4, 4, 1, 64)
