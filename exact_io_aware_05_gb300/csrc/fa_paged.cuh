@@ -1182,13 +1182,20 @@ struct Parts {
     bool none;   // no entry at all
 };
 
+// (SHORT: by 32-bit divisions where they do.)
+template <bool SHORT = false>
 __device__ __forceinline__ Parts parts_of(long long share, long long first, int ul, int nt)   // a.where[0], [1 + b]
 {
     Parts p{0, 0, 0, nt == 0};
     if (nt > 0) {
         const long long t = first + (long long)ul * nt;
-        p.c0 = (int)(t / share);
-        p.c1 = (int)((t + nt - 1) / share);
+        if (SHORT && ((t + nt) | share) >> 32 == 0) {
+            p.c0 = (int)((uint32_t)t / (uint32_t)share);
+            p.c1 = (int)((uint32_t)(t + nt - 1) / (uint32_t)share);
+        } else {
+            p.c0 = (int)(t / share);
+            p.c1 = (int)((t + nt - 1) / share);
+        }
         p.s0 = 2ll * p.c0 + (t == p.c0 * share ? 0 : 1);
     }
     return p;
@@ -1350,9 +1357,10 @@ __global__ void __launch_bounds__(kJoinThreads) range_join_kernel(const __grid_c
     constexpr int F = D / 32, AHEAD = 4;
     pdl_launch();
     const int lane = (int)lane_id();
-    const long long row = (long long)blockIdx.x * (kJoinThreads / 32) + warp_id();   // (b Hq + head) Tq + t
-    const bool here = row < (long long)a.B * a.Hq * a.Tq;
-    const int t = (int)(row % a.Tq), head = (int)(row / a.Tq % a.Hq), b = (int)(row / a.Tq / a.Hq);
+    const uint32_t row = blockIdx.x * (kJoinThreads / 32) + warp_id();   // (b Hq + head) Tq + t
+    const bool here = row < (uint32_t)(a.B * a.Hq * a.Tq);
+    const uint32_t bh = row / (uint32_t)a.Tq, b32 = bh / (uint32_t)a.Hq;
+    const int t = (int)(row - bh * (uint32_t)a.Tq), head = (int)(bh - b32 * (uint32_t)a.Hq), b = (int)b32;
     const int h = head / a.G, i = (head - h * a.G) * a.Tq + t, rb = i / a.rows, ri = i - rb * a.rows;
     // the lengths in front of the wait, as in paged_join_kernel
     const int len = here ? length_in_range(a, __ldcg(a.lens + b)) : 0, nt = here ? tiles_in<true>(a, len) : 0;
@@ -1362,7 +1370,7 @@ __global__ void __launch_bounds__(kJoinThreads) range_join_kernel(const __grid_c
     const long long share = __ldcg(a.where), place = __ldcg(a.where + 1 + b);
     if (a.may_whole && share == 0)
         return;   // whole units: nothing is left to do
-    const Parts p = parts_of(share, place, rb * a.Hkv + h, nt);
+    const Parts p = parts_of<true>(share, place, rb * a.Hkv + h, nt);
     if (!p.none && p.c0 == p.c1)
         return;
     const long long stride = (long long)a.rows * (D + 2);
@@ -1415,7 +1423,7 @@ __global__ void __launch_bounds__(kJoinThreads) range_join_kernel(const __grid_c
     const float k = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
     for (int f = 0; f < F; f += 2)
-        *reinterpret_cast<uint32_t *>(a.o + row * D + lane * F + f) = pack_bf16x2(x[f] * k, x[f + 1] * k);
+        *reinterpret_cast<uint32_t *>(a.o + (long long)row * D + lane * F + f) = pack_bf16x2(x[f] * k, x[f + 1] * k);
     if (lane == 0)
         a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
 }

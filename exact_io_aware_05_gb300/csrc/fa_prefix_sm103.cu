@@ -86,7 +86,8 @@ struct PrefixArgs {
     float *part;      // [unit][run][row] of D floats, then of (m, l)
     long long ml_at;  // floats in front of the (m, l)
     int B, Hq, Hkv, G, Tq, GT, R, RP;   // rows of a KV head, and CTAs' blocks of them
-    int causal, P, num_pages, ps_shift, cap, tiles, runs;
+    int causal, P, num_pages, ps_shift, cap, runs;
+    int run_tiles, run_more;            // tiles of a run; the first run_more have one more
     float scale_log2;
     uint64_t timeout_ns;
     int withhold;     // test builds: the arrive that is left out
@@ -154,7 +155,7 @@ __global__ void __launch_bounds__(XCfg<D, FP8>::NTHREADS, 1)
     const int rp = (int)blockIdx.x % a.RP, hr = (int)blockIdx.x / a.RP, run = hr % a.runs, h = hr / a.runs;
     const int row0 = rp * NQ * BR;
     const int nq = NQ == 2 && a.R - row0 > BR ? 2 : 1;   // query tiles with a row
-    const int t0 = (int)((long long)a.tiles * run / a.runs), n = (int)((long long)a.tiles * (run + 1) / a.runs) - t0;
+    const int t0 = run * a.run_tiles + min(run, a.run_more), n = a.run_tiles + (run < a.run_more ? 1 : 0);
     if (threadIdx.x == 0) {
         for (int s = 0; s < NSLOT; ++s) {
             mbar_init(bar(C::B_FULL + s), FP8 ? 128 : 1);
@@ -533,6 +534,12 @@ struct PrefixJoinArgs {
     long long n;           // rows of o
 };
 
+// x / y of nonnegative values, which seldom have more than 32 bits.
+__device__ __forceinline__ long long quotient(long long x, long long y)
+{
+    return ((x | y) >> 32) == 0 ? (long long)((uint32_t)x / (uint32_t)y) : x / y;
+}
+
 // W warps a row: each takes every W-th state (the runs', then the own entries'), a lane D / 32 features; then the
 // warps' sums.  The first states of each warp are under way before anything is known of them.
 template <int D, int W>
@@ -542,12 +549,15 @@ __global__ void __launch_bounds__(128) prefix_join_kernel(const __grid_constant_
     __shared__ float sum[W == 1 ? 1 : 4][D], red[4];
     pdl_launch();
     const int warp = (int)warp_id() % W, lane = (int)lane_id();
-    const long long row = (long long)blockIdx.x * (4 / W) + warp_id() / W;   // (b Hq + head) Tq + t
+    // 32-bit divisions: those of 64 bits were 3 us of it
+    const uint32_t row32 = blockIdx.x * (4 / W) + warp_id() / W;   // (b Hq + head) Tq + t
+    const long long row = row32;
     if (row >= a.n) {
         pdl_wait();
         return;
     }
-    const int t = (int)(row % a.Tq), head = (int)(row / a.Tq % a.Hq), b = (int)(row / a.Tq / a.Hq);
+    const uint32_t bh = row32 / (uint32_t)a.Tq, b32 = bh / (uint32_t)a.Hq;
+    const int t = (int)(row32 - bh * (uint32_t)a.Tq), head = (int)(bh - b32 * (uint32_t)a.Hq), b = (int)b32;
     const int h = head / a.G, i = (head - h * a.G) * a.Tq + t, r = b * a.GT + i;   // KV head, row of its group, of its matrix
     const long long at = (long long)(h * a.RP + r / a.rows) * a.runs * a.rows + r % a.rows;
     // The lengths may be read in front of the wait: all kernels before the attention's had ended when this one
@@ -591,7 +601,8 @@ __global__ void __launch_bounds__(128) prefix_join_kernel(const __grid_constant_
         const long long share = where0;
         whole = share == 0;
         if (!whole) {
-            const long long tile = where1 + (long long)(rb * a.own.Hkv + h) * nt, c0 = tile / share, c1 = (tile + nt - 1) / share;
+            const long long tile = where1 + (long long)(rb * a.own.Hkv + h) * nt;
+            const long long c0 = quotient(tile, share), c1 = quotient(tile + nt - 1, share);
             whole = c0 == c1;
             own = (int)(c1 - c0) + 1;
             first = a.own.part + (2 * c0 + (tile == c0 * share ? 0 : 1)) * stride;
@@ -814,8 +825,9 @@ int prefix_launch(const fa_kv_cache &c, const void *q, void *o, float *lse, int 
     while ((1 << a.ps_shift) < c.page_size)
         ++a.ps_shift;
     a.cap = c.max_pages * c.page_size;
-    a.tiles = cut.tiles;
     a.runs = cut.runs;
+    a.run_tiles = cut.tiles / cut.runs;
+    a.run_more = cut.tiles % cut.runs;
     a.scale_log2 = std::min(scale * 1.4426950408889634f, FLT_MAX);
     a.timeout_ns = wait_timeout_ns();
     a.withhold = WITHHOLD_NONE;
