@@ -163,12 +163,17 @@ __global__ void __launch_bounds__(kRopeThreads, 2) append_kernel(const __grid_co
     // projection
     const int tile = (int)(blockIdx.x / a.groups), group = (int)blockIdx.x - tile * a.groups;
     const long long tok = (long long)tile * (kRopeThreads / TPR) + threadIdx.x / TPR;
+    const Slice sl = slice_of(vec, a.rotate ? a.rot : 0, INTER);
+    __shared__ __align__(16) float weight[2][NORM ? D : 1];
+    if constexpr (NORM) {
+        put_norm_weights<D>(a.norm, sl, weight);
+        __syncthreads();
+    }
     if (tok >= n)
         return;
     const int b = (int)tok / a.T, t = (int)tok - b * a.T;
     const int len = a.lens[b], cap = a.max_pages << a.ps_shift;
     const int nb = a.new_lens ? a.new_lens[b] : a.T;
-    const Slice sl = slice_of(vec, a.rotate ? a.rot : 0, INTER);
     const int h0 = group * a.heads_per_cta, h1 = min(a.Hq + 2 * a.Hkv, h0 + a.heads_per_cta);
     const bool turns = sl.pair >= 0 && h0 < a.Hq + a.Hkv;
     int pos[8];
@@ -177,13 +182,6 @@ __global__ void __launch_bounds__(kRopeThreads, 2) append_kernel(const __grid_co
         for (int j = 0; j < 8; ++j)
             pos[j] = a.pos[(long long)tab.axis[sl.pair + j] * n + tok];
     }
-    float wf[8], wg[8];   // of the first tensor that the group has
-    auto weights = [&](int which) {
-        norm_weights(a.norm, which, sl.e0, wf);
-        norm_weights(a.norm, which, sl.e1, wg);
-    };
-    if (NORM && h0 < a.Hq + a.Hkv)
-        weights(h0 < a.Hq ? 0 : 1);
     if (len < 0 || len > cap || nb < 0 || nb > a.T || nb > len) {
         if (vec == 0 && t == 0 && group == 0)
             atomicCAS(&g_cache_status, 0, kStatusBadIndex);
@@ -223,7 +221,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) append_kernel(const __grid_co
             o += a.qo.sh;
         };
         if constexpr (NORM)
-            each_head_normed<E, D>(x, a.q.sh, count, sl, wf, wg, a.norm.eps, put);
+            each_head_normed<E, D, 4>(x, a.q.sh, count, sl, weight[0], a.norm.eps, [] {}, put);
         else
             each_head(x, a.q.sh, count, sl, put);
     }
@@ -249,13 +247,10 @@ __global__ void __launch_bounds__(kRopeThreads, 2) append_kernel(const __grid_co
                     a.order[w] = (a.seen ? a.seen[b] - nb : len - nb) + t;
             }
         };
-        if constexpr (NORM) {
-            if (h0 < a.Hq)
-                weights(1);
-            each_head_normed<E, D>(x, a.k.sh, count, sl, wf, wg, a.norm.eps, put);
-        } else {
+        if constexpr (NORM)
+            each_head_normed<E, D, 4>(x, a.k.sh, count, sl, weight[1], a.norm.eps, [] {}, put);
+        else
             each_head(x, a.k.sh, count, sl, put);
-        }
     }
     if (part(a.Hq + a.Hkv, a.Hkv, first, count)) {
         const E *x = static_cast<const E *>(a.v.p) + b * a.v.sb + first * a.v.sh + t * a.v.st;

@@ -206,49 +206,67 @@ __device__ __forceinline__ float sum_squares(const float (&f)[8], const float (&
     return s0 + s1;
 }
 
-// each_head with rows normed by weights wf (at e0) and wg (at e1) on the way.  The sums of all heads under
-// way are put together before the first of them is used.
-template <typename E, int D, typename Put>
-__device__ __forceinline__ void each_head_normed(const E *x, long long sx, int n, const Slice &sl, const float (&wf)[8],
-                                                 const float (&wg)[8], float eps, Put put)
+// The weights of both tensors in shared memory, [2][D]; the threads of the block's first row or two put them there.
+template <int D>
+__device__ __forceinline__ void put_norm_weights(const NormArgs &a, const Slice &sl, float (*weight)[D])
 {
-    constexpr int AHEAD = sizeof(E) == 2 ? 4 : 3;
+    constexpr int TPR = D / 16;
+    if (threadIdx.x < 2 * TPR) {
+        const int w = threadIdx.x / TPR;
+        float t[8];
+        norm_weights(a, w, sl.e0, t);
+        store8(weight[w] + sl.e0, t);
+        norm_weights(a, w, sl.e1, t);
+        store8(weight[w] + sl.e1, t);
+    }
+}
+
+// each_head with rows normed by `weight` (shared memory) on the way.  Loads run AHEAD heads ahead: a head's values go
+// to fp32 registers, its buffer is filled again, and only then they are used.  between() runs behind the first
+// loads.
+template <typename E, int D, int AHEAD, typename Between, typename Put>
+__device__ __forceinline__ void each_head_normed(const E *x, long long sx, int n, const Slice &sl, const float *weight, float eps,
+                                                 Between between, Put put)
+{
     x += sl.e0;
     const int gap = sl.e1 - sl.e0;
-    for (int i = 0; i < n; i += AHEAD, x += AHEAD * sx) {
-        Raw8<E> p[AHEAD] = {}, q[AHEAD] = {};
-        float r[AHEAD];
+    Raw8<E> p[AHEAD], q[AHEAD];
+    auto fill = [&](int u) {
+        p[u].load(x);
+        q[u].load(x + gap);
+        x += sx;
+    };
 #pragma unroll
-        for (int u = 0; u < AHEAD; ++u)
-            if (i + u < n) {
-                p[u].load(x + u * sx);
-                q[u].load(x + u * sx + gap);
-            }
+    for (int u = 0; u < AHEAD; ++u)
+        if (u < n)
+            fill(u);
+    between();
+    for (int i = 0; i < n; i += AHEAD) {
 #pragma unroll
         for (int u = 0; u < AHEAD; ++u) {
+            if (i + u >= n)
+                break;
             float f[8], g[8];
             p[u].get(f);
             q[u].get(g);
-            r[u] = sum_squares(f, g);
-        }
-#pragma unroll
-        for (int u = 0; u < AHEAD; ++u)
-            r[u] = __frsqrt_rn(fmaf(row_sum<D / 16>(r[u]), 1.f / D, eps));
-#pragma unroll
-        for (int u = 0; u < AHEAD; ++u)
-            if (i + u < n) {
-                float f[8], g[8];
-                p[u].get(f);
-                q[u].get(g);
+            if (i + u + AHEAD < n)
+                fill(u);
+            const float r = __frsqrt_rn(fmaf(row_sum<D / 16>(sum_squares(f, g)), 1.f / D, eps));
+            auto scale = [&](float(&z)[8], int e) {
+                Raw8<float> rw;
+                float ww[8];
+                rw.load(weight + e);
+                rw.get(ww);
 #pragma unroll
                 for (int j = 0; j < 8; j += 2) {
-                    fmul2(f[j], f[j + 1], f[j], f[j + 1], r[u], r[u]);
-                    fmul2(g[j], g[j + 1], g[j], g[j + 1], r[u], r[u]);
-                    fmul2(f[j], f[j + 1], f[j], f[j + 1], wf[j], wf[j + 1]);
-                    fmul2(g[j], g[j + 1], g[j], g[j + 1], wg[j], wg[j + 1]);
+                    fmul2(z[j], z[j + 1], z[j], z[j + 1], r, r);
+                    fmul2(z[j], z[j + 1], z[j], z[j + 1], ww[j], ww[j + 1]);
                 }
-                put(i + u, f, g);
-            }
+            };
+            scale(f, sl.e0);
+            scale(g, sl.e1);
+            put(i + u, f, g);
+        }
     }
 }
 
