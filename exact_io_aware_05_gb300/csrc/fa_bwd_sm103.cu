@@ -1247,7 +1247,7 @@ int launch_bwd(const void *q, const void *k, const void *v, const void *o, const
         a.sinks = mask.sinks < Tk ? mask.sinks : Tk;
         const bool sinks = mask.left >= 0 && a.sinks > 0;
         a.nsb = sinks ? (a.sinks + BK - 1) / BK : 0;
-        a.parts = sinks ? bwd_sink_parts(Tq, Tk, mask) : 1;
+        a.parts = sinks ? bwd_sink_parts((size_t)BH, Tq, Tk, mask) : 1;
         a.part_len = ((Tq + BQ - 1) / BQ + a.parts - 1) / a.parts;
         a.sink_part = ws.sink_part;
         const long long units = (long long)BH * (a.nkb + (long long)a.nsb * (a.parts - 1));
@@ -1306,21 +1306,25 @@ int launch_bwd(const void *q, const void *k, const void *v, const void *o, const
 // Units that a key block with sinks is cut into.  It sees all nqb query blocks behind it, a window's block about
 // wq: in one piece it would keep one CTA busy when the others have ended (65536 rows, 6 heads of 64, window 512: 1417 us
 // in one piece, 373 in 64), so a part is as long as a window's block, but not shorter than 8, below which its
-// start and its sums cost more (B2 H16 T8192 d128, window 256: 329 us by 3, 308 by 8, 328 by 16).  Of sizes only: the
-// sums' order, and the workspace, do not depend on the device.
-int bwd_sink_parts(int Tq, int Tk, const MaskSpec &mask)
+// start and its sums cost more (B2 H16 T8192 d128, window 256: 329 us by 3, 308 by 8, 328 by 16).  And there are up to
+// eight parts for an SM, which also bounds their sums' memory: more have nothing left to even out (H32 T16384 d128, window
+// 512, 2048 sinks: 1936 us with 16 parts, 1 GB, 1739 with 4, 1649 with 2, 2029 in one piece; H32 T32768 d64, 8192 sinks: 7925
+// us with 32 parts, 4 GB, 6465 in one piece).  Of sizes only: the sums' order, and the workspace, do not depend on
+// the device.
+int bwd_sink_parts(size_t BH, int Tq, int Tk, const MaskSpec &mask)
 {
     const long long nqb = (Tq + BQ - 1) / BQ;
     const int sinks = mask.sinks < Tk ? mask.sinks : Tk;
-    if (mask.left < 0 || sinks <= 0)
+    if (mask.left < 0 || sinks <= 0 || BH == 0)
         return 1;
     const long long wq = std::min<long long>(mask.left / BQ + 2, nqb), most = std::max(wq, 8ll);
-    return (int)std::min<long long>(std::max((nqb + most - 1) / most, 1ll), 64);
+    const long long blocks = (long long)std::min<size_t>(BH, 1 << 20) * ((sinks + BK - 1) / BK);   // key blocks with sinks
+    return (int)std::min(std::max((nqb + most - 1) / most, 1ll), std::min(std::max(8 * 152 / blocks, 1ll), 64ll));
 }
 
 size_t bwd_sink_bytes(size_t BH, int Tq, int Tk, int d, const MaskSpec &mask)
 {
-    const int parts = bwd_sink_parts(Tq, Tk, mask);
+    const int parts = bwd_sink_parts(BH, Tq, Tk, mask);
     if (parts == 1)
         return 0;
     const int sinks = mask.sinks < Tk ? mask.sinks : Tk;

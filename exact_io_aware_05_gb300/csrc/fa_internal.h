@@ -118,7 +118,7 @@ struct BwdWorkspace {
     int *bound;      // [BH][Tq_pad / 128]
     float *sink_part = nullptr;   // behind them: partial dV, dK of split key blocks (bwd_sink_bytes; 0: none)
 };
-int bwd_sink_parts(int Tq, int Tk, const MaskSpec &mask);
+int bwd_sink_parts(size_t BH, int Tq, int Tk, const MaskSpec &mask);
 size_t bwd_sink_bytes(size_t BH, int Tq, int Tk, int d, const MaskSpec &mask);
 size_t bwd_row_stride(int Tq);
 size_t bwd_workspace_bytes(size_t BH, int Tq, int d);
