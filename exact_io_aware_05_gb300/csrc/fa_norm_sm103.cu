@@ -353,12 +353,12 @@ int norm_rope_bwd_launch(const fa_heads *x, const fa_heads *dy, const fa_heads *
     // group has a CTA.  B2 T1021 of 6 + 2 heads of 64, fp32: a head a group is 344 tiles, two of them for some CTAs
     const int tok = kNormThreads / (spec.d / 16), least = (int)((H + kNormCtas - 3) / (kNormCtas - 2));
     const long long tiles = (a.n + tok - 1) / tok;
-    auto groups_of = [&](int hpc) { return (a.H[0] + hpc - 1) / hpc; };
+    auto groups_of = [&](int w, int hpc) { return a.H[w] / hpc + (a.H[w] % hpc > 0); };
     a.heads_per_cta = least > 1 ? least : 1;
-    while (a.heads_per_cta < 32 && (groups_of(a.heads_per_cta) + (a.H[1] + a.heads_per_cta - 1) / a.heads_per_cta) * tiles > kNormCtas)
+    while (a.heads_per_cta < 32 && (groups_of(0, a.heads_per_cta) + groups_of(1, a.heads_per_cta)) * tiles > kNormCtas)
         ++a.heads_per_cta;
-    a.G0 = groups_of(a.heads_per_cta);
-    a.groups = a.G0 + (a.H[1] + a.heads_per_cta - 1) / a.heads_per_cta;
+    a.G0 = groups_of(0, a.heads_per_cta);
+    a.groups = a.G0 + groups_of(1, a.heads_per_cta);
     a.groups = a.groups > 0 ? a.groups : 1;
     a.dw[0] = dq_weight;
     a.dw[1] = dk_weight;

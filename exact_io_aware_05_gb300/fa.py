@@ -212,6 +212,14 @@ def fa_fwd_masked(q, k, v, o, lse, window=(-1, -1), block_mask=None, scale: floa
                                                _stream(stream)))
 
 
+def _sink_bounds(left, sinks) -> tuple:
+    """As C ints: ctypes would take the lowest 32 bits of longer ones."""
+    left, sinks = int(left), int(sinks)
+    if not all(-1 << 31 <= x < 1 << 31 for x in (left, sinks)):
+        raise ValueError(f"window_left and n_sinks: expected up to 2^31 - 1, got {left} and {sinks}")
+    return left, sinks
+
+
 def fa_fwd_sinks(q, k, v, o, lse, window_left: int, n_sinks: int, scale: float, stream=None) -> None:
     """fa_fwd under a causal window of window_left + 1 keys (-1: no left bound) and the first n_sinks keys, which
     stay visible to every row behind them."""
@@ -223,7 +231,7 @@ def fa_fwd_sinks(q, k, v, o, lse, window_left: int, n_sinks: int, scale: float, 
     _need(o, "o", torch.bfloat16, (B, H, Tq, d), dev)
     _need(lse, "lse", torch.float32, (B, H, Tq), dev)
     _launch("fa_fwd_sinks", _lib.fa_fwd_sinks, q.get_device(), stream, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, H, Tq,
-            Tk, d, int(window_left), int(n_sinks), float(scale))
+            Tk, d, *_sink_bounds(window_left, n_sinks), float(scale))
 
 
 def fa_decode_workspace_bytes(B: int, H: int, Tq: int, Tk: int, d: int) -> int:
@@ -349,8 +357,7 @@ def attention_forward(q, k, v, causal: bool, scale: float, stream=None, window=N
     window (which replaces `causal`) or a block mask, fa_fwd_masked; with a window (left, 0) and sinks,
     fa_fwd_sinks."""
     B, H, Tq, Tk, d = _shapes(q, k)
-    o = torch.empty_like(q)
-    lse = torch.empty((B, H, Tq), dtype=torch.float32, device=q.device)
+    o, lse = _empties(stream, q.device, (q.shape, q.dtype), ((B, H, Tq), torch.float32))
     if sinks:
         fa_fwd_sinks(q, k, v, o, lse, _sink_window(causal, window, block_mask), sinks, scale, stream)
     elif window is not None or block_mask is not None:
@@ -461,7 +468,7 @@ def fa_bwd_masked(q, k, v, o, lse, dO, dq, dk, dv, window=(-1, -1), block_mask=N
 
 
 def fa_bwd_sinks_workspace_bytes(B: int, H: int, Tq: int, Tk: int, d: int, window_left: int, n_sinks: int) -> int:
-    return int(_lib.fa_bwd_sinks_workspace_bytes(B, H, Tq, Tk, d, window_left, n_sinks))
+    return int(_lib.fa_bwd_sinks_workspace_bytes(B, H, Tq, Tk, d, *_sink_bounds(window_left, n_sinks)))
 
 
 def fa_bwd_sinks(q, k, v, o, lse, dO, dq, dk, dv, window_left: int, n_sinks: int, scale: float, workspace: torch.Tensor,
@@ -477,7 +484,7 @@ def fa_bwd_sinks(q, k, v, o, lse, dO, dq, dk, dv, window_left: int, n_sinks: int
     if workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace: must be a contiguous tensor on the same device")
     _launch("fa_bwd_sinks", _lib.fa_bwd_sinks, q.get_device(), stream, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dO),
-            _ptr(dq), _ptr(dk), _ptr(dv), B, H, Tq, Tk, d, int(window_left), int(n_sinks), int(bool(deterministic)), float(scale),
+            _ptr(dq), _ptr(dk), _ptr(dv), B, H, Tq, Tk, d, *_sink_bounds(window_left, n_sinks), int(bool(deterministic)), float(scale),
             _ptr(workspace), workspace.nbytes)
 
 
@@ -693,9 +700,10 @@ def rope_backward(dq_out, dk_out, positions, spec: RopeSpec, stream=None):
 class HeadNorm:
     """Norms of query and key heads of width d (fa_head_norm in include/fa.h): a row x becomes
     weight x / sqrt(mean(x^2) + eps).  q_weight and k_weight: [d] bf16 or float32, both of one type, or None
-    (ones).  Checks its tensors once and keeps them; their contents are read at each call, so a weight that an
-    optimizer changes in place is taken as it is.  A tensor assigned to q_weight or k_weight is checked
-    and takes the place of the one before (a captured graph keeps the one that it was captured with)."""
+    (ones).  Checks its tensors and keeps them; their contents are read at each call, so a weight that an
+    optimizer changes in place is taken as it is, and one that has other memory by then (`weight.data = ...`, as when
+    a module is converted) is checked again.  A tensor assigned to q_weight or k_weight is checked and takes the place
+    of the one before (a captured graph keeps the memory that it was captured with)."""
 
     _WEIGHTS = ("q_weight", "k_weight")
 
@@ -704,28 +712,42 @@ class HeadNorm:
             raise ValueError(f"d: expected 64, 128 or 256, got {d}")
         if not 0.0 < float(eps) < float("inf"):
             raise ValueError(f"eps: expected a finite value above 0, got {eps}")
-        self.__dict__.update(d=int(d), eps=float(eps), q_weight=None, k_weight=None, _index=-1,
+        self.__dict__.update(d=int(d), eps=float(eps), q_weight=None, k_weight=None, _index=-1, _places=(None, None),
                              _c=_HeadNorm(d=int(d), dtype=FA_BF16, eps=float(eps)))
         if self._c.eps == 0.0:
             raise ValueError(f"eps: {eps} is 0 in fp32")
-        self.__dict__["_ref"] = ctypes.addressof(self._c)
+        self.__dict__["_address"] = ctypes.addressof(self._c)
         self.q_weight, self.k_weight = q_weight, k_weight
 
     def __setattr__(self, name, t):
         if name not in self._WEIGHTS:
             raise AttributeError(f"{name} of a HeadNorm is fixed")
-        other = self.__dict__["k_weight" if name == "q_weight" else "q_weight"]
-        if t is not None:
-            if not isinstance(t, torch.Tensor):
-                raise TypeError(f"{name}: expected a tensor, got {type(t).__name__}")
-            if t.dtype not in (torch.bfloat16, torch.float32):
-                raise TypeError(f"{name}: expected torch.bfloat16 or torch.float32, got {t.dtype}")
-            _need(t, name, t.dtype if other is None else other.dtype, (self.d,), t.device if other is None else other.device)
-        there = other if t is None else t
+        if t is not None and not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name}: expected a tensor, got {type(t).__name__}")
+        both = {w: t if w == name else self.__dict__[w] for w in self._WEIGHTS}
+        first = None
+        for w in (("k_weight", "q_weight") if name == "q_weight" else self._WEIGHTS):   # the assigned one last
+            x = both[w]
+            if x is None:
+                continue
+            if x.dtype not in (torch.bfloat16, torch.float32):
+                raise TypeError(f"{w}: expected torch.bfloat16 or torch.float32, got {x.dtype}")
+            _need(x, w, x.dtype if first is None else first.dtype, (self.d,), x.device if first is None else first.device)
+            first = x if first is None else first
         self.__dict__[name] = t
-        self.__dict__["_index"] = -1 if there is None else there.get_device()
-        setattr(self._c, name, _ptr(t))
-        self._c.dtype = FA_F32 if there is not None and there.dtype is torch.float32 else FA_BF16
+        self.__dict__["_index"] = -1 if first is None else first.get_device()
+        self.__dict__["_places"] = tuple(None if x is None else x.data_ptr() for x in both.values())
+        self._c.q_weight, self._c.k_weight = (None if x is None else _ptr(x) for x in both.values())
+        self._c.dtype = FA_F32 if first is not None and first.dtype is torch.float32 else FA_BF16
+
+    @property
+    def _ref(self):
+        """The structure's address, its pointers those of the weights as they are now."""
+        at = self.__dict__
+        q, k = at["q_weight"], at["k_weight"]
+        if at["_places"] != (None if q is None else q.data_ptr(), None if k is None else k.data_ptr()):
+            self.q_weight = q
+        return at["_address"]
 
     def __delattr__(self, name):
         raise AttributeError(f"{name} of a HeadNorm cannot be deleted")
@@ -737,6 +759,7 @@ class HeadNorm:
 def _need_norm(norm, spec, index) -> None:
     if not isinstance(norm, HeadNorm):
         raise TypeError(f"norm: expected a HeadNorm, got {type(norm).__name__}")
+    norm._ref   # its weights as they are now
     if norm.d != spec.d:
         raise ValueError(f"norm: expected head width {spec.d}, got {norm.d}")
     if (norm.q_weight is not None or norm.k_weight is not None) and norm._index != index:
@@ -1000,7 +1023,7 @@ def fa_decode_paged_window(cache: KVCache, q, o, lse, window_left: int, n_sinks:
 def _decode_window(cache, q, o, lse, window_left, n_sinks, scale, workspace, stream) -> None:
     Hq, Tq = _need_decode(cache, q, o, lse, workspace)
     _launch("fa_decode_paged_window", _lib.fa_decode_paged_window, cache._index, stream, cache._ref, q.data_ptr(), o.data_ptr(),
-            lse.data_ptr(), Hq, Tq, int(window_left), int(n_sinks), scale, workspace.data_ptr(), workspace.nbytes)
+            lse.data_ptr(), Hq, Tq, *_sink_bounds(window_left, n_sinks), scale, workspace.data_ptr(), workspace.nbytes)
 
 
 def fa_decode_paged_shared_workspace_bytes(cache: KVCache, Hq: int, Tq: int, prefix_pages: torch.Tensor) -> int:

@@ -257,6 +257,22 @@ def test_both_ways_of_calling(fa):
         fa.fa_norm_rope_bwd(q, q, qo, pos, spec, norm, dq_weight=torch.empty(128, device=DEV))      # no workspace
 
 
+def test_weights_with_other_memory(fa):
+    """A weight whose data is replaced, as when a module is converted, is read where it is now."""
+    q, k, pos, freqs, axis, w, _ = case(CASES[1], 17)
+    spec, p = fa.RopeSpec(128, freqs, axis), torch.nn.Parameter(w[0].clone())
+    norm = fa.HeadNorm(128, p, p)
+    fa.norm_rope_forward(q, k, pos, spec, norm)
+    for t in (w[1], w[1].bfloat16()):
+        p.data = t.clone()
+        assert all(torch.equal(a, b) for a, b in zip(fa.norm_rope_forward(q, k, pos, spec, norm),
+                                                     fa.norm_rope_forward(q, k, pos, spec, fa.HeadNorm(128, t, t))))
+    p.data = p.data.cpu()
+    with pytest.raises(ValueError):
+        fa.norm_rope_forward(q, k, pos, spec, norm)
+    assert fa.fa_sync_status() == fa.FA_OK
+
+
 def test_captured_and_on_another_stream(fa):
     """A training step's calls in a graph, replayed with other inputs, and on a stream of their own."""
     q, k, pos, freqs, axis, w, pair = case(CASES[1], 13)

@@ -51,6 +51,8 @@ def test_backward_refusals(fa):
     assert call(qw=None, kw=None, ws=None, nb=0) in NO_GPU
     assert call(T=0, qw=None, kw=None, ws=None) == 0
     assert call(T=0) in NO_GPU                            # the weights' gradients are still to be set
+    many = (Heads * 2)(heads(fa, 0, H=2 ** 30), heads(fa, 1, H=2 ** 30 - 1))
+    assert call(g=many, x=many, dx=many, T=0) in NO_GPU
     assert call(x=None) == INVALID and call(dx=x) == INVALID
     assert call(ws=None) == INVALID and call(nb=need - 1) == INVALID and call(ws=P + 10 * MB + 128) == INVALID
     assert call(n=1) == INVALID and call(n=1, kw=None) in NO_GPU
@@ -99,6 +101,23 @@ def test_handle(fa):
     with pytest.raises(TypeError):
         n.k_weight = 1.0
     assert n.k_weight is f32
+    # other memory for a weight that it holds, of another type too
+    p = torch.nn.Parameter(torch.ones(64))
+    n.k_weight = p
+    p.data = torch.full((64,), 2.0)
+    assert n._ref == ctypes.addressof(n._c) and n._c.k_weight == p.data_ptr()
+    p.data = p.data.bfloat16()
+    assert n._ref and n._c.k_weight == p.data_ptr() and n._c.dtype == fa.FA_BF16
+    n.q_weight = w
+    p.data = p.data.float()
+    with pytest.raises(TypeError):
+        n._ref                                 # one of them has become fp32
+    p.data = torch.ones(32, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        n._ref
+    n.k_weight = f32.bfloat16()
+    n.q_weight = None
+    n.k_weight = f32
     for name in ("eps", "d", "other"):
         with pytest.raises(AttributeError):
             setattr(n, name, 1)

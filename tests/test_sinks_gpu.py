@@ -166,6 +166,11 @@ def test_captured_and_on_another_stream(fa):
     graph.replay()
     want = fa.attention_forward(q, k, v, False, 0.125, window=(100, 0), sinks=4)
     assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    side.wait_stream(torch.cuda.current_stream())
+    want = fa.attention_forward(q, k, v, False, 0.125, window=(100, 0), sinks=4, stream=side)
+    grads = fa.attention_backward(q, k, v, *want, do, False, 0.125, window=(100, 0), sinks=4, stream=side, deterministic=True)
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(a, b) for a, b in zip((o, lse, dq, dk, dv), (*want, *grads)))
     assert fa.fa_sync_status() == fa.FA_OK
 
 

@@ -29,6 +29,17 @@ def test_refusals(fa):
     assert bwd(nbytes=fa.fa_bwd_sinks_workspace_bytes(1, 1, 100, 100, 64, 5, 2) - 1) == INVALID
 
 
+def test_bounds_beyond_32_bits(fa):
+    t = torch.empty((1, 1, 4, 64), dtype=torch.bfloat16)
+    for left, sinks in ((2 ** 32, 0), (5, 2 ** 32 + 1), (-2 ** 40, 0)):
+        with pytest.raises(ValueError):
+            fa.fa_fwd_sinks(t, t, t, t, torch.empty((1, 1, 4)), left, sinks, 1.0)
+        with pytest.raises(ValueError):
+            fa.fa_bwd_sinks(t, t, t, t, torch.empty((1, 1, 4)), t, t, t, t, left, sinks, 1.0, t)
+        with pytest.raises(ValueError):
+            fa.fa_bwd_sinks_workspace_bytes(1, 1, 4, 4, 64, left, sinks)
+
+
 def test_workspace(fa):
     """The partial sums: per head and key block with sinks, parts x (dV and dK) x 128 rows of d floats; none without
     a left bound or sinks."""
@@ -39,4 +50,7 @@ def test_workspace(fa):
             extra, unit = size(*args, left, sinks) - base(*args), args[0] * args[1] * -(-min(sinks, args[3]) // 128) * 2 * 128 * args[4] * 4
             assert extra % unit == 0 and extra // unit in (0, *range(2, 65))
     assert size(1, 1, 3000, 3000, 128, 255, 4) - base(1, 1, 3000, 3000, 128) == 3 * 2 * 128 * 128 * 4   # 24 query blocks, 8 a part
+    for sinks in (128, 2000, 65536):       # up to eight parts for each of the 152 SMs
+        assert size(1, 32, 65536, 65536, 64, 100, sinks) - base(1, 32, 65536, 65536, 64) <= 8 * 152 * 2 * 128 * 64 * 4
+    assert size(0, 3, 100, 100, 64, 5, 1) == base(0, 3, 100, 100, 64)
     assert size(1, 1, 100, 100, 64, -2, 0) == 0 and size(1, 1, 100, 100, 64, 0, -1) == 0 and size(1, 1, 100, 100, 96, 0, 1) == 0
