@@ -254,6 +254,27 @@ __device__ __forceinline__ int tiles_of(const PagedArgs &a, int b)
     return tiles_in<RANGED>(a, length_of(a, b));
 }
 
+// The sequence of up to 64 that comes `rank`-th by its tiles, most first and equal ones in order: lane i has the tiles
+// of sequences i and 32 + i, x and y; `most` is the largest.
+__device__ __forceinline__ int longest_first(int rank, int n, int x, int y, int most)
+{
+    const int lane = (int)lane_id();
+    x = lane < n ? x : -1;
+    y = 32 + lane < n ? y : -1;
+    int lo = 0, hi = most;   // the tiles of the one sought: the largest t that more than `rank` sequences reach
+    while (lo < hi) {
+        const int t = (lo + hi + 1) >> 1;
+        if (__popc(__ballot_sync(0xffffffffu, x >= t)) + __popc(__ballot_sync(0xffffffffu, y >= t)) > rank)
+            lo = t;
+        else
+            hi = t - 1;
+    }
+    rank -= __popc(__ballot_sync(0xffffffffu, x > lo)) + __popc(__ballot_sync(0xffffffffu, y > lo));
+    const uint32_t ex = __ballot_sync(0xffffffffu, x == lo), ey = __ballot_sync(0xffffffffu, y == lo);
+    const int nx = __popc(ex);
+    return rank < nx ? __fns(ex, 0, rank + 1) : 32 + __fns(ey, 0, rank - nx + 1);
+}
+
 // Tiles a CTA takes of the batch's `total`: equal shares, but at least 128 entries, below which
 // the joining costs more than they do.
 template <typename I>
@@ -322,6 +343,11 @@ __device__ __forceinline__ Place place_of(const PagedArgs &a, long long &share, 
         if ((int)blockIdx.x < a.B * per) {
             p.b = (int)blockIdx.x / per;
             p.ul = (int)blockIdx.x - p.b * per;
+            // Not all start at once: the longest first, unless most are about as long.  us in order of length and of the
+            // batch, 8 KV heads of 128: 64 sequences of 20 to 700 entries 25.8 and 28.0, 48 of 10 to 3000 under a window
+            // of 1501 43.1 and 49.9, 64 of 100 to 2000 under one of 701 39.4 and 37.5
+            if (RANGED && a.B <= 64 && a.B * per > a.grid && 5 * total < 4ll * longest * a.B * per)
+                p.b = longest_first(p.b, a.B, nt0, 32 + lane < a.B ? tiles_of<RANGED>(a, 32 + lane) : 0, longest);
             p.left = p.nt = tiles_of<RANGED>(a, p.b);
         }
         return p;

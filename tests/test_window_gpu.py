@@ -105,6 +105,18 @@ def test_many_lengths(fa, seed):
     test_window(fa, (lens, Hkv * G, Hkv, d, ps, Tq, left, sinks, fp8))
 
 
+@pytest.mark.parametrize("B,Hkv,d,fp8,lens", [
+    (64, 8, 128, False, "ragged"), (50, 8, 128, False, "ragged"), (33, 10, 128, True, "equal"), (20, 12, 256, False, "ragged"),
+    (64, 8, 64, True, "one"), (63, 6, 64, False, "few"),
+])
+def test_more_units_than_start_at_once(fa, B, Hkv, d, fp8, lens):
+    """They are taken in order of length, each of them once."""
+    rng = np.random.default_rng(B)
+    lens = {"ragged": rng.integers(0, 1500, B), "equal": np.repeat([1, 400], B)[:B], "one": np.where(np.arange(B) == 40, 1200, 3),
+            "few": np.where(rng.random(B) < 0.3, 700, rng.integers(0, 40, B))}[lens]
+    test_window(fa, ([int(x) for x in lens], Hkv, Hkv, d, 16, 1, 900, 4, fp8))
+
+
 def test_no_left_bound_is_the_whole_cache(fa):
     cache = make_cache(fa, 5, [900, 33], 2, 128, 16)
     q = randn(gen(6), 2, 8, 2, 128)
