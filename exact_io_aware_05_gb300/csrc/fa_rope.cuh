@@ -287,12 +287,16 @@ inline Row3 row3(const fa_heads &x) { return Row3{x.data, x.stride_b, x.stride_h
 
 // Heads one thread runs over: as few as let all CTAs be resident (two an SM), 32 at most.  With 8, 16,
 // 32 and 48 heads the q and k of B8 H32 T4096 d128 take 175, 163, 162 and 163 us, and 4193 new tokens of
-// 32 + 16 heads 24.6, 24.1, 21.1 and 26.7.
+// 32 + 16 heads in e4m3 24.6, 24.1, 21.1 and 26.7, with 24 18.1: what counts is the groups, not the average (5 heads of
+// B2 T3817 d128, normed: groups of 4 and 1 10.3 us, of 5 7.5).
 inline int heads_per_cta(long long tokens, int H, int d)
 {
-    const long long ctas = (tokens * (d / 16) + kRopeThreads - 1) / kRopeThreads * H, slots = 2 * device_sm_count();
-    const long long n = (ctas + slots - 1) / slots;
-    return (int)(n < 1 ? 1 : n > 32 ? 32 : n);
+    const long long tiles = (tokens * (d / 16) + kRopeThreads - 1) / kRopeThreads, slots = 2 * device_sm_count();
+    long long n = (tiles * H + slots - 1) / slots;
+    n = n < 1 ? 1 : n;
+    while (n < 32 && n < H && tiles * ((H + n - 1) / n) > slots)   // groups of n heads, the last with fewer
+        ++n;
+    return (int)(n > 32 ? 32 : n);
 }
 
 inline NormArgs norm_args(const fa_head_norm &n)
