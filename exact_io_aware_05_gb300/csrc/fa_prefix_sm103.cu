@@ -763,21 +763,26 @@ int join_run(const PrefixJoinArgs &j, cudaStream_t s)
 
 }  // namespace
 
-// Whether the prefix by itself is faster than every sequence reading it: an estimate of both, in us.  Without it each
-// sequence's P entries come from HBM or L2 at about 6.5 TB/s; with it the three kernels take 10.5 (14 at d 256), the
-// states 4.4 for 1000 rows of d 128, the prefix itself 5 TB/s.  us without and with, 8 KV heads of 128 and 4 query heads each,
-// batch x entries: 2 x 8192 15.1 and 17.3, 4 x 512 10.2 and 11.9, 4 x 2048 11.9 and 14.6, 4 x 8192 20.5 and 18.5,
-// 8 x 512 11.3 and 10.9, 8 x 2048 15.4 and 14.8, 16 x 512 13.5 and 11.5, 16 x 2048 21.1 and 15.0, 32 x 512 12.6 and
-// 14.5, 32 x 2048 30.6 and 18.4, 64 x 128 11.5 and 19.7, 64 x 512 26.1 and 20.4, 64 x 8192 177 and 31; 4 KV heads of 64,
-// 16 x 512 9.9 and 10.7, 16 x 2048 12.7 and 10.9; 8 of 256, 16 x 512 13.1 and 18.2, 16 x 2048 30.8 and 22.1.
+// Whether the prefix by itself is faster than every sequence reading it: estimates of both, less what they have in
+// common, fitted to 1762 pairs of measurements (1 to 90 sequences, prefixes of 64 to 24576 entries, 1 to 256 rows a KV
+// head, all widths and types): the choice is 1.9% slower than the better of the two on average and 48% at worst, where
+// both take 16 us or so.  Without it, the sequences' rows times entries count (at least eight rows, the columns of a
+// product), the bytes, which come out of L2 up to some 90 MB, and the row tiles; with it, its bytes and the rows' states.
+// us without and with, 8 KV heads of 128 and 4 query heads each, batch x entries: 2 x 8192 15.1 and 17.3, 4 x 512 10.2
+// and 11.9, 4 x 8192 20.5 and 18.5, 16 x 2048 21.1 and 15.0, 64 x 128 11.5 and 19.7, 64 x 8192 177 and 31; 3 KV heads of
+// 128 with 56 rows each, 1 x 2048 15.2 and 12.5, 6 x 8192 (e4m3) 35.0 and 23.5, 64 x 2048 86.0 and 37.8.
 // (The test library computes it by itself whatever the sizes.)
 bool prefix_pays(const fa_kv_cache &c, int Hq, int Tq, int n_pages)
 {
     if (FA_TEST_WITHHOLD)
         return true;
-    const double entry = (double)c.Hkv * 2 * c.d * (c.dtype == FA_E4M3 ? 1 : 2), once = entry * n_pages * c.page_size * 1e-6;   // MB
-    const double rows = (double)c.B * Hq * Tq * c.d / 128e3;
-    return 7.0 + c.B * once / 6.5 >= (c.d == 256 ? 14.0 : 10.5) + 4.4 * rows + once / 5.0;
+    const bool f8 = c.dtype == FA_E4M3;
+    const double P = (double)n_pages * c.page_size, once = P * c.Hkv * 2 * c.d * (f8 ? 1 : 2) * 1e-6;   // MB
+    const int M = Hq / c.Hkv * Tq, blocks = (M + 63) / 64;
+    const double pairs = c.B * P * c.Hkv * std::max(M, 8) * c.d * 1e-9;
+    const double without = 0.9 * std::min(M, 64) / 16 + 0.022 * blocks * c.B * once + (f8 ? 16 : 40) * pairs +
+                           0.1 * (c.B - 1) * std::max(0.0, once - 90);
+    return without >= 3.7 + 0.8 * ((double)c.B * Hq * Tq * c.d / 128e3) + 0.19 * once;
 }
 
 // Behind one another: the own entries' workspace, their o (fp32) and lse, the runs' states.

@@ -117,12 +117,14 @@ SMALL = [
 ]
 LARGE = [   # sizes at which the library computes the prefix by itself
     (208, [5, 3, 40, 0] * 20, 6, 6, 128, 16, 1, True, False),
-    (20000 // 32 * 32, [900, 31, 0], 12, 3, 64, 32, 1, True, False),
+    (20000 // 32 * 32, [900, 31, 0, 1, 1], 12, 3, 64, 32, 1, True, False),
     (192, [1] * 130, 8, 8, 64, 64, 1, True, False),
     (4096, [5, 0, 9, 1, 1, 1, 1, 1], 4, 4, 256, 32, 1, True, False),
-    (4096, [5, 0, 9, 100, -7, 1, 1, 1, 1, 1, 1, 1], 8, 4, 128, 64, 1, True, True),
-    (8192, [5, 0, 9, 100, -7, 1, 1, 1, 1, 1, 1, 1], 4, 4, 64, 16, 1, False, True),
+    (4096, [5, 0, 9, 100, -7, 1, 1, 1, 1, 1, 1, 1] * 2, 8, 4, 128, 64, 1, True, True),
+    (8192, [5, 0, 9, 100, -7, 1, 1, 1, 1, 1, 1, 1] * 2, 4, 4, 64, 16, 1, False, True),
     (4096, [3, 0, 0, 1, 1, 1, 1, 1], 4, 4, 256, 256, 1, True, True),
+    (2048, [3], 24, 3, 128, 16, 7, True, False),                         # many rows of one sequence
+    (2048, [3, 900], 32, 2, 64, 32, 4, True, True),
 ]
 
 
@@ -211,10 +213,10 @@ def test_far_pages(fa, always):
 
 def test_both_ways_captured_and_two_streams(fa):
     cache, pages = shared_cache(fa, 11, 8192, [500, 3, 70], 4, 128, 16)
-    q = randn(gen(12), 3, 8, 1, 128)
-    check(fa, None, cache, pages, 8192, 8, 1, sequences=[1])
-    o, o2, lse, lse2 = torch.empty_like(q), torch.empty_like(q), torch.empty((3, 8, 1), device=DEV), torch.empty((3, 8, 1), device=DEV)
-    n = fa.fa_decode_paged_shared_workspace_bytes(cache, 8, 1, pages)
+    q = randn(gen(12), 3, 64, 1, 128)
+    check(fa, None, cache, pages, 8192, 64, 1, sequences=[1])
+    o, o2, lse, lse2 = torch.empty_like(q), torch.empty_like(q), torch.empty((3, 64, 1), device=DEV), torch.empty((3, 64, 1), device=DEV)
+    n = fa.fa_decode_paged_shared_workspace_bytes(cache, 64, 1, pages)
     ws, ws2 = (torch.full((n,), 255, dtype=torch.uint8, device=DEV) for _ in range(2))
     fa.fa_decode_paged_shared(cache, q, o, lse, pages, 0.1, ws)
     fa._decode_shared(cache, q, o2, lse2, pages, 0.1, ws, True, None)
