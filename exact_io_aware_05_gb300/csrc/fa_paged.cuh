@@ -345,7 +345,9 @@ __device__ __forceinline__ Place place_of(const PagedArgs &a, long long &share, 
             p.ul = (int)blockIdx.x - p.b * per;
             // Not all start at once: the longest first, unless most are about as long.  us in order of length and of the
             // batch, 8 KV heads of 128: 64 sequences of 20 to 700 entries 25.8 and 28.0, 48 of 10 to 3000 under a window
-            // of 1501 43.1 and 49.9, 64 of 100 to 2000 under one of 701 39.4 and 37.5
+            // of 1501 43.1 and 49.9, 64 of 100 to 2000 under one of 701 39.4 and 37.5.  More sequences, two units for every
+            // place, do not gain (ranks for up to 128: 76 of 20 to 700 31.9 and 30.7, 70 of 10 to 3000 64.6 and 62.1), and four
+            // lengths a lane cost the others 1 us
             if (RANGED && a.B <= 64 && a.B * per > a.grid && 5 * total < 4ll * longest * a.B * per)
                 p.b = longest_first(p.b, a.B, nt0, 32 + lane < a.B ? tiles_of<RANGED>(a, 32 + lane) : 0, longest);
             p.left = p.nt = tiles_of<RANGED>(a, p.b);

@@ -107,7 +107,8 @@ def test_many_lengths(fa, seed):
 
 @pytest.mark.parametrize("B,Hkv,d,fp8,lens", [
     (64, 8, 128, False, "ragged"), (50, 8, 128, False, "ragged"), (33, 10, 128, True, "equal"), (20, 12, 256, False, "ragged"),
-    (64, 8, 64, True, "one"), (63, 6, 64, False, "few"),
+    (64, 8, 64, True, "one"), (63, 6, 64, False, "few"), (110, 4, 128, False, "ragged"), (128, 3, 128, False, "few"),
+    (140, 3, 128, False, "ragged"),
 ])
 def test_more_units_than_start_at_once(fa, B, Hkv, d, fp8, lens):
     """They are taken in order of length, each of them once."""
