@@ -70,6 +70,15 @@ inline int grid_aligned_group(int gmax, int levels, int grid)
     return gmax;
 }
 
+// Heads per group where all passes run the same way: units go round the heads of a group, and the CTAs, neighbours
+// presumably on different dies, round the units, so that with an even number a head's units keep to one die.  Backward
+// under a window of 1024 with 4 sinks, B8 H32 T4096 d128: 1571 to 1640 us with 4, 6, 8, 10 and 12 heads, 1850 to 1930
+// with 3, 5, 7 and 9; forward 495 to 513 and 504 to 529.
+inline int even_group(int g, int BH)
+{
+    return g >= BH ? BH : g < 2 ? (BH < 2 ? BH : 2) : g & ~1;
+}
+
 // Allowed (row, key) pairs: key l is allowed for row r iff
 //   r + Tk - Tq - left <= l <= r + Tk - Tq + right   (left, right = -1: that side unbounded)
 // and, with a block mask, block[(r / 128) * nkbm + l / 128] != 0 for the head's mask
