@@ -36,8 +36,8 @@
 //
 // A causal window with sinks (the first keys, which every row sees) has an instance of its own: a key block with sinks
 // visits every query block behind it, in parts where it would outlast the others, whose fp32 sums a kernel of their own
-// joins in order; the others visit a window's.  B8 H32 T4096 d128, 1024 keys and 4 sinks: 1620 us, of them 1300 the tile
-// loop (930 TFLOP/s over the visible pairs; nine blocks a unit for eight blocks' worth of pairs, and between units the
+// joins in order; the others visit a window's.  B8 H32 T4096 d128, 1024 keys and 4 sinks: 1560 us, of them 1235 the tile
+// loop (977 TFLOP/s over the visible pairs; nine blocks a unit for eight blocks' worth of pairs, and between units the
 // tensor cores wait for the next K and V and for dV and dK to be read), 180 the preprocess, 115 dQ, 30 the join.
 #include <algorithm>
 
