@@ -542,7 +542,7 @@ int fa_decode_paged_shared(const fa_kv_cache *cache, const void *q, void *o, flo
         return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     return n_prefix_pages == 0 || cache->num_pages == 0 || !fa::prefix_pays(*cache, Hq, Tq, n_prefix_pages)
-               ? fa::paged_launch(*cache, q, o, lse, Hq, Tq, causal, scale, 0, workspace, s)
+               ? fa::paged_launch(*cache, q, o, lse, Hq, Tq, causal, scale, 0, workspace, s, prefix_pages, n_prefix_pages)
                : fa::prefix_launch(*cache, q, o, lse, Hq, Tq, causal, prefix_pages, n_prefix_pages, scale, workspace, s);
 }
 

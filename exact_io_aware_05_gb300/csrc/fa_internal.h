@@ -181,8 +181,9 @@ int norm_rope_bwd_launch(const fa_heads *x, const fa_heads *dy, const fa_heads *
 int evict_launch(const fa_kv_cache &c, int budget, int n_first, int n_recent, float *weight_out, int *order_out,
                  int *lens_out, int *kept, cudaStream_t s);
 size_t paged_workspace_bytes(int B, int Hq, int Hkv, int Tq, int max_len, int d, int accumulate);
+// first_pages: the first n_first pages of every sequence, read in place of their entries in the block table.
 int paged_launch(const fa_kv_cache &c, const void *q, void *o, float *lse, int Hq, int Tq, int causal, float scale,
-                 int accumulate, void *workspace, cudaStream_t s);
+                 int accumulate, void *workspace, cudaStream_t s, const int *first_pages = nullptr, int n_first = 0);
 int paged_window_launch(const fa_kv_cache &c, const void *q, void *o, float *lse, int Hq, int Tq, int left, int sinks,
                         float scale, void *workspace, cudaStream_t s);
 // Where the states of the entries behind a prefix are, for the kernel that joins them with the prefix's.

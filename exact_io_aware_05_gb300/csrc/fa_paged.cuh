@@ -112,10 +112,12 @@ struct PagedArgs {
     float *lse, *weight;
     const float *ks, *vs;
     const int *block_table, *lens;
+    const int *first_pages;   // not RANGED: every sequence's first n_first pages, in place of the table's
     float *part;     // [2 grid][rows][D] then m, l [rows]
     long long *where;   // [0] the share, [1 + b] the first tile of sequence b (not of an empty one)
     float *scores;   // [sequence][KV head][row][cap]
     int B, Hq, Hkv, G, Tq, M, rows, RB, causal, num_pages, max_pages, ps_shift, cap, grid, whole, may_whole, kt;
+    int n_first;
     // RANGED.  left >= 0: row t, at position p = lens - Tq + t, sees slots from p - left, and those below
     // sinks.  left < 0: slots from base.
     int left, sinks, base, span;   // span: slots that a unit sees, at most
@@ -513,7 +515,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, ROWS>::CTAS)
             auto seen = [&](int slot, int n) { return slot < len && (!RANGED || slot + n > vis.from || slot < vis.sinks); };
             auto page_at = [&](int tile) {   // -1: nothing there
                 const int slot = slot_of(tile);
-                return mine && seen(slot, 1 << bp_shift) ? table[slot >> a.ps_shift] : -1;
+                if (!mine || !seen(slot, 1 << bp_shift))
+                    return -1;
+                const int i = slot >> a.ps_shift;
+                return !RANGED && i < a.n_first ? a.first_pages[i] : table[i];
             };
             int page = page_at(p.tile);
             for (int i = 0; i < cnt; ++i, ++n) {

@@ -10,10 +10,12 @@ size_t paged_workspace_bytes(int B, int Hq, int Hkv, int Tq, int max_len, int d,
 }
 
 int paged_launch(const fa_kv_cache &c, const void *q, void *o, float *lse, int Hq, int Tq, int causal, float scale,
-                 int accumulate, void *workspace, cudaStream_t s)
+                 int accumulate, void *workspace, cudaStream_t s, const int *first_pages, int n_first)
 {
     status_in_use(STATUS_PAGED);
     PagedArgs a = paged_args(c, q, o, lse, Hq, Tq, causal, scale, workspace);
+    a.first_pages = first_pages;
+    a.n_first = n_first;
     // several row blocks of a unit: only the join can add their weights
     const bool can = !accumulate || a.RB == 1;
     a.whole = can && a.cap <= (c.d == 256 ? kWholeSlots / 2 : kWholeSlots);

@@ -1034,8 +1034,10 @@ def fa_decode_paged_shared_workspace_bytes(cache: KVCache, Hq: int, Tq: int, pre
 
 def fa_decode_paged_shared(cache: KVCache, q, o, lse, prefix_pages: torch.Tensor, scale: float, workspace: torch.Tensor,
                            causal: bool = True, stream=None) -> None:
-    """fa_decode_paged for a batch whose sequences all begin with the same full pages, prefix_pages (int32 [n], the first
-    n entries of each sequence's block table): they are read once for all of them."""
+    """fa_decode_paged for a batch whose sequences all begin with the same full pages, prefix_pages (int32 [n], read in
+    place of the first n entries of each sequence's block table): they are read once for all of them, where the sizes say
+    that this is faster.  Then the prefix's probabilities have 8 bits, and an infinity or NaN in its v may reach
+    sequences that end before it (include/fa.h)."""
     st = _fast.decode_shared(cache._ref, cache._index, q, o, lse, prefix_pages, scale, workspace, causal, stream)
     if st != FA_OK:
         _again(st, "fa_decode_paged_shared", _decode_shared, cache, q, o, lse, prefix_pages, scale, workspace, causal, stream)
@@ -1054,7 +1056,8 @@ def _decode_shared(cache, q, o, lse, prefix_pages, scale, workspace, causal, str
 def attention_decode_paged(cache: KVCache, q, scale: float, causal: bool = True, accumulate: bool = False,
                            workspace=None, stream=None, window=None, sinks: int = 0, prefix_pages=None):
     """Allocates O, lse (and the workspace if not given) and runs fa_decode_paged; with a window (left, 0),
-    and sinks, fa_decode_paged_window; with prefix_pages, fa_decode_paged_shared."""
+    and sinks, fa_decode_paged_window; with prefix_pages, fa_decode_paged_shared (whose results differ from
+    fa_decode_paged's as described there)."""
     if q.dim() != 4:
         raise ValueError("q must be [B, Hq, Tq, d]")
     if window is None and sinks and not causal:

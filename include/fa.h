@@ -381,15 +381,15 @@ int fa_decode_paged_window(const fa_kv_cache *cache, const void *q, void *o, flo
 
 /*
  * fa_decode_paged for a batch whose sequences all begin with the same n_prefix_pages full pages,
- * prefix_pages (int32, device memory): the first entries of each sequence's row of the block table too, as far
- * as its length reaches.  The prefix is read once for the rows of all sequences, in matrix products of
+ * prefix_pages (int32, device memory), which stands for the first entries of every sequence's row of the block table:
+ * those are not looked at.  The prefix is read once for the rows of all sequences, in matrix products of
  * 128 rows; each sequence's own entries, behind it, as by fa_decode_paged; and the two are joined.  (Where the sizes
- * say that reading so little for every sequence is faster, it is fa_decode_paged.)  Results as
+ * say that reading so little for every sequence is faster, it is, by fa_decode_paged's kernel.)  Results as
  * fa_decode_paged's, except that a probability meets a v of the prefix as bf16, 2^-8 of it off at most, and that
  * an infinity or NaN in the v of a prefix's entry may reach every row of its KV head in the batch.  A sequence
  * may be shorter than the prefix (one of length 0, a place of the batch without a request, sees
- * nothing).  A page of prefix_pages out of range counts as masked for all (FA_ERR_BAD_INDEX).  n_prefix_pages 0
- * to max_pages; 0 is fa_decode_paged.  workspace: fa_decode_paged_shared_workspace_bytes bytes (dtype: the cache's),
+ * nothing).  A page of prefix_pages out of range counts as masked for all (FA_ERR_BAD_INDEX; where no sequence
+ * reaches it, it may go unreported).  n_prefix_pages 0 to max_pages; 0 is fa_decode_paged.  workspace: fa_decode_paged_shared_workspace_bytes bytes (dtype: the cache's),
  * 256-byte aligned, contents on entry ignored, not shared by calls that may overlap in time.
  */
 size_t fa_decode_paged_shared_workspace_bytes(int B, int Hq, int Hkv, int Tq, int max_pages, int page_size, int d,
