@@ -647,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, ROWS>::CTAS)
         bool ok = true;
         // All CTAs are there, and the join's blocks take nothing from them (0.2 to 0.4 us); where no join
         // follows, the next call's do (240 units of 512 14.1 us instead of 13.2)
-        // (own entries behind a shared prefix: its kernel does not wait for this one, and takes the SMs that are done)
+        // (own entries behind a shared prefix: its kernel's CTAs take the SMs that are done, and wait there)
         if ((whole && !a.whole) || (RANGED && a.o32))
             pdl_launch();
         if (RT == 1 && p.left > 0)

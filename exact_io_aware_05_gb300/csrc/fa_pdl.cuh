@@ -14,7 +14,9 @@ namespace fa {
 // so (or ended); it runs its prologue and stops at its pdl_wait().  pdl_wait(): returns when the
 // kernels before this one have ended and their writes are visible.  Every CTA of such a kernel
 // calls it before its first access to device memory, so that the end of a kernel still means the
-// end of all before it.
+// end of all before it.  One exception: the kernels that join states read a length in front of it, past the L1
+// (__ldcg).  The kernel before each of them says pdl_launch() only behind its own pdl_wait(), on every path, and
+// so whatever wrote the lengths has ended.
 __device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

@@ -192,8 +192,10 @@ __global__ void __launch_bounds__(XCfg<D, FP8>::NTHREADS, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const WaitCtx ctx{abort_flag, &g_prefix_status[0], a.timeout_ns};
-    // No wait here: the kernel before this one, that of the sequences' own entries, lets this one start only once
-    // all of it is past its own wait, and nothing that it writes is read.  The wait is at the end
+    // q, the lengths and the pages may come from the kernel in front of the own entries', which has ended by now;
+    // but that its writes are visible here is promised behind the wait alone (68 us without it at 64 sequences and 32768
+    // entries, 69 with it: CTAs that find a free SM wait for the last of the own entries)
+    pdl_wait();
     pdl_launch();
 
     if (warp < 4) {
@@ -525,7 +527,6 @@ __global__ void __launch_bounds__(XCfg<D, FP8>::NTHREADS, 1)
         tc_fence_after();
         tmem_dealloc(tmem, C::TMEM_COLS);
     }
-    pdl_wait();   // the end of this kernel means the end of the one before it
 }
 
 // ------------------------------------------------------------------ join
@@ -565,9 +566,9 @@ __global__ void __launch_bounds__(128) prefix_join_kernel(const __grid_constant_
     const int t = (int)(row32 - bh * (uint32_t)a.Tq), head = (int)(bh - b32 * (uint32_t)a.Hq), b = (int)b32;
     const int h = head / a.G, i = (head - h * a.G) * a.Tq + t, r = b * a.GT + i;   // KV head, row of its group, of its matrix
     const long long at = (long long)(h * a.RP + r / a.rows) * a.runs * a.rows + r % a.rows;
-    // The lengths may be read in front of the wait: all kernels before the attention's had ended when this one
-    // was launched.  Behind it, everything whose place is known goes together, the own entries' state as if it were whole
-    int len = a.own.lens[b];
+    // The lengths may be read in front of the wait, past the L1: this kernel is launched when every CTA of the prefix's
+    // is past its own wait.  Behind it, everything whose place is known goes together, the own entries' state as if it were whole
+    int len = __ldcg(a.own.lens + b);
     len = len < 0 || len > a.own.cap ? 0 : len;
     pdl_wait();
     const long long where0 = a.own.whole ? 0 : __ldcg(a.own.where), where1 = a.own.whole ? 0 : __ldcg(a.own.where + 1 + b);
