@@ -1263,13 +1263,13 @@ int launch_bwd(const void *q, const void *k, const void *v, const void *o, const
         // heads per group: Q, dO, K, V of the group within ~80 MB of L2, a whole number of
         // passes where possible (B8 H32 N4096 d128: 19 heads; measured faster than 12).  The
         // masked instances keep same-direction passes, as their units' lengths do not follow the order, and
-        // smaller groups: ~48 MB under a block mask, four heads under a window (B8 H32 T4096 d128, 1024 keys and 4 sinks,
+        // smaller groups: ~48 MB under a block mask, four heads under a window, one under the widest (B8 H32 T4096 d128, 1024 keys and 4 sinks,
         // by heads: 2 1580, 4 1571, 8 1610, 12 1640, 16 1690, 1 1943 us; one pass or a few: all heads).
         const double bytes_head = 2.0 * (Tq + Tk) * D * 2.0;
         int gsz = (int)((masked ? 48.0 : 80.0) * 1024 * 1024 / (bytes_head > 1 ? bytes_head : 1));
         gsz = gsz < 1 ? 1 : (gsz > BH ? BH : gsz);
         if (mask.left >= 0 && !mask.block)
-            gsz = a.units >= 4 * sms ? 4 : BH;
+            gsz = window_group(Tq, mask.left, BK, 8 * D, kBwdWindowBytes, a.units >= 4 * sms ? 4 : BH);
         a.group = masked ? even_group(gsz, BH) : grid_aligned_group(gsz, a.nkb, a.units < sms ? a.units : sms);
         a.timeout_ns = wait_timeout_ns();
         a.withhold = WITHHOLD_NONE;

@@ -1122,13 +1122,13 @@ int launch(const void *q, const void *k, const void *v, void *o, float *lse, int
     // heads per group: keep the group's K and V within ~80 MB of L2, a whole number of
     // passes where possible (B8 H32 N4096 d128: 38 heads; measured faster than 24).  The
     // masked instances keep same-direction passes, as their units' lengths do not follow the order, and
-    // smaller groups: ~48 MB under a block mask, eight heads under a window, whose blocks are soon done with.
+    // smaller groups: ~48 MB under a block mask, eight heads under a window (one under the widest).
     const double kv_head = 2.0 * Tk * D * 2.0;
     const int grid = a.units < device_sm_count() ? a.units : device_sm_count();
     int g = (int)((a.masked ? 48.0 : 80.0) * 1024 * 1024 / (kv_head > 1 ? kv_head : 1));
     g = g < 1 ? 1 : (g > BH ? BH : g);
     if (mask.left >= 0 && !mask.block)
-        g = 8;
+        g = window_group(Tk, mask.left, L::NQ * BR, 4 * D, kFwdWindowBytes, 8);
     a.group = a.masked ? even_group(g, BH) : grid_aligned_group(g, a.nqb, grid);
     a.timeout_ns = wait_timeout_ns();
     a.withhold = WITHHOLD_NONE;

@@ -73,11 +73,27 @@ inline int grid_aligned_group(int gmax, int levels, int grid)
 // Heads per group where all passes run the same way: units go round the heads of a group, and the CTAs, neighbours
 // presumably on different dies, round the units, so that with an even number a head's units keep to one die.  Backward
 // under a window of 1024 with 4 sinks, B8 H32 T4096 d128: 1571 to 1640 us with 4, 6, 8, 10 and 12 heads, 1850 to 1930
-// with 3, 5, 7 and 9; forward 495 to 513 and 504 to 529.
+// with 3, 5, 7 and 9; forward 495 to 513 and 504 to 529.  A single head stays one: backward under a block mask of which 5% is
+// left, 65536 rows of d 128, one, two and four heads 6.73, 7.66 and 8.54 ms.
 inline int even_group(int g, int BH)
 {
-    return g >= BH ? BH : g < 2 ? (BH < 2 ? BH : 2) : g & ~1;
+    return g >= BH ? BH : g < 2 ? 1 : g & ~1;
 }
+
+// Heads per group under a left bound: `most`, unless what one head keeps in use alone is more than `budget`, and several
+// would drive each other out of the L2.  Under a window of left keys it is that of `left` rows and of those that 152
+// units of `unit_rows` rows span, at most all T; bytes_row: of K and V forward, of Q, dO and dQ's fp32 sums backward.
+// Measured with 1 and 8 heads forward, 1 and 4 backward, in ms (d 128 but where said):
+//   T 131072, 130000 keys 25.8 and 27.1, 67.1 and 70.7; 100000 24.5 and 25.8, 62.7 and 64.9; 60000 18.2 and 18.9, 46.5
+//   and 47.6; 30000 (35 and 51 MB) 10.5 and 10.6, 26.9 and 26.9; T 65536, 60000 keys (34 and 67 MB) 6.91 and 6.58, 16.6
+//   and 16.4; 30000 4.86 and 4.76, 11.7 and 11.5; T 32768, 31000 keys 3.53 and 3.39, 8.66 and 8.45; d 256, T 131072, 120000
+//   keys 26.9 and 27.5 (4 heads); d 64, T 262144, 200000 keys 40.4 and 40.5 (4), 90.0 and 89.8.
+inline int window_group(int T, int left, int unit_rows, int bytes_row, long long budget, int most)
+{
+    const long long rows = (long long)left + 152ll * unit_rows;
+    return (rows < T ? rows : T) * bytes_row > budget ? 1 : most;
+}
+constexpr long long kFwdWindowBytes = 48ll << 20, kBwdWindowBytes = 72ll << 20;
 
 // Allowed (row, key) pairs: key l is allowed for row r iff
 //   r + Tk - Tq - left <= l <= r + Tk - Tq + right   (left, right = -1: that side unbounded)
