@@ -1172,9 +1172,10 @@ __global__ void __launch_bounds__(256) bwd_sink_join_kernel(const float *__restr
 
 template <int D>
 int launch_bwd(const void *q, const void *k, const void *v, const void *o, const float *lse, const void *dO,
-               void *dq, void *dk, void *dv, int BH, int Tq, int Tk, const MaskSpec &mask, float scale,
+               void *dq, void *dk, void *dv, int BH, int Tq, int Tk, const MaskSpec &asked, float scale,
                const BwdWorkspace &ws, int stages, cudaStream_t s)
 {
+    const MaskSpec mask = effective_mask(asked, Tk);
     const int causal = mask.right == 0 ? 1 : 0;
     const bool masked = mask.left >= 0 || mask.right > 0 || mask.block;
     using L = BwdLayout<D>;
@@ -1320,8 +1321,9 @@ int launch_bwd(const void *q, const void *k, const void *v, const void *o, const
 // 512, 2048 sinks: 1936 us with 16 parts, 1 GB, 1739 with 4, 1649 with 2, 2029 in one piece; H32 T32768 d64, 8192 sinks: 7925
 // us with 32 parts, 4 GB, 6465 in one piece).  Of sizes only: the sums' order, and the workspace, do not depend on
 // the device.
-int bwd_sink_parts(size_t BH, int Tq, int Tk, const MaskSpec &mask)
+int bwd_sink_parts(size_t BH, int Tq, int Tk, const MaskSpec &asked)
 {
+    const MaskSpec mask = effective_mask(asked, Tk);
     const long long nqb = (Tq + BQ - 1) / BQ;
     const int sinks = mask.sinks < Tk ? mask.sinks : Tk;
     if (mask.left < 0 || sinks <= 0 || BH == 0)

@@ -107,6 +107,17 @@ struct MaskSpec {
     int per_head;
     int sinks = 0;
 };
+// A left bound that hides no key of Tk (every row's position is below Tk) is none.  Causal with one and without, us, B8 H32
+// T4096 d128: forward 1002 and 803, backward 2512 and 2346; T 1024 109 and 94, 296 and 276; B1 H16 T32768 3440 and 3130, 8440
+// and 8480; B1 H6 T65536 d64 4310 and 3910, 9240 and 8810.
+inline MaskSpec effective_mask(MaskSpec m, int Tk)
+{
+    if (m.left >= 0 && (long long)m.left + m.sinks >= Tk - 1)   // keys from sinks to Tk - 2 - left would be hidden
+        m.left = -1;
+    if (m.left < 0)
+        m.sinks = 0;
+    return m;
+}
 inline MaskSpec causal_spec(int causal) { return MaskSpec{-1, causal ? 0 : -1, nullptr, 0}; }
 
 // Kernel launchers (arguments already validated by the ABI layer).

@@ -58,3 +58,32 @@ def test_groups_under_a_window(chosen):
         assert both[small] == (8, 4), small
     for wide in ((131072, 60000, 128), (131072, 130000, 128), (131072, 2 ** 31 - 1, 128), (262144, 200000, 64), (2 ** 31 - 1, 2 ** 31 - 1, 256)):
         assert both[wide] == (1, 1), wide
+
+
+MASKS = [((5, 0, 0), 100), ((98, 0, 4), 100), ((99, 0, 4), 100), ((99, -1, 0), 100), ((0, 0, 100), 100), ((0, 0, 99), 100), ((-1, 0, 7), 100),
+         ((2 ** 31 - 1, 0, 2 ** 31 - 1), 1), ((0, 0, 0), 1), ((0, 5, 0), 2)]
+
+
+def test_left_bounds_that_hide_nothing(tmp_path):
+    """(left, right, sinks) and Tk: none where every key of every row is seen, and no sinks without a left bound."""
+    if shutil.which("g++") is None or not os.path.isdir(CUDA_INC):
+        pytest.skip("g++ or the CUDA headers are not available")
+    rows = ", ".join("{%d, %d, %d, %d}" % (*m, tk) for m, tk in MASKS)
+    (tmp_path / "mask.cpp").write_text(r"""
+#include "fa_internal.h"
+#include <cstdio>
+int main() {
+    const int rows[][4] = {%s};
+    for (const auto &r : rows) {
+        const fa::MaskSpec m = fa::effective_mask(fa::MaskSpec{r[0], r[1], nullptr, 0, r[2]}, r[3]);
+        std::printf("%%d %%d %%d\n", m.left, m.right, m.sinks);
+    }
+    return 0;
+}
+""" % rows)
+    exe = tmp_path / "mask"
+    subprocess.run(["g++", "-std=c++17", "-O1", "-I", CSRC, "-I", CUDA_INC, str(tmp_path / "mask.cpp"), "-o", str(exe)], check=True)
+    out = list(map(int, subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.split()))
+    for i, ((left, right, sinks), tk) in enumerate(MASKS):
+        hides = left >= 0 and any(l < p - left and l >= sinks for p in range(min(tk, 200)) for l in range(p + 1))
+        assert tuple(out[3 * i:3 * i + 3]) == ((left, right, sinks) if hides else (-1, right, 0)), (left, right, sinks, tk)

@@ -54,3 +54,11 @@ def test_workspace(fa):
         assert size(1, 32, 65536, 65536, 64, 100, sinks) - base(1, 32, 65536, 65536, 64) <= 8 * 152 * 2 * 128 * 64 * 4
     assert size(0, 3, 100, 100, 64, 5, 1) == base(0, 3, 100, 100, 64)
     assert size(1, 1, 100, 100, 64, -2, 0) == 0 and size(1, 1, 100, 100, 64, 0, -1) == 0 and size(1, 1, 100, 100, 96, 0, 1) == 0
+
+
+def test_no_parts_where_the_left_bound_hides_nothing(fa):
+    size, base = fa.fa_bwd_sinks_workspace_bytes, fa.fa_bwd_workspace_bytes
+    for args in ((1, 1, 3000, 3000, 128), (2, 3, 777, 5000, 64)):
+        for left, sinks in ((100, args[3]), (0, 10 ** 9), (args[3] - 1, 4), (2 ** 31 - 1, 4)):
+            assert size(*args, left, sinks) == base(*args), (left, sinks)
+        assert size(*args, 100, args[3] - 1) >= base(*args)
