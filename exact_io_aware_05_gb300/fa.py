@@ -712,7 +712,7 @@ class HeadNorm:
             raise ValueError(f"d: expected 64, 128 or 256, got {d}")
         if not 0.0 < float(eps) < float("inf"):
             raise ValueError(f"eps: expected a finite value above 0, got {eps}")
-        self.__dict__.update(d=int(d), eps=float(eps), q_weight=None, k_weight=None, _index=-1, _places=(None, None),
+        self.__dict__.update(d=int(d), eps=float(eps), q_weight=None, k_weight=None, _index=-1, _places=(None, None), _dtype=None,
                              _c=_HeadNorm(d=int(d), dtype=FA_BF16, eps=float(eps)))
         if self._c.eps == 0.0:
             raise ValueError(f"eps: {eps} is 0 in fp32")
@@ -736,16 +736,19 @@ class HeadNorm:
             first = x if first is None else first
         self.__dict__[name] = t
         self.__dict__["_index"] = -1 if first is None else first.get_device()
+        self.__dict__["_dtype"] = None if first is None else first.dtype
         self.__dict__["_places"] = tuple(None if x is None else x.data_ptr() for x in both.values())
         self._c.q_weight, self._c.k_weight = (None if x is None else _ptr(x) for x in both.values())
         self._c.dtype = FA_F32 if first is not None and first.dtype is torch.float32 else FA_BF16
 
     @property
     def _ref(self):
-        """The structure's address, its pointers those of the weights as they are now."""
+        """The structure's address, its pointers and type those of the weights as they are now.  Memory may have been
+        given back and have come again for another type or layout: the address alone does not tell."""
         at = self.__dict__
-        q, k = at["q_weight"], at["k_weight"]
-        if at["_places"] != (None if q is None else q.data_ptr(), None if k is None else k.data_ptr()):
+        q, k, d, dtype, (qp, kp) = at["q_weight"], at["k_weight"], at["d"], at["_dtype"], at["_places"]
+        if (q is not None and (q.data_ptr() != qp or q.dtype is not dtype or q.numel() != d or not q.is_contiguous())) or \
+                (k is not None and (k.data_ptr() != kp or k.dtype is not dtype or k.numel() != d or not k.is_contiguous())):
             self.q_weight = q
         return at["_address"]
 
