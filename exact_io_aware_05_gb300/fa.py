@@ -13,6 +13,7 @@ every nonzero status raises ``FAError``.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 import struct
 
@@ -213,8 +214,8 @@ def fa_fwd_masked(q, k, v, o, lse, window=(-1, -1), block_mask=None, scale: floa
 
 
 def _sink_bounds(left, sinks) -> tuple:
-    """As C ints: ctypes would take the lowest 32 bits of longer ones."""
-    left, sinks = int(left), int(sinks)
+    """As C ints: ctypes would take the lowest 32 bits of longer ones.  A number with a fraction is no count of keys."""
+    left, sinks = operator.index(left), operator.index(sinks)
     if not all(-1 << 31 <= x < 1 << 31 for x in (left, sinks)):
         raise ValueError(f"window_left and n_sinks: expected up to 2^31 - 1, got {left} and {sinks}")
     return left, sinks

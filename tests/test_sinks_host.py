@@ -62,3 +62,20 @@ def test_no_parts_where_the_left_bound_hides_nothing(fa):
         for left, sinks in ((100, args[3]), (0, 10 ** 9), (args[3] - 1, 4), (2 ** 31 - 1, 4)):
             assert size(*args, left, sinks) == base(*args), (left, sinks)
         assert size(*args, 100, args[3] - 1) >= base(*args)
+
+
+def test_bounds_are_whole_numbers(fa):
+    t = torch.empty((1, 1, 4, 64), dtype=torch.bfloat16)
+    for left, sinks in ((600.5, 4), (600.0, 4), (600, 4.5), (None, 4), ("600", 4)):
+        with pytest.raises(TypeError):
+            fa.fa_fwd_sinks(t, t, t, t, torch.empty((1, 1, 4)), left, sinks, 1.0)
+        with pytest.raises(TypeError):
+            fa.fa_bwd_sinks(t, t, t, t, torch.empty((1, 1, 4)), t, t, t, t, left, sinks, 1.0, t)
+        with pytest.raises(TypeError):
+            fa.fa_bwd_sinks_workspace_bytes(1, 1, 4, 4, 64, left, sinks)
+        cache = fa.alloc_kv_cache(1, 1, 64, 16, device="cpu")
+        q, o, lse = torch.empty((1, 1, 1, 64), dtype=torch.bfloat16), torch.empty((1, 1, 1, 64), dtype=torch.bfloat16), torch.empty((1, 1, 1))
+        with pytest.raises(TypeError):
+            fa.fa_decode_paged_window(cache, q, o, lse, left, sinks, 1.0, torch.empty(256, dtype=torch.uint8))
+    for left, sinks in ((torch.tensor(100), 4), (True, torch.tensor(4))):
+        assert fa.fa_bwd_sinks_workspace_bytes(1, 1, 3000, 3000, 64, left, sinks) == fa.fa_bwd_sinks_workspace_bytes(1, 1, 3000, 3000, 64, int(left), 4)
