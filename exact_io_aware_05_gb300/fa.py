@@ -1064,6 +1064,8 @@ def attention_decode_paged(cache: KVCache, q, scale: float, causal: bool = True,
     fa_decode_paged's as described there)."""
     if q.dim() != 4:
         raise ValueError("q must be [B, Hq, Tq, d]")
+    if _sink_bounds(-1, sinks)[1] < 0:
+        raise ValueError(f"sinks: expected 0 or more, got {sinks}")
     if window is None and sinks and not causal:
         raise ValueError("sinks: give a window, or causal rows")
     if window is not None and (window[1] != 0 or not causal or accumulate):

@@ -58,3 +58,15 @@ def test_shared_workspace(fa):
         assert size(*args, dtype, pages + 1) == 0 and size(*args, dtype, -1) == 0 and size(*args, fa.FA_F32, 1) == 0
     assert size(5, 8, 3, 1, 100, 16, 64, 0, 1) == 0 and size(5, 8, 2, 17, 100, 16, 64, 0, 1) == 0
     assert size(5, 8, 2, 1, 100, 16, 96, 0, 1) == 0
+
+
+def test_sinks_that_are_no_count(fa):
+    """Without a window they do not reach the library, and are checked all the same."""
+    cache = fa.alloc_kv_cache(1, 1, 64, 16, device="cpu")
+    q = torch.empty((1, 1, 1, 64), dtype=torch.bfloat16)
+    for kw in (dict(), dict(window=(5, 0)), dict(prefix_pages=torch.zeros(1, dtype=torch.int32))):
+        for bad in (-3, 2 ** 32):
+            with pytest.raises(ValueError, match="sinks"):
+                fa.attention_decode_paged(cache, q, 0.1, sinks=bad, **kw)
+        with pytest.raises(TypeError):
+            fa.attention_decode_paged(cache, q, 0.1, sinks=1.5, **kw)
