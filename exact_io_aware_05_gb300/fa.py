@@ -259,12 +259,11 @@ def fa_decode(q, k, v, o, lse, causal: bool, scale: float, workspace: torch.Tens
 def attention_decode(q, k, v, causal: bool, scale: float, workspace=None, stream=None):
     """Allocates O, lse (and the workspace if not given) and runs fa_decode."""
     B, H, Tq, Tk, d = _shapes(q, k)
-    o = torch.empty_like(q)
-    lse = torch.empty((B, H, Tq), dtype=torch.float32, device=q.device)
+    specs = [(q.shape, q.dtype), ((B, H, Tq), torch.float32)]
     if workspace is None:
-        n = fa_decode_workspace_bytes(B, H, Tq, Tk, d)
-        workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
-    fa_decode(q, k, v, o, lse, causal, scale, workspace, stream)
+        specs.append(((max(fa_decode_workspace_bytes(B, H, Tq, Tk, d), 256),), torch.uint8))
+    o, lse, *own = _empties(stream, q.device, *specs)
+    fa_decode(q, k, v, o, lse, causal, scale, own[0] if own else workspace, stream)
     return o, lse
 
 
@@ -381,15 +380,11 @@ class FP8Operands(dict):
     q_descale [B,H,ceil(Tq/128)], k_descale [B,H,ceil(Tk/128)], v_descale [B,H,d] (f32)."""
 
 
-def alloc_fp8(B, H, Tq, Tk, d, device) -> FP8Operands:
+def alloc_fp8(B, H, Tq, Tk, d, device, stream=None) -> FP8Operands:
     u8, f32 = torch.uint8, torch.float32
-    return FP8Operands(
-        q8=torch.empty((B, H, Tq, d), dtype=u8, device=device),
-        k8=torch.empty((B, H, Tk, d), dtype=u8, device=device),
-        vt8=torch.empty((B, H, d, fa_fp8_vt_stride(Tk)), dtype=u8, device=device),
-        q_descale=torch.empty((B, H, -(-Tq // 128)), dtype=f32, device=device),
-        k_descale=torch.empty((B, H, -(-Tk // 128)), dtype=f32, device=device),
-        v_descale=torch.empty((B, H, d), dtype=f32, device=device))
+    specs = dict(q8=((B, H, Tq, d), u8), k8=((B, H, Tk, d), u8), vt8=((B, H, d, fa_fp8_vt_stride(Tk)), u8),
+                 q_descale=((B, H, -(-Tq // 128)), f32), k_descale=((B, H, -(-Tk // 128)), f32), v_descale=((B, H, d), f32))
+    return FP8Operands(zip(specs, _empties(stream, torch.device(device), *specs.values())))
 
 
 def _need_fp8(x: FP8Operands, B, H, Tq, Tk, d, dev):
@@ -411,7 +406,7 @@ def fa_fp8_quantize(q, k, v, signs=None, out: FP8Operands = None, stream=None) -
     _need(v, "v", torch.bfloat16, (B, H, Tk, d), dev)
     if signs is not None:
         _need(signs, "signs", torch.float32, (d,), dev)
-    x = alloc_fp8(B, H, Tq, Tk, d, dev) if out is None else out
+    x = alloc_fp8(B, H, Tq, Tk, d, dev, stream) if out is None else out
     _need_fp8(x, B, H, Tq, Tk, d, dev)
     _check("fa_fp8_quantize", _lib.fa_fp8_quantize(
         _ptr(q), _ptr(k), _ptr(v), _ptr(signs), B, H, Tq, Tk, d, _ptr(x["q8"]), _ptr(x["k8"]), _ptr(x["vt8"]),
@@ -437,8 +432,7 @@ def attention_forward_fp8(q, k, v, causal: bool, scale: float, signs=None, strea
     """fa_fp8_quantize then fa_fwd_fp8; returns (o, lse, the FP8 operands)."""
     x = fa_fp8_quantize(q, k, v, signs, stream=stream)
     B, H, Tq, d = q.shape
-    o = torch.empty_like(q)
-    lse = torch.empty((B, H, Tq), dtype=torch.float32, device=q.device)
+    o, lse = _empties(stream, q.device, (q.shape, q.dtype), ((B, H, Tq), torch.float32))
     fa_fwd_fp8(x, o, lse, causal, scale, stream)
     return o, lse, x
 
@@ -495,17 +489,16 @@ def attention_backward(q, k, v, o, lse, dO, causal: bool, scale: float, workspac
     (fa_bwd_deterministic when `deterministic`; fa_bwd_masked with a window, which
     replaces `causal`, or a block mask; fa_bwd_sinks with a window (left, 0) and sinks)."""
     B, H, Tq, Tk, d = _shapes(q, k)
+    left = _sink_window(causal, window, block_mask) if sinks else None
+    specs = [(t.shape, t.dtype) for t in (q, k, v)]
+    if workspace is None:
+        n = fa_bwd_sinks_workspace_bytes(B, H, Tq, Tk, d, left, sinks) if sinks else fa_bwd_workspace_bytes(B, H, Tq, Tk, d)
+        specs.append(((max(n, 256),), torch.uint8))
+    dq, dk, dv, *own = _empties(stream, q.device, *specs)
+    ws = own[0] if own else workspace
     if sinks:
-        left = _sink_window(causal, window, block_mask)
-        specs = [(t.shape, t.dtype) for t in (q, k, v)]
-        if workspace is None:
-            specs.append(((max(fa_bwd_sinks_workspace_bytes(B, H, Tq, Tk, d, left, sinks), 256),), torch.uint8))
-        dq, dk, dv, *own = _empties(stream, q.device, *specs)
-        fa_bwd_sinks(q, k, v, o, lse, dO, dq, dk, dv, left, sinks, scale, own[0] if own else workspace, deterministic, stream)
-        return dq, dk, dv
-    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-    ws = alloc_workspace(B, H, Tq, Tk, d, q.device) if workspace is None else workspace
-    if window is not None or block_mask is not None:
+        fa_bwd_sinks(q, k, v, o, lse, dO, dq, dk, dv, left, sinks, scale, ws, deterministic, stream)
+    elif window is not None or block_mask is not None:
         if window is None:
             window = (-1, 0 if causal else -1)
         elif causal:
