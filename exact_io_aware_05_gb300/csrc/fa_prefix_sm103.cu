@@ -771,9 +771,12 @@ int join_run(const PrefixJoinArgs &j, cudaStream_t s)
 
 // Whether the prefix by itself is faster than every sequence reading it: estimates of both, less what they have in
 // common, fitted to 1762 pairs of measurements (1 to 90 sequences, prefixes of 64 to 24576 entries, 1 to 256 rows a KV
-// head, all widths and types): the choice is 1.9% slower than the better of the two on average and 48% at worst, where
-// both take 16 us or so.  Without it, the sequences' rows times entries count (at least eight rows, the columns of a
-// product), the bytes, which come out of L2 up to some 90 MB, and the row tiles; with it, its bytes and the rows' states.
+// head, all widths and types) and held against 1260 more (1 to 8 sequences, 12288 to 196608 entries): the choice is 1.9%
+// and 1.0% slower than the better of the two on average, 48% and 55% at worst, where both take 13 to 25 us.  Without it,
+// the sequences' rows times entries count (at least eight rows, the columns of a product), the bytes, which come out of
+// L2 up to some 90 MB, and the row tiles; with it, its bytes and the rows' states, and where it is long in e4m3 the
+// conversion of its codes, by tiles of 128 entries an SM.  (8 KV heads of 64 over 196608 entries, two sequences: 80 us
+// without, 160 with; the long ones in e4m3 were 4.9% slower on average, 99% at worst, before that term, 0.8% and 43% now.)
 // us without and with, 8 KV heads of 128 and 4 query heads each, batch x entries: 2 x 8192 15.1 and 17.3, 4 x 512 10.2
 // and 11.9, 4 x 8192 20.5 and 18.5, 16 x 2048 21.1 and 15.0, 64 x 128 11.5 and 19.7, 64 x 8192 177 and 31; 3 KV heads of
 // 128 with 56 rows each, 1 x 2048 15.2 and 12.5, 6 x 8192 (e4m3) 35.0 and 23.5, 64 x 2048 86.0 and 37.8.
@@ -788,7 +791,8 @@ bool prefix_pays(const fa_kv_cache &c, int Hq, int Tq, int n_pages)
     const double pairs = c.B * P * c.Hkv * std::max(M, 8) * c.d * 1e-9;
     const double without = 0.9 * std::min(M, 64) / 16 + 0.022 * blocks * c.B * once + (f8 ? 16 : 40) * pairs +
                            0.1 * (c.B - 1) * std::max(0.0, once - 90);
-    return without >= 3.7 + 0.8 * ((double)c.B * Hq * Tq * c.d / 128e3) + 0.19 * once;
+    const double codes = f8 ? 0.8 * std::max(0.0, P * c.Hkv / 128 / kSMs - 1) : 0;
+    return without >= 3.7 + 0.8 * ((double)c.B * Hq * Tq * c.d / 128e3) + 0.19 * once + codes;
 }
 
 // Behind one another: the own entries' workspace, their o (fp32) and lse, the runs' states.
