@@ -149,7 +149,8 @@ __device__ __forceinline__ void put8(void *base, long long at, const float (&x)[
 }
 
 // Heads run q, then k, then v; a token's slot and page are looked up once per thread.  NORM: the rows of q
-// and k are normed before they turn.
+// and k are normed before they turn, their loads four heads ahead (4 sequences of 1000 tokens, 32 + 8 heads of 128: bf16
+// 16.6 us, 17.2 with six, 14.7 without a norm; e4m3 18.9, 19.4 and 15.6; 16 + 16 heads of 64 10.0, 10.5 and 8.0).
 template <int D, bool INTER, bool FP8, bool NORM>
 __global__ void __launch_bounds__(kRopeThreads, 2) append_kernel(const __grid_constant__ RopeTable tab,
                                                               const __grid_constant__ AppendArgs a)

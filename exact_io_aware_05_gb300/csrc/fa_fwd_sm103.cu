@@ -43,8 +43,9 @@
 // l < sinks)) has an instance of its own: a tile visits the blocks of the sinks and those of its window in closed form,
 // and the elements of a block that an edge cuts are masked by the bits of 32-key words.  The products bound it, with
 // the blocks that are visited in part: B8 H32 T4096 d128, 1024 keys and 4 sinks (8 blocks' worth of pairs in 10 blocks)
-// 494 us, 978 TFLOP/s over the visible pairs; B1 H6 T65536 d64, 4096 and 4 498 us, 803 TFLOP/s, where the exponentials
-// are; B2 H6, 1021 rows over 5003 keys of d 256, 777 and 5 25.6 us, 96 units on 152 SMs.
+// 494 us, 978 TFLOP/s over the visible pairs.  At d 64 the chain of S, softmax and P V does, as without a mask (ex2 is busy
+// less than half of the time): B1 H6 T65536, 4096 and 4 498 us, 803 TFLOP/s.  B2 H6, 1021 rows over 5003 keys of d 256, 777
+// and 5 25.6 us: 96 units on 152 SMs.
 #include "fa_common.cuh"
 #include "fa_internal.h"
 

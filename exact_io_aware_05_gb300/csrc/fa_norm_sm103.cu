@@ -10,8 +10,10 @@
 // writes dx.  A thread has 16 features of one token (8 pairs) and runs over heads with the token's
 // sines and cosines in registers and the weights in shared memory; the D / 16 threads of a row put their sums
 // together by shuffles, while the loads of the next heads are under way.  Measured, q and k of B8 H32 T4096 d128 in
-// bf16: 162 us forward (6.6 TB/s), 255 backward (6.3).  dw: each thread adds up its features over all its rows,
-// each CTA its threads, and a second kernel the CTAs, in a fixed order: the same bits on every run.
+// bf16: 162 us forward (6.6 TB/s), 255 backward (6.3).  Backward, a head group has as many CTAs as any other, and where
+// their heads differ the largest groups end last: 32 + 8 heads 209 us (4.8 TB/s; B4 in fp32 195, 5.2), 40 + 8 305 (4.0),
+// 64 + 8 334 (5.4).  dw: each thread adds up its features over all its rows, each CTA its threads, and a second kernel
+// the CTAs, in a fixed order: the same bits on every run.
 #include <climits>
 
 #include "fa_common.cuh"

@@ -24,9 +24,10 @@
 //   * P enters its product as bf16, as in the forward pass: 2^-8 of each probability.
 // Measured: 64 sequences, 8 KV heads of 128 with 4 query heads each, 32768 entries (bf16): 34 us, of them 10 the start, the
 // first tile and the states' way out and 1.9 for each 256 rows by 128 entries, the forward pass's rate; with the
-// sequences' own 20 to 700 entries (26) and the join (8) 68 us, where every sequence reading the prefix by itself takes
-// 760. 16 sequences with 4 new rows, 4 KV heads of 64 with 4 query heads each, 65536 entries in e4m3: 33 of 46.5 us (each
-// by itself: 93); there the issue slots and the exponentials are both two thirds busy.
+// sequences' own 20 to 700 entries (26) and the join (8), one after the other, 69 us, where every sequence reading the
+// prefix by itself takes 760.  16 sequences with 4 new rows, 4 KV heads of 64 with 4 query heads each, 65536 entries in
+// e4m3: 33 of 48 us (each by itself: 93); there the issue slots are half busy, ex2 a quarter, and one warpgroup of four
+// converts the codes.
 #include <algorithm>
 #include <cfloat>
 #include <climits>
